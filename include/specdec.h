@@ -63,6 +63,7 @@ extern "C" {
 
 #define SPECDEC_VERSION 100  /* 1.0.0 */
 #define SPECDEC_MAX_DRAFT 31 /* D <= 31: D+1 rows fit one warp ballot */
+#define SPECDEC_MAX_TREE 64  /* nodes of a draft tree, the pending token included */
 #define SPECDEC_GREEDY_SCRATCH_BYTES 73728 /* static scratch of specdec_verify_greedy_noalloc */
 
 typedef enum {
@@ -520,6 +521,216 @@ typedef struct {
 } specdec_admit_args;
 
 int specdec_pool_admit(const specdec_admit_args* args, void* stream);
+
+/*
+ * Speculation with a tree of drafts.  [IE5, "Draft Possible Tokens, Then Verify Them Together",
+ * for the cycle; BSDDR section 2.2 for the batch's layout.  The pages verify one chain of drafts
+ * per row; a tree holds several chains that share their beginnings, is verified in one pass, and
+ * commits the accepted path.]
+ *
+ * The tree of row b: parents[b][0 .. T) (int32, 1 <= T <= SPECDEC_MAX_TREE).  Node 0 is the
+ * pending token (parent -1); node i > 0 is a drafted token that follows node parents[b][i], with
+ * 0 <= parents[b][i] < i; a parent of -2 marks a node that the row does not use (node 0 too: the
+ * row then uses none).  Siblings are ordered by node index.  parents = NULL stands for the chain
+ * parents[b][i] = i - 1.  Any other parent, or one that is itself unused, is
+ * SPECDEC_ERR_INPUT_RANGE.
+ * The target's pass over the tree works on the left-padded batch (width W, N_b committed tokens):
+ * node i's K/V are at column W - 1 + i and its position is N_b - 1 + depth(i), with depth(0) = 0.
+ *
+ * A round: for every layer specdec_rotary_append and specdec_tree_attention, then one of the two
+ * tree verifications, then specdec_tree_commit with specdec_realign (whose drafts are the accepted
+ * path's tokens).  The operators serve; none has a gradient.
+ */
+
+/*
+ * Rotary positions of the queries and keys of new tokens, and the append of their K/V to one
+ * layer of the cache.
+ *   q   [B][T][heads_q][head_dim], k, v [B][T][cache.heads][head_dim] of the cache's dtype; the
+ *       heads of a token are contiguous, rows and tokens `*_stride_row` / `*_stride_token`
+ *       elements apart (so slices of one fused projection will do).
+ *   q_out  as q, with strides of its own; may be q itself (same strides).
+ *   table  [table_len][rot_dim / 2][2] float32: cosine and sine of position p for each of the
+ *       rot_dim / 2 pairs, made once per model (any scaling for long contexts is in it).
+ * Of every head the first rot_dim values are rotated and the rest copied: with pair i made of
+ * values (i, i + rot_dim / 2), or of (2i, 2i + 1) if `interleaved`,
+ *   (x1, x2) -> (x1 * cos - x2 * sin, x1 * sin + x2 * cos), in fp32, rounded once.
+ * Rotated keys and copied values are written to columns of row b of `cache`, layer `layer`
+ * (with cache.rows == 1 and B > 1 every batch row writes to cache row 0).
+ * Columns and positions, one of two ways:
+ *   - a verification pass: n_committed [B], width [1] (and parents): as described above, of
+ *     unused nodes neither column is written;
+ *   - explicit (positions and columns both [B][T], n_committed/width/parents NULL): token t of
+ *     row b has position positions[b][t] and goes to column columns[b][t]; a negative column
+ *     marks a token that is padding and is not written.  T is not limited to SPECDEC_MAX_TREE.
+ * The q_out of an unused node or padding token is zero.
+ * Device-detected errors: N_b outside [1, W], a bad parent, a position outside [0, table_len)
+ * (SPECDEC_ERR_INPUT_RANGE), a column at or beyond cache.cap_cols (SPECDEC_ERR_CAPACITY); the
+ * tokens concerned (all of the row, for the first two) are not written.
+ * Two tokens must not name one column.  Limits: B >= 0, T >= 1, B * T < 2^31; rot_dim even, in
+ * [2, head_dim]; head_dim * element size a multiple of 16 bytes; element-aligned q, k, v, q_out;
+ * table 8-byte aligned.  q_out may overlap nothing else.
+ */
+typedef struct {
+  specdec_kv_view cache;
+  int layer, B, T, heads_q, rot_dim, interleaved, table_len;
+  const void *q, *k, *v;
+  void* q_out;
+  long long q_stride_row, q_stride_token;      /* elements */
+  long long k_stride_row, k_stride_token;
+  long long v_stride_row, v_stride_token;
+  long long q_out_stride_row, q_out_stride_token;
+  const float* table;             /* [table_len][rot_dim / 2][2] */
+  const int32_t* n_committed;     /* [B]     verification pass, else NULL */
+  const int32_t* width;           /* [1] */
+  const int32_t* parents;         /* [B][T], or NULL (a chain) */
+  const int32_t* positions;       /* [B][T]  explicit, else NULL */
+  const int32_t* columns;         /* [B][T] */
+  int32_t* dev_status;            /* [1] */
+} specdec_rotary_args;
+
+int specdec_rotary_append(const specdec_rotary_args* args, void* stream);
+
+/*
+ * Attention of a verification pass over one layer of the cache: the pending token and the
+ * drafted nodes of every row against the row's committed columns and the nodes' own.
+ *   out_i = sum_c p_ic v_c,  p_i = softmax over c of scale * (q_i . k_c),  where c runs over the
+ *   committed columns [W - N_b, W - 1) and the columns W - 1 + j of node i and its ancestors j.
+ * Query head h reads K/V head h div (heads_q / cache.heads).  T = 1 is single-token decoding.
+ *   q [B][T][heads_q][head_dim], out the same shape, each with its own row and token strides
+ *   (heads contiguous), in the cache's dtype; lse [B][T][heads_q] float32 out (may be NULL): the
+ *   natural logarithm of the sum of exp(scale * q . k).
+ * An unused node gives zeros (lse: -infinity).  Columns that a node does not see, and what they
+ * hold (NaN included), do not enter its result; the cache beyond the nodes' columns and left of
+ * the committed ones is not used.
+ * Rows elsewhere than right-aligned in their own cache row (a pool's arena): first_col != NULL
+ * gives the first column of each row's committed tokens, so that node i is at column
+ * first_col + N_b - 1 + i (width is then not read and may be NULL); rows != NULL [B] makes batch
+ * row b read n_committed[rows[b]] and first_col[rows[b]]; with cache.rows == 1 and B > 1 every
+ * batch row reads cache row 0.
+ *   workspace  device buffer of specdec_tree_attention_workspace bytes, zero-filled before its
+ *              first use; every call leaves the part that has to be zero so (see the conventions
+ *              above).
+ * Scores, the softmax's maximum and sum and the output's sum are held in fp32; with bf16 tensors
+ * the softmax's weights are rounded to bf16 for the second matrix product.
+ * Device-detected errors: N_b < 1, N_b > W, a negative row index or first column, a bad
+ * parent (SPECDEC_ERR_INPUT_RANGE), a node's column beyond cache.cap_cols
+ * (SPECDEC_ERR_CAPACITY); the row concerned is not written.
+ * Limits: 0 <= B <= 1024, 1 <= T <= SPECDEC_MAX_TREE, heads_q a multiple of cache.heads, head_dim
+ * a multiple of 16 bytes and at most 256, scale finite; q, out 16-byte aligned with strides that
+ * are multiples of 16 bytes; out overlaps nothing else.
+ */
+typedef struct {
+  specdec_kv_view cache;
+  int layer, B, T, heads_q;
+  float scale;
+  const void* q;
+  void* out;
+  float* lse;                     /* [B][T][heads_q], or NULL */
+  long long q_stride_row, q_stride_token;      /* elements */
+  long long out_stride_row, out_stride_token;
+  const int32_t* n_committed;     /* [B], or by `rows` */
+  const int32_t* width;           /* [1] */
+  const int32_t* parents;         /* [B][T], or NULL (a chain) */
+  const int32_t* rows;            /* [B], or NULL */
+  const int32_t* first_col;       /* NULL: right-aligned at W */
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* dev_status;            /* [1] */
+} specdec_tree_attention_args;
+
+int specdec_tree_attention(const specdec_tree_attention_args* args, void* stream);
+
+/* Workspace bytes specdec_tree_attention needs for this shape on the current device, whatever the
+ * lengths are (0 for an invalid shape). */
+size_t specdec_tree_attention_workspace(int dtype, int B, int T, int heads_q, int heads_kv,
+                                        int head_dim);
+
+/*
+ * Greedy verification of a tree.  [IE5 "Exactness Means Different Things For Greedy And Sampled
+ * Output", "Draft Possible Tokens, Then Verify Them Together", along the tree's paths.]
+ * Row b's walk starts at node 0.  At a node the target's choice is the maximum of its score row
+ * (lowest token index on ties, NaN never chosen); the walk goes on to the node's first child that
+ * carries that token, and ends where there is none or at depth D.
+ *   logits  [B][T][row_stride], row (b, i) the target's scores after node i, first V read;
+ *   tokens  [B][T] int32 node tokens (tokens[b][0], the pending token, is not read);
+ *   accept_len [B] out: a_b, the accepted nodes;  out_token [B] out: the target's choice at the
+ *           walk's last node;  path [B][D] out: the accepted nodes, -1 from a_b on;
+ *   draft   [B][D] out: their tokens, 0 from a_b on (the drafts of a realignment or append).
+ * Only the score rows on the walk are read.  A row without used nodes gives a_b = 0, token -1.
+ * A visited row of only NaN sets SPECDEC_ERR_INPUT_RANGE (the walk ends there with token -1); a
+ * bad parent also does (that row's outputs are not written); a token outside [0, V) never
+ * matches.  Limits: B >= 0, 1 <= T <= SPECDEC_MAX_TREE, 1 <= D <= SPECDEC_MAX_DRAFT, 1 <= V,
+ * row_stride >= V; logits element-aligned.  parents may be NULL (a chain).
+ */
+int specdec_verify_tree_greedy(const void* logits, int dtype, int B, int T, int V,
+                               long long row_stride, const int32_t* tokens,
+                               const int32_t* parents, int D, int32_t* accept_len,
+                               int32_t* out_token, int32_t* path, int32_t* draft,
+                               int32_t* dev_status, void* stream);
+
+/*
+ * Sampled verification of a tree (speculative rejection sampling among siblings).  [IE5
+ * "Exactness Means Different Things For Greedy And Sampled Output": accept x with probability
+ * min(1, p(x)/q(x)), after a rejection go on with normalize(max(0, p - q)).]
+ *   target_logits, draft_logits [B][T][row_stride]: p = softmax(target row / temperature) and
+ *   q = softmax(draft row / temperature) of the distribution after each node; draft rows of nodes
+ *   without children are not read.
+ * The walk starts at node 0.  At a node its children c are tried in order: child i (token x) is
+ * accepted iff u[b][i] < p(x) / q(x) and the walk goes on there; otherwise p becomes
+ * normalize(max(0, p - q)) (p stays where that is zero everywhere) and, unless `replacement`, q
+ * becomes q without x, normalised (siblings drawn without replacement; with `replacement` != 0
+ * they were drawn independently and q stays).  With every child rejected, at a leaf or at depth
+ * D, the token is drawn from p: the first index whose running sum exceeds u[b][0] * (total).
+ * So the committed tokens are distributed as the target's own, if node i's token was drawn from
+ * q.  p(x) = 0 rejects whatever q(x) is; q(x) = 0 < p(x) accepts.
+ *   uniforms [B][T] float32 in [0, 1): u[b][0] for the draw, u[b][i] for node i;
+ *   accept_len, out_token, path, draft  as for greedy verification.
+ * Probabilities and sums in fp32 (sums of a row are taken pairwise over 16-byte vectors, threads
+ * and CTAs).  Only the rows on the walk are read.  A score of -infinity is a token of probability
+ * zero (sampling settings such as top-k may be applied that way).
+ * Device-detected errors (SPECDEC_ERR_INPUT_RANGE): a bad parent or a used uniform outside
+ * [0, 1) (the row's outputs are not written); a token outside [0, V) on the walk (it is
+ * rejected without changing p and q); a visited row with NaN, +infinity or nothing above
+ * -infinity (the walk ends there with token -1).  Limits as for greedy verification, and
+ * temperature > 0 and finite; both score tensors have the same dtype and row_stride.
+ */
+int specdec_verify_tree_sample(const void* target_logits, const void* draft_logits, int dtype,
+                               int B, int T, int V, long long row_stride, float temperature,
+                               const int32_t* tokens, const int32_t* parents,
+                               const float* uniforms, int replacement, int D,
+                               int32_t* accept_len, int32_t* out_token, int32_t* path,
+                               int32_t* draft, int32_t* dev_status, void* stream);
+
+/*
+ * Commit of the accepted path: every layer's K/V columns of the accepted nodes become
+ * contiguous, as those of an accepted chain are.  For row b and i = 1 .. a_b the column of node
+ * path[b][i-1] of `src`, W - 1 + path[b][i-1], goes
+ *   - with width_dst NULL to column W - 1 + i of `dst` (before a realignment; dst may be the same
+ *     view as src: moved in place);
+ *   - with width_dst given to column *width_dst - 2 - a_b + i of `dst` (after a realignment from
+ *     src into dst that took the accepted length a_b: it put the first a_b nodes' columns there).
+ * For a pool, first_col (and rows) as for specdec_tree_attention give the nodes' columns from
+ * first_col + N - 1 (n_committed is then needed; width is not read): in place only.
+ * Device-detected errors: a_b outside [0, D], a path that is not increasing or leaves
+ * [1, T), W < 1 (SPECDEC_ERR_INPUT_RANGE), a column outside a cache (SPECDEC_ERR_CAPACITY); the
+ * row concerned is not moved.  src and dst: equal geometry except cap_cols, and either the same
+ * view or no overlap.  Limits: 0 <= B <= 1024, 1 <= T <= SPECDEC_MAX_TREE,
+ * 1 <= D <= SPECDEC_MAX_DRAFT.
+ */
+typedef struct {
+  specdec_kv_view src, dst;
+  int B, T, D;
+  const int32_t* width;           /* [1] */
+  const int32_t* width_dst;       /* [1], or NULL */
+  const int32_t* accept_len;      /* [B] */
+  const int32_t* path;            /* [B][D] */
+  const int32_t* n_committed;     /* NULL, or with first_col */
+  const int32_t* rows;            /* [B], or NULL */
+  const int32_t* first_col;       /* NULL: right-aligned at W */
+  int32_t* dev_status;            /* [1] */
+} specdec_tree_commit_args;
+
+int specdec_tree_commit(const specdec_tree_commit_args* args, void* stream);
 
 /*
  * Arena allocator (HOST only, thread safe).  Columns [0, cols) of the pool's K/V arena are handed

@@ -24,6 +24,16 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) {
   return __uint_as_float(static_cast<uint32_t>(*p) << 16);
 }
 
+// Rounding to bf16 (nearest, ties to even; NaN stays NaN), and two values in one word.
+__device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+__device__ __forceinline__ uint16_t bf16_bits(float x) {
+  return static_cast<uint16_t>(bf16_pack(x, 0.f) & 0xFFFFu);
+}
+
 // Unpack one 16-byte vector into floats: 8 for bf16, 4 for fp32.
 template <typename T> struct Vec;
 template <> struct Vec<uint16_t> {
@@ -42,6 +52,46 @@ template <> struct Vec<float> {
   }
   __device__ __forceinline__ static float scalar(const float* p) { return *p; }
 };
+
+// ----------------------------------------------------------------------------------- keys
+
+// Score -> unsigned integer with the same order (-0 counted as +0).  NaN is never encoded.
+__device__ __forceinline__ uint32_t order_bits(float f) {
+  const uint32_t u = (f == 0.f) ? 0u : __float_as_uint(f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Key of (score, index): larger score first, then lower index.  0 means "no element".
+__device__ __forceinline__ unsigned long long make_key(float v, int i) {
+  return (static_cast<unsigned long long>(order_bits(v)) << 32) | static_cast<uint32_t>(~i);
+}
+
+// Fold one element (indices visited in ascending order by this thread) into the running best.
+// NaN is never taken; the first non-NaN element of a row is always taken (even -inf).
+__device__ __forceinline__ void take(float x, int e, float& bv, int& bi) {
+  if (x == x && (bi < 0 || x > bv)) { bv = x; bi = e; }
+}
+
+// Fold N consecutive elements starting at index e0 (max tree, first occurrence).
+template <int N>
+__device__ __forceinline__ void take_vector(const float* x, int e0, float& bv, int& bi) {
+  float t[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) t[k] = x[k];
+#pragma unroll
+  for (int w = N / 2; w > 0; w >>= 1)
+#pragma unroll
+    for (int k = 0; k < w; ++k) t[k] = fmaxf(t[k], t[k + w]);  // fmaxf drops NaN operands
+  const float m = t[0];
+  if (m == m && (bi < 0 || m > bv)) {
+    int k = 0;
+#pragma unroll
+    for (int q = N - 1; q >= 0; --q)
+      if (x[q] == m) k = q;  // first occurrence
+    bv = m;
+    bi = e0 + k;
+  }
+}
 
 // Programmatic dependent launch.  A kernel launched with programmatic stream serialization may
 // start before the kernel ahead of it on the stream has finished; pdl_wait() blocks until that
@@ -166,5 +216,44 @@ int cluster_for_one_wave(const void* kernel, int rows, int c_min, int c_max, int
 int map_cuda_error(cudaError_t); // SPECDEC_OK or SPECDEC_ERR_CUDA (clears non-sticky errors)
 
 inline int elem_size(int dtype) { return dtype == SPECDEC_F32 ? 4 : dtype == SPECDEC_BF16 ? 2 : 0; }
+
+// A K/V cache view in bytes.
+struct ByteView {
+  char* base;
+  long long sl, skv, srow, shead;  // bytes
+};
+
+// Host checks of a view: sizes, and 16-byte columns, strides and base.
+inline int check_view(const specdec_kv_view& v, int es_expect) {
+  const int es = elem_size(v.dtype);
+  if (es == 0 || !v.base) return SPECDEC_ERR_INVALID_ARG;
+  if (es_expect && es != es_expect) return SPECDEC_ERR_INVALID_ARG;
+  if (v.layers < 1 || v.rows < 1 || v.heads < 1 || v.head_dim < 1 || v.cap_cols < 1)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (v.stride_layer < 0 || v.stride_kv < 0 || v.stride_row < 0 || v.stride_head < 0)
+    return SPECDEC_ERR_INVALID_ARG;
+  const long long cb = static_cast<long long>(v.head_dim) * es;
+  if (cb % 16 || reinterpret_cast<uintptr_t>(v.base) % 16 || (v.stride_layer * es) % 16 ||
+      (v.stride_kv * es) % 16 || (v.stride_row * es) % 16 || (v.stride_head * es) % 16)
+    return SPECDEC_ERR_UNSUPPORTED;
+  if (static_cast<long long>(v.cap_cols) * cb > (1LL << 40)) return SPECDEC_ERR_UNSUPPORTED;
+  return SPECDEC_OK;
+}
+
+// Byte span [lo, hi) a view can address (for overlap checks).
+inline void view_span(const specdec_kv_view& v, uintptr_t& lo, uintptr_t& hi) {
+  const long long es = elem_size(v.dtype);
+  const long long last = (v.layers - 1) * v.stride_layer + v.stride_kv +
+                         (v.rows - 1) * v.stride_row + (v.heads - 1) * v.stride_head +
+                         static_cast<long long>(v.cap_cols) * v.head_dim;
+  lo = reinterpret_cast<uintptr_t>(v.base);
+  hi = lo + static_cast<uintptr_t>(last * es);
+}
+
+inline ByteView to_bytes(const specdec_kv_view& v) {
+  const long long es = elem_size(v.dtype);
+  return ByteView{static_cast<char*>(v.base), v.stride_layer * es, v.stride_kv * es,
+                  v.stride_row * es, v.stride_head * es};
+}
 
 }  // namespace specdec

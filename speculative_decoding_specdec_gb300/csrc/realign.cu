@@ -65,11 +65,6 @@ constexpr int kLptRows = 256;  // scheduled in place: longest-first item order u
 
 enum Mode { kEqspec = 0, kPoolGather = 1, kPoolAppend = 2 };
 
-struct ByteView {
-  char* base;
-  long long sl, skv, srow, shead;  // bytes
-};
-
 struct Params {
   ByteView src, dst;
   int mode, R, D, L, H, col_bytes, tile, stages, copy_engine, in_place, by_slot;
@@ -620,38 +615,6 @@ __global__ void __launch_bounds__(kThreads) realign_kernel(const Params p) {
     write_metadata(p, s, static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x,
                    G * kThreads, threadIdx.x, kThreads);
   }
-}
-
-int check_view(const specdec_kv_view& v, int es_expect) {
-  const int es = elem_size(v.dtype);
-  if (es == 0 || !v.base) return SPECDEC_ERR_INVALID_ARG;
-  if (es_expect && es != es_expect) return SPECDEC_ERR_INVALID_ARG;
-  if (v.layers < 1 || v.rows < 1 || v.heads < 1 || v.head_dim < 1 || v.cap_cols < 1)
-    return SPECDEC_ERR_INVALID_ARG;
-  if (v.stride_layer < 0 || v.stride_kv < 0 || v.stride_row < 0 || v.stride_head < 0)
-    return SPECDEC_ERR_INVALID_ARG;
-  const long long cb = static_cast<long long>(v.head_dim) * es;
-  if (cb % 16 || reinterpret_cast<uintptr_t>(v.base) % 16 || (v.stride_layer * es) % 16 ||
-      (v.stride_kv * es) % 16 || (v.stride_row * es) % 16 || (v.stride_head * es) % 16)
-    return SPECDEC_ERR_UNSUPPORTED;
-  if (static_cast<long long>(v.cap_cols) * cb > (1LL << 40)) return SPECDEC_ERR_UNSUPPORTED;
-  return SPECDEC_OK;
-}
-
-// Byte span [lo, hi) a view can address (for overlap checks).
-void view_span(const specdec_kv_view& v, uintptr_t& lo, uintptr_t& hi) {
-  const long long es = elem_size(v.dtype);
-  const long long last = (v.layers - 1) * v.stride_layer + v.stride_kv +
-                         (v.rows - 1) * v.stride_row + (v.heads - 1) * v.stride_head +
-                         static_cast<long long>(v.cap_cols) * v.head_dim;
-  lo = reinterpret_cast<uintptr_t>(v.base);
-  hi = lo + static_cast<uintptr_t>(last * es);
-}
-
-ByteView to_bytes(const specdec_kv_view& v) {
-  const long long es = elem_size(v.dtype);
-  return ByteView{static_cast<char*>(v.base), v.stride_layer * es, v.stride_kv * es,
-                  v.stride_row * es, v.stride_head * es};
 }
 
 int launch(Params& p, cudaStream_t stream) {

@@ -1,0 +1,446 @@
+// Attention of a draft tree over the cache: host entry, and the kernel for fp32 tensors and for
+// head sizes that the tensor-core kernels do not take.
+//
+// attn_fma_kernel.  fp32 has no tensor-core product of full precision, so this is the FMA pipe:
+// RG warps, each with 4 query rows, share a tile of 32 columns of K and V in shared memory
+// (cp.async, two stages).  A lane computes the scores of one column (its K vector against four
+// broadcast Q vectors), the softmax of a row is warp-local, and for the second product a lane owns
+// 4 (or 8) of the head's values.  Shared-memory reads bound it: 8 wavefronts per 16 FMAs.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "tree_attention.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kTile = 32;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16-byte asynchronous copy global -> shared; zero-fills where `take` is false.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               ::"r"(smem_addr(dst)), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Bytes of a column in shared memory: 16 more than its values, so that the 16-byte reads of
+// eight neighbouring columns fall into different banks.
+__host__ __device__ constexpr int pitch_of(int hd, int es) { return hd * es + 16; }
+
+__host__ inline size_t fma_smem(int RG, int hd, int es) {
+  return static_cast<size_t>(4) * kTile * pitch_of(hd, es) + static_cast<size_t>(RG) * 4 * hd * 4 +
+         static_cast<size_t>(RG) * kTile * 16;
+}
+
+// 4 consecutive values of a column as floats.
+template <typename T> __device__ __forceinline__ float4 load4(const char* p);
+template <> __device__ __forceinline__ float4 load4<float>(const char* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <> __device__ __forceinline__ float4 load4<uint16_t>(const char* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+}
+template <typename T> __device__ __forceinline__ void store4(char* p, float4 v);
+template <> __device__ __forceinline__ void store4<float>(char* p, float4 v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+template <> __device__ __forceinline__ void store4<uint16_t>(char* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pack(v.x, v.y), bf16_pack(v.z, v.w));
+}
+
+// RG: groups of 4 query rows (warps); NB: blocks of 128 head values (1 or 2).
+template <typename T, int RG, int NB>
+__global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
+  constexpr int kThreads = RG * 32, M = RG * 4;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ AttnPlan plan;
+  __shared__ int s_par[kMaxTree], s_flag, s_bad;
+  __shared__ unsigned long long s_anc[kMaxTree];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hd = p.hd, pitch = pitch_of(hd, sizeof(T)), vecs = hd * static_cast<int>(sizeof(T)) / 16;
+  char* s_k = smem;                                   // [2][kTile] columns
+  char* s_v = s_k + 2 * kTile * pitch;
+  float* s_q = reinterpret_cast<float*>(s_v + 2 * kTile * pitch);  // [M][hd], times scale_log2
+  float4* s_p = reinterpret_cast<float4*>(s_q + M * hd) + warp * kTile;  // [kTile] x 4 rows
+  if (warp == 0) attn_plan(p, kTile, plan);
+  __syncthreads();
+  const AttnShares sh = attn_shares(p, plan);
+  const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
+  if (sh.total == 0 || g >= sh.groups) return;
+  const long long x1 = sh.start(g + 1);
+  const int nrows = min(M, p.T * p.G - mt * M);  // query rows of this M-tile: (node, head) pairs
+  int row_b = -1;
+  for (long long x = sh.start(g); x < x1;) {
+    const AttnSegment seg = attn_segment(p, plan, x, x1);
+    x += seg.tile1 - seg.tile0;
+    int err;
+    const AttnRow row = attn_row(p, seg.b, &err);
+    if (seg.b != row_b) {  // a new batch row: its tree
+      row_b = seg.b;
+      __syncthreads();
+      if (p.parents) {
+        for (int i = tid; i < p.T; i += kThreads) s_par[i] = p.parents[seg.b * p.T + i];
+        __syncthreads();
+      }
+      bool bad = false;
+      for (int i = tid; i < p.T; i += kThreads)
+        s_anc[i] = tree_ancestors(p.parents ? s_par : nullptr, i, bad);
+      if (bad) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
+      s_bad = 0;
+      __syncthreads();
+      if (bad) s_bad = 1;
+    }
+    __syncthreads();
+    if (s_bad) {  // not written; every CTA of the row sees the same
+      row_b = -1;
+      continue;
+    }
+    for (int i = tid; i < M * hd; i += kThreads) {
+      const int r = i / hd, d = i - r * hd, rr = mt * M + r;
+      float v = 0.f;
+      if (r < nrows) {
+        const int t = rr / p.G, qh = seg.h * p.G + rr % p.G;
+        v = Vec<T>::scalar(reinterpret_cast<const T*>(p.q + seg.b * p.qr + t * p.qt) + qh * hd + d);
+      }
+      s_q[i] = v * p.scale_log2;
+    }
+    unsigned long long anc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = warp * 4 + k;
+      anc[k] = r < nrows ? s_anc[(mt * M + r) / p.G] : 0ull;
+    }
+    const long long crow = p.one_row ? 0 : seg.b;
+    const char* kbase = p.cache.base + crow * p.cache.srow + seg.h * p.cache.shead +
+                        static_cast<long long>(row.first) * hd * sizeof(T);
+    const char* vbase = kbase + p.cache.skv;
+    auto fetch = [&](int tile) {
+      const int stage = tile & 1;
+      for (int i = tid; i < kTile * vecs; i += kThreads) {
+        const int c = i / vecs, v = i - c * vecs, col = tile * kTile + c;
+        const bool in = col < row.cols;
+        const long long at = (static_cast<long long>(in ? col : 0) * vecs + v) * 16;
+        cp_async16(s_k + (stage * kTile + c) * pitch + v * 16, kbase + at, in);
+        cp_async16(s_v + (stage * kTile + c) * pitch + v * 16, vbase + at, in);
+      }
+      cp_async_commit();
+    };
+    float m[4], l[4];
+    float4 o[4][NB];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      m[k] = -INFINITY;
+      l[k] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) o[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    fetch(seg.tile0);
+    for (int tile = seg.tile0; tile < seg.tile1; ++tile) {
+      if (tile + 1 < seg.tile1) {
+        fetch(tile + 1);
+        cp_async_wait<1>();
+      } else {
+        cp_async_wait<0>();
+      }
+      __syncthreads();
+      const char* sk = s_k + ((tile & 1) * kTile + lane) * pitch;
+      const char* sv = s_v + (tile & 1) * kTile * pitch;
+      float z[4] = {0.f, 0.f, 0.f, 0.f};
+      const float* qrow = s_q + warp * 4 * hd;
+      for (int d = 0; d < hd; d += 4) {
+        const float4 kk = load4<T>(sk + d * sizeof(T));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 qq = *reinterpret_cast<const float4*>(qrow + k * hd + d);
+          z[k] = fmaf(qq.x, kk.x, z[k]);
+          z[k] = fmaf(qq.y, kk.y, z[k]);
+          z[k] = fmaf(qq.z, kk.z, z[k]);
+          z[k] = fmaf(qq.w, kk.w, z[k]);
+        }
+      }
+      const int col = tile * kTile + lane, node = col - row.old;
+      float4 pr;
+      float* pv = reinterpret_cast<float*>(&pr);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool see = node < 0 ? anc[k] != 0 : node < p.T && (anc[k] >> node & 1);
+        float s = see ? z[k] : -INFINITY;
+        float mx = s;
+#pragma unroll
+        for (int j = 16; j > 0; j >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, j));
+        const float mn = fmaxf(m[k], mx);
+        const float off = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every weight is zero
+        const float f = ex2(m[k] - off);
+        pv[k] = ex2(s - off);
+        float sum = pv[k];
+#pragma unroll
+        for (int j = 16; j > 0; j >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
+        l[k] = l[k] * f + sum;
+        m[k] = mn;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          o[k][j].x *= f;
+          o[k][j].y *= f;
+          o[k][j].z *= f;
+          o[k][j].w *= f;
+        }
+      }
+      s_p[lane] = pr;
+      __syncwarp();
+      // nodes' columns may hold anything where a row does not see them: weight 0 is skipped there
+      const int c_end = min(kTile, row.cols - tile * kTile), plain = min(c_end, max(0, row.old - tile * kTile));
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int d = j * 128 + lane * 4;
+        if (d < hd) {
+          for (int c = 0; c < plain; ++c) {
+            const float4 w = s_p[c], vv = load4<T>(sv + c * pitch + d * sizeof(T));
+            const float* wk = reinterpret_cast<const float*>(&w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[k][j].x = fmaf(wk[k], vv.x, o[k][j].x);
+              o[k][j].y = fmaf(wk[k], vv.y, o[k][j].y);
+              o[k][j].z = fmaf(wk[k], vv.z, o[k][j].z);
+              o[k][j].w = fmaf(wk[k], vv.w, o[k][j].w);
+            }
+          }
+          for (int c = plain; c < c_end; ++c) {
+            const float4 w = s_p[c], vv = load4<T>(sv + c * pitch + d * sizeof(T));
+            const float* wk = reinterpret_cast<const float*>(&w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (wk[k] != 0.f) {
+                o[k][j].x = fmaf(wk[k], vv.x, o[k][j].x);
+                o[k][j].y = fmaf(wk[k], vv.y, o[k][j].y);
+                o[k][j].z = fmaf(wk[k], vv.z, o[k][j].z);
+                o[k][j].w = fmaf(wk[k], vv.w, o[k][j].w);
+              }
+          }
+        }
+      }
+      __syncthreads();  // the stage may be filled again
+    }
+    // a row of no used node keeps l = 0; rows the committed columns alone
+    if (seg.tile0 > 0 || seg.tile1 < seg.tiles) {
+      const int slot = attn_slot(p, sh, g, mt, seg.unit0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = warp * 4 + k;
+        if (r >= nrows) continue;
+        if (lane == 0) p.part_ml[static_cast<long long>(slot) * M + r] = make_float2(m[k], l[k]);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int d = j * 128 + lane * 4;
+          if (d < hd)
+            *reinterpret_cast<float4*>(p.part_o + (static_cast<long long>(slot) * M + r) * hd + d) = o[k][j];
+        }
+      }
+      const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1);
+      const bool last = attn_last(p, seg.b, seg.h, mt, g1 - g0 + 1, &s_flag);
+      if (!last) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = warp * 4 + k;
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) o[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r >= nrows) continue;
+        for (int gg = g0; gg <= g1; ++gg) {
+          const long long at = static_cast<long long>(attn_slot(p, sh, gg, mt, seg.unit0)) * M + r;
+          const float2 ml = __ldcg(p.part_ml + at);
+          const float mn = fmaxf(m[k], ml.x), off = mn == -INFINITY ? 0.f : mn;
+          const float f = ex2(m[k] - off), f2 = ex2(ml.x - off);
+          l[k] = l[k] * f + ml.y * f2;
+          m[k] = mn;
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            const int d = j * 128 + lane * 4;
+            if (d < hd) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * hd + d));
+              o[k][j].x = o[k][j].x * f + v.x * f2;
+              o[k][j].y = o[k][j].y * f + v.y * f2;
+              o[k][j].z = o[k][j].z * f + v.z * f2;
+              o[k][j].w = o[k][j].w * f + v.w * f2;
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = warp * 4 + k, rr = mt * M + r;
+      if (r >= nrows) continue;
+      const int t = rr / p.G, qh = seg.h * p.G + rr % p.G;
+      const float inv = anc[k] ? 1.f / l[k] : 0.f;
+      char* y = p.out + seg.b * p.outr + t * p.outt + static_cast<long long>(qh) * hd * sizeof(T);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int d = j * 128 + lane * 4;
+        if (d < hd)
+          store4<T>(y + d * sizeof(T), make_float4(o[k][j].x * inv, o[k][j].y * inv,
+                                                   o[k][j].z * inv, o[k][j].w * inv));
+      }
+      if (p.lse && lane == 0)
+        p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + qh] =
+            anc[k] ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------- host
+
+struct AttnShape {
+  int M, MT, groups, grid, min_tiles;
+  size_t smem;
+};
+
+// Rows per M-tile, CTAs and shares of a shape; 0 CTAs if there is no device.
+AttnShape fma_shape(int es, int T, int G, int hd) {
+  AttnShape s = {};
+  const int rows = T * G;
+  const int RG = rows <= 4 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : 8;
+  s.M = RG * 4;
+  s.MT = (rows + s.M - 1) / s.M;
+  s.smem = fma_smem(RG, hd, es);
+  const int per_sm = std::max(1, std::min(8, static_cast<int>((220 * 1024) / (s.smem + 6 * 1024))));
+  s.groups = std::max(1, sm_count() * per_sm / s.MT);
+  s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
+  s.min_tiles = 2;
+  return s;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct AttnWorkspace {
+  size_t ticket, ml, o, bytes;  // offsets
+};
+AttnWorkspace attn_workspace(const AttnShape& s, int B, int H, int hd) {
+  AttnWorkspace w;
+  w.ticket = 0;
+  w.ml = round256(static_cast<size_t>(B) * H * s.MT * 4);
+  w.o = w.ml + round256(static_cast<size_t>(s.grid) * 2 * s.M * 8);
+  w.bytes = w.o + round256(static_cast<size_t>(s.grid) * 2 * s.M * hd * 4);
+  return w;
+}
+
+template <typename T, int RG, int NB>
+int launch_fma(const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
+  auto kernel = attn_fma_kernel<T, RG, NB>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(s.smem));
+  if (e != cudaSuccess) return map_cuda_error(e);
+  kernel<<<s.grid, RG * 32, s.smem, stream>>>(p);
+  return map_cuda_error(cudaGetLastError());
+}
+template <typename T, int NB>
+int launch_fma_rows(const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
+  switch (s.M) {
+    case 4: return launch_fma<T, 1, NB>(p, s, stream);
+    case 8: return launch_fma<T, 2, NB>(p, s, stream);
+    case 16: return launch_fma<T, 4, NB>(p, s, stream);
+    default: return launch_fma<T, 8, NB>(p, s, stream);
+  }
+}
+
+bool attn_sizes_ok(int dtype, int B, int T, int heads_q, int heads_kv, int head_dim) {
+  const int es = elem_size(dtype);
+  return es != 0 && B >= 1 && B <= kAttnMaxRows && T >= 1 && T <= SPECDEC_MAX_TREE &&
+         heads_kv >= 1 && heads_q >= heads_kv && heads_q % heads_kv == 0 && head_dim >= 1 &&
+         head_dim <= 256 && head_dim * es % 16 == 0 && heads_q <= 65536;
+}
+
+}  // namespace
+}  // namespace specdec
+
+extern "C" size_t specdec_tree_attention_workspace(int dtype, int B, int T, int heads_q,
+                                                   int heads_kv, int head_dim) {
+  using namespace specdec;
+  if (!attn_sizes_ok(dtype, B, T, heads_q, heads_kv, head_dim)) return 0;
+  const AttnShape s = fma_shape(elem_size(dtype), T, heads_q / heads_kv, head_dim);
+  return attn_workspace(s, B, heads_kv, head_dim).bytes;
+}
+
+extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void* stream) {
+  using namespace specdec;
+  if (!a) return SPECDEC_ERR_INVALID_ARG;
+  if (a->B < 0 || a->T < 1 || a->heads_q < 1 || a->layer < 0 || !std::isfinite(a->scale))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (a->B > kAttnMaxRows || a->T > SPECDEC_MAX_TREE) return SPECDEC_ERR_UNSUPPORTED;
+  if (a->B == 0) return SPECDEC_OK;
+  const int st = check_view(a->cache, 0);
+  if (st) return st;
+  const specdec_kv_view& c = a->cache;
+  const long long es = elem_size(c.dtype);
+  if (a->layer >= c.layers || !(c.rows >= a->B || c.rows == 1) || a->heads_q % c.heads)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!attn_sizes_ok(c.dtype, a->B, a->T, a->heads_q, c.heads, c.head_dim))
+    return SPECDEC_ERR_UNSUPPORTED;
+  if (!a->q || !a->out || !a->n_committed || !a->dev_status || !a->workspace)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!a->first_col && (!a->width || a->rows || (c.rows == 1 && a->B > 1)))
+    return SPECDEC_ERR_INVALID_ARG;
+  const long long strides = a->q_stride_row | a->q_stride_token | a->out_stride_row |
+                            a->out_stride_token;
+  if (a->q_stride_row < 0 || a->q_stride_token < 0 || a->out_stride_row < 0 ||
+      a->out_stride_token < 0)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(a->q) % 16 || reinterpret_cast<uintptr_t>(a->out) % 16 ||
+      (strides * es) % 16 || reinterpret_cast<uintptr_t>(a->lse) % 4)
+    return SPECDEC_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(a->workspace) % 256) return SPECDEC_ERR_INVALID_ARG;
+  if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
+  const int G = a->heads_q / c.heads;
+  const AttnShape s = fma_shape(static_cast<int>(es), a->T, G, c.head_dim);
+  const AttnWorkspace w = attn_workspace(s, a->B, c.heads, c.head_dim);
+  if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
+  AttnParams p = {};
+  p.cache = to_bytes(c);
+  p.cache.base += a->layer * p.cache.sl;
+  p.q = static_cast<const char*>(a->q);
+  p.out = static_cast<char*>(a->out);
+  p.lse = a->lse;
+  p.qr = a->q_stride_row * es;
+  p.qt = a->q_stride_token * es;
+  p.outr = a->out_stride_row * es;
+  p.outt = a->out_stride_token * es;
+  p.n_committed = a->n_committed;
+  p.width = a->width;
+  p.parents = a->parents;
+  p.rows = a->rows;
+  p.first_col = a->first_col;
+  p.status = a->dev_status;
+  char* ws = static_cast<char*>(a->workspace);
+  p.ticket = reinterpret_cast<unsigned*>(ws + w.ticket);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
+  p.scale_log2 = a->scale * kLog2e;
+  p.B = a->B;
+  p.T = a->T;
+  p.Hq = a->heads_q;
+  p.H = c.heads;
+  p.G = G;
+  p.hd = c.head_dim;
+  p.cap = c.cap_cols;
+  p.one_row = c.rows == 1 ? 1 : 0;
+  p.MT = s.MT;
+  p.groups = s.groups;
+  p.min_tiles = s.min_tiles;
+  cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  if (es == 2)
+    return c.head_dim <= 128 ? launch_fma_rows<uint16_t, 1>(p, s, stream_)
+                             : launch_fma_rows<uint16_t, 2>(p, s, stream_);
+  return c.head_dim <= 128 ? launch_fma_rows<float, 1>(p, s, stream_)
+                           : launch_fma_rows<float, 2>(p, s, stream_);
+}

@@ -1,0 +1,170 @@
+// What the tree attention kernels share: parameters, the split of the work, the partial results.
+//
+// The mathematics.  For a query row r (node t, query head) with scores z_c = scale * (q . k_c):
+//   m = max z_c, l = sum 2^((z_c - m) log2 e), o = sum 2^((z_c - m) log2 e) v_c,  out = o / l,
+// over any order of the columns in one pass: a larger maximum m' rescales l and o by 2^(m - m'),
+// and two parts of a row's columns merge the same way.
+//
+// The split.  A unit is one K/V head of one batch row: its columns are those of the row's
+// committed tokens and then of the T nodes, contiguous in the cache, cut into tiles.  All query
+// rows (node, query head of the group) of the unit use the same columns; M of them make an M-tile.
+// The tiles of all units, in order, are cut into equal contiguous shares, one per group of
+// MT CTAs (MT M-tiles), so ragged lengths leave no CTA idle and the MT CTAs that stream the same
+// columns do so at the same time (one DRAM read, the rest from L2).  A unit that lies in one share
+// is finished by its CTA; one cut by share borders is written as partial results (m, l, o) to the
+// workspace, and the CTA that takes the unit's last ticket merges them in share order, so results
+// do not depend on which CTA came last.  A share has at most two cut units (its first and last).
+#pragma once
+
+#include "tree.cuh"
+
+namespace specdec {
+
+constexpr int kAttnMaxRows = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnParams {
+  ByteView cache;  // of the layer, bytes
+  const char* q;
+  char* out;
+  float* lse;
+  long long qr, qt, outr, outt;  // bytes between rows and tokens
+  const int32_t *n_committed, *width, *parents, *rows, *first_col;
+  int32_t* status;
+  unsigned* ticket;  // [B * H * MT], zero between calls
+  float2* part_ml;   // [grid * 2][M]
+  float* part_o;     // [grid * 2][M][hd]
+  float scale_log2;  // scale * log2(e)
+  int B, T, Hq, H, G, hd, cap, one_row, MT, groups, min_tiles;
+};
+
+// One batch row's columns.
+struct AttnRow {
+  int first, old, cols;  // first column, committed columns N - 1, all columns N - 1 + T (0: error)
+};
+
+__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b, int* err) {
+  const int r = p.rows ? p.rows[b] : b;
+  *err = 0;
+  if (r < 0) {
+    *err = SPECDEC_ERR_INPUT_RANGE;
+    return AttnRow{0, 0, 0};
+  }
+  const int n = p.n_committed[r];
+  long long first;
+  bool bad = n < 1;
+  if (p.first_col) {
+    first = p.first_col[r];
+    bad |= first < 0;
+  } else {
+    const int W = *p.width;
+    bad |= n > W;
+    first = static_cast<long long>(W) - n;
+  }
+  if (bad) {
+    *err = SPECDEC_ERR_INPUT_RANGE;
+    return AttnRow{0, 0, 0};
+  }
+  if (first + n - 1 + p.T > p.cap) {
+    *err = SPECDEC_ERR_CAPACITY;
+    return AttnRow{0, 0, 0};
+  }
+  return AttnRow{static_cast<int>(first), n - 1, n - 1 + p.T};
+}
+
+// The plan in shared memory: tiles of the rows before row b, per K/V head.
+struct AttnPlan {
+  int pre[kAttnMaxRows + 1];
+};
+
+// Built by warp 0 of every CTA (the caller synchronises); CTA 0 records errors.
+__device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, AttnPlan& plan) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int tiles = 0;
+    if (b < p.B) {
+      int err;
+      const AttnRow r = attn_row(p, b, &err);
+      if (err && blockIdx.x == 0) set_status(p.status, err);
+      tiles = (r.cols + tile - 1) / tile;
+    }
+    int inc = tiles;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += o;
+    }
+    if (b < p.B) plan.pre[b] = carry + inc - tiles;
+    carry += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) plan.pre[p.B] = carry;
+}
+
+// Shares of the tile sequence: group g has [start(g), start(g + 1)).
+struct AttnShares {
+  long long total;
+  int groups;
+  __device__ long long start(int g) const { return total * g / groups; }
+  __device__ int owner(long long x) const {  // the largest g with start(g) <= x
+    return static_cast<int>(((x + 1) * groups - 1) / total);
+  }
+};
+__device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const AttnPlan& plan) {
+  AttnShares s;
+  s.total = static_cast<long long>(plan.pre[p.B]) * p.H;
+  const long long most = s.total / p.min_tiles;
+  s.groups = most < 1 ? 1 : most < p.groups ? static_cast<int>(most) : p.groups;
+  return s;
+}
+
+// A contiguous run of tiles of one unit inside a share.
+struct AttnSegment {
+  int b, h, tile0, tile1, tiles;  // unit, its tiles [tile0, tile1) of `tiles`
+  long long unit0;                // place of the unit's first tile in the sequence
+};
+__device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnPlan& plan,
+                                                    long long x, long long end) {
+  int lo = 0, hi = p.B - 1;  // the last row with pre * H <= x that has tiles
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<long long>(plan.pre[mid]) * p.H <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  AttnSegment s;
+  s.b = lo;
+  s.tiles = plan.pre[lo + 1] - plan.pre[lo];
+  const int rem = static_cast<int>(x - static_cast<long long>(plan.pre[lo]) * p.H);
+  s.h = rem / s.tiles;
+  s.tile0 = rem - s.h * s.tiles;
+  s.tile1 = static_cast<int>(min(static_cast<long long>(s.tiles), s.tile0 + (end - x)));
+  s.unit0 = x - s.tile0;
+  return s;
+}
+
+// Takes a ticket of the unit's M-tile mt; true in every thread for the CTA that took the last one
+// (the partial results of all are then visible to it).  n: CTAs that share the unit.
+__device__ __forceinline__ bool attn_last(const AttnParams& p, int b, int h, int mt, int n,
+                                          int* s_flag) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned* t = &p.ticket[(static_cast<long long>(b) * p.H + h) * p.MT + mt];
+    const unsigned old = atomicAdd(t, 1u);
+    *s_flag = old + 1 == static_cast<unsigned>(n);
+    if (*s_flag) *t = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  return *s_flag != 0;
+}
+
+// Slot of the partial result that share g's CTA of M-tile mt wrote for the unit that begins at
+// unit0: 0 if its segment starts the share, else 1.
+__device__ __forceinline__ int attn_slot(const AttnParams& p, const AttnShares& sh, int g, int mt,
+                                         long long unit0) {
+  return 2 * (g * p.MT + mt) + (sh.start(g) >= unit0 ? 0 : 1);
+}
+
+}  // namespace specdec

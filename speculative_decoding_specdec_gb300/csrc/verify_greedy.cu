@@ -37,44 +37,6 @@ constexpr int kMinUnits = 512;      // fewest units a CTA is given
 constexpr int kMaxSegs = 1024;      // row segments one CTA may touch (shared-memory key slots)
 constexpr long long kMaxShare = 1LL << 30;  // units per CTA, at most (32-bit local offsets)
 
-// Score -> unsigned integer with the same order (-0 counted as +0).  NaN is never encoded.
-__device__ __forceinline__ uint32_t order_bits(float f) {
-  const uint32_t u = (f == 0.f) ? 0u : __float_as_uint(f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-// Key of (score, index): larger score first, then lower index.  0 means "no element".
-__device__ __forceinline__ unsigned long long make_key(float v, int i) {
-  return (static_cast<unsigned long long>(order_bits(v)) << 32) | static_cast<uint32_t>(~i);
-}
-
-// Fold one element (indices visited in ascending order by this thread) into the running best.
-// NaN is never taken; the first non-NaN element of a row is always taken (even -inf).
-__device__ __forceinline__ void take(float x, int e, float& bv, int& bi) {
-  if (x == x && (bi < 0 || x > bv)) { bv = x; bi = e; }
-}
-
-// Fold N consecutive elements starting at index e0 (max tree, first occurrence).
-template <int N>
-__device__ __forceinline__ void take_vector(const float* x, int e0, float& bv, int& bi) {
-  float t[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) t[k] = x[k];
-#pragma unroll
-  for (int w = N / 2; w > 0; w >>= 1)
-#pragma unroll
-    for (int k = 0; k < w; ++k) t[k] = fmaxf(t[k], t[k + w]);  // fmaxf drops NaN operands
-  const float m = t[0];
-  if (m == m && (bi < 0 || m > bv)) {
-    int k = 0;
-#pragma unroll
-    for (int q = N - 1; q >= 0; --q)
-      if (x[q] == m) k = q;  // first occurrence
-    bv = m;
-    bi = e0 + k;
-  }
-}
-
 __device__ __forceinline__ void red_max_gpu(unsigned long long* p, unsigned long long v) {
   asm volatile("red.relaxed.gpu.global.max.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }

@@ -23,6 +23,7 @@ F32, BF16 = 0, 1
 MAX_DRAFT = 31
 GREEDY_SCRATCH_BYTES = 73728   # SPECDEC_GREEDY_SCRATCH_BYTES
 REALIGN_PDL = 1                # SPECDEC_REALIGN_PDL
+MAX_TREE = 64                  # SPECDEC_MAX_TREE
 
 c_i32p = ctypes.POINTER(ctypes.c_int32)
 
@@ -82,6 +83,42 @@ class AdmitArgs(ctypes.Structure):
                 ("pool_ids", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("cache", KvView), ("layer", ctypes.c_int), ("B", ctypes.c_int),
+                ("T", ctypes.c_int), ("heads_q", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("table_len", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p),
+                ("q_stride_row", ctypes.c_longlong), ("q_stride_token", ctypes.c_longlong),
+                ("k_stride_row", ctypes.c_longlong), ("k_stride_token", ctypes.c_longlong),
+                ("v_stride_row", ctypes.c_longlong), ("v_stride_token", ctypes.c_longlong),
+                ("q_out_stride_row", ctypes.c_longlong),
+                ("q_out_stride_token", ctypes.c_longlong), ("table", ctypes.c_void_p),
+                ("n_committed", ctypes.c_void_p), ("width", ctypes.c_void_p),
+                ("parents", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("columns", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+class TreeAttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", KvView), ("layer", ctypes.c_int), ("B", ctypes.c_int),
+                ("T", ctypes.c_int), ("heads_q", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_stride_row", ctypes.c_longlong), ("q_stride_token", ctypes.c_longlong),
+                ("out_stride_row", ctypes.c_longlong), ("out_stride_token", ctypes.c_longlong),
+                ("n_committed", ctypes.c_void_p), ("width", ctypes.c_void_p),
+                ("parents", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("first_col", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p)]
+
+
+class TreeCommitArgs(ctypes.Structure):
+    _fields_ = [("src", KvView), ("dst", KvView), ("B", ctypes.c_int), ("T", ctypes.c_int),
+                ("D", ctypes.c_int), ("width", ctypes.c_void_p), ("width_dst", ctypes.c_void_p),
+                ("accept_len", ctypes.c_void_p), ("path", ctypes.c_void_p),
+                ("n_committed", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("first_col", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
 SLOT_FREE, SLOT_ACTIVE, SLOT_FINISHED_EOS, SLOT_FINISHED_LENGTH = range(4)
 
 
@@ -125,6 +162,20 @@ lib.specdec_pool_schedule.restype = _i
 lib.specdec_pool_schedule.argtypes = [ctypes.POINTER(ScheduleArgs), _vp]
 lib.specdec_pool_admit.restype = _i
 lib.specdec_pool_admit.argtypes = [ctypes.POINTER(AdmitArgs), _vp]
+lib.specdec_rotary_append.restype = _i
+lib.specdec_rotary_append.argtypes = [ctypes.POINTER(RotaryArgs), _vp]
+lib.specdec_tree_attention.restype = _i
+lib.specdec_tree_attention.argtypes = [ctypes.POINTER(TreeAttentionArgs), _vp]
+lib.specdec_tree_attention_workspace.restype = _sz
+lib.specdec_tree_attention_workspace.argtypes = [_i, _i, _i, _i, _i, _i]
+lib.specdec_verify_tree_greedy.restype = _i
+lib.specdec_verify_tree_greedy.argtypes = [_vp, _i, _i, _i, _i, _ll, _vp, _vp, _i, _vp, _vp, _vp,
+                                           _vp, _vp, _vp]
+lib.specdec_verify_tree_sample.restype = _i
+lib.specdec_verify_tree_sample.argtypes = [_vp, _vp, _i, _i, _i, _i, _ll, _f, _vp, _vp, _vp, _i,
+                                           _i, _vp, _vp, _vp, _vp, _vp, _vp]
+lib.specdec_tree_commit.restype = _i
+lib.specdec_tree_commit.argtypes = [ctypes.POINTER(TreeCommitArgs), _vp]
 _i64, _i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
 lib.specdec_arena_create.restype = _i
 lib.specdec_arena_create.argtypes = [_i64, ctypes.POINTER(_vp)]
@@ -518,6 +569,187 @@ def pool_admit(slots, cols, caps, limits, prompt_ids, prompt_off, D, arena_cols,
                     ("dev_status", status)):
         setattr(a, name, t.data_ptr())
     _check(lib.specdec_pool_admit(ctypes.byref(a), _stream(stream)), "specdec_pool_admit")
+
+
+# ------------------------------------------------------------------------ tree speculation
+
+def _int32s(t, shape, name, optional=False):
+    """Device address of a contiguous int32 CUDA tensor of that shape (None if optional)."""
+    if t is None and optional:
+        return None
+    if (t.dtype is not torch.int32 or not t.is_cuda or t.shape != shape
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {list(shape)} int32 CUDA tensor")
+    return t.data_ptr()
+
+
+def _per_row(t, name, optional=False):
+    """Device address of a contiguous int32 CUDA tensor with one value per row or slot."""
+    if t is None and optional:
+        return None
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    return t.data_ptr()
+
+
+def _new_tokens(t, B, T, H, cache, name):
+    """(address, row stride, token stride) of a [B, T, H, head_dim] tensor of the cache's dtype
+    whose heads are contiguous."""
+    hd = cache.shape[5]
+    if t.shape != (B, T, H, hd) or t.dtype != cache.dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a [{B}, {T}, {H}, {hd}] {cache.dtype} CUDA tensor")
+    s = t.stride()
+    if s[3] != 1 or (s[2] != hd and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), s[0], s[1]
+
+
+def rotary_append(q, k, v, cache, layer, table, q_out, status, n_committed=None, width=None,
+                  parents=None, positions=None, columns=None, interleaved=False, stream=None):
+    """Rotary positions of the new tokens' q [B, T, Hq, hd] (into ``q_out``) and k [B, T, H, hd],
+    and the append of k and v to their columns of ``cache`` [L, 2, rows, H, cap, hd], layer
+    ``layer``.  ``table`` [positions, rot_dim / 2, 2] float32 holds cosines and sines.  Columns and
+    positions come from a verification pass (``n_committed``, ``width`` and ``parents``, None for a
+    chain) or are given (``positions``, ``columns`` [B, T], negative columns: padding)."""
+    B, T, Hq, hd = q.shape
+    a = RotaryArgs()
+    a.cache = kv_view(cache)
+    a.layer, a.B, a.T, a.heads_q = int(layer), B, T, Hq
+    if (table.dim() != 3 or table.shape[2] != 2 or table.dtype is not torch.float32
+            or not table.is_cuda or not table.is_contiguous()):
+        raise ValueError("table must be a contiguous [positions, rot_dim / 2, 2] float32 CUDA tensor")
+    a.rot_dim, a.interleaved, a.table_len = 2 * table.shape[1], int(bool(interleaved)), table.shape[0]
+    a.table = table.data_ptr()
+    H = cache.shape[3]
+    a.q, a.q_stride_row, a.q_stride_token = _new_tokens(q, B, T, Hq, cache, "q")
+    a.k, a.k_stride_row, a.k_stride_token = _new_tokens(k, B, T, H, cache, "k")
+    a.v, a.v_stride_row, a.v_stride_token = _new_tokens(v, B, T, H, cache, "v")
+    a.q_out, a.q_out_stride_row, a.q_out_stride_token = _new_tokens(q_out, B, T, Hq, cache, "q_out")
+    if positions is None and columns is None:
+        a.n_committed = _int32s(n_committed, (B,), "n_committed")
+        a.width = _per_row(width, "width")
+        a.parents = _int32s(parents, (B, T), "parents", True)
+    else:
+        if n_committed is not None or width is not None or parents is not None:
+            raise ValueError("positions and columns exclude n_committed, width and parents")
+        a.positions = _int32s(positions, (B, T), "positions")
+        a.columns = _int32s(columns, (B, T), "columns")
+    a.dev_status = _per_row(status, "status")
+    _check(lib.specdec_rotary_append(ctypes.byref(a), _stream(stream)), "specdec_rotary_append")
+
+
+def tree_attention_workspace_bytes(q, cache) -> int:
+    """Workspace bytes tree_attention needs for this q [B, T, Hq, hd] over this cache, whatever
+    the lengths."""
+    B, T, Hq, hd = q.shape
+    return int(lib.specdec_tree_attention_workspace(dtype_code(q.dtype), B, T, Hq, cache.shape[3],
+                                                    hd))
+
+
+def tree_attention(q, cache, layer, out, n_committed, width, parents, status, workspace,
+                   scale=None, lse=None, rows=None, first_col=None, stream=None):
+    """Attention of a verification pass: q [B, T, Hq, hd] (node 0 the pending token, the others the
+    drafted tree of ``parents`` [B, T], None for a chain) against every row's committed columns of
+    ``cache`` [L, 2, rows, H, cap, hd], layer ``layer``, and the nodes' own ancestors, into
+    ``out`` (and ``lse`` [B, T, Hq] float32).  ``scale`` defaults to hd ** -0.5.  ``workspace``: a
+    zero-filled uint8 CUDA tensor of tree_attention_workspace_bytes(q, cache), reused as is.
+    ``first_col`` (and ``rows``): tokens elsewhere than right-aligned at ``width``, as in a pool's
+    arena."""
+    B, T, Hq, hd = q.shape
+    a = TreeAttentionArgs()
+    a.cache = kv_view(cache)
+    a.layer, a.B, a.T, a.heads_q = int(layer), B, T, Hq
+    a.scale = hd ** -0.5 if scale is None else float(scale)
+    a.q, a.q_stride_row, a.q_stride_token = _new_tokens(q, B, T, Hq, cache, "q")
+    a.out, a.out_stride_row, a.out_stride_token = _new_tokens(out, B, T, Hq, cache, "out")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.shape != (B, T, Hq) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [B, T, Hq] float32 tensor")
+        a.lse = lse.data_ptr()
+    a.n_committed = (_int32s(n_committed, (B,), "n_committed") if rows is None
+                     else _per_row(n_committed, "n_committed"))
+    a.width = _per_row(width, "width", first_col is not None)
+    a.parents = _int32s(parents, (B, T), "parents", True)
+    a.rows = _int32s(rows, (B,), "rows", True)
+    a.first_col = _per_row(first_col, "first_col", True)
+    wp, a.workspace_bytes = _workspace(workspace, 0, "tree_attention")
+    a.workspace = wp
+    a.dev_status = _per_row(status, "status")
+    _check(lib.specdec_tree_attention(ctypes.byref(a), _stream(stream)), "specdec_tree_attention")
+
+
+def _tree_outputs(B, T, tokens, parents, accept_len, out_token, path, draft, status):
+    if path.dim() != 2:
+        raise ValueError("path must be [B, D]")
+    D = path.shape[1]
+    return (_int32s(tokens, (B, T), "tokens"), _int32s(parents, (B, T), "parents", True), D,
+            _int32s(accept_len, (B,), "accept_len"), _int32s(out_token, (B,), "out_token"),
+            _int32s(path, (B, D), "path"), _int32s(draft, (B, D), "draft"),
+            _per_row(status, "status"))
+
+
+def verify_tree_greedy(logits, tokens, parents, accept_len, out_token, path, draft, status,
+                       stream=None):
+    """Greedy verification of the trees (``tokens``, ``parents`` [B, T]; parents None: chains)
+    against the target's scores ``logits`` [B, T, V]: accept_len [B], out_token [B], the accepted
+    nodes ``path`` [B, D] (-1 behind them; the walk goes at most D deep) and their tokens ``draft``
+    [B, D] (0 behind them), ready for a realignment."""
+    B, T, V = logits.shape
+    rs = _score_rows(logits, B, T, "logits")
+    if not logits.is_cuda:
+        raise ValueError("logits: expected a CUDA tensor")
+    tok, par, D, a, y, pa, dr, st = _tree_outputs(B, T, tokens, parents, accept_len, out_token,
+                                                  path, draft, status)
+    _check(lib.specdec_verify_tree_greedy(logits.data_ptr(), dtype_code(logits.dtype), B, T, V, rs,
+                                          tok, par, D, a, y, pa, dr, st, _stream(stream)),
+           "specdec_verify_tree_greedy")
+
+
+def verify_tree_sample(target_logits, draft_logits, tokens, parents, uniforms, temperature,
+                       accept_len, out_token, path, draft, status, replacement=False,
+                       stream=None):
+    """Sampled verification of the trees against the target's [B, T, V] and the draft model's
+    [B, T, V] scores: uniforms [B, T] (column 0 for the final draw, column i for node i);
+    ``replacement`` if the draft model drew siblings independently, else without replacement.
+    Outputs as for verify_tree_greedy."""
+    B, T, V = target_logits.shape
+    rs = _score_rows(target_logits, B, T, "target_logits")
+    if (draft_logits.shape != target_logits.shape or draft_logits.dtype != target_logits.dtype
+            or _score_rows(draft_logits, B, T, "draft_logits") != rs):
+        raise ValueError("target and draft scores must share shape, dtype and row stride")
+    if (uniforms.dtype is not torch.float32 or uniforms.shape != (B, T)
+            or not uniforms.is_contiguous()):
+        raise ValueError("uniforms must be a contiguous [B, T] float32 tensor")
+    if not (target_logits.is_cuda and draft_logits.is_cuda and uniforms.is_cuda):
+        raise ValueError("scores and uniforms: expected CUDA tensors")
+    tok, par, D, a, y, pa, dr, st = _tree_outputs(B, T, tokens, parents, accept_len, out_token,
+                                                  path, draft, status)
+    _check(lib.specdec_verify_tree_sample(
+        target_logits.data_ptr(), draft_logits.data_ptr(), dtype_code(target_logits.dtype), B, T,
+        V, rs, float(temperature), tok, par, uniforms.data_ptr(), int(bool(replacement)), D, a, y,
+        pa, dr, st, _stream(stream)), "specdec_verify_tree_sample")
+
+
+def tree_commit(src, dst, width, accept_len, path, status, width_dst=None, nodes=MAX_TREE,
+                n_committed=None, rows=None, first_col=None, stream=None):
+    """Make the accepted paths' K/V columns contiguous (see specdec.h): in place (``dst`` is
+    ``src``) before a realignment, or into the realigned cache ``dst`` of width ``width_dst``
+    after it.  ``first_col`` (with ``n_committed`` and ``rows``): in a pool's arena."""
+    B, D = path.shape
+    a = TreeCommitArgs()
+    a.src = kv_view(src)
+    a.dst = a.src if dst is src else kv_view(dst)
+    a.B, a.T, a.D = B, int(nodes), D
+    a.width = _per_row(width, "width", first_col is not None)
+    a.width_dst = _per_row(width_dst, "width_dst", True)
+    a.accept_len = _int32s(accept_len, (B,), "accept_len")
+    a.path = _int32s(path, (B, D), "path")
+    a.n_committed = _per_row(n_committed, "n_committed", True)
+    a.rows = _int32s(rows, (B,), "rows", True)
+    a.first_col = _per_row(first_col, "first_col", True)
+    a.dev_status = _per_row(status, "status")
+    _check(lib.specdec_tree_commit(ctypes.byref(a), _stream(stream)), "specdec_tree_commit")
 
 
 class Arena:
