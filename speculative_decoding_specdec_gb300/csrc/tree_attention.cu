@@ -78,10 +78,10 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
   const AttnShares sh = attn_shares(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   if (sh.total == 0 || g >= sh.groups) return;
-  const long long x1 = sh.start(g + 1);
+  const int x1 = sh.start(g + 1);
   const int nrows = min(M, p.T * p.G - mt * M);  // query rows of this M-tile: (node, head) pairs
   int row_b = -1;
-  for (long long x = sh.start(g); x < x1;) {
+  for (int x = sh.start(g); x < x1;) {
     const AttnSegment seg = attn_segment(p, plan, x, x1);
     x += seg.tile1 - seg.tile0;
     int err;
@@ -302,8 +302,9 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
 // ------------------------------------------------------------------------------------- host
 
 struct AttnShape {
-  int M, MT, groups, grid, min_tiles;
+  int M, MT, groups, grid, tile, min_tiles;
   size_t smem;
+  bool tc;
 };
 
 // Rows per M-tile, CTAs and shares of a shape; 0 CTAs if there is no device.
@@ -317,6 +318,20 @@ AttnShape fma_shape(int es, int T, int G, int hd) {
   const int per_sm = std::max(1, std::min(8, static_cast<int>((220 * 1024) / (s.smem + 6 * 1024))));
   s.groups = std::max(1, sm_count() * per_sm / s.MT);
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
+  s.tile = kTile;
+  s.min_tiles = 2;
+  return s;
+}
+
+// The kernel and its shape: tensor cores for bf16 heads of 64 and 128 values.
+AttnShape attn_shape(int es, int T, int G, int hd) {
+  if (es != 2 || (hd != 64 && hd != 128) || T * G <= 16) return fma_shape(es, T, G, hd);
+  AttnShape s = {};
+  s.tc = true;
+  attn_tc_shape(T * G, &s.M, &s.MT);
+  s.groups = std::max(1, sm_count() / s.MT);
+  s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
+  s.tile = 128;
   s.min_tiles = 2;
   return s;
 }
@@ -368,7 +383,7 @@ extern "C" size_t specdec_tree_attention_workspace(int dtype, int B, int T, int 
                                                    int heads_kv, int head_dim) {
   using namespace specdec;
   if (!attn_sizes_ok(dtype, B, T, heads_q, heads_kv, head_dim)) return 0;
-  const AttnShape s = fma_shape(elem_size(dtype), T, heads_q / heads_kv, head_dim);
+  const AttnShape s = attn_shape(elem_size(dtype), T, heads_q / heads_kv, head_dim);
   return attn_workspace(s, B, heads_kv, head_dim).bytes;
 }
 
@@ -402,9 +417,15 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   if (reinterpret_cast<uintptr_t>(a->workspace) % 256) return SPECDEC_ERR_INVALID_ARG;
   if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
   const int G = a->heads_q / c.heads;
-  const AttnShape s = fma_shape(static_cast<int>(es), a->T, G, c.head_dim);
+  AttnShape s = attn_shape(static_cast<int>(es), a->T, G, c.head_dim);
+  // no more groups than the longest rows could give work to
+  const long long tiles = static_cast<long long>(a->B) * c.heads * ((c.cap_cols - 1) / s.tile + 1);
+  s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
+  s.grid = s.groups * s.MT;
   const AttnWorkspace w = attn_workspace(s, a->B, c.heads, c.head_dim);
   if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
+  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kTile + 2) >= (1LL << 31))
+    return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   AttnParams p = {};
   p.cache = to_bytes(c);
   p.cache.base += a->layer * p.cache.sl;
@@ -438,6 +459,7 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   p.groups = s.groups;
   p.min_tiles = s.min_tiles;
   cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  if (s.tc) return launch_attn_tc(p, c.rows, s.grid, stream_);
   if (es == 2)
     return c.head_dim <= 128 ? launch_fma_rows<uint16_t, 1>(p, s, stream_)
                              : launch_fma_rows<uint16_t, 2>(p, s, stream_);

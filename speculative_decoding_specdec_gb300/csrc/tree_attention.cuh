@@ -102,43 +102,46 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, AttnPla
   if (lane == 0) plan.pre[p.B] = carry;
 }
 
-// Shares of the tile sequence: group g has [start(g), start(g + 1)).
+// Shares of the tile sequence: group g has [start(g), start(g + 1)); the first `rem` have one tile
+// more than the others.  (32-bit: the host checks that the longest sequence fits.)
 struct AttnShares {
-  long long total;
-  int groups;
-  __device__ long long start(int g) const { return total * g / groups; }
-  __device__ int owner(long long x) const {  // the largest g with start(g) <= x
-    return static_cast<int>(((x + 1) * groups - 1) / total);
+  int total, groups, base, rem;
+  __device__ int start(int g) const { return g * base + min(g, rem); }
+  __device__ int owner(int x) const {  // the group whose share holds tile x
+    const int more = rem * (base + 1);
+    return x < more ? x / (base + 1) : rem + (x - more) / base;
   }
 };
 __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const AttnPlan& plan) {
   AttnShares s;
-  s.total = static_cast<long long>(plan.pre[p.B]) * p.H;
-  const long long most = s.total / p.min_tiles;
-  s.groups = most < 1 ? 1 : most < p.groups ? static_cast<int>(most) : p.groups;
+  s.total = plan.pre[p.B] * p.H;
+  const int most = s.total / p.min_tiles;
+  s.groups = most < 1 ? 1 : min(most, p.groups);
+  s.base = s.total / s.groups;
+  s.rem = s.total - s.base * s.groups;
   return s;
 }
 
 // A contiguous run of tiles of one unit inside a share.
 struct AttnSegment {
   int b, h, tile0, tile1, tiles;  // unit, its tiles [tile0, tile1) of `tiles`
-  long long unit0;                // place of the unit's first tile in the sequence
+  int unit0;                      // place of the unit's first tile in the sequence
 };
 __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnPlan& plan,
-                                                    long long x, long long end) {
-  int lo = 0, hi = p.B - 1;  // the last row with pre * H <= x that has tiles
+                                                    int x, int end) {
+  int lo = 0, hi = p.B - 1;  // the last row with pre * H <= x: it has tiles
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<long long>(plan.pre[mid]) * p.H <= x) lo = mid;
+    if (plan.pre[mid] * p.H <= x) lo = mid;
     else hi = mid - 1;
   }
   AttnSegment s;
   s.b = lo;
   s.tiles = plan.pre[lo + 1] - plan.pre[lo];
-  const int rem = static_cast<int>(x - static_cast<long long>(plan.pre[lo]) * p.H);
+  const int rem = x - plan.pre[lo] * p.H;
   s.h = rem / s.tiles;
   s.tile0 = rem - s.h * s.tiles;
-  s.tile1 = static_cast<int>(min(static_cast<long long>(s.tiles), s.tile0 + (end - x)));
+  s.tile1 = min(s.tiles, s.tile0 + (end - x));
   s.unit0 = x - s.tile0;
   return s;
 }
@@ -163,8 +166,13 @@ __device__ __forceinline__ bool attn_last(const AttnParams& p, int b, int h, int
 // Slot of the partial result that share g's CTA of M-tile mt wrote for the unit that begins at
 // unit0: 0 if its segment starts the share, else 1.
 __device__ __forceinline__ int attn_slot(const AttnParams& p, const AttnShares& sh, int g, int mt,
-                                         long long unit0) {
+                                         int unit0) {
   return 2 * (g * p.MT + mt) + (sh.start(g) >= unit0 ? 0 : 1);
 }
+
+// The tensor-core kernel (tree_attention_tc.cu): rows per M-tile and M-tiles for R query rows per
+// K/V head, and its launch (rows: of the cache).
+void attn_tc_shape(int R, int* M, int* MT);
+int launch_attn_tc(const AttnParams& p, int rows, int grid, cudaStream_t stream);
 
 }  // namespace specdec

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -163,9 +164,9 @@ lib.specdec_pool_schedule.argtypes = [ctypes.POINTER(ScheduleArgs), _vp]
 lib.specdec_pool_admit.restype = _i
 lib.specdec_pool_admit.argtypes = [ctypes.POINTER(AdmitArgs), _vp]
 lib.specdec_rotary_append.restype = _i
-lib.specdec_rotary_append.argtypes = [ctypes.POINTER(RotaryArgs), _vp]
+lib.specdec_rotary_append.argtypes = [_vp, _vp]  # specdec_rotary_args
 lib.specdec_tree_attention.restype = _i
-lib.specdec_tree_attention.argtypes = [ctypes.POINTER(TreeAttentionArgs), _vp]
+lib.specdec_tree_attention.argtypes = [_vp, _vp]  # specdec_tree_attention_args
 lib.specdec_tree_attention_workspace.restype = _sz
 lib.specdec_tree_attention_workspace.argtypes = [_i, _i, _i, _i, _i, _i]
 lib.specdec_verify_tree_greedy.restype = _i
@@ -175,7 +176,7 @@ lib.specdec_verify_tree_sample.restype = _i
 lib.specdec_verify_tree_sample.argtypes = [_vp, _vp, _i, _i, _i, _i, _ll, _f, _vp, _vp, _vp, _i,
                                            _i, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.specdec_tree_commit.restype = _i
-lib.specdec_tree_commit.argtypes = [ctypes.POINTER(TreeCommitArgs), _vp]
+lib.specdec_tree_commit.argtypes = [_vp, _vp]  # specdec_tree_commit_args
 _i64, _i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
 lib.specdec_arena_create.restype = _i
 lib.specdec_arena_create.argtypes = [_i64, ctypes.POINTER(_vp)]
@@ -572,34 +573,65 @@ def pool_admit(slots, cols, caps, limits, prompt_ids, prompt_off, D, arena_cols,
 
 
 # ------------------------------------------------------------------------ tree speculation
+#
+# One of these calls is made per layer and round, and the smallest take a few microseconds on the
+# GPU, so the marshalling is kept short: each argument struct is packed by one call (the formats
+# lay out the ctypes structures above), and a tensor's layout is read once.
 
-def _int32s(t, shape, name, optional=False):
-    """Device address of a contiguous int32 CUDA tensor of that shape (None if optional)."""
-    if t is None and optional:
-        return None
+_KV = "Pqqqqiiiiii"
+_PACK_ROTARY = struct.Struct("@" + _KV + "iiiiiii" + "PPPP" + "qqqqqqqq" + "PPPPPPP")
+_PACK_ATTENTION = struct.Struct("@" + _KV + "iiiif" + "PPP" + "qqqq" + "PPPPPPnP")
+_PACK_COMMIT = struct.Struct("@" + _KV + _KV + "iii" + "PPPPPPPP")
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_cuda_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _raw(stream):
+    return _raw_stream(_cuda_device()) if stream is None else stream.cuda_stream
+
+
+def _kv(t):
+    """The fields of specdec_kv_view for a cache [L, 2, rows, H, cap, head_dim]."""
+    shape, s, code = t.shape, t.stride(), _DTYPES.get(t.dtype)
+    if len(shape) != 6 or shape[1] != 2:
+        raise ValueError("cache must be [L, 2, rows, H, cap, head_dim]")
+    hd = shape[5]
+    if s[5] != 1 or s[4] != hd or code is None or not t.is_cuda:
+        raise ValueError("cache must be a float32 or bfloat16 CUDA tensor with contiguous columns")
+    return t.data_ptr(), s[0], s[1], s[2], s[3], code, shape[0], shape[2], shape[3], hd, shape[4]
+
+
+def _ints(t, shape, name):
+    """Device address of a contiguous int32 CUDA tensor of that shape; of None, 0."""
+    if t is None:
+        return 0
     if (t.dtype is not torch.int32 or not t.is_cuda or t.shape != shape
             or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {list(shape)} int32 CUDA tensor")
     return t.data_ptr()
 
 
-def _per_row(t, name, optional=False):
-    """Device address of a contiguous int32 CUDA tensor with one value per row or slot."""
-    if t is None and optional:
-        return None
+def _ints_of_any(t, name):
+    """Device address of a contiguous int32 CUDA tensor (one value, or one per slot); of None, 0."""
+    if t is None:
+        return 0
     if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
     return t.data_ptr()
 
 
-def _new_tokens(t, B, T, H, cache, name):
-    """(address, row stride, token stride) of a [B, T, H, head_dim] tensor of the cache's dtype
-    whose heads are contiguous."""
-    hd = cache.shape[5]
-    if t.shape != (B, T, H, hd) or t.dtype != cache.dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a [{B}, {T}, {H}, {hd}] {cache.dtype} CUDA tensor")
+def _given(t, name):
+    if t is None:
+        raise ValueError(f"{name} is needed")
+    return t
+
+
+def _tokens(t, shape, dtype, name):
+    """(address, row stride, token stride) of [B, T, heads, head_dim] whose heads are contiguous."""
     s = t.stride()
-    if s[3] != 1 or (s[2] != hd and H > 1):
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a {list(shape)} {dtype} CUDA tensor")
+    if s[3] != 1 or (s[2] != shape[3] and shape[2] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return t.data_ptr(), s[0], s[1]
 
@@ -611,31 +643,36 @@ def rotary_append(q, k, v, cache, layer, table, q_out, status, n_committed=None,
     ``layer``.  ``table`` [positions, rot_dim / 2, 2] float32 holds cosines and sines.  Columns and
     positions come from a verification pass (``n_committed``, ``width`` and ``parents``, None for a
     chain) or are given (``positions``, ``columns`` [B, T], negative columns: padding)."""
-    B, T, Hq, hd = q.shape
-    a = RotaryArgs()
-    a.cache = kv_view(cache)
-    a.layer, a.B, a.T, a.heads_q = int(layer), B, T, Hq
-    if (table.dim() != 3 or table.shape[2] != 2 or table.dtype is not torch.float32
-            or not table.is_cuda or not table.is_contiguous()):
+    view = _kv(cache)
+    dtype = cache.dtype
+    shape = q.shape
+    B, T, Hq, hd = shape
+    new = (B, T, view[8], view[9])
+    tab = table.shape
+    if (len(tab) != 3 or tab[2] != 2 or table.dtype is not torch.float32 or not table.is_cuda
+            or not table.is_contiguous()):
         raise ValueError("table must be a contiguous [positions, rot_dim / 2, 2] float32 CUDA tensor")
-    a.rot_dim, a.interleaved, a.table_len = 2 * table.shape[1], int(bool(interleaved)), table.shape[0]
-    a.table = table.data_ptr()
-    H = cache.shape[3]
-    a.q, a.q_stride_row, a.q_stride_token = _new_tokens(q, B, T, Hq, cache, "q")
-    a.k, a.k_stride_row, a.k_stride_token = _new_tokens(k, B, T, H, cache, "k")
-    a.v, a.v_stride_row, a.v_stride_token = _new_tokens(v, B, T, H, cache, "v")
-    a.q_out, a.q_out_stride_row, a.q_out_stride_token = _new_tokens(q_out, B, T, Hq, cache, "q_out")
+    if hd != view[9]:
+        raise ValueError("q and the cache must have one head_dim")
+    qp, qr, qt = _tokens(q, shape, dtype, "q")
+    kp, kr, kt = _tokens(k, new, dtype, "k")
+    vp, vr, vt = _tokens(v, new, dtype, "v")
+    op, outr, outt = _tokens(q_out, shape, dtype, "q_out")
     if positions is None and columns is None:
-        a.n_committed = _int32s(n_committed, (B,), "n_committed")
-        a.width = _per_row(width, "width")
-        a.parents = _int32s(parents, (B, T), "parents", True)
+        where = (_ints(_given(n_committed, "n_committed"), (B,), "n_committed"),
+                 _ints_of_any(_given(width, "width"), "width"), _ints(parents, (B, T), "parents"),
+                 0, 0)
     else:
         if n_committed is not None or width is not None or parents is not None:
             raise ValueError("positions and columns exclude n_committed, width and parents")
-        a.positions = _int32s(positions, (B, T), "positions")
-        a.columns = _int32s(columns, (B, T), "columns")
-    a.dev_status = _per_row(status, "status")
-    _check(lib.specdec_rotary_append(ctypes.byref(a), _stream(stream)), "specdec_rotary_append")
+        where = (0, 0, 0, _ints(_given(positions, "positions"), (B, T), "positions"),
+                 _ints(_given(columns, "columns"), (B, T), "columns"))
+    args = _PACK_ROTARY.pack(*view, layer, B, T, Hq, 2 * tab[1], 1 if interleaved else 0, tab[0],
+                             qp, kp, vp, op, qr, qt, kr, kt, vr, vt, outr, outt, table.data_ptr(),
+                             *where, _ints_of_any(_given(status, "status"), "status"))
+    rc = lib.specdec_rotary_append(args, _raw(stream))
+    if rc:
+        _check(rc, "specdec_rotary_append")
 
 
 def tree_attention_workspace_bytes(q, cache) -> int:
@@ -655,38 +692,44 @@ def tree_attention(q, cache, layer, out, n_committed, width, parents, status, wo
     zero-filled uint8 CUDA tensor of tree_attention_workspace_bytes(q, cache), reused as is.
     ``first_col`` (and ``rows``): tokens elsewhere than right-aligned at ``width``, as in a pool's
     arena."""
-    B, T, Hq, hd = q.shape
-    a = TreeAttentionArgs()
-    a.cache = kv_view(cache)
-    a.layer, a.B, a.T, a.heads_q = int(layer), B, T, Hq
-    a.scale = hd ** -0.5 if scale is None else float(scale)
-    a.q, a.q_stride_row, a.q_stride_token = _new_tokens(q, B, T, Hq, cache, "q")
-    a.out, a.out_stride_row, a.out_stride_token = _new_tokens(out, B, T, Hq, cache, "out")
+    view = _kv(cache)
+    dtype = cache.dtype
+    shape = q.shape
+    B, T, Hq, hd = shape
+    if hd != view[9]:
+        raise ValueError("q and the cache must have one head_dim")
+    qp, qr, qt = _tokens(q, shape, dtype, "q")
+    op, outr, outt = _tokens(out, shape, dtype, "out")
+    lp = 0
     if lse is not None:
-        _need(lse, torch.float32, "lse")
-        if lse.shape != (B, T, Hq) or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous [B, T, Hq] float32 tensor")
-        a.lse = lse.data_ptr()
-    a.n_committed = (_int32s(n_committed, (B,), "n_committed") if rows is None
-                     else _per_row(n_committed, "n_committed"))
-    a.width = _per_row(width, "width", first_col is not None)
-    a.parents = _int32s(parents, (B, T), "parents", True)
-    a.rows = _int32s(rows, (B,), "rows", True)
-    a.first_col = _per_row(first_col, "first_col", True)
-    wp, a.workspace_bytes = _workspace(workspace, 0, "tree_attention")
-    a.workspace = wp
-    a.dev_status = _per_row(status, "status")
-    _check(lib.specdec_tree_attention(ctypes.byref(a), _stream(stream)), "specdec_tree_attention")
+        if (lse.dtype is not torch.float32 or lse.shape != (B, T, Hq) or not lse.is_cuda
+                or not lse.is_contiguous()):
+            raise ValueError("lse must be a contiguous [B, T, Hq] float32 CUDA tensor")
+        lp = lse.data_ptr()
+    np_ = (_ints(_given(n_committed, "n_committed"), (B,), "n_committed") if rows is None
+           else _ints_of_any(_given(n_committed, "n_committed"), "n_committed"))
+    if (workspace.dtype is not torch.uint8 or not workspace.is_cuda
+            or not workspace.is_contiguous()):
+        raise ValueError("tree_attention: workspace must be a contiguous CUDA uint8 tensor")
+    args = _PACK_ATTENTION.pack(
+        *view, layer, B, T, Hq, hd ** -0.5 if scale is None else scale, qp, op, lp, qr, qt, outr,
+        outt, np_, _ints_of_any(width, "width"), _ints(parents, (B, T), "parents"),
+        _ints(rows, (B,), "rows"), _ints_of_any(first_col, "first_col"), workspace.data_ptr(),
+        workspace.numel(), _ints_of_any(_given(status, "status"), "status"))
+    rc = lib.specdec_tree_attention(args, _raw(stream))
+    if rc:
+        _check(rc, "specdec_tree_attention")
 
 
-def _tree_outputs(B, T, tokens, parents, accept_len, out_token, path, draft, status):
-    if path.dim() != 2:
-        raise ValueError("path must be [B, D]")
-    D = path.shape[1]
-    return (_int32s(tokens, (B, T), "tokens"), _int32s(parents, (B, T), "parents", True), D,
-            _int32s(accept_len, (B,), "accept_len"), _int32s(out_token, (B,), "out_token"),
-            _int32s(path, (B, D), "path"), _int32s(draft, (B, D), "draft"),
-            _per_row(status, "status"))
+def _scores(t, name):
+    """(address, dtype code, B, T, V, row stride) of evenly spaced score rows [B, T, V]."""
+    shape, s, code = t.shape, t.stride(), _DTYPES.get(t.dtype)
+    if len(shape) != 3 or s[2] != 1 or (shape[0] > 1 and s[0] != shape[1] * s[1]):
+        raise ValueError(f"{name}: expected [B, T, V] with evenly spaced rows of unit stride")
+    if code is None or not t.is_cuda:
+        raise ValueError(f"{name}: expected a float32 or bfloat16 CUDA tensor")
+    # (a row stride below V, as an expanded tensor has, is refused by the library)
+    return t.data_ptr(), code, shape[0], shape[1], shape[2], s[1]
 
 
 def verify_tree_greedy(logits, tokens, parents, accept_len, out_token, path, draft, status,
@@ -695,15 +738,18 @@ def verify_tree_greedy(logits, tokens, parents, accept_len, out_token, path, dra
     against the target's scores ``logits`` [B, T, V]: accept_len [B], out_token [B], the accepted
     nodes ``path`` [B, D] (-1 behind them; the walk goes at most D deep) and their tokens ``draft``
     [B, D] (0 behind them), ready for a realignment."""
-    B, T, V = logits.shape
-    rs = _score_rows(logits, B, T, "logits")
-    if not logits.is_cuda:
-        raise ValueError("logits: expected a CUDA tensor")
-    tok, par, D, a, y, pa, dr, st = _tree_outputs(B, T, tokens, parents, accept_len, out_token,
-                                                  path, draft, status)
-    _check(lib.specdec_verify_tree_greedy(logits.data_ptr(), dtype_code(logits.dtype), B, T, V, rs,
-                                          tok, par, D, a, y, pa, dr, st, _stream(stream)),
-           "specdec_verify_tree_greedy")
+    zp, code, B, T, V, rs = _scores(logits, "logits")
+    D = path.shape[-1]
+    one, two, tree = (B,), (B, D), (B, T)
+    rc = lib.specdec_verify_tree_greedy(
+        zp, code, B, T, V, rs, _ints(_given(tokens, "tokens"), tree, "tokens"),
+        _ints(parents, tree, "parents"), D,
+        _ints(_given(accept_len, "accept_len"), one, "accept_len"),
+        _ints(_given(out_token, "out_token"), one, "out_token"), _ints(path, two, "path"),
+        _ints(_given(draft, "draft"), two, "draft"),
+        _ints_of_any(_given(status, "status"), "status"), _raw(stream))
+    if rc:
+        _check(rc, "specdec_verify_tree_greedy")
 
 
 def verify_tree_sample(target_logits, draft_logits, tokens, parents, uniforms, temperature,
@@ -713,22 +759,25 @@ def verify_tree_sample(target_logits, draft_logits, tokens, parents, uniforms, t
     [B, T, V] scores: uniforms [B, T] (column 0 for the final draw, column i for node i);
     ``replacement`` if the draft model drew siblings independently, else without replacement.
     Outputs as for verify_tree_greedy."""
-    B, T, V = target_logits.shape
-    rs = _score_rows(target_logits, B, T, "target_logits")
-    if (draft_logits.shape != target_logits.shape or draft_logits.dtype != target_logits.dtype
-            or _score_rows(draft_logits, B, T, "draft_logits") != rs):
+    zp, *like = _scores(target_logits, "target_logits")
+    wp, *same = _scores(draft_logits, "draft_logits")
+    if like != same:
         raise ValueError("target and draft scores must share shape, dtype and row stride")
-    if (uniforms.dtype is not torch.float32 or uniforms.shape != (B, T)
+    code, B, T, V, rs = like
+    D = path.shape[-1]
+    one, two, tree = (B,), (B, D), (B, T)
+    if (uniforms.dtype is not torch.float32 or uniforms.shape != tree or not uniforms.is_cuda
             or not uniforms.is_contiguous()):
-        raise ValueError("uniforms must be a contiguous [B, T] float32 tensor")
-    if not (target_logits.is_cuda and draft_logits.is_cuda and uniforms.is_cuda):
-        raise ValueError("scores and uniforms: expected CUDA tensors")
-    tok, par, D, a, y, pa, dr, st = _tree_outputs(B, T, tokens, parents, accept_len, out_token,
-                                                  path, draft, status)
-    _check(lib.specdec_verify_tree_sample(
-        target_logits.data_ptr(), draft_logits.data_ptr(), dtype_code(target_logits.dtype), B, T,
-        V, rs, float(temperature), tok, par, uniforms.data_ptr(), int(bool(replacement)), D, a, y,
-        pa, dr, st, _stream(stream)), "specdec_verify_tree_sample")
+        raise ValueError("uniforms must be a contiguous [B, T] float32 CUDA tensor")
+    rc = lib.specdec_verify_tree_sample(
+        zp, wp, code, B, T, V, rs, temperature, _ints(_given(tokens, "tokens"), tree, "tokens"),
+        _ints(parents, tree, "parents"), uniforms.data_ptr(), 1 if replacement else 0, D,
+        _ints(_given(accept_len, "accept_len"), one, "accept_len"),
+        _ints(_given(out_token, "out_token"), one, "out_token"), _ints(path, two, "path"),
+        _ints(_given(draft, "draft"), two, "draft"),
+        _ints_of_any(_given(status, "status"), "status"), _raw(stream))
+    if rc:
+        _check(rc, "specdec_verify_tree_sample")
 
 
 def tree_commit(src, dst, width, accept_len, path, status, width_dst=None, nodes=MAX_TREE,
@@ -737,19 +786,17 @@ def tree_commit(src, dst, width, accept_len, path, status, width_dst=None, nodes
     ``src``) before a realignment, or into the realigned cache ``dst`` of width ``width_dst``
     after it.  ``first_col`` (with ``n_committed`` and ``rows``): in a pool's arena."""
     B, D = path.shape
-    a = TreeCommitArgs()
-    a.src = kv_view(src)
-    a.dst = a.src if dst is src else kv_view(dst)
-    a.B, a.T, a.D = B, int(nodes), D
-    a.width = _per_row(width, "width", first_col is not None)
-    a.width_dst = _per_row(width_dst, "width_dst", True)
-    a.accept_len = _int32s(accept_len, (B,), "accept_len")
-    a.path = _int32s(path, (B, D), "path")
-    a.n_committed = _per_row(n_committed, "n_committed", True)
-    a.rows = _int32s(rows, (B,), "rows", True)
-    a.first_col = _per_row(first_col, "first_col", True)
-    a.dev_status = _per_row(status, "status")
-    _check(lib.specdec_tree_commit(ctypes.byref(a), _stream(stream)), "specdec_tree_commit")
+    one = (B,)
+    sv = _kv(src)
+    args = _PACK_COMMIT.pack(
+        *sv, *(sv if dst is src else _kv(dst)), B, nodes, D, _ints_of_any(width, "width"),
+        _ints_of_any(width_dst, "width_dst"),
+        _ints(_given(accept_len, "accept_len"), one, "accept_len"), _ints(path, (B, D), "path"),
+        _ints_of_any(n_committed, "n_committed"), _ints(rows, one, "rows"),
+        _ints_of_any(first_col, "first_col"), _ints_of_any(_given(status, "status"), "status"))
+    rc = lib.specdec_tree_commit(args, _raw(stream))
+    if rc:
+        _check(rc, "specdec_tree_commit")
 
 
 class Arena:
