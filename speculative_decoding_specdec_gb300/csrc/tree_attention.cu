@@ -304,8 +304,9 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
 struct AttnShape {
   int M, MT, groups, grid, tile, min_tiles;
   size_t smem;
-  bool tc;
+  int kind;
 };
+enum { kFma = 0, kMma = 1, kTc = 2 };
 
 // Rows per M-tile, CTAs and shares of a shape; 0 CTAs if there is no device.
 AttnShape fma_shape(int es, int T, int G, int hd) {
@@ -323,16 +324,23 @@ AttnShape fma_shape(int es, int T, int G, int hd) {
   return s;
 }
 
-// The kernel and its shape: tensor cores for bf16 heads of 64 and 128 values.
+// The kernel and its shape for bf16 heads of 64 and 128 values: 16-row or 256-row tiles on the
+// tensor cores, by the number of query rows.
 AttnShape attn_shape(int es, int T, int G, int hd) {
-  if (es != 2 || (hd != 64 && hd != 128) || T * G <= 16) return fma_shape(es, T, G, hd);
+  if (es != 2 || (hd != 64 && hd != 128)) return fma_shape(es, T, G, hd);
   AttnShape s = {};
-  s.tc = true;
-  attn_tc_shape(T * G, &s.M, &s.MT);
-  s.groups = std::max(1, sm_count() / s.MT);
+  int per_sm = 1;
+  if (T * G <= 16) {
+    s.kind = kMma;
+    attn_mma_shape(T * G, hd, &s.M, &s.MT, &per_sm);
+  } else {
+    s.kind = kTc;
+    attn_tc_shape(T * G, &s.M, &s.MT);
+  }
+  s.groups = std::max(1, sm_count() * per_sm / s.MT);
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
   s.tile = 128;
-  s.min_tiles = 2;
+  s.min_tiles = 1;
   return s;
 }
 
@@ -459,7 +467,8 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   p.groups = s.groups;
   p.min_tiles = s.min_tiles;
   cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
-  if (s.tc) return launch_attn_tc(p, c.rows, s.grid, stream_);
+  if (s.kind == kTc) return launch_attn_tc(p, c.rows, s.grid, stream_);
+  if (s.kind == kMma) return launch_attn_mma(p, c.rows, s.grid, stream_);
   if (es == 2)
     return c.head_dim <= 128 ? launch_fma_rows<uint16_t, 1>(p, s, stream_)
                              : launch_fma_rows<uint16_t, 2>(p, s, stream_);
