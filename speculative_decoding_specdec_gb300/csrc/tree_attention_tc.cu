@@ -27,12 +27,12 @@ namespace specdec {
 namespace {
 
 constexpr int kThreads = 384;  // the last two warps only make whole warpgroups of registers
-// Registers per thread: 384 x 168 at launch; 2 x 128 x 216 + 128 x 64 = 63488 of those 64512.
-constexpr int kRegsSoftmax = 216, kRegsOther = 64;
+// Registers per thread: 384 x 168 at launch; 2 x 128 x 224 + 128 x 56 = those 64512.
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 constexpr int kCols = 128;     // columns of a K/V tile
 constexpr int kRows = 128;     // rows of an accumulator
 constexpr int kStages = 2;
-constexpr uint32_t kTries = 1u << 17, kNs = 20000;  // a wait gives up after about 2.6 s
+constexpr uint32_t kTries = 1u << 22;  // polls after which a wait gives up
 constexpr float kGrow = 8.f;   // log2 of the growth of the maximum that is let pass
 
 __device__ __forceinline__ float ex2(float x) {
@@ -41,7 +41,7 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-  return mbar_wait_sleep(bar, parity, kTries, kNs);
+  return mbar_wait_bounded(bar, parity, kTries);
 }
 // The wait of a whole warp: one answer, so that its lanes stay together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -67,6 +67,31 @@ struct Bars {
 
 __device__ __forceinline__ bool inf_or_nan(uint32_t w) {  // either of two bf16 values
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// Pairs of floats: one instruction for two.
+__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return pack2u(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 template <int HD> struct Smem {
@@ -98,7 +123,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   __shared__ AttnPlan plan;
   __shared__ Bars bar;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_par[kMaxTree], s_flag, s_bad;
+  __shared__ int s_par[kMaxTree], s_bad;
   __shared__ unsigned long long s_anc[kMaxTree], s_poison;
   __shared__ float2 s_ml[kRows];
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
@@ -125,6 +150,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  pdl_launch_dependents();  // the merge of cut units may be set up
   const uint32_t tmem = s_tmem;
   const AttnShares sh = attn_shares(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
@@ -171,70 +197,94 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------------------- MMA
+    // The whole warp follows the jobs and one elected lane issues.  What an MMA's operands are made
+    // of is the same in all lanes and made so for the compiler to see (the shuffles): an MMA takes
+    // its descriptors from uniform registers, and moving them there lane by lane took longer than
+    // the products.
     constexpr uint32_t id_s = mma_idesc(kRows, kCols, false), id_o = mma_idesc(kRows, HD, true);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t sm = __shfl_sync(0xffffffffu, smem_addr(smem), 0);
+    const uint64_t q_desc = mma_desc(sm + S::q, 16, 1024), k_desc = mma_desc(sm + S::k, 16, 1024),
+                   v_desc = mma_desc(sm + S::v, kCols * 128, 1024);
+    const bool pair = __shfl_sync(0xffffffffu, two ? 1 : 0, 0) != 0;
     int kv = 0, seg_no = 0, done[2] = {0, 0};  // tiles, segments, jobs of A and B so far
     for (int x = x0; x < x1 && ok; ++seg_no) {
       const AttnSegment seg = attn_segment(p, plan, x, x1);
-      const int n = seg.tile1 - seg.tile0, jobs = two ? 2 * n : n;
+      const int n = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0), jobs = pair ? 2 * n : n;
       x += n;
       int err;
       const AttnRow row = attn_row(p, seg.b, &err);
-      // S = Q K^T of job i: tile i / 2 for A or B (two), or tile i
+      // columns from here on need care: tile `clean` holds the first of them
+      const int clean = row.old / kCols - seg.tile0;
+      // S = Q K^T of job i: tile i / 2 for A or B (pair), or tile i
+      auto k_ready = [&](int i) {
+        const int t = kv + (pair ? i >> 1 : i);
+        if (!pair || !(i & 1)) ok = ok && warp_wait(&bar.k_full[t % kStages], (t / kStages) & 1);
+      };
       auto scores = [&](int i) {
-        const int a = i & 1, t = kv + (two ? i >> 1 : i), st = t % kStages;
-        if (!two || a == 0) ok = ok && warp_wait(&bar.k_full[st], (t / kStages) & 1);
-        if (!ok) return;
-        if (lane == 0) {
-          const uint32_t qa = smem_addr(smem + S::q + (two ? a : 0) * S::kQ);
-          const uint32_t ka = smem_addr(smem + S::k + st * S::kTile);
+        const int a = i & 1, t = kv + (pair ? i >> 1 : i), st = t % kStages;
+        const uint64_t qa = q_desc + (pair ? a : 0) * (S::kQ / 16), ka = k_desc + st * (S::kTile / 16);
+        const uint32_t d = tm + a * kCols;
+        if (elect_one()) {
+#pragma unroll
           for (int s = 0; s < kSteps; ++s)
-            mma_ss(tmem + a * kCols,
-                   mma_desc(qa + (s >> 2) * kRows * 128 + (s & 3) * 32, 16, 1024),
-                   mma_desc(ka + (s >> 2) * kCols * 128 + (s & 3) * 32, 16, 1024), id_s, s > 0);
+            mma_ss(d, qa + ((s >> 2) * kRows * 128 + (s & 3) * 32) / 16,
+                   ka + ((s >> 2) * kCols * 128 + (s & 3) * 32) / 16, id_s, s > 0);
           mma_commit(&bar.s_full[a]);
-          if (!two || a == 1) mma_commit(&bar.k_empty[st]);
+          if (!pair || a == 1) mma_commit(&bar.k_empty[st]);
         }
         __syncwarp();
       };
       ok = warp_wait(&bar.q_full, seg_no & 1);
       tmem_fence_after();
-      for (int i = 0; i < 2 && i < jobs && ok; ++i) scores(i);
+      k_ready(0);
+      if (ok) scores(0);
+      if (jobs > 1) {
+        k_ready(1);
+        if (ok) scores(1);
+      }
       for (int i = 0; i < jobs && ok; ++i) {
-        const int a = i & 1, tile = two ? i >> 1 : i, t = kv + tile, st = t % kStages;
-        char* vt = smem + S::v + st * S::kTile;
-        if (!two || a == 0) {
+        const int a = i & 1, tile = pair ? i >> 1 : i, t = kv + tile, st = t % kStages;
+        if (!pair || a == 0) {
           if (!(ok = warp_wait(&bar.v_full[st], (t / kStages) & 1))) break;
-          const int col0 = (seg.tile0 + tile) * kCols;
-          if (col0 + kCols > row.old) {  // clean V where it may hold anything
-            for (int c = max(0, row.old - col0); c < kCols; ++c) {
+          if (tile >= clean) {  // clean V where it may hold anything: a lane per column
+            const int col0 = (seg.tile0 + tile) * kCols;
+            char* vt = smem + S::v + st * S::kTile;
+            for (int c = lane; c < kCols; c += 32) {
               const int node = col0 + c - row.old;
-              const bool used = node < p.T && s_anc[node] != 0;
-              uint4* v = reinterpret_cast<uint4*>(vt + swizzled(c, lane, kCols));
-              bool bad = false;
-              if (used) {
-                if (lane < HD / 8) {
-                  const uint4 w = *v;
-                  bad = inf_or_nan(w.x) || inf_or_nan(w.y) || inf_or_nan(w.z) || inf_or_nan(w.w);
+              if (node < 0) continue;
+              bool drop = node >= p.T || s_anc[node] == 0;
+              if (!drop) {
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < HD / 8; ++k) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(vt + swizzled(c, k, kCols));
+                  bad |= inf_or_nan(w.x) || inf_or_nan(w.y) || inf_or_nan(w.z) || inf_or_nan(w.w);
                 }
-                bad = __any_sync(0xffffffffu, bad);
-                if (bad && lane == 0) s_poison |= 1ull << node;
+                if (bad) atomicOr(&s_poison, 1ull << node);
+                drop = bad;
               }
-              if ((!used || bad) && lane < HD / 8) *v = make_uint4(0, 0, 0, 0);
+              if (drop)
+#pragma unroll
+                for (int k = 0; k < HD / 8; ++k)
+                  *reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)) = make_uint4(0, 0, 0, 0);
             }
             fence_async_smem();
             __syncwarp();
           }
         }
         if (i == jobs - 1 && lane == 0) arrive(&bar.v_clean);  // the segment's V has been seen
-        if (!(ok = warp_wait(&bar.p_ready[a], done[a] & 1))) break;
+        if (i + 2 < jobs) k_ready(i + 2);
+        if (!ok || !(ok = warp_wait(&bar.p_ready[a], done[a] & 1))) break;
         ++done[a];
         tmem_fence_after();
-        if (lane == 0) {
-          const uint32_t va = smem_addr(vt);
-          for (int s = 0; s < kCols / 16; ++s)
-            mma_ts(tmem + (2 + a) * kCols, tmem + a * kCols + s * 8,
-                   mma_desc(va + s * 2048, kCols * 128, 1024), id_o, i >= 2 || s > 0);
-          if (!two || a == 1) mma_commit(&bar.v_empty[st]);
+        const uint64_t va = v_desc + st * (S::kTile / 16);
+        const uint32_t d = tm + (2 + a) * kCols, w = tm + a * kCols;
+        if (elect_one()) {
+          mma_ts(d, w, va, id_o, i >= 2);
+#pragma unroll
+          for (int s = 1; s < kCols / 16; ++s) mma_ts(d, w + s * 8, va + s * (2048 / 16), id_o, true);
+          if (!pair || a == 1) mma_commit(&bar.v_empty[st]);
           if (i + 2 >= jobs) mma_commit(&bar.o_done[a]);
         }
         __syncwarp();
@@ -282,21 +332,32 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       }
       if (tid == 0) s_poison = 0;
       {  // Q rows, swizzled; rows that do not exist are zero
-        constexpr int kChunks = HD / 8;
-        for (int i = tid; i < (two ? 2 : 1) * kRows * kChunks; i += 256) {
-          const int q = i / kChunks, c = i % kChunks, qq = mt * 2 * kRows + q;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (q < nrows) {
-            const int t = qq / p.G, h = seg.h * p.G + qq % p.G;
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + seg.b * p.qr + t * p.qt +
-                                                     static_cast<long long>(h) * HD * 2) + c);
-            v.x ^= flip;
-            v.y ^= flip;
-            v.z ^= flip;
-            v.w ^= flip;
+        constexpr int kChunks = HD / 8, kPer = 256 / kChunks, kLoads = 2 * kRows / kPer,
+                      kBatch = kLoads / 2;
+        const int c = tid % kChunks, q0 = tid / kChunks;
+#pragma unroll 1
+        for (int k0 = 0; k0 < (two ? kLoads : kLoads / 2); k0 += kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {  // loads first: they wait for memory together
+            const int q = q0 + (k0 + k) * kPer, qq = mt * 2 * kRows + q;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (q < nrows) {
+              const int t = qq / p.G, h = seg.h * p.G + qq - t * p.G;
+              v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + seg.b * p.qr + t * p.qt +
+                                                          static_cast<long long>(h) * HD * 2) + c);
+            }
           }
-          *reinterpret_cast<uint4*>(smem + S::q + (q / kRows) * S::kQ +
-                                    swizzled(q % kRows, c, kRows)) = v;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int q = q0 + (k0 + k) * kPer;
+            v[k].x ^= flip;
+            v[k].y ^= flip;
+            v[k].z ^= flip;
+            v[k].w ^= flip;
+            *reinterpret_cast<uint4*>(smem + S::q + (q / kRows) * S::kQ +
+                                      swizzled(q % kRows, c, kRows)) = v[k];
+          }
         }
         fence_async_smem();
         arrive(&bar.q_full);
@@ -310,29 +371,42 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         if (!idle) {
           tmem_fence_after();
           const int base = (seg.tile0 + (two ? j : 2 * j + a)) * kCols - row.old;
-          // Two passes over the scores in tensor memory, 32 columns at a time: all 128 in registers
-          // would leave too few for the rest.
-          const auto load = [&](int c, uint32_t (&s)[32]) {
-            tmem_ld32(t_s + c * 32, s);
-            tmem_wait_ld();
-            if (base + kCols > 0) {
-              const uint32_t vis = visible32(anc, base + c * 32);
+          // One pass with the maximum so far: weights are taken against it while the tile's own
+          // maximum is found, and only where that is too large are they taken again.
+          uint32_t w[4][16];
+          uint64_t sum[2];
+          float mx;
+          auto weigh = [&] {
+            const float off = m == -INFINITY ? 0.f : m;
+            const uint64_t scale2 = pack2(scale, scale), off2 = pack2(-off, -off);
+            float top[2] = {-INFINITY, -INFINITY};
+            sum[0] = sum[1] = 0;
+            uint32_t s[2][32];
+            tmem_ld32(t_s, s[0]);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(vis >> k & 1)) s[k] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t(&v)[32] = s[c & 1];
+              tmem_wait_ld32(v);
+              if (c < 3) tmem_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
+              if (base + kCols > 0) {
+                const uint32_t vis = visible32(anc, base + c * 32);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!(vis >> k & 1)) v[k] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                top[k & 1] = fmaxf(top[k & 1], fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+                const float2 z = unpack2(fma2(pack2u(v[2 * k], v[2 * k + 1]), scale2, off2));
+                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                sum[k & 1] = add2(sum[k & 1], pack2(e0, e1));
+                // rounded to bf16: with V in bf16 the product takes nothing wider
+                w[c][k] = bf16_pack(e0, e1);
+              }
             }
+            mx = fmaxf(top[0], top[1]) * scale;
           };
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            load(c, s);
-            float q[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int k = 0; k < 32; ++k) q[k & 3] = fmaxf(q[k & 3], __uint_as_float(s[k]));
-            mx = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3]));
-          }
-          mx *= scale;
+          weigh();
           const bool up = mx > m + kGrow || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, up)) {
             const float mn = up ? mx : m;
@@ -344,29 +418,18 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
               for (int c = 0; c < HD / 16; ++c) {
                 uint32_t o[16];
                 tmem_ld16(t_o + c * 16, o);
-                tmem_wait_ld();
+                tmem_wait_ld16(o);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                 tmem_st16(t_o + c * 16, o);
               }
             }
+            weigh();
           }
-          const float off = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {  // the weights go over scores that have been read
-            uint32_t s[32], w[16];
-            load(c, s);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float e0 = ex2(fmaf(__uint_as_float(s[2 * k]), scale, -off));
-              const float e1 = ex2(fmaf(__uint_as_float(s[2 * k + 1]), scale, -off));
-              sum[k & 3] += e0 + e1;
-              w[k] = bf16_pack(e0, e1);
-            }
-            tmem_st16(t_s + c * 16, w);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, w[c]);
+          const float2 both = unpack2(add2(sum[0], sum[1]));
+          l += both.x + both.y;
           tmem_wait_st();
           tmem_fence_before();
         }
@@ -384,7 +447,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         uint32_t u[32];
         if (jobs > 0 && !idle) {
           tmem_ld32(t_o + c * 32, u);
-          tmem_wait_ld();
+          tmem_wait_ld32(u);
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = jobs > 0 && !idle ? __uint_as_float(u[k]) : 0.f;
@@ -470,51 +533,6 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         continue;
       }
       if (owner) p.part_ml[static_cast<long long>(slot) * 2 * kRows + pr] = make_float2(m, l);
-      if (s_bad) continue;
-      // the unit's last CTA merges the parts in share order
-      const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1);
-      __threadfence();
-      named_bar_sync(1, 256);
-      if (tid == 0) {
-        unsigned* t = &p.ticket[(static_cast<long long>(seg.b) * p.H + seg.h) * p.MT + mt];
-        const unsigned old = atomicAdd(t, 1u);
-        s_flag = old + 1 == static_cast<unsigned>(g1 - g0 + 1);
-        if (s_flag) *t = 0;
-        __threadfence();
-      }
-      named_bar_sync(1, 256);
-      if (!s_flag || !mine) continue;
-      float mm = -INFINITY, ll = 0.f;
-      for (int gg = g0; gg <= g1; ++gg) {
-        const float2 w = __ldcg(p.part_ml + static_cast<long long>(attn_slot(p, sh, gg, mt, seg.unit0)) * 2 * kRows + pr);
-        const float mn = fmaxf(mm, w.x), of = mn == -INFINITY ? 0.f : mn;
-        ll = ll * ex2(mm - of) + w.y * ex2(w.x - of);
-        mm = mn;
-      }
-      const float of = mm == -INFINITY ? 0.f : mm, inv = anc ? 1.f / ll : 0.f;
-      // one row per thread, or (with A and B on the same rows) half of a row's values each
-      const int c0 = two ? 0 : a * (HD / 64), c1 = two ? HD / 32 : c0 + HD / 64;
-#pragma unroll 1
-      for (int c = c0; c < c1; ++c) {
-        float o[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = 0.f;
-        for (int gg = g0; gg <= g1; ++gg) {
-          const long long sl = attn_slot(p, sh, gg, mt, seg.unit0);
-          const float f = ex2(__ldcg(p.part_ml + sl * 2 * kRows + pr).x - of);
-          const float4* w = reinterpret_cast<const float4*>(p.part_o) + (sl * (HD / 4) + c * 8) * 2 * kRows + pr;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 v = __ldcg(w + k * 2 * kRows);
-            o[4 * k] += v.x * f;
-            o[4 * k + 1] += v.y * f;
-            o[4 * k + 2] += v.z * f;
-            o[4 * k + 3] += v.w * f;
-          }
-        }
-        store_out(c, o, inv);
-      }
-      if (two || a == 0) store_lse(mm, ll);
     }
   }
   if (!ok) set_status(p.status, SPECDEC_ERR_TIMEOUT);
@@ -527,6 +545,72 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   }
 }
 
+// Units that share borders cut, merged by a launch of their own: it spreads the parts over the GPU
+// and needs no tickets.  (The CTA that came last, merging alone, took 10 us for 2 or 3 parts of
+// 128 KB and 90 us for 19.)  CTA = border and 32 rows; thread = row and 4 * kPer of its values.
+template <int HD>
+__global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
+  constexpr int kPer = HD / 32;  // float4 a thread holds
+  __shared__ AttnPlan plan;
+  __shared__ int s_par[kMaxTree];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  if (warp == 0) attn_plan(p, kCols, plan);
+  __syncthreads();
+  const AttnShares sh = attn_shares(p, plan);
+  const int border = blockIdx.x + 1, block = blockIdx.y & 7, mt = blockIdx.y >> 3;
+  if (sh.total == 0 || border >= sh.groups) return;
+  const int x = sh.start(border);
+  const AttnSegment seg = attn_segment(p, plan, x, x + 1);
+  const int b = seg.b, h = seg.h, unit0 = seg.unit0;
+  if (seg.tile0 == 0) return;                       // the border cuts no unit
+  const int g0 = sh.owner(unit0), g1 = sh.owner(unit0 + seg.tiles - 1);
+  if (border != g0 + 1) return;                     // another border of the same unit
+  if (p.parents && tid < p.T) s_par[tid] = p.parents[b * p.T + tid];
+  __syncthreads();
+  bool bad = false;
+  if (tid < p.T) (void)tree_ancestors(p.parents ? s_par : nullptr, tid, bad);
+  if (__syncthreads_or(bad)) return;                // the attention reported it
+  const int pr = block * 32 + lane, rr = mt * 2 * kRows + pr;
+  if (rr >= p.T * p.G) return;
+  const int t = rr / p.G, qh = h * p.G + rr % p.G;
+  const bool live = tree_ancestors(p.parents ? s_par : nullptr, t, bad) != 0;
+  float m = -INFINITY, l = 0.f;
+  for (int g = g0; g <= g1; ++g) {
+    const float2 w = p.part_ml[static_cast<long long>(attn_slot(p, sh, g, mt, unit0)) * 2 * kRows + pr];
+    const float mn = fmaxf(m, w.x), off = mn == -INFINITY ? 0.f : mn;
+    l = l * ex2(m - off) + w.y * ex2(w.x - off);
+    m = mn;
+  }
+  const float off = m == -INFINITY ? 0.f : m, inv = live ? 1.f / l : 0.f;
+  float4 o[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int d0 = warp * kPer;  // first float4
+#pragma unroll 4
+  for (int g = g0; g <= g1; ++g) {
+    const long long sl = attn_slot(p, sh, g, mt, unit0);
+    const float f = ex2(p.part_ml[sl * 2 * kRows + pr].x - off);
+    const float4* w = reinterpret_cast<const float4*>(p.part_o) + (sl * (HD / 4) + d0) * 2 * kRows + pr;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const float4 v = w[k * 2 * kRows];
+      o[k].x += v.x * f;
+      o[k].y += v.y * f;
+      o[k].z += v.z * f;
+      o[k].w += v.w * f;
+    }
+  }
+  char* y = p.out + b * p.outr + t * p.outt + static_cast<long long>(qh) * HD * 2 + d0 * 8;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    *reinterpret_cast<uint2*>(y + k * 8) = make_uint2(bf16_pack(o[k].x * inv, o[k].y * inv),
+                                                      bf16_pack(o[k].z * inv, o[k].w * inv));
+  if (p.lse && warp == 0)
+    p.lse[(static_cast<long long>(b) * p.T + t) * p.Hq + qh] =
+        live ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 template <int HD>
 int launch_tc(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {
   auto kernel = attn_tc_kernel<HD>;
@@ -534,7 +618,18 @@ int launch_tc(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return map_cuda_error(e);
   kernel<<<grid, kThreads, smem, stream>>>(p, map);
-  return map_cuda_error(cudaGetLastError());
+  const cudaError_t e2 = cudaGetLastError();
+  if (e2 != cudaSuccess || p.groups == 1) return map_cuda_error(e2);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.groups - 1, p.MT * 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return map_cuda_error(cudaLaunchKernelEx(&cfg, attn_merge_kernel<HD>, p));
 }
 
 }  // namespace
