@@ -23,16 +23,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 16-byte asynchronous copy global -> shared; zero-fills where `take` is false.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-               ::"r"(smem_addr(dst)), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Bytes of a column in shared memory: 16 more than its values, so that the 16-byte reads of
 // eight neighbouring columns fall into different banks.
 __host__ __device__ constexpr int pitch_of(int hd, int es) { return hd * es + 16; }
@@ -81,11 +71,8 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
   const int x1 = sh.start(g + 1);
   const int nrows = min(M, p.T * p.G - mt * M);  // query rows of this M-tile: (node, head) pairs
   int row_b = -1;
-  for (int x = sh.start(g); x < x1;) {
-    const AttnSegment seg = attn_segment(p, plan, x, x1);
-    x += seg.tile1 - seg.tile0;
-    int err;
-    const AttnRow row = attn_row(p, seg.b, &err);
+  AttnSegment seg;
+  for (int x = sh.start(g); attn_next(p, plan, x, x1, seg); x = seg.next) {
     if (seg.b != row_b) {  // a new batch row: its tree
       row_b = seg.b;
       __syncthreads();
@@ -123,13 +110,13 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
     }
     const long long crow = p.one_row ? 0 : seg.b;
     const char* kbase = p.cache.base + crow * p.cache.srow + seg.h * p.cache.shead +
-                        static_cast<long long>(row.first) * hd * sizeof(T);
+                        static_cast<long long>(seg.first) * hd * sizeof(T);
     const char* vbase = kbase + p.cache.skv;
     auto fetch = [&](int tile) {
       const int stage = tile & 1;
       for (int i = tid; i < kTile * vecs; i += kThreads) {
         const int c = i / vecs, v = i - c * vecs, col = tile * kTile + c;
-        const bool in = col < row.cols;
+        const bool in = col < seg.cols;
         const long long at = (static_cast<long long>(in ? col : 0) * vecs + v) * 16;
         cp_async16(s_k + (stage * kTile + c) * pitch + v * 16, kbase + at, in);
         cp_async16(s_v + (stage * kTile + c) * pitch + v * 16, vbase + at, in);
@@ -169,7 +156,7 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
           z[k] = fmaf(qq.w, kk.w, z[k]);
         }
       }
-      const int col = tile * kTile + lane, node = col - row.old;
+      const int col = tile * kTile + lane, node = col - seg.old;
       float4 pr;
       float* pv = reinterpret_cast<float*>(&pr);
 #pragma unroll
@@ -199,7 +186,7 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
       s_p[lane] = pr;
       __syncwarp();
       // nodes' columns may hold anything where a row does not see them: weight 0 is skipped there
-      const int c_end = min(kTile, row.cols - tile * kTile), plain = min(c_end, max(0, row.old - tile * kTile));
+      const int c_end = min(kTile, seg.cols - tile * kTile), plain = min(c_end, max(0, seg.old - tile * kTile));
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int d = j * 128 + lane * 4;
@@ -302,7 +289,7 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
 // ------------------------------------------------------------------------------------- host
 
 struct AttnShape {
-  int M, MT, groups, grid, tile, min_tiles;
+  int M, MT, groups, grid, tile, min_tiles, open;
   size_t smem;
   int kind;
 };
@@ -341,6 +328,7 @@ AttnShape attn_shape(int es, int T, int G, int hd) {
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
   s.tile = 128;
   s.min_tiles = 1;
+  s.open = s.kind == kTc ? 3 : 0;
   return s;
 }
 
@@ -427,12 +415,12 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   const int G = a->heads_q / c.heads;
   AttnShape s = attn_shape(static_cast<int>(es), a->T, G, c.head_dim);
   // no more groups than the longest rows could give work to
-  const long long tiles = static_cast<long long>(a->B) * c.heads * ((c.cap_cols - 1) / s.tile + 1);
+  const long long tiles = static_cast<long long>(a->B) * c.heads * ((c.cap_cols - 1) / s.tile + 1 + s.open);
   s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
   s.grid = s.groups * s.MT;
   const AttnWorkspace w = attn_workspace(s, a->B, c.heads, c.head_dim);
   if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
-  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kTile + 2) >= (1LL << 31))
+  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kTile + 8) >= (1LL << 31))
     return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   AttnParams p = {};
   p.cache = to_bytes(c);
@@ -466,6 +454,8 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   p.MT = s.MT;
   p.groups = s.groups;
   p.min_tiles = s.min_tiles;
+  p.open = s.open;
+  p.g_shift = (G & (G - 1)) == 0 ? __builtin_ctz(G) : -1;
   cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
   if (s.kind == kTc) return launch_attn_tc(p, c.rows, s.grid, stream_);
   if (s.kind == kMma) return launch_attn_mma(p, c.rows, s.grid, stream_);

@@ -35,7 +35,7 @@ struct AttnParams {
   float2* part_ml;   // [grid * 2][M]
   float* part_o;     // [grid * 2][M][hd]
   float scale_log2;  // scale * log2(e)
-  int B, T, Hq, H, G, hd, cap, one_row, MT, groups, min_tiles;
+  int B, T, Hq, H, G, hd, cap, one_row, MT, groups, min_tiles, open, g_shift;  // g_shift: log2 G, or -1
 };
 
 // One batch row's columns.
@@ -72,23 +72,27 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b, int* err
   return AttnRow{static_cast<int>(first), n - 1, n - 1 + p.T};
 }
 
-// The plan in shared memory: tiles of the rows before row b, per K/V head.
+// The plan in shared memory: tiles of the rows before row b, per K/V head, and the rows.
 struct AttnPlan {
-  int pre[kAttnMaxRows + 1];
+  int pre[kAttnMaxRows + 1], first[kAttnMaxRows], old[kAttnMaxRows];
 };
 
+// A unit counts `p.open` tiles more than it has, for what a CTA spends on opening and closing it,
+// so that shares with many short units take no longer than others.
 // Built by warp 0 of every CTA (the caller synchronises); CTA 0 records errors.
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, AttnPlan& plan) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int tiles = 0;
+    int tiles = 0, first = 0, old = 0;
     if (b < p.B) {
       int err;
       const AttnRow r = attn_row(p, b, &err);
       if (err && blockIdx.x == 0) set_status(p.status, err);
-      tiles = (r.cols + tile - 1) / tile;
+      tiles = r.cols > 0 ? (r.cols + tile - 1) / tile + p.open : 0;
+      first = r.first;
+      old = r.old;
     }
     int inc = tiles;
 #pragma unroll
@@ -96,7 +100,11 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, AttnPla
       const int o = __shfl_up_sync(0xffffffffu, inc, k);
       if (lane >= k) inc += o;
     }
-    if (b < p.B) plan.pre[b] = carry + inc - tiles;
+    if (b < p.B) {
+      plan.pre[b] = carry + inc - tiles;
+      plan.first[b] = first;
+      plan.old[b] = old;
+    }
     carry += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (lane == 0) plan.pre[p.B] = carry;
@@ -122,10 +130,13 @@ __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const Att
   return s;
 }
 
-// A contiguous run of tiles of one unit inside a share.
+// A contiguous run of tiles of one unit inside a share (it may have none, if the share ends in what
+// the unit counts for being opened).
 struct AttnSegment {
   int b, h, tile0, tile1, tiles;  // unit, its tiles [tile0, tile1) of `tiles`
   int unit0;                      // place of the unit's first tile in the sequence
+  int next;                       // place behind the segment
+  int first, old, cols;           // its columns: AttnRow
 };
 __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnPlan& plan,
                                                     int x, int end) {
@@ -137,13 +148,29 @@ __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const A
   }
   AttnSegment s;
   s.b = lo;
-  s.tiles = plan.pre[lo + 1] - plan.pre[lo];
-  const int rem = x - plan.pre[lo] * p.H;
-  s.h = rem / s.tiles;
-  s.tile0 = rem - s.h * s.tiles;
-  s.tile1 = min(s.tiles, s.tile0 + (end - x));
-  s.unit0 = x - s.tile0;
+  const int span = plan.pre[lo + 1] - plan.pre[lo], rem = x - plan.pre[lo] * p.H;
+  s.h = rem / span;
+  const int at = rem - s.h * span;
+  s.next = min(end, x - at + span);
+  s.tiles = span - p.open;
+  s.tile0 = max(0, at - p.open);
+  s.tile1 = max(0, s.next - x + at - p.open);
+  s.unit0 = x - at + p.open;
+  s.first = plan.first[lo];
+  s.old = plan.old[lo];
+  s.cols = s.old + p.T;
   return s;
+}
+
+// The next segment with tiles at or behind x; false at the share's end.
+__device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& plan, int x, int end,
+                                          AttnSegment& s) {
+  while (x < end) {
+    s = attn_segment(p, plan, x, end);
+    if (s.tile1 > s.tile0) return true;
+    x = s.next;
+  }
+  return false;
 }
 
 // Takes a ticket of the unit's M-tile mt; true in every thread for the CTA that took the last one
@@ -164,11 +191,24 @@ __device__ __forceinline__ bool attn_last(const AttnParams& p, int b, int h, int
 }
 
 // Slot of the partial result that share g's CTA of M-tile mt wrote for the unit that begins at
-// unit0: 0 if its segment starts the share, else 1.
+// unit0 (its first tile's place): 0 if its segment starts the share, else 1.
 __device__ __forceinline__ int attn_slot(const AttnParams& p, const AttnShares& sh, int g, int mt,
                                          int unit0) {
   return 2 * (g * p.MT + mt) + (sh.start(g) >= unit0 ? 0 : 1);
 }
+
+// 16-byte asynchronous copy global -> shared; zero-fills where `take` is false.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               ::"r"(smem_addr(dst)), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // The tensor-core kernel (tree_attention_tc.cu): rows per M-tile and M-tiles for R query rows per
 // K/V head, and its launch (rows: of the cache).

@@ -62,7 +62,8 @@ template <int HD> struct Smem {
 // Walks the tiles of a share, segment by segment.
 struct Cursor {
   AttnSegment seg;
-  int x, tile;  // place in the sequence, tile of the segment
+  int tile;   // of the segment
+  bool more;  // not behind the last
 };
 
 template <int HD>
@@ -96,11 +97,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 
   // The warp's slice of the cursor's tile into stage `st` (nothing if the row ends before it).
   auto fetch = [&](const Cursor& c, int st) {
-    int err;
-    const AttnRow row = attn_row(p, c.seg.b, &err);
     const int col = c.tile * kTileCols + warp * kCols;
     if (lane == 0) {
-      if (col < row.cols) {
+      if (col < c.seg.cols) {
         mbar_arrive_expect_tx(&s_full[warp][st], 2 * S::kSlice);
         const int crow = p.one_row ? 0 : c.seg.b;
 #pragma unroll
@@ -108,35 +107,30 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
           for (int j = 0; j < kPanels; ++j)
             tma_load_5d(mem + (st * 2 + kv) * S::kSlice + j * kCols * 128, &map, j * 64,
-                        row.first + col, c.seg.h, crow, kv, &s_full[warp][st]);
+                        c.seg.first + col, c.seg.h, crow, kv, &s_full[warp][st]);
       } else {
         mbar_arrive_expect_tx(&s_full[warp][st], 0);
       }
     }
   };
   auto advance = [&](Cursor& c) {
-    ++c.x;
-    if (++c.tile >= c.seg.tile1 && c.x < x1) {
-      c.seg = attn_segment(p, plan, c.x, x1);
+    if (++c.tile >= c.seg.tile1) {
+      c.more = attn_next(p, plan, c.seg.next, x1, c.seg);
       c.tile = c.seg.tile0;
     }
   };
   Cursor ahead;
-  ahead.x = sh.start(g);
-  ahead.seg = attn_segment(p, plan, ahead.x, x1);
+  ahead.more = attn_next(p, plan, sh.start(g), x1, ahead.seg);
   ahead.tile = ahead.seg.tile0;
   int loaded = 0;  // tiles asked for so far
-  for (; loaded < kStages && ahead.x < x1; ++loaded) {
+  for (; loaded < kStages && ahead.more; ++loaded) {
     fetch(ahead, loaded);
     advance(ahead);
   }
   int used = 0, row_b = -1;
   bool ok = true;
-  for (int x = sh.start(g); x < x1;) {
-    const AttnSegment seg = attn_segment(p, plan, x, x1);
-    x += seg.tile1 - seg.tile0;
-    int err;
-    const AttnRow row = attn_row(p, seg.b, &err);
+  AttnSegment seg;
+  for (int x = sh.start(g); attn_next(p, plan, x, x1, seg); x = seg.next) {
     if (seg.b != row_b) {
       row_b = seg.b;
       __syncthreads();
@@ -180,8 +174,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       const int st = used % kStages;
       ok = ok && __all_sync(0xffffffffu, mbar_wait_sleep(&s_full[warp][st], (used / kStages) & 1,
                                                          kTries, kNs));
-      const int col = tile * kTileCols + warp * kCols, base = col - row.old;
-      if (ok && col < row.cols) {
+      const int col = tile * kTileCols + warp * kCols, base = col - seg.old;
+      if (ok && col < seg.cols) {
         const char* km = mem + st * 2 * S::kSlice;
         char* vm = mem + (st * 2 + 1) * S::kSlice;
         const uint32_t ka = smem_addr(km), va = smem_addr(vm);
@@ -277,7 +271,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         }
       }
       __syncwarp();
-      if (ok && ahead.x < x1) {
+      if (ok && ahead.more) {
         fetch(ahead, loaded % kStages);
         advance(ahead);
         ++loaded;

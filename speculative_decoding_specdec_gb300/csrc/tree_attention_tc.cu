@@ -7,8 +7,8 @@
 //   warps 0-3, 4-7  softmax of A, B: one thread per row reads its 128 scores from tensor memory,
 //                   keeps maximum and sum, writes the weights back as bf16 over the scores;
 //   warp 8          TMA: K and V tiles of 128 columns into two stages each (128-byte swizzle);
-//   warp 9          one thread issues S = Q K^T (both operands in shared memory) and
-//                   O += P V (P from tensor memory, V as it lies: MN-major).
+//   warps 9, 10     one thread each issues S = Q K^T (both operands in shared memory) and
+//                   O += P V (P from tensor memory, V as it lies: MN-major) of A, of B.
 // Tensor memory (512 columns): S/P of A and B, O of A and B, 128 columns each.
 // The running maximum is only followed when it grows by more than 2^8 in weight: O is then rescaled
 // by the row's thread between its scores' arrival and its weights' release, when no MMA of that
@@ -26,7 +26,7 @@ namespace specdec {
 
 namespace {
 
-constexpr int kThreads = 384;  // the last two warps only make whole warpgroups of registers
+constexpr int kThreads = 384;  // (the last warp only completes the third warpgroup)
 // Registers per thread: 384 x 168 at launch; 2 x 128 x 224 + 128 x 56 = those 64512.
 constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 constexpr int kCols = 128;     // columns of a K/V tile
@@ -128,17 +128,20 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   __shared__ float2 s_ml[kRows];
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
+  const int nrows = min(2 * kRows, p.T * p.G - mt * 2 * kRows);  // query rows of this pair
+  const bool two = nrows > kRows;  // A and B are different rows, else alternate tiles
   if (warp == 0) attn_plan(p, kCols, plan);
   if (warp == 9) tmem_alloc(&s_tmem, 512);
   if (tid == 32) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.k_full[i], 1);
-      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.k_empty[i], two ? 2 : 1);  // A's and B's products, or the tile's one
       mbar_init(&bar.v_full[i], 1);
-      mbar_init(&bar.v_empty[i], 1);
+      mbar_init(&bar.v_empty[i], two ? 2 : 1);
     }
     mbar_init(&bar.q_full, 256);
-    mbar_init(&bar.v_clean, 1);
+    mbar_init(&bar.v_clean, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_ready[i], 128);
@@ -153,11 +156,8 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   pdl_launch_dependents();  // the merge of cut units may be set up
   const uint32_t tmem = s_tmem;
   const AttnShares sh = attn_shares(p, plan);
-  const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   const bool work = sh.total > 0 && g < sh.groups;
   const int x0 = work ? sh.start(g) : 0, x1 = work ? sh.start(g + 1) : 0;
-  const int nrows = min(2 * kRows, p.T * p.G - mt * 2 * kRows);  // query rows of this pair
-  const bool two = nrows > kRows;  // A and B are different rows, else alternate tiles
   bool ok = true;
 
   if (warp >= 8) {
@@ -166,20 +166,19 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     // ------------------------------------------------------------------------------- TMA
     if (lane == 0) {
       int kv = 0;  // tiles so far
-      for (int x = x0; x < x1 && ok;) {
-        const AttnSegment seg = attn_segment(p, plan, x, x1);
-        x += seg.tile1 - seg.tile0;
-        int err;
-        const AttnRow row = attn_row(p, seg.b, &err);
+      AttnSegment seg;
+      for (int x = x0; ok && attn_next(p, plan, x, x1, seg); x = seg.next) {
         const int crow = p.one_row ? 0 : seg.b;
         for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++kv) {
-          const int st = kv % kStages, col = row.first + tile * kCols;
+          const int st = kv % kStages, col = seg.first + tile * kCols;
           const uint32_t ph = (kv / kStages) & 1;
           if (!(ok = wait(&bar.k_empty[st], ph ^ 1))) break;
           mbar_arrive_expect_tx(&bar.k_full[st], S::kTile);
           for (int j = 0; j < kPanels; ++j)
             tma_load_5d(smem + S::k + st * S::kTile + j * kCols * 128, &map, j * 64, col, seg.h,
                         crow, 0, &bar.k_full[st]);
+          // the first product needs K and Q: what comes after must not stand before Q in the queue
+          if (kv == 0 && !(ok = wait(&bar.q_full, 0))) break;
           if (!(ok = wait(&bar.v_empty[st], ph ^ 1))) break;
           mbar_arrive_expect_tx(&bar.v_full[st], S::kTile);
           for (int j = 0; j < kPanels; ++j)
@@ -195,101 +194,101 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           (void)wait(&bar.v_full[i % kStages], (i / kStages) & 1);
         }
     }
-  } else if (warp == 9) {
+  } else if (warp < 11) {
     // ------------------------------------------------------------------------------- MMA
-    // The whole warp follows the jobs and one elected lane issues.  What an MMA's operands are made
-    // of is the same in all lanes and made so for the compiler to see (the shuffles): an MMA takes
+    // Warp 9 for accumulator A, warp 10 for B: while one waits, the other's products run.  The
+    // whole warp follows its jobs and one elected lane issues.  What an MMA's operands are made of
+    // is the same in all lanes and made so for the compiler to see (the shuffles): an MMA takes
     // its descriptors from uniform registers, and moving them there lane by lane took longer than
     // the products.
     constexpr uint32_t id_s = mma_idesc(kRows, kCols, false), id_o = mma_idesc(kRows, HD, true);
+    const int a = __shfl_sync(0xffffffffu, warp, 0) - 9;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t sm = __shfl_sync(0xffffffffu, smem_addr(smem), 0);
-    const uint64_t q_desc = mma_desc(sm + S::q, 16, 1024), k_desc = mma_desc(sm + S::k, 16, 1024),
-                   v_desc = mma_desc(sm + S::v, kCols * 128, 1024);
     const bool pair = __shfl_sync(0xffffffffu, two ? 1 : 0, 0) != 0;
-    int kv = 0, seg_no = 0, done[2] = {0, 0};  // tiles, segments, jobs of A and B so far
-    for (int x = x0; x < x1 && ok; ++seg_no) {
-      const AttnSegment seg = attn_segment(p, plan, x, x1);
-      const int n = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0), jobs = pair ? 2 * n : n;
-      x += n;
-      int err;
-      const AttnRow row = attn_row(p, seg.b, &err);
-      // columns from here on need care: tile `clean` holds the first of them
-      const int clean = row.old / kCols - seg.tile0;
-      // S = Q K^T of job i: tile i / 2 for A or B (pair), or tile i
-      auto k_ready = [&](int i) {
-        const int t = kv + (pair ? i >> 1 : i);
-        if (!pair || !(i & 1)) ok = ok && warp_wait(&bar.k_full[t % kStages], (t / kStages) & 1);
-      };
-      auto scores = [&](int i) {
-        const int a = i & 1, t = kv + (pair ? i >> 1 : i), st = t % kStages;
-        const uint64_t qa = q_desc + (pair ? a : 0) * (S::kQ / 16), ka = k_desc + st * (S::kTile / 16);
-        const uint32_t d = tm + a * kCols;
+    const uint64_t q_desc = mma_desc(sm + S::q + (pair ? a : 0) * S::kQ, 16, 1024),
+                   k_desc = mma_desc(sm + S::k, 16, 1024),
+                   v_desc = mma_desc(sm + S::v, kCols * 128, 1024);
+    const uint32_t t_s = tm + a * kCols, t_o = tm + (2 + a) * kCols;
+    int kv = 0, seg_no = 0, done = 0;  // tiles, segments, jobs so far
+    AttnSegment seg;
+    for (int x = x0; ok && attn_next(p, plan, x, x1, seg); x = seg.next, ++seg_no) {
+      const int n = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0);
+      const int jobs = pair ? n : (n - a + 1) >> 1;  // tiles 0, 1, .. or every second one from a
+      const int clean = seg.old / kCols - seg.tile0;  // the first tile that needs care
+      auto tile_of = [&](int j) { return pair ? j : 2 * j + a; };
+      auto scores = [&](int j) {  // S = Q K^T
+        const int st = (kv + tile_of(j)) % kStages;
+        const uint64_t ka = k_desc + st * (S::kTile / 16);
         if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < kSteps; ++s)
-            mma_ss(d, qa + ((s >> 2) * kRows * 128 + (s & 3) * 32) / 16,
+            mma_ss(t_s, q_desc + ((s >> 2) * kRows * 128 + (s & 3) * 32) / 16,
                    ka + ((s >> 2) * kCols * 128 + (s & 3) * 32) / 16, id_s, s > 0);
           mma_commit(&bar.s_full[a]);
-          if (!pair || a == 1) mma_commit(&bar.k_empty[st]);
+          mma_commit(&bar.k_empty[st]);
         }
         __syncwarp();
       };
+      auto full = [&](uint64_t* bars, int j) {
+        const int t = kv + tile_of(j);
+        return warp_wait(&bars[t % kStages], (t / kStages) & 1);
+      };
       ok = warp_wait(&bar.q_full, seg_no & 1);
       tmem_fence_after();
-      k_ready(0);
-      if (ok) scores(0);
-      if (jobs > 1) {
-        k_ready(1);
-        if (ok) scores(1);
+      if (jobs > 0) {
+        ok = ok && full(bar.k_full, 0);
+        if (ok) scores(0);
       }
-      for (int i = 0; i < jobs && ok; ++i) {
-        const int a = i & 1, tile = pair ? i >> 1 : i, t = kv + tile, st = t % kStages;
-        if (!pair || a == 0) {
-          if (!(ok = warp_wait(&bar.v_full[st], (t / kStages) & 1))) break;
-          if (tile >= clean) {  // clean V where it may hold anything: a lane per column
-            const int col0 = (seg.tile0 + tile) * kCols;
-            char* vt = smem + S::v + st * S::kTile;
-            for (int c = lane; c < kCols; c += 32) {
-              const int node = col0 + c - row.old;
-              if (node < 0) continue;
-              bool drop = node >= p.T || s_anc[node] == 0;
-              if (!drop) {
-                bool bad = false;
+      for (int j = 0; j < jobs && ok; ++j) {
+        const int tile = tile_of(j), st = (kv + tile) % kStages;
+        if (!(ok = full(bar.v_full, j))) break;
+        const int steps = min(kCols / 16, (seg.cols - (seg.tile0 + tile) * kCols + 15) >> 4);
+        if (tile >= clean) {  // clean V where it may hold anything: a lane per column
+          const int col0 = (seg.tile0 + tile) * kCols;
+          char* vt = smem + S::v + st * S::kTile;
+          // (steps of 16 columns behind the last are left out of the product)
+          for (int c = max(0, seg.old - col0) + (pair ? a * 32 : 0) + lane; c < steps * 16;
+               c += pair ? 64 : 32) {
+            const int node = col0 + c - seg.old;
+            bool drop = node >= p.T || s_anc[node] == 0;
+            if (!drop) {
+              bool bad = false;
 #pragma unroll
-                for (int k = 0; k < HD / 8; ++k) {
-                  const uint4 w = *reinterpret_cast<const uint4*>(vt + swizzled(c, k, kCols));
-                  bad |= inf_or_nan(w.x) || inf_or_nan(w.y) || inf_or_nan(w.z) || inf_or_nan(w.w);
-                }
-                if (bad) atomicOr(&s_poison, 1ull << node);
-                drop = bad;
+              for (int k = 0; k < HD / 8; ++k) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vt + swizzled(c, k, kCols));
+                bad |= inf_or_nan(w.x) || inf_or_nan(w.y) || inf_or_nan(w.z) || inf_or_nan(w.w);
               }
-              if (drop)
-#pragma unroll
-                for (int k = 0; k < HD / 8; ++k)
-                  *reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)) = make_uint4(0, 0, 0, 0);
+              if (bad) atomicOr(&s_poison, 1ull << node);
+              drop = bad;
             }
-            fence_async_smem();
-            __syncwarp();
+            if (drop)
+#pragma unroll
+              for (int k = 0; k < HD / 8; ++k)
+                *reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)) = make_uint4(0, 0, 0, 0);
           }
+          fence_async_smem();
+          if (pair) named_bar_sync(4, 64);  // both have cleaned their half
+          else __syncwarp();
         }
-        if (i == jobs - 1 && lane == 0) arrive(&bar.v_clean);  // the segment's V has been seen
-        if (i + 2 < jobs) k_ready(i + 2);
-        if (!ok || !(ok = warp_wait(&bar.p_ready[a], done[a] & 1))) break;
-        ++done[a];
+        if (j == jobs - 1 && lane == 0) arrive(&bar.v_clean);  // the segment's V has been seen
+        if (j + 1 < jobs && !(ok = full(bar.k_full, j + 1))) break;
+        if (!(ok = warp_wait(&bar.p_ready[a], done & 1))) break;
+        ++done;
         tmem_fence_after();
         const uint64_t va = v_desc + st * (S::kTile / 16);
-        const uint32_t d = tm + (2 + a) * kCols, w = tm + a * kCols;
         if (elect_one()) {
-          mma_ts(d, w, va, id_o, i >= 2);
+          mma_ts(t_o, t_s, va, id_o, j > 0);
 #pragma unroll
-          for (int s = 1; s < kCols / 16; ++s) mma_ts(d, w + s * 8, va + s * (2048 / 16), id_o, true);
-          if (!pair || a == 1) mma_commit(&bar.v_empty[st]);
-          if (i + 2 >= jobs) mma_commit(&bar.o_done[a]);
+          for (int s = 1; s < kCols / 16; ++s)
+            if (s < steps) mma_ts(t_o, t_s + s * 8, va + s * (2048 / 16), id_o, true);
+          mma_commit(&bar.v_empty[st]);
+          if (j + 1 == jobs) mma_commit(&bar.o_done[a]);
         }
         __syncwarp();
-        if (i + 2 < jobs) scores(i + 2);
+        if (j + 1 < jobs) scores(j + 1);
       }
+      if (jobs == 0 && lane == 0) arrive(&bar.v_clean);
       kv += n;
     }
   }
@@ -306,63 +305,56 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     const uint32_t t_s = tmem + lane_base + a * kCols, t_o = tmem + lane_base + (2 + a) * kCols;
     // a scale of zero as the smallest one: hidden scores are -infinity and have to stay so
     const float scale = fmaxf(fabsf(p.scale_log2), 1.2e-38f);
-    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale turns Q
-    int seg_no = 0, seen = 0, ends = 0, row_b = -1;  // segments, jobs, accumulations so far
-    for (int x = x0; x < x1 && ok; ++seg_no) {
-      const AttnSegment seg = attn_segment(p, plan, x, x1);
-      const int n = seg.tile1 - seg.tile0;
-      x += n;
-      int err;
-      const AttnRow row = attn_row(p, seg.b, &err);
-      // the segment before is done with what is written now; all agree to go on
-      if (!(ok = named_bar_all(1, 256, ok))) break;
-      if (seg.b != row_b) {
-        row_b = seg.b;
-        if (p.parents && tid < p.T) s_par[tid] = p.parents[seg.b * p.T + tid];
-        if (tid == 0) s_bad = 0;
-        named_bar_sync(1, 256);
-        if (tid < p.T) {
-          bool bad = false;
-          s_anc[tid] = tree_ancestors(p.parents ? s_par : nullptr, tid, bad);
-          if (bad) {
-            s_bad = 1;
-            set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
-          }
+    int seg_no = 0, seen = 0, ends = 0;  // segments, jobs, accumulations so far
+    // A thread copies its 16-byte chunk of every kPer-th Q row straight to shared memory (rows that
+    // do not exist are zero): holding them in registers over the segment before made the compiler
+    // spill them, one round trip to memory each.  What the next segment will read is asked into L2.
+    constexpr int kChunks = HD / 8, kPer = 256 / kChunks, kLoads = 2 * kRows / kPer;
+    const int qc = tid % kChunks, q0 = tid / kChunks, nq = two ? kLoads : kLoads / 2;
+    auto ask = [&](const AttnSegment& sg) {
+      const char* base = p.q + sg.b * p.qr + static_cast<long long>(sg.h) * p.G * HD * 2 + qc * 16;
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int q = q0 + k * kPer, qq = mt * 2 * kRows + q;
+        if (k < nq) {
+          const int t = p.g_shift >= 0 ? qq >> p.g_shift : qq / p.G;
+          cp_async16(smem + S::q + (q / kRows) * S::kQ + swizzled(q % kRows, qc, kRows),
+                     q < nrows ? base + t * p.qt + (qq - t * p.G) * (HD * 2) : p.q, q < nrows);
         }
       }
-      if (tid == 0) s_poison = 0;
-      {  // Q rows, swizzled; rows that do not exist are zero
-        constexpr int kChunks = HD / 8, kPer = 256 / kChunks, kLoads = 2 * kRows / kPer,
-                      kBatch = kLoads / 2;
-        const int c = tid % kChunks, q0 = tid / kChunks;
-#pragma unroll 1
-        for (int k0 = 0; k0 < (two ? kLoads : kLoads / 2); k0 += kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {  // loads first: they wait for memory together
-            const int q = q0 + (k0 + k) * kPer, qq = mt * 2 * kRows + q;
-            v[k] = make_uint4(0, 0, 0, 0);
-            if (q < nrows) {
-              const int t = qq / p.G, h = seg.h * p.G + qq - t * p.G;
-              v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + seg.b * p.qr + t * p.qt +
-                                                          static_cast<long long>(h) * HD * 2) + c);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int q = q0 + (k0 + k) * kPer;
-            v[k].x ^= flip;
-            v[k].y ^= flip;
-            v[k].z ^= flip;
-            v[k].w ^= flip;
-            *reinterpret_cast<uint4*>(smem + S::q + (q / kRows) * S::kQ +
-                                      swizzled(q % kRows, c, kRows)) = v[k];
-          }
+      if (p.parents && tid < p.T) s_par[tid] = __ldg(p.parents + sg.b * p.T + tid);
+    };
+    // Q has arrived: ancestors, and the products may begin
+    auto open = [&] {
+      if (tid < p.T) {
+        bool bad = false;
+        s_anc[tid] = tree_ancestors(p.parents ? s_par : nullptr, tid, bad);
+        if (bad) {
+          s_bad = 1;
+          set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
         }
-        fence_async_smem();
-        arrive(&bar.q_full);
       }
+      cp_async_wait_all();
+      if (p.scale_log2 < 0.f)  // a negative scale turns Q (each thread what it copied)
+        for (int k = 0; k < nq; ++k) {
+          const int q = q0 + k * kPer;
+          uint4* v = reinterpret_cast<uint4*>(smem + S::q + (q / kRows) * S::kQ + swizzled(q % kRows, qc, kRows));
+          *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
+        }
+      fence_async_smem();
+      arrive(&bar.q_full);
+    };
+    AttnSegment seg;
+    bool more = attn_next(p, plan, x0, x1, seg);
+    if (more) {
+      ask(seg);
+      if (tid == 0) s_bad = 0;
       named_bar_sync(1, 256);
+      open();
+      named_bar_sync(1, 256);
+    }
+    for (; more; ++seg_no) {
+      const int n = seg.tile1 - seg.tile0;
       const unsigned long long anc = mine ? s_anc[t_of] : 0ull;
       const int jobs = two ? n : (n - a + 1) >> 1;
       float m = -INFINITY, l = 0.f;
@@ -370,7 +362,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         if (!(ok = warp_wait(&bar.s_full[a], seen & 1))) break;
         if (!idle) {
           tmem_fence_after();
-          const int base = (seg.tile0 + (two ? j : 2 * j + a)) * kCols - row.old;
+          const int base = (seg.tile0 + (two ? j : 2 * j + a)) * kCols - seg.old;
           // One pass with the maximum so far: weights are taken against it while the tile's own
           // maximum is found, and only where that is too large are they taken again.
           uint32_t w[4][16];
@@ -436,10 +428,22 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         arrive(&bar.p_ready[a]);
       }
       // ----------------------------------------------------------------------------- output
-      if (jobs > 0) ok = ok && warp_wait(&bar.o_done[a], ends++ & 1);
+      // Every score of both accumulators has been read, so Q may be replaced: the next segment is
+      // opened, and its first products run, before this one is written out.
+      const AttnSegment now = seg;
+      if (!(ok = named_bar_all(1, 256, ok))) break;
+      more = attn_next(p, plan, seg.next, x1, seg);
+      if (more) ask(seg);
+      if (jobs > 0) ok = warp_wait(&bar.o_done[a], ends++ & 1);
       ok = ok && warp_wait(&bar.v_clean, seg_no & 1);
       tmem_fence_after();
       if (anc & s_poison) l = __int_as_float(0x7FC00000);
+      const bool write = mine && !s_bad;
+      if (!(ok = named_bar_all(1, 256, ok))) break;  // all have read s_poison and s_bad
+      if (tid == 0) s_bad = 0;
+      if (tid == 0) s_poison = 0;
+      named_bar_sync(1, 256);
+      if (more) open();
       // this row's sums, B's merged into A's where both hold parts of one row
       float fa = 1.f, fb = 0.f;
       float* swap = reinterpret_cast<float*>(smem + S::q + S::kQ);  // [HD / 2][128], Q of B's rows
@@ -452,10 +456,10 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = jobs > 0 && !idle ? __uint_as_float(u[k]) : 0.f;
       };
-      const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
-      const int slot = whole ? 0 : attn_slot(p, sh, g, mt, seg.unit0);
-      char* y = p.out + seg.b * p.outr + t_of * p.outt +
-                static_cast<long long>(seg.h * p.G + (mine ? rr % p.G : 0)) * HD * 2;
+      const bool whole = now.tile0 == 0 && now.tile1 == now.tiles;
+      const int slot = whole ? 0 : attn_slot(p, sh, g, mt, now.unit0);
+      char* y = p.out + now.b * p.outr + t_of * p.outt +
+                static_cast<long long>(now.h * p.G + (mine ? rr % p.G : 0)) * HD * 2;
       auto store_out = [&](int c, const float (&o)[32], float inv) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -467,10 +471,9 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       };
       auto store_lse = [&](float mm, float ll) {
         if (p.lse)
-          p.lse[(static_cast<long long>(seg.b) * p.T + t_of) * p.Hq + seg.h * p.G + rr % p.G] =
+          p.lse[(static_cast<long long>(now.b) * p.T + t_of) * p.Hq + now.h * p.G + rr % p.G] =
               anc ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
       };
-      const bool write = mine && !s_bad && ok;
       // one chunk of the row's merged sums goes to the output, or to the partial results
       auto emit = [&](int c, const float (&o)[32]) {
         if (!write) return;
@@ -530,9 +533,10 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       const bool owner = write && (two || a == 0);
       if (whole) {
         if (owner) store_lse(m, l);
-        continue;
+      } else if (owner) {
+        p.part_ml[static_cast<long long>(slot) * 2 * kRows + pr] = make_float2(m, l);
       }
-      if (owner) p.part_ml[static_cast<long long>(slot) * 2 * kRows + pr] = make_float2(m, l);
+      named_bar_sync(1, 256);  // the next segment's ancestors are there
     }
   }
   if (!ok) set_status(p.status, SPECDEC_ERR_TIMEOUT);
@@ -551,8 +555,10 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 template <int HD>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   constexpr int kPer = HD / 32;  // float4 a thread holds
+  constexpr int kBlock = 64;     // parts at a time
   __shared__ AttnPlan plan;
   __shared__ int s_par[kMaxTree];
+  __shared__ float2 s_ml[kBlock][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   if (warp == 0) attn_plan(p, kCols, plan);
@@ -563,7 +569,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   const int x = sh.start(border);
   const AttnSegment seg = attn_segment(p, plan, x, x + 1);
   const int b = seg.b, h = seg.h, unit0 = seg.unit0;
-  if (seg.tile0 == 0) return;                       // the border cuts no unit
+  if (x <= unit0) return;                           // the border cuts no unit's tiles
   const int g0 = sh.owner(unit0), g1 = sh.owner(unit0 + seg.tiles - 1);
   if (border != g0 + 1) return;                     // another border of the same unit
   if (p.parents && tid < p.T) s_par[tid] = p.parents[b * p.T + tid];
@@ -572,35 +578,51 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   if (tid < p.T) (void)tree_ancestors(p.parents ? s_par : nullptr, tid, bad);
   if (__syncthreads_or(bad)) return;                // the attention reported it
   const int pr = block * 32 + lane, rr = mt * 2 * kRows + pr;
-  if (rr >= p.T * p.G) return;
-  const int t = rr / p.G, qh = h * p.G + rr % p.G;
+  const int t = min(rr / p.G, p.T - 1), qh = h * p.G + rr % p.G;  // (rows that do not exist are not stored)
   const bool live = tree_ancestors(p.parents ? s_par : nullptr, t, bad) != 0;
+  // the parts in blocks: their rows' (m, l) into shared memory at once, then the sums
+  const int parts = g1 - g0 + 1, d0 = warp * kPer;  // d0: first float4
   float m = -INFINITY, l = 0.f;
-  for (int g = g0; g <= g1; ++g) {
-    const float2 w = p.part_ml[static_cast<long long>(attn_slot(p, sh, g, mt, unit0)) * 2 * kRows + pr];
-    const float mn = fmaxf(m, w.x), off = mn == -INFINITY ? 0.f : mn;
-    l = l * ex2(m - off) + w.y * ex2(w.x - off);
-    m = mn;
-  }
-  const float off = m == -INFINITY ? 0.f : m, inv = live ? 1.f / l : 0.f;
   float4 o[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int d0 = warp * kPer;  // first float4
-#pragma unroll 4
-  for (int g = g0; g <= g1; ++g) {
-    const long long sl = attn_slot(p, sh, g, mt, unit0);
-    const float f = ex2(p.part_ml[sl * 2 * kRows + pr].x - off);
-    const float4* w = reinterpret_cast<const float4*>(p.part_o) + (sl * (HD / 4) + d0) * 2 * kRows + pr;
+  const float4* base = reinterpret_cast<const float4*>(p.part_o) + d0 * 2 * kRows + pr;
+  for (int i0 = 0; i0 < parts; i0 += kBlock) {
+    const int n = min(kBlock, parts - i0);
+    __syncthreads();
+    for (int i = warp; i < n; i += 8)
+      s_ml[i][lane] = p.part_ml[static_cast<long long>(attn_slot(p, sh, g0 + i0 + i, mt, unit0)) * 2 * kRows + pr];
+    __syncthreads();
+    float mn = m;
+    for (int i = 0; i < n; ++i) mn = fmaxf(mn, s_ml[i][lane].x);
+    const float off = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - off);
+    m = mn;
+    l *= f0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const float4 v = w[k * 2 * kRows];
-      o[k].x += v.x * f;
-      o[k].y += v.y * f;
-      o[k].z += v.z * f;
-      o[k].w += v.w * f;
+      o[k].x *= f0;
+      o[k].y *= f0;
+      o[k].z *= f0;
+      o[k].w *= f0;
+    }
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float4* w = base + attn_slot(p, sh, g0 + i0 + i, mt, unit0) * static_cast<long long>(HD / 4 * 2 * kRows);
+      const float2 ml = s_ml[i][lane];
+      const float f = ex2(ml.x - off);
+      l += ml.y * f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const float4 v = w[k * 2 * kRows];
+        o[k].x += v.x * f;
+        o[k].y += v.y * f;
+        o[k].z += v.z * f;
+        o[k].w += v.w * f;
+      }
     }
   }
+  const float inv = live ? 1.f / l : 0.f;
+  if (rr >= p.T * p.G) return;
   char* y = p.out + b * p.outr + t * p.outt + static_cast<long long>(qh) * HD * 2 + d0 * 8;
 #pragma unroll
   for (int k = 0; k < kPer; ++k)
