@@ -10,9 +10,10 @@
 //   warps 9, 10     one thread each issues S = Q K^T (both operands in shared memory) and
 //                   O += P V (P from tensor memory, V as it lies: MN-major) of A, of B.
 // Tensor memory (512 columns): S/P of A and B, O of A and B, 128 columns each.
-// The running maximum is only followed when it grows by more than 2^8 in weight: O is then rescaled
-// by the row's thread between its scores' arrival and its weights' release, when no MMA of that
-// accumulator is in flight.  Weights below 2^8 lose nothing: bf16 and fp32 have the range.
+// The running maximum is only followed when it grows by more than 2^32 in weight (and from the
+// first columns on): until then weights, their sum and O are that much larger, which neither fp32
+// nor bf16 minds.  O is then rescaled by the row's thread, when no product of that accumulator is
+// in flight.
 //
 // A tile that holds nodes' columns or the end of a row needs care: its V columns behind the nodes
 // and of unused nodes are zeroed in shared memory (0 * NaN is NaN in a matrix product), and so are
@@ -33,7 +34,7 @@ constexpr int kCols = 128;     // columns of a K/V tile
 constexpr int kRows = 128;     // rows of an accumulator
 constexpr int kStages = 2;
 constexpr uint32_t kTries = 1u << 22;  // polls after which a wait gives up
-constexpr float kGrow = 8.f;   // log2 of the growth of the maximum that is let pass
+constexpr float kGrow = 32.f;  // log2 of the growth of the maximum that is let pass
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -62,7 +63,7 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 
 struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full, v_clean, s_full[2], p_half[2], p_ready[2], o_half[2], o_done[2];
 };
 
 __device__ __forceinline__ bool inf_or_nan(uint32_t w) {  // either of two bf16 values
@@ -144,7 +145,9 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     mbar_init(&bar.v_clean, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_half[i], 128);
       mbar_init(&bar.p_ready[i], 128);
+      mbar_init(&bar.o_half[i], 1);
       mbar_init(&bar.o_done[i], 1);
     }
     fence_mbar_init();
@@ -273,14 +276,23 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         }
         if (j == jobs - 1 && lane == 0) arrive(&bar.v_clean);  // the segment's V has been seen
         if (j + 1 < jobs && !(ok = full(bar.k_full, j + 1))) break;
-        if (!(ok = warp_wait(&bar.p_ready[a], done & 1))) break;
-        ++done;
-        tmem_fence_after();
         const uint64_t va = v_desc + st * (S::kTile / 16);
+        if (!(ok = warp_wait(&bar.p_half[a], done & 1))) break;
+        tmem_fence_after();
         if (elect_one()) {
           mma_ts(t_o, t_s, va, id_o, j > 0);
 #pragma unroll
-          for (int s = 1; s < kCols / 16; ++s)
+          for (int s = 1; s < kCols / 32; ++s)
+            if (s < steps) mma_ts(t_o, t_s + s * 8, va + s * (2048 / 16), id_o, true);
+          mma_commit(&bar.o_half[a]);
+        }
+        __syncwarp();
+        if (!(ok = warp_wait(&bar.p_ready[a], done & 1))) break;
+        ++done;
+        tmem_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int s = kCols / 32; s < kCols / 16; ++s)
             if (s < steps) mma_ts(t_o, t_s + s * 8, va + s * (2048 / 16), id_o, true);
           mma_commit(&bar.v_empty[st]);
           if (j + 1 == jobs) mma_commit(&bar.o_done[a]);
@@ -363,67 +375,79 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         if (!idle) {
           tmem_fence_after();
           const int base = (seg.tile0 + (two ? j : 2 * j + a)) * kCols - seg.old;
-          // One pass with the maximum so far: weights are taken against it while the tile's own
-          // maximum is found, and only where that is too large are they taken again.
-          uint32_t w[4][16];
-          uint64_t sum[2];
-          float mx;
-          auto weigh = [&] {
-            const float off = m == -INFINITY ? 0.f : m;
-            const uint64_t scale2 = pack2(scale, scale), off2 = pack2(-off, -off);
-            float top[2] = {-INFINITY, -INFINITY};
-            sum[0] = sum[1] = 0;
-            uint32_t s[2][32];
-            tmem_ld32(t_s, s[0]);
+          // Half of the columns at a time, in one pass with the maximum so far: weights are taken
+          // against it while the half's own maximum is found, and only where that is too large are
+          // they taken again.  The first half enters the product while the second is weighed.
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t(&v)[32] = s[c & 1];
-              tmem_wait_ld32(v);
-              if (c < 3) tmem_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
-              if (base + kCols > 0) {
-                const uint32_t vis = visible32(anc, base + c * 32);
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t w[2][16];
+            uint64_t sum[2];
+            float mx;
+            auto weigh = [&] {
+              const float off = m == -INFINITY ? 0.f : m;
+              const uint64_t scale2 = pack2(scale, scale), off2 = pack2(-off, -off);
+              float top[2] = {-INFINITY, -INFINITY};
+              sum[0] = sum[1] = 0;
+              uint32_t s[2][32];
+              tmem_ld32(t_s + hf * 64, s[0]);
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (!(vis >> k & 1)) v[k] = __float_as_uint(-INFINITY);
+              for (int c = 0; c < 2; ++c) {
+                uint32_t(&v)[32] = s[c];
+                tmem_wait_ld32(v);
+                if (c == 0) tmem_ld32(t_s + hf * 64 + 32, s[1]);
+                if (base + kCols > 0) {
+                  const uint32_t vis = visible32(anc, base + hf * 64 + c * 32);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    if (!(vis >> k & 1)) v[k] = __float_as_uint(-INFINITY);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  top[k & 1] = fmaxf(top[k & 1], fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+                  const float2 z = unpack2(fma2(pack2u(v[2 * k], v[2 * k + 1]), scale2, off2));
+                  const float e0 = ex2(z.x), e1 = ex2(z.y);
+                  sum[k & 1] = add2(sum[k & 1], pack2(e0, e1));
+                  // rounded to bf16: with V in bf16 the product takes nothing wider
+                  w[c][k] = bf16_pack(e0, e1);
+                }
               }
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                top[k & 1] = fmaxf(top[k & 1], fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
-                const float2 z = unpack2(fma2(pack2u(v[2 * k], v[2 * k + 1]), scale2, off2));
-                const float e0 = ex2(z.x), e1 = ex2(z.y);
-                sum[k & 1] = add2(sum[k & 1], pack2(e0, e1));
-                // rounded to bf16: with V in bf16 the product takes nothing wider
-                w[c][k] = bf16_pack(e0, e1);
-              }
-            }
-            mx = fmaxf(top[0], top[1]) * scale;
-          };
-          weigh();
-          const bool up = mx > m + kGrow || (m == -INFINITY && mx > m);
-          if (__any_sync(0xffffffffu, up)) {
-            const float mn = up ? mx : m;
-            const float f = up ? ex2(m - mn) : 1.f;
-            l *= f;
-            m = mn;
-            if (j > 0) {
-#pragma unroll 1
-              for (int c = 0; c < HD / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld16(t_o + c * 16, o);
-                tmem_wait_ld16(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st16(t_o + c * 16, o);
-              }
-            }
+              mx = fmaxf(top[0], top[1]) * scale;
+            };
             weigh();
-          }
+            const bool up = mx > m + kGrow || (m == -INFINITY && mx > m);
+            if (__any_sync(0xffffffffu, up)) {
+              const float mn = up ? mx : m;
+              const float f = up ? ex2(m - mn) : 1.f;
+              l *= f;
+              m = mn;
+              if (hf == 1) {  // the first half's product is on its way into O
+                ok = warp_wait(&bar.o_half[a], seen & 1);
+                tmem_fence_after();
+              }
+              if (j > 0 || hf == 1) {
+#pragma unroll 1
+                for (int c = 0; c < HD / 16; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(t_o + c * 16, o);
+                  tmem_wait_ld16(o);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, w[c]);
-          const float2 both = unpack2(add2(sum[0], sum[1]));
-          l += both.x + both.y;
-          tmem_wait_st();
-          tmem_fence_before();
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tmem_st16(t_o + c * 16, o);
+                }
+              }
+              weigh();
+            }
+            // the weights go over scores that have been read
+            tmem_st16(t_s + hf * 32, w[0]);
+            tmem_st16(t_s + hf * 32 + 16, w[1]);
+            const float2 both = unpack2(add2(sum[0], sum[1]));
+            l += both.x + both.y;
+            tmem_wait_st();
+            tmem_fence_before();
+            if (hf == 0) arrive(&bar.p_half[a]);
+          }
+        } else {
+          arrive(&bar.p_half[a]);
         }
         arrive(&bar.p_ready[a]);
       }
@@ -560,7 +584,6 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   __shared__ int s_par[kMaxTree];
   __shared__ float2 s_ml[kBlock][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
   if (warp == 0) attn_plan(p, kCols, plan);
   __syncthreads();
   const AttnShares sh = attn_shares(p, plan);
@@ -580,6 +603,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   const int pr = block * 32 + lane, rr = mt * 2 * kRows + pr;
   const int t = min(rr / p.G, p.T - 1), qh = h * p.G + rr % p.G;  // (rows that do not exist are not stored)
   const bool live = tree_ancestors(p.parents ? s_par : nullptr, t, bad) != 0;
+  pdl_wait();  // (what is read before, the attention read too)
   // the parts in blocks: their rows' (m, l) into shared memory at once, then the sums
   const int parts = g1 - g0 + 1, d0 = warp * kPer;  // d0: first float4
   float m = -INFINITY, l = 0.f;
