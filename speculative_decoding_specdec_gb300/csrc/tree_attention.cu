@@ -328,19 +328,20 @@ AttnShape attn_shape(int es, int T, int G, int hd) {
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
   s.tile = 128;
   s.min_tiles = 1;
-  s.open = s.kind == kTc ? 3 : 0;
+  s.open = s.kind == kTc ? 6 : 0;
   return s;
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct AttnWorkspace {
-  size_t ticket, ml, o, bytes;  // offsets
+  size_t ticket, cuts, ml, o, bytes;  // offsets
 };
 AttnWorkspace attn_workspace(const AttnShape& s, int B, int H, int hd) {
   AttnWorkspace w;
   w.ticket = 0;
-  w.ml = round256(static_cast<size_t>(B) * H * s.MT * 4);
+  w.cuts = round256(static_cast<size_t>(B) * H * s.MT * 4);
+  w.ml = w.cuts + round256(static_cast<size_t>(s.groups) * 16);
   w.o = w.ml + round256(static_cast<size_t>(s.grid) * 2 * s.M * 8);
   w.bytes = w.o + round256(static_cast<size_t>(s.grid) * 2 * s.M * hd * 4);
   return w;
@@ -420,7 +421,7 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   s.grid = s.groups * s.MT;
   const AttnWorkspace w = attn_workspace(s, a->B, c.heads, c.head_dim);
   if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
-  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kTile + 8) >= (1LL << 31))
+  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kTile + 16) >= (1LL << 31))
     return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   AttnParams p = {};
   p.cache = to_bytes(c);
@@ -440,6 +441,7 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   p.status = a->dev_status;
   char* ws = static_cast<char*>(a->workspace);
   p.ticket = reinterpret_cast<unsigned*>(ws + w.ticket);
+  p.cuts = reinterpret_cast<int4*>(ws + w.cuts);
   p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.scale_log2 = a->scale * kLog2e;

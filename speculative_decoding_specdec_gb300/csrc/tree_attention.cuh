@@ -34,6 +34,7 @@ struct AttnParams {
   unsigned* ticket;  // [B * H * MT], zero between calls
   float2* part_ml;   // [grid * 2][M]
   float* part_o;     // [grid * 2][M][hd]
+  int4* cuts;        // [groups], tensor-core kernel: the units that borders cut
   float scale_log2;  // scale * log2(e)
   int B, T, Hq, H, G, hd, cap, one_row, MT, groups, min_tiles, open, g_shift;  // g_shift: log2 G, or -1
 };

@@ -33,7 +33,7 @@ constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 constexpr int kCols = 128;     // columns of a K/V tile
 constexpr int kRows = 128;     // rows of an accumulator
 constexpr int kStages = 2;
-constexpr uint32_t kTries = 1u << 22;  // polls after which a wait gives up
+constexpr uint32_t kTries = 1u << 18;  // polls after which a wait gives up
 constexpr float kGrow = 32.f;  // log2 of the growth of the maximum that is let pass
 
 __device__ __forceinline__ float ex2(float x) {
@@ -365,6 +365,15 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       open();
       named_bar_sync(1, 256);
     }
+    // What the merge has to know of the border before this share, if it is the first one that cuts
+    // a unit: the unit, its parts' first slot and how many there are.
+    if (mt == 0 && tid == 0) {
+      int4 cut = make_int4(0, 0, 0, 0);
+      if (more && !s_bad && x0 > seg.unit0 && sh.owner(seg.unit0) == g - 1)
+        cut = make_int4(seg.b, seg.h, sh.start(g - 1) >= seg.unit0 ? 0 : 1,
+                        sh.owner(seg.unit0 + seg.tiles - 1) - g + 2);
+      p.cuts[g] = cut;
+    }
     for (; more; ++seg_no) {
       const int n = seg.tile1 - seg.tile0;
       const unsigned long long anc = mine ? s_anc[t_of] : 0ull;
@@ -558,7 +567,8 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       if (whole) {
         if (owner) store_lse(m, l);
       } else if (owner) {
-        p.part_ml[static_cast<long long>(slot) * 2 * kRows + pr] = make_float2(m, l);
+        // (a row without a used node is told by an infinite sum)
+        p.part_ml[static_cast<long long>(slot) * 2 * kRows + pr] = make_float2(m, anc ? l : INFINITY);
       }
       named_bar_sync(1, 256);  // the next segment's ancestors are there
     }
@@ -580,32 +590,18 @@ template <int HD>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   constexpr int kPer = HD / 32;  // float4 a thread holds
   constexpr int kBlock = 64;     // parts at a time
-  __shared__ AttnPlan plan;
-  __shared__ int s_par[kMaxTree];
   __shared__ float2 s_ml[kBlock][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) attn_plan(p, kCols, plan);
-  __syncthreads();
-  const AttnShares sh = attn_shares(p, plan);
-  const int border = blockIdx.x + 1, block = blockIdx.y & 7, mt = blockIdx.y >> 3;
-  if (sh.total == 0 || border >= sh.groups) return;
-  const int x = sh.start(border);
-  const AttnSegment seg = attn_segment(p, plan, x, x + 1);
-  const int b = seg.b, h = seg.h, unit0 = seg.unit0;
-  if (x <= unit0) return;                           // the border cuts no unit's tiles
-  const int g0 = sh.owner(unit0), g1 = sh.owner(unit0 + seg.tiles - 1);
-  if (border != g0 + 1) return;                     // another border of the same unit
-  if (p.parents && tid < p.T) s_par[tid] = p.parents[b * p.T + tid];
-  __syncthreads();
-  bool bad = false;
-  if (tid < p.T) (void)tree_ancestors(p.parents ? s_par : nullptr, tid, bad);
-  if (__syncthreads_or(bad)) return;                // the attention reported it
-  const int pr = block * 32 + lane, rr = mt * 2 * kRows + pr;
-  const int t = min(rr / p.G, p.T - 1), qh = h * p.G + rr % p.G;  // (rows that do not exist are not stored)
-  const bool live = tree_ancestors(p.parents ? s_par : nullptr, t, bad) != 0;
-  pdl_wait();  // (what is read before, the attention read too)
+  const int g0 = blockIdx.x, block = blockIdx.y & 7, mt = blockIdx.y >> 3;
+  const int pr = block * 32 + lane, rr = mt * 2 * kRows + pr, t = rr / p.G;
+  pdl_wait();
+  const int4 cut = __ldcg(p.cuts + g0 + 1);
+  const int b = cut.x, qh = cut.y * p.G + rr - t * p.G, parts = cut.w;
+  if (parts < 2) return;
+  auto slot = [&](int i) { return 2ll * ((g0 + i) * p.MT + mt) + (i == 0 ? cut.z : 0); };
   // the parts in blocks: their rows' (m, l) into shared memory at once, then the sums
-  const int parts = g1 - g0 + 1, d0 = warp * kPer;  // d0: first float4
+  const int d0 = warp * kPer;  // first float4
+  bool live = true;
   float m = -INFINITY, l = 0.f;
   float4 o[kPer];
 #pragma unroll
@@ -615,8 +611,9 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
     const int n = min(kBlock, parts - i0);
     __syncthreads();
     for (int i = warp; i < n; i += 8)
-      s_ml[i][lane] = p.part_ml[static_cast<long long>(attn_slot(p, sh, g0 + i0 + i, mt, unit0)) * 2 * kRows + pr];
+      s_ml[i][lane] = p.part_ml[slot(i0 + i) * 2 * kRows + pr];
     __syncthreads();
+    live &= s_ml[0][lane].y != INFINITY;
     float mn = m;
     for (int i = 0; i < n; ++i) mn = fmaxf(mn, s_ml[i][lane].x);
     const float off = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - off);
@@ -631,7 +628,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
     }
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const float4* w = base + attn_slot(p, sh, g0 + i0 + i, mt, unit0) * static_cast<long long>(HD / 4 * 2 * kRows);
+      const float4* w = base + slot(i0 + i) * (HD / 4 * 2 * kRows);
       const float2 ml = s_ml[i][lane];
       const float f = ex2(ml.x - off);
       l += ml.y * f;
