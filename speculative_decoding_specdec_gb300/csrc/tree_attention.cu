@@ -460,7 +460,7 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   p.g_shift = (G & (G - 1)) == 0 ? __builtin_ctz(G) : -1;
   cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
   if (s.kind == kTc) return launch_attn_tc(p, c.rows, s.grid, stream_);
-  if (s.kind == kMma) return launch_attn_mma(p, c.rows, s.grid, stream_);
+  if (s.kind == kMma) return launch_attn_mma(p, s.M, c.rows, s.grid, stream_);
   if (es == 2)
     return c.head_dim <= 128 ? launch_fma_rows<uint16_t, 1>(p, s, stream_)
                              : launch_fma_rows<uint16_t, 2>(p, s, stream_);

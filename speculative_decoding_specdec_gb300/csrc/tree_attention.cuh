@@ -217,6 +217,6 @@ void attn_tc_shape(int R, int* M, int* MT);
 int launch_attn_tc(const AttnParams& p, int rows, int grid, cudaStream_t stream);
 // The kernel for few rows (tree_attention_mma.cu).
 void attn_mma_shape(int R, int hd, int* M, int* MT, int* per_sm);
-int launch_attn_mma(const AttnParams& p, int rows, int grid, cudaStream_t stream);
+int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, cudaStream_t stream);
 
 }  // namespace specdec

@@ -1,14 +1,16 @@
 // Attention of a draft tree over the cache for few query rows per K/V head: bf16, head sizes 64
-// and 128, M-tiles of 16 rows.
+// and 128, M-tiles of 8 or 16 rows.
 //
 // With at most 16 rows (a token or a short chain with one or a few query heads per K/V head) a
 // K/V column of 512 bytes meets 16 * 512 flops: HBM bounds it, and tensor memory's 128-row tiles
-// would be nearly empty.  So a warp is the unit: it streams its own 32 columns of each 128-column
+// would be nearly empty.  So a warp is the unit: it streams its own 16 columns of each 128-column
 // tile by TMA (128-byte swizzle) into two private stages, without any CTA-wide barrier, and runs
-// both products with m16n8k16: S = Q K^T (Q in registers for the whole segment), the softmax
-// weights' accumulator layout is the next product's A operand as it stands, O += P V.  Each warp
-// keeps maximum, sum and O of its columns; the four are merged in shared memory when the
-// segment ends, while the next segment's tiles are already on their way.
+// both products with m16n8k16, transposed so that the columns (or the head's values) fill the 16
+// and the query rows the 8: S^T = K Q^T (Q in registers for the whole segment) and O^T += V^T P^T,
+// the weights turned by one movmatrix per 8 x 8.  Query rows as the 16 took twice the
+// instructions for 8 rows, and four warps left the SM's latencies uncovered.  Each warp keeps
+// maximum, sum and O of its columns; the eight are merged in shared memory when the segment ends,
+// while the next segment's tiles are already on their way.
 #include <cmath>
 
 #include "tcgen05.cuh"
@@ -17,12 +19,12 @@
 namespace specdec {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kRows = 16;
-constexpr int kCols = 32;                // columns of a warp's slice of a tile
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kCols = 16;                // columns of a warp's slice of a tile
 constexpr int kTileCols = kCols * kWarps;
 constexpr int kStages = 2;
 constexpr uint32_t kTries = 1u << 17, kNs = 20000;  // a wait gives up after about 2.6 s
+constexpr float kGrow = 32.f;  // log2 of the growth of the maximum that is let pass
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -47,15 +49,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The transpose of an 8 x 8 matrix of 16-bit values held as a product's result is.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ bool inf_or_nan(uint32_t w) {  // either of two bf16 values
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 
-template <int HD> struct Smem {
+template <int HD, int NT> struct Smem {
   static constexpr int kSlice = kCols * HD * 2;               // K or V of a warp's slice
   static constexpr int kWarp = kStages * 2 * kSlice;          // [stage][K, V]
+  static constexpr int kRows = 8 * NT;
   static constexpr int kPitch = HD + 4;                       // floats of a row to merge
-  static constexpr int merge = kWarps * kWarp;                // [warp][16][kPitch]
+  static constexpr int merge = kWarps * kWarp;                // [warp][kRows][kPitch]
   static constexpr int bytes = merge + kWarps * kRows * kPitch * 4 + 1024;
 };
 
@@ -66,11 +75,12 @@ struct Cursor {
   bool more;  // not behind the last
 };
 
-template <int HD>
+// NT: groups of 8 query rows.
+template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads)
 attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
-  using S = Smem<HD>;
-  constexpr int kSteps = HD / 16, kPanels = HD / 64;
+  using S = Smem<HD, NT>;
+  constexpr int kSteps = HD / 16, kPanels = HD / 64, kRows = S::kRows;
   extern __shared__ char raw[];
   __shared__ AttnPlan plan;
   __shared__ uint64_t s_full[kWarps][kStages];
@@ -147,28 +157,37 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       }
       __syncthreads();
     }
-    // this thread's rows gr and gr + 8: Q as A operand, ancestors
-    uint32_t q[kSteps][4];
-    unsigned long long anc[2];
+    // Q as B operand (this thread's rows 8n + gr), and the ancestors of its results' rows
+    // 8n + 2 qd and one more
+    uint32_t q[NT][kSteps][2];
+    unsigned long long anc[NT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = gr + 8 * i, rr = mt * kRows + r;
-      const bool in = r < nrows;
-      const int t = in ? rr / p.G : 0, h = seg.h * p.G + (in ? rr % p.G : 0);
-      anc[i] = in ? s_anc[t] : 0ull;
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + gr, rr = mt * kRows + r;
+      const int t = r < nrows ? rr / p.G : 0, h = seg.h * p.G + (r < nrows ? rr % p.G : 0);
       const char* src = p.q + seg.b * p.qr + t * p.qt + static_cast<long long>(h) * HD * 2 + qd * 4;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        q[s][i] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + s * 32)) ^ flip : 0u;
-        q[s][i + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + s * 32 + 16)) ^ flip : 0u;
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          q[n][s][i] = r < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + s * 32 + i * 16)) ^ flip : 0u;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ro = 8 * n + 2 * qd + i;
+        anc[n][i] = ro < nrows ? s_anc[(mt * kRows + ro) / p.G] : 0ull;
       }
     }
-    float o[HD / 8][4];
+    float o[NT][kSteps][4];
+    float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int j = 0; j < HD / 8; ++j)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
     unsigned long long poison = 0;
     for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++used) {
       const int st = used % kStages;
@@ -176,98 +195,106 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
                                                          kTries, kNs));
       const int col = tile * kTileCols + warp * kCols, base = col - seg.old;
       if (ok && col < seg.cols) {
-        const char* km = mem + st * 2 * S::kSlice;
         char* vm = mem + (st * 2 + 1) * S::kSlice;
-        const uint32_t ka = smem_addr(km), va = smem_addr(vm);
-        float s[kCols / 8][4];
-#pragma unroll
-        for (int j = 0; j < kCols / 8; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[j][k] = 0.f;
+        const uint32_t ka = smem_addr(mem + st * 2 * S::kSlice), va = smem_addr(vm);
         const int mi = lane >> 3, mr = lane & 7;  // matrix and row this lane addresses
+        float s[NT][2][4];  // (two sums of every other step: shorter chains)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[n][0][k] = s[n][1][k] = 0.f;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
+          const int c = (mi & 1) * 8 + mr, ch = k * 2 + (mi >> 1);
+          uint32_t f[4];
+          ldmatrix4(ka + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ mr) << 4), f[0], f[1], f[2], f[3]);
 #pragma unroll
-          for (int j = 0; j < kCols / 16; ++j) {
-            const int c = j * 16 + (mi >> 1) * 8 + mr, ch = k * 2 + (mi & 1);
-            uint32_t b0, b1, b2, b3;
-            ldmatrix4(ka + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ mr) << 4), b0, b1, b2, b3);
-            mma16816(s[2 * j], q[k], b0, b1);
-            mma16816(s[2 * j + 1], q[k], b2, b3);
-          }
+          for (int n = 0; n < NT; ++n) mma16816(s[n][k & 1], f, q[n][k][0], q[n][k][1]);
         }
+        float z[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[n][k] = (s[n][0][k] + s[n][1][k]) * scale;
         if (base + kCols > 0) {
           // columns behind the committed ones: what each row sees, and V where it may hold anything
 #pragma unroll
-          for (int j = 0; j < kCols / 8; ++j)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int node = base + j * 8 + qd * 2 + (k & 1);
-              if (node >= 0 && !(node < p.T && (anc[k >> 1] >> node & 1))) s[j][k] = -INFINITY;
+              const int node = base + gr + (k >> 1) * 8;
+              if (node >= 0 && !(node < p.T && (anc[n][k & 1] >> node & 1))) z[n][k] = -INFINITY;
             }
-          const int node = base + lane;  // a lane looks after one column
-          bool bad = false;
+          const int c = lane & 15, node = base + c;  // two lanes look after a column
+          bool bad = false, drop = false;
           if (node >= 0) {
-            const bool live = node < p.T && s_anc[node] != 0;
-            if (live)
-              for (int ch = 0; ch < HD / 8; ++ch) {
-                const uint4 v = *reinterpret_cast<const uint4*>(vm + (ch >> 3) * kCols * 128 + lane * 128 + (((ch & 7) ^ (lane & 7)) << 4));
+            drop = node >= p.T || s_anc[node] == 0;
+            if (!drop)
+              for (int ch = (lane >> 4) * (HD / 16); ch < ((lane >> 4) + 1) * (HD / 16); ++ch) {
+                const uint4 v = *reinterpret_cast<const uint4*>(vm + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ (c & 7)) << 4));
                 bad |= inf_or_nan(v.x) || inf_or_nan(v.y) || inf_or_nan(v.z) || inf_or_nan(v.w);
               }
-            if (!live || bad)
-              for (int ch = 0; ch < HD / 8; ++ch)
-                *reinterpret_cast<uint4*>(vm + (ch >> 3) * kCols * 128 + lane * 128 + (((ch & 7) ^ (lane & 7)) << 4)) = make_uint4(0, 0, 0, 0);
           }
-          const unsigned long long which = __ballot_sync(0xffffffffu, bad);
-          if (which) poison |= base >= 0 ? which << base : which >> -base;
+          unsigned long long which = __ballot_sync(0xffffffffu, bad);
+          which = (which | which >> 16) & 0xffffu;
+          drop |= which >> c & 1;
+          if (drop)
+            for (int ch = (lane >> 4) * (HD / 16); ch < ((lane >> 4) + 1) * (HD / 16); ++ch)
+              *reinterpret_cast<uint4*>(vm + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ (c & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+          poison |= base >= 0 ? which << base : which >> -base;
           fence_async_smem();
           __syncwarp();
         }
-        float f[2];
+        // the maximum is followed only where it grows much: until then weights, sum and O are that
+        // much larger, which neither fp32 nor bf16 minds
         bool up = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = s[0][2 * i];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < kCols / 8; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scale;
-          const float mn = fmaxf(m[i], mx);
-          up |= mn > m[i];
-          f[i] = mn > m[i] ? ex2(m[i] - mn) : 1.f;
-          m[i] = mn;
-          const float off = mn == -INFINITY ? 0.f : mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < kCols / 8; ++j) {
-            s[j][2 * i] = ex2(fmaf(s[j][2 * i], scale, -off));
-            s[j][2 * i + 1] = ex2(fmaf(s[j][2 * i + 1], scale, -off));
-            sum += s[j][2 * i] + s[j][2 * i + 1];
+          for (int i = 0; i < 2; ++i) {
+            const float mx = fmaxf(z[n][i], z[n][i + 2]);
+            up |= mx > m[n][i] + kGrow || (m[n][i] == -INFINITY && mx > m[n][i]);
           }
-          l[i] = l[i] * f[i] + sum;
-        }
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-          for (int j = 0; j < HD / 8; ++j) {
-            o[j][0] *= f[0];
-            o[j][1] *= f[0];
-            o[j][2] *= f[1];
-            o[j][3] *= f[1];
-          }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float mx = fmaxf(z[n][i], z[n][i + 2]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              if (mx > m[n][i]) {
+                const float f = ex2(m[n][i] - mx);
+                m[n][i] = mx;
+                l[n][i] *= f;
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) {
+                  o[n][j][i] *= f;
+                  o[n][j][i + 2] *= f;
+                }
+              }
+            }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float e[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k] = ex2(z[n][k] - (m[n][k & 1] == -INFINITY ? 0.f : m[n][k & 1]));
+          l[n][0] += e[0] + e[2];
+          l[n][1] += e[1] + e[3];
+          // the weights, rounded to bf16: with V in bf16 the product takes nothing wider
+          pb[n][0] = transposed(bf16_pack(e[0], e[1]));
+          pb[n][1] = transposed(bf16_pack(e[2], e[3]));
         }
 #pragma unroll
-        for (int kb = 0; kb < kCols / 16; ++kb) {
-          // the weights, rounded to bf16: with V in bf16 the product takes nothing wider
-          const uint32_t pa[4] = {bf16_pack(s[2 * kb][0], s[2 * kb][1]), bf16_pack(s[2 * kb][2], s[2 * kb][3]),
-                                  bf16_pack(s[2 * kb + 1][0], s[2 * kb + 1][1]), bf16_pack(s[2 * kb + 1][2], s[2 * kb + 1][3])};
+        for (int j = 0; j < kSteps; ++j) {
+          const int c = (mi >> 1) * 8 + mr, ch = j * 2 + (mi & 1);
+          uint32_t f[4];
+          ldmatrix4t(va + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ mr) << 4), f[0], f[1], f[2], f[3]);
 #pragma unroll
-          for (int n = 0; n < HD / 16; ++n) {
-            const int c = kb * 16 + (mi & 1) * 8 + mr, ch = n * 2 + (mi >> 1);
-            uint32_t b0, b1, b2, b3;
-            ldmatrix4t(va + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ mr) << 4), b0, b1, b2, b3);
-            mma16816(o[2 * n], pa, b0, b1);
-            mma16816(o[2 * n + 1], pa, b2, b3);
-          }
+          for (int n = 0; n < NT; ++n) mma16816(o[n][j], f, pb[n][0], pb[n][1]);
         }
       }
       __syncwarp();
@@ -277,41 +304,47 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         ++loaded;
       }
     }
-    // ------------------------------------------------------------- the four warps' parts
+    // ------------------------------------------------------------- the eight warps' parts
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (anc[i] & poison) l[i] = __int_as_float(0x7FC00000);  // the row sees a column that is not finite
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 4);
+        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 8);
+        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
+        if (anc[n][i] & poison) l[n][i] = __int_as_float(0x7FC00000);  // the row sees a column that is not finite
+      }
     __syncthreads();  // the segment before has been merged
-    if (qd == 0) {
-      s_ml[warp][gr] = make_float2(m[0], l[0]);
-      s_ml[warp][gr + 8] = make_float2(m[1], l[1]);
-    }
 #pragma unroll
-    for (int j = 0; j < HD / 8; ++j) {
-      float* w = merge + (warp * kRows + gr) * S::kPitch + j * 8 + qd * 2;
-      *reinterpret_cast<float2*>(w) = make_float2(o[j][0], o[j][1]);
-      *reinterpret_cast<float2*>(w + 8 * S::kPitch) = make_float2(o[j][2], o[j][3]);
+    for (int n = 0; n < NT; ++n) {
+      if (gr == 0) {
+        s_ml[warp][8 * n + 2 * qd] = make_float2(m[n][0], l[n][0]);
+        s_ml[warp][8 * n + 2 * qd + 1] = make_float2(m[n][1], l[n][1]);
+      }
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          merge[(warp * kRows + 8 * n + 2 * qd + (k & 1)) * S::kPitch + j * 16 + gr + (k >> 1) * 8] = o[n][j][k];
     }
     __syncthreads();
-    const int r = tid >> 3, d0 = (tid & 7) * 4;  // row, and every 32nd group of 4 values from d0
+    // 16 threads per row: every 16th group of 4 values from d0
+    const int r = tid >> 4, d0 = (tid & 15) * 4;
     const int rr = mt * kRows + r;
     const bool mine = r < nrows && !s_bad;
     const int t = mine ? rr / p.G : 0, h = seg.h * p.G + (mine ? rr % p.G : 0);
     const bool live = mine && s_anc[t] != 0;
     float mm = -INFINITY, ll = 0.f;
-    float4 acc[HD / 32];
+    float4 acc[HD / 64];
 #pragma unroll
-    for (int j = 0; j < HD / 32; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < HD / 64; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 ml, auto at) {  // one more part of the row
       const float mn = fmaxf(mm, ml.x), off = mn == -INFINITY ? 0.f : mn;
       const float fa = ex2(mm - off), fb = ex2(ml.x - off);
       ll = ll * fa + ml.y * fb;
       mm = mn;
 #pragma unroll
-      for (int j = 0; j < HD / 32; ++j) {
+      for (int j = 0; j < HD / 64; ++j) {
         const float4 v = at(j);
         acc[j].x = acc[j].x * fa + v.x * fb;
         acc[j].y = acc[j].y * fa + v.y * fb;
@@ -319,18 +352,19 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         acc[j].w = acc[j].w * fa + v.w * fb;
       }
     };
+    if (mine)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      add(s_ml[w][r], [&](int j) {
-        return *reinterpret_cast<const float4*>(merge + (w * kRows + r) * S::kPitch + d0 + j * 32);
-      });
+      for (int w = 0; w < kWarps; ++w)
+            add(s_ml[w][r], [&](int j) {
+          return *reinterpret_cast<const float4*>(merge + (w * kRows + r) * S::kPitch + d0 + j * 64);
+        });
     if (seg.tile0 > 0 || seg.tile1 < seg.tiles) {
       const long long at = static_cast<long long>(attn_slot(p, sh, g, mt, seg.unit0)) * kRows + r;
       if (mine) {
         if (d0 == 0) p.part_ml[at] = make_float2(mm, ll);
 #pragma unroll
-        for (int j = 0; j < HD / 32; ++j)
-          *reinterpret_cast<float4*>(p.part_o + at * HD + d0 + j * 32) = acc[j];
+        for (int j = 0; j < HD / 64; ++j)
+          *reinterpret_cast<float4*>(p.part_o + at * HD + d0 + j * 64) = acc[j];
       }
       if (s_bad) continue;
       const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1);
@@ -338,12 +372,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       mm = -INFINITY;
       ll = 0.f;
 #pragma unroll
-      for (int j = 0; j < HD / 32; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < HD / 64; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (mine)
         for (int gg = g0; gg <= g1; ++gg) {
           const long long a2 = static_cast<long long>(attn_slot(p, sh, gg, mt, seg.unit0)) * kRows + r;
           add(__ldcg(p.part_ml + a2), [&](int j) {
-            return __ldcg(reinterpret_cast<const float4*>(p.part_o + a2 * HD + d0 + j * 32));
+            return __ldcg(reinterpret_cast<const float4*>(p.part_o + a2 * HD + d0 + j * 64));
           });
         }
     }
@@ -351,8 +385,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     const float inv = live ? 1.f / ll : 0.f;
     char* y = p.out + seg.b * p.outr + t * p.outt + static_cast<long long>(h) * HD * 2;
 #pragma unroll
-    for (int j = 0; j < HD / 32; ++j)
-      *reinterpret_cast<uint2*>(y + (d0 + j * 32) * 2) =
+    for (int j = 0; j < HD / 64; ++j)
+      *reinterpret_cast<uint2*>(y + (d0 + j * 64) * 2) =
           make_uint2(bf16_pack(acc[j].x * inv, acc[j].y * inv), bf16_pack(acc[j].z * inv, acc[j].w * inv));
     if (p.lse && d0 == 0)
       p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + h] =
@@ -366,10 +400,10 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   }
 }
 
-template <int HD>
+template <int HD, int NT>
 int launch_mma(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {
-  auto kernel = attn_mma_kernel<HD>;
-  constexpr int smem = Smem<HD>::bytes;
+  auto kernel = attn_mma_kernel<HD, NT>;
+  constexpr int smem = Smem<HD, NT>::bytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return map_cuda_error(e);
   kernel<<<grid, kThreads, smem, stream>>>(p, map);
@@ -379,15 +413,17 @@ int launch_mma(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream
 }  // namespace
 
 void attn_mma_shape(int R, int hd, int* M, int* MT, int* per_sm) {
-  *M = kRows;
-  *MT = (R + kRows - 1) / kRows;
-  *per_sm = hd == 64 ? 2 : 1;  // by shared memory
+  *M = R <= 8 ? 8 : 16;
+  *MT = (R + *M - 1) / *M;
+  *per_sm = hd == 64 && *M == 8 ? 2 : 1;  // by shared memory
 }
 
-int launch_attn_mma(const AttnParams& p, int rows, int grid, cudaStream_t stream) {
+int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, cudaStream_t stream) {
   CUtensorMap map;
   if (!kv_tensor_map(&map, p.cache, p.hd, p.cap, p.H, rows, kCols)) return SPECDEC_ERR_UNSUPPORTED;
-  return p.hd == 64 ? launch_mma<64>(p, map, grid, stream) : launch_mma<128>(p, map, grid, stream);
+  if (M == 8)
+    return p.hd == 64 ? launch_mma<64, 1>(p, map, grid, stream) : launch_mma<128, 1>(p, map, grid, stream);
+  return p.hd == 64 ? launch_mma<64, 2>(p, map, grid, stream) : launch_mma<128, 2>(p, map, grid, stream);
 }
 
 }  // namespace specdec
