@@ -54,7 +54,6 @@ template <typename T, int RG, int NB>
 __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
   constexpr int kThreads = RG * 32, M = RG * 4;
   extern __shared__ __align__(16) char smem[];
-  __shared__ AttnPlan plan;
   __shared__ int s_par[kMaxTree], s_flag, s_bad;
   __shared__ unsigned long long s_anc[kMaxTree];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -63,6 +62,7 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
   char* s_v = s_k + 2 * kTile * pitch;
   float* s_q = reinterpret_cast<float*>(s_v + 2 * kTile * pitch);  // [M][hd], times scale_log2
   float4* s_p = reinterpret_cast<float4*>(s_q + M * hd) + warp * kTile;  // [kTile] x 4 rows
+  const AttnPlan plan = attn_plan_at(reinterpret_cast<float4*>(s_q + M * hd) + RG * kTile, p.B);
   if (warp == 0) attn_plan(p, kTile, plan);
   __syncthreads();
   const AttnShares sh = attn_shares(p, plan);
@@ -317,18 +317,18 @@ AttnShape attn_shape(int es, int T, int G, int hd) {
   if (es != 2 || (hd != 64 && hd != 128)) return fma_shape(es, T, G, hd);
   AttnShape s = {};
   int per_sm = 1;
-  if (T * G <= 16) {
+  if (T * G <= 32) {
     s.kind = kMma;
-    attn_mma_shape(T * G, hd, &s.M, &s.MT, &per_sm);
+    attn_mma_shape(T * G, hd, &s.M, &s.MT, &s.tile, &per_sm);
   } else {
     s.kind = kTc;
     attn_tc_shape(T * G, &s.M, &s.MT);
+    s.tile = 128;
   }
   s.groups = std::max(1, sm_count() * per_sm / s.MT);
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
-  s.tile = 128;
   s.min_tiles = 1;
-  s.open = s.kind == kTc ? 6 : 0;
+  s.open = s.kind == kTc ? 6 : 3;
   return s;
 }
 
@@ -351,9 +351,9 @@ template <typename T, int RG, int NB>
 int launch_fma(const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
   auto kernel = attn_fma_kernel<T, RG, NB>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(s.smem));
+                                             static_cast<int>(s.smem) + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<s.grid, RG * 32, s.smem, stream>>>(p);
+  kernel<<<s.grid, RG * 32, s.smem + attn_plan_bytes(p.B), stream>>>(p);
   return map_cuda_error(cudaGetLastError());
 }
 template <typename T, int NB>

@@ -75,13 +75,18 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b, int* err
 
 // The plan in shared memory: tiles of the rows before row b, per K/V head, and the rows.
 struct AttnPlan {
-  int pre[kAttnMaxRows + 1], first[kAttnMaxRows], old[kAttnMaxRows];
+  int *pre, *first, *old;  // [B + 1], [B], [B]
 };
+__host__ __device__ constexpr int attn_plan_bytes(int B) { return (3 * B + 1) * 4; }
+__device__ __forceinline__ AttnPlan attn_plan_at(void* smem, int B) {
+  int* p = static_cast<int*>(smem);
+  return AttnPlan{p, p + B + 1, p + 2 * B + 1};
+}
 
 // A unit counts `p.open` tiles more than it has, for what a CTA spends on opening and closing it,
 // so that shares with many short units take no longer than others.
 // Built by warp 0 of every CTA (the caller synchronises); CTA 0 records errors.
-__device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, AttnPlan& plan) {
+__device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, const AttnPlan& plan) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -216,7 +221,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 void attn_tc_shape(int R, int* M, int* MT);
 int launch_attn_tc(const AttnParams& p, int rows, int grid, cudaStream_t stream);
 // The kernel for few rows (tree_attention_mma.cu).
-void attn_mma_shape(int R, int hd, int* M, int* MT, int* per_sm);
+void attn_mma_shape(int R, int hd, int* M, int* MT, int* tile, int* per_sm);
 int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, cudaStream_t stream);
 
 }  // namespace specdec

@@ -3,13 +3,13 @@
 //
 // With at most 16 rows (a token or a short chain with one or a few query heads per K/V head) a
 // K/V column of 512 bytes meets 16 * 512 flops: HBM bounds it, and tensor memory's 128-row tiles
-// would be nearly empty.  So a warp is the unit: it streams its own 16 columns of each 128-column
+// would be nearly empty.  So a warp is the unit: it streams its own 16 columns of each 64-column
 // tile by TMA (128-byte swizzle) into two private stages, without any CTA-wide barrier, and runs
 // both products with m16n8k16, transposed so that the columns (or the head's values) fill the 16
 // and the query rows the 8: S^T = K Q^T (Q in registers for the whole segment) and O^T += V^T P^T,
-// the weights turned by one movmatrix per 8 x 8.  Query rows as the 16 took twice the
-// instructions for 8 rows, and four warps left the SM's latencies uncovered.  Each warp keeps
-// maximum, sum and O of its columns; the eight are merged in shared memory when the segment ends,
+// the weights turned by one movmatrix per 8 x 8.  (Query rows as the 16 took twice the
+// instructions for 8 rows.)  Each warp keeps
+// maximum, sum and O of its columns; the CTA's are merged in shared memory when the segment ends,
 // while the next segment's tiles are already on their way.
 #include <cmath>
 
@@ -19,7 +19,7 @@
 namespace specdec {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kCols = 16;                // columns of a warp's slice of a tile
 constexpr int kTileCols = kCols * kWarps;
 constexpr int kStages = 2;
@@ -82,12 +82,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   using S = Smem<HD, NT>;
   constexpr int kSteps = HD / 16, kPanels = HD / 64, kRows = S::kRows;
   extern __shared__ char raw[];
-  __shared__ AttnPlan plan;
   __shared__ uint64_t s_full[kWarps][kStages];
   __shared__ int s_par[kMaxTree], s_flag, s_bad;
   __shared__ unsigned long long s_anc[kMaxTree];
   __shared__ float2 s_ml[kWarps][kRows];
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
+  const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, p.B);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, qd = lane & 3;
   if (warp == 0) attn_plan(p, kTileCols, plan);
   if (lane == 0) {
@@ -304,7 +304,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         ++loaded;
       }
     }
-    // ------------------------------------------------------------- the eight warps' parts
+    // ------------------------------------------------------------- the warps' parts
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -328,23 +328,24 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           merge[(warp * kRows + 8 * n + 2 * qd + (k & 1)) * S::kPitch + j * 16 + gr + (k >> 1) * 8] = o[n][j][k];
     }
     __syncthreads();
-    // 16 threads per row: every 16th group of 4 values from d0
-    const int r = tid >> 4, d0 = (tid & 15) * 4;
+    // kPer threads per row: every kPer-th group of 4 values from d0
+    constexpr int kPer = kThreads / kRows, kVecs = HD / 4 / kPer;
+    const int r = tid / kPer, d0 = tid % kPer * 4;
     const int rr = mt * kRows + r;
     const bool mine = r < nrows && !s_bad;
     const int t = mine ? rr / p.G : 0, h = seg.h * p.G + (mine ? rr % p.G : 0);
     const bool live = mine && s_anc[t] != 0;
     float mm = -INFINITY, ll = 0.f;
-    float4 acc[HD / 64];
+    float4 acc[kVecs];
 #pragma unroll
-    for (int j = 0; j < HD / 64; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < kVecs; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 ml, auto at) {  // one more part of the row
       const float mn = fmaxf(mm, ml.x), off = mn == -INFINITY ? 0.f : mn;
       const float fa = ex2(mm - off), fb = ex2(ml.x - off);
       ll = ll * fa + ml.y * fb;
       mm = mn;
 #pragma unroll
-      for (int j = 0; j < HD / 64; ++j) {
+      for (int j = 0; j < kVecs; ++j) {
         const float4 v = at(j);
         acc[j].x = acc[j].x * fa + v.x * fb;
         acc[j].y = acc[j].y * fa + v.y * fb;
@@ -356,15 +357,15 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
             add(s_ml[w][r], [&](int j) {
-          return *reinterpret_cast<const float4*>(merge + (w * kRows + r) * S::kPitch + d0 + j * 64);
+          return *reinterpret_cast<const float4*>(merge + (w * kRows + r) * S::kPitch + d0 + j * kPer * 4);
         });
     if (seg.tile0 > 0 || seg.tile1 < seg.tiles) {
       const long long at = static_cast<long long>(attn_slot(p, sh, g, mt, seg.unit0)) * kRows + r;
       if (mine) {
         if (d0 == 0) p.part_ml[at] = make_float2(mm, ll);
 #pragma unroll
-        for (int j = 0; j < HD / 64; ++j)
-          *reinterpret_cast<float4*>(p.part_o + at * HD + d0 + j * 64) = acc[j];
+        for (int j = 0; j < kVecs; ++j)
+          *reinterpret_cast<float4*>(p.part_o + at * HD + d0 + j * kPer * 4) = acc[j];
       }
       if (s_bad) continue;
       const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1);
@@ -372,21 +373,35 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       mm = -INFINITY;
       ll = 0.f;
 #pragma unroll
-      for (int j = 0; j < HD / 64; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (mine)
+      for (int j = 0; j < kVecs; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine) {
+        // the maximum first, so that the parts' loads depend on nothing and wait together
+        const auto at = [&](int gg) { return static_cast<long long>(attn_slot(p, sh, gg, mt, seg.unit0)) * kRows + r; };
+#pragma unroll 8
+        for (int gg = g0; gg <= g1; ++gg) mm = fmaxf(mm, __ldcg(&p.part_ml[at(gg)].x));
+        const float off = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
         for (int gg = g0; gg <= g1; ++gg) {
-          const long long a2 = static_cast<long long>(attn_slot(p, sh, gg, mt, seg.unit0)) * kRows + r;
-          add(__ldcg(p.part_ml + a2), [&](int j) {
-            return __ldcg(reinterpret_cast<const float4*>(p.part_o + a2 * HD + d0 + j * 64));
-          });
+          const float2 ml = __ldcg(p.part_ml + at(gg));
+          const float f = ex2(ml.x - off);
+          ll += ml.y * f;
+#pragma unroll
+          for (int j = 0; j < kVecs; ++j) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(gg) * HD + d0 + j * kPer * 4));
+            acc[j].x += v.x * f;
+            acc[j].y += v.y * f;
+            acc[j].z += v.z * f;
+            acc[j].w += v.w * f;
+          }
         }
+      }
     }
     if (!mine) continue;
     const float inv = live ? 1.f / ll : 0.f;
     char* y = p.out + seg.b * p.outr + t * p.outt + static_cast<long long>(h) * HD * 2;
 #pragma unroll
-    for (int j = 0; j < HD / 64; ++j)
-      *reinterpret_cast<uint2*>(y + (d0 + j * 64) * 2) =
+    for (int j = 0; j < kVecs; ++j)
+      *reinterpret_cast<uint2*>(y + (d0 + j * kPer * 4) * 2) =
           make_uint2(bf16_pack(acc[j].x * inv, acc[j].y * inv), bf16_pack(acc[j].z * inv, acc[j].w * inv));
     if (p.lse && d0 == 0)
       p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + h] =
@@ -404,18 +419,20 @@ template <int HD, int NT>
 int launch_mma(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {
   auto kernel = attn_mma_kernel<HD, NT>;
   constexpr int smem = Smem<HD, NT>::bytes;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<grid, kThreads, smem, stream>>>(p, map);
+  kernel<<<grid, kThreads, smem + attn_plan_bytes(p.B), stream>>>(p, map);
   return map_cuda_error(cudaGetLastError());
 }
 
 }  // namespace
 
-void attn_mma_shape(int R, int hd, int* M, int* MT, int* per_sm) {
+void attn_mma_shape(int R, int hd, int* M, int* MT, int* tile, int* per_sm) {
   *M = R <= 8 ? 8 : 16;
   *MT = (R + *M - 1) / *M;
-  *per_sm = hd == 64 && *M == 8 ? 2 : 1;  // by shared memory
+  *tile = kTileCols;
+  *per_sm = hd == 64 ? 4 : 2;  // by shared memory: one CTA opens or merges while another streams
 }
 
 int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, cudaStream_t stream) {

@@ -121,13 +121,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   using S = Smem<HD>;
   constexpr int kSteps = HD / 16, kPanels = HD / 64;
   extern __shared__ char raw[];
-  __shared__ AttnPlan plan;
   __shared__ Bars bar;
   __shared__ uint32_t s_tmem;
   __shared__ int s_par[kMaxTree], s_bad;
   __shared__ unsigned long long s_anc[kMaxTree], s_poison;
   __shared__ float2 s_ml[kRows];
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
+  const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, p.B);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   const int nrows = min(2 * kRows, p.T * p.G - mt * 2 * kRows);  // query rows of this pair
@@ -658,9 +658,10 @@ template <int HD>
 int launch_tc(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {
   auto kernel = attn_tc_kernel<HD>;
   constexpr int smem = Smem<HD>::bytes;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<grid, kThreads, smem, stream>>>(p, map);
+  kernel<<<grid, kThreads, smem + attn_plan_bytes(p.B), stream>>>(p, map);
   const cudaError_t e2 = cudaGetLastError();
   if (e2 != cudaSuccess || p.groups == 1) return map_cuda_error(e2);
   cudaLaunchConfig_t cfg = {};
