@@ -30,11 +30,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kUnroll = 4;  // 16-byte loads in flight per thread and row
+constexpr int kUnroll = 4;  // 16-byte loads in flight per thread
 
 struct TreeParams {
   const void *target, *draft_scores;
-  int T, V, D, C, replacement;
+  int T, V, D, C, replacement, vec;  // vec: rows are 16-byte aligned
   long long row_stride;
   float c2;  // log2(e) / temperature
   const int32_t *tokens, *parents;
@@ -89,101 +89,149 @@ __device__ void write_walk(const TreeParams& p, int b, const Walk& w, int a, int
   }
 }
 
-// Elements [lo, hi) of a row: fv(first index, values, VN) for whole 16-byte vectors and
-// fs(index, value) for the few elements around them.  Threads take consecutive vectors.
-template <typename T, typename FV, typename FS>
-__device__ __forceinline__ void scan_slice(const T* row, int lo, int hi, FV fv, FS fs) {
+// One 16-byte vector of a row: elements [v * VN, v * VN + VN), minus infinity behind V.  `vec`: rows
+// are 16-byte aligned.  Rows with another stride or start take single elements.
+template <typename T>
+__device__ __forceinline__ uint4 load_scores(const T* row, int v, int V, bool vec) {
   constexpr int VN = Vec<T>::N;
-  const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row + lo) % 16 / sizeof(T));
-  const int head = min(hi - lo, mis ? VN - mis : 0);
-  const int nv = (hi - lo - head) / VN;
-  const int tid = threadIdx.x;
-  if (tid < head) fs(lo + tid, Vec<T>::scalar(row + lo + tid));
-  const T* body = row + lo + head;
-  for (int v0 = 0; v0 < nv; v0 += kThreads * kUnroll) {
-    uint4 r[kUnroll];
+  if (vec && (v + 1) * VN <= V) return ldg_stream(row + static_cast<long long>(v) * VN);
+  uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int v = v0 + k * kThreads + tid;
-      if (v < nv) r[k] = ldg_stream(body + static_cast<long long>(v) * VN);
-    }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int v = v0 + k * kThreads + tid;
-      if (v < nv) {
-        float x[VN];
-        Vec<T>::unpack(r[k], x);
-        fv(lo + head + v * VN, x);
-      }
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      const int e = v * VN + k;
+      w[k] = e < V ? __float_as_uint(__ldg(reinterpret_cast<const float*>(row) + e)) : 0xFF800000u;
+    } else {
+      const int e = v * VN + 2 * k;
+      const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+      w[k] = (e < V ? __ldg(r + e) : 0xFF80u) | (e + 1 < V ? __ldg(r + e + 1) : 0xFF80u) << 16;
     }
   }
-  const int tail = lo + head + nv * VN + tid;
-  if (tail < hi) fs(tail, Vec<T>::scalar(row + tail));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ int slice_start(int V, int rank, int C) {
-  return static_cast<int>(static_cast<long long>(V) * rank / C);
+__device__ __forceinline__ int slice_start(int vecs, int rank, int C) {
+  return static_cast<int>(static_cast<long long>(vecs) * rank / C);
+}
+
+// The barriers of the exchanges.  Exchange n uses buffer n & 1; `bytes` arrive from the cluster.
+struct Exchange {
+  uint64_t bar[2];
+};
+constexpr uint32_t kExchangeTries = 1u << 22;
+
+__device__ __forceinline__ void exchange_expect(Exchange& x, int n, uint32_t bytes) {
+  if (threadIdx.x == 0) mbar_arrive_expect_tx(&x.bar[n & 1], bytes);
+}
+__device__ __forceinline__ bool exchange_wait(Exchange& x, int n) {
+  return mbar_wait_bounded(&x.bar[n & 1], (n >> 1) & 1, kExchangeTries);
 }
 
 // ------------------------------------------------------------------------------------- greedy
 
-template <typename T>
+// kAll: every row is read before the walk, a warp per row; else the walk's rows, one by one.
+template <typename T, bool kAll>
 __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams p) {
   constexpr int VN = Vec<T>::N;
   __shared__ Walk w;
+  __shared__ Exchange x;
   __shared__ unsigned long long s_warp[kWarps];
   __shared__ unsigned long long s_rec[2][kMaxCluster];
+  __shared__ unsigned long long s_all[kAll ? kMaxTree : 1][kMaxCluster];
+  __shared__ int s_choice[kMaxTree];
   const int rank = static_cast<int>(cluster_rank()), b = blockIdx.x / p.C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool ok = load_tree(p, b, w);
-  cluster_sync_all();  // every CTA of the cluster has started: its shared memory may be written
-  if (!ok) {
-    if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
-    return;
+  if (tid == 0) {
+    mbar_init(&x.bar[0], 1);
+    mbar_init(&x.bar[1], 1);
+    fence_mbar_init();
   }
-  const int lo = slice_start(p.V, rank, p.C), hi = slice_start(p.V, rank + 1, p.C);
-  int cur = 0, a = 0, token = -1, buf = 0;
-  while (w.par[0] != kUnusedNode) {
-    const T* row = static_cast<const T*>(p.target) +
-                   (static_cast<long long>(b) * p.T + cur) * p.row_stride;
+  const bool ok = load_tree(p, b, w);
+  const T* rows = static_cast<const T*>(p.target) + static_cast<long long>(b) * p.T * p.row_stride;
+  const int vecs = (p.V + VN - 1) / VN, v0 = slice_start(vecs, rank, p.C), v1 = slice_start(vecs, rank + 1, p.C);
+  // the best of a row's vectors [v0, v1), taken `step` apart from v0 + first by this thread
+  auto best = [&](const T* row, int first, int step) {
     float bv = 0.f;
     int bi = -1;
-    unsigned long long key = 0;
-    scan_slice(row, lo, hi,
-               [&](int e, const float* x) { take_vector<VN>(x, e, bv, bi); },
-               [&](int e, float x) { if (x == x) key = max(key, make_key(x, e)); });
-    if (bi >= 0) key = max(key, make_key(bv, bi));
+    for (int v = v0 + first; v < v1; v += step * kUnroll) {
+      uint4 r[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (v + k * step < v1) r[k] = load_scores(row, v + k * step, p.V, p.vec);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (v + k * step < v1) {
+          float f[VN];
+          Vec<T>::unpack(r[k], f);
+          take_vector<VN>(f, (v + k * step) * VN, bv, bi);
+        }
+    }
+    unsigned long long key = bi >= 0 && bi < p.V ? make_key(bv, bi) : 0ull;
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, k));
-    if (lane == 0) s_warp[warp] = key;
-    __syncthreads();
-    if (warp == 0) {
-      key = lane < kWarps ? s_warp[lane] : 0ull;
+    return key;
+  };
+  cluster_sync_all();  // every CTA of the cluster has started: its shared memory may be written
+  bool alive = true;
+  int a = 0, token = -1;
+  if (ok && w.par[0] != kUnusedNode) {
+    if (kAll) {
+      exchange_expect(x, 0, p.T * p.C * 8);
+      for (int i = warp; i < p.T; i += kWarps) {
+        const unsigned long long key = w.par[i] == kUnusedNode ? 0ull : best(rows + i * p.row_stride, lane, 32);
+        if (lane < p.C) cluster_send(cluster_map(&s_all[i][rank], lane), key, cluster_map(&x.bar[0], lane));
+      }
+      alive = exchange_wait(x, 0);
+      if (alive && tid < p.T) {
+        unsigned long long key = s_all[tid][0];
+        for (int r = 1; r < p.C; ++r) key = max(key, s_all[tid][r]);
+        s_choice[tid] = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
+      }
+      __syncthreads();
+    }
+    for (int cur = 0, n = 0; alive; ++n) {
+      int choice;
+      if (kAll) {
+        choice = s_choice[cur];
+      } else {
+        exchange_expect(x, n, p.C * 8);
+        unsigned long long key = best(rows + cur * p.row_stride, tid, kThreads);
+        if (lane == 0) s_warp[warp] = key;
+        __syncthreads();
+        if (warp == 0) {
+          key = lane < kWarps ? s_warp[lane] : 0ull;
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, k));
-      if (lane < p.C) cluster_st_u64(cluster_map(&s_rec[buf][rank], lane), key);
+          for (int k = 16; k > 0; k >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, k));
+          if (lane < p.C)
+            cluster_send(cluster_map(&s_rec[n & 1][rank], lane), key, cluster_map(&x.bar[n & 1], lane));
+        }
+        if (!(alive = exchange_wait(x, n))) break;
+        key = s_rec[n & 1][0];
+        for (int r = 1; r < p.C; ++r) key = max(key, s_rec[n & 1][r]);
+        choice = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
+      }
+      if (choice < 0) {  // only NaN
+        if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
+        break;
+      }
+      const int next = a < p.D ? next_child(w, p.T, cur, cur, [&](int i) { return w.tok[i] == choice; })
+                               : p.T;
+      if (next == p.T) {
+        token = choice;
+        break;
+      }
+      if (tid == 0) w.path[a] = next;
+      ++a;
+      cur = next;
     }
-    cluster_sync_all();
-    key = s_rec[buf][0];
-    for (int r = 1; r < p.C; ++r) key = max(key, s_rec[buf][r]);
-    buf ^= 1;
-    if (key == 0) {  // only NaN
-      if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
-      break;
-    }
-    const int choice = static_cast<int>(~static_cast<uint32_t>(key));
-    const int next = a < p.D ? next_child(w, p.T, cur, cur, [&](int i) { return w.tok[i] == choice; })
-                             : p.T;
-    if (next == p.T) {
-      token = choice;
-      break;
-    }
-    if (tid == 0) w.path[a] = next;
-    ++a;
-    cur = next;
   }
   __syncthreads();
-  if (rank == 0) write_walk(p, b, w, a, token);
+  if (!ok || !alive) {
+    if (rank == 0 && tid == 0) set_status(p.status, ok ? SPECDEC_ERR_TIMEOUT : SPECDEC_ERR_INPUT_RANGE);
+  } else if (rank == 0) {
+    write_walk(p, b, w, a, token);
+  }
+  cluster_sync_all();  // no CTA leaves while another might still write to it
 }
 
 // ------------------------------------------------------------------------------------ sampled
@@ -216,30 +264,24 @@ __device__ __forceinline__ void probabilities(const Stage& s, float c2, int repl
   }
 }
 
-struct Record {
-  float a, b, c, d;
-};
-
-// Sum of (x, y) over the CTA, in every thread of warp 0.
-__device__ __forceinline__ float2 block_sum(float2 v, float2* s_warp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The same of a vector's elements e0 .. e0 + N - 1 (a stage's numbers are read once for all).
+template <int N>
+__device__ __forceinline__ void probabilities(const Stage& s, float c2, int replacement, int e0,
+                                              const float* zt, const float* zq, float* pv, float* qv) {
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, k);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, k);
+  for (int k = 0; k < N; ++k) {
+    pv[k] = ex2(fmaf(zt[k], c2, -s.mt)) * s.it;
+    qv[k] = ex2(fmaf(zq[k], c2, -s.mq)) * s.iq;
   }
-  if (lane == 0) s_warp[warp] = v;
-  __syncthreads();
-  v = make_float2(0.f, 0.f);
-  if (warp == 0) {
-    if (lane < kWarps) v = s_warp[lane];
+  for (int i = 0; i < s.k; ++i) {
+    const float ir = s.ir[i], iqs = s.iqs[i];
+    const int at = s.tok[i] - e0;
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, k);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, k);
+    for (int k = 0; k < N; ++k) {
+      if (ir > 0.f) pv[k] = fmaxf(pv[k] - qv[k], 0.f) * ir;
+      if (!replacement) qv[k] = at == k ? 0.f : qv[k] * iqs;
     }
   }
-  return v;
 }
 
 // (m, l): maximum of x * c2 and the sum of 2^(x * c2 - m).
@@ -250,6 +292,20 @@ __device__ __forceinline__ MaxSum merged(MaxSum a, MaxSum b) {
   const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY) return MaxSum{m, a.l + b.l};  // nothing yet (or NaN, which has to stay)
   return MaxSum{m, a.l * ex2(a.m - m) + b.l * ex2(b.m - m)};
+}
+__device__ __forceinline__ MaxSum warp_merged(MaxSum s) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1)
+    s = merged(s, MaxSum{__shfl_xor_sync(0xffffffffu, s.m, k),
+                         __shfl_xor_sync(0xffffffffu, s.l, k)});
+  return s;
+}
+template <int N> __device__ __forceinline__ float tree_sum(float* t) {
+#pragma unroll
+  for (int h = N / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int k = 0; k < h; ++k) t[k] += t[k + h];
+  return t[0];
 }
 template <int N> __device__ __forceinline__ void fold(MaxSum& s, const float* x, float c2) {
   float mx = x[0];
@@ -265,64 +321,41 @@ template <int N> __device__ __forceinline__ void fold(MaxSum& s, const float* x,
   float t[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) t[k] = ex2(fmaf(x[k], c2, -off));
-#pragma unroll
-  for (int h = N / 2; h > 0; h >>= 1)
-#pragma unroll
-    for (int k = 0; k < h; ++k) t[k] += t[k + h];
-  s.l += t[0];
+  s.l += tree_sum<N>(t);
 }
-template <typename T>
-__device__ __forceinline__ MaxSum slice_max_sum(const T* row, int lo, int hi, float c2,
-                                                MaxSum* s_warp) {
-  constexpr int VN = Vec<T>::N;
-  MaxSum s{-INFINITY, 0.f};
-  scan_slice(row, lo, hi, [&](int, const float* x) { fold<VN>(s, x, c2); },
-             [&](int, float x) { fold<1>(s, &x, c2); });
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ float2 warp_sum(float2 v) {
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1)
-    s = merged(s, MaxSum{__shfl_xor_sync(0xffffffffu, s.m, k),
-                         __shfl_xor_sync(0xffffffffu, s.l, k)});
-  if (lane == 0) s_warp[warp] = s;
-  __syncthreads();
-  s = MaxSum{-INFINITY, 0.f};
-  if (warp == 0) {
-    if (lane < kWarps) s = s_warp[lane];
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1)
-      s = merged(s, MaxSum{__shfl_xor_sync(0xffffffffu, s.m, k),
-                           __shfl_xor_sync(0xffffffffu, s.l, k)});
+  for (int k = 16; k > 0; k >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, k);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, k);
   }
-  return s;
+  return v;
 }
 
-// Warp 0 writes this CTA's record into every CTA of the cluster.
-__device__ __forceinline__ void send(Record* slot, int C, Record r) {
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32 && lane < C) {
-    const uint32_t a = cluster_map(slot, lane);
-    cluster_st_f32(a, r.a);
-    cluster_st_f32(a + 4, r.b);
-    cluster_st_f32(a + 8, r.c);
-    cluster_st_f32(a + 12, r.d);
-  }
-}
+constexpr int kHold = 10;      // vectors of each row a thread holds
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) tree_sample_kernel(const TreeParams p) {
+// kKeep: a thread's vectors of both rows stay in its registers while a node is worked on (loaded
+// once; every test and the draw go over registers); else each pass loads them again, from L2.
+template <typename T, bool kKeep>
+__global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreeParams p) {
   constexpr int VN = Vec<T>::N;
   __shared__ Walk w;
   __shared__ Stage st;
+  __shared__ Exchange x;
   __shared__ float s_u[kMaxTree], s_zt[kMaxTree], s_zq[kMaxTree];
-  __shared__ MaxSum s_ms[2][kWarps];
-  __shared__ float2 s_sum[kWarps];
-  __shared__ Record s_rec[2][kMaxCluster];
+  __shared__ float4 s_warp[kWarps], s_rec[2][kMaxCluster];
   __shared__ float s_mass[kMaxCluster];  // each CTA's share of p's mass, not normalised
+  __shared__ float s_entry[kHold * kWarps];
   __shared__ int s_token;
   const int rank = static_cast<int>(cluster_rank()), b = blockIdx.x / p.C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* target = static_cast<const T*>(p.target) + static_cast<long long>(b) * p.T * p.row_stride;
   const T* drafts = static_cast<const T*>(p.draft_scores) + static_cast<long long>(b) * p.T * p.row_stride;
+  if (tid == 0) {
+    mbar_init(&x.bar[0], 1);
+    mbar_init(&x.bar[1], 1);
+    fence_mbar_init();
+  }
   bool ok = load_tree(p, b, w);
   // every child's scores at its parent, fetched once (the tests need no exchange of them)
   bool bad_u = false;
@@ -337,29 +370,81 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(const TreeParams 
   }
   ok &= !__syncthreads_or(bad_u);
   cluster_sync_all();  // every CTA of the cluster has started: its shared memory may be written
-  if (!ok) {
-    if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
-    return;
-  }
-  const int lo = slice_start(p.V, rank, p.C), hi = slice_start(p.V, rank + 1, p.C);
-  int cur = 0, a = 0, token = -1, buf = 0;
-  const bool walking = w.par[0] != kUnusedNode;
-  bool draw = walking;
+  const int vecs = (p.V + VN - 1) / VN, v0 = slice_start(vecs, rank, p.C), v1 = slice_start(vecs, rank + 1, p.C);
+  const bool walking = ok && w.par[0] != kUnusedNode;
+  bool draw = walking, alive = true;
+  int cur = 0, a = 0, n = 0, token = -1;
+  uint4 ht[kHold], hq[kHold];
+  const T *zt = target, *zq = drafts;
+  bool inner = false;
+  auto load = [&](int first) {  // kHold runs of kThreads vectors from `first`
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      const int v = first + k * kThreads + tid;
+      if (v < v1) ht[k] = load_scores(zt, v, p.V, p.vec);
+    }
+    if (inner)
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {
+        const int v = first + k * kThreads + tid;
+        if (v < v1) hq[k] = load_scores(zq, v, p.V, p.vec);
+      }
+  };
+  // f(v, target's values, draft's) over this thread's vectors
+  auto over = [&](auto f) {
+    for (int first = v0; first < v1; first += kHold * kThreads) {
+      if (!kKeep) load(first);
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {
+        const int v = first + k * kThreads + tid;
+        if (v < v1) {
+          float t[VN], q[VN];
+          Vec<T>::unpack(ht[k], t);
+          Vec<T>::unpack(hq[k], q);
+          f(v, t, q);
+        }
+      }
+      if (kKeep) break;
+    }
+  };
+  // this CTA's record (in warp 0) to every CTA, and theirs
+  auto exchange = [&](float4 r) {
+    if (warp == 0 && lane < p.C)
+      cluster_send4(cluster_map(&s_rec[n & 1][rank], lane), r, cluster_map(&x.bar[n & 1], lane));
+    alive = __syncthreads_and(exchange_wait(x, n) ? 1 : 0) != 0;
+    ++n;
+    return s_rec[(n - 1) & 1];
+  };
   while (walking) {
-    const T* zt = target + cur * p.row_stride;
-    const T* zq = drafts + cur * p.row_stride;
+    zt = target + cur * p.row_stride;
+    zq = drafts + cur * p.row_stride;
     int child = a < p.D ? next_child(w, p.T, cur, cur, [](int) { return true; }) : p.T;
-    const bool inner = child < p.T;
-    MaxSum t = slice_max_sum(zt, lo, hi, p.c2, s_ms[0]);
-    MaxSum q{0.f, 1.f};
-    if (inner) q = slice_max_sum(zq, lo, hi, p.c2, s_ms[1]);
-    send(&s_rec[buf][rank], p.C, Record{t.m, t.l, q.m, q.l});
-    cluster_sync_all();
+    inner = child < p.T;
+    exchange_expect(x, n, p.C * 16);
+    if (kKeep) load(v0);
+    MaxSum t{-INFINITY, 0.f}, q{-INFINITY, 0.f};
+    over([&](int, const float* ft, const float* fq) {
+      fold<VN>(t, ft, p.c2);
+      if (inner) fold<VN>(q, fq, p.c2);
+    });
+    t = warp_merged(t);
+    if (inner) q = warp_merged(q);
+    if (lane == 0) s_warp[warp] = make_float4(t.m, t.l, q.m, q.l);
+    __syncthreads();
+    float4 mine = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (warp == 0) {
+      if (lane < kWarps) mine = s_warp[lane];
+      t = warp_merged(MaxSum{mine.x, mine.y});
+      if (inner) q = warp_merged(MaxSum{mine.z, mine.w});
+      mine = make_float4(t.m, t.l, q.m, q.l);
+    }
+    const float4* rec = exchange(mine);
+    if (!alive) break;
     MaxSum tt{-INFINITY, 0.f}, qq{-INFINITY, 0.f};
     for (int r = 0; r < p.C; ++r) {
-      const Record x = s_rec[buf][r];
-      tt = merged(tt, MaxSum{x.a, x.b});
-      qq = merged(qq, MaxSum{x.c, x.d});
+      const float4 y = rec[r];
+      tt = merged(tt, MaxSum{y.x, y.y});
+      if (inner) qq = merged(qq, MaxSum{y.z, y.w});
     }
     if (!(tt.l > 0.f && tt.l < INFINITY && tt.m < INFINITY) ||
         (inner && !(qq.l > 0.f && qq.l < INFINITY && qq.m < INFINITY))) {
@@ -370,55 +455,57 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(const TreeParams 
     if (tid == 0) {
       st.mt = tt.m;
       st.it = 1.f / tt.l;
-      st.mq = qq.m;
+      st.mq = inner ? qq.m : 0.f;
       st.iq = inner ? 1.f / qq.l : 0.f;
       st.k = 0;
     }
-    if (tid < p.C) {
-      const Record x = s_rec[buf][tid];
-      s_mass[tid] = x.a == -INFINITY ? 0.f : x.b * ex2(x.a - tt.m);
-    }
-    buf ^= 1;
+    if (tid < p.C) s_mass[tid] = rec[tid].x == -INFINITY ? 0.f : rec[tid].y * ex2(rec[tid].x - tt.m);
     __syncthreads();
     bool accepted = false;
     while (child < p.T) {
-      const int x = w.tok[child];
-      if (x < 0 || x >= p.V) {
+      const int c = w.tok[child];
+      if (c < 0 || c >= p.V) {
         if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
       } else {
-        float pv, qv;
-        probabilities(st, p.c2, p.replacement, x, s_zt[child], s_zq[child], pv, qv);
-        if (s_u[child] * qv < pv) {
+        float pc, qc;
+        probabilities(st, p.c2, p.replacement, c, s_zt[child], s_zq[child], pc, qc);
+        if (s_u[child] * qc < pc) {
           accepted = true;
           break;
         }
         // rejected: the residual's mass and what is left of q
+        exchange_expect(x, n, p.C * 16);
         float2 sum = make_float2(0.f, 0.f);
-        auto one = [&](int e, float z1, float z2) {
-          float pe, qe;
-          probabilities(st, p.c2, p.replacement, e, z1, z2, pe, qe);
-          sum.x += fmaxf(pe - qe, 0.f);
-          sum.y += e == x ? 0.f : qe;
-        };
-        // the draft row may be aligned otherwise than the target's: read element by element there
-        scan_slice(zt, lo, hi,
-                   [&](int e, const float* v) {
+        over([&](int v, const float* ft, const float* fq) {
+          float pe[VN], qe[VN];
+          probabilities<VN>(st, p.c2, p.replacement, v * VN, ft, fq, pe, qe);
 #pragma unroll
-                     for (int k = 0; k < VN; ++k) one(e + k, v[k], Vec<T>::scalar(zq + e + k));
-                   },
-                   [&](int e, float v) { one(e, v, Vec<T>::scalar(zq + e)); });
-        sum = block_sum(sum, s_sum);
-        send(&s_rec[buf][rank], p.C, Record{sum.x, sum.y, 0.f, 0.f});
-        cluster_sync_all();
+          for (int k = 0; k < VN; ++k) {
+            pe[k] = fmaxf(pe[k] - qe[k], 0.f);
+            if (v * VN + k == c) qe[k] = 0.f;
+          }
+          sum.x += tree_sum<VN>(pe);
+          sum.y += tree_sum<VN>(qe);
+        });
+        sum = warp_sum(sum);
+        if (lane == 0) s_warp[warp] = make_float4(sum.x, sum.y, 0.f, 0.f);
+        __syncthreads();
+        float4 r4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (warp == 0) {
+          if (lane < kWarps) r4 = s_warp[lane];
+          sum = warp_sum(make_float2(r4.x, r4.y));
+          r4 = make_float4(sum.x, sum.y, 0.f, 0.f);
+        }
+        rec = exchange(r4);
+        if (!alive) break;
         float R = 0.f, Q = 0.f;
         for (int r = 0; r < p.C; ++r) {
-          R += s_rec[buf][r].a;
-          Q += s_rec[buf][r].b;
+          R += rec[r].x;
+          Q += rec[r].y;
         }
-        if (tid < p.C && R > 0.f) s_mass[tid] = s_rec[buf][tid].a;
-        buf ^= 1;
+        if (tid < p.C && R > 0.f) s_mass[tid] = rec[tid].x;
         if (tid == 0) {
-          st.tok[st.k] = x;
+          st.tok[st.k] = c;
           st.ir[st.k] = R > 0.f ? 1.f / R : 0.f;
           st.iqs[st.k] = Q > 0.f ? 1.f / Q : 0.f;
           ++st.k;
@@ -427,101 +514,158 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(const TreeParams 
       }
       child = next_child(w, p.T, cur, child, [](int) { return true; });
     }
-    if (!accepted) break;
+    if (!alive || !accepted) break;
     if (tid == 0) w.path[a] = child;
     ++a;
     cur = child;
     __syncthreads();  // the stage is rewritten for the next node
   }
   // The draw: the CTA whose slice holds u * total finds the token (rank order, so ascending).
-  if (draw) {
+  if (!ok || !alive) {
+    if (rank == 0 && tid == 0) set_status(p.status, ok ? SPECDEC_ERR_TIMEOUT : SPECDEC_ERR_INPUT_RANGE);
+  } else if (draw) {
     // Every thread finds the same owner; the last CTA with any mass takes what rounding leaves.
-    float total = 0.f, before = 0.f, run0 = 0.f;
+    float total = 0.f, before = 0.f, run = 0.f;
     for (int r = 0; r < p.C; ++r) total += s_mass[r];
     int owner = -1, last = 0;
     for (int r = 0; r < p.C; ++r) {
       const float m = s_mass[r];
       if (m > 0.f) {
-        if (owner < 0) before = run0;
-        if (owner < 0 && run0 + m > s_u[0] * total) owner = r;
+        if (owner < 0) before = run;
+        if (owner < 0 && run + m > s_u[0] * total) owner = r;
         last = r;
       }
-      run0 += m;
+      run += m;
     }
     if (owner < 0) owner = last;
     if (rank == owner) {
-      const float goal = s_u[0];           // probabilities() are masses over the total
-      const T* zt = target + cur * p.row_stride;
-      const T* zq = drafts + cur * p.row_stride;
-      const bool inner = st.iq > 0.f;
-      auto mass = [&](int e) {
-        float pe, qe;
-        probabilities(st, p.c2, p.replacement, e, Vec<T>::scalar(zt + e),
-                      inner ? Vec<T>::scalar(zq + e) : 0.f, pe, qe);
-        return pe;
-      };
-      // warps take consecutive chunks
-      const int n = hi - lo, c0 = lo + static_cast<int>(static_cast<long long>(n) * warp / kWarps),
-                c1 = lo + static_cast<int>(static_cast<long long>(n) * (warp + 1) / kWarps);
-      float s = 0.f;
-      for (int e = c0 + lane; e < c1; e += 32) s += mass(e);
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-      if (lane == 0) s_sum[warp] = make_float2(s, 0.f);
-      if (tid == 0) s_token = -1;
-      __syncthreads();
+      const float goal = s_u[0];  // probabilities() are masses over the total
+      // Masses of 32 consecutive vectors (a warp's in one run), kHold runs at a time; the entry
+      // where the running sum passes the goal, then the vector in it, then the element.
       float run = before / total;
-      int pick = -1, end = -1;
-      float start = 0.f;
-      for (int k = 0; k < kWarps; ++k) {
-        const float v = s_sum[k].x;
-        if (v > 0.f) {
-          end = k;
-          if (pick < 0 && run + v > goal) {
-            pick = k;
-            start = run;
-          }
-          if (pick < 0) start = run;
-        }
-        run += v;
-      }
-      if (pick < 0) pick = end;
-      if (warp == pick) {
-        int found = -1, some = -1;
-        float at = start;
-        for (int e0 = c0; e0 < c1 && found < 0; e0 += 32) {
-          const int e = e0 + lane;
-          const float v = e < c1 ? mass(e) : 0.f;
-          float inc = v;
+      int pick = -1, last_v = -1;  // first vector of the chosen entry, of the last with any mass
+      float start = 0.f, last_start = 0.f;
+      for (int first = v0; first < v1 && pick < 0; first += kHold * kThreads) {
+        if (!kKeep) load(first);
 #pragma unroll
-          for (int k = 1; k < 32; k <<= 1) {
-            const float o = __shfl_up_sync(0xffffffffu, inc, k);
-            if (lane >= k) inc += o;
+        for (int k = 0; k < kHold; ++k) {
+          const int v = first + k * kThreads + tid;
+          float m = 0.f;
+          if (v < v1) {
+            float ft[VN], fq[VN], pe[VN], qe[VN];
+            Vec<T>::unpack(ht[k], ft);
+            Vec<T>::unpack(hq[k], fq);
+            probabilities<VN>(st, p.c2, p.replacement, v * VN, ft, fq, pe, qe);
+            m = tree_sum<VN>(pe);
           }
-          const unsigned over = __ballot_sync(0xffffffffu, v > 0.f && at + inc > goal);
-          const unsigned pos = __ballot_sync(0xffffffffu, v > 0.f);
-          if (over) found = e0 + __ffs(over) - 1;
-          if (pos) some = e0 + 31 - __clz(pos);
-          at += __shfl_sync(0xffffffffu, inc, 31);
+          m = warp_sum(make_float2(m, 0.f)).x;
+          if (lane == 0) s_entry[k * kWarps + warp] = m;
         }
-        if (lane == 0) s_token = found >= 0 ? found : some;
+        __syncthreads();
+        constexpr int kEach = kHold * kWarps / 32;  // entries per lane; every warp finds the same
+        float e[kEach], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) sum += e[i] = s_entry[lane * kEach + i];
+        float inc = sum;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const float o = __shfl_up_sync(0xffffffffu, inc, k);
+          if (lane >= k) inc += o;
+        }
+        float at = run + inc - sum;  // before this lane's entries
+        int mine = -1, some = -1;
+        float mine_at = 0.f, some_at = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          if (e[i] > 0.f) {
+            some = i;
+            some_at = at;
+            if (mine < 0 && at + e[i] > goal) {
+              mine = i;
+              mine_at = at;
+            }
+          }
+          at += e[i];
+        }
+        auto vector_of = [&](int l, int i) {
+          const int entry = l * kEach + i;
+          return first + entry / kWarps * kThreads + entry % kWarps * 32;
+        };
+        const unsigned over = __ballot_sync(0xffffffffu, mine >= 0), any = __ballot_sync(0xffffffffu, some >= 0);
+        if (over) {
+          const int l = __ffs(over) - 1;
+          pick = vector_of(l, __shfl_sync(0xffffffffu, mine, l));
+          start = __shfl_sync(0xffffffffu, mine_at, l);
+        } else if (any) {
+          const int l = 31 - __clz(any);
+          last_v = vector_of(l, __shfl_sync(0xffffffffu, some, l));
+          last_start = __shfl_sync(0xffffffffu, some_at, l);
+        }
+        run += __shfl_sync(0xffffffffu, inc, 31);
+        __syncthreads();
+      }
+      if (pick < 0) {
+        pick = last_v;
+        start = last_start;
+      }
+      if (warp == 0) {
+        const int v = pick + lane;
+        float pe[VN], m = 0.f;
+#pragma unroll
+        for (int k = 0; k < VN; ++k) pe[k] = 0.f;
+        if (v < v1) {
+          float ft[VN], fq[VN], qe[VN], sum[VN];
+          Vec<T>::unpack(load_scores(zt, v, p.V, p.vec), ft);
+          if (inner) Vec<T>::unpack(load_scores(zq, v, p.V, p.vec), fq);
+          else Vec<T>::unpack(make_uint4(0, 0, 0, 0), fq);
+          probabilities<VN>(st, p.c2, p.replacement, v * VN, ft, fq, pe, qe);
+#pragma unroll
+          for (int k = 0; k < VN; ++k) sum[k] = pe[k];
+          m = tree_sum<VN>(sum);
+        }
+        float inc = m;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const float o = __shfl_up_sync(0xffffffffu, inc, k);
+          if (lane >= k) inc += o;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, m > 0.f && start + inc > goal),
+                       any = __ballot_sync(0xffffffffu, m > 0.f);
+        if (lane == (over ? __ffs(over) - 1 : 31 - __clz(any))) {
+          float at = start + inc - m;
+          int found = -1, some = 0;
+#pragma unroll
+          for (int k = 0; k < VN; ++k)
+            if (pe[k] > 0.f) {
+              at += pe[k];
+              some = k;
+              if (found < 0 && at > goal) found = k;
+            }
+          s_token = v * VN + (found >= 0 ? found : some);
+        }
       }
       __syncthreads();
       token = s_token;
       write_walk(p, b, w, a, token);
     }
-  } else {
+  } else if (rank == 0) {
     __syncthreads();
-    if (rank == 0) write_walk(p, b, w, a, -1);
+    write_walk(p, b, w, a, -1);
   }
+  cluster_sync_all();  // no CTA leaves while another might still write to it
+}
+
+// Clusters that read their rows' slices with a few vectors per thread, all rows' clusters at once if
+// they fit.  Returns the CTAs per cluster.
+template <typename K>
+int tree_cluster(K kernel, int B, int V, int es, int* cache) {
+  const long long vecs = static_cast<long long>(V) * es / 16;
+  const int most = static_cast<int>(std::min<long long>(kMaxCluster, vecs / kThreads + 1));
+  return cluster_for_one_wave(reinterpret_cast<const void*>(kernel), B, 1, most, kThreads, 0, cache);
 }
 
 template <typename K>
-int launch_tree(K kernel, TreeParams& p, int B, int es, int* cache, cudaStream_t s) {
-  // CTAs that each have a few vectors per thread to read, and all rows' clusters at once if they fit
-  const long long vecs = static_cast<long long>(p.V) * es / 16;
-  const int most = static_cast<int>(std::min<long long>(kMaxCluster, vecs / kThreads + 1));
-  p.C = cluster_for_one_wave(reinterpret_cast<const void*>(kernel), B, 1, most, kThreads, 0, cache);
+int launch_tree(K kernel, const TreeParams& p, int B, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -541,6 +685,29 @@ int launch_tree(K kernel, TreeParams& p, int B, int es, int* cache, cudaStream_t
   return map_cuda_error(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
+template <typename T>
+int launch_greedy(TreeParams& p, int B, cudaStream_t s) {
+  static int caches[2][64 * 17];
+  // All rows at once where a CTA's share of them takes it less time than the steps of a walk do:
+  // about 2 us a step against 25 KB a us and CTA, and 30 MB in all.
+  p.C = tree_cluster(tree_greedy_kernel<T, true>, B, p.V, sizeof(T), caches[0]);
+  const long long bytes = static_cast<long long>(p.T) * p.V * sizeof(T);
+  if (bytes / p.C <= (128 << 10) && bytes * B <= (30 << 20))
+    return launch_tree(tree_greedy_kernel<T, true>, p, B, s);
+  p.C = tree_cluster(tree_greedy_kernel<T, false>, B, p.V, sizeof(T), caches[1]);
+  return launch_tree(tree_greedy_kernel<T, false>, p, B, s);
+}
+
+template <typename T>
+int launch_sample(TreeParams& p, int B, cudaStream_t s) {
+  static int caches[2][64 * 17];
+  p.C = tree_cluster(tree_sample_kernel<T, true>, B, p.V, sizeof(T), caches[0]);
+  const int vecs = (p.V + Vec<T>::N - 1) / Vec<T>::N;
+  if ((vecs + p.C - 1) / p.C <= kHold * kThreads) return launch_tree(tree_sample_kernel<T, true>, p, B, s);
+  p.C = tree_cluster(tree_sample_kernel<T, false>, B, p.V, sizeof(T), caches[1]);
+  return launch_tree(tree_sample_kernel<T, false>, p, B, s);
+}
+
 int check_tree(const void* logits, int dtype, int B, int T, int V, long long row_stride,
                const int32_t* tokens, int D, const int32_t* accept_len, const int32_t* out_token,
                const int32_t* path, const int32_t* draft, const int32_t* status) {
@@ -555,8 +722,6 @@ int check_tree(const void* logits, int dtype, int B, int T, int V, long long row
   if (B > (1 << 20) || row_stride > (1LL << 40) / es / T / B) return SPECDEC_ERR_UNSUPPORTED;
   return SPECDEC_OK;
 }
-
-int g_active_greedy[2][64 * 17], g_active_sample[2][64 * 17];
 
 }  // namespace
 }  // namespace specdec
@@ -584,9 +749,9 @@ extern "C" int specdec_verify_tree_greedy(const void* logits, int dtype, int B, 
   p.draft = draft;
   p.status = dev_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == SPECDEC_BF16)
-    return launch_tree(tree_greedy_kernel<uint16_t>, p, B, 2, g_active_greedy[0], s);
-  return launch_tree(tree_greedy_kernel<float>, p, B, 4, g_active_greedy[1], s);
+  const long long es = elem_size(dtype);
+  p.vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && row_stride * es % 16 == 0;
+  return dtype == SPECDEC_BF16 ? launch_greedy<uint16_t>(p, B, s) : launch_greedy<float>(p, B, s);
 }
 
 extern "C" int specdec_verify_tree_sample(const void* target_logits, const void* draft_logits,
@@ -622,7 +787,8 @@ extern "C" int specdec_verify_tree_sample(const void* target_logits, const void*
   p.draft = draft;
   p.status = dev_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == SPECDEC_BF16)
-    return launch_tree(tree_sample_kernel<uint16_t>, p, B, 2, g_active_sample[0], s);
-  return launch_tree(tree_sample_kernel<float>, p, B, 4, g_active_sample[1], s);
+  const long long es = elem_size(dtype);
+  p.vec = reinterpret_cast<uintptr_t>(target_logits) % 16 == 0 &&
+          reinterpret_cast<uintptr_t>(draft_logits) % 16 == 0 && row_stride * es % 16 == 0;
+  return dtype == SPECDEC_BF16 ? launch_sample<uint16_t>(p, B, s) : launch_sample<float>(p, B, s);
 }
