@@ -203,19 +203,6 @@ __device__ __forceinline__ int attn_slot(const AttnParams& p, const AttnShares& 
   return 2 * (g * p.MT + mt) + (sh.start(g) >= unit0 ? 0 : 1);
 }
 
-// 16-byte asynchronous copy global -> shared; zero-fills where `take` is false.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-               ::"r"(smem_addr(dst)), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // The tensor-core kernel (tree_attention_tc.cu): rows per M-tile and M-tiles for R query rows per
 // K/V head, and its launch (rows: of the cache).
 void attn_tc_shape(int R, int* M, int* MT);

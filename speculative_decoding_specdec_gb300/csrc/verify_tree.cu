@@ -332,12 +332,14 @@ __device__ __forceinline__ float2 warp_sum(float2 v) {
   return v;
 }
 
-constexpr int kHold = 10;      // vectors of each row a thread holds
+constexpr int kRuns = 6;                      // runs of kThreads vectors that are held of a row
+constexpr int kHold = kRuns * kThreads;       // 48 KB of each row: two CTAs per SM
 
-// kKeep: a thread's vectors of both rows stay in its registers while a node is worked on (loaded
-// once; every test and the draw go over registers); else each pass loads them again, from L2.
+// kKeep: the slices of both rows stay in shared memory while a node is worked on (loaded once, all
+// at once; every test and the draw go over them); else each pass loads them again, from L2.
+// (In registers they took a code so long that fetching it was most of a small batch's time.)
 template <typename T, bool kKeep>
-__global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreeParams p) {
   constexpr int VN = Vec<T>::N;
   __shared__ Walk w;
   __shared__ Stage st;
@@ -345,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreePara
   __shared__ float s_u[kMaxTree], s_zt[kMaxTree], s_zq[kMaxTree];
   __shared__ float4 s_warp[kWarps], s_rec[2][kMaxCluster];
   __shared__ float s_mass[kMaxCluster];  // each CTA's share of p's mass, not normalised
-  __shared__ float s_entry[kHold * kWarps];
+  __shared__ float s_entry[kRuns * kWarps];
+  extern __shared__ uint4 hold[];  // kKeep: [2][kHold]
   __shared__ int s_token;
   const int rank = static_cast<int>(cluster_rank()), b = blockIdx.x / p.C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -374,37 +377,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreePara
   const bool walking = ok && w.par[0] != kUnusedNode;
   bool draw = walking, alive = true;
   int cur = 0, a = 0, n = 0, token = -1;
-  uint4 ht[kHold], hq[kHold];
   const T *zt = target, *zq = drafts;
   bool inner = false;
-  auto load = [&](int first) {  // kHold runs of kThreads vectors from `first`
-#pragma unroll
-    for (int k = 0; k < kHold; ++k) {
-      const int v = first + k * kThreads + tid;
-      if (v < v1) ht[k] = load_scores(zt, v, p.V, p.vec);
-    }
-    if (inner)
-#pragma unroll
-      for (int k = 0; k < kHold; ++k) {
-        const int v = first + k * kThreads + tid;
-        if (v < v1) hq[k] = load_scores(zq, v, p.V, p.vec);
+  auto load = [&] {  // a thread copies what it will read
+    for (int v = v0 + tid; v < v1; v += kThreads) {
+      const int i = v - v0;
+      if (p.vec && (v + 1) * VN <= p.V) {
+        cp_async16(hold + i, zt + static_cast<long long>(v) * VN, true);
+        if (inner) cp_async16(hold + kHold + i, zq + static_cast<long long>(v) * VN, true);
+      } else {
+        hold[i] = load_scores(zt, v, p.V, p.vec);
+        if (inner) hold[kHold + i] = load_scores(zq, v, p.V, p.vec);
       }
+    }
+    cp_async_wait_all();
+  };
+  auto get = [&](int v, float* t, float* q) {  // a vector's scores in both rows
+    Vec<T>::unpack(kKeep ? hold[v - v0] : load_scores(zt, v, p.V, p.vec), t);
+    if (inner) Vec<T>::unpack(kKeep ? hold[kHold + v - v0] : load_scores(zq, v, p.V, p.vec), q);
   };
   // f(v, target's values, draft's) over this thread's vectors
   auto over = [&](auto f) {
-    for (int first = v0; first < v1; first += kHold * kThreads) {
-      if (!kKeep) load(first);
-#pragma unroll
-      for (int k = 0; k < kHold; ++k) {
-        const int v = first + k * kThreads + tid;
-        if (v < v1) {
-          float t[VN], q[VN];
-          Vec<T>::unpack(ht[k], t);
-          Vec<T>::unpack(hq[k], q);
-          f(v, t, q);
-        }
-      }
-      if (kKeep) break;
+#pragma unroll 2
+    for (int v = v0 + tid; v < v1; v += kThreads) {
+      float t[VN], q[VN];
+      get(v, t, q);
+      f(v, t, q);
     }
   };
   // this CTA's record (in warp 0) to every CTA, and theirs
@@ -421,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreePara
     int child = a < p.D ? next_child(w, p.T, cur, cur, [](int) { return true; }) : p.T;
     inner = child < p.T;
     exchange_expect(x, n, p.C * 16);
-    if (kKeep) load(v0);
+    if (kKeep) load();
     MaxSum t{-INFINITY, 0.f}, q{-INFINITY, 0.f};
     over([&](int, const float* ft, const float* fq) {
       fold<VN>(t, ft, p.c2);
@@ -540,21 +538,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreePara
     if (owner < 0) owner = last;
     if (rank == owner) {
       const float goal = s_u[0];  // probabilities() are masses over the total
-      // Masses of 32 consecutive vectors (a warp's in one run), kHold runs at a time; the entry
+      // Masses of 32 consecutive vectors (a warp's in one run), kRuns runs at a time; the entry
       // where the running sum passes the goal, then the vector in it, then the element.
       float run = before / total;
       int pick = -1, last_v = -1;  // first vector of the chosen entry, of the last with any mass
       float start = 0.f, last_start = 0.f;
-      for (int first = v0; first < v1 && pick < 0; first += kHold * kThreads) {
-        if (!kKeep) load(first);
-#pragma unroll
-        for (int k = 0; k < kHold; ++k) {
+      for (int first = v0; first < v1 && pick < 0; first += kHold) {
+#pragma unroll 1
+        for (int k = 0; k < kRuns; ++k) {
           const int v = first + k * kThreads + tid;
           float m = 0.f;
           if (v < v1) {
             float ft[VN], fq[VN], pe[VN], qe[VN];
-            Vec<T>::unpack(ht[k], ft);
-            Vec<T>::unpack(hq[k], fq);
+            get(v, ft, fq);
             probabilities<VN>(st, p.c2, p.replacement, v * VN, ft, fq, pe, qe);
             m = tree_sum<VN>(pe);
           }
@@ -562,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreePara
           if (lane == 0) s_entry[k * kWarps + warp] = m;
         }
         __syncthreads();
-        constexpr int kEach = kHold * kWarps / 32;  // entries per lane; every warp finds the same
+        constexpr int kEach = kRuns * kWarps / 32;  // entries per lane; every warp finds the same
         float e[kEach], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) sum += e[i] = s_entry[lane * kEach + i];
@@ -617,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreePara
           float ft[VN], fq[VN], qe[VN], sum[VN];
           Vec<T>::unpack(load_scores(zt, v, p.V, p.vec), ft);
           if (inner) Vec<T>::unpack(load_scores(zq, v, p.V, p.vec), fq);
-          else Vec<T>::unpack(make_uint4(0, 0, 0, 0), fq);
           probabilities<VN>(st, p.c2, p.replacement, v * VN, ft, fq, pe, qe);
 #pragma unroll
           for (int k = 0; k < VN; ++k) sum[k] = pe[k];
@@ -658,14 +653,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sample_kernel(const TreePara
 // Clusters that read their rows' slices with a few vectors per thread, all rows' clusters at once if
 // they fit.  Returns the CTAs per cluster.
 template <typename K>
-int tree_cluster(K kernel, int B, int V, int es, int* cache) {
+int tree_cluster(K kernel, int B, int V, int es, size_t smem, int* cache) {
   const long long vecs = static_cast<long long>(V) * es / 16;
   const int most = static_cast<int>(std::min<long long>(kMaxCluster, vecs / kThreads + 1));
-  return cluster_for_one_wave(reinterpret_cast<const void*>(kernel), B, 1, most, kThreads, 0, cache);
+  return cluster_for_one_wave(reinterpret_cast<const void*>(kernel), B, 1, most, kThreads, smem, cache);
 }
 
 template <typename K>
-int launch_tree(K kernel, const TreeParams& p, int B, cudaStream_t s) {
+int launch_tree(K kernel, const TreeParams& p, int B, size_t smem, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -674,6 +669,7 @@ int launch_tree(K kernel, const TreeParams& p, int B, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(B * p.C);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -690,22 +686,29 @@ int launch_greedy(TreeParams& p, int B, cudaStream_t s) {
   static int caches[2][64 * 17];
   // All rows at once where a CTA's share of them takes it less time than the steps of a walk do:
   // about 2 us a step against 25 KB a us and CTA, and 30 MB in all.
-  p.C = tree_cluster(tree_greedy_kernel<T, true>, B, p.V, sizeof(T), caches[0]);
+  p.C = tree_cluster(tree_greedy_kernel<T, true>, B, p.V, sizeof(T), 0, caches[0]);
   const long long bytes = static_cast<long long>(p.T) * p.V * sizeof(T);
   if (bytes / p.C <= (128 << 10) && bytes * B <= (30 << 20))
-    return launch_tree(tree_greedy_kernel<T, true>, p, B, s);
-  p.C = tree_cluster(tree_greedy_kernel<T, false>, B, p.V, sizeof(T), caches[1]);
-  return launch_tree(tree_greedy_kernel<T, false>, p, B, s);
+    return launch_tree(tree_greedy_kernel<T, true>, p, B, 0, s);
+  p.C = tree_cluster(tree_greedy_kernel<T, false>, B, p.V, sizeof(T), 0, caches[1]);
+  return launch_tree(tree_greedy_kernel<T, false>, p, B, 0, s);
 }
 
 template <typename T>
 int launch_sample(TreeParams& p, int B, cudaStream_t s) {
   static int caches[2][64 * 17];
-  p.C = tree_cluster(tree_sample_kernel<T, true>, B, p.V, sizeof(T), caches[0]);
-  const int vecs = (p.V + Vec<T>::N - 1) / Vec<T>::N;
-  if ((vecs + p.C - 1) / p.C <= kHold * kThreads) return launch_tree(tree_sample_kernel<T, true>, p, B, s);
-  p.C = tree_cluster(tree_sample_kernel<T, false>, B, p.V, sizeof(T), caches[1]);
-  return launch_tree(tree_sample_kernel<T, false>, p, B, s);
+  constexpr size_t kSmem = 2 * kHold * 16;
+  const cudaError_t e = cudaFuncSetAttribute(tree_sample_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmem));
+  if (e != cudaSuccess) return map_cuda_error(e);
+  // the slices held, if need be by more CTAs per row than one wave has room for
+  const int vecs = (p.V + Vec<T>::N - 1) / Vec<T>::N, least = (vecs + kHold - 1) / kHold;
+  if (least <= kMaxCluster) {
+    p.C = std::max(least, tree_cluster(tree_sample_kernel<T, true>, B, p.V, sizeof(T), kSmem, caches[0]));
+    return launch_tree(tree_sample_kernel<T, true>, p, B, kSmem, s);
+  }
+  p.C = tree_cluster(tree_sample_kernel<T, false>, B, p.V, sizeof(T), 0, caches[1]);
+  return launch_tree(tree_sample_kernel<T, false>, p, B, 0, s);
 }
 
 int check_tree(const void* logits, int dtype, int B, int T, int V, long long row_stride,
