@@ -127,6 +127,15 @@ __device__ __forceinline__ bool exchange_wait(Exchange& x, int n) {
   return mbar_wait_bounded(&x.bar[n & 1], (n >> 1) & 1, kExchangeTries);
 }
 
+// The largest key of a warp, in every lane: scores first, then, among those that tie, the complemented
+// index (two integer reductions in place of five 64-bit shuffles).
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long key) {
+  const uint32_t hi = static_cast<uint32_t>(key >> 32);
+  const uint32_t top = __reduce_max_sync(0xffffffffu, hi);
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == top ? static_cast<uint32_t>(key) : 0u);
+  return static_cast<unsigned long long>(top) << 32 | lo;
+}
+
 // ------------------------------------------------------------------------------------- greedy
 
 // kAll: every row is read before the walk, a warp per row; else the walk's rows, one by one.
@@ -166,10 +175,7 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
           take_vector<VN>(f, (v + k * step) * VN, bv, bi);
         }
     }
-    unsigned long long key = bi >= 0 && bi < p.V ? make_key(bv, bi) : 0ull;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, k));
-    return key;
+    return warp_max(bi >= 0 && bi < p.V ? make_key(bv, bi) : 0ull);
   };
   cluster_sync_all();  // every CTA of the cluster has started: its shared memory may be written
   bool alive = true;
@@ -199,9 +205,7 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
         if (lane == 0) s_warp[warp] = key;
         __syncthreads();
         if (warp == 0) {
-          key = lane < kWarps ? s_warp[lane] : 0ull;
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, k));
+          key = warp_max(lane < kWarps ? s_warp[lane] : 0ull);
           if (lane < p.C)
             cluster_send(cluster_map(&s_rec[n & 1][rank], lane), key, cluster_map(&x.bar[n & 1], lane));
         }
@@ -293,12 +297,14 @@ __device__ __forceinline__ MaxSum merged(MaxSum a, MaxSum b) {
   if (m == -INFINITY) return MaxSum{m, a.l + b.l};  // nothing yet (or NaN, which has to stay)
   return MaxSum{m, a.l * ex2(a.m - m) + b.l * ex2(b.m - m)};
 }
+// A warp's: the maximum by one integer reduction of its order-preserving bits, then the sums to it.
 __device__ __forceinline__ MaxSum warp_merged(MaxSum s) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, order_bits(s.m));
+  const float m = __uint_as_float(top & 0x80000000u ? top ^ 0x80000000u : ~top);
+  s.l *= s.m == -INFINITY ? 1.f : ex2(s.m - m);  // (nothing yet, or NaN, which has to stay)
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1)
-    s = merged(s, MaxSum{__shfl_xor_sync(0xffffffffu, s.m, k),
-                         __shfl_xor_sync(0xffffffffu, s.l, k)});
-  return s;
+  for (int k = 16; k > 0; k >>= 1) s.l += __shfl_xor_sync(0xffffffffu, s.l, k);
+  return MaxSum{m, s.l};
 }
 template <int N> __device__ __forceinline__ float tree_sum(float* t) {
 #pragma unroll
