@@ -567,7 +567,7 @@ int specdec_pool_admit(const specdec_admit_args* args, void* stream);
  * (SPECDEC_ERR_INPUT_RANGE), a column at or beyond cache.cap_cols (SPECDEC_ERR_CAPACITY); the
  * tokens concerned (all of the row, for the first two) are not written.
  * Two tokens must not name one column.  Limits: B >= 0, T >= 1, B * T < 2^31; rot_dim even, in
- * [2, head_dim]; head_dim * element size a multiple of 16 bytes; element-aligned q, k, v, q_out;
+ * [2, head_dim]; head_dim at most 512 and head_dim * element size a multiple of 16 bytes; element-aligned q, k, v, q_out;
  * table 8-byte aligned.  q_out may overlap nothing else.
  */
 typedef struct {

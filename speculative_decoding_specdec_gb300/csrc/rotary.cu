@@ -11,13 +11,16 @@
 // prefill, the launch and one dependent chain of loads (parents or position, table, values) for
 // a verification pass.  The unit of work is one 16-byte vector of a head, or a pair of them in
 // the half layout, whose mates lie rot_dim / 2 values apart; consecutive threads take consecutive
-// vectors.  One grid row of CTAs serves a token.
+// vectors.
+#include <algorithm>
+
 #include "tree.cuh"
 
 namespace specdec {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;  // heads in flight per thread
 
 struct RotaryParams {
   ByteView cache;  // of the layer
@@ -73,91 +76,99 @@ __device__ bool locate(const RotaryParams& p, int b, int t, int& pos, int& col) 
   return true;
 }
 
-// N consecutive values as floats, and back, by one 16-byte access (N = Vec<T>::N) or one scalar.
-template <typename T, int N>
-__device__ __forceinline__ void load_values(const T* x, float* f) {
-  if constexpr (N == 1) f[0] = Vec<T>::scalar(x);
-  else Vec<T>::unpack(*reinterpret_cast<const uint4*>(x), f);
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_values(T* y, const float* f) {
-  if constexpr (N == 1) {
-    if constexpr (sizeof(T) == 2) *y = bf16_bits(f[0]);
-    else *y = f[0];
-  } else if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(y) = make_uint4(bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]),
-                                              bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7]));
-  } else {
-    *reinterpret_cast<float4*>(y) = make_float4(f[0], f[1], f[2], f[3]);
+// N consecutive values as they lie, as floats, and back: one 16-byte access (N = Vec<T>::N) or one
+// scalar.
+template <typename T, int N> struct Values {
+  using Raw = uint4;
+  __device__ __forceinline__ static Raw load(const T* x) { return *reinterpret_cast<const uint4*>(x); }
+  __device__ __forceinline__ static Raw zero() { return make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ static void unpack(Raw r, float* f) { Vec<T>::unpack(r, f); }
+  __device__ __forceinline__ static Raw pack(const float* f) {
+    if constexpr (sizeof(T) == 2)
+      return make_uint4(bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7]));
+    else
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
-}
+  __device__ __forceinline__ static void store(T* y, Raw r) { *reinterpret_cast<uint4*>(y) = r; }
+};
+template <typename T> struct Values<T, 1> {
+  using Raw = T;
+  __device__ __forceinline__ static Raw load(const T* x) { return *x; }
+  __device__ __forceinline__ static Raw zero() { return T(0); }
+  __device__ __forceinline__ static void unpack(Raw r, float* f) { f[0] = Vec<T>::scalar(&r); }
+  __device__ __forceinline__ static Raw pack(const float* f) {
+    if constexpr (sizeof(T) == 2) return bf16_bits(f[0]);
+    else return f[0];
+  }
+  __device__ __forceinline__ static void store(T* y, Raw r) { *y = r; }
+};
 
 // A unit is two runs of N values of a head: N pairs to turn (the runs are rot_dim / 2 apart in
 // the half layout, and one behind the other when interleaved), or 2N values to copy.  One thread
 // reads both runs before it writes either, so q_out may be q.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
+template <typename T, int N, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams p) {
   const int b = blockIdx.x / p.T, t = blockIdx.x % p.T;
   int pos = 0, col = 0;
   const bool write = locate(p, b, t, pos, col);
   if (!write && pos < 0) return;  // an error was recorded
+  // A thread keeps its place in the head, so its cosines and sines are read once for all heads.
+  const int half = p.rot / 2, per_head = p.hd / (2 * N), turned = half / N;
+  const int step = kThreads / per_head, j = threadIdx.x % per_head;
+  if (threadIdx.x >= step * per_head) return;
   const long long row = p.one_row ? 0 : b;
-  const int half = p.rot / 2;
-  const float2* cs = p.table + static_cast<long long>(pos) * half;
-  const int per_head = p.hd / (2 * N), turned = half / N;
-  const int total = (p.Hq + 2 * p.H) * per_head;
-  for (int u = blockIdx.y * kThreads + threadIdx.x; u < total; u += gridDim.y * kThreads) {
-    const int h = u / per_head, j = u % per_head;
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.H;
-    if (!is_q && !write) break;
-    const int hk = is_q ? h : is_v ? h - p.Hq - p.H : h - p.Hq;
-    const char* src = is_q ? p.q + b * p.qr + t * p.qt
-                           : is_v ? p.v + b * p.vr + t * p.vt : p.k + b * p.kr + t * p.kt;
-    const T* x = reinterpret_cast<const T*>(src) + hk * p.hd;
-    T* y = is_q ? reinterpret_cast<T*>(p.qo + b * p.or_ + t * p.ot) + hk * p.hd
-                : reinterpret_cast<T*>(p.cache.base + (is_v ? p.cache.skv : 0) +
-                                       row * p.cache.srow + hk * p.cache.shead) +
-                      static_cast<long long>(col) * p.hd;
-    const bool turn = j < turned && !is_v;
-    const int e0 = turn && !p.interleaved ? j * N : 2 * j * N;
-    const int e1 = turn && !p.interleaved ? e0 + half : e0 + N;
-    float f0[N], f1[N];
-    load_values<T, N>(x + e0, f0);
-    load_values<T, N>(x + e1, f1);
-    if (turn && p.interleaved) {  // pairs are neighbours in the 2N values
-      float v[2 * N];
+  const bool turns = j < turned;
+  float2 c[N];
+  if (turns && write) {
+    const float2* cs = p.table + static_cast<long long>(pos) * half + j * N;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        v[k] = f0[k];
-        v[N + k] = f1[k];
-      }
+    for (int k = 0; k < N; ++k) c[k] = __ldg(cs + k);
+  }
+  const bool far = turns && !kInterleaved;  // the two runs lie rot_dim / 2 apart
+  const int e0 = far ? j * N : 2 * j * N, e1 = far ? e0 + half : e0 + N;
+  const int heads = write ? p.Hq + 2 * p.H : p.Hq;
+  const char *q = p.q + b * p.qr + t * p.qt, *k = p.k + b * p.kr + t * p.kt,
+             *v = p.v + b * p.vr + t * p.vt;
+  char *qo = p.qo + b * p.or_ + t * p.ot,
+       *to = p.cache.base + row * p.cache.srow + static_cast<long long>(col) * p.hd * sizeof(T);
+  for (int h0 = blockIdx.y * step + threadIdx.x / per_head; h0 < heads; h0 += gridDim.y * step * kHeads) {
+    typename Values<T, N>::Raw r0[kHeads], r1[kHeads];
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float2 c = cs[j * N + k];
-        const float a = v[2 * k], m = v[2 * k + 1];
-        v[2 * k] = a * c.x - m * c.y;
-        v[2 * k + 1] = a * c.y + m * c.x;
-      }
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        f0[k] = v[k];
-        f1[k] = v[N + k];
-      }
-    } else if (turn) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float2 c = cs[j * N + k];
-        const float a = f0[k], m = f1[k];
-        f0[k] = a * c.x - m * c.y;
-        f1[k] = a * c.y + m * c.x;
+    for (int i = 0; i < kHeads; ++i) {  // loads first: they wait for memory together
+      const int h = h0 + i * gridDim.y * step;
+      r0[i] = r1[i] = Values<T, N>::zero();
+      if (h < heads && write) {
+        const T* x = reinterpret_cast<const T*>(h < p.Hq ? q : h < p.Hq + p.H ? k : v) +
+                     (h < p.Hq ? h : h < p.Hq + p.H ? h - p.Hq : h - p.Hq - p.H) * p.hd;
+        r0[i] = Values<T, N>::load(x + e0);
+        r1[i] = Values<T, N>::load(x + e1);
       }
     }
-    if (!write) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) f0[k] = f1[k] = 0.f;
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = h0 + i * gridDim.y * step;
+      if (h >= heads) break;
+      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.H;
+      T* y = is_q ? reinterpret_cast<T*>(qo) + h * p.hd
+                  : reinterpret_cast<T*>(to + (is_v ? p.cache.skv : 0) + (h - p.Hq - (is_v ? p.H : 0)) * p.cache.shead);
+      if (turns && !is_v && write) {
+        // pairs: neighbours of the 2N values, or one of each run
+        float w[2 * N];
+        Values<T, N>::unpack(r0[i], w);
+        Values<T, N>::unpack(r1[i], w + N);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int a = kInterleaved ? 2 * n : n, b = kInterleaved ? 2 * n + 1 : N + n;
+          const float x1 = w[a], x2 = w[b];
+          w[a] = x1 * c[n].x - x2 * c[n].y;
+          w[b] = x1 * c[n].y + x2 * c[n].x;
+        }
+        r0[i] = Values<T, N>::pack(w);
+        r1[i] = Values<T, N>::pack(w + N);
+      }
+      Values<T, N>::store(y + e0, r0[i]);
+      Values<T, N>::store(y + e1, r1[i]);
     }
-    store_values<T, N>(y + e0, f0);
-    store_values<T, N>(y + e1, f1);
   }
 }
 
@@ -168,9 +179,14 @@ int launch_rotary(const RotaryParams& p, int B, cudaStream_t s) {
                          reinterpret_cast<uintptr_t>(p.v) | reinterpret_cast<uintptr_t>(p.qo) |
                          p.qr | p.qt | p.kr | p.kt | p.vr | p.vt | p.or_ | p.ot;
   const bool vec = bits % 16 == 0 && p.rot % (2 * N) == 0 && p.hd % (2 * N) == 0;
-  const dim3 grid(B * p.T);
-  if (vec) rotary_kernel<T, N><<<grid, kThreads, 0, s>>>(p);
-  else rotary_kernel<T, 1><<<grid, kThreads, 0, s>>>(p);
+  // few tokens: a token's heads over several CTAs
+  const int per_pass = kThreads / (p.hd / (2 * (vec ? N : 1))), passes = (p.Hq + 2 * p.H + per_pass - 1) / per_pass;
+  const int want = (4 * std::max(1, sm_count()) + B * p.T - 1) / (B * p.T);
+  const dim3 grid(B * p.T, std::max(1, std::min(want, passes)));
+  if (vec && p.interleaved) rotary_kernel<T, N, true><<<grid, kThreads, 0, s>>>(p);
+  else if (vec) rotary_kernel<T, N, false><<<grid, kThreads, 0, s>>>(p);
+  else if (p.interleaved) rotary_kernel<T, 1, true><<<grid, kThreads, 0, s>>>(p);
+  else rotary_kernel<T, 1, false><<<grid, kThreads, 0, s>>>(p);
   return map_cuda_error(cudaGetLastError());
 }
 
@@ -200,7 +216,8 @@ extern "C" int specdec_rotary_append(const specdec_rotary_args* a, void* stream)
       reinterpret_cast<uintptr_t>(a->table) % sizeof(float2))
     return SPECDEC_ERR_INVALID_ARG;
   if ((pass && a->T > SPECDEC_MAX_TREE) || static_cast<long long>(a->B) * a->T >= (1LL << 31) ||
-      static_cast<long long>(a->heads_q + 2LL * c.heads) * c.head_dim >= (1LL << 30))
+      static_cast<long long>(a->heads_q + 2LL * c.heads) * c.head_dim >= (1LL << 30) ||
+      c.head_dim > 2 * kThreads)
     return SPECDEC_ERR_UNSUPPORTED;
   RotaryParams p = {};
   p.cache = to_bytes(c);
