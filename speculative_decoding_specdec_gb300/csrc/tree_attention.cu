@@ -1,11 +1,13 @@
 // Attention of a draft tree over the cache: host entry, and the kernel for fp32 tensors and for
 // head sizes that the tensor-core kernels do not take.
 //
-// attn_fma_kernel.  fp32 has no tensor-core product of full precision, so this is the FMA pipe:
-// RG warps, each with 4 query rows, share a tile of 32 columns of K and V in shared memory
-// (cp.async, two stages).  A lane computes the scores of one column (its K vector against four
-// broadcast Q vectors), the softmax of a row is warp-local, and for the second product a lane owns
-// 4 (or 8) of the head's values.  Shared-memory reads bound it: 8 wavefronts per 16 FMAs.
+// attn_fma_kernel.  fp32 has no tensor-core product of full precision, so this is the FMA pipe, R
+// query rows at a time.  As in the kernel for few rows, a warp is the unit: it streams its own 16
+// columns of each tile into two private stages, one bulk copy per column and lane, without any
+// CTA-wide barrier.  For the scores a lane has half of a column's values (one 16-byte read of K
+// against R broadcast reads of Q); for O a lane owns 4 (or 8) of the head's values (one read of V
+// and R / 4 broadcast reads of the weights for 4 R FMAs).  HBM bounds few rows, the FMA pipe and
+// its operands' shared-memory reads many.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -15,7 +17,11 @@
 namespace specdec {
 namespace {
 
-constexpr int kTile = 32;
+constexpr int kCols = 16;      // columns of a warp's slice of a tile
+constexpr int kStages = 2;
+constexpr int kMaxWarps = 8;
+constexpr uint32_t kTries = 1u << 17, kNs = 20000;  // a wait gives up after about 2.6 s
+constexpr float kGrow = 32.f;  // log2 of the growth of the maximum that is let pass
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -27,9 +33,14 @@ __device__ __forceinline__ float ex2(float x) {
 // eight neighbouring columns fall into different banks.
 __host__ __device__ constexpr int pitch_of(int hd, int es) { return hd * es + 16; }
 
-__host__ inline size_t fma_smem(int RG, int hd, int es) {
-  return static_cast<size_t>(4) * kTile * pitch_of(hd, es) + static_cast<size_t>(RG) * 4 * hd * 4 +
-         static_cast<size_t>(RG) * kTile * 16;
+constexpr int kRowsTile = 32;  // columns of a tile of the kernel for more rows
+__host__ inline size_t fma_rows_smem(int hd, int es) {
+  return static_cast<size_t>(4) * kRowsTile * pitch_of(hd, es) + static_cast<size_t>(32) * hd * 4 + 8 * kRowsTile * 16;
+}
+
+// Shared memory of a warp: stages, weights, and its O to be merged; and of the CTA: Q.
+__host__ __device__ constexpr int fma_warp_bytes(int R, int hd, int es) {
+  return kStages * 2 * kCols * pitch_of(hd, es) + kCols * R * 4 + R * hd * 4;
 }
 
 // 4 consecutive values of a column as floats.
@@ -49,10 +60,301 @@ template <> __device__ __forceinline__ void store4<uint16_t>(char* p, float4 v) 
   *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pack(v.x, v.y), bf16_pack(v.z, v.w));
 }
 
-// RG: groups of 4 query rows (warps); NB: blocks of 128 head values (1 or 2).
-template <typename T, int RG, int NB>
-__global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
-  constexpr int kThreads = RG * 32, M = RG * 4;
+// Walks the tiles of a share, segment by segment.
+struct Cursor {
+  AttnSegment seg;
+  int tile;   // of the segment
+  bool more;  // not behind the last
+};
+
+// R: query rows of an M-tile; NB: blocks of 128 head values (1 or 2).
+template <typename T, int R, int NB>
+__global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnParams p) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ uint64_t s_full[kMaxWarps][kStages];
+  __shared__ int s_par[kMaxTree], s_flag, s_bad;
+  __shared__ unsigned long long s_anc[kMaxTree];
+  __shared__ float2 s_ml[kMaxWarps][R];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
+  const int hd = p.hd, es = sizeof(T), pitch = pitch_of(hd, es), col_bytes = hd * es, tile_cols = kCols * warps;
+  const int warp_bytes = fma_warp_bytes(R, hd, es);
+  float* s_q = reinterpret_cast<float*>(smem);                     // [R][hd], times scale_log2
+  char* mem = smem + R * hd * 4 + warp * warp_bytes;               // [stage][K, V][kCols] columns
+  float* s_p = reinterpret_cast<float*>(mem + kStages * 2 * kCols * pitch);  // [kCols][R]
+  auto merge = [&](int w) {                                        // [R][hd] of warp w
+    return reinterpret_cast<float*>(smem + R * hd * 4 + w * warp_bytes + kStages * 2 * kCols * pitch) + kCols * R;
+  };
+  const AttnPlan plan = attn_plan_at(smem + R * hd * 4 + warps * warp_bytes, p.B);
+  if (warp == 0) attn_plan(p, tile_cols, plan);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const AttnShares sh = attn_shares(p, plan);
+  const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
+  if (sh.total == 0 || g >= sh.groups) return;
+  const int x1 = sh.start(g + 1);
+  const int nrows = min(R, p.T * p.G - mt * R);  // query rows of this M-tile: (node, head) pairs
+  // The warp's columns of the cursor's tile into stage `st`: lanes 0..15 copy K's, the others V's.
+  auto fetch = [&](const Cursor& c, int st) {
+    const int col = c.tile * tile_cols + warp * kCols, n = max(0, min(kCols, c.seg.cols - col));
+    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][st], 2 * n * col_bytes);
+    __syncwarp();
+    const int j = lane & 15, kv = lane >> 4;
+    if (j < n)
+      bulk_g2s(mem + ((st * 2 + kv) * kCols + j) * pitch,
+               p.cache.base + kv * p.cache.skv + (p.one_row ? 0 : c.seg.b) * p.cache.srow +
+                   c.seg.h * p.cache.shead + static_cast<long long>(c.seg.first + col + j) * col_bytes,
+               col_bytes, &s_full[warp][st]);
+  };
+  auto advance = [&](Cursor& c) {
+    if (++c.tile >= c.seg.tile1) {
+      c.more = attn_next(p, plan, c.seg.next, x1, c.seg);
+      c.tile = c.seg.tile0;
+    }
+  };
+  Cursor ahead;
+  ahead.more = attn_next(p, plan, sh.start(g), x1, ahead.seg);
+  ahead.tile = ahead.seg.tile0;
+  int loaded = 0, used = 0, row_b = -1;  // tiles asked for, tiles done
+  for (; loaded < kStages && ahead.more; ++loaded) {
+    fetch(ahead, loaded);
+    advance(ahead);
+  }
+  bool ok = true;
+  AttnSegment seg;
+  for (int x = sh.start(g); attn_next(p, plan, x, x1, seg); x = seg.next) {
+    __syncthreads();  // the segment before is done with Q and the tree
+    const bool other = seg.b != row_b;
+    row_b = seg.b;
+    if (other) {
+      if (p.parents && tid < p.T) s_par[tid] = p.parents[seg.b * p.T + tid];
+      if (tid == 0) s_bad = 0;
+    }
+    for (int i = tid * 4; i < R * hd; i += threads * 4) {
+      const int r = i / hd, d = i - r * hd, rr = mt * R + r;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nrows) {
+        const int t = rr / p.G, qh = seg.h * p.G + rr - t * p.G;
+        v = load4<T>(p.q + seg.b * p.qr + t * p.qt + (static_cast<long long>(qh) * hd + d) * es);
+      }
+      *reinterpret_cast<float4*>(s_q + i) = make_float4(v.x * p.scale_log2, v.y * p.scale_log2,
+                                                        v.z * p.scale_log2, v.w * p.scale_log2);
+    }
+    __syncthreads();
+    if (other) {
+      for (int i = tid; i < p.T; i += threads) {
+        bool bad = false;
+        s_anc[i] = tree_ancestors(p.parents ? s_par : nullptr, i, bad);
+        if (bad) {
+          s_bad = 1;
+          set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
+        }
+      }
+      __syncthreads();
+    }
+    float m[R], l[R];
+    float4 o[R][NB];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) o[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++used) {
+      const int st = used % kStages;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_sleep(&s_full[warp][st], (used / kStages) & 1, kTries, kNs));
+      const int col = tile * tile_cols + warp * kCols;
+      if (ok && col < seg.cols) {
+        const char* sk = mem + (st * 2 * kCols + (lane & 15)) * pitch;
+        const char* sv = mem + (st * 2 + 1) * kCols * pitch;
+        float z[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) z[r] = 0.f;
+        const int n4 = hd / 4, mid = (n4 + 1) / 2;  // the two lanes of a column take half each
+        for (int i = lane >> 4 ? mid : 0, end = lane >> 4 ? n4 : mid; i < end; ++i) {
+          const float4 kk = load4<T>(sk + i * 4 * es);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float4 qq = *reinterpret_cast<const float4*>(s_q + r * hd + i * 4);
+            z[r] = fmaf(qq.x, kk.x, z[r]);
+            z[r] = fmaf(qq.y, kk.y, z[r]);
+            z[r] = fmaf(qq.z, kk.z, z[r]);
+            z[r] = fmaf(qq.w, kk.w, z[r]);
+          }
+        }
+        __syncwarp();
+        const int node = col + (lane & 15) - seg.old;
+        bool up = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          z[r] += __shfl_xor_sync(0xffffffffu, z[r], 16);
+          if (node >= 0) {
+            const int rr = mt * R + r;
+            const bool see = node < p.T && r < nrows && (s_anc[p.g_shift >= 0 ? rr >> p.g_shift : rr / p.G] >> node & 1);
+            if (!see) z[r] = -INFINITY;
+          }
+          up |= z[r] > m[r] + kGrow || (m[r] == -INFINITY && z[r] > m[r]);
+        }
+        // the maximum is followed only where it grows much: until then weights, sum and O are that
+        // much larger, which fp32 does not mind
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float mx = z[r];
+#pragma unroll
+            for (int j = 8; j > 0; j >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, j));
+            if (mx > m[r]) {
+              const float f = ex2(m[r] - mx);
+              m[r] = mx;
+              l[r] *= f;
+#pragma unroll
+              for (int j = 0; j < NB; ++j) {
+                o[r][j].x *= f;
+                o[r][j].y *= f;
+                o[r][j].z *= f;
+                o[r][j].w *= f;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          z[r] = ex2(z[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+          l[r] += z[r];  // (both lanes of a column: halved at the end)
+        }
+        if (lane < 16)
+#pragma unroll
+          for (int r = 0; r < R; r += 4)
+            *reinterpret_cast<float4*>(s_p + lane * R + r) = make_float4(z[r], z[r + 1], z[r + 2], z[r + 3]);
+        __syncwarp();
+        // nodes' columns may hold anything where a row does not see them: weight 0 is skipped there
+        const int c_end = min(kCols, seg.cols - col), plain = min(c_end, max(0, seg.old - col));
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int d = j * 128 + lane * 4;
+          if (d < hd) {
+            auto column = [&](int c, bool skip) {
+              const float4 vv = load4<T>(sv + c * pitch + d * es);
+#pragma unroll
+              for (int r = 0; r < R; r += 4) {
+                const float4 w4 = *reinterpret_cast<const float4*>(s_p + c * R + r);
+                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (!skip || w[k] != 0.f) {
+                    o[r + k][j].x = fmaf(w[k], vv.x, o[r + k][j].x);
+                    o[r + k][j].y = fmaf(w[k], vv.y, o[r + k][j].y);
+                    o[r + k][j].z = fmaf(w[k], vv.z, o[r + k][j].z);
+                    o[r + k][j].w = fmaf(w[k], vv.w, o[r + k][j].w);
+                  }
+              }
+            };
+            if (plain == kCols) {
+#pragma unroll 4
+              for (int c = 0; c < kCols; ++c) column(c, false);
+            } else {
+              for (int c = 0; c < c_end; ++c) column(c, c >= plain);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (ok && ahead.more) {
+        fetch(ahead, loaded % kStages);
+        advance(ahead);
+        ++loaded;
+      }
+    }
+    // ------------------------------------------------------------- the warps' parts
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int j = 16; j > 0; j >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], j);
+      if (lane == 0) s_ml[warp][r] = make_float2(m[r], 0.5f * l[r]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int d = j * 128 + lane * 4;
+        if (d < hd) *reinterpret_cast<float4*>(merge(warp) + r * hd + d) = o[r][j];
+      }
+    }
+    __syncthreads();
+    const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
+    const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1), n4 = hd / 4;
+    // 4 values of row r, merged over `parts` parts that `ml(i)` and `at(i)` give
+    auto merged = [&](int parts, auto ml, auto at, float& mm, float& ll) {
+      mm = -INFINITY;
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) mm = fmaxf(mm, ml(i).x);
+      const float off = mm == -INFINITY ? 0.f : mm;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      ll = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) {
+        const float2 y = ml(i);
+        const float4 v = at(i);
+        const float f = ex2(y.x - off);
+        ll += y.y * f;
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+      }
+      return acc;
+    };
+    auto store = [&](int r, int i, float4 acc, float mm, float ll) {
+      const int rr = mt * R + r, t = rr / p.G, qh = seg.h * p.G + rr - t * p.G;
+      const bool live = s_anc[t] != 0;
+      const float inv = live ? 1.f / ll : 0.f;
+      store4<T>(p.out + seg.b * p.outr + t * p.outt + (static_cast<long long>(qh) * hd + i * 4) * es,
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (p.lse && i == 0)
+        p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + qh] =
+            live ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    };
+    const int slot = whole ? 0 : attn_slot(p, sh, g, mt, seg.unit0);
+    if (!s_bad)
+      for (int k = tid; k < nrows * n4; k += threads) {
+        const int r = k / n4, i = k - r * n4;
+        float mm, ll;
+        const float4 acc = merged(warps, [&](int w) { return s_ml[w][r]; },
+                                  [&](int w) { return *reinterpret_cast<const float4*>(merge(w) + r * hd + i * 4); }, mm, ll);
+        if (whole) {
+          store(r, i, acc, mm, ll);
+        } else {
+          const long long at = static_cast<long long>(slot) * R + r;
+          if (i == 0) p.part_ml[at] = make_float2(mm, ll);
+          *reinterpret_cast<float4*>(p.part_o + at * hd + i * 4) = acc;
+        }
+      }
+    if (whole || s_bad) continue;
+    if (!attn_last(p, seg.b, seg.h, mt, g1 - g0 + 1, &s_flag)) continue;
+    for (int k = tid; k < nrows * n4; k += threads) {
+      const int r = k / n4, i = k - r * n4;
+      auto at = [&](int j) { return static_cast<long long>(attn_slot(p, sh, g0 + j, mt, seg.unit0)) * R + r; };
+      float mm, ll;
+      const float4 acc = merged(g1 - g0 + 1, [&](int j) { return __ldcg(p.part_ml + at(j)); },
+                                [&](int j) { return __ldcg(reinterpret_cast<const float4*>(p.part_o + at(j) * hd + i * 4)); }, mm, ll);
+      store(r, i, acc, mm, ll);
+    }
+  }
+  if (!ok) {
+    set_status(p.status, SPECDEC_ERR_TIMEOUT);
+    // no copy outlives the CTA: those asked for and not waited for have landed
+    for (int i = used; i < loaded; ++i)
+      (void)mbar_wait_sleep(&s_full[warp][i % kStages], (i / kStages) & 1, kTries, kNs);
+  }
+}
+
+// More than 32 rows: the FMA pipe bounds it, so 8 warps of 4 rows each share a tile of 32 columns in
+// shared memory (cp.async, two stages) in place of streaming their own.  A lane computes the scores
+// of one column, the softmax of a row is warp-local, and for O a lane owns 4 (or 8) of the head's
+// values.  NB: blocks of 128 head values (1 or 2).
+template <typename T, int NB>
+__global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) {
+  constexpr int RG = 8, kThreads = RG * 32, M = RG * 4, kTile = kRowsTile;
   extern __shared__ __align__(16) char smem[];
   __shared__ int s_par[kMaxTree], s_flag, s_bad;
   __shared__ unsigned long long s_anc[kMaxTree];
@@ -289,7 +591,7 @@ __global__ void __launch_bounds__(RG * 32) attn_fma_kernel(const AttnParams p) {
 // ------------------------------------------------------------------------------------- host
 
 struct AttnShape {
-  int M, MT, groups, grid, tile, min_tiles, open;
+  int M, MT, groups, grid, tile, min_tiles, open, warps;
   size_t smem;
   int kind;
 };
@@ -299,15 +601,30 @@ enum { kFma = 0, kMma = 1, kTc = 2 };
 AttnShape fma_shape(int es, int T, int G, int hd) {
   AttnShape s = {};
   const int rows = T * G;
-  const int RG = rows <= 4 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : 8;
-  s.M = RG * 4;
+  // (64 rows of 128 values: 122 us against 177 of the other kernel; 32 rows of 64: 51 against 36)
+  if (rows > 32) {
+    s.M = 32;
+    s.MT = (rows + 31) / 32;
+    s.warps = 8;
+    s.smem = fma_rows_smem(hd, es);
+    const int per_sm = std::max(1, static_cast<int>((212 * 1024) / (s.smem + 14 * 1024)));
+    s.groups = std::max(1, sm_count() * std::min(per_sm, 2) / s.MT);
+    s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
+    s.tile = kRowsTile;
+    s.min_tiles = 2;
+    return s;
+  }
+  s.M = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   s.MT = (rows + s.M - 1) / s.M;
-  s.smem = fma_smem(RG, hd, es);
-  const int per_sm = std::max(1, std::min(8, static_cast<int>((220 * 1024) / (s.smem + 6 * 1024))));
-  s.groups = std::max(1, sm_count() * per_sm / s.MT);
+  // one CTA per SM of as many warps as have room (the plan of 1024 rows takes 12 KB)
+  const int room = 212 * 1024 - s.M * hd * 4;
+  s.warps = std::max(1, std::min(kMaxWarps, room / fma_warp_bytes(s.M, hd, es)));
+  s.smem = static_cast<size_t>(s.M) * hd * 4 + static_cast<size_t>(s.warps) * fma_warp_bytes(s.M, hd, es);
+  s.groups = std::max(1, sm_count() / s.MT);
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
-  s.tile = kTile;
-  s.min_tiles = 2;
+  s.tile = kCols * s.warps;
+  s.min_tiles = 1;
+  s.open = 2;
   return s;
 }
 
@@ -347,22 +664,21 @@ AttnWorkspace attn_workspace(const AttnShape& s, int B, int H, int hd) {
   return w;
 }
 
-template <typename T, int RG, int NB>
-int launch_fma(const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
-  auto kernel = attn_fma_kernel<T, RG, NB>;
+template <typename T, typename K>
+int launch_fma(K kernel, const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(s.smem) + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<s.grid, RG * 32, s.smem + attn_plan_bytes(p.B), stream>>>(p);
+  kernel<<<s.grid, s.warps * 32, s.smem + attn_plan_bytes(p.B), stream>>>(p);
   return map_cuda_error(cudaGetLastError());
 }
 template <typename T, int NB>
 int launch_fma_rows(const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
   switch (s.M) {
-    case 4: return launch_fma<T, 1, NB>(p, s, stream);
-    case 8: return launch_fma<T, 2, NB>(p, s, stream);
-    case 16: return launch_fma<T, 4, NB>(p, s, stream);
-    default: return launch_fma<T, 8, NB>(p, s, stream);
+    case 4: return launch_fma<T>(attn_fma_kernel<T, 4, NB>, p, s, stream);
+    case 8: return launch_fma<T>(attn_fma_kernel<T, 8, NB>, p, s, stream);
+    case 16: return launch_fma<T>(attn_fma_kernel<T, 16, NB>, p, s, stream);
+    default: return launch_fma<T>(attn_fma_rows_kernel<T, NB>, p, s, stream);
   }
 }
 
@@ -421,7 +737,7 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   s.grid = s.groups * s.MT;
   const AttnWorkspace w = attn_workspace(s, a->B, c.heads, c.head_dim);
   if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
-  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kTile + 16) >= (1LL << 31))
+  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kCols + 16) >= (1LL << 31))
     return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   AttnParams p = {};
   p.cache = to_bytes(c);
