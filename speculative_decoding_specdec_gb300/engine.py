@@ -8,6 +8,8 @@ examined afterwards.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import specdec
@@ -175,6 +177,95 @@ class EqspecBatch:
                         schedule=self.sched_words)
         self.cur = d
         self.round = r + 1
+
+
+def rotary_table(positions, rot_dim, base=10000.0, scaling=None, factor=1.0, original=0,
+                 beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """Cosines and sines [positions, rot_dim / 2, 2] (float32, made in float64) for
+    ``specdec.rotary_append``: frequencies base ** (-2i / rot_dim), and for contexts ``factor`` times
+    the trained length (``original`` positions)
+      - "linear": every frequency divided by ``factor``;
+      - "base":   the base raised so that the lowest frequency is divided by ``factor``;
+      - "bands":  frequencies that turn less than ``beta_slow`` times within ``original`` positions
+        divided by ``factor``, those that turn more than ``beta_fast`` times kept, a linear ramp
+        between, and cosines and sines times 0.1 ln(factor) + 1."""
+    half = rot_dim // 2
+    if rot_dim < 2 or rot_dim % 2 or positions < 1 or factor <= 0:
+        raise ValueError("rot_dim must be even and positive, positions and factor positive")
+    i = torch.arange(half, dtype=torch.float64)
+    if scaling == "base" and half > 1:
+        base = base * factor ** (half / (half - 1))
+    freq = base ** (-i / half)
+    amplitude = 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "bands":
+        if original < 1:
+            raise ValueError("bands need the original number of positions")
+        turns = original * freq / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+        freq = freq * (keep + (1 - keep) / factor)
+        amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling}")
+    angle = torch.arange(positions, dtype=torch.float64)[:, None] * freq
+    return (torch.stack((angle.cos(), angle.sin()), -1) * amplitude).float().to(device)
+
+
+class TreeBatch(EqspecBatch):
+    """A left-padded batch that drafts trees of up to ``nodes`` tokens (the pending one included),
+    ``D`` deep.  A round: per layer ``rotary_append`` and ``attention`` (the target's verification
+    pass over the tree), one of the ``verify_tree_*``, then ``commit_realign``; what a round accepts
+    is kept in the history as for chains, and its path and tokens in ``path`` and ``drafts``.
+    ``cap`` needs room for the width and the tree: W + nodes - 1 columns."""
+
+    def __init__(self, layers, heads_q, heads, head_dim, kv_dtype, B, nodes, D, cap, max_rounds,
+                 device="cuda", pad_id=0, in_place=False, scheduled=True):
+        super().__init__(layers, heads, head_dim, kv_dtype, B, D, cap, max_rounds, device=device,
+                         pad_id=pad_id, in_place=in_place, scheduled=scheduled)
+        if not 1 <= nodes <= specdec.MAX_TREE:
+            raise ValueError(f"nodes must be in [1, {specdec.MAX_TREE}]")
+        self.nodes, self.heads_q = nodes, heads_q
+        i32 = dict(dtype=torch.int32, device=self.status.device)
+        self.path = torch.zeros((B, D), **i32)
+        self.drafts = torch.zeros((B, D), **i32)
+
+    def rotary_append(self, layer, q, k, v, table, q_out, parents, interleaved=False, stream=None):
+        """Positions of the tree's queries and keys, and its K/V into the cache's columns."""
+        specdec.rotary_append(q, k, v, self.cache, layer, table, q_out, self.status,
+                              n_committed=self.n_committed, width=self.width, parents=parents,
+                              interleaved=interleaved, stream=stream)
+
+    def attention(self, layer, q, out, parents, scale=None, lse=None, stream=None):
+        """Attention of the tree over the committed columns and each node's ancestors."""
+        ws = self.workspaces.get("tree", specdec.tree_attention_workspace_bytes(q, self.cache))
+        specdec.tree_attention(q, self.cache, layer, out, self.n_committed, self.width, parents,
+                               self.status, ws, scale=scale, lse=lse, stream=stream)
+
+    def verify_tree_greedy(self, logits, tokens, parents, stream=None):
+        self._results_row()
+        specdec.verify_tree_greedy(logits, tokens, parents, self.accept_len, self.out_token,
+                                   self.path, self.drafts, self.status, stream)
+
+    def verify_tree_sample(self, target_logits, draft_logits, tokens, parents, uniforms,
+                           temperature, replacement=False, stream=None):
+        self._results_row()
+        specdec.verify_tree_sample(target_logits, draft_logits, tokens, parents, uniforms,
+                                   temperature, self.accept_len, self.out_token, self.path,
+                                   self.drafts, self.status, replacement, stream)
+
+    def commit_realign(self, stream=None):
+        """The accepted paths' columns made contiguous and the batch realigned: in place the commit
+        comes first, with two caches it writes behind what the realignment moved."""
+        src, width, r = self.cache, self.width, self.round
+        if self.in_place:
+            specdec.tree_commit(src, src, width, self.accept_len, self.path, self.status,
+                                nodes=self.nodes, stream=stream)
+            self.realign(self.drafts, stream=stream)
+        else:
+            self.realign(self.drafts, stream=stream)
+            specdec.tree_commit(src, self.cache, width, self.accept_len, self.path, self.status,
+                                width_dst=self.w_hist[r + 1], nodes=self.nodes, stream=stream)
 
 
 class HostRounds:
