@@ -7,8 +7,8 @@
 //   warps 0-3, 4-7  softmax of A, B: one thread per row reads its 128 scores from tensor memory,
 //                   keeps maximum and sum, writes the weights back as bf16 over the scores;
 //   warp 8          TMA: K and V tiles of 128 columns into two stages each (128-byte swizzle);
-//   warps 9, 10     one thread each issues S = Q K^T (both operands in shared memory) and
-//                   O += P V (P from tensor memory, V as it lies: MN-major) of A, of B.
+//   warp 9          one thread issues S = Q K^T (both operands in shared memory) and
+//                   O += P V (P from tensor memory, V as it lies: MN-major).
 // Tensor memory (512 columns): S/P of A and B, O of A and B, 128 columns each.
 // The running maximum is only followed when it grows by more than 2^32 in weight (and from the
 // first columns on): until then weights, their sum and O are that much larger, which neither fp32
@@ -27,7 +27,7 @@ namespace specdec {
 
 namespace {
 
-constexpr int kThreads = 384;  // (the last warp only completes the third warpgroup)
+constexpr int kThreads = 384;  // (the last two warps only complete the third warpgroup)
 // Registers per thread: 384 x 168 at launch; 2 x 128 x 224 + 128 x 56 = those 64512.
 constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 constexpr int kCols = 128;     // columns of a K/V tile
@@ -63,7 +63,7 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 
 struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full, v_clean, s_full[2], p_half[2], p_ready[2], o_half[2], o_done[2];
+  uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2];
 };
 
 __device__ __forceinline__ bool inf_or_nan(uint32_t w) {  // either of two bf16 values
@@ -137,17 +137,15 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   if (tid == 32) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.k_full[i], 1);
-      mbar_init(&bar.k_empty[i], two ? 2 : 1);  // A's and B's products, or the tile's one
+      mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.v_full[i], 1);
-      mbar_init(&bar.v_empty[i], two ? 2 : 1);
+      mbar_init(&bar.v_empty[i], 1);
     }
     mbar_init(&bar.q_full, 256);
-    mbar_init(&bar.v_clean, 2);
+    mbar_init(&bar.v_clean, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_half[i], 128);
       mbar_init(&bar.p_ready[i], 128);
-      mbar_init(&bar.o_half[i], 1);
       mbar_init(&bar.o_done[i], 1);
     }
     fence_mbar_init();
@@ -197,62 +195,64 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           (void)wait(&bar.v_full[i % kStages], (i / kStages) & 1);
         }
     }
-  } else if (warp < 11) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------------------------- MMA
-    // Warp 9 for accumulator A, warp 10 for B: while one waits, the other's products run.  The
-    // whole warp follows its jobs and one elected lane issues.  What an MMA's operands are made of
+    // The whole warp follows the jobs, A's and B's in turn, and one elected lane issues.  In turn,
+    // so that one accumulator's softmax runs beside the other's products: with a warp for each, the
+    // two fell into step, and both waited while both computed.  A wait costs this warp about 200
+    // cycles even where there is nothing to wait for, with the tensor cores idle, so it has one per
+    // job: the softmax's threads see to V and the next K before they release the weights.  What an MMA's operands are made of
     // is the same in all lanes and made so for the compiler to see (the shuffles): an MMA takes
     // its descriptors from uniform registers, and moving them there lane by lane took longer than
     // the products.
     constexpr uint32_t id_s = mma_idesc(kRows, kCols, false), id_o = mma_idesc(kRows, HD, true);
-    const int a = __shfl_sync(0xffffffffu, warp, 0) - 9;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t sm = __shfl_sync(0xffffffffu, smem_addr(smem), 0);
     const bool pair = __shfl_sync(0xffffffffu, two ? 1 : 0, 0) != 0;
-    const uint64_t q_desc = mma_desc(sm + S::q + (pair ? a : 0) * S::kQ, 16, 1024),
-                   k_desc = mma_desc(sm + S::k, 16, 1024),
+    const uint64_t q_desc = mma_desc(sm + S::q, 16, 1024), k_desc = mma_desc(sm + S::k, 16, 1024),
                    v_desc = mma_desc(sm + S::v, kCols * 128, 1024);
-    const uint32_t t_s = tm + a * kCols, t_o = tm + (2 + a) * kCols;
-    int kv = 0, seg_no = 0, done = 0;  // tiles, segments, jobs so far
+    int kv = 0, seg_no = 0, done[2] = {0, 0};  // tiles, segments, jobs of A and B so far
     AttnSegment seg;
     for (int x = x0; ok && attn_next(p, plan, x, x1, seg); x = seg.next, ++seg_no) {
-      const int n = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0);
-      const int jobs = pair ? n : (n - a + 1) >> 1;  // tiles 0, 1, .. or every second one from a
+      const int n = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0), jobs = pair ? 2 * n : n;
       const int clean = seg.old / kCols - seg.tile0;  // the first tile that needs care
-      auto tile_of = [&](int j) { return pair ? j : 2 * j + a; };
-      auto scores = [&](int j) {  // S = Q K^T
-        const int st = (kv + tile_of(j)) % kStages;
-        const uint64_t ka = k_desc + st * (S::kTile / 16);
+      // Job i is tile i / 2 for A or B (pair), or tile i for one of them.
+      auto tile_of = [&](int i) { return pair ? i >> 1 : i; };
+      auto full = [&](uint64_t* bars, int i) {  // K or V of job i
+        const int t = kv + tile_of(i);
+        if (!pair || !(i & 1)) ok = ok && warp_wait(&bars[t % kStages], (t / kStages) & 1);
+      };
+      auto scores = [&](int i) {  // S = Q K^T
+        const int a = i & 1, st = (kv + tile_of(i)) % kStages;
+        const uint64_t qa = q_desc + (pair ? a : 0) * (S::kQ / 16), ka = k_desc + st * (S::kTile / 16);
+        const uint32_t d = tm + a * kCols;
         if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < kSteps; ++s)
-            mma_ss(t_s, q_desc + ((s >> 2) * kRows * 128 + (s & 3) * 32) / 16,
+            mma_ss(d, qa + ((s >> 2) * kRows * 128 + (s & 3) * 32) / 16,
                    ka + ((s >> 2) * kCols * 128 + (s & 3) * 32) / 16, id_s, s > 0);
           mma_commit(&bar.s_full[a]);
-          mma_commit(&bar.k_empty[st]);
+          if (!pair || a == 1) mma_commit(&bar.k_empty[st]);
         }
         __syncwarp();
       };
-      auto full = [&](uint64_t* bars, int j) {
-        const int t = kv + tile_of(j);
-        return warp_wait(&bars[t % kStages], (t / kStages) & 1);
-      };
       ok = warp_wait(&bar.q_full, seg_no & 1);
       tmem_fence_after();
-      if (jobs > 0) {
-        ok = ok && full(bar.k_full, 0);
-        if (ok) scores(0);
+      for (int i = 0; i < 2 && i < jobs; ++i) {
+        full(bar.k_full, i);
+        if (ok) scores(i);
       }
-      for (int j = 0; j < jobs && ok; ++j) {
-        const int tile = tile_of(j), st = (kv + tile) % kStages;
-        if (!(ok = full(bar.v_full, j))) break;
-        const int steps = min(kCols / 16, (seg.cols - (seg.tile0 + tile) * kCols + 15) >> 4);
-        if (tile >= clean) {  // clean V where it may hold anything: a lane per column
-          const int col0 = (seg.tile0 + tile) * kCols;
+      for (int i = 0; i < jobs && ok; ++i) {
+        const int a = i & 1, tile = tile_of(i), st = (kv + tile) % kStages;
+        const int col0 = (seg.tile0 + tile) * kCols;
+        const int steps = min(kCols / 16, (seg.cols - col0 + 15) >> 4);
+        if (tile >= clean && (!pair || a == 0)) {
+          full(bar.v_full, i);
+          if (!ok) break;
+          // clean V where it may hold anything: a lane per column (steps of 16 columns behind the
+          // last are left out of the product)
           char* vt = smem + S::v + st * S::kTile;
-          // (steps of 16 columns behind the last are left out of the product)
-          for (int c = max(0, seg.old - col0) + (pair ? a * 32 : 0) + lane; c < steps * 16;
-               c += pair ? 64 : 32) {
+          for (int c = max(0, seg.old - col0) + lane; c < steps * 16; c += 32) {
             const int node = col0 + c - seg.old;
             bool drop = node >= p.T || s_anc[node] == 0;
             if (!drop) {
@@ -271,36 +271,26 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
                 *reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)) = make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();
-          if (pair) named_bar_sync(4, 64);  // both have cleaned their half
-          else __syncwarp();
+          __syncwarp();
         }
-        if (j == jobs - 1 && lane == 0) arrive(&bar.v_clean);  // the segment's V has been seen
-        if (j + 1 < jobs && !(ok = full(bar.k_full, j + 1))) break;
+        if (i == jobs - 1 && lane == 0) arrive(&bar.v_clean);  // the segment's V has been seen
         const uint64_t va = v_desc + st * (S::kTile / 16);
-        if (!(ok = warp_wait(&bar.p_half[a], done & 1))) break;
+        const uint32_t d = tm + (2 + a) * kCols, w = tm + a * kCols;
+        // weights, and with them V and the next K: one wait per job
+        if (!(ok = warp_wait(&bar.p_ready[a], done[a] & 1))) break;
+        ++done[a];
         tmem_fence_after();
         if (elect_one()) {
-          mma_ts(t_o, t_s, va, id_o, j > 0);
+          mma_ts(d, w, va, id_o, i >= 2);
 #pragma unroll
-          for (int s = 1; s < kCols / 32; ++s)
-            if (s < steps) mma_ts(t_o, t_s + s * 8, va + s * (2048 / 16), id_o, true);
-          mma_commit(&bar.o_half[a]);
+          for (int s = 1; s < kCols / 16; ++s)
+            if (s < steps) mma_ts(d, w + s * 8, va + s * (2048 / 16), id_o, true);
+          if (!pair || a == 1) mma_commit(&bar.v_empty[st]);
+          if (i + 2 >= jobs) mma_commit(&bar.o_done[a]);
         }
         __syncwarp();
-        if (!(ok = warp_wait(&bar.p_ready[a], done & 1))) break;
-        ++done;
-        tmem_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int s = kCols / 32; s < kCols / 16; ++s)
-            if (s < steps) mma_ts(t_o, t_s + s * 8, va + s * (2048 / 16), id_o, true);
-          mma_commit(&bar.v_empty[st]);
-          if (j + 1 == jobs) mma_commit(&bar.o_done[a]);
-        }
-        __syncwarp();
-        if (j + 1 < jobs) scores(j + 1);
+        if (i + 2 < jobs) scores(i + 2);
       }
-      if (jobs == 0 && lane == 0) arrive(&bar.v_clean);
       kv += n;
     }
   }
@@ -317,7 +307,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     const uint32_t t_s = tmem + lane_base + a * kCols, t_o = tmem + lane_base + (2 + a) * kCols;
     // a scale of zero as the smallest one: hidden scores are -infinity and have to stay so
     const float scale = fmaxf(fabsf(p.scale_log2), 1.2e-38f);
-    int seg_no = 0, seen = 0, ends = 0;  // segments, jobs, accumulations so far
+    int seg_no = 0, seen = 0, ends = 0, kv = 0;  // segments, jobs, accumulations, tiles so far
     // A thread copies its 16-byte chunk of every kPer-th Q row straight to shared memory (rows that
     // do not exist are zero): holding them in registers over the segment before made the compiler
     // spill them, one round trip to memory each.  What the next segment will read is asked into L2.
@@ -386,7 +376,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           const int base = (seg.tile0 + (two ? j : 2 * j + a)) * kCols - seg.old;
           // Half of the columns at a time, in one pass with the maximum so far: weights are taken
           // against it while the half's own maximum is found, and only where that is too large are
-          // they taken again.  The first half enters the product while the second is weighed.
+          // they taken again.
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t w[2][16];
@@ -429,11 +419,18 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
               const float f = up ? ex2(m - mn) : 1.f;
               l *= f;
               m = mn;
-              if (hf == 1) {  // the first half's product is on its way into O
-                ok = warp_wait(&bar.o_half[a], seen & 1);
-                tmem_fence_after();
+              if (hf == 1) {  // the first half's weights, not yet in the product (rounded once more, where rarely needed)
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                  uint32_t u[16];
+                  tmem_ld16(t_s + c * 16, u);
+                  tmem_wait_ld16(u);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) u[k] = bf16_pack(bf16_lo(u[k]) * f, bf16_hi(u[k]) * f);
+                  tmem_st16(t_s + c * 16, u);
+                }
               }
-              if (j > 0 || hf == 1) {
+              if (j > 0) {
 #pragma unroll 1
                 for (int c = 0; c < HD / 16; ++c) {
                   uint32_t o[16];
@@ -452,14 +449,18 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
             const float2 both = unpack2(add2(sum[0], sum[1]));
             l += both.x + both.y;
             tmem_wait_st();
-            tmem_fence_before();
-            if (hf == 0) arrive(&bar.p_half[a]);
           }
-        } else {
-          arrive(&bar.p_half[a]);
+          tmem_fence_before();
+        }
+        {  // this tile's V, and the K of this accumulator's next one
+          const int t = kv + (two ? j : 2 * j + a), next = t + (two ? 1 : 2);
+          if (r == 0) ok = wait(&bar.v_full[t % kStages], (t / kStages) & 1);
+          if (r == 32 && j + 1 < jobs) ok = wait(&bar.k_full[next % kStages], (next / kStages) & 1);
+          ok = __all_sync(0xffffffffu, ok);
         }
         arrive(&bar.p_ready[a]);
       }
+      kv += n;
       // ----------------------------------------------------------------------------- output
       // Every score of both accumulators has been read, so Q may be replaced: the next segment is
       // opened, and its first products run, before this one is written out.
