@@ -374,89 +374,76 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         if (!idle) {
           tmem_fence_after();
           const int base = (seg.tile0 + (two ? j : 2 * j + a)) * kCols - seg.old;
-          // Half of the columns at a time, in one pass with the maximum so far: weights are taken
-          // against it while the half's own maximum is found, and only where that is too large are
-          // they taken again.
+          // One pass with the maximum so far: weights are taken against it while the tile's own
+          // maximum is found, and only where that is too large are they taken again.
+          uint32_t w[4][16];
+          uint64_t sum[2];
+          float mx;
+          auto weigh = [&] {
+            const float off = m == -INFINITY ? 0.f : m;
+            const uint64_t scale2 = pack2(scale, scale), off2 = pack2(-off, -off);
+            float top[2] = {-INFINITY, -INFINITY};
+            sum[0] = sum[1] = 0;
+            uint32_t s[2][32];
+            tmem_ld32(t_s, s[0]);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t w[2][16];
-            uint64_t sum[2];
-            float mx;
-            auto weigh = [&] {
-              const float off = m == -INFINITY ? 0.f : m;
-              const uint64_t scale2 = pack2(scale, scale), off2 = pack2(-off, -off);
-              float top[2] = {-INFINITY, -INFINITY};
-              sum[0] = sum[1] = 0;
-              uint32_t s[2][32];
-              tmem_ld32(t_s + hf * 64, s[0]);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t(&v)[32] = s[c & 1];
+              tmem_wait_ld32(v);
+              if (c < 3) tmem_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
+              if (base + kCols > 0) {
+                const uint32_t vis = visible32(anc, base + c * 32);
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t(&v)[32] = s[c];
-                tmem_wait_ld32(v);
-                if (c == 0) tmem_ld32(t_s + hf * 64 + 32, s[1]);
-                if (base + kCols > 0) {
-                  const uint32_t vis = visible32(anc, base + hf * 64 + c * 32);
-#pragma unroll
-                  for (int k = 0; k < 32; ++k)
-                    if (!(vis >> k & 1)) v[k] = __float_as_uint(-INFINITY);
-                }
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  top[k & 1] = fmaxf(top[k & 1], fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
-                  const float2 z = unpack2(fma2(pack2u(v[2 * k], v[2 * k + 1]), scale2, off2));
-                  const float e0 = ex2(z.x), e1 = ex2(z.y);
-                  sum[k & 1] = add2(sum[k & 1], pack2(e0, e1));
-                  // rounded to bf16: with V in bf16 the product takes nothing wider
-                  w[c][k] = bf16_pack(e0, e1);
-                }
+                for (int k = 0; k < 32; ++k)
+                  if (!(vis >> k & 1)) v[k] = __float_as_uint(-INFINITY);
               }
-              mx = fmaxf(top[0], top[1]) * scale;
-            };
-            weigh();
-            const bool up = mx > m + kGrow || (m == -INFINITY && mx > m);
-            if (__any_sync(0xffffffffu, up)) {
-              const float mn = up ? mx : m;
-              const float f = up ? ex2(m - mn) : 1.f;
-              l *= f;
-              m = mn;
-              if (hf == 1) {  // the first half's weights, not yet in the product (rounded once more, where rarely needed)
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                  uint32_t u[16];
-                  tmem_ld16(t_s + c * 16, u);
-                  tmem_wait_ld16(u);
 #pragma unroll
-                  for (int k = 0; k < 16; ++k) u[k] = bf16_pack(bf16_lo(u[k]) * f, bf16_hi(u[k]) * f);
-                  tmem_st16(t_s + c * 16, u);
-                }
+              for (int k = 0; k < 16; ++k) {
+                top[k & 1] = fmaxf(top[k & 1], fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+                const float2 z = unpack2(fma2(pack2u(v[2 * k], v[2 * k + 1]), scale2, off2));
+                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                sum[k & 1] = add2(sum[k & 1], pack2(e0, e1));
+                // rounded to bf16: with V in bf16 the product takes nothing wider
+                w[c][k] = bf16_pack(e0, e1);
               }
-              if (j > 0) {
-#pragma unroll 1
-                for (int c = 0; c < HD / 16; ++c) {
-                  uint32_t o[16];
-                  tmem_ld16(t_o + c * 16, o);
-                  tmem_wait_ld16(o);
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                  tmem_st16(t_o + c * 16, o);
-                }
-              }
-              weigh();
             }
-            // the weights go over scores that have been read
-            tmem_st16(t_s + hf * 32, w[0]);
-            tmem_st16(t_s + hf * 32 + 16, w[1]);
-            const float2 both = unpack2(add2(sum[0], sum[1]));
-            l += both.x + both.y;
-            tmem_wait_st();
+            mx = fmaxf(top[0], top[1]) * scale;
+          };
+          weigh();
+          const bool up = mx > m + kGrow || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, up)) {
+            const float mn = up ? mx : m;
+            const float f = up ? ex2(m - mn) : 1.f;
+            l *= f;
+            m = mn;
+            if (j > 0) {
+#pragma unroll 1
+              for (int c = 0; c < HD / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(t_o + c * 16, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st16(t_o + c * 16, o);
+              }
+            }
+            weigh();
           }
-          tmem_fence_before();
+          // the weights go over scores that have been read
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, w[c]);
+          const float2 both = unpack2(add2(sum[0], sum[1]));
+          l += both.x + both.y;
         }
         {  // this tile's V, and the K of this accumulator's next one
           const int t = kv + (two ? j : 2 * j + a), next = t + (two ? 1 : 2);
           if (r == 0) ok = wait(&bar.v_full[t % kStages], (t / kStages) & 1);
           if (r == 32 && j + 1 < jobs) ok = wait(&bar.k_full[next % kStages], (next / kStages) & 1);
           ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!idle) {
+          tmem_wait_st();
+          tmem_fence_before();
         }
         arrive(&bar.p_ready[a]);
       }
