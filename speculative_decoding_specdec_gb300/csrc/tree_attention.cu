@@ -645,7 +645,7 @@ AttnShape attn_shape(int es, int T, int G, int hd) {
   s.groups = std::max(1, sm_count() * per_sm / s.MT);
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
   s.min_tiles = 1;
-  s.open = s.kind == kTc ? 6 : 3;
+  s.open = s.kind == kTc ? (T * G > 128 ? 6 : 4) : 3;
   return s;
 }
 

@@ -6,7 +6,7 @@
 // softmax runs while the tensor cores work for the other.
 //   warps 0-3, 4-7  softmax of A, B: one thread per row reads its 128 scores from tensor memory,
 //                   keeps maximum and sum, writes the weights back as bf16 over the scores;
-//   warp 8          TMA: K and V tiles of 128 columns into two stages each (128-byte swizzle);
+//   warps 8, 10     TMA: K, V tiles of 128 columns into two stages or three (128-byte swizzle);
 //   warp 9          one thread issues S = Q K^T (both operands in shared memory) and
 //                   O += P V (P from tensor memory, V as it lies: MN-major).
 // Tensor memory (512 columns): S/P of A and B, O of A and B, 128 columns each.
@@ -27,12 +27,13 @@ namespace specdec {
 
 namespace {
 
-constexpr int kThreads = 384;  // (the last two warps only complete the third warpgroup)
+constexpr int kThreads = 384;  // (the last warp only completes the third warpgroup)
 // Registers per thread: 384 x 168 at launch; 2 x 128 x 224 + 128 x 56 = those 64512.
 constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 constexpr int kCols = 128;     // columns of a K/V tile
 constexpr int kRows = 128;     // rows of an accumulator
-constexpr int kStages = 2;
+constexpr int kStages = 2;      // of V, and of K where A and B are different rows; else K has one more
+constexpr int kMaxKStages = 3;
 constexpr uint32_t kTries = 1u << 18;  // polls after which a wait gives up
 constexpr float kGrow = 32.f;  // log2 of the growth of the maximum that is let pass
 
@@ -62,7 +63,7 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 }
 
 struct Bars {
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kMaxKStages], k_empty[kMaxKStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2];
 };
 
@@ -100,6 +101,8 @@ template <int HD> struct Smem {
   static constexpr int q = 0;                          // A's rows, then B's
   static constexpr int k = 2 * kQ, v = k + kStages * kTile;
   static constexpr int bytes = v + kStages * kTile + 1024;  // and alignment to 1024
+  // K's stage i: the third is where B's rows of Q would be
+  __host__ __device__ static constexpr int k_stage(int i) { return i < kStages ? k + i * kTile : kQ; }
 };
 
 // Byte offset of 16-byte chunk `c` of row `r` in a [rows][HD] bf16 tile: panels of 64 values,
@@ -135,9 +138,11 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   if (warp == 0) attn_plan(p, kCols, plan);
   if (warp == 9) tmem_alloc(&s_tmem, 512);
   if (tid == 32) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxKStages; ++i) {
       mbar_init(&bar.k_full[i], 1);
       mbar_init(&bar.k_empty[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.v_full[i], 1);
       mbar_init(&bar.v_empty[i], 1);
     }
@@ -159,41 +164,37 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   const AttnShares sh = attn_shares(p, plan);
   const bool work = sh.total > 0 && g < sh.groups;
   const int x0 = work ? sh.start(g) : 0, x1 = work ? sh.start(g + 1) : 0;
+  const int nk = two ? kStages : kMaxKStages;
   bool ok = true;
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-  if (warp == 8) {
+  if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------------------------- TMA
+    // Warp 8 for K, warp 10 for V: one for both would hold K back until a stage of V is free.
     if (lane == 0) {
-      int kv = 0;  // tiles so far
+      const bool is_v = warp == 10;
+      const int stages = is_v ? kStages : nk;
+      uint64_t *full = is_v ? bar.v_full : bar.k_full, *empty = is_v ? bar.v_empty : bar.k_empty;
+      int n = 0;  // tiles so far
       AttnSegment seg;
       for (int x = x0; ok && attn_next(p, plan, x, x1, seg); x = seg.next) {
         const int crow = p.one_row ? 0 : seg.b;
-        for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++kv) {
-          const int st = kv % kStages, col = seg.first + tile * kCols;
-          const uint32_t ph = (kv / kStages) & 1;
-          if (!(ok = wait(&bar.k_empty[st], ph ^ 1))) break;
-          mbar_arrive_expect_tx(&bar.k_full[st], S::kTile);
-          for (int j = 0; j < kPanels; ++j)
-            tma_load_5d(smem + S::k + st * S::kTile + j * kCols * 128, &map, j * 64, col, seg.h,
-                        crow, 0, &bar.k_full[st]);
+        for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
+          const int st = n % stages, col = seg.first + tile * kCols;
           // the first product needs K and Q: what comes after must not stand before Q in the queue
-          if (kv == 0 && !(ok = wait(&bar.q_full, 0))) break;
-          if (!(ok = wait(&bar.v_empty[st], ph ^ 1))) break;
-          mbar_arrive_expect_tx(&bar.v_full[st], S::kTile);
+          if (n == (is_v ? 0 : 1) && !(ok = wait(&bar.q_full, 0))) break;
+          if (!(ok = wait(&empty[st], ((n / stages) & 1) ^ 1))) break;
+          mbar_arrive_expect_tx(&full[st], S::kTile);
+          char* to = smem + (is_v ? S::v + st * S::kTile : S::k_stage(st));
           for (int j = 0; j < kPanels; ++j)
-            tma_load_5d(smem + S::v + st * S::kTile + j * kCols * 128, &map, j * 64, col, seg.h,
-                        crow, 1, &bar.v_full[st]);
+            tma_load_5d(to + j * kCols * 128, &map, j * 64, col, seg.h, crow, is_v, &full[st]);
         }
       }
       // no copy outlives the CTA: the last ones issued have landed (their tiles were used) unless
       // a wait gave up
       if (!ok)
-        for (int i = max(0, kv - kStages); i <= kv; ++i) {
-          (void)wait(&bar.k_full[i % kStages], (i / kStages) & 1);
-          (void)wait(&bar.v_full[i % kStages], (i / kStages) & 1);
-        }
+        for (int i = max(0, n - stages); i < n; ++i) (void)wait(&full[i % stages], (i / stages) & 1);
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------------------- MMA
@@ -209,7 +210,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t sm = __shfl_sync(0xffffffffu, smem_addr(smem), 0);
     const bool pair = __shfl_sync(0xffffffffu, two ? 1 : 0, 0) != 0;
-    const uint64_t q_desc = mma_desc(sm + S::q, 16, 1024), k_desc = mma_desc(sm + S::k, 16, 1024),
+    const uint64_t q_desc = mma_desc(sm + S::q, 16, 1024), k_desc = mma_desc(sm, 16, 1024),
                    v_desc = mma_desc(sm + S::v, kCols * 128, 1024);
     int kv = 0, seg_no = 0, done[2] = {0, 0};  // tiles, segments, jobs of A and B so far
     AttnSegment seg;
@@ -218,13 +219,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       const int clean = seg.old / kCols - seg.tile0;  // the first tile that needs care
       // Job i is tile i / 2 for A or B (pair), or tile i for one of them.
       auto tile_of = [&](int i) { return pair ? i >> 1 : i; };
-      auto full = [&](uint64_t* bars, int i) {  // K or V of job i
+      auto full = [&](uint64_t* bars, int stages, int i) {  // K or V of job i
         const int t = kv + tile_of(i);
-        if (!pair || !(i & 1)) ok = ok && warp_wait(&bars[t % kStages], (t / kStages) & 1);
+        if (!pair || !(i & 1)) ok = ok && warp_wait(&bars[t % stages], (t / stages) & 1);
       };
       auto scores = [&](int i) {  // S = Q K^T
-        const int a = i & 1, st = (kv + tile_of(i)) % kStages;
-        const uint64_t qa = q_desc + (pair ? a : 0) * (S::kQ / 16), ka = k_desc + st * (S::kTile / 16);
+        const int a = i & 1, st = pair ? (kv + (i >> 1)) % kStages : (kv + i) % kMaxKStages;
+        const uint64_t qa = q_desc + (pair ? a : 0) * (S::kQ / 16), ka = k_desc + S::k_stage(st) / 16;
         const uint32_t d = tm + a * kCols;
         if (elect_one()) {
 #pragma unroll
@@ -239,7 +240,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       ok = warp_wait(&bar.q_full, seg_no & 1);
       tmem_fence_after();
       for (int i = 0; i < 2 && i < jobs; ++i) {
-        full(bar.k_full, i);
+        full(bar.k_full, nk, i);
         if (ok) scores(i);
       }
       for (int i = 0; i < jobs && ok; ++i) {
@@ -247,7 +248,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         const int col0 = (seg.tile0 + tile) * kCols;
         const int steps = min(kCols / 16, (seg.cols - col0 + 15) >> 4);
         if (tile >= clean && (!pair || a == 0)) {
-          full(bar.v_full, i);
+          full(bar.v_full, kStages, i);
           if (!ok) break;
           // clean V where it may hold anything: a lane per column (steps of 16 columns behind the
           // last are left out of the product)
@@ -438,7 +439,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         {  // this tile's V, and the K of this accumulator's next one
           const int t = kv + (two ? j : 2 * j + a), next = t + (two ? 1 : 2);
           if (r == 0) ok = wait(&bar.v_full[t % kStages], (t / kStages) & 1);
-          if (r == 32 && j + 1 < jobs) ok = wait(&bar.k_full[next % kStages], (next / kStages) & 1);
+          if (r == 32 && j + 1 < jobs) ok = wait(&bar.k_full[next % nk], (next / nk) & 1);
           ok = __all_sync(0xffffffffu, ok);
         }
         if (!idle) {
@@ -467,15 +468,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       if (more) open();
       // this row's sums, B's merged into A's where both hold parts of one row
       float fa = 1.f, fb = 0.f;
-      float* swap = reinterpret_cast<float*>(smem + S::q + S::kQ);  // [HD / 2][128], Q of B's rows
-      auto part = [&](int c, float (&o)[32]) {  // columns 32c .. of this accumulator's O
+      auto part = [&](uint32_t from, int c, float (&o)[32]) {  // columns 32c .. of an accumulator's O
         uint32_t u[32];
-        if (jobs > 0 && !idle) {
-          tmem_ld32(t_o + c * 32, u);
-          tmem_wait_ld32(u);
-        }
+        tmem_ld32(from + c * 32, u);
+        tmem_wait_ld32(u);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = jobs > 0 && !idle ? __uint_as_float(u[k]) : 0.f;
+        for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(u[k]);
       };
       const bool whole = now.tile0 == 0 && now.tile1 == now.tiles;
       const int slot = whole ? 0 : attn_slot(p, sh, g, mt, now.unit0);
@@ -508,49 +506,34 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
             w[k * 2 * kRows] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       };
-      if (two) {
+      // Tensor memory's lanes are a warp's by its place in the warpgroup, so A's threads reach B's O
+      // of the same rows themselves; only (m, l) has to be passed.
+      if (!two) {
+        if (a == 1) s_ml[r] = make_float2(m, l);
+        named_bar_sync(2, 256);
+        tmem_fence_after();
+        if (a == 0 && n > 1) {
+          const float2 b = s_ml[r];
+          const float mn = fmaxf(m, b.x), off = mn == -INFINITY ? 0.f : mn;
+          fa = ex2(m - off);
+          fb = ex2(b.x - off);
+          l = l * fa + b.y * fb;
+          m = mn;
+        }
+      }
+      if ((two || a == 0) && !idle)
 #pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
           float o[32];
-          part(c, o);
+          part(t_o, c, o);
+          if (!two && n > 1) {
+            float q[32];
+            part(t_o + kCols, c, q);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = o[k] * fa + q[k] * fb;
+          }
           emit(c, o);
         }
-      } else {
-        if (a == 1) s_ml[r] = make_float2(m, l);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (half) named_bar_sync(3, 256);  // A has read the first half
-          if (a == 1) {
-#pragma unroll 1
-            for (int c = 0; c < HD / 64; ++c) {
-              float o[32];
-              part(half * (HD / 64) + c, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) swap[(c * 32 + k) * kRows + r] = o[k];
-            }
-          }
-          named_bar_sync(2, 256);
-          if (a == 0) {
-            if (half == 0) {
-              const float2 b = s_ml[r];
-              const float mn = fmaxf(m, b.x), off = mn == -INFINITY ? 0.f : mn;
-              fa = ex2(m - off);
-              fb = ex2(b.x - off);
-              l = l * fa + b.y * fb;
-              m = mn;
-            }
-#pragma unroll 1
-            for (int c = 0; c < HD / 64; ++c) {
-              float o[32];
-              part(half * (HD / 64) + c, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                o[k] = o[k] * fa + swap[(c * 32 + k) * kRows + r] * fb;
-              emit(half * (HD / 64) + c, o);
-            }
-          }
-        }
-      }
       const bool owner = write && (two || a == 0);
       if (whole) {
         if (owner) store_lse(m, l);
