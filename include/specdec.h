@@ -615,8 +615,8 @@ int specdec_rotary_append(const specdec_rotary_args* args, void* stream);
  * Device-detected errors: N_b < 1, N_b > W, a negative row index or first column, a bad
  * parent (SPECDEC_ERR_INPUT_RANGE), a node's column beyond cache.cap_cols
  * (SPECDEC_ERR_CAPACITY); the row concerned is not written.
- * Limits: 0 <= B <= 1024, 1 <= T <= SPECDEC_MAX_TREE, heads_q a multiple of cache.heads, head_dim
- * a multiple of 16 bytes and at most 256, scale finite; q, out 16-byte aligned with strides that
+ * Limits: 0 <= B <= 1024, 1 <= T <= SPECDEC_MAX_TREE, heads_q a multiple of cache.heads with at most
+ * 65536 query rows (T * heads_q / cache.heads) per K/V head, head_dim a multiple of 16 bytes and at most 256, scale finite; q, out 16-byte aligned with strides that
  * are multiples of 16 bytes; out overlaps nothing else.
  */
 typedef struct {

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
         }
       }
     if (whole || s_bad) continue;
-    if (!attn_last(p, seg.b, seg.h, mt, g1 - g0 + 1, &s_flag)) continue;
+    if (!attn_last(p, g0, mt, g1 - g0 + 1, &s_flag)) continue;
     for (int k = tid; k < nrows * n4; k += threads) {
       const int r = k / n4, i = k - r * n4;
       auto at = [&](int j) { return static_cast<long long>(attn_slot(p, sh, g0 + j, mt, seg.unit0)) * R + r; };
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
         }
       }
       const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1);
-      const bool last = attn_last(p, seg.b, seg.h, mt, g1 - g0 + 1, &s_flag);
+      const bool last = attn_last(p, g0, mt, g1 - g0 + 1, &s_flag);
       if (!last) continue;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -596,6 +596,7 @@ struct AttnShape {
   int kind;
 };
 enum { kFma = 0, kMma = 1, kTc = 2 };
+constexpr long long kFewColumns = 128 << 10;
 
 // Rows per M-tile, CTAs and shares of a shape; 0 CTAs if there is no device.
 AttnShape fma_shape(int es, int T, int G, int hd) {
@@ -628,36 +629,45 @@ AttnShape fma_shape(int es, int T, int G, int hd) {
   return s;
 }
 
-// The kernel and its shape for bf16 heads of 64 and 128 values: 16-row or 256-row tiles on the
-// tensor cores, by the number of query rows.
-AttnShape attn_shape(int es, int T, int G, int hd) {
+// The kernel and its shape for bf16 heads of 64 and 128 values: tiles of 8 or 16 query rows, or of
+// 256.  Up to 16 rows the former, whose tiles the latter would leave nearly empty; up to 32 rows it
+// is ahead on short work (2 rows of 100 columns, 8 K/V heads: 8.8 us in one launch against 9.0 in
+// two) and behind on long (16 rows of up to 4096 columns, 8 K/V heads: 47 us against 43).
+// `columns`: an upper bound of the columns of all units.
+AttnShape attn_shape(int es, int T, int G, int hd, long long columns) {
   if (es != 2 || (hd != 64 && hd != 128)) return fma_shape(es, T, G, hd);
   AttnShape s = {};
   int per_sm = 1;
-  if (T * G <= 32) {
+  if (T * G <= 16 || (T * G <= 32 && columns <= kFewColumns)) {
     s.kind = kMma;
     attn_mma_shape(T * G, hd, &s.M, &s.MT, &s.tile, &per_sm);
+    s.open = 3;
   } else {
     s.kind = kTc;
     attn_tc_shape(T * G, &s.M, &s.MT);
     s.tile = 128;
+    s.open = T * G > 128 ? 6 : 4;
   }
   s.groups = std::max(1, sm_count() * per_sm / s.MT);
   s.grid = sm_count() > 0 ? s.groups * s.MT : 0;
   s.min_tiles = 1;
-  s.open = s.kind == kTc ? (T * G > 128 ? 6 : 4) : 3;
   return s;
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
+// The tickets come first and take the same room whatever the shape, so that no shape's other data
+// ever lies where another expects zeros.
+constexpr size_t kTicketBytes = 32 << 10;
+constexpr int kMaxQueries = 65536;  // query rows per K/V head
+
 struct AttnWorkspace {
   size_t ticket, cuts, ml, o, bytes;  // offsets
 };
-AttnWorkspace attn_workspace(const AttnShape& s, int B, int H, int hd) {
+AttnWorkspace attn_workspace(const AttnShape& s, int hd) {
   AttnWorkspace w;
   w.ticket = 0;
-  w.cuts = round256(static_cast<size_t>(B) * H * s.MT * 4);
+  w.cuts = kTicketBytes;
   w.ml = w.cuts + round256(static_cast<size_t>(s.groups) * 16);
   w.o = w.ml + round256(static_cast<size_t>(s.grid) * 2 * s.M * 8);
   w.bytes = w.o + round256(static_cast<size_t>(s.grid) * 2 * s.M * hd * 4);
@@ -686,7 +696,7 @@ bool attn_sizes_ok(int dtype, int B, int T, int heads_q, int heads_kv, int head_
   const int es = elem_size(dtype);
   return es != 0 && B >= 1 && B <= kAttnMaxRows && T >= 1 && T <= SPECDEC_MAX_TREE &&
          heads_kv >= 1 && heads_q >= heads_kv && heads_q % heads_kv == 0 && head_dim >= 1 &&
-         head_dim <= 256 && head_dim * es % 16 == 0 && heads_q <= 65536;
+         head_dim <= 256 && head_dim * es % 16 == 0 && heads_q / heads_kv <= kMaxQueries / T;
 }
 
 }  // namespace
@@ -696,8 +706,12 @@ extern "C" size_t specdec_tree_attention_workspace(int dtype, int B, int T, int 
                                                    int heads_kv, int head_dim) {
   using namespace specdec;
   if (!attn_sizes_ok(dtype, B, T, heads_q, heads_kv, head_dim)) return 0;
-  const AttnShape s = attn_shape(elem_size(dtype), T, heads_q / heads_kv, head_dim);
-  return attn_workspace(s, B, heads_kv, head_dim).bytes;
+  size_t most = 0;  // of the kernels that the lengths may decide for
+  for (const long long columns : {0LL, kFewColumns + 1}) {
+    const AttnShape s = attn_shape(elem_size(dtype), T, heads_q / heads_kv, head_dim, columns);
+    most = std::max(most, attn_workspace(s, head_dim).bytes);
+  }
+  return most;
 }
 
 extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void* stream) {
@@ -730,13 +744,15 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   if (reinterpret_cast<uintptr_t>(a->workspace) % 256) return SPECDEC_ERR_INVALID_ARG;
   if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
   const int G = a->heads_q / c.heads;
-  AttnShape s = attn_shape(static_cast<int>(es), a->T, G, c.head_dim);
+  AttnShape s = attn_shape(static_cast<int>(es), a->T, G, c.head_dim,
+                           static_cast<long long>(a->B) * c.heads * c.cap_cols);
   // no more groups than the longest rows could give work to
   const long long tiles = static_cast<long long>(a->B) * c.heads * ((c.cap_cols - 1) / s.tile + 1 + s.open);
   s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
   s.grid = s.groups * s.MT;
-  const AttnWorkspace w = attn_workspace(s, a->B, c.heads, c.head_dim);
+  const AttnWorkspace w = attn_workspace(s, c.head_dim);
   if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
+  if (s.grid > static_cast<int>(kTicketBytes / 4)) return SPECDEC_ERR_UNSUPPORTED;
   if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kCols + 16) >= (1LL << 31))
     return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   AttnParams p = {};

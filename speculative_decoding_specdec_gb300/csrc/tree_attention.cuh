@@ -31,7 +31,7 @@ struct AttnParams {
   long long qr, qt, outr, outt;  // bytes between rows and tokens
   const int32_t *n_committed, *width, *parents, *rows, *first_col;
   int32_t* status;
-  unsigned* ticket;  // [B * H * MT], zero between calls
+  unsigned* ticket;  // [groups * MT], zero between calls
   float2* part_ml;   // [grid * 2][M]
   float* part_o;     // [grid * 2][M][hd]
   int4* cuts;        // [groups], tensor-core kernel: the units that borders cut
@@ -179,14 +179,14 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& p
   return false;
 }
 
-// Takes a ticket of the unit's M-tile mt; true in every thread for the CTA that took the last one
-// (the partial results of all are then visible to it).  n: CTAs that share the unit.
-__device__ __forceinline__ bool attn_last(const AttnParams& p, int b, int h, int mt, int n,
-                                          int* s_flag) {
+// Takes a ticket of a cut unit's M-tile mt; true in every thread for the CTA that took the last one
+// (the partial results of all are then visible to it).  n: CTAs that share the unit, the first of
+// them of share g0, which names the ticket: a share is the first of one cut unit at most.
+__device__ __forceinline__ bool attn_last(const AttnParams& p, int g0, int mt, int n, int* s_flag) {
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    unsigned* t = &p.ticket[(static_cast<long long>(b) * p.H + h) * p.MT + mt];
+    unsigned* t = &p.ticket[g0 * p.MT + mt];
     const unsigned old = atomicAdd(t, 1u);
     *s_flag = old + 1 == static_cast<unsigned>(n);
     if (*s_flag) *t = 0;

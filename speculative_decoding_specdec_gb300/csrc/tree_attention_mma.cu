@@ -369,7 +369,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       }
       if (s_bad) continue;
       const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1);
-      if (!attn_last(p, seg.b, seg.h, mt, g1 - g0 + 1, &s_flag)) continue;
+      if (!attn_last(p, g0, mt, g1 - g0 + 1, &s_flag)) continue;
       mm = -INFINITY;
       ll = 0.f;
 #pragma unroll

@@ -201,6 +201,24 @@ def test_workspace_is_reused_and_results_repeat():
             np.testing.assert_array_equal(got, want)
 
 
+def test_one_workspace_for_shapes_of_any_size():
+    """What one shape leaves in the workspace (cut units' parts of long rows) disturbs no other, with
+    many or few units, rows and splits, in either direction."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    rng = np.random.default_rng(4)
+    shapes = [(1, 64, 16, 1, 128, 6000, torch.bfloat16), (24, 1, 16, 16, 128, 700, torch.bfloat16), (1, 2, 4, 1, 64, 3000, torch.float32),
+              (16, 2, 32, 8, 64, 900, torch.bfloat16), (2, 20, 4, 4, 128, 1200, torch.bfloat16), (8, 1, 8, 8, 128, 500, torch.float32)]
+    made = [inputs(rng, B, T, Hq, H, hd, np.full(B, n), dt) + (np.full(B, n),) for B, T, Hq, H, hd, n, dt in shapes]
+    ws = torch.zeros(max(sd.tree_attention_workspace_bytes(q, c) for q, c, _, _ in made), dtype=torch.uint8, device=DEV)
+    want = [run(q, c, 1, n, W, None)[0] for q, c, W, n in made]
+    for order in (range(6), reversed(range(6)), (0, 1, 0, 3, 2, 5, 4, 1)):
+        for i in order:
+            q, c, W, n = made[i]
+            got, _, st = run(q, c, 1, n, W, None, ws=ws)
+            assert st == 0
+            np.testing.assert_array_equal(got, want[i])
+
+
 def test_strides_layers_and_another_stream():
     import speculative_decoding_specdec_gb300.specdec as sd
     rng = np.random.default_rng(5)
