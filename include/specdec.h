@@ -674,7 +674,7 @@ int specdec_verify_tree_greedy(const void* logits, int dtype, int B, int T, int 
  * min(1, p(x)/q(x)), after a rejection go on with normalize(max(0, p - q)).]
  *   target_logits, draft_logits [B][T][row_stride]: p = softmax(target row / temperature) and
  *   q = softmax(draft row / temperature) of the distribution after each node; draft rows of nodes
- *   without children are not read.
+ *   without children are not used.
  * The walk starts at node 0.  At a node its children c are tried in order: child i (token x) is
  * accepted iff u[b][i] < p(x) / q(x) and the walk goes on there; otherwise p becomes
  * normalize(max(0, p - q)) (p stays where that is zero everywhere) and, unless `replacement`, q

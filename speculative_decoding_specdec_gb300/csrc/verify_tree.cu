@@ -30,6 +30,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
+static_assert(kMaxCluster <= kWarps, "a warp per CTA sums its records");
 constexpr int kUnroll = 4;  // 16-byte loads in flight per thread
 
 struct TreeParams {
@@ -63,12 +64,25 @@ __device__ __forceinline__ int next_child(const Walk& w, int T, int cur, int las
   return T;
 }
 
-// Load and check the tree.  Returns false (in every CTA of the cluster) where it is bad.
-__device__ bool load_tree(const TreeParams& p, int b, Walk& w) {
+// A node's parent and token on their way from memory (thread = node).
+struct NodeLoad {
+  int par, tok;
+};
+__device__ __forceinline__ NodeLoad ask_tree(const TreeParams& p, int b) {
+  const int i = threadIdx.x;
+  NodeLoad n{i - 1, 0};
+  if (i < p.T) {
+    if (p.parents) n.par = __ldg(p.parents + b * p.T + i);
+    n.tok = __ldg(p.tokens + b * p.T + i);
+  }
+  return n;
+}
+// The tree in shared memory, checked.  Returns false (in every CTA of the cluster) where it is bad.
+__device__ __forceinline__ bool place_tree(const TreeParams& p, NodeLoad n, Walk& w) {
   const int i = threadIdx.x;
   if (i < p.T) {
-    w.par[i] = p.parents ? p.parents[b * p.T + i] : i - 1;
-    w.tok[i] = p.tokens[b * p.T + i];
+    w.par[i] = n.par;
+    w.tok[i] = n.tok;
   }
   __syncthreads();
   bool bad = false;
@@ -144,8 +158,7 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
   constexpr int VN = Vec<T>::N;
   __shared__ Walk w;
   __shared__ Exchange x;
-  __shared__ unsigned long long s_warp[kWarps];
-  __shared__ unsigned long long s_rec[2][kMaxCluster];
+  __shared__ unsigned long long s_rec[2][kAll ? 1 : kMaxCluster * kWarps];  // a key of every warp of the cluster
   __shared__ unsigned long long s_all[kAll ? kMaxTree : 1][kMaxCluster];
   __shared__ int s_choice[kMaxTree];
   const int rank = static_cast<int>(cluster_rank()), b = blockIdx.x / p.C;
@@ -155,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
     mbar_init(&x.bar[1], 1);
     fence_mbar_init();
   }
-  const bool ok = load_tree(p, b, w);
+  const NodeLoad node = ask_tree(p, b);
   const T* rows = static_cast<const T*>(p.target) + static_cast<long long>(b) * p.T * p.row_stride;
   const int vecs = (p.V + VN - 1) / VN, v0 = slice_start(vecs, rank, p.C), v1 = slice_start(vecs, rank + 1, p.C);
   // the best of a row's vectors [v0, v1), taken `step` apart from v0 + first by this thread
@@ -177,6 +190,9 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
     }
     return warp_max(bi >= 0 && bi < p.V ? make_key(bv, bi) : 0ull);
   };
+  unsigned long long key = 0;
+  if (!kAll) key = best(rows, tid, kThreads);  // the root's row, while the tree is on its way
+  const bool ok = place_tree(p, node, w);
   cluster_sync_all();  // every CTA of the cluster has started: its shared memory may be written
   bool alive = true;
   int a = 0, token = -1;
@@ -184,12 +200,12 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
     if (kAll) {
       exchange_expect(x, 0, p.T * p.C * 8);
       for (int i = warp; i < p.T; i += kWarps) {
-        const unsigned long long key = w.par[i] == kUnusedNode ? 0ull : best(rows + i * p.row_stride, lane, 32);
-        if (lane < p.C) cluster_send(cluster_map(&s_all[i][rank], lane), key, cluster_map(&x.bar[0], lane));
+        const unsigned long long mine = w.par[i] == kUnusedNode ? 0ull : best(rows + i * p.row_stride, lane, 32);
+        if (lane < p.C) cluster_send(cluster_map(&s_all[i][rank], lane), mine, cluster_map(&x.bar[0], lane));
       }
       alive = exchange_wait(x, 0);
       if (alive && tid < p.T) {
-        unsigned long long key = s_all[tid][0];
+        key = s_all[tid][0];
         for (int r = 1; r < p.C; ++r) key = max(key, s_all[tid][r]);
         s_choice[tid] = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
       }
@@ -200,18 +216,15 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
       if (kAll) {
         choice = s_choice[cur];
       } else {
-        exchange_expect(x, n, p.C * 8);
-        unsigned long long key = best(rows + cur * p.row_stride, tid, kThreads);
-        if (lane == 0) s_warp[warp] = key;
-        __syncthreads();
-        if (warp == 0) {
-          key = warp_max(lane < kWarps ? s_warp[lane] : 0ull);
-          if (lane < p.C)
-            cluster_send(cluster_map(&s_rec[n & 1][rank], lane), key, cluster_map(&x.bar[n & 1], lane));
-        }
-        if (!(alive = exchange_wait(x, n))) break;
-        key = s_rec[n & 1][0];
-        for (int r = 1; r < p.C; ++r) key = max(key, s_rec[n & 1][r]);
+        // every warp's key to every CTA, and all of them reduced by every warp
+        exchange_expect(x, n, p.C * kWarps * 8);
+        if (n > 0) key = best(rows + cur * p.row_stride, tid, kThreads);
+        if (lane < p.C)
+          cluster_send(cluster_map(&s_rec[n & 1][rank * kWarps + warp], lane), key, cluster_map(&x.bar[n & 1], lane));
+        if (!(alive = __all_sync(0xffffffffu, exchange_wait(x, n)))) break;
+        key = 0;
+        for (int i = lane; i < p.C * kWarps; i += 32) key = max(key, s_rec[n & 1][i]);
+        key = warp_max(key);
         choice = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
       }
       if (choice < 0) {  // only NaN
@@ -229,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
       cur = next;
     }
   }
-  __syncthreads();
+  alive = __syncthreads_and(alive) != 0;
   if (!ok || !alive) {
     if (rank == 0 && tid == 0) set_status(p.status, ok ? SPECDEC_ERR_TIMEOUT : SPECDEC_ERR_INPUT_RANGE);
   } else if (rank == 0) {
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
   __shared__ Stage st;
   __shared__ Exchange x;
   __shared__ float s_u[kMaxTree], s_zt[kMaxTree], s_zq[kMaxTree];
-  __shared__ float4 s_warp[kWarps], s_rec[2][kMaxCluster];
+  __shared__ float4 s_rec[2][kMaxCluster * kWarps];  // a record of every warp of the cluster
   __shared__ float s_mass[kMaxCluster];  // each CTA's share of p's mass, not normalised
   __shared__ float s_entry[kRuns * kWarps];
   extern __shared__ uint4 hold[];  // kKeep: [2][kHold]
@@ -365,7 +378,24 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
     mbar_init(&x.bar[1], 1);
     fence_mbar_init();
   }
-  bool ok = load_tree(p, b, w);
+  const NodeLoad node = ask_tree(p, b);
+  const int vecs = (p.V + VN - 1) / VN, v0 = slice_start(vecs, rank, p.C), v1 = slice_start(vecs, rank + 1, p.C);
+  const T *zt = target, *zq = drafts;
+  bool inner = p.T > 1;
+  auto load = [&] {  // a thread copies what it will read
+    for (int v = v0 + tid; v < v1; v += kThreads) {
+      const int i = v - v0;
+      if (p.vec && (v + 1) * VN <= p.V) {
+        cp_async16(hold + i, zt + static_cast<long long>(v) * VN, true);
+        if (inner) cp_async16(hold + kHold + i, zq + static_cast<long long>(v) * VN, true);
+      } else {
+        hold[i] = load_scores(zt, v, p.V, p.vec);
+        if (inner) hold[kHold + i] = load_scores(zq, v, p.V, p.vec);
+      }
+    }
+  };
+  if (kKeep) load();  // the root's rows, while the tree is on its way
+  bool ok = place_tree(p, node, w);
   // every child's scores at its parent, fetched once (the tests need no exchange of them)
   bool bad_u = false;
   if (ok && tid < p.T && w.par[tid] != kUnusedNode) {
@@ -379,25 +409,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
   }
   ok &= !__syncthreads_or(bad_u);
   cluster_sync_all();  // every CTA of the cluster has started: its shared memory may be written
-  const int vecs = (p.V + VN - 1) / VN, v0 = slice_start(vecs, rank, p.C), v1 = slice_start(vecs, rank + 1, p.C);
   const bool walking = ok && w.par[0] != kUnusedNode;
   bool draw = walking, alive = true;
   int cur = 0, a = 0, n = 0, token = -1;
-  const T *zt = target, *zq = drafts;
-  bool inner = false;
-  auto load = [&] {  // a thread copies what it will read
-    for (int v = v0 + tid; v < v1; v += kThreads) {
-      const int i = v - v0;
-      if (p.vec && (v + 1) * VN <= p.V) {
-        cp_async16(hold + i, zt + static_cast<long long>(v) * VN, true);
-        if (inner) cp_async16(hold + kHold + i, zq + static_cast<long long>(v) * VN, true);
-      } else {
-        hold[i] = load_scores(zt, v, p.V, p.vec);
-        if (inner) hold[kHold + i] = load_scores(zq, v, p.V, p.vec);
-      }
-    }
-    cp_async_wait_all();
-  };
   auto get = [&](int v, float* t, float* q) {  // a vector's scores in both rows
     Vec<T>::unpack(kKeep ? hold[v - v0] : load_scores(zt, v, p.V, p.vec), t);
     if (inner) Vec<T>::unpack(kKeep ? hold[kHold + v - v0] : load_scores(zq, v, p.V, p.vec), q);
@@ -411,21 +425,37 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
       f(v, t, q);
     }
   };
-  // this CTA's record (in warp 0) to every CTA, and theirs
+  // This warp's record to every CTA, and all warps' of the cluster.
   auto exchange = [&](float4 r) {
-    if (warp == 0 && lane < p.C)
-      cluster_send4(cluster_map(&s_rec[n & 1][rank], lane), r, cluster_map(&x.bar[n & 1], lane));
-    alive = __syncthreads_and(exchange_wait(x, n) ? 1 : 0) != 0;
-    ++n;
-    return s_rec[(n - 1) & 1];
+    if (lane < p.C)
+      cluster_send4(cluster_map(&s_rec[n & 1][rank * kWarps + warp], lane), r, cluster_map(&x.bar[n & 1], lane));
+    alive = __all_sync(0xffffffffu, exchange_wait(x, n));
+    return s_rec[n++ & 1];
+  };
+  const int records = p.C * kWarps;
+  // Each CTA's share of p's mass, from the records of the exchange that gave p (before the next one
+  // is sent: its buffer may then be written to).  Warp r sums rank r's.
+  auto sum_masses = [&](const float4* rec, float top) {  // top: what softmax sums are relative to
+    if (warp < p.C) {
+      float m = 0.f;
+      if (lane < kWarps) {
+        const float4 y = rec[warp * kWarps + lane];
+        m = top == -INFINITY ? y.x : y.x == -INFINITY ? 0.f : y.y * ex2(y.x - top);
+      }
+      m = warp_sum(make_float2(m, 0.f)).x;
+      if (lane == 0) s_mass[warp] = m;
+    }
   };
   while (walking) {
     zt = target + cur * p.row_stride;
     zq = drafts + cur * p.row_stride;
     int child = a < p.D ? next_child(w, p.T, cur, cur, [](int) { return true; }) : p.T;
     inner = child < p.T;
-    exchange_expect(x, n, p.C * 16);
-    if (kKeep) load();
+    exchange_expect(x, n, records * 16);
+    if (kKeep) {
+      if (n > 0) load();
+      cp_async_wait_all();
+    }
     MaxSum t{-INFINITY, 0.f}, q{-INFINITY, 0.f};
     over([&](int, const float* ft, const float* fq) {
       fold<VN>(t, ft, p.c2);
@@ -433,23 +463,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
     });
     t = warp_merged(t);
     if (inner) q = warp_merged(q);
-    if (lane == 0) s_warp[warp] = make_float4(t.m, t.l, q.m, q.l);
-    __syncthreads();
-    float4 mine = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-    if (warp == 0) {
-      if (lane < kWarps) mine = s_warp[lane];
-      t = warp_merged(MaxSum{mine.x, mine.y});
-      if (inner) q = warp_merged(MaxSum{mine.z, mine.w});
-      mine = make_float4(t.m, t.l, q.m, q.l);
-    }
-    const float4* rec = exchange(mine);
+    const float4* rec = exchange(make_float4(t.m, t.l, q.m, q.l));
     if (!alive) break;
     MaxSum tt{-INFINITY, 0.f}, qq{-INFINITY, 0.f};
-    for (int r = 0; r < p.C; ++r) {
-      const float4 y = rec[r];
+    for (int i = lane; i < records; i += 32) {
+      const float4 y = rec[i];
       tt = merged(tt, MaxSum{y.x, y.y});
       if (inner) qq = merged(qq, MaxSum{y.z, y.w});
     }
+    tt = warp_merged(tt);
+    if (inner) qq = warp_merged(qq);
     if (!(tt.l > 0.f && tt.l < INFINITY && tt.m < INFINITY) ||
         (inner && !(qq.l > 0.f && qq.l < INFINITY && qq.m < INFINITY))) {
       if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
       st.iq = inner ? 1.f / qq.l : 0.f;
       st.k = 0;
     }
-    if (tid < p.C) s_mass[tid] = rec[tid].x == -INFINITY ? 0.f : rec[tid].y * ex2(rec[tid].x - tt.m);
+    sum_masses(rec, tt.m);
     __syncthreads();
     bool accepted = false;
     while (child < p.T) {
@@ -478,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
           break;
         }
         // rejected: the residual's mass and what is left of q
-        exchange_expect(x, n, p.C * 16);
+        exchange_expect(x, n, records * 16);
         float2 sum = make_float2(0.f, 0.f);
         over([&](int v, const float* ft, const float* fq) {
           float pe[VN], qe[VN];
@@ -492,22 +515,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
           sum.y += tree_sum<VN>(qe);
         });
         sum = warp_sum(sum);
-        if (lane == 0) s_warp[warp] = make_float4(sum.x, sum.y, 0.f, 0.f);
-        __syncthreads();
-        float4 r4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (warp == 0) {
-          if (lane < kWarps) r4 = s_warp[lane];
-          sum = warp_sum(make_float2(r4.x, r4.y));
-          r4 = make_float4(sum.x, sum.y, 0.f, 0.f);
-        }
-        rec = exchange(r4);
+        rec = exchange(make_float4(sum.x, sum.y, 0.f, 0.f));
         if (!alive) break;
-        float R = 0.f, Q = 0.f;
-        for (int r = 0; r < p.C; ++r) {
-          R += rec[r].x;
-          Q += rec[r].y;
+        sum = make_float2(0.f, 0.f);
+        for (int i = lane; i < records; i += 32) {
+          sum.x += rec[i].x;
+          sum.y += rec[i].y;
         }
-        if (tid < p.C && R > 0.f) s_mass[tid] = rec[tid].x;
+        sum = warp_sum(sum);
+        const float R = sum.x, Q = sum.y;
+        if (R > 0.f) sum_masses(rec, -INFINITY);
         if (tid == 0) {
           st.tok[st.k] = c;
           st.ir[st.k] = R > 0.f ? 1.f / R : 0.f;
@@ -525,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
     __syncthreads();  // the stage is rewritten for the next node
   }
   // The draw: the CTA whose slice holds u * total finds the token (rank order, so ascending).
+  alive = __syncthreads_and(alive) != 0;
   if (!ok || !alive) {
     if (rank == 0 && tid == 0) set_status(p.status, ok ? SPECDEC_ERR_TIMEOUT : SPECDEC_ERR_INPUT_RANGE);
   } else if (draw) {
