@@ -342,6 +342,11 @@ template <int N> __device__ __forceinline__ void fold(MaxSum& s, const float* x,
   for (int k = 0; k < N; ++k) t[k] = ex2(fmaf(x[k], c2, -off));
   s.l += tree_sum<N>(t);
 }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+  return v;
+}
 __device__ __forceinline__ float2 warp_sum(float2 v) {
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) {
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
         const float4 y = rec[warp * kWarps + lane];
         m = top == -INFINITY ? y.x : y.x == -INFINITY ? 0.f : y.y * ex2(y.x - top);
       }
-      m = warp_sum(make_float2(m, 0.f)).x;
+      m = warp_sum(m);
       if (lane == 0) s_mass[warp] = m;
     }
   };
@@ -546,20 +551,20 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
   if (!ok || !alive) {
     if (rank == 0 && tid == 0) set_status(p.status, ok ? SPECDEC_ERR_TIMEOUT : SPECDEC_ERR_INPUT_RANGE);
   } else if (draw) {
-    // Every thread finds the same owner; the last CTA with any mass takes what rounding leaves.
-    float total = 0.f, before = 0.f, run = 0.f;
-    for (int r = 0; r < p.C; ++r) total += s_mass[r];
-    int owner = -1, last = 0;
-    for (int r = 0; r < p.C; ++r) {
-      const float m = s_mass[r];
-      if (m > 0.f) {
-        if (owner < 0) before = run;
-        if (owner < 0 && run + m > s_u[0] * total) owner = r;
-        last = r;
-      }
-      run += m;
+    // Every warp finds the same owner, a lane per CTA; the last one with any mass takes what rounding
+    // leaves.
+    const float share = lane < p.C ? s_mass[lane] : 0.f;
+    float upto = share;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const float o = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += o;
     }
-    if (owner < 0) owner = last;
+    const float total = __shfl_sync(0xffffffffu, upto, 31);
+    const unsigned past = __ballot_sync(0xffffffffu, share > 0.f && upto > s_u[0] * total),
+                   some_mass = __ballot_sync(0xffffffffu, share > 0.f);
+    const int owner = past ? __ffs(past) - 1 : 31 - __clz(some_mass);
+    const float before = __shfl_sync(0xffffffffu, upto - share, owner);
     if (rank == owner) {
       const float goal = s_u[0];  // probabilities() are masses over the total
       // Masses of 32 consecutive vectors (a warp's in one run), kRuns runs at a time; the entry
@@ -568,8 +573,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
       int pick = -1, last_v = -1;  // first vector of the chosen entry, of the last with any mass
       float start = 0.f, last_start = 0.f;
       for (int first = v0; first < v1 && pick < 0; first += kHold) {
-#pragma unroll 1
-        for (int k = 0; k < kRuns; ++k) {
+        const int runs = min(kRuns, (v1 - first + kThreads - 1) / kThreads);
+#pragma unroll 2
+        for (int k = 0; k < runs; ++k) {
           const int v = first + k * kThreads + tid;
           float m = 0.f;
           if (v < v1) {
@@ -578,14 +584,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
             probabilities<VN>(st, p.c2, p.replacement, v * VN, ft, fq, pe, qe);
             m = tree_sum<VN>(pe);
           }
-          m = warp_sum(make_float2(m, 0.f)).x;
+          m = warp_sum(m);
           if (lane == 0) s_entry[k * kWarps + warp] = m;
         }
         __syncthreads();
         constexpr int kEach = kRuns * kWarps / 32;  // entries per lane; every warp finds the same
         float e[kEach], sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) sum += e[i] = s_entry[lane * kEach + i];
+        for (int i = 0; i < kEach; ++i) {
+          e[i] = lane * kEach + i < runs * kWarps ? s_entry[lane * kEach + i] : 0.f;
+          sum += e[i];
+        }
         float inc = sum;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -635,8 +644,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
         for (int k = 0; k < VN; ++k) pe[k] = 0.f;
         if (v < v1) {
           float ft[VN], fq[VN], qe[VN], sum[VN];
-          Vec<T>::unpack(load_scores(zt, v, p.V, p.vec), ft);
-          if (inner) Vec<T>::unpack(load_scores(zq, v, p.V, p.vec), fq);
+          get(v, ft, fq);
           probabilities<VN>(st, p.c2, p.replacement, v * VN, ft, fq, pe, qe);
 #pragma unroll
           for (int k = 0; k < VN; ++k) sum[k] = pe[k];
