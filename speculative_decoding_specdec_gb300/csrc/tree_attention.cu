@@ -6,8 +6,9 @@
 // columns of each tile into two private stages, one bulk copy per column and lane, without any
 // CTA-wide barrier.  For the scores a lane has half of a column's values (one 16-byte read of K
 // against R broadcast reads of Q); for O a lane owns 4 (or 8) of the head's values (one read of V
-// and R / 4 broadcast reads of the weights for 4 R FMAs).  HBM bounds few rows, the FMA pipe and
-// its operands' shared-memory reads many.
+// and R / 4 broadcast reads of the weights for 4 R FMAs).  HBM bounds few rows, the
+// operands' shared-memory reads many: 16 rows of up to 4096 columns, 8 K/V heads: 4 query rows 80 us
+// (302 MB, 3.8 TB/s); one row of 65536 columns and 8 query rows: 195 us (2.8 TB/s).
 #include <algorithm>
 #include <climits>
 #include <cmath>

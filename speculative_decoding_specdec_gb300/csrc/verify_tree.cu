@@ -17,7 +17,9 @@
 // sent back.  Two record buffers alternate: the barrier between two exchanges separates a
 // record's readers from its next writer.
 // What bounds it: the chain of dependent steps (row latency, block reduction, cluster barrier);
-// the visited rows are a few hundred KB per step.
+// the visited rows are a few hundred KB per step.  Measured: greedy, 8 trees of 16 nodes, V 32000:
+// 9.4 us; 16 trees of 64 nodes, V 151936: 21 us; sampled, 32 trees of 16 nodes, V 151552: 45 us, where
+// a node takes 2500 cycles to load, 3000 to 5000 to fold and 4400 to 6500 to exchange.
 #include <algorithm>
 #include <climits>
 #include <cmath>
