@@ -32,6 +32,8 @@
  *     either once before its first use: every call leaves it all zero again (also when it reports
  *     an out-of-range input through dev_status), so it is reused as is, for any shape it is large
  *     enough for.  Calls that may overlap on the GPU need separate ones (one per stream).
+ *     Attention of a tree takes one too (specdec_tree_attention_workspace): zero it once when it is
+ *     allocated; one that is large enough for the largest shape serves every shape.
  *   - Every call is asynchronous on `stream` (a cudaStream_t passed as void*; NULL = the legacy
  *     default stream).  The return value reports host-detected problems only: an invalid
  *     argument, an unsupported configuration, or a failed launch.  It does not wait for the GPU.
