@@ -563,7 +563,7 @@ int specdec_pool_admit(const specdec_admit_args* args, void* stream);
  *     unused nodes neither column is written;
  *   - explicit (positions and columns both [B][T], n_committed/width/parents NULL): token t of
  *     row b has position positions[b][t] and goes to column columns[b][t]; a negative column
- *     marks a token that is padding and is not written.  T is not limited to SPECDEC_MAX_TREE.
+ *     marks a token that is padding (whatever its position says) and is not written.  T is not limited to SPECDEC_MAX_TREE.
  * The q_out of an unused node or padding token is zero.
  * Device-detected errors: N_b outside [1, W], a bad parent, a position outside [0, table_len)
  * (SPECDEC_ERR_INPUT_RANGE), a column at or beyond cache.cap_cols (SPECDEC_ERR_CAPACITY); the

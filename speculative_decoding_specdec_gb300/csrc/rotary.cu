@@ -34,13 +34,17 @@ struct RotaryParams {
   int T, Hq, H, hd, rot, interleaved, table_len, cap, one_row;
 };
 
-// Position and column of token t of row b; false if nothing is to be written for it.  All
-// threads of the CTA get the same answer.
+// Position and column of token t of row b; false if nothing is to be written to the cache for it:
+// with pos >= 0 its q_out is zero, with pos < 0 an error was recorded.  All threads of the CTA get
+// the same answer.
 __device__ bool locate(const RotaryParams& p, int b, int t, int& pos, int& col) {
   if (p.positions) {
     pos = p.positions[static_cast<long long>(b) * p.T + t];
     col = p.columns[static_cast<long long>(b) * p.T + t];
-    if (col < 0) return false;
+    if (col < 0) {  // padding, whatever its position says
+      pos = 0;
+      return false;
+    }
   } else {
     __shared__ int s_par[kMaxTree];
     const int n = p.n_committed[b], W = *p.width;

@@ -1,0 +1,49 @@
+"""The tree operators at the edges of what their callers may pass, against the oracle.
+
+Comparisons are exact (copies, zeros, whole numbers, results that must not depend on what is hidden)
+or take the bounds that are derived in the operator's own test file.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.tree_oracle as TO
+import test_gpu_rotary as R
+from tree_testlib import DEV, i32, numpy64, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("position", [-1, -2 ** 31, 40, 2 ** 31 - 1])   # (the table has 40)
+@pytest.mark.parametrize("hd,rot,interleaved", [(64, 64, False), (80, 20, True)])
+def test_a_padding_tokens_position_does_not_matter(dtype, in_place, position, hd, rot, interleaved):
+    """A token with a negative column is padding whatever its position says: q_out is zero, nothing
+    is written to the cache and no error recorded."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    gen = torch.Generator().manual_seed(1)
+    B, T, H = 2, 6, 2
+    q, k, v = (torch.randn(B, T, H, hd, generator=gen).to(dtype).to(DEV) for _ in range(3))
+    cache = torch.randn(1, 2, B, H, 9, hd, generator=gen).to(dtype).to(DEV)
+    pos = np.tile(np.arange(T), (B, 1))
+    col = pos + 2
+    for b, t, c in ((0, 0, -1), (0, 1, -5), (1, 5, -2 ** 31)):
+        pos[b, t], col[b, t] = position, c
+    q0, want, table, st = numpy64(q), numpy64(cache), R.make_table(40, rot), status()
+    out = q if in_place else torch.full_like(q, 7.0)
+    sd.rotary_append(q, k, v, cache, 0, table, out, st, positions=i32(pos), columns=i32(col), interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    got, cs = numpy64(cache), numpy64(table)
+    for b in range(B):
+        for t in range(T):
+            if col[b, t] < 0:
+                assert (out[b, t] == 0).all()
+                continue
+            c, s = cs[pos[b, t], :, 0], cs[pos[b, t], :, 1]
+            R.close(numpy64(out[b, t]), TO.rotate(q0[b, t], c, s, interleaved), q0[b, t], dtype)
+            R.close(got[0, 0, b, :, col[b, t]], TO.rotate(numpy64(k[b, t]), c, s, interleaved), numpy64(k[b, t]), dtype)
+            want[0, 0, b, :, col[b, t]] = got[0, 0, b, :, col[b, t]]
+            want[0, 1, b, :, col[b, t]] = numpy64(v[b, t])
+    np.testing.assert_array_equal(got, want)
