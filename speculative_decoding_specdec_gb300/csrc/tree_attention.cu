@@ -308,9 +308,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
     auto store = [&](int r, int i, float4 acc, float mm, float ll) {
       const int rr = mt * R + r, t = rr / p.G, qh = seg.h * p.G + rr - t * p.G;
       const bool live = s_anc[t] != 0;
-      const float inv = live ? 1.f / ll : 0.f;
+      const float inv = 1.f / ll;
       store4<T>(p.out + seg.b * p.outr + t * p.outt + (static_cast<long long>(qh) * hd + i * 4) * es,
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                live ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
       if (p.lse && i == 0)
         p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + qh] =
             live ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
@@ -573,14 +573,14 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
       const int r = warp * 4 + k, rr = mt * M + r;
       if (r >= nrows) continue;
       const int t = rr / p.G, qh = seg.h * p.G + rr % p.G;
-      const float inv = anc[k] ? 1.f / l[k] : 0.f;
+      const float inv = 1.f / l[k];
       char* y = p.out + seg.b * p.outr + t * p.outt + static_cast<long long>(qh) * hd * sizeof(T);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int d = j * 128 + lane * 4;
         if (d < hd)
-          store4<T>(y + d * sizeof(T), make_float4(o[k][j].x * inv, o[k][j].y * inv,
-                                                   o[k][j].z * inv, o[k][j].w * inv));
+          store4<T>(y + d * sizeof(T), anc[k] ? make_float4(o[k][j].x * inv, o[k][j].y * inv, o[k][j].z * inv, o[k][j].w * inv)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f));
       }
       if (p.lse && lane == 0)
         p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + qh] =

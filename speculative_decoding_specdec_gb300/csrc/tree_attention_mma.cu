@@ -400,12 +400,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       }
     }
     if (!mine) continue;
-    const float inv = live ? 1.f / ll : 0.f;
+    const float inv = 1.f / ll;
     char* y = p.out + seg.b * p.outr + t * p.outt + static_cast<long long>(h) * HD * 2;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
       *reinterpret_cast<uint2*>(y + (d0 + j * kPer * 4) * 2) =
-          make_uint2(bf16_pack(acc[j].x * inv, acc[j].y * inv), bf16_pack(acc[j].z * inv, acc[j].w * inv));
+          live ? make_uint2(bf16_pack(acc[j].x * inv, acc[j].y * inv), bf16_pack(acc[j].z * inv, acc[j].w * inv)) : make_uint2(0, 0);
     if (p.lse && d0 == 0)
       p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + h] =
           live ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;

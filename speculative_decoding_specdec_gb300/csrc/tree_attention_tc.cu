@@ -484,14 +484,16 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       const int slot = whole ? 0 : attn_slot(p, sh, g, mt, now.unit0);
       char* y = p.out + now.b * p.outr + t_of * p.outt +
                 static_cast<long long>(now.h * p.G + (mine ? rr % p.G : 0)) * HD * 2;
-      auto store_out = [&](int c, const float (&o)[32], float inv) {
+      auto store_out = [&](int c, const float (&o)[32]) {  // (zeros for an unused node, whatever o is)
+        const float inv = 1.f / l;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           *reinterpret_cast<uint4*>(y + c * 64 + k * 16) =
-              make_uint4(bf16_pack(o[8 * k] * inv, o[8 * k + 1] * inv),
-                         bf16_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                         bf16_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                         bf16_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+              anc ? make_uint4(bf16_pack(o[8 * k] * inv, o[8 * k + 1] * inv),
+                               bf16_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                               bf16_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                               bf16_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv))
+                  : make_uint4(0, 0, 0, 0);
       };
       auto store_lse = [&](float mm, float ll) {
         if (p.lse)
@@ -502,7 +504,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       auto emit = [&](int c, const float (&o)[32]) {
         if (!write) return;
         if (whole) {
-          store_out(c, o, anc ? 1.f / l : 0.f);
+          store_out(c, o);
         } else {
           float4* w = reinterpret_cast<float4*>(p.part_o) +
                       (static_cast<long long>(slot) * (HD / 4) + c * 8) * 2 * kRows + pr;
@@ -618,13 +620,13 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
       }
     }
   }
-  const float inv = live ? 1.f / l : 0.f;
+  const float inv = 1.f / l;
   if (rr >= p.T * p.G) return;
   char* y = p.out + b * p.outr + t * p.outt + static_cast<long long>(qh) * HD * 2 + d0 * 8;
 #pragma unroll
   for (int k = 0; k < kPer; ++k)
-    *reinterpret_cast<uint2*>(y + k * 8) = make_uint2(bf16_pack(o[k].x * inv, o[k].y * inv),
-                                                      bf16_pack(o[k].z * inv, o[k].w * inv));
+    *reinterpret_cast<uint2*>(y + k * 8) = live ? make_uint2(bf16_pack(o[k].x * inv, o[k].y * inv), bf16_pack(o[k].z * inv, o[k].w * inv))
+                                                : make_uint2(0, 0);
   if (p.lse && warp == 0)
     p.lse[(static_cast<long long>(b) * p.T + t) * p.Hq + qh] =
         live ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;

@@ -9,7 +9,8 @@ import torch
 
 import oracle.tree_oracle as TO
 import test_gpu_rotary as R
-from tree_testlib import DEV, i32, numpy64, status
+import test_gpu_tree_attention as A
+from tree_testlib import DEV, i32, numpy64, random_parents, status
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,37 @@ def test_a_padding_tokens_position_does_not_matter(dtype, in_place, position, hd
             want[0, 0, b, :, col[b, t]] = got[0, 0, b, :, col[b, t]]
             want[0, 1, b, :, col[b, t]] = numpy64(v[b, t])
     np.testing.assert_array_equal(got, want)
+
+
+# Query rows per K/V head for every kernel and place a row's result is written from: (T, G, hd, the
+# committed columns of a unit that share borders cut, or of one that they do not)
+SHAPES = [(5, 2, 64), (12, 2, 128), (20, 5, 64), (16, 8, 128), (25, 8, 128), (50, 8, 64)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,G,hd", SHAPES + [(6, 2, 80), (10, 4, 256)])
+@pytest.mark.parametrize("n", [[40, 9, 150], [5000]])
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+def test_unused_nodes_give_zeros_whatever_there_is(dtype, T, G, hd, n, where):
+    """Zeros (lse: -infinity) for unused nodes, also where their q is NaN or infinite or a committed
+    column is, and no trace of that q in any other row."""
+    rng = np.random.default_rng(T * G + hd)
+    B, H, n = len(n), 2 if len(n) > 1 else 1, np.array(n)
+    q, cache, W = A.inputs(rng, B, T, H * G, H, hd, n, dtype)
+    par = random_parents(rng, B, T, unused=0.3)
+    par[:, T - 1] = -2
+    if B > 1:
+        par[1] = -2
+    A.hide(cache, n, W, T, par)
+    unused, clean, held = par == -2, q.clone(), cache.clone()
+    for b in range(B):
+        for j, t in enumerate(np.flatnonzero(unused[b])):
+            if where == "q":
+                q[b, t] = (float("nan"), float("inf"), -float("inf"))[j % 3]
+        if where != "q":
+            cache[1, 0 if where == "k" else 1, b, :, W - 2, 3] = float("nan")
+    out, lse, st = A.run(q, cache, 1, n, W, par)
+    assert st == 0
+    assert (out[unused] == 0).all() and np.isneginf(lse[unused]).all()
+    if where == "q":
+        A.check(out, lse, clean, held, 1, n, W, par)
