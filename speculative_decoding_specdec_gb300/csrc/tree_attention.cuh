@@ -203,6 +203,59 @@ __device__ __forceinline__ int attn_slot(const AttnParams& p, const AttnShares& 
   return 2 * (g * p.MT + mt) + (sh.start(g) >= unit0 ? 0 : 1);
 }
 
+// V of nodes that is not finite, in the kernels of matrix products.  There a hidden column has the
+// weight 0, and 0 * NaN is NaN, so such values of a node's V are zero in shared memory, and the rows
+// that see the node get them added from the cache to what has been written (attn_add_not_finite):
+// their weight is not zero, and whatever it is the result in that place of the head is an infinity
+// or NaN.  Both out of line: among the loops they cost every call 1.5 to 2.5 %.
+__device__ __forceinline__ bool inf_or_nan(uint32_t w) {  // either of two bf16 values
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool inf_or_nan(uint4 v) {
+  return inf_or_nan(v.x) || inf_or_nan(v.y) || inf_or_nan(v.z) || inf_or_nan(v.w);
+}
+// Zeros in the place of what is not finite in the 16-byte chunks [c0, c1) of row r of a tile of
+// `rows` rows in panels of 64 values (the 128-byte swizzle).
+inline __device__ __noinline__ void attn_make_finite(char* tile, int r, int rows, int c0, int c1) {
+  auto of = [](uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+  };
+  for (int c = c0; c < c1; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    *at = make_uint4(of(at->x), of(at->y), of(at->z), of(at->w));
+  }
+}
+// V of a segment's first node (the columns of the others follow).
+__device__ __forceinline__ const char* attn_node_v(const AttnParams& p, const AttnSegment& s) {
+  return p.cache.base + p.cache.skv + (p.one_row ? 0 : s.b) * p.cache.srow + s.h * p.cache.shead +
+         (static_cast<long long>(s.first) + s.old) * p.hd * 2;
+}
+// Groups of 4 values d0, d0 + step, .. of a row that this thread has written, as bf16 to `out` or
+// (out == nullptr) as partial sums, part + 4-value group * part_step; nodes: those that the row sees
+// and whose V, from `v` on, is not finite somewhere.
+inline __device__ __noinline__ void attn_add_not_finite(unsigned long long nodes, const char* v, int hd, int d0, int step,
+                                                 char* out, float4* part, int part_step) {
+  for (; nodes; nodes &= nodes - 1) {
+    const char* from = v + (__ffsll(nodes) - 1) * hd * 2;
+    for (int d = d0; d < hd; d += step) {
+      const uint2 w = *reinterpret_cast<const uint2*>(from + d * 2);
+      auto of = [](float x) { return fabsf(x) < INFINITY ? 0.f : x; };  // (an infinity or NaN)
+      const float4 x = make_float4(of(bf16_lo(w.x)), of(bf16_hi(w.x)), of(bf16_lo(w.y)), of(bf16_hi(w.y)));
+      if (out) {
+        uint2* at = reinterpret_cast<uint2*>(out + d * 2);
+        const uint2 y = *at;
+        *at = make_uint2(bf16_pack(bf16_lo(y.x) + x.x, bf16_hi(y.x) + x.y), bf16_pack(bf16_lo(y.y) + x.z, bf16_hi(y.y) + x.w));
+      } else {
+        float4* at = part + static_cast<long long>(d / 4) * part_step;
+        const float4 y = *at;
+        *at = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+      }
+    }
+  }
+}
+
 // The tensor-core kernel (tree_attention_tc.cu): rows per M-tile and M-tiles for R query rows per
 // K/V head, and its launch (rows: of the cache).
 void attn_tc_shape(int R, int* M, int* MT);

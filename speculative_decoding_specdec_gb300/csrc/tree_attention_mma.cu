@@ -58,9 +58,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-__device__ __forceinline__ bool inf_or_nan(uint32_t w) {  // either of two bf16 values
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
 
 template <int HD, int NT> struct Smem {
   static constexpr int kSlice = kCols * HD * 2;               // K or V of a warp's slice
@@ -87,7 +84,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   extern __shared__ char raw[];
   __shared__ uint64_t s_full[kWarps][kStages];
   __shared__ int s_par[kMaxTree], s_flag, s_bad;
-  __shared__ unsigned long long s_anc[kMaxTree];
+  __shared__ unsigned long long s_anc[kMaxTree], s_poison[kWarps];
   __shared__ float2 s_ml[kWarps][kRows];
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
   const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, p.B);
@@ -191,7 +188,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
     }
-    unsigned long long poison = 0;
+    unsigned long long poison = 0;  // nodes whose V is not finite somewhere
     for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++used) {
       const int st = used % kStages;
       ok = ok && __all_sync(0xffffffffu, mbar_wait_sleep(&s_full[warp][st], (used / kStages) & 1,
@@ -230,20 +227,20 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
             }
           const int c = lane & 15, node = base + c;  // two lanes look after a column
           bool bad = false, drop = false;
+          const int ch0 = (lane >> 4) * (HD / 16), ch1 = ch0 + HD / 16;
+          auto at = [&](int ch) {
+            return reinterpret_cast<uint4*>(vm + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ (c & 7)) << 4));
+          };
           if (node >= 0) {
             drop = node >= p.T || s_anc[node] == 0;
             if (!drop)
-              for (int ch = (lane >> 4) * (HD / 16); ch < ((lane >> 4) + 1) * (HD / 16); ++ch) {
-                const uint4 v = *reinterpret_cast<const uint4*>(vm + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ (c & 7)) << 4));
-                bad |= inf_or_nan(v.x) || inf_or_nan(v.y) || inf_or_nan(v.z) || inf_or_nan(v.w);
-              }
+              for (int ch = ch0; ch < ch1; ++ch) bad |= inf_or_nan(*at(ch));
           }
+          if (drop)
+            for (int ch = ch0; ch < ch1; ++ch) *at(ch) = make_uint4(0, 0, 0, 0);
+          if (bad) attn_make_finite(vm, c, kCols, ch0, ch1);
           unsigned long long which = __ballot_sync(0xffffffffu, bad);
           which = (which | which >> 16) & 0xffffu;
-          drop |= which >> c & 1;
-          if (drop)
-            for (int ch = (lane >> 4) * (HD / 16); ch < ((lane >> 4) + 1) * (HD / 16); ++ch)
-              *reinterpret_cast<uint4*>(vm + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ (c & 7)) << 4)) = make_uint4(0, 0, 0, 0);
           poison |= base >= 0 ? which << base : which >> -base;
           fence_async_smem();
           __syncwarp();
@@ -315,9 +312,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 4);
         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 8);
         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
-        if (anc[n][i] & poison) l[n][i] = __int_as_float(0x7FC00000);  // the row sees a column that is not finite
       }
     __syncthreads();  // the segment before has been merged
+    if (lane == 0) s_poison[warp] = poison;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (gr == 0) {
@@ -330,7 +327,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         for (int k = 0; k < 4; ++k)
           merge[(warp * kRows + 8 * n + 2 * qd + (k & 1)) * S::kPitch + j * 16 + gr + (k >> 1) * 8] = o[n][j][k];
     }
-    __syncthreads();
+    const bool poisoned = __syncthreads_or(poison != 0);
     // kPer threads per row: every kPer-th group of 4 values from d0
     constexpr int kPer = kThreads / kRows, kVecs = HD / 4 / kPer;
     const int r = tid / kPer, d0 = tid % kPer * 4;
@@ -359,9 +356,11 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     if (mine)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
-            add(s_ml[w][r], [&](int j) {
+        add(s_ml[w][r], [&](int j) {
           return *reinterpret_cast<const float4*>(merge + (w * kRows + r) * S::kPitch + d0 + j * kPer * 4);
         });
+    unsigned long long hit = 0;
+    if (poisoned && mine) hit = (s_poison[0] | s_poison[1] | s_poison[2] | s_poison[3]) & s_anc[t];
     if (seg.tile0 > 0 || seg.tile1 < seg.tiles) {
       const long long at = static_cast<long long>(attn_slot(p, sh, g, mt, seg.unit0)) * kRows + r;
       if (mine) {
@@ -369,6 +368,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
           *reinterpret_cast<float4*>(p.part_o + at * HD + d0 + j * kPer * 4) = acc[j];
+        if (hit) attn_add_not_finite(hit, attn_node_v(p, seg), HD, d0, kPer * 4, nullptr, reinterpret_cast<float4*>(p.part_o + at * HD), 1);
+        hit = 0;
       }
       if (s_bad) continue;
       const int g0 = sh.owner(seg.unit0), g1 = sh.owner(seg.unit0 + seg.tiles - 1);
@@ -406,6 +407,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     for (int j = 0; j < kVecs; ++j)
       *reinterpret_cast<uint2*>(y + (d0 + j * kPer * 4) * 2) =
           live ? make_uint2(bf16_pack(acc[j].x * inv, acc[j].y * inv), bf16_pack(acc[j].z * inv, acc[j].w * inv)) : make_uint2(0, 0);
+    if (hit) attn_add_not_finite(hit, attn_node_v(p, seg), HD, d0, kPer * 4, y, nullptr, 0);
     if (p.lse && d0 == 0)
       p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + h] =
           live ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;

@@ -21,8 +21,9 @@
 // 1740 of them.  About 10000 cycles pass before the first tile.
 //
 // A tile that holds nodes' columns or the end of a row needs care: its V columns behind the nodes
-// and of unused nodes are zeroed in shared memory (0 * NaN is NaN in a matrix product), and so are
-// those of used nodes that hold something that is not finite; rows that see such a node get NaN.
+// and of unused nodes are zeroed in shared memory (0 * NaN is NaN in a matrix product), and so is
+// what is not finite of the used nodes'; the rows that see such a node get it back from the cache
+// when they are written.
 #include <cmath>
 
 #include "tcgen05.cuh"
@@ -71,10 +72,6 @@ struct Bars {
   uint64_t k_full[kMaxKStages], k_empty[kMaxKStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2];
 };
-
-__device__ __forceinline__ bool inf_or_nan(uint32_t w) {  // either of two bf16 values
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
 
 // Pairs of floats: one instruction for two.
 __device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
@@ -260,21 +257,20 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           char* vt = smem + S::v + st * S::kTile;
           for (int c = max(0, seg.old - col0) + lane; c < steps * 16; c += 32) {
             const int node = col0 + c - seg.old;
-            bool drop = node >= p.T || s_anc[node] == 0;
+            const bool drop = node >= p.T || s_anc[node] == 0;
+            auto at = [&](int k) { return reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)); };
             if (!drop) {
               bool bad = false;
 #pragma unroll
-              for (int k = 0; k < HD / 8; ++k) {
-                const uint4 w = *reinterpret_cast<const uint4*>(vt + swizzled(c, k, kCols));
-                bad |= inf_or_nan(w.x) || inf_or_nan(w.y) || inf_or_nan(w.z) || inf_or_nan(w.w);
+              for (int k = 0; k < HD / 8; ++k) bad |= inf_or_nan(*at(k));
+              if (bad) {
+                atomicOr(&s_poison, 1ull << node);
+                attn_make_finite(vt, c, kCols, 0, HD / 8);
               }
-              if (bad) atomicOr(&s_poison, 1ull << node);
-              drop = bad;
-            }
-            if (drop)
+            } else {
 #pragma unroll
-              for (int k = 0; k < HD / 8; ++k)
-                *reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)) = make_uint4(0, 0, 0, 0);
+              for (int k = 0; k < HD / 8; ++k) *at(k) = make_uint4(0, 0, 0, 0);
+            }
           }
           fence_async_smem();
           __syncwarp();
@@ -464,7 +460,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       if (jobs > 0) ok = warp_wait(&bar.o_done[a], ends++ & 1);
       ok = ok && warp_wait(&bar.v_clean, seg_no & 1);
       tmem_fence_after();
-      if (anc & s_poison) l = __int_as_float(0x7FC00000);
+      const unsigned long long poison = anc & s_poison;  // nodes it sees whose V is not finite somewhere
       const bool write = mine && !s_bad;
       if (!(ok = named_bar_all(1, 256, ok))) break;  // all have read s_poison and s_bad
       if (tid == 0) s_bad = 0;
@@ -542,6 +538,9 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           emit(c, o);
         }
       const bool owner = write && (two || a == 0);
+      if (poison && owner)
+        attn_add_not_finite(poison, attn_node_v(p, now), HD, 0, 4, whole ? y : nullptr,
+                            reinterpret_cast<float4*>(p.part_o) + static_cast<long long>(slot) * (HD / 4) * 2 * kRows + pr, 2 * kRows);
       if (whole) {
         if (owner) store_lse(m, l);
       } else if (owner) {

@@ -82,3 +82,32 @@ def test_unused_nodes_give_zeros_whatever_there_is(dtype, T, G, hd, n, where):
     assert (out[unused] == 0).all() and np.isneginf(lse[unused]).all()
     if where == "q":
         A.check(out, lse, clean, held, 1, n, W, par)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,G,hd", SHAPES)
+@pytest.mark.parametrize("n", [[40, 9, 150], [5000]])
+@pytest.mark.parametrize("value", ["inf", "-inf", "nan"])
+def test_a_value_that_is_not_finite_stays_in_its_dimension(dtype, T, G, hd, n, value):
+    """V of a node is not finite in some of the head's values: nodes that see it are not finite in
+    those, and everything else (lse, which V does not enter, too) is what it was."""
+    rng = np.random.default_rng(T * G + hd + 1)
+    B, H, n = len(n), 2 if len(n) > 1 else 1, np.array(n)
+    q, cache, W = A.inputs(rng, B, T, H * G, H, hd, n, dtype)
+    par = random_parents(rng, B, T, deep=0.5)
+    clean, lse0, _ = A.run(q, cache, 1, n, W, par)
+    nodes, dims = (T // 2, T - 1), (0, 3, hd - 1)
+    for node in nodes:
+        for d in dims:
+            cache[1, 1, :, :, W - 1 + node, d] = float(value)
+    out, lse, st = A.run(q, cache, 1, n, W, par)
+    assert st == 0
+    np.testing.assert_array_equal(lse, lse0)
+    rest = [d for d in range(hd) if d not in dims]
+    np.testing.assert_array_equal(out[..., rest], clean[..., rest])
+    for b in range(B):
+        for t in range(T):
+            if set(nodes) & set(TO.line_of(par[b], t)):
+                assert not np.isfinite(out[b, t][:, dims]).any()
+            else:
+                np.testing.assert_array_equal(out[b, t], clean[b, t])
