@@ -16,31 +16,43 @@ from . import specdec
 
 
 class Workspaces:
-    """Zero-filled verification workspaces, one per kind, grown on demand (a workspace is left
-    zero-filled by every call, so one buffer serves every shape it is large enough for)."""
+    """Workspaces, one per kind, zero-filled when they are made and grown on demand.  Every call
+    leaves zero what has to be zero for the next one, so one buffer serves every shape it is large
+    enough for.
+
+    ``stream`` is the one the call will use (None: the current one): the zeros are written on it, so
+    they come before the call.  A buffer that has been outgrown is kept, since calls in flight on any
+    stream, or captured in a graph, may still use it."""
 
     def __init__(self, device):
         self.device = device
         self._ws = {}
+        self._outgrown = []
 
-    def get(self, kind, nbytes):
+    def _zeros(self, shape, dtype, stream):
+        with torch.cuda.stream(stream):
+            return torch.zeros(shape, dtype=dtype, device=self.device)
+
+    def get(self, kind, nbytes, stream=None):
         ws = self._ws.get(kind)
         if ws is None or ws.numel() < nbytes:
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            if ws is not None:
+                self._outgrown.append(ws)
+            ws = self._zeros(max(nbytes, 256), torch.uint8, stream)
             self._ws[kind] = ws
         return ws
 
-    def greedy(self, logits, draft):
+    def greedy(self, logits, draft, stream=None):
         B, D = draft.shape
-        return self.get("greedy", specdec.greedy_workspace_bytes(B, D))
+        return self.get("greedy", specdec.greedy_workspace_bytes(B, D), stream)
 
-    def bounds(self, draft):
+    def bounds(self, draft, stream=None):
         """Keep-bound buffer [B, 2D+1, 2] int32 for the sampling settings."""
         B, D = draft.shape
         key = ("bounds", B, D)
         t = self._ws.get(key)
         if t is None:
-            t = torch.zeros((B, 2 * D + 1, 2), dtype=torch.int32, device=self.device)
+            t = self._zeros((B, 2 * D + 1, 2), torch.int32, stream)
             self._ws[key] = t
         return t
 
@@ -138,7 +150,7 @@ class EqspecBatch:
     def verify_greedy(self, logits, draft, stream=None):
         self._results_row()
         specdec.verify_greedy(logits, draft, self.accept_len, self.out_token, self.status,
-                              self.workspaces.greedy(logits, draft), stream)
+                              self.workspaces.greedy(logits, draft, stream), stream)
 
     def verify_sample(self, target_logits, draft_logits, draft, uniforms, temperature,
                       residual=None, stream=None, top_k=0, top_p=1.0, seed=None):
@@ -148,7 +160,7 @@ class EqspecBatch:
         self._results_row()
         bounds = None
         if (0 < top_k < target_logits.shape[-1]) or top_p < 1.0:
-            bounds = self.workspaces.bounds(draft)
+            bounds = self.workspaces.bounds(draft, stream)
             specdec.sampling_filter(target_logits, draft_logits, temperature, top_k, top_p,
                                     bounds, self.status, stream)
         if uniforms is None:
@@ -238,7 +250,7 @@ class TreeBatch(EqspecBatch):
 
     def attention(self, layer, q, out, parents, scale=None, lse=None, stream=None):
         """Attention of the tree over the committed columns and each node's ancestors."""
-        ws = self.workspaces.get("tree", specdec.tree_attention_workspace_bytes(q, self.cache))
+        ws = self.workspaces.get("tree", specdec.tree_attention_workspace_bytes(q, self.cache), stream)
         specdec.tree_attention(q, self.cache, layer, out, self.n_committed, self.width, parents,
                                self.status, ws, scale=scale, lse=lse, stream=stream)
 
@@ -434,7 +446,7 @@ class ExspecPool:
     def verify_greedy(self, logits, draft, stream=None):
         """Greedy verification of every slot: logits [S, D+1, V], draft [S, D] in slot order."""
         specdec.verify_greedy(logits, draft, self.accept_len, self.out_token, self.status,
-                              self.workspaces.greedy(logits, draft), stream)
+                              self.workspaces.greedy(logits, draft, stream), stream)
 
     def verify_sample(self, target_logits, draft_logits, draft, uniforms, temperature,
                       stream=None):
@@ -610,7 +622,7 @@ class SequencePool:
         """Greedy verification of every slot: logits [S, D+1, V], draft [S, D] in slot order
         (rows of slots that are not scheduled are ignored)."""
         specdec.verify_greedy(logits, draft, self.accept_len, self.out_token, self.status,
-                              self.workspaces.greedy(logits, draft), stream)
+                              self.workspaces.greedy(logits, draft, stream), stream)
 
     def gather(self, off, n, uniform, stream=None):
         """Repad batch perm[off:off+n] into the batch buffer (uniform batches: lengths only)."""
