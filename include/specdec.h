@@ -557,7 +557,7 @@ int specdec_pool_admit(const specdec_admit_args* args, void* stream);
  * values (i, i + rot_dim / 2), or of (2i, 2i + 1) if `interleaved`,
  *   (x1, x2) -> (x1 * cos - x2 * sin, x1 * sin + x2 * cos), in fp32, rounded once.
  * Rotated keys and copied values are written to columns of row b of `cache`, layer `layer`
- * (with cache.rows == 1 and B > 1 every batch row writes to cache row 0).
+ * (with cache.rows == 1 and B > 1 every batch row writes to cache row 0: explicit columns only).
  * Columns and positions, one of two ways:
  *   - a verification pass: n_committed [B], width [1] (and parents): as described above, of
  *     unused nodes neither column is written;

@@ -214,6 +214,8 @@ extern "C" int specdec_rotary_append(const specdec_rotary_args* a, void* stream)
   if (pass ? !a->n_committed || !a->width || a->positions || a->columns
            : !a->positions || !a->columns)
     return SPECDEC_ERR_INVALID_ARG;
+  // (in one cache row the batch rows' nodes would go to the same columns)
+  if (pass && c.rows == 1 && a->B > 1) return SPECDEC_ERR_INVALID_ARG;
   if (!a->q || !a->k || !a->v || !a->q_out || !a->table || !a->dev_status)
     return SPECDEC_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(a->q) % es || reinterpret_cast<uintptr_t>(a->k) % es ||

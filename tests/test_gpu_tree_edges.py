@@ -111,3 +111,27 @@ def test_a_value_that_is_not_finite_stays_in_its_dimension(dtype, T, G, hd, n, v
                 assert not np.isfinite(out[b, t][:, dims]).any()
             else:
                 np.testing.assert_array_equal(out[b, t], clean[b, t])
+
+
+def test_rotary_into_one_cache_row():
+    """Rows of an arena (one cache row): columns that are given are taken, a verification pass, whose
+    nodes would all go to the same columns, is refused."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    gen = torch.Generator().manual_seed(2)
+    B, T, H, hd = 3, 4, 2, 64
+    q, k, v = (torch.randn(B, T, H, hd, generator=gen).to(DEV) for _ in range(3))
+    cache, table, st = torch.zeros(1, 2, 1, H, 30, hd, device=DEV), R.make_table(20, hd), status()
+    pos, col = np.tile(np.arange(T), (B, 1)), np.array([[20, 21, 22, 23], [3, 4, 5, 6], [10, 11, 12, 13]])
+    out = torch.empty_like(q)
+    sd.rotary_append(q, k, v, cache, 0, table, out, st, positions=i32(pos), columns=i32(col))
+    want, cs = np.zeros((H, 30, hd)), numpy64(table)
+    for b in range(B):
+        want[:, col[b]] = numpy64(v)[b].transpose(1, 0, 2)
+        for t in range(T):
+            R.close(numpy64(cache)[0, 0, 0, :, col[b, t]], TO.rotate(numpy64(k)[b, t], cs[t, :, 0], cs[t, :, 1], False), numpy64(k)[b, t], torch.float32)
+    np.testing.assert_array_equal(numpy64(cache)[0, 1, 0], want)
+    before = cache.clone()
+    with pytest.raises(sd.SpecdecError):
+        sd.rotary_append(q, k, v, cache, 0, table, out, st, n_committed=i32([2, 2, 2]), width=i32([2]))
+    torch.cuda.synchronize()
+    assert int(st) == 0 and torch.equal(cache, before)
