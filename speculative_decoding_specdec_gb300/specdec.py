@@ -620,6 +620,13 @@ def _ints_of_any(t, name):
     return t.data_ptr()
 
 
+def _at_least(t, count, name):
+    """As _ints_of_any, of a tensor of which ``count`` values are read."""
+    if t is not None and t.numel() < count:
+        raise ValueError(f"{name} must have {count} values")
+    return _ints_of_any(t, name)
+
+
 def _given(t, name):
     if t is None:
         raise ValueError(f"{name} is needed")
@@ -714,8 +721,10 @@ def tree_attention(q, cache, layer, out, n_committed, width, parents, status, wo
     args = _PACK_ATTENTION.pack(
         *view, layer, B, T, Hq, hd ** -0.5 if scale is None else scale, qp, op, lp, qr, qt, outr,
         outt, np_, _ints_of_any(width, "width"), _ints(parents, (B, T), "parents"),
-        _ints(rows, (B,), "rows"), _ints_of_any(first_col, "first_col"), workspace.data_ptr(),
-        workspace.numel(), _ints_of_any(_given(status, "status"), "status"))
+        _ints(rows, (B,), "rows"),
+        _at_least(first_col, B if rows is None else n_committed.numel(), "first_col"),
+        workspace.data_ptr(), workspace.numel(),
+        _ints_of_any(_given(status, "status"), "status"))
     rc = lib.specdec_tree_attention(args, _raw(stream))
     if rc:
         _check(rc, "specdec_tree_attention")
@@ -792,8 +801,10 @@ def tree_commit(src, dst, width, accept_len, path, status, width_dst=None, nodes
         *sv, *(sv if dst is src else _kv(dst)), B, nodes, D, _ints_of_any(width, "width"),
         _ints_of_any(width_dst, "width_dst"),
         _ints(_given(accept_len, "accept_len"), one, "accept_len"), _ints(path, (B, D), "path"),
-        _ints_of_any(n_committed, "n_committed"), _ints(rows, one, "rows"),
-        _ints_of_any(first_col, "first_col"), _ints_of_any(_given(status, "status"), "status"))
+        _at_least(n_committed, B if rows is None else 1, "n_committed"), _ints(rows, one, "rows"),
+        _at_least(first_col, B if rows is None or n_committed is None else n_committed.numel(),
+                  "first_col"),
+        _ints_of_any(_given(status, "status"), "status"))
     rc = lib.specdec_tree_commit(args, _raw(stream))
     if rc:
         _check(rc, "specdec_tree_commit")

@@ -135,3 +135,26 @@ def test_rotary_into_one_cache_row():
         sd.rotary_append(q, k, v, cache, 0, table, out, st, n_committed=i32([2, 2, 2]), width=i32([2]))
     torch.cuda.synchronize()
     assert int(st) == 0 and torch.equal(cache, before)
+
+
+def test_slots_columns_and_lengths_go_together():
+    """Without ``rows`` there is a length and a first column per batch row, with it one of each per
+    slot: tensors that are too short are refused, not read behind their end."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    q = torch.zeros(3, 2, 2, 64, device=DEV)
+    arena = torch.zeros(1, 2, 1, 2, 40, 64, device=DEV)
+    st, ws = status(), torch.zeros(sd.tree_attention_workspace_bytes(q, arena), dtype=torch.uint8, device=DEV)
+    n3, c3, n5, c5, rows = i32([2, 2, 2]), i32([0, 10, 20]), i32([2] * 5), i32([0, 6, 12, 18, 24]), i32([4, 0, 2])
+    def attend(n, first, rows=None):
+        sd.tree_attention(q, arena, 0, torch.empty_like(q), n, None, None, st, ws, first_col=first, rows=rows)
+    def commit(n, first, rows=None):
+        sd.tree_commit(arena, arena, None, i32([1, 0, 1]), i32([[1], [-1], [1]]), st, nodes=2, n_committed=n, first_col=first, rows=rows)
+    for call in (attend, commit):
+        call(n3, c3)
+        call(n5, c5, rows)
+        call(n3, c5)
+        for bad in ((n3, c3[:2]), (n3[:2], c3), (n3[:1], c3[:1]), (n5, c3, rows)):
+            with pytest.raises(ValueError):
+                call(*bad)
+    torch.cuda.synchronize()
+    assert int(st) == 0
