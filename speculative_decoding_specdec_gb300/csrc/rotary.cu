@@ -69,7 +69,13 @@ __device__ bool locate(const RotaryParams& p, int b, int t, int& pos, int& col) 
       pos = -1;
       return false;
     }
-    pos = n - 1 + depth;
+    // (a width near the integers' end is beyond every cache, and its columns must not wrap around)
+    if (W > p.cap - t) {
+      if (threadIdx.x == 0) set_status(p.status, SPECDEC_ERR_CAPACITY);
+      pos = -1;
+      return false;
+    }
+    pos = n - 1 + depth;  // at most W - 1 + t
     col = W - 1 + t;
   }
   if (pos < 0 || pos >= p.table_len || col >= p.cap) {
@@ -186,7 +192,7 @@ int launch_rotary(const RotaryParams& p, int B, cudaStream_t s) {
   const bool vec = bits % 16 == 0 && p.rot % (2 * N) == 0 && p.hd % (2 * N) == 0;
   // few tokens: a token's heads over several CTAs
   const int per_pass = kThreads / (p.hd / (2 * (vec ? N : 1))), passes = (p.Hq + 2 * p.H + per_pass - 1) / per_pass;
-  const int want = (4 * std::max(1, sm_count()) + B * p.T - 1) / (B * p.T);
+  const int want = (4 * std::max(1, sm_count()) - 1) / (B * p.T) + 1;
   const dim3 grid(B * p.T, std::max(1, std::min(want, passes)));
   if (vec && p.interleaved) rotary_kernel<T, N, true><<<grid, kThreads, 0, s>>>(p);
   else if (vec) rotary_kernel<T, N, false><<<grid, kThreads, 0, s>>>(p);

@@ -158,3 +158,26 @@ def test_slots_columns_and_lengths_go_together():
                 call(*bad)
     torch.cuda.synchronize()
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("W", [2 ** 31 - 1, 2 ** 31 - 3, 12])
+@pytest.mark.parametrize("tree", [False, True])
+def test_rotary_at_a_width_beyond_the_cache(W, tree):
+    """Columns W - 1 + t that the cache does not have, the largest integers among them: reported, and
+    nothing is written for those nodes."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    gen = torch.Generator().manual_seed(6)
+    B, T, H, hd, cap = 2, 5, 2, 64, 14
+    q, k, v = (torch.randn(B, T, H, hd, generator=gen).to(DEV) for _ in range(3))
+    cache = torch.randn(1, 2, B, H, cap, hd, generator=gen).to(DEV)
+    want, table, st = cache.clone(), R.make_table(30, hd), status()
+    out = torch.full_like(q, 7.0)
+    par = None if not tree else i32([[-1, 0, 0, 1, 3]] * B)
+    sd.rotary_append(q, k, v, cache, 0, table, out, st, n_committed=i32([3, 12]), width=i32([W]), parents=par)
+    torch.cuda.synchronize()
+    assert int(st) == sd.ERR_CAPACITY
+    fit = max(0, min(T, cap + 1 - W))
+    assert torch.equal(cache[..., :11, :], want[..., :11, :]) and (fit > 0 or torch.equal(cache, want))
+    if fit:
+        assert torch.equal(cache[0, 1, :, :, W - 1:W - 1 + fit], v[:, :fit].transpose(1, 2))
+    assert (out[:, fit:] == 7).all() and (out[:, :fit] != 7).any() == (fit > 0)
