@@ -20,7 +20,8 @@ struct CommitParams {
   ByteView src, dst;
   const int32_t *width, *width_dst, *accept_len, *path, *n_committed, *rows, *first_col;
   int32_t* status;
-  int B, T, D, L, H, src_cap, dst_cap, col_vecs, src_one_row;
+  int B, T, D, src_cap, dst_cap, src_one_row;
+  unsigned L, H, col_vecs;
 };
 
 __global__ void __launch_bounds__(kThreads) commit_kernel(const CommitParams p) {
@@ -63,10 +64,11 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const CommitParams p) 
     return;
   }
   const long long row = p.src_one_row ? 0 : b;
-  const int total = p.L * 2 * p.H * p.col_vecs;
-  for (int u = blockIdx.y * kThreads + threadIdx.x; u < total; u += gridDim.y * kThreads) {
+  // (unsigned: below 2^31 vectors, and a step more, which is below 2^24, does not wrap around)
+  const unsigned total = 2u * p.L * p.H * p.col_vecs, step = gridDim.y * kThreads;
+  for (unsigned u = blockIdx.y * kThreads + threadIdx.x; u < total; u += step) {
     const int vec = u % p.col_vecs;
-    int q = u / p.col_vecs;
+    unsigned q = u / p.col_vecs;
     const int h = q % p.H;
     q /= p.H;
     const int kv = q & 1, l = q >> 1;
@@ -142,7 +144,7 @@ extern "C" int specdec_tree_commit(const specdec_tree_commit_args* a, void* stre
   p.H = s.heads;
   p.src_cap = s.cap_cols;
   p.dst_cap = d.cap_cols;
-  p.col_vecs = static_cast<int>(vecs);
+  p.col_vecs = static_cast<unsigned>(vecs);
   p.src_one_row = s.rows == 1 ? 1 : 0;
   // every thread one vector where the grid's second dimension allows it
   const int slices = static_cast<int>((total + kThreads - 1) / kThreads);

@@ -181,3 +181,20 @@ def test_rotary_at_a_width_beyond_the_cache(W, tree):
     if fit:
         assert torch.equal(cache[0, 1, :, :, W - 1:W - 1 + fit], v[:, :fit].transpose(1, 2))
     assert (out[:, fit:] == 7).all() and (out[:, :fit] != 7).any() == (fit > 0)
+
+
+def test_commit_of_nearly_two_to_the_31_vectors():
+    """As many layers and heads as a call takes (repeated views of one head's columns): the count of
+    vectors and the grid's step add up behind 2^31."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    src, dst = torch.randn(1, 2, 1, 1, 9, 4, device=DEV), torch.randn(1, 2, 1, 1, 12, 4, device=DEV)
+    want, st = dst.clone(), status()
+    want[..., 6:8, :] = src[..., [4, 7], :]
+    def wide(t):
+        return t.expand(32767, -1, -1, 32768, -1, -1)
+    sd.tree_commit(wide(src), wide(dst), i32([4]), i32([2]), i32([[1, 4, -1]]), st, width_dst=i32([9]), nodes=6)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and torch.equal(dst, want)
+    with pytest.raises(sd.SpecdecError):
+        sd.tree_commit(src.expand(32768, -1, -1, 32768, -1, -1), dst.expand(32768, -1, -1, 32768, -1, -1), i32([4]), i32([2]),
+                       i32([[1, 4, -1]]), st, width_dst=i32([9]), nodes=6)
