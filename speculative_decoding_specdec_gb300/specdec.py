@@ -733,12 +733,13 @@ def tree_attention(q, cache, layer, out, n_committed, width, parents, status, wo
 def _scores(t, name):
     """(address, dtype code, B, T, V, row stride) of evenly spaced score rows [B, T, V]."""
     shape, s, code = t.shape, t.stride(), _DTYPES.get(t.dtype)
-    if len(shape) != 3 or s[2] != 1 or (shape[0] > 1 and s[0] != shape[1] * s[1]):
+    if len(shape) != 3 or s[2] != 1 or (shape[0] > 1 and shape[1] > 1 and s[0] != shape[1] * s[1]):
         raise ValueError(f"{name}: expected [B, T, V] with evenly spaced rows of unit stride")
     if code is None or not t.is_cuda:
         raise ValueError(f"{name}: expected a float32 or bfloat16 CUDA tensor")
     # (a row stride below V, as an expanded tensor has, is refused by the library)
-    return t.data_ptr(), code, shape[0], shape[1], shape[2], s[1]
+    return (t.data_ptr(), code, shape[0], shape[1], shape[2],
+            s[0] if shape[1] == 1 and shape[0] > 1 else s[1])
 
 
 def verify_tree_greedy(logits, tokens, parents, accept_len, out_token, path, draft, status,

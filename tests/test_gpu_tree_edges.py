@@ -10,6 +10,7 @@ import torch
 import oracle.tree_oracle as TO
 import test_gpu_rotary as R
 import test_gpu_tree_attention as A
+import test_gpu_tree_verify as V
 from tree_testlib import DEV, i32, numpy64, random_parents, status
 
 pytestmark = pytest.mark.gpu
@@ -198,3 +199,25 @@ def test_commit_of_nearly_two_to_the_31_vectors():
     with pytest.raises(sd.SpecdecError):
         sd.tree_commit(src.expand(32768, -1, -1, 32768, -1, -1), dst.expand(32768, -1, -1, 32768, -1, -1), i32([4]), i32([2]),
                        i32([[1, 4, -1]]), st, width_dst=i32([9]), nodes=6)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_scores_of_one_position_of_a_longer_pass(dtype):
+    """One token per row whose scores are a slice [:, -1:] of a pass over several: evenly spaced rows."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    rng = np.random.default_rng(5)
+    z = torch.as_tensor(rng.normal(size=(3, 4, 600)) * 3, dtype=torch.float32).to(dtype).to(DEV)
+    tok, u = np.zeros((3, 1), int), np.array([[0.1], [0.5], [0.9]], np.float32)
+    for s in (z[:, -1:], z[:1, 1:2], z[:, :1]):
+        B = s.shape[0]
+        got, st = V.run_greedy(s, tok[:B], None, 1)
+        assert st == 0 and got[0].tolist() == [0] * B
+        assert got[1].tolist() == [TO.greedy_choice(r) for r in numpy64(s)[:, 0]]
+        got, st = V.run_sample(s, s, tok[:B], None, u[:B], 1.0, 1, False)
+        assert st == 0 and got[0].tolist() == [0] * B
+        for b in range(B):
+            edges = np.cumsum(TO.softmax(numpy64(s)[b, 0]))
+            y = int(got[1][b])
+            assert (edges[y - 1] if y else 0) - 1e-5 <= u[b, 0] <= edges[y] + 1e-5
+    with pytest.raises(ValueError):
+        sd.verify_tree_greedy(z[:, :2], i32(np.zeros((3, 2))), None, *V.outputs(3, 1), status())
