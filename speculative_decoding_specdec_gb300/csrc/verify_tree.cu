@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) tree_greedy_kernel(const TreeParams 
         for (int r = 1; r < p.C; ++r) key = max(key, s_all[tid][r]);
         s_choice[tid] = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
       }
-      __syncthreads();
+      alive = __syncthreads_and(alive) != 0;  // (a wait that gave up did so for all)
     }
     for (int cur = 0, n = 0; alive; ++n) {
       int choice;
@@ -471,7 +471,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
     t = warp_merged(t);
     if (inner) q = warp_merged(q);
     const float4* rec = exchange(make_float4(t.m, t.l, q.m, q.l));
-    if (!alive) break;
     MaxSum tt{-INFINITY, 0.f}, qq{-INFINITY, 0.f};
     for (int i = lane; i < records; i += 32) {
       const float4 y = rec[i];
@@ -480,12 +479,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
     }
     tt = warp_merged(tt);
     if (inner) qq = warp_merged(qq);
-    if (!(tt.l > 0.f && tt.l < INFINITY && tt.m < INFINITY) ||
-        (inner && !(qq.l > 0.f && qq.l < INFINITY && qq.m < INFINITY))) {
-      if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
-      draw = false;
-      break;
-    }
+    const bool fine = tt.l > 0.f && tt.l < INFINITY && tt.m < INFINITY &&
+                      (!inner || (qq.l > 0.f && qq.l < INFINITY && qq.m < INFINITY));
     if (tid == 0) {
       st.mt = tt.m;
       st.it = 1.f / tt.l;
@@ -494,7 +489,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
       st.k = 0;
     }
     sum_masses(rec, tt.m);
-    __syncthreads();
+    // One warp's wait may give up where another's does not: all leave together, or barriers would wait
+    // for those that have left.
+    if (!(alive = __syncthreads_and(alive) != 0)) break;
+    if (!fine) {
+      if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
+      draw = false;
+      break;
+    }
     bool accepted = false;
     while (child < p.T) {
       const int c = w.tok[child];
@@ -523,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
         });
         sum = warp_sum(sum);
         rec = exchange(make_float4(sum.x, sum.y, 0.f, 0.f));
-        if (!alive) break;
         sum = make_float2(0.f, 0.f);
         for (int i = lane; i < records; i += 32) {
           sum.x += rec[i].x;
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
           st.iqs[st.k] = Q > 0.f ? 1.f / Q : 0.f;
           ++st.k;
         }
-        __syncthreads();
+        if (!(alive = __syncthreads_and(alive) != 0)) break;
       }
       child = next_child(w, p.T, cur, child, [](int) { return true; });
     }
