@@ -680,7 +680,8 @@ int specdec_verify_tree_greedy(const void* logits, int dtype, int B, int T, int 
  *   without children are not used.
  * The walk starts at node 0.  At a node its children c are tried in order: child i (token x) is
  * accepted iff u[b][i] < p(x) / q(x) and the walk goes on there; otherwise p becomes
- * normalize(max(0, p - q)) (p stays where that is zero everywhere) and, unless `replacement`, q
+ * normalize(max(0, p - q)) (p stays where that is zero everywhere, or sums to less than 2^-126, the
+ * smallest number that the probabilities are held in) and, unless `replacement`, q
  * becomes q without x, normalised (siblings drawn without replacement; with `replacement` != 0
  * they were drawn independently and q stays).  With every child rejected, at a leaf or at depth
  * D, the token is drawn from p: the first index whose running sum exceeds u[b][0] * (total).

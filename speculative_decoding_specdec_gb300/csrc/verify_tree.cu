@@ -262,6 +262,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The smallest normal number.  A residual below it counts as none: its inverse may be infinite, and
+// infinity times the zeros of the residual NaN.
+constexpr float kLeastMass = 1.17549435e-38f;
+
 // p and q at the current node after `k` rejections: softmaxes of the two rows, then one step
 // max(0, p - q) / R and q without the rejected token, over Q, per rejection.
 struct Stage {
@@ -532,10 +536,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
         }
         sum = warp_sum(sum);
         const float R = sum.x, Q = sum.y;
-        if (R > 0.f) sum_masses(rec, -INFINITY);
+        const bool left = R >= kLeastMass;
+        if (left) sum_masses(rec, -INFINITY);
         if (tid == 0) {
           st.tok[st.k] = c;
-          st.ir[st.k] = R > 0.f ? 1.f / R : 0.f;
+          st.ir[st.k] = left ? 1.f / R : 0.f;
           st.iqs[st.k] = Q > 0.f ? 1.f / Q : 0.f;
           ++st.k;
         }

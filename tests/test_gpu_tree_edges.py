@@ -221,3 +221,16 @@ def test_scores_of_one_position_of_a_longer_pass(dtype):
             assert (edges[y - 1] if y else 0) - 1e-5 <= u[b, 0] <= edges[y] + 1e-5
     with pytest.raises(ValueError):
         sd.verify_tree_greedy(z[:, :2], i32(np.zeros((3, 2))), None, *V.outputs(3, 1), status())
+
+
+@pytest.mark.parametrize("replacement", [False, True])
+def test_a_residual_too_small_to_be_inverted_leaves_p(replacement):
+    """p and q agree but for tokens of about 2^-126: what a rejection leaves is a sum whose inverse is
+    infinite in fp32."""
+    z, w = torch.full((1, 2, 40), -float("inf")), torch.full((1, 2, 40), -float("inf"))
+    z[0, 0, [7, 20, 31]] = torch.tensor([0.0, -87.0, -87.0])
+    w[0, 0, [7, 20, 31]] = torch.tensor([0.0, -86.5, -87.1])
+    u = np.array([[0.5, 0.9]], np.float32)               # p / q of token 20 is 0.61
+    got, st = V.run_sample(z.to(DEV), w.to(DEV), np.array([[0, 20]]), np.array([[-1, 0]]), u, 1.0, 1, replacement)
+    assert st == 0
+    V.same_walk(got, 0, [], 7, [0, 20], 1)
