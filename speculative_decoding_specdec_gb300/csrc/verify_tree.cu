@@ -451,7 +451,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_sample_kernel(const TreePara
       float m = 0.f;
       if (lane < kWarps) {
         const float4 y = rec[warp * kWarps + lane];
-        m = top == -INFINITY ? y.x : y.x == -INFINITY ? 0.f : y.y * ex2(y.x - top);
+        // (near 2^-126, where ex2 gives zero, the roundings of y.x and of a score decide whether its
+        // probability is zero: a CTA counts only where some of its probabilities surely are not)
+        m = top == -INFINITY ? y.x : y.x - top < -125.f ? 0.f : y.y * ex2(y.x - top);
       }
       m = warp_sum(m);
       if (lane == 0) s_mass[warp] = m;

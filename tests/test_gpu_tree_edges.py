@@ -234,3 +234,25 @@ def test_a_residual_too_small_to_be_inverted_leaves_p(replacement):
     got, st = V.run_sample(z.to(DEV), w.to(DEV), np.array([[0, 20]]), np.array([[-1, 0]]), u, 1.0, 1, replacement)
     assert st == 0
     V.same_walk(got, 0, [], 7, [0, 20], 1)
+
+
+def test_a_draw_of_zero_beside_probabilities_that_round_to_zero():
+    """u = 0 takes the first token of any probability.  A slice of the vocabulary holds one score where
+    2^x is just not zero or just zero, as the roundings have it: the token is one that has a
+    probability, whichever that is."""
+    c2 = np.float32(1.4426950408889634)
+    top = np.linspace(1, 20, 4001).astype(np.float32)[:, None]
+    mt = top * c2
+    x = ((np.float64(mt) - 126) / np.float64(c2)).astype(np.float32)
+    x = (x + np.arange(-4, 5) * np.spacing(x)).astype(np.float32)
+    twice = x * c2 - mt                                                         # rounded, and again
+    once = (x.astype(np.float64) * np.float64(c2) - np.float64(mt)).astype(np.float32)
+    at = (twice >= -126) & (once < -126)
+    pick, top = torch.as_tensor(x[at])[:32], torch.as_tensor(np.broadcast_to(top, x.shape)[at])[:32]
+    assert len(pick) > 8
+    for V_ in (4096, 32768):
+        z = torch.full((len(pick), 1, V_), -float("inf"))
+        z[:, 0, 3], z[:, 0, V_ - 6] = pick, top
+        u = np.zeros((len(pick), 1), np.float32)
+        got, st = V.run_sample(z.to(DEV), z.to(DEV), np.zeros((len(pick), 1), int), None, u, 1.0, 1, False)
+        assert st == 0 and set(got[1].tolist()) <= {3, V_ - 6}
