@@ -256,3 +256,106 @@ def test_a_draw_of_zero_beside_probabilities_that_round_to_zero():
         u = np.zeros((len(pick), 1), np.float32)
         got, st = V.run_sample(z.to(DEV), z.to(DEV), np.zeros((len(pick), 1), int), None, u, 1.0, 1, False)
         assert st == 0 and set(got[1].tolist()) <= {3, V_ - 6}
+
+
+@pytest.mark.parametrize("dtype,V_", [(torch.float32, 262147), (torch.bfloat16, 400009)])
+@pytest.mark.parametrize("replacement", [False, True])
+def test_sampled_vocabularies_that_no_cluster_holds(dtype, V_, replacement):
+    """Slices too large for shared memory are read again in every pass, and the draw goes over them
+    in several windows: the token is one near the start, in the middle and at the end."""
+    rng = np.random.default_rng(V_)
+    par, tok = np.array([[-1, 0, 0, 1, -2]] * 6), np.zeros((6, 5), int)
+    z = rng.normal(size=(6, 5, V_))
+    heavy = np.r_[2, rng.integers(0, V_, 9), V_ - 2]
+    z[:, :, heavy] = np.log(V_) - 0.2 * np.arange(len(heavy))
+    z = torch.as_tensor(z, dtype=torch.float32).to(dtype)
+    w = (z.float() + 0.5 * torch.as_tensor(rng.normal(size=z.shape), dtype=torch.float32)).to(dtype)
+    for b in range(6):
+        for node in (0, 1):
+            kids = TO.children(par[b], node)
+            tok[b, kids] = rng.choice(heavy, len(kids), replace=False)
+    u = rng.random((6, 5)).astype(np.float32)
+    u[2:4, 1:] = 0.9999                       # children are rejected: the draw is from the residual
+    zz, ww, want = numpy64(z), numpy64(w), []
+    for b in range(6):                        # u[0] in the middle of a heavy token's share
+        path, _, p, margins = TO.verify_sample(zz[b], ww[b], tok[b], par[b], u[b].astype(np.float64), 0.9, 3, replacement)
+        edges = np.cumsum(p)
+        likely = np.flatnonzero(p > 2e-3)
+        y = int(likely[(0, -1, len(likely) // 2)[b % 3]])
+        u[b, 0] = (edges[y] - p[y] / 2) / edges[-1]
+        want.append((path, y, min(margins)))
+    got, st = V.run_sample(z.to(DEV), w.to(DEV), tok, par, u, 0.9, 3, replacement)
+    assert st == 0
+    assert sum(m < 1e-4 for _, _, m in want) <= 1
+    for b, (path, y, margin) in enumerate(want):
+        if margin >= 1e-4:
+            V.same_walk(got, b, path, y, tok[b], 3)
+
+
+@pytest.mark.parametrize("T,G", [(40, 2), (40, 4)])
+def test_a_unit_of_very_many_parts(T, G):
+    """One K/V head over so many columns that more shares hold parts of it than the merge takes in
+    at a time."""
+    rng = np.random.default_rng(T * G)
+    n = np.array([20011])
+    q, cache, W = A.inputs(rng, 1, T, G, 1, 128, n, torch.bfloat16, layers=2)
+    par = random_parents(rng, 1, T, unused=0.1)
+    A.hide(cache, n, W, T, par)
+    out, lse, st = A.run(q, cache, 1, n, W, par)
+    assert st == 0
+    A.check(out, lse, q, cache, 1, n, W, par)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_trees_path_is_appended_to_its_pool_slots(dtype):
+    """Rounds of a pool with trees: gathered into the padded buffer or verified in their slots, the
+    committed paths appended as a chain's drafts are; every slot then holds its sequence's columns."""
+    import speculative_decoding_specdec_gb300.specdec as sd
+    rng = np.random.default_rng(3)
+    S, cap, L, H, hd, T, D, vocab = 7, 90, 2, 2, 64, 10, 4, 200
+    lens = [5, 17, 30, 17, 2, 17, 11]
+    rows = [list(rng.integers(0, vocab, n)) for n in lens]
+    tag = torch.randn(cap, vocab, L, 2, H, hd, generator=torch.Generator().manual_seed(0)).to(dtype).to(DEV)
+    arena = torch.full((L, 2, 1, H, S * cap, hd), float("nan"), dtype=dtype, device=DEV)
+    ids = np.zeros((S, cap), int)
+    for s, r in enumerate(rows):
+        ids[s, :len(r)] = r
+        for i, x in enumerate(r[:-1]):
+            arena[:, :, 0, :, s * cap + i] = tag[i, x]
+    col, caps, length, pool_ids = i32(np.arange(S) * cap), i32([cap] * S), i32(lens), i32(ids)
+    scratch = torch.full((L, 2, 4, H, 80, hd), float("nan"), dtype=dtype, device=DEV)
+    sids, smask, spos = (torch.zeros(4, 80, dtype=d, device=DEV) for d in (torch.int32, torch.uint8, torch.int32))
+    blen, width, st = i32(np.zeros(4)), i32([0]), status()
+    for batch, in_place in (([0, 2, 4], False), ([1, 3, 5], True), ([6, 0, 3, 1], False), ([5, 2], False)):
+        B = len(batch)
+        slots = i32(batch)
+        sd.pool_gather(arena, scratch, slots, D, col, caps, length, pool_ids, blen[:B], width, st, sids, smask, spos, in_place=in_place)
+        par = random_parents(rng, B, T, unused=0.1)
+        z, tok = np.full((B, T, vocab), -1.0), rng.integers(0, vocab, (B, T))
+        for b, s in enumerate(batch):
+            tok[b, 0] = rows[s][-1]
+            for t in range(T):
+                line = TO.line_of(par[b], t)
+                if line:
+                    where = (s * cap + len(rows[s]) - 1) if in_place else int(width) - 1
+                    (arena[:, :, 0] if in_place else scratch[:, :, b])[:, :, :, where + t] = tag[len(rows[s]) - 2 + len(line), tok[b, t]]
+                kids = TO.children(par[b], t)
+                z[b, t, tok[b, kids[-1]] if kids and rng.random() < 0.8 else rng.integers(vocab)] = 1
+        a, y, path, draft = V.outputs(B, D)
+        sd.verify_tree_greedy(torch.as_tensor(z, dtype=torch.float32).to(DEV), i32(tok), i32(par), a, y, path, draft, st)
+        if in_place:
+            sd.tree_commit(arena, arena, None, a, path, st, nodes=T, n_committed=length, rows=slots, first_col=col)
+        else:
+            sd.tree_commit(scratch, scratch, width, a, path, st, nodes=T)
+        sd.pool_append(arena, scratch, slots, D, col, caps, length, pool_ids, blen[:B], width, a, y, draft, st, in_place=in_place)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        for b, s in enumerate(batch):
+            nodes, token = TO.verify_greedy(z[b], tok[b], par[b], D)
+            V.same_walk([x.cpu().numpy() for x in (a, y, path, draft)], b, nodes, token, tok[b], D)
+            rows[s] += [int(tok[b, i]) for i in nodes] + [token]
+        assert length.tolist() == [len(r) for r in rows]
+    for s, r in enumerate(rows):
+        assert pool_ids[s, :len(r)].tolist() == r
+        for i, x in enumerate(r[:-1]):
+            assert torch.equal(arena[:, :, 0, :, s * cap + i], tag[i, x])
