@@ -199,8 +199,11 @@ def rotary_table(positions, rot_dim, base=10000.0, scaling=None, factor=1.0, ori
       - "linear": every frequency divided by ``factor``;
       - "base":   the base raised so that the lowest frequency is divided by ``factor``;
       - "bands":  frequencies that turn less than ``beta_slow`` times within ``original`` positions
-        divided by ``factor``, those that turn more than ``beta_fast`` times kept, a linear ramp
-        between, and cosines and sines times 0.1 ln(factor) + 1."""
+        divided by ``factor``, those that turn more than ``beta_fast`` times kept, between them a ramp
+        that is linear in the turns, and cosines and sines times 0.1 ln(factor) + 1: as published by
+        Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models".  Weights
+        that were run with a ramp along the pair's index, or without the amplitude, need a table of
+        their own: the operator takes any."""
     half = rot_dim // 2
     if rot_dim < 2 or rot_dim % 2 or positions < 1 or factor <= 0:
         raise ValueError("rot_dim must be even and positive, positions and factor positive")
@@ -214,6 +217,8 @@ def rotary_table(positions, rot_dim, base=10000.0, scaling=None, factor=1.0, ori
     elif scaling == "bands":
         if original < 1:
             raise ValueError("bands need the original number of positions")
+        if not beta_fast > beta_slow:
+            raise ValueError("beta_fast must be above beta_slow")
         turns = original * freq / (2 * math.pi)
         keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
         freq = freq * (keep + (1 - keep) / factor)
