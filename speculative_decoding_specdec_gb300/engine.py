@@ -208,7 +208,9 @@ def rotary_table(positions, rot_dim, base=10000.0, scaling=None, factor=1.0, ori
     if rot_dim < 2 or rot_dim % 2 or positions < 1 or factor <= 0:
         raise ValueError("rot_dim must be even and positive, positions and factor positive")
     i = torch.arange(half, dtype=torch.float64)
-    if scaling == "base" and half > 1:
+    if scaling == "base":
+        if half == 1:
+            raise ValueError("the base changes nothing about a single frequency")
         base = base * factor ** (half / (half - 1))
     freq = base ** (-i / half)
     amplitude = 1.0

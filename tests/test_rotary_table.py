@@ -29,6 +29,7 @@ def test_bands_ramp_with_the_turns_within_the_trained_length(rot, base, factor, 
 @pytest.mark.parametrize("bad", [
     dict(scaling="bands", original=64, beta_fast=1.0, beta_slow=1.0),    # no ramp between
     dict(scaling="bands", original=64, beta_fast=1.0, beta_slow=32.0),
+    dict(scaling="base", rot_dim=2),                                     # one frequency, always 1
     dict(scaling="bands", original=64, beta_fast=float("nan"))])
 def test_settings_without_a_table_are_refused(bad):
     with pytest.raises(ValueError):
