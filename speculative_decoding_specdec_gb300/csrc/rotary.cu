@@ -35,16 +35,13 @@ struct RotaryParams {
 };
 
 // Position and column of token t of row b; false if nothing is to be written to the cache for it:
-// with pos >= 0 its q_out is zero, with pos < 0 an error was recorded.  All threads of the CTA get
-// the same answer.
+// it is padding (col < 0) or an unused node (pos = 0), whose q_out is zero, or an error was recorded
+// (pos < 0 <= col).  All threads of the CTA get the same answer.
 __device__ bool locate(const RotaryParams& p, int b, int t, int& pos, int& col) {
   if (p.positions) {
     pos = p.positions[static_cast<long long>(b) * p.T + t];
     col = p.columns[static_cast<long long>(b) * p.T + t];
-    if (col < 0) {  // padding, whatever its position says
-      pos = 0;
-      return false;
-    }
+    if (col < 0) return false;
   } else {
     __shared__ int s_par[kMaxTree];
     const int n = p.n_committed[b], W = *p.width;
@@ -122,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams 
   const int b = blockIdx.x / p.T, t = blockIdx.x % p.T;
   int pos = 0, col = 0;
   const bool write = locate(p, b, t, pos, col);
-  if (!write && pos < 0) return;  // an error was recorded
+  if (!write && pos < 0 && col >= 0) return;  // an error was recorded
   // A thread keeps its place in the head, so its cosines and sines are read once for all heads.
   const int half = p.rot / 2, per_head = p.hd / (2 * N), turned = half / N;
   const int step = kThreads / per_head, j = threadIdx.x % per_head;
