@@ -615,6 +615,8 @@ int specdec_rotary_append(const specdec_rotary_args* args, void* stream);
  *              above).
  * Scores, the softmax's maximum and sum and the output's sum are held in fp32; with bf16 tensors
  * the softmax's weights are rounded to bf16 for the second matrix product.
+ * The kernel is chosen by dtype, T, heads, head_dim and the cache's capacity: results repeat bit for
+ * bit for one shape, and may round differently in a cache of another capacity.
  * Device-detected errors: N_b < 1, N_b > W, a negative row index or first column, a bad
  * parent (SPECDEC_ERR_INPUT_RANGE), a node's column beyond cache.cap_cols
  * (SPECDEC_ERR_CAPACITY); the row concerned is not written.
@@ -659,7 +661,8 @@ size_t specdec_tree_attention_workspace(int dtype, int B, int T, int heads_q, in
  *   accept_len [B] out: a_b, the accepted nodes;  out_token [B] out: the target's choice at the
  *           walk's last node;  path [B][D] out: the accepted nodes, -1 from a_b on;
  *   draft   [B][D] out: their tokens, 0 from a_b on (the drafts of a realignment or append).
- * Only the score rows on the walk are read.  A row without used nodes gives a_b = 0, token -1.
+ * Only the score rows on the walk enter the result (where the rows are small, those of all used
+ * nodes are read).  A row without used nodes gives a_b = 0, token -1.
  * A visited row of only NaN sets SPECDEC_ERR_INPUT_RANGE (the walk ends there with token -1); a
  * bad parent also does (that row's outputs are not written); a token outside [0, V) never
  * matches.  Limits: B >= 0, 1 <= T <= SPECDEC_MAX_TREE, 1 <= D <= SPECDEC_MAX_DRAFT, 1 <= V,
@@ -690,7 +693,7 @@ int specdec_verify_tree_greedy(const void* logits, int dtype, int B, int T, int 
  *   uniforms [B][T] float32 in [0, 1): u[b][0] for the draw, u[b][i] for node i;
  *   accept_len, out_token, path, draft  as for greedy verification.
  * Probabilities and sums in fp32 (sums of a row are taken pairwise over 16-byte vectors, threads
- * and CTAs).  Only the rows on the walk are read.  A score of -infinity is a token of probability
+ * and CTAs).  Only the rows on the walk enter the result.  A score of -infinity is a token of probability
  * zero (sampling settings such as top-k may be applied that way).
  * Device-detected errors (SPECDEC_ERR_INPUT_RANGE): a bad parent or a used uniform outside
  * [0, 1) (the row's outputs are not written); a token outside [0, V) on the walk (it is

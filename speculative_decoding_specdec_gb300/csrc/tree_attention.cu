@@ -8,7 +8,9 @@
 // against R broadcast reads of Q); for O a lane owns 4 (or 8) of the head's values (one read of V
 // and R / 4 broadcast reads of the weights for 4 R FMAs).  HBM bounds few rows, the
 // operands' shared-memory reads many: 16 rows of up to 4096 columns, 8 K/V heads: 4 query rows 80 us
-// (302 MB, 3.8 TB/s); one row of 65536 columns and 8 query rows: 195 us (2.8 TB/s).
+// (302 MB, 3.8 TB/s); one row of 65536 columns and 8 query rows: 193 us (2.8 TB/s).
+// bf16 heads of other sizes than 64 and 128 come here too: chains of 6, 32 heads of 96, 8 rows of up
+// to 1024 columns: 55 us.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -631,9 +633,11 @@ AttnShape fma_shape(int es, int T, int G, int hd) {
 }
 
 // The kernel and its shape for bf16 heads of 64 and 128 values: tiles of 8 or 16 query rows, or of
-// 256.  Up to 16 rows the former, whose tiles the latter would leave nearly empty; up to 32 rows it
-// is ahead on short work (2 rows of 100 columns, 8 K/V heads: 8.8 us in one launch against 9.0 in
-// two) and behind on long (16 rows of up to 4096 columns, 8 K/V heads: 47 us against 43).
+// 256.  Up to 16 rows the former, whose tiles the latter would leave nearly empty.  From 17 to 32 rows
+// by the columns that the cache has: the former is ahead on few (one row of 6400, 4 K/V heads, 25
+// thousand in all: 20 us against 41; 100 thousand: 22 against 27), the latter on many (200 thousand:
+// 31.0 against 31.4 and 34.7 against 34.2; 800 thousand: 73 against 67).  So the same tokens in a
+// cache of another capacity may take the other kernel, with other roundings.
 // `columns`: an upper bound of the columns of all units.
 AttnShape attn_shape(int es, int T, int G, int hd, long long columns) {
   if (es != 2 || (hd != 64 && hd != 128)) return fma_shape(es, T, G, hd);

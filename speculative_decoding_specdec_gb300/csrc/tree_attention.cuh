@@ -12,8 +12,9 @@
 // MT CTAs (MT M-tiles), so ragged lengths leave no CTA idle and the MT CTAs that stream the same
 // columns do so at the same time (one DRAM read, the rest from L2).  A unit that lies in one share
 // is finished by its CTA; one cut by share borders is written as partial results (m, l, o) to the
-// workspace, and the CTA that takes the unit's last ticket merges them in share order, so results
-// do not depend on which CTA came last.  A share has at most two cut units (its first and last).
+// workspace and merged in share order, so that results do not depend on which CTA came last: by the
+// CTA that takes the unit's last ticket, or (tensor-core kernel, whose parts are larger) by a launch
+// of its own.  A share has at most two cut units (its first and last).
 #pragma once
 
 #include "tree.cuh"

@@ -11,9 +11,8 @@
 // instructions for 8 rows.)  Each warp keeps
 // maximum, sum and O of its columns; the CTA's are merged in shared memory when the segment ends,
 // while the next segment's tiles are already on their way.
-// Measured: 8 rows of 128 to 1024 columns, 32 K/V heads, chains of 6: 23 us (3.3 TB/s, in
-// 256 units); one row of 131071 columns, 8 K/V heads of 4
-// query heads: 89 us (6.1 TB/s).
+// Measured: 8 rows of 128 to 1024 columns, 32 K/V heads, chains of 6: 24 us (3.2 TB/s, in
+// 256 units); one row of 131071 columns, 8 K/V heads of 4 query heads: 89 us (6.0 TB/s).
 #include <cmath>
 
 #include "tcgen05.cuh"

@@ -16,9 +16,10 @@
 // in flight.
 //
 // What bounds it.  512 rows over 4600 columns (32 trees of 32 nodes, 16 query heads per K/V head):
-// 86 us, 0.79 PFLOP/s; 256 rows over 131071 columns: 124 us, 1.11 PFLOP/s and 4.3 TB/s.  A tile pair
-// takes about 3300 cycles where its products take 2048 at the peak rate; a tile's softmax is 1600 to
-// 1740 of them.  About 10000 cycles pass before the first tile.
+// 86 us, 0.79 PFLOP/s; 256 rows over 131071 columns: 124 us, 1.10 PFLOP/s and 4.3 TB/s.  In the latter
+// a CTA takes 54 tile pairs in 212000 active cycles, 3900 a pair where its products take 2048 at the
+// peak rate (the tensor pipe is busy for 52 %): an accumulator's softmax stands between its two
+// products.  In the former the pipe is busy for 43 %: more segments are opened and closed.
 //
 // A tile that holds nodes' columns or the end of a row needs care: its V columns behind the nodes
 // and of unused nodes are zeroed in shared memory (0 * NaN is NaN in a matrix product), and so is
@@ -202,9 +203,9 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     // ------------------------------------------------------------------------------- MMA
     // The whole warp follows the jobs, A's and B's in turn, and one elected lane issues.  In turn,
     // so that one accumulator's softmax runs beside the other's products: with a warp for each, the
-    // two fell into step, and both waited while both computed.  A wait costs this warp about 200
-    // cycles even where there is nothing to wait for, with the tensor cores idle, so it has one per
-    // job: the softmax's threads see to V and the next K before they release the weights.  What an MMA's operands are made of
+    // two fell into step, and both waited while both computed.  A wait costs this warp time even
+    // where there is nothing to wait for, with the tensor cores idle, so it has one per job: the
+    // softmax's threads see to V and the next K before they release the weights.  What an MMA's operands are made of
     // is the same in all lanes and made so for the compiler to see (the shuffles): an MMA takes
     // its descriptors from uniform registers, and moving them there lane by lane took longer than
     // the products.
@@ -312,7 +313,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     int seg_no = 0, seen = 0, ends = 0, kv = 0;  // segments, jobs, accumulations, tiles so far
     // A thread copies its 16-byte chunk of every kPer-th Q row straight to shared memory (rows that
     // do not exist are zero): holding them in registers over the segment before made the compiler
-    // spill them, one round trip to memory each.  What the next segment will read is asked into L2.
+    // spill them, one round trip to memory each.
     constexpr int kChunks = HD / 8, kPer = 256 / kChunks, kLoads = 2 * kRows / kPer;
     const int qc = tid % kChunks, q0 = tid / kChunks, nq = two ? kLoads : kLoads / 2;
     auto ask = [&](const AttnSegment& sg) {
@@ -561,8 +562,9 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 }
 
 // Units that share borders cut, merged by a launch of their own: it spreads the parts over the GPU
-// and needs no tickets.  (The CTA that came last, merging alone, took about 20000 cycles
-// for 2 or 3 parts of 128 KB, one part after the other.)  CTA = border and 32 rows; thread = row and 4 * kPer of its values.
+// and needs no tickets, where the CTA that came last would add parts of 128 KB one after the other
+// behind the last share.  CTA = border and 32 rows; thread = row and 4 * kPer of its values.
+// Measured alone and cold (ncu), 75 borders of 512 rows: 14.7 us for 30 MB, the loads' latency.
 template <int HD>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   constexpr int kPer = HD / 32;  // float4 a thread holds

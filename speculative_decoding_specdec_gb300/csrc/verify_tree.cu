@@ -11,15 +11,17 @@
 //
 // GB300 mapping.  A walk visits few of the T rows (one more than it accepts), and which ones is
 // known only on the way, so one thread-block cluster walks one batch row and reads the visited
-// rows alone.  Its CTAs split the vocabulary; every step ends in one exchange (each CTA writes its
-// record into every CTA's shared memory, a cluster barrier, everyone reduces the records in rank
-// order), after which all threads of the cluster hold the same decision and no result has to be
-// sent back.  Two record buffers alternate: the barrier between two exchanges separates a
-// record's readers from its next writer.
-// What bounds it: the chain of dependent steps (row latency, block reduction, cluster barrier);
-// the visited rows are a few hundred KB per step.  Measured: greedy, 8 trees of 16 nodes, V 32000:
-// 9.4 us; 16 trees of 64 nodes, V 151936: 21 us; sampled, 32 trees of 16 nodes, V 151552: 45 us, where
-// a node takes 2500 cycles to load, 3000 to 5000 to fold and 4400 to 6500 to exchange.
+// rows alone (greedy: all used rows at once where they are small, see launch_greedy).  Its CTAs split
+// the vocabulary; every step ends in one exchange: each warp stores its record into every CTA's
+// shared memory, by stores that count their bytes on a barrier there, and every warp reduces all
+// records in rank order.  All threads of the cluster then hold the same decision and no result has to
+// be sent back.  Two record buffers alternate.  A buffer is written again by exchange n + 2, which a
+// warp sends after it has received all of exchange n + 1, and every warp sends its part of that after
+// it has read exchange n: no record is overwritten before it was read.
+// What bounds it: the chain of dependent steps (row latency, reduction, exchange); the visited rows
+// are a few hundred KB per step.  Measured: greedy, 8 trees of 16 nodes, V 32000: 9.5 us; 16 trees of
+// 64 nodes, V 151936: 21 us; sampled, 32 trees of 16 nodes, V 151552: 45 us (67000 cycles, of which
+// the special-function unit is busy for 16 %, issue 47 %; barriers and loads are waited for most).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -727,7 +729,11 @@ template <typename T>
 int launch_greedy(TreeParams& p, int B, cudaStream_t s) {
   static int caches[2][64 * 17];
   // All rows at once where a CTA's share of them takes it less time than the steps of a walk do:
-  // about 2 us a step against 25 KB a us and CTA, and 30 MB in all.
+  // about 2 us a step against 25 KB a us and CTA, and 30 MB in all.  bf16, 8 rows, about two accepted
+  // nodes, all at once against one by one: V 4000, 16 nodes 8.1 | 10.4 us, 32 nodes (256 KB a CTA)
+  // 11.1 | 8.3; V 32000, 16 nodes 8.4 | 11.2, 32 nodes 11.6 | 9.2; V 151936, 4 nodes 10.4 | 9.1 (the
+  // rule's loss), 8 nodes 12.7 | 11.8; 32 rows, V 32000, 16 nodes (31 MB) 11.6 | 13.6.  A walk that
+  // accepts nothing is ahead one by one throughout (V 32000, 16 nodes, one row: 7.6 | 5.5).
   p.C = tree_cluster(tree_greedy_kernel<T, true>, B, p.V, sizeof(T), 0, caches[0]);
   const long long bytes = static_cast<long long>(p.T) * p.V * sizeof(T);
   if (bytes / p.C <= (128 << 10) && bytes * B <= (30 << 20))
