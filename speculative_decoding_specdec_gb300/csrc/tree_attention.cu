@@ -345,8 +345,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
   }
   if (!ok) {
     set_status(p.status, SPECDEC_ERR_TIMEOUT);
-    // no copy outlives the CTA: those asked for and not waited for have landed
-    for (int i = used; i < loaded; ++i)
+    // no copy outlives the CTA: each stage's last one, which may be the one whose wait gave up, is
+    // waited for (a stage is filled again only when its copy before has landed)
+    for (int i = max(0, loaded - kStages); i < loaded; ++i)
       (void)mbar_wait_sleep(&s_full[warp][i % kStages], (i / kStages) & 1, kTries, kNs);
   }
 }
