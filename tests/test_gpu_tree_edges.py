@@ -359,3 +359,17 @@ def test_a_trees_path_is_appended_to_its_pool_slots(dtype):
         assert pool_ids[s, :len(r)].tolist() == r
         for i, x in enumerate(r[:-1]):
             assert torch.equal(arena[:, :, 0, :, s * cap + i], tag[i, x])
+
+
+@pytest.mark.parametrize("dtype,hd", [(torch.float32, 4), (torch.float32, 12), (torch.bfloat16, 8), (torch.bfloat16, 40), (torch.float32, 252), (torch.bfloat16, 248)])
+@pytest.mark.parametrize("T,G", [(1, 1), (3, 4), (16, 3)])
+def test_the_smallest_and_oddest_heads(dtype, hd, T, G):
+    """Heads of one 16-byte vector and of numbers of vectors that divide nothing."""
+    rng = np.random.default_rng(hd + T)
+    n = np.array([70, 3])
+    q, cache, W = A.inputs(rng, 2, T, G, 1, hd, n, dtype)
+    par = random_parents(rng, 2, T, unused=0.1)
+    A.hide(cache, n, W, T, par)
+    out, lse, st = A.run(q, cache, 1, n, W, par)
+    assert st == 0
+    A.check(out, lse, q, cache, 1, n, W, par)
