@@ -71,7 +71,7 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 
 struct Bars {
   uint64_t k_full[kMaxKStages], k_empty[kMaxKStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2], drained;
 };
 
 // Pairs of floats: one instruction for two.
@@ -151,6 +151,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     }
     mbar_init(&bar.q_full, 256);
     mbar_init(&bar.v_clean, 1);
+    mbar_init(&bar.drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_ready[i], 128);
@@ -295,6 +296,11 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         if (i + 2 < jobs) scores(i + 2);
       }
       kv += n;
+    }
+    // where a wait gave up, products may still be on their way to tensor memory, which is freed below
+    if (!ok) {
+      if (elect_one()) mma_commit(&bar.drained);
+      (void)warp_wait(&bar.drained, 0);
     }
   }
   } else {
@@ -550,6 +556,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       }
       named_bar_sync(1, 256);  // the next segment's ancestors are there
     }
+    if (!ok) cp_async_wait_all();  // (Q of a segment that was not opened)
   }
   if (!ok) set_status(p.status, SPECDEC_ERR_TIMEOUT);
   __syncwarp();
