@@ -603,8 +603,8 @@ int specdec_rotary_append(const specdec_rotary_args* args, void* stream);
  *   natural logarithm of the sum of exp(scale * q . k).
  * An unused node gives zeros (lse: -infinity).  Columns that a node does not see, and what they
  * hold (NaN included), do not enter its result; a value of V that is not finite in a column that it
- * sees enters that value of the head alone (and never lse); the cache beyond the nodes' columns and left of
- * the committed ones is not used.
+ * sees enters that value of the head alone (and never lse); the cache beyond the nodes' columns and
+ * left of the committed ones is not used.
  * Rows elsewhere than right-aligned in their own cache row (a pool's arena): first_col != NULL
  * gives the first column of each row's committed tokens, so that node i is at column
  * first_col + N_b - 1 + i (width is then not read and may be NULL); rows != NULL [B] makes batch
