@@ -593,6 +593,28 @@ typedef struct {
 int specdec_rotary_append(const specdec_rotary_args* args, void* stream);
 
 /*
+ * The same with norms of the heads of q and k before their rotation, as some models have them:
+ *   y = x / sqrt(mean of x^2 over the head + eps) * (weight_offset + weight),
+ * in fp32 over all head_dim values, then the rotation of the first rot_dim, rounded once.  v is copied.
+ *   q_weight, k_weight  [head_dim] of weight_dtype, each or both NULL: not normed (weight_offset 0, or 1
+ *       for models that hold their weights less one);
+ *   start  [B] or NULL: added to every position of row b, for rows that stand behind a prefix which
+ *       another cache holds (specdec_prefix_attention); columns are not moved by it.
+ * Everything else, errors and limits included, is as for specdec_rotary_append; besides, a negative
+ * start, or a position that it carries beyond the table, is SPECDEC_ERR_INPUT_RANGE.  eps finite and
+ * not negative, weight_offset finite; weights element-aligned.
+ */
+typedef struct {
+  specdec_rotary_args rotary;
+  const void *q_weight, *k_weight;
+  int weight_dtype;
+  float eps, weight_offset;
+  const int32_t* start;           /* [B], or NULL */
+} specdec_norm_rotary_args;
+
+int specdec_norm_rotary_append(const specdec_norm_rotary_args* args, void* stream);
+
+/*
  * Attention of a verification pass over one layer of the cache: the pending token and the
  * drafted nodes of every row against the row's committed columns and the nodes' own.
  *   out_i = sum_c p_ic v_c,  p_i = softmax over c of scale * (q_i . k_c),  where c runs over the

@@ -74,31 +74,6 @@ struct Bars {
   uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2], drained;
 };
 
-// Pairs of floats: one instruction for two.
-__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  return pack2u(__float_as_uint(lo), __float_as_uint(hi));
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 template <int HD> struct Smem {
   static constexpr int kQ = kRows * HD * 2, kTile = kCols * HD * 2;
   static constexpr int q = 0;                          // A's rows, then B's

@@ -100,6 +100,12 @@ class RotaryArgs(ctypes.Structure):
                 ("columns", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
+class NormRotaryArgs(ctypes.Structure):
+    _fields_ = [("rotary", RotaryArgs), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("start", ctypes.c_void_p)]
+
+
 class TreeAttentionArgs(ctypes.Structure):
     _fields_ = [("cache", KvView), ("layer", ctypes.c_int), ("B", ctypes.c_int),
                 ("T", ctypes.c_int), ("heads_q", ctypes.c_int), ("scale", ctypes.c_float),
@@ -165,6 +171,8 @@ lib.specdec_pool_admit.restype = _i
 lib.specdec_pool_admit.argtypes = [ctypes.POINTER(AdmitArgs), _vp]
 lib.specdec_rotary_append.restype = _i
 lib.specdec_rotary_append.argtypes = [_vp, _vp]  # specdec_rotary_args
+lib.specdec_norm_rotary_append.restype = _i
+lib.specdec_norm_rotary_append.argtypes = [_vp, _vp]  # specdec_norm_rotary_args
 lib.specdec_tree_attention.restype = _i
 lib.specdec_tree_attention.argtypes = [_vp, _vp]  # specdec_tree_attention_args
 lib.specdec_tree_attention_workspace.restype = _sz
@@ -579,7 +587,9 @@ def pool_admit(slots, cols, caps, limits, prompt_ids, prompt_off, D, arena_cols,
 # lay out the ctypes structures above), and a tensor's layout is read once.
 
 _KV = "Pqqqqiiiiii"
-_PACK_ROTARY = struct.Struct("@" + _KV + "iiiiiii" + "PPPP" + "qqqqqqqq" + "PPPPPPP")
+_ROTARY = _KV + "iiiiiii" + "PPPP" + "qqqqqqqq" + "PPPPPPP"
+_PACK_ROTARY = struct.Struct("@" + _ROTARY)
+_PACK_NORM_ROTARY = struct.Struct("@" + _ROTARY + "PPiffP")
 _PACK_ATTENTION = struct.Struct("@" + _KV + "iiiif" + "PPP" + "qqqq" + "PPPPPPnP")
 _PACK_COMMIT = struct.Struct("@" + _KV + _KV + "iii" + "PPPPPPPP")
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -643,13 +653,9 @@ def _tokens(t, shape, dtype, name):
     return t.data_ptr(), s[0], s[1]
 
 
-def rotary_append(q, k, v, cache, layer, table, q_out, status, n_committed=None, width=None,
-                  parents=None, positions=None, columns=None, interleaved=False, stream=None):
-    """Rotary positions of the new tokens' q [B, T, Hq, hd] (into ``q_out``) and k [B, T, H, hd],
-    and the append of k and v to their columns of ``cache`` [L, 2, rows, H, cap, hd], layer
-    ``layer``.  ``table`` [positions, rot_dim / 2, 2] float32 holds cosines and sines.  Columns and
-    positions come from a verification pass (``n_committed``, ``width`` and ``parents``, None for a
-    chain) or are given (``positions``, ``columns`` [B, T], negative columns: padding)."""
+def _rotary_fields(q, k, v, cache, layer, table, q_out, status, n_committed, width, parents,
+                   positions, columns, interleaved):
+    """The fields of specdec_rotary_args."""
     view = _kv(cache)
     dtype = cache.dtype
     shape = q.shape
@@ -674,12 +680,50 @@ def rotary_append(q, k, v, cache, layer, table, q_out, status, n_committed=None,
             raise ValueError("positions and columns exclude n_committed, width and parents")
         where = (0, 0, 0, _ints(_given(positions, "positions"), (B, T), "positions"),
                  _ints(_given(columns, "columns"), (B, T), "columns"))
-    args = _PACK_ROTARY.pack(*view, layer, B, T, Hq, 2 * tab[1], 1 if interleaved else 0, tab[0],
-                             qp, kp, vp, op, qr, qt, kr, kt, vr, vt, outr, outt, table.data_ptr(),
-                             *where, _ints_of_any(_given(status, "status"), "status"))
-    rc = lib.specdec_rotary_append(args, _raw(stream))
+    return (*view, layer, B, T, Hq, 2 * tab[1], 1 if interleaved else 0, tab[0], qp, kp, vp, op,
+            qr, qt, kr, kt, vr, vt, outr, outt, table.data_ptr(), *where,
+            _ints_of_any(_given(status, "status"), "status"))
+
+
+def rotary_append(q, k, v, cache, layer, table, q_out, status, n_committed=None, width=None,
+                  parents=None, positions=None, columns=None, interleaved=False, stream=None):
+    """Rotary positions of the new tokens' q [B, T, Hq, hd] (into ``q_out``) and k [B, T, H, hd],
+    and the append of k and v to their columns of ``cache`` [L, 2, rows, H, cap, hd], layer
+    ``layer``.  ``table`` [positions, rot_dim / 2, 2] float32 holds cosines and sines.  Columns and
+    positions come from a verification pass (``n_committed``, ``width`` and ``parents``, None for a
+    chain) or are given (``positions``, ``columns`` [B, T], negative columns: padding)."""
+    rc = lib.specdec_rotary_append(
+        _PACK_ROTARY.pack(*_rotary_fields(q, k, v, cache, layer, table, q_out, status, n_committed,
+                                          width, parents, positions, columns, interleaved)),
+        _raw(stream))
     if rc:
         _check(rc, "specdec_rotary_append")
+
+
+def norm_rotary_append(q, k, v, cache, layer, table, q_out, status, q_weight, k_weight, eps=1e-6,
+                       weight_offset=0.0, start=None, n_committed=None, width=None, parents=None,
+                       positions=None, columns=None, interleaved=False, stream=None):
+    """As rotary_append, with the heads of q and k normed before they are rotated:
+    x / sqrt(mean(x^2) + eps) * (weight_offset + weight).  ``q_weight``, ``k_weight`` [hd]: float32 or
+    bfloat16, both of one type, None for a side without a norm.  ``start`` [B]: added to the rows'
+    positions (the length of a prefix that they share)."""
+    fields = _rotary_fields(q, k, v, cache, layer, table, q_out, status, n_committed, width, parents,
+                            positions, columns, interleaved)
+    one, at, code = (q.shape[3],), [0, 0], F32
+    for i, t in enumerate((q_weight, k_weight)):
+        if t is None:
+            continue
+        code = _DTYPES.get(t.dtype)
+        if code is None or t.shape != one or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("weights must be contiguous [head_dim] float32 or bfloat16 CUDA tensors")
+        at[i] = t.data_ptr()
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    rc = lib.specdec_norm_rotary_append(
+        _PACK_NORM_ROTARY.pack(*fields, *at, code, eps, weight_offset,
+                               _ints(start, (q.shape[0],), "start")), _raw(stream))
+    if rc:
+        _check(rc, "specdec_norm_rotary_append")
 
 
 def tree_attention_workspace_bytes(q, cache) -> int:
