@@ -250,6 +250,50 @@ int specdec_sampling_filter(const void* target_logits, const void* draft_logits,
                             float top_p, void* keep_bounds, int32_t* dev_status, void* stream);
 
 /*
+ * Tokens drawn from score rows with each row's own sampling settings: the drafts that a draft model
+ * proposes, or the token after a prefill.  [IE5, "Draft Possible Tokens, Then Verify Them Together":
+ * sampling settings "such as temperature and top-p"; "Exactness Means Different Things For Greedy
+ * And Sampled Output": both models use the same settings.]
+ *
+ *   logits       [R][row_stride] scores (dtype F32 or BF16), first V of a row read; element-aligned.
+ *   temperature  [R] float32 >= 0, or NULL: 1.  0 takes the highest score, lowest index on ties.
+ *   top_k        [R] int32 >= 0, or NULL: off.  0 or >= V is off; else the first top_k tokens in order of
+ *                score (highest first, ties by lower index) are kept.
+ *   top_p        [R] float32 in (0, 1], or NULL: 1.  Below 1 it keeps, of these and in the same order,
+ *                every token whose preceding probability mass (of what top_k kept) is below top_p.
+ *   min_p        [R] float32 in [0, 1], or NULL: 0.  Keeps tokens with at least min_p times the highest
+ *                probability.
+ *   uniforms     [R] float32 in [0, 1).
+ *   token        [R] int32 out: the first kept token, by ascending id, whose running mass exceeds
+ *                uniforms[r] times the kept mass.
+ *   logprob      [R] float32 out, or NULL: the natural logarithm of its probability among the kept (0 at
+ *                temperature 0).
+ *   keep_bounds  NULL, or specdec_keep_bound out of row r at keep_bounds[r * bounds_stride]: the row's
+ *                kept set, as specdec_verify_sample takes it (key 0 and index INT32_MAX: all).
+ * One read of the scores.  Masses are whole numbers of 2^-42 of the highest, each taken to about 2^-27
+ * of itself: sums do not depend on their order, and tokens below 2^-42 of the highest are not drawn.
+ * Device-detected errors (SPECDEC_ERR_INPUT_RANGE; the row's outputs are not written): a setting or
+ * uniform out of its range (NaN included), a row with NaN, +infinity or nothing above -infinity.
+ * Limits: R >= 0, V >= 1, row_stride >= V, bounds_stride >= 1 for several rows; a row of at most 1.4 MB
+ * (SPECDEC_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  const void* logits;
+  int dtype, R, V;
+  long long row_stride;           /* elements */
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p, *uniforms;
+  int32_t* token;
+  float* logprob;
+  void* keep_bounds;
+  long long bounds_stride;        /* bounds from one row's to the next's */
+  int32_t* dev_status;            /* [1] */
+} specdec_sample_args;
+
+int specdec_sample(const specdec_sample_args* args, void* stream);
+
+/*
  * A view of a K/V cache in device memory.  Element (layer l, k-or-v kv, row r, head h,
  * column c, e) lives at  base + l*stride_layer + kv*stride_kv + r*stride_row + h*stride_head
  *                        + c*head_dim + e          (strides in elements).

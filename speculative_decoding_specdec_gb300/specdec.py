@@ -100,6 +100,16 @@ class RotaryArgs(ctypes.Structure):
                 ("columns", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
+class SampleArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("R", ctypes.c_int),
+                ("V", ctypes.c_int), ("row_stride", ctypes.c_longlong),
+                ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p),
+                ("uniforms", ctypes.c_void_p), ("token", ctypes.c_void_p),
+                ("logprob", ctypes.c_void_p), ("keep_bounds", ctypes.c_void_p),
+                ("bounds_stride", ctypes.c_longlong), ("dev_status", ctypes.c_void_p)]
+
+
 class NormRotaryArgs(ctypes.Structure):
     _fields_ = [("rotary", RotaryArgs), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
@@ -173,6 +183,8 @@ lib.specdec_rotary_append.restype = _i
 lib.specdec_rotary_append.argtypes = [_vp, _vp]  # specdec_rotary_args
 lib.specdec_norm_rotary_append.restype = _i
 lib.specdec_norm_rotary_append.argtypes = [_vp, _vp]  # specdec_norm_rotary_args
+lib.specdec_sample.restype = _i
+lib.specdec_sample.argtypes = [_vp, _vp]  # specdec_sample_args
 lib.specdec_tree_attention.restype = _i
 lib.specdec_tree_attention.argtypes = [_vp, _vp]  # specdec_tree_attention_args
 lib.specdec_tree_attention_workspace.restype = _sz
@@ -591,6 +603,7 @@ _ROTARY = _KV + "iiiiiii" + "PPPP" + "qqqqqqqq" + "PPPPPPP"
 _PACK_ROTARY = struct.Struct("@" + _ROTARY)
 _PACK_NORM_ROTARY = struct.Struct("@" + _ROTARY + "PPiffP")
 _PACK_ATTENTION = struct.Struct("@" + _KV + "iiiif" + "PPP" + "qqqq" + "PPPPPPnP")
+_PACK_SAMPLE = struct.Struct("@Piiiq" + "PPPPPPPP" + "qP")
 _PACK_COMMIT = struct.Struct("@" + _KV + _KV + "iii" + "PPPPPPPP")
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 _cuda_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
@@ -832,6 +845,45 @@ def verify_tree_sample(target_logits, draft_logits, tokens, parents, uniforms, t
         _ints_of_any(_given(status, "status"), "status"), _raw(stream))
     if rc:
         _check(rc, "specdec_verify_tree_sample")
+
+
+def _per_row(t, shape, dtype, name):
+    """Device address of a contiguous CUDA tensor of that shape and dtype; of None, 0."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} CUDA tensor")
+    return t.data_ptr()
+
+
+def sample(logits, uniforms, token, status, temperature=None, top_k=None, top_p=None, min_p=None,
+           logprob=None, keep_bounds=None, stream=None):
+    """Tokens from scores ``logits`` [R, V] with each row's settings: ``temperature`` (0: the highest
+    score), ``top_p``, ``min_p`` [R] float32 and ``top_k`` [R] int32, None for none, and ``uniforms``
+    [R] float32 in [0, 1); ``token`` [R] int32 out, ``logprob`` [R] float32 out.  ``keep_bounds``
+    [R, 2] int32 (rows may be strided): the kept sets, as verify_sample takes them, so that
+    ``bounds[:, D + 1 + j]`` of a verification's [B, 2 D + 1, 2] is filled as draft j is drawn."""
+    shape, s, code = logits.shape, logits.stride(), _DTYPES.get(logits.dtype)
+    if len(shape) != 2 or code is None or not logits.is_cuda or (s[1] != 1 and shape[1] > 1):
+        raise ValueError("logits must be a [R, V] float32 or bfloat16 CUDA tensor with rows of unit stride")
+    R, V = shape
+    one, f32 = (R,), torch.float32
+    kp = ks = 0
+    if keep_bounds is not None:
+        b = keep_bounds.stride()
+        if (keep_bounds.dtype is not torch.int32 or keep_bounds.shape != (R, 2) or not keep_bounds.is_cuda
+                or b[1] != 1 or b[0] % 2):
+            raise ValueError("keep_bounds must be a [R, 2] int32 CUDA tensor of whole bounds")
+        kp, ks = keep_bounds.data_ptr(), b[0] // 2
+    args = _PACK_SAMPLE.pack(
+        logits.data_ptr(), code, R, V, s[0] if R > 1 else V, _per_row(temperature, one, f32, "temperature"),
+        _ints(top_k, one, "top_k"), _per_row(top_p, one, f32, "top_p"), _per_row(min_p, one, f32, "min_p"),
+        _per_row(_given(uniforms, "uniforms"), one, f32, "uniforms"),
+        _ints(_given(token, "token"), one, "token"), _per_row(logprob, one, f32, "logprob"), kp, ks,
+        _ints_of_any(_given(status, "status"), "status"))
+    rc = lib.specdec_sample(args, _raw(stream))
+    if rc:
+        _check(rc, "specdec_sample")
 
 
 def tree_commit(src, dst, width, accept_len, path, status, width_dst=None, nodes=MAX_TREE,
