@@ -7,20 +7,17 @@
 // the last that is kept, and the kept set is told by its (score, index).  The draw is the first token
 // by index whose running mass exceeds u times the sum.
 //
-// Masses are integers (2^-42 of the highest), so sums do not depend on their order and rows repeat
-// bit for bit.  A mass is off by about 2^-27 of itself: z is held in two floats, split into eighths
-// with a table of 2^(-i/8) and a Taylor polynomial of e^w, |w| < 0.044.  fp32 exponentials, off by
-// 2^-22 in one direction for every token of one bf16 score, would move the borders between tokens
-// enough to turn a draw in some ten thousand.
-//
 // A cluster holds a row in its CTAs' shared memory, read once from HBM; everything after is on chip:
 //   1. the highest score (and whether there is NaN);
-//   2. only where top-k or top-p is set: a histogram of 1024 bins of z (32 an octave down to 2^-16, 16 an
-//      octave down to 2^-48) with counts and masses, each CTA's merged over the cluster by parts; the
-//      bin that holds a cut; its tokens, listed in every CTA and ranked by comparing all pairs.  A bin
-//      of more tokens than the list has room for is split by key until it has few, or equal ones,
-//      which are counted by index;
+//   2. only where top-k or top-p is set: a histogram of counts over 2048 bins of z (64 an octave),
+//      each CTA's merged over the cluster by parts; the bin that holds a cut; its tokens, listed in every
+//      CTA and ranked by comparing all pairs.  Which bin holds top-p's cut is guessed from the counts
+//      and the bins' middles, and settled by a pass that sums what lies before and in it, which also
+//      moves the next guess: a pass or two, and no sums by atomics.  A bin of more tokens than the
+//      list has room for is split by key until it has few, or equal ones, which are counted by index;
 //   3. the kept masses' sums by warp, CTA and cluster, and in the warp that owns the draw the token.
+// Masses are fp32 exponentials, added up within a 16-byte vector and then as whole numbers of 2^-42 of
+// the highest: the sums depend on no order and no number of CTAs, so a row repeats bit for bit.
 #include <algorithm>
 #include <cmath>
 
@@ -30,10 +27,9 @@ namespace specdec {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024, kList = 1024;
+constexpr int kBins = 2048, kPer = kBins / kThreads, kList = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kMassBits = 42;
-constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
 
 struct SampleParams {
   const char* x;
@@ -59,44 +55,32 @@ __device__ __forceinline__ uint32_t remote_load(uint32_t a) {
   return v;
 }
 
-// 2^-(i/8) as an integer of 30 bits and, times 2^26, as a float.
-struct Entry {
-  uint32_t whole;
-  float f26;
-};
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-// A row's scale: its highest score and log2(e) / T in two floats.
+// A row's scale: its highest score, and log2(e) / T in two floats (the second at most 1: times a
+// difference of scores it is finite, or the difference is not).
 struct Scale {
   float top, sh, sl;
-  const Entry* table;
-  // z, to a float's precision and never falling as x falls
+  // Never falling as x falls.
   __device__ __forceinline__ float z(float x) const { return (top - x) * sh; }
-  // The mass as m * 2^(-30 - n); 0 beyond 2^-60.
-  __device__ __forceinline__ uint32_t mass(float x, int& n) const {
-    const float d = top - x, back = d - top, lost = (top - (d - back)) - (x + back);  // d and what it lost
-    const float zh = d * sh, zl = fmaf(d, sh, -zh) + fmaf(d, sl, lost * sh);
-    const float qm = fmaf(zh, 8.f, kMagic);
-    const int q = __float_as_int(qm) - __float_as_int(kMagic);
-    const float w = (fmaf(qm - kMagic, -0.125f, zh) + zl) * -0.693147181f;
-    const float e = w * fmaf(w, fmaf(w, fmaf(w, fmaf(w, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f), 1.f);  // e^w - 1
-    const bool in = zh < 60.f;
-    const Entry t = table[q & 7];
-    n = in ? q >> 3 : 0;
-    return in ? t.whole + ((__float_as_int(fmaf(e, t.f26, kMagic)) - __float_as_int(kMagic)) << 4) : 0u;
+  __device__ __forceinline__ float exponent(float x) const {  // -z
+    const float d = x - top;
+    return fmaf(d, sh, d * sl);
   }
-  __device__ __forceinline__ unsigned long long mass42(float x) const {
-    int n;
-    const unsigned long long m = mass(x, n);
-    return m << (kMassBits - 30) >> n;
-  }
+  // (a score of -infinity makes the exponent NaN or -infinity, either of which the maximum drops)
+  __device__ __forceinline__ float mass(float x) const { return ex2(fmaxf(exponent(x), -200.f)); }
 };
-__device__ __forceinline__ int bin_of(float z) {
-  const float b = z < 16.f ? z * 32.f : fminf(fmaf(z, 16.f, 256.f), kBins - 1.f);
-  return static_cast<int>(b);
+__device__ __forceinline__ int bin_of(float z) { return static_cast<int>(fminf(z * 64.f, kBins - 1.f)); }
+// A sum of masses, at most 8, as a whole number of 2^-42 (what is less is dropped).
+__device__ __forceinline__ unsigned long long whole(float v) {
+  const uint32_t bits = __float_as_uint(v), e = bits >> 23;
+  const unsigned long long m = static_cast<unsigned long long>((bits & 0x7FFFFFu) | 0x800000u) << 22;
+  return e < 70 ? 0 : m >> (130 - e);  // v = m 2^(e - 172)
 }
-__device__ __forceinline__ int octave_of(int bin) { return bin < 512 ? bin >> 5 : 16 + ((bin - 512) >> 4); }
-// A mass in units of 2^-30 of its bin's octave (at most 1 of those).
-__device__ __forceinline__ uint32_t in_octave(uint32_t m, int n, int octave) { return n > octave ? m >> (n - octave) : m; }
 
 // floor(f * x) and ceil(f * x) for 0 <= f < 1.
 __device__ __forceinline__ unsigned long long times(float f, unsigned long long x, bool up) {
@@ -127,17 +111,21 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) { 
 }
 
 struct Shared {
-  unsigned long long slot[2][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
-  unsigned long long warp_a[kWarps], warp_b[kWarps];
-  unsigned long long found[4];
-  uint32_t best, listed;
-  uint32_t lo, hi;
-  Entry table[8];
+  unsigned long long slot[2][3][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
+  unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kWarps];
+  double min_p_cut;
+  float warp_f[kWarps];
+  uint32_t best, listed, lo, hi, min_p_key;
+  uint32_t count_before, count;
+  float est_before, est;
+  int found;
 };
 
-// Counts and masses of one thread's two bins and of all before them.
+// One thread's bins: how many tokens they hold, what those weigh by the bins' middles, and both of all
+// before them.
 struct Bins {
-  unsigned long long count[2], mass[2], rel[2], count_before[2], mass_before[2];
+  uint32_t count[kPer], count_before;
+  float est[kPer], est_before;
 };
 
 template <typename T>
@@ -153,28 +141,49 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   }();
   const int r = blockIdx.x / C;
   uint4* s_x = reinterpret_cast<uint4*>(smem);
-  uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(p.pv) * 16);  // [3][kBins], or this CTA's list
-  uint32_t* s_all = s_hist + 3 * kBins;                                                    // merged, or the cluster's list
+  uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(p.pv) * 16);  // [kBins], or this CTA's list
+  uint32_t* s_all = s_hist + kBins;                                                        // merged, or the cluster's list
   int turn = 0;
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before the first remote store)
-  // Every CTA's value, in s.slot[..][rank] of each.
-  auto gather = [&](unsigned long long v) -> const unsigned long long* {
-    const unsigned long long* got = s.slot[turn];
-    if (C == 1) {
-      if (tid == 0) s.slot[turn][0] = v;
-      __syncthreads();
-    } else {
-      if (tid < C) remote_store(cluster_map(&s.slot[turn][rank], tid), v);
-      __syncwarp();
-      cluster_sync_all();
-    }
-    turn ^= 1;
-    return got;
-  };
   auto together = [&] {
     __syncwarp();
     if (C == 1) __syncthreads();
     else cluster_sync_all();
+  };
+  // Every CTA's values, the same in all its threads: s.slot[..][i][rank] in each.
+  using Slots = const unsigned long long (*)[kMaxCluster];
+  auto gather = [&](unsigned long long a, unsigned long long b, unsigned long long c) -> Slots {
+    Slots got = s.slot[turn];
+    if (tid < 3 * C) {
+      const int i = tid / C;
+      remote_store(cluster_map(&s.slot[turn][i][rank], tid - i * C), i == 0 ? a : i == 1 ? b : c);
+    }
+    together();
+    turn ^= 1;
+    return got;
+  };
+  // Sums of three values over the warp, the CTA and the cluster, in all threads.
+  auto sum_all = [&](unsigned long long& a, unsigned long long& b, unsigned long long& c) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    c = warp_sum(c);
+    __syncthreads();
+    if (lane == 0) {
+      s.warp_a[warp] = a;
+      s.warp_b[warp] = b;
+      s.warp_c[warp] = c;
+    }
+    __syncthreads();
+    a = warp_sum(lane < kWarps ? s.warp_a[lane] : 0);
+    b = warp_sum(lane < kWarps ? s.warp_b[lane] : 0);
+    c = warp_sum(lane < kWarps ? s.warp_c[lane] : 0);
+    const Slots all = gather(a, b, c);
+    a = b = c = 0;
+    for (int i = 0; i < C; ++i) {
+      a += all[0][i];
+      b += all[1][i];
+      c += all[2][i];
+    }
   };
 
   // ---------------------------------------------------------------------- the row, once
@@ -188,11 +197,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   auto index_of = [&](int v) { return (base + v) * N - skew; };  // of a vector's first element
   float top = -INFINITY;
   bool odd = false;  // NaN or +infinity
-  if (tid == 0) s.listed = 0;
-  if (tid < 8) {
-    const double f = exp2(-tid / 8.0);
-    s.table[tid] = Entry{static_cast<uint32_t>(f * 1073741824.0 + 0.5), static_cast<float>(f * 67108864.0)};
-  }
+  // (in 64 bits, where they are slow, by one thread while the scores come)
+  if (tid == kThreads - 1 && min_p > 0.f) s.min_p_cut = static_cast<double>(temperature) * log(static_cast<double>(min_p));
   const uint4 none = sizeof(T) == 2 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                                     : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
 #pragma unroll 4
@@ -228,9 +234,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   for (int w = 1; w < kWarps; ++w) mine = max(mine, s.warp_a[w]) | ((mine | s.warp_a[w]) & 1);
   if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
   {
-    const unsigned long long* all = gather(mine);
-    mine = all[0];
-    for (int i = 1; i < C; ++i) mine = max(mine, all[i]) | ((mine | all[i]) & 1);
+    const Slots all = gather(mine, 0, 0);
+    mine = all[0][0];
+    for (int i = 1; i < C; ++i) mine = max(mine, all[0][i]) | ((mine | all[0][i]) & 1);
   }
   const uint32_t top_key = static_cast<uint32_t>(mine >> 1);
   auto score_of = [](uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); };
@@ -265,147 +271,204 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     unsigned long long least = s.warp_b[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) least = min(least, s.warp_b[w]);
-    const unsigned long long* all = gather(least);
-    for (int i = 0; i < C; ++i) least = min(least, all[i]);
+    const Slots all = gather(least, 0, 0);
+    for (int i = 0; i < C; ++i) least = min(least, all[0][i]);
     if (rank == 0 && tid == 0) write(static_cast<int>(least), 0.f, top_key, static_cast<int>(least));
     return;
   }
-  const double per = fmin(1.4426950408889634 / static_cast<double>(temperature), 1e30);
   Scale sc;
   sc.top = top;
-  sc.sh = static_cast<float>(per);
-  sc.sl = static_cast<float>(per - static_cast<double>(sc.sh));
-  sc.table = s.table;
+  constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;  // log2(e) in two floats
+  sc.sh = fminf(__fdiv_rn(kLog2eHi, temperature), 1e30f);
+  sc.sl = sc.sh < 1e7f ? __fdiv_rn(fmaf(-sc.sh, temperature, kLog2eHi) + kLog2eLo, temperature) : 0.f;
 
   // ---------------------------------------------------------------------- the cuts
   uint32_t cut_key = 0;       // kept: a larger key, or this one up to index cut_last
   int cut_last = INT32_MAX;
+  float cut = -INFINITY;      // its score
+  auto in_row = [&](int e) { return e >= 0 && e < p.V; };
+  auto is_kept = [&](float x, int e) { return x > cut || (x == cut && e <= cut_last); };
   const bool by_mass = top_p < 1.f, by_count = top_k > 0 && top_k < p.V;
   if (by_mass || by_count) {
-    // Histogram of what `in` accepts, merged over the cluster, with the sums before each bin.
-    // in(x): the element's place, or -1; oct(place): the octave that its masses are in units of;
-    // down(place): what takes those, times 2^(kMassBits - 30), to the sums' unit.
-    auto histogram = [&](auto in, auto oct, auto down) {
-      for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[i] = 0;
+    // Counts by place (place(x): -1 for none), merged over the cluster; middle(b): what a token of bin
+    // b weighs, roughly.
+    auto histogram = [&](auto place, auto middle) {
+      for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
       __syncthreads();
-      uint32_t far = 0;  // (the last place, of most elements in a peaked row, is counted by itself)
+      uint32_t far = 0;  // (the last place is counted apart: it may hold nearly all of a row)
       each([&](float x, int e) {
-        const int place = e >= 0 && e < p.V ? in(x) : -1;
-        if (place == kBins - 1) {
-          ++far;
-        } else if (place >= 0) {
-          atomicAdd(&s_hist[place], 1u);
-        }
-        if (by_mass && place >= 0) {
-          int n;
-          const uint32_t m = sc.mass(x, n), rel = in_octave(m, n, oct(place));
-          if (m != 0) {  // in two halves, so that sums of 2^16 of them and more fit 32 bits
-            atomicAdd(&s_hist[kBins + place], rel >> 15);
-            atomicAdd(&s_hist[2 * kBins + place], rel & 0x7FFFu);
-          }
-        }
+        const int at = in_row(e) ? place(x) : -1;
+        if (at == kBins - 1) ++far;
+        else if (at >= 0) atomicAdd(&s_hist[at], 1u);
       });
       far = __reduce_add_sync(0xffffffffu, far);
       if (lane == 0 && far) atomicAdd(&s_hist[kBins - 1], far);
       together();
-      // a CTA adds up its part of the bins over all, 4 threads a bin, and tells all
-      unsigned long long* all_rel = reinterpret_cast<unsigned long long*>(s_all);
-      uint32_t* all_count = s_all + 2 * kBins;
-      const int part = kBins / C;
-      for (int i = tid; i < part * 4; i += kThreads) {
-        const int b = rank * part + (i >> 2), q = i & 3;
-        unsigned long long count = 0, rel = 0;
-        for (int c = q; c < C; c += 4) {
-          const uint32_t a = cluster_map(&s_hist[b], c);
-          count += remote_load(a);
-          rel += (static_cast<unsigned long long>(remote_load(a + 4 * kBins)) << 15) + remote_load(a + 8 * kBins);
+      if (C > 1) {  // a CTA adds up its part of the bins over all, and tells all
+        const int part = kBins / C;
+        for (int i = tid; i < part; i += kThreads) {
+          const int b = rank * part + i;
+          uint32_t count = 0;
+          for (int c = 0; c < C; ++c) count += remote_load(cluster_map(&s_hist[b], c));
+          for (int c = 0; c < C; ++c) remote_store(cluster_map(&s_all[b], c), count);
         }
-        count += __shfl_xor_sync(0xffffffffu, count, 1);
-        rel += __shfl_xor_sync(0xffffffffu, rel, 1);
-        count += __shfl_xor_sync(0xffffffffu, count, 2);
-        rel += __shfl_xor_sync(0xffffffffu, rel, 2);
-        for (int c = q; c < C; c += 4) {
-          remote_store(cluster_map(&all_rel[b], c), rel);
-          remote_store(cluster_map(&all_count[b], c), static_cast<uint32_t>(count));
-        }
+        together();
       }
-      together();
       Bins g;
+      uint32_t count = 0;
+      float est = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        g.count[i] = all_count[2 * tid + i];
-        g.rel[i] = all_rel[2 * tid + i];
-        g.mass[i] = g.rel[i] << (kMassBits - 30) >> down(2 * tid + i);
+      for (int i = 0; i < kPer; ++i) {
+        g.count[i] = (C > 1 ? s_all : s_hist)[kPer * tid + i];
+        g.est[i] = static_cast<float>(g.count[i]) * middle(kPer * tid + i);
+        count += g.count[i];
+        est += g.est[i];
       }
-      const unsigned long long ca = warp_scan(g.count[0] + g.count[1]), ma = warp_scan(g.mass[0] + g.mass[1]);
+      uint32_t ca = count;
+      float ea = est;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t oc = __shfl_up_sync(0xffffffffu, ca, d);
+        const float oe = __shfl_up_sync(0xffffffffu, ea, d);
+        if (lane >= d) {
+          ca += oc;
+          ea += oe;
+        }
+      }
       if (lane == 31) {
         s.warp_a[warp] = ca;
-        s.warp_b[warp] = ma;
+        s.warp_f[warp] = ea;
       }
       __syncthreads();
-      unsigned long long cb = ca - g.count[0] - g.count[1], mb = ma - g.mass[0] - g.mass[1];
+      g.count_before = ca - count;
+      g.est_before = ea - est;
       for (int w = 0; w < warp; ++w) {
-        cb += s.warp_a[w];
-        mb += s.warp_b[w];
+        g.count_before += static_cast<uint32_t>(s.warp_a[w]);
+        g.est_before += s.warp_f[w];
       }
-      g.count_before[0] = cb;
-      g.count_before[1] = cb + g.count[0];
-      g.mass_before[0] = mb;
-      g.mass_before[1] = mb + g.mass[0];
       return g;
     };
-    // The last bin that is not empty and begins before `target` tokens, or that much mass: its place,
-    // and in s.found what is before it and in it (tokens, mass, tokens, relative mass).
-    auto bin_with = [&](const Bins& g, bool mass, unsigned long long target) {
+    // The last bin in [lo, hi) that is not empty and begins before `tokens` tokens, or before `est`; -1
+    // if there is none.  What it holds and what comes before it are left in s.
+    auto bin_with = [&](const Bins& g, bool mass, uint32_t tokens, float est, int lo, int hi) {
       __syncthreads();
       if (tid == 0) s.best = 0;
       __syncthreads();
-      bool have[2];
+      uint32_t cb = g.count_before;
+      float eb = g.est_before;
+      int at = -1;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        have[i] = g.count[i] > 0 && (mass ? g.mass_before[i] : g.count_before[i]) < target;
-        if (have[i]) atomicMax(&s.best, 2 * tid + i + 1);
+      for (int i = 0; i < kPer; ++i) {
+        const int b = kPer * tid + i;
+        if (g.count[i] > 0 && b >= lo && b < hi && (mass ? eb < est : cb < tokens)) at = i;
+        cb += g.count[i];
+        eb += g.est[i];
+      }
+      if (at >= 0) atomicMax(&s.best, kPer * tid + at + 1);
+      __syncthreads();
+      const int best = static_cast<int>(s.best) - 1;
+      if (best >= 0 && tid == best / kPer) {
+        cb = g.count_before;
+        eb = g.est_before;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (kPer * tid + i == best) {
+            s.count_before = cb;
+            s.est_before = eb;
+            s.count = g.count[i];
+            s.est = g.est[i];
+          }
+          cb += g.count[i];
+          eb += g.est[i];
+        }
       }
       __syncthreads();
-      const int at = static_cast<int>(s.best) - 1;
-      if (tid == at >> 1) {
-        const int i = at & 1;
-        s.found[0] = i ? g.count_before[1] : g.count_before[0];
-        s.found[1] = i ? g.mass_before[1] : g.mass_before[0];
-        s.found[2] = i ? g.count[1] : g.count[0];
-        s.found[3] = i ? g.rel[1] : g.rel[0];
-      }
-      __syncthreads();
-      return at;
+      return best;
     };
-    const Bins bins = histogram([&](float x) { return bin_of(sc.z(x)); }, octave_of, octave_of);
+    // The bin with the cut of a target of mass, what is left of it there (in `target`), and in s what
+    // the bin holds.  kind(b) gives a test of scores: 1 before bin b (of what the histogram counted),
+    // 2 in it, 0 neither.  With `fraction` the target is that much of what is kept so far, which the
+    // first pass finds and est_total guesses.
+    auto mass_bin = [&](const Bins& g, auto kind, float fraction, float est_total, unsigned long long& target) {
+      int lo = 0, hi = kBins, low = -1;  // low: the last bin that was found to begin before the target
+      unsigned long long low_before = 0;
+      float want = fraction > 0.f ? fraction * est_total : static_cast<float>(target) * (1.f / (1ull << kMassBits));
+      for (int round = 0; round < 48 && lo < hi; ++round) {
+        // a guess; after a few the middle (so the bounds meet within the rounds there are)
+        const int mid = lo + 1 + (hi - lo) / 2;
+        int b = round < 5 ? bin_with(g, true, 0, want, lo, hi) : -1;
+        if (b < 0) b = bin_with(g, true, 0, INFINITY, lo, min(mid, hi));
+        if (b < 0) {
+          lo = mid;
+          continue;
+        }
+        const float est_before = s.est_before;
+        const auto test = kind(b);
+        unsigned long long before = 0, in = 0, all = 0;
+        const bool first = fraction > 0.f;
+        for (int v = v0 + lane; v < v1; v += 32) {
+          float x[N];
+          Vec<T>::unpack(s_x[v], x);
+          float vb = 0.f, vi = 0.f, va = 0.f;
+          const int e = index_of(v);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {  // (places outside the row weigh nothing)
+            const float m = sc.mass(x[k]);
+            const int c = test(x[k]);
+            vb += c == 1 ? m : 0.f;
+            vi += c == 2 ? m : 0.f;
+            if (first) va += is_kept(x[k], e + k) ? m : 0.f;
+          }
+          before += whole(vb);
+          in += whole(vi);
+          all += whole(va);
+        }
+        sum_all(before, in, all);
+        if (first) {
+          target = max(1ull, times(fraction, all, true));
+          fraction = 0.f;
+        }
+        if (before >= target) {
+          hi = b;
+        } else {
+          low = b;
+          low_before = before;
+          if (target <= before + in) break;
+          lo = b + 1;  // (where rounding has put the target between two bins, the earlier one is taken whole)
+        }
+        // the next guess: as much further as the target is from what has been summed
+        want = est_before + (static_cast<float>(target) - static_cast<float>(before)) * (1.f / (1ull << kMassBits));
+      }
+      (void)bin_with(g, true, 0, INFINITY, low, low + 1);  // (the last one tried may be another)
+      target -= low_before;
+      return low;
+    };
+    const Bins bins = histogram([&](float x) { return bin_of(sc.z(x)); }, [](int b) { return ex2((b + 0.5f) * (-1.f / 64)); });
+    float est_kept = 0.f;
 
     // The cut: the last token of the order before which there are fewer than `target` tokens, or less
-    // mass.  Sets cut_key and cut_last; returns the mass up to and with it (if masses are counted).
-    auto find_cut = [&](bool mass, unsigned long long target) -> unsigned long long {
-      const int bin = bin_with(bins, mass, target);
-      const int oct = octave_of(bin);
-      const unsigned long long mass_before = s.found[1];
-      unsigned long long count = s.found[2], rel = s.found[3], left;  // of the tokens still in question, and what is left of the target
+    // than `fraction` of the mass kept so far.  Sets cut_key, cut and cut_last.
+    auto find_cut = [&](bool mass, unsigned long long target, float fraction) {
+      int bin;
       if (mass) {
-        const unsigned long long want = target - mass_before, whole = rel << (kMassBits - 30) >> oct;
-        left = want >= whole ? rel : min(rel, ((want << oct) + ((1ull << (kMassBits - 30)) - 1)) >> (kMassBits - 30));
-        left = max(left, 1ull);
+        bin = mass_bin(bins, [&](int b) {
+          return [&sc, b](float x) {
+            const float z = sc.z(x) * 64.f;
+            return z < b ? 1 : (z < b + 1 || b == kBins - 1 ? 2 : 0);
+          };
+        }, fraction, est_kept, target);
       } else {
-        left = target - s.found[0];
+        bin = bin_with(bins, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
+        target -= s.count_before;
+        est_kept = s.est_before + s.est;
       }
-      unsigned long long rel_before = 0;  // in the bin, of what is kept for certain
-      uint32_t klo = 0, khi = 0xFFFFFFFFu;
+      uint32_t count = s.count, klo = 0, khi = 0;
+      bool by_key = false;
       auto inside = [&](float x) {
         const uint32_t key = order_bits(x);
-        return key >= klo && key <= khi && bin_of(sc.z(x)) == bin;
+        return by_key ? key >= klo && key <= khi : bin_of(sc.z(x)) == bin;
       };
-      auto rel_of = [&](float x) {
-        int n;
-        const uint32_t m = sc.mass(x, n);
-        return in_octave(m, n, oct);
-      };
-      for (int round = 0; count > kList && round < 8; ++round) {  // (each leaves a thousandth of the keys)
+      for (int round = 0; count > kList && round < 8; ++round) {  // (each leaves a two-thousandth of the keys)
         __syncthreads();
         if (tid == 0) {
           s.lo = 0xFFFFFFFFu;
@@ -414,7 +477,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         __syncthreads();
         uint32_t lo = 0xFFFFFFFFu, hi = 0;
         each([&](float x, int e) {
-          if (e >= 0 && e < p.V && inside(x)) {
+          if (in_row(e) && inside(x)) {
             lo = min(lo, order_bits(x));
             hi = max(hi, order_bits(x));
           }
@@ -426,204 +489,216 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
           atomicMax(&s.hi, hi);
         }
         __syncthreads();
-        const unsigned long long* all = gather(static_cast<unsigned long long>(s.hi) << 32 | s.lo);
+        const Slots all = gather(s.lo, s.hi, 0);
         klo = 0xFFFFFFFFu;
         khi = 0;
         for (int i = 0; i < C; ++i) {
-          klo = min(klo, static_cast<uint32_t>(all[i]));
-          khi = max(khi, static_cast<uint32_t>(all[i] >> 32));
+          klo = min(klo, static_cast<uint32_t>(all[0][i]));
+          khi = max(khi, static_cast<uint32_t>(all[1][i]));
         }
+        by_key = true;
         if (klo == khi) break;
-        const int shift = max(0, 22 - __clz(khi - klo));
-        const Bins g = histogram([&](float x) { return inside(x) ? static_cast<int>((khi - order_bits(x)) >> shift) : -1; },
-                                 [&](int) { return oct; }, [](int) { return kMassBits - 30; });  // (sums in the bin's unit)
-        const int at = bin_with(g, mass, left);
-        const uint32_t first = khi - (static_cast<uint32_t>(at) << shift);
-        khi = first;
-        if (first - klo >= 1u << shift) klo = first - ((1u << shift) - 1);
-        left -= mass ? s.found[1] : s.found[0];
-        rel_before += s.found[1];
-        count = s.found[2];
-        rel = s.found[3];
+        const int shift = max(0, 21 - __clz(khi - klo));
+        const uint32_t a = klo, z = khi;
+        auto first_of = [=](int b) { return z - (static_cast<uint32_t>(b) << shift); };  // a bin's highest key
+        const Bins g = histogram([&](float x) { return inside(x) ? static_cast<int>((z - order_bits(x)) >> shift) : -1; },
+                                 [&](int b) { return b <= static_cast<int>((z - a) >> shift) ? sc.mass(score_of(max(a, first_of(b)))) : 0.f; });
+        int at;
+        if (mass) {
+          at = mass_bin(g, [&](int b) {
+            const uint32_t h = first_of(b);
+            return [=](float x) {
+              const uint32_t key = order_bits(x);
+              return key > z || key < a ? 0 : key > h ? 1 : h - key < (1u << shift) ? 2 : 0;
+            };
+          }, 0.f, 0.f, target);
+        } else {
+          at = bin_with(g, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
+          target -= s.count_before;
+        }
+        count = s.count;
+        khi = first_of(at);
+        if (khi - klo >= 1u << shift) klo = khi - ((1u << shift) - 1);
       }
       if (count > kList) {
         // equal scores: the last one by index
         const uint32_t key = klo;
-        const uint32_t one = rel_of(score_of(key));
-        const unsigned long long want = !mass ? left : one == 0 ? count : min(count, (left + one - 1) / one);
+        const float score = score_of(key);
+        const unsigned long long one = whole(sc.mass(score));
+        const unsigned long long want = !mass ? target : one == 0 ? count : min(static_cast<unsigned long long>(count), (target + one - 1) / one);
         unsigned long long n = 0;
-        each([&](float x, int e) { n += e >= 0 && e < p.V && order_bits(x) == key; });
+        each([&](float x, int e) { n += in_row(e) && x == score; });
         n = warp_sum(n);
         __syncthreads();
         if (lane == 0) s.warp_a[warp] = n;
+        if (tid == 0) s.found = 0;
         __syncthreads();
         unsigned long long before = 0, total = 0;
         for (int w = 0; w < kWarps; ++w) {
           before += w < warp ? s.warp_a[w] : 0;
           total += s.warp_a[w];
         }
-        const unsigned long long* all = gather(total);
-        for (int i = 0; i < rank; ++i) before += all[i];
-        __syncthreads();
-        if (tid == 0) s.found[0] = 0;
-        __syncthreads();
+        const Slots all = gather(total, 0, 0);
+        for (int i = 0; i < rank; ++i) before += all[0][i];
         if (before < want && want <= before + n) {  // this warp has it
           for (int vv = v0; vv < v1; vv += 32) {
             const int v = vv + lane;
             float x[N];
-            if (v < v1) Vec<T>::unpack(s_x[v], x);
+            Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
             const int e = index_of(v);
             unsigned long long here = 0;
 #pragma unroll
-            for (int k = 0; k < N; ++k) here += v < v1 && e + k >= 0 && e + k < p.V && order_bits(x[k]) == key;
+            for (int k = 0; k < N; ++k) here += v < v1 && in_row(e + k) && x[k] == score;
             const unsigned long long scan = warp_scan(here);
             unsigned long long at = before + scan - here;
 #pragma unroll
             for (int k = 0; k < N; ++k)
-              if (v < v1 && e + k >= 0 && e + k < p.V && order_bits(x[k]) == key && ++at == want) s.found[0] = e + k + 1;
+              if (v < v1 && in_row(e + k) && x[k] == score && ++at == want) s.found = e + k + 1;
             before += __shfl_sync(0xffffffffu, scan, 31);
           }
         }
         __syncthreads();
-        const unsigned long long* who = gather(s.found[0]);
+        const Slots who = gather(s.found, 0, 0);
         unsigned long long last = 0;
-        for (int i = 0; i < C; ++i) last = max(last, who[i]);
+        for (int i = 0; i < C; ++i) last = max(last, who[0][i]);
         cut_key = key;
         cut_last = static_cast<int>(last) - 1;
-        rel_before += want * one;
       } else {
         // this CTA's tokens in question, then everyone's in every CTA, in order of rank
-        uint32_t *l_key = s_hist, *l_index = s_hist + kList, *l_rel = s_hist + 2 * kList;
-        uint32_t *a_key = s_all, *a_index = s_all + kList, *a_rel = s_all + 2 * kList;
+        uint32_t *l_key = s_hist, *l_index = s_hist + kList, *a_key = s_all, *a_index = s_all + kList;
         together();  // all are done with the histograms
-        if (tid == 0) s.listed = 0;
+        if (tid == 0) {
+          s.listed = 0;
+          s.best = 0;
+        }
         __syncthreads();
         each([&](float x, int e) {
-          if (e >= 0 && e < p.V && inside(x)) {
+          if (in_row(e) && inside(x)) {
             const uint32_t i = atomicAdd(&s.listed, 1u);
             l_key[i] = order_bits(x);
             l_index[i] = e;
-            l_rel[i] = by_mass ? rel_of(x) : 0;
           }
         });
         __syncthreads();
-        const unsigned long long* all = gather(s.listed);
+        const Slots all = gather(s.listed, 0, 0);
         int n = 0;
         for (int c = 0; c < C; ++c) {
-          const int m = static_cast<int>(all[c]);
-          for (int i = tid; i < 3 * m; i += kThreads) {
-            const int f = i / m, j = i - f * m;
+          const int m = static_cast<int>(all[0][c]);
+          for (int i = tid; i < 2 * m; i += kThreads) {
+            const int f = i >= m ? 1 : 0, j = i - f * m;
             s_all[f * kList + n + j] = remote_load(cluster_map(&s_hist[f * kList + j], c));
           }
           n += m;
         }
-        if (tid == 0) s.best = 0;
         __syncthreads();
         // a warp ranks a token: what is before it, and whether it is kept
-        auto before_of = [&](int i, unsigned long long& tokens, unsigned long long& sum) {
-          const unsigned long long me = static_cast<unsigned long long>(a_key[i]) << 32 | ~a_index[i];
-          tokens = sum = 0;
-          for (int j = lane; j < n; j += 32)
-            if ((static_cast<unsigned long long>(a_key[j]) << 32 | ~a_index[j]) > me) {
-              ++tokens;
-              sum += a_rel[j];
-            }
-          tokens = warp_sum(tokens);
-          sum = warp_sum(sum);
-        };
         for (int i = rank * kWarps + warp; i < n; i += C * kWarps) {
-          unsigned long long tokens, sum;
-          before_of(i, tokens, sum);
-          if (lane == 0 && (mass ? sum : tokens) < left) atomicMax(&s.best, static_cast<uint32_t>(tokens) << 16 | (i + 1));
+          const unsigned long long me = static_cast<unsigned long long>(a_key[i]) << 32 | ~a_index[i];
+          uint32_t tokens = 0;
+          unsigned long long sum = 0;
+          for (int j = lane; j < n; j += 32) {
+            const uint32_t key = a_key[j];
+            if ((static_cast<unsigned long long>(key) << 32 | ~a_index[j]) > me) {
+              ++tokens;
+              if (mass) sum += whole(sc.mass(score_of(key)));
+            }
+          }
+          tokens = __reduce_add_sync(0xffffffffu, tokens);
+          if (mass) sum = warp_sum(sum);
+          if (lane == 0 && (mass ? sum : tokens) < target) atomicMax(&s.best, tokens << 16 | (i + 1));
         }
         __syncthreads();
-        const unsigned long long* who = gather(s.best);
+        const Slots who = gather(s.best, 0, 0);  // (and the lists may be written again)
         unsigned long long best = 0;
-        for (int i = 0; i < C; ++i) best = max(best, who[i]);
-        const int at = static_cast<int>(best & 0xFFFF) - 1;
+        for (int i = 0; i < C; ++i) best = max(best, who[0][i]);
+        const int at = max(0, static_cast<int>(best & 0xFFFF) - 1);  // (the first token is always kept)
         cut_key = a_key[at];
         cut_last = static_cast<int>(a_index[at]);
-        unsigned long long tokens, sum;
-        before_of(at, tokens, sum);
-        rel_before += sum + a_rel[at];
-        together();  // the lists may be written again
       }
-      return mass_before + (rel_before << (kMassBits - 30) >> oct);
+      cut = score_of(cut_key);
     };
-    unsigned long long kept = 0;
     if (by_count) {
-      kept = find_cut(false, top_k);
-    } else if (by_mass) {  // all of it
-      const unsigned long long end = bins.mass_before[1] + bins.mass[1];
-      __syncthreads();
-      if (tid == kThreads - 1) s.found[0] = end;
-      __syncthreads();
-      kept = s.found[0];
+      find_cut(false, top_k, 0.f);
+    } else {
+      (void)bin_with(bins, true, 0, INFINITY, 0, kBins);
+      est_kept = s.est_before + s.est;
     }
-    if (by_mass) (void)find_cut(true, max(1ull, times(top_p, kept, true)));
+    if (by_mass) find_cut(true, 0, top_p);
   }
   if (min_p > 0.f) {
-    const double cut = static_cast<double>(top) + static_cast<double>(temperature) * log(static_cast<double>(min_p));
-    const float least = __double2float_ru(fmax(cut, -3.4028234663852886e38));
-    const uint32_t key = order_bits(least);  // (the highest score's own at most)
+    if (tid == 0) {
+      const float least = __double2float_ru(fmax(static_cast<double>(top) + s.min_p_cut, -3.4028234663852886e38));
+      s.min_p_key = order_bits(least);  // (the highest score's own at most)
+    }
+    __syncthreads();
+    const uint32_t key = s.min_p_key;
     if (key > cut_key) {
       cut_key = key;
       cut_last = INT32_MAX;
+      cut = score_of(key);
     }
   }
 
   // ---------------------------------------------------------------------- the draw
   const bool cuts = cut_key != 0;
-  const float cut = score_of(cut_key);
-  auto kept_mass = [&](float x, int e) -> unsigned long long {
-    if (cuts && !(x > cut || (x == cut && e <= cut_last))) return 0;
-    return sc.mass42(x);
+  // the running masses of a vector's tokens, as sums of floats: the last is what the vector adds
+  auto running = [&](int v, float (&m)[N], float (&x)[N]) {
+    Vec<T>::unpack(s_x[v], x);
+    const int e = index_of(v);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float mass = sc.mass(x[k]);
+      sum += !cuts || is_kept(x[k], e + k) ? mass : 0.f;
+      m[k] = sum;
+    }
   };
   unsigned long long sum = 0;
-  each([&](float x, int e) { sum += kept_mass(x, e); });
+  for (int v = v0 + lane; v < v1; v += 32) {
+    float m[N], x[N];
+    running(v, m, x);
+    sum += whole(m[N - 1]);
+  }
   sum = warp_sum(sum);
   __syncthreads();
   if (lane == 0) s.warp_a[warp] = sum;
   __syncthreads();
-  unsigned long long before = 0, mine_all = 0;
+  unsigned long long before = 0, cta = 0;
   for (int w = 0; w < kWarps; ++w) {
     before += w < warp ? s.warp_a[w] : 0;
-    mine_all += s.warp_a[w];
+    cta += s.warp_a[w];
   }
-  const unsigned long long* all = gather(mine_all);
+  const Slots all = gather(cta, 0, 0);
   unsigned long long total = 0;
   for (int i = 0; i < C; ++i) {
-    before += i < rank ? all[i] : 0;
-    total += all[i];
+    before += i < rank ? all[0][i] : 0;
+    total += all[0][i];
   }
   const unsigned long long want = times(u, total, false);  // the first whose running mass is above it
   if (want < before || want >= before + sum) return;
   for (int vv = v0; vv < v1; vv += 32) {
     const int v = vv + lane;
-    float x[N];
-    Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
-    const int e = index_of(v);
+    float m[N], x[N];
     unsigned long long here = 0;
-#pragma unroll
-    for (int k = 0; k < N; ++k) here += kept_mass(x[k], e + k);
-    const unsigned long long scan = warp_scan(here);
-    unsigned long long at = before + scan - here;
+    if (v < v1) {
+      running(v, m, x);
+      here = whole(m[N - 1]);
+    }
+    const unsigned long long scan = warp_scan(here), at = before + scan - here;
     if (want >= at && want < at + here) {
       int token = 0;
       float score = 0.f;
       bool got = false;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        at += kept_mass(x[k], e + k);
-        if (!got && at > want) {
+      for (int k = 0; k < N; ++k)
+        if (!got && at + whole(m[k]) > want) {
           got = true;
-          token = e + k;
+          token = index_of(v) + k;
           score = x[k];
         }
-      }
-      const double lp = (static_cast<double>(score) - static_cast<double>(top)) / static_cast<double>(temperature) -
-                        log(static_cast<double>(total) * (1.0 / (1ull << kMassBits)));
-      write(token, static_cast<float>(lp), cut_key, cut_last);
+      // the highest mass is 1 and among the kept: the sum's logarithm from what it is above 1
+      const float above = static_cast<float>(total - (1ull << kMassBits)) * (1.f / (1ull << kMassBits));
+      write(token, fmaf(sc.exponent(score), 0.693147181f, -log1pf(above)), cut_key, cut_last);
     }
     const unsigned long long step = __shfl_sync(0xffffffffu, scan, 31);
     if (want < before + step) return;
@@ -636,7 +711,7 @@ template <typename T>
 int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
   const int vectors = (p.V + 2 * N - 2) / N;  // whatever the row's alignment
-  const size_t extra = p.top_k || p.top_p ? 6 * kBins * 4 : 0;
+  const size_t extra = p.top_k || p.top_p ? 2 * kBins * 4 : 0;
   constexpr size_t kRoom = 200 << 10;
   const int sms = std::max(1, sm_count());
   int C = 1;

@@ -1,10 +1,14 @@
 """Tokens drawn with sampling settings, against the float64 oracle.
 
-Tolerances.  A mass is off by at most 2^-26 of itself (2^-27 in what is added to the table's entry, 2^-28
-and less in z, the polynomial and the entry) and by 2^-42 of the highest where it is cut off.  So a running
-mass over the kept mass is off by at most DELTA(V) = 2 * (2^-26 + V * 2^-42): a token is right if u
-lies within DELTA of its interval, and a top-p cut if top_p does.  A log probability is that of the
-token's score, off by DELTA in the sum's logarithm and by one rounding to fp32.
+Tolerances.  A mass 2^-z is off by ex2's 2^-22 of itself (2 ulp) and by z's error times ln 2: the
+difference of scores, its product with log2(e) / T and that factor's second float are three roundings,
+3 * 2^-24 of z.  Summed over the row, with sum p z <= log2 V (the entropy of the probabilities p is
+log2(sum of masses) + sum p z, the highest mass being 1, and at most log2 V), that is 3 ln 2 log2(V)
+2^-24 of the sum.  A vector's sum takes 7 additions, and whole numbers drop 2^-42 each.  So a running mass
+over the kept mass is off by at most DELTA(V), twice all that: a token is right if u lies within DELTA of
+its interval, and a top-p cut if top_p does.  A log probability is -(z ln 2 + log1p(sum - 1)), both terms
+of one sign and in fp32: z takes the three roundings, ln 2 and the fused product and sum two more, sum - 1
+one and log1p one ulp (two): under 6 * 2^-24 of itself, besides DELTA in the sum.
 """
 import ctypes
 
@@ -17,7 +21,7 @@ from tree_testlib import DEV, i32, status
 
 
 def delta(V):
-    return 2 * (2.0 ** -26 + V * 2.0 ** -42)
+    return 2 * (2.0 ** -22 + 3 * np.log(2) * np.log2(max(V, 2)) * 2.0 ** -24 + 7 * 2.0 ** -24 + V * 2.0 ** -42)
 
 
 def f32(x, R):
@@ -82,7 +86,7 @@ def run(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lead=0, gap=0, exa
         assert lo - delta(V) <= float(uu[r]) <= hi + delta(V), (r, got[r], want)
         e = SO.masses(row, t)
         exact = (row[got[r]] - row.max()) / float(np.float32(t)) - np.log(e[ids].sum())
-        assert abs(lp[r] - exact) <= 2 * delta(V) + 2.0 ** -23 * abs(exact) + 2.0 ** -149
+        assert abs(lp[r] - exact) <= delta(V) + 6 * 2.0 ** -24 * abs(exact) + 2.0 ** -149
     return got, kb
 
 
