@@ -10,7 +10,8 @@
 // A cluster holds a row in its CTAs' shared memory, read once from HBM; everything after is on chip:
 //   1. the highest score (and whether there is NaN);
 //   2. only where top-k or top-p is set: a histogram of counts over 2048 bins of z (64 an octave),
-//      each CTA's merged over the cluster by parts; the bin that holds a cut; its tokens, listed in every
+//      each CTA's merged over the cluster by parts.  Where the tokens up to the cut are few they are listed
+//      and sorted.  Otherwise: the bin that holds a cut; its tokens, listed in every
 //      CTA and ranked by comparing all pairs.  Which bin holds top-p's cut is guessed from the counts
 //      and the bins' middles, and settled by a pass that sums what lies before and in it, which also
 //      moves the next guess: a pass or two, and no sums by atomics.  A bin of more tokens than the
@@ -26,10 +27,11 @@
 namespace specdec {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kPer = kBins / kThreads, kList = 1024;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBins = 2048, kPer = kBins / kThreads, kList = 1024, kEach = kList / kThreads;
 constexpr int kMaxCluster = 8;
 constexpr int kMassBits = 42;
+constexpr uint32_t kTries = 1u << 17, kNs = 20000;  // a wait gives up after about 2.6 s
 
 struct SampleParams {
   const char* x;
@@ -113,6 +115,7 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) { 
 struct Shared {
   unsigned long long slot[2][3][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
   unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kWarps];
+  uint64_t bar[kWarps];
   double min_p_cut;
   float warp_f[kWarps];
   uint32_t best, listed, lo, hi, min_p_key;
@@ -201,49 +204,72 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   if (tid == kThreads - 1 && min_p > 0.f) s.min_p_cut = static_cast<double>(temperature) * log(static_cast<double>(min_p));
   const uint4 none = sizeof(T) == 2 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                                     : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  // A warp fetches its own vectors: those that lie in the row whole by one bulk copy, all of a CTA's in
+  // flight together; the others by element.
+  const int whole0 = max(v0, min(v1, (skew > 0 ? 1 : 0) - base)), whole1 = max(whole0, min(v1, (p.V + skew) / N - base));
+  if (lane == 0) {
+    mbar_init(&s.bar[warp], 1);
+    fence_mbar_init();
+    if (whole1 > whole0) {
+      mbar_arrive_expect_tx(&s.bar[warp], (whole1 - whole0) * 16);
+      bulk_g2s(s_x + whole0, row + static_cast<long long>(index_of(whole0)) * static_cast<int>(sizeof(T)), (whole1 - whole0) * 16, &s.bar[warp]);
+    }
+  }
+  for (int v = v0 + lane; v < v1; v += 32) {
+    if (v >= whole0 && v < whole1) continue;
+    uint4 w = none;
+    T* q = reinterpret_cast<T*>(&w);
+    const int e = index_of(v);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (e + k >= 0 && e + k < p.V) q[k] = reinterpret_cast<const T*>(row)[e + k];
+    s_x[v] = w;
+  }
+  __syncwarp();
+  const bool late = whole1 > whole0 && !mbar_wait_sleep(&s.bar[warp], 0, kTries, kNs);
 #pragma unroll 4
   for (int v = v0 + lane; v < v1; v += 32) {
-    const int e = index_of(v);
-    uint4 w = none;
-    if (e >= 0 && e + N <= p.V) {
-      w = ldg_stream(row + static_cast<long long>(e) * static_cast<int>(sizeof(T)));
-    } else {
-      T* q = reinterpret_cast<T*>(&w);
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (e + k >= 0 && e + k < p.V) q[k] = reinterpret_cast<const T*>(row)[e + k];
-    }
-    s_x[v] = w;
     float f[N];
-    Vec<T>::unpack(w, f);
+    Vec<T>::unpack(s_x[v], f);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       top = fmaxf(top, f[k]);
       odd |= !(f[k] < INFINITY);
     }
   }
+  if (late) (void)mbar_wait_sleep(&s.bar[warp], 0, kTries, kNs);  // (no copy outlives the CTA)
   const bool bad_setting = !(temperature >= 0.f && temperature < INFINITY) || top_k < 0 || !(top_p > 0.f && top_p <= 1.f) ||
                            !(min_p >= 0.f && min_p <= 1.f) || !(u >= 0.f && u < 1.f);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   odd = __any_sync(0xffffffffu, odd);
   if (lane == 0) s.warp_a[warp] = static_cast<unsigned long long>(order_bits(top)) << 1 | (odd ? 1 : 0);
-  __syncthreads();
-  unsigned long long mine = s.warp_a[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) mine = max(mine, s.warp_a[w]) | ((mine | s.warp_a[w]) & 1);
+  const bool gave_up = __syncthreads_or(late);
+  unsigned long long mine;
+  {
+    const unsigned long long one = s.warp_a[lane % kWarps];
+    mine = static_cast<unsigned long long>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(one >> 1))) << 1 |
+           (__any_sync(0xffffffffu, one & 1) ? 1 : 0);
+  }
   if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
   {
-    const Slots all = gather(mine, 0, 0);
+    const Slots all = gather(mine, gave_up, 0);
     mine = all[0][0];
-    for (int i = 1; i < C; ++i) mine = max(mine, all[0][i]) | ((mine | all[0][i]) & 1);
+    unsigned long long any = all[1][0];
+    for (int i = 1; i < C; ++i) {
+      mine = max(mine, all[0][i]) | ((mine | all[0][i]) & 1);
+      any |= all[1][i];
+    }
+    if (any) {  // every CTA leaves: nothing is sent any more
+      if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_TIMEOUT);
+      return;
+    }
   }
   const uint32_t top_key = static_cast<uint32_t>(mine >> 1);
   auto score_of = [](uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); };
   top = score_of(top_key);
   if (bad_setting || (mine & 1) || top == -INFINITY) {
     if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
-    together();  // no CTA leaves while another may write to it
     return;
   }
   auto each = [&](auto f) {  // this thread's elements: f(score, index)
@@ -281,6 +307,22 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;  // log2(e) in two floats
   sc.sh = fminf(__fdiv_rn(kLog2eHi, temperature), 1e30f);
   sc.sl = sc.sh < 1e7f ? __fdiv_rn(fmaf(-sc.sh, temperature, kLog2eHi) + kLog2eLo, temperature) : 0.f;
+
+  // The least key that min-p keeps, by all threads.
+  auto min_p_key = [&] {
+    if (tid == 0) {
+      const float least = __double2float_ru(fmax(static_cast<double>(top) + s.min_p_cut, -3.4028234663852886e38));
+      s.min_p_key = order_bits(least);  // (the highest score's own at most)
+    }
+    __syncthreads();
+    return s.min_p_key;
+  };
+  // The drawn token, of a sum of kept masses.
+  auto finish = [&](int token, float score, unsigned long long total, uint32_t key, int last) {
+    // the highest mass is 1 and among the kept: the sum's logarithm from what it is above 1
+    const float above = static_cast<float>(total - (1ull << kMassBits)) * (1.f / (1ull << kMassBits));
+    write(token, fmaf(sc.exponent(score), 0.693147181f, -log1pf(above)), key, last);
+  };
 
   // ---------------------------------------------------------------------- the cuts
   uint32_t cut_key = 0;       // kept: a larger key, or this one up to index cut_last
@@ -444,7 +486,145 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
       return low;
     };
     const Bins bins = histogram([&](float x) { return bin_of(sc.z(x)); }, [](int b) { return ex2((b + 0.5f) * (-1.f / 64)); });
-    float est_kept = 0.f;
+
+    // Most settings keep few tokens.  Where the bins up to the cut's hold no more than the list, one pass
+    // lists them all (and, for top-p alone, sums the row); the first CTA sorts them and does the rest.
+    // For top-p the bin is guessed from the bins' middles (2 % beyond what they say), and the listed
+    // mass shows whether it was far enough.
+    (void)bin_with(bins, true, 0, INFINITY, 0, kBins);
+    float est_kept = s.est_before + s.est;
+    const int enough = by_count ? bin_with(bins, false, top_k, 0.f, 0, kBins) : bin_with(bins, true, 0, 1.02f * top_p * est_kept, 0, kBins);
+    if (s.count_before + s.count <= kList) {
+      unsigned long long* l_list = reinterpret_cast<unsigned long long*>(s_hist);
+      unsigned long long* list = reinterpret_cast<unsigned long long*>(s_all);
+      together();  // all are done with the histograms
+      if (tid == 0) s.listed = 0;
+      __syncthreads();
+      unsigned long long total = 0, in_list = 0;
+      const bool alone = !by_count;
+      for (int v = v0 + lane; v < v1; v += 32) {
+        float x[N];
+        Vec<T>::unpack(s_x[v], x);
+        const int e = index_of(v);
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          if (alone) sum += sc.mass(x[k]);
+          if (in_row(e + k) && bin_of(sc.z(x[k])) <= enough) {
+            l_list[atomicAdd(&s.listed, 1u)] = static_cast<unsigned long long>(order_bits(x[k])) << 32 | ~static_cast<uint32_t>(e + k);
+            if (alone) in_list += whole(sc.mass(x[k]));
+          }
+        }
+        if (alone) total += whole(sum);
+      }
+      unsigned long long listed = 0;
+      __syncthreads();
+      if (tid == 0) listed = s.listed;
+      sum_all(total, in_list, listed);
+      const unsigned long long target = alone ? max(1ull, times(top_p, total, true)) : 0;
+      if (in_list >= target) {
+        // its place among the first CTA's: behind those of the CTAs before
+        const Slots all = gather(s.listed, 0, 0);
+        int first = 0;
+        for (int i = 0; i < rank; ++i) first += static_cast<int>(all[0][i]);
+        const uint32_t to = cluster_map(list, 0);
+        for (uint32_t i = tid; i < s.listed; i += kThreads) remote_store(to + (first + i) * 8, l_list[i]);
+        together();
+        if (rank != 0) return;
+        const int n = static_cast<int>(listed);
+        int size = 32;
+        while (size < n) size *= 2;
+        // (sorted downwards, `skip` fills up: 0 is below every token)
+        auto sort = [&](int used) {
+          for (int i = used + tid; i < size; i += kThreads) list[i] = 0;
+          __syncthreads();
+          for (int run = 2; run <= size; run *= 2)
+            for (int gap = run / 2; gap > 0; gap /= 2) {
+              for (int i = tid; i < size / 2; i += kThreads) {
+                const int lo = 2 * i - (i & (gap - 1)), hi = lo + gap;
+                const unsigned long long x = list[lo], y = list[hi];
+                if ((x < y) == ((lo & run) == 0)) {
+                  list[lo] = y;
+                  list[hi] = x;
+                }
+              }
+              if (gap > 32 || gap == 1) __syncthreads();
+              else __syncwarp();
+            }
+        };
+        sort(n);
+        // masses and what is before: neighbours in a thread
+        unsigned long long m[kEach], before[kEach], sum;
+        const int mine0 = kEach * tid;
+        auto scan = [&](int used, auto mass_of) {
+          unsigned long long own = 0;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            m[i] = mine0 + i < used ? whole(sc.mass(mass_of(list[mine0 + i]))) : 0;
+            own += m[i];
+          }
+          const unsigned long long inc = warp_scan(own);
+          __syncthreads();
+          if (lane == 31) s.warp_a[warp] = inc;
+          __syncthreads();
+          unsigned long long at = inc - own;
+          sum = 0;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) at += s.warp_a[w];
+            sum += s.warp_a[w];
+          }
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            before[i] = at;
+            at += m[i];
+          }
+        };
+        // how many of this thread's, over all threads: the tokens that are kept come first
+        auto count = [&](auto test) {
+          int c = 0;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) c += test(i) ? 1 : 0;
+          c = __reduce_add_sync(0xffffffffu, c);
+          __syncthreads();
+          if (lane == 0) s.warp_a[warp] = c;
+          __syncthreads();
+          c = 0;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) c += static_cast<int>(s.warp_a[w]);
+          return c;
+        };
+        int kept = by_count ? min(n, top_k) : n;
+        scan(kept, [&](unsigned long long t) { return score_of(static_cast<uint32_t>(t >> 32)); });
+        if (by_mass) {
+          const unsigned long long below = alone ? target : max(1ull, times(top_p, sum, true));
+          kept = count([&](int i) { return mine0 + i < kept && before[i] < below; });
+        }
+        if (min_p > 0.f) {
+          const uint32_t least = min_p_key();
+          kept = count([&](int i) { return mine0 + i < kept && list[mine0 + i] >> 32 >= least; });
+        }
+        const unsigned long long last = list[kept - 1];
+        const uint32_t last_key = static_cast<uint32_t>(last >> 32);
+        // in order of index: (~index, key) downwards
+        __syncthreads();
+        for (int i = tid; i < kept; i += kThreads) list[i] = list[i] << 32 | list[i] >> 32;
+        size = 32;
+        while (size < kept) size *= 2;
+        __syncthreads();
+        sort(kept);
+        scan(kept, [&](unsigned long long t) { return score_of(static_cast<uint32_t>(t)); });
+        const unsigned long long want = times(u, sum, false);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+          if (want >= before[i] && want < before[i] + m[i]) {
+            const unsigned long long t = list[mine0 + i];
+            finish(static_cast<int>(~static_cast<uint32_t>(t >> 32)), score_of(static_cast<uint32_t>(t)), sum, last_key,
+                   static_cast<int>(~static_cast<uint32_t>(last)));
+          }
+        return;
+      }
+    }
 
     // The cut: the last token of the order before which there are fewer than `target` tokens, or less
     // than `fraction` of the mass kept so far.  Sets cut_key, cut and cut_last.
@@ -617,21 +797,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
       }
       cut = score_of(cut_key);
     };
-    if (by_count) {
-      find_cut(false, top_k, 0.f);
-    } else {
-      (void)bin_with(bins, true, 0, INFINITY, 0, kBins);
-      est_kept = s.est_before + s.est;
-    }
+    if (by_count) find_cut(false, top_k, 0.f);
     if (by_mass) find_cut(true, 0, top_p);
   }
   if (min_p > 0.f) {
-    if (tid == 0) {
-      const float least = __double2float_ru(fmax(static_cast<double>(top) + s.min_p_cut, -3.4028234663852886e38));
-      s.min_p_key = order_bits(least);  // (the highest score's own at most)
-    }
-    __syncthreads();
-    const uint32_t key = s.min_p_key;
+    const uint32_t key = min_p_key();
     if (key > cut_key) {
       cut_key = key;
       cut_last = INT32_MAX;
@@ -654,10 +824,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     }
   };
   unsigned long long sum = 0;
-  for (int v = v0 + lane; v < v1; v += 32) {
-    float m[N], x[N];
-    running(v, m, x);
-    sum += whole(m[N - 1]);
+  if (cuts) {
+    for (int v = v0 + lane; v < v1; v += 32) {
+      float m[N], x[N];
+      running(v, m, x);
+      sum += whole(m[N - 1]);
+    }
+  } else {
+#pragma unroll 4
+    for (int v = v0 + lane; v < v1; v += 32) {
+      float x[N], vector = 0.f;
+      Vec<T>::unpack(s_x[v], x);
+#pragma unroll
+      for (int k = 0; k < N; ++k) vector += sc.mass(x[k]);
+      sum += whole(vector);
+    }
   }
   sum = warp_sum(sum);
   __syncthreads();
@@ -696,9 +877,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
           token = index_of(v) + k;
           score = x[k];
         }
-      // the highest mass is 1 and among the kept: the sum's logarithm from what it is above 1
-      const float above = static_cast<float>(total - (1ull << kMassBits)) * (1.f / (1ull << kMassBits));
-      write(token, fmaf(sc.exponent(score), 0.693147181f, -log1pf(above)), cut_key, cut_last);
+      finish(token, score, total, cut_key, cut_last);
     }
     const unsigned long long step = __shfl_sync(0xffffffffu, scan, 31);
     if (want < before + step) return;
@@ -706,7 +885,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   }
 }
 
-// CTAs of a row: as many as one wave has room for, at least what its scores need.
 template <typename T>
 int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
@@ -714,9 +892,11 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   const size_t extra = p.top_k || p.top_p ? 2 * kBins * 4 : 0;
   constexpr size_t kRoom = 200 << 10;
   const int sms = std::max(1, sm_count());
+  // CTAs that an SM holds at once, and of a row: what its scores need, then more while all rows' run at once
+  auto bytes = [&](int c) { return static_cast<size_t>((vectors - 1) / c + 1) * 16 + extra; };
+  auto resident = [&](int c) { return std::min<long long>(4, (220 << 10) / (bytes(c) + (2 << 10))) * sms; };
   int C = 1;
-  while (C < kMaxCluster && (static_cast<size_t>((vectors - 1) / C + 1) * 16 > (96 << 10) || (static_cast<long long>(R) * C * 2 <= 2 * sms && vectors > C * 256)))
-    C *= 2;
+  while (C < kMaxCluster && (bytes(C) > (112 << 10) || (R * 2LL * C <= resident(2 * C) && vectors > C * 256))) C *= 2;
   p.pv = (vectors - 1) / C + 1;
   const size_t smem = static_cast<size_t>(p.pv) * 16 + extra;
   if (smem > kRoom) return SPECDEC_ERR_UNSUPPORTED;
