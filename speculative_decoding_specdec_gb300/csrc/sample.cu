@@ -29,8 +29,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kPer = kBins / kThreads, kList = 1024, kEach = kList / kThreads;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kMassBits = 42;
+constexpr long long kMaxRow = 1400 << 10;  // bytes
 constexpr uint32_t kTries = 1u << 17, kNs = 20000;  // a wait gives up after about 2.6 s
 
 struct SampleParams {
@@ -84,6 +85,29 @@ __device__ __forceinline__ unsigned long long whole(float v) {
   return e < 70 ? 0 : m >> (130 - e);  // v = m 2^(e - 172)
 }
 
+// The natural logarithm of 0 < f <= 1 in two floats, to about 2^-40: f = 2^k m, ln m = 2 artanh(r) with
+// r = (m - 1) / (m + 1), |r| <= 0.2, whose first term alone needs both.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two log_two(float f) {
+  int k;
+  float m = frexpf(f, &k);
+  if (m < 0.75f) {
+    m *= 2.f;
+    --k;
+  }
+  const float n = m - 1.f, d = m + 1.f, d_lo = m - (d - 1.f);  // m - 1 is exact
+  const float r = __fdiv_rn(n, d), r_lo = __fdiv_rn(fmaf(-r, d, n) - r * d_lo, d);
+  const float q = r * r, series = r * q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 13, 1.f / 11), 1.f / 9), 1.f / 7), 1.f / 5), 1.f / 3);
+  // k ln 2: the first float has few enough bits for an exact product
+  const float kf = static_cast<float>(k), base = kf * 0.693359375f;
+  const float hi = base + 2.f * r, back = hi - base;
+  const float lo = ((base - (hi - back)) + (2.f * r - back)) + fmaf(kf, -2.12194440e-4f, 2.f * (series + r_lo));
+  const float sum = hi + lo;
+  return Two{sum, lo - (sum - hi)};
+}
+
 // floor(f * x) and ceil(f * x) for 0 <= f < 1.
 __device__ __forceinline__ unsigned long long times(float f, unsigned long long x, bool up) {
   int e;
@@ -116,23 +140,23 @@ struct Shared {
   unsigned long long slot[2][3][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
   unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kWarps];
   uint64_t bar[kWarps];
-  double min_p_cut;
   float warp_f[kWarps];
-  uint32_t best, listed, lo, hi, min_p_key;
+  uint32_t best, listed, lo, hi;
   uint32_t count_before, count;
   float est_before, est;
   int found;
 };
 
-// One thread's bins: how many tokens they hold, what those weigh by the bins' middles, and both of all
-// before them.
+// One thread's bins: how many tokens they hold, and of all before them how many those are and what they
+// weigh by the bins' middles.
 struct Bins {
   uint32_t count[kPer], count_before;
-  float est[kPer], est_before;
+  float est_before;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+// kCuts: whether there may be top-k or top-p.
+template <typename T, bool kCuts>
+__global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const SampleParams p) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) char smem[];
   __shared__ Shared s;
@@ -200,8 +224,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   auto index_of = [&](int v) { return (base + v) * N - skew; };  // of a vector's first element
   float top = -INFINITY;
   bool odd = false;  // NaN or +infinity
-  // (in 64 bits, where they are slow, by one thread while the scores come)
-  if (tid == kThreads - 1 && min_p > 0.f) s.min_p_cut = static_cast<double>(temperature) * log(static_cast<double>(min_p));
   const uint4 none = sizeof(T) == 2 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                                     : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
   // A warp fetches its own vectors: those that lie in the row whole by one bulk copy, all of a CTA's in
@@ -308,14 +330,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   sc.sh = fminf(__fdiv_rn(kLog2eHi, temperature), 1e30f);
   sc.sl = sc.sh < 1e7f ? __fdiv_rn(fmaf(-sc.sh, temperature, kLog2eHi) + kLog2eLo, temperature) : 0.f;
 
-  // The least key that min-p keeps, by all threads.
+  // The least key that min-p keeps: of the first float that is not below max + T ln(min_p), in two floats
+  // (64 bits are so slow here that one logarithm in them took 5 us).
   auto min_p_key = [&] {
-    if (tid == 0) {
-      const float least = __double2float_ru(fmax(static_cast<double>(top) + s.min_p_cut, -3.4028234663852886e38));
-      s.min_p_key = order_bits(least);  // (the highest score's own at most)
-    }
-    __syncthreads();
-    return s.min_p_key;
+    const Two l = log_two(min_p);
+    const float a = temperature * l.hi, b = fmaf(temperature, l.hi, -a) + temperature * l.lo;
+    float hi = top + a;
+    const float back = hi - top, rest = (top - (hi - back)) + (a - back) + b;
+    const float sum = hi + rest, over = rest - (sum - hi);
+    if (!(sum > -INFINITY)) return 0u;  // (below every score: all are kept)
+    uint32_t key = order_bits(sum);
+    if (over > 0.f) ++key;              // the next float
+    return min(key, top_key);
   };
   // The drawn token, of a sum of kept masses.
   auto finish = [&](int token, float score, unsigned long long total, uint32_t key, int last) {
@@ -331,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   auto in_row = [&](int e) { return e >= 0 && e < p.V; };
   auto is_kept = [&](float x, int e) { return x > cut || (x == cut && e <= cut_last); };
   const bool by_mass = top_p < 1.f, by_count = top_k > 0 && top_k < p.V;
-  if (by_mass || by_count) {
+  if (kCuts && (by_mass || by_count)) {
     // Counts by place (place(x): -1 for none), merged over the cluster; middle(b): what a token of bin
     // b weighs, roughly.
     auto histogram = [&](auto place, auto middle) {
@@ -362,9 +388,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         g.count[i] = (C > 1 ? s_all : s_hist)[kPer * tid + i];
-        g.est[i] = static_cast<float>(g.count[i]) * middle(kPer * tid + i);
         count += g.count[i];
-        est += g.est[i];
+        est += static_cast<float>(g.count[i]) * middle(kPer * tid + i);
       }
       uint32_t ca = count;
       float ea = est;
@@ -392,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     };
     // The last bin in [lo, hi) that is not empty and begins before `tokens` tokens, or before `est`; -1
     // if there is none.  What it holds and what comes before it are left in s.
-    auto bin_with = [&](const Bins& g, bool mass, uint32_t tokens, float est, int lo, int hi) {
+    auto bin_with = [&](const Bins& g, auto middle, bool mass, uint32_t tokens, float est, int lo, int hi) {
       __syncthreads();
       if (tid == 0) s.best = 0;
       __syncthreads();
@@ -404,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         const int b = kPer * tid + i;
         if (g.count[i] > 0 && b >= lo && b < hi && (mass ? eb < est : cb < tokens)) at = i;
         cb += g.count[i];
-        eb += g.est[i];
+        if (mass) eb += static_cast<float>(g.count[i]) * middle(b);
       }
       if (at >= 0) atomicMax(&s.best, kPer * tid + at + 1);
       __syncthreads();
@@ -414,14 +439,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         eb = g.est_before;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
+          const float est_in = static_cast<float>(g.count[i]) * middle(kPer * tid + i);
           if (kPer * tid + i == best) {
             s.count_before = cb;
             s.est_before = eb;
             s.count = g.count[i];
-            s.est = g.est[i];
+            s.est = est_in;
           }
           cb += g.count[i];
-          eb += g.est[i];
+          eb += est_in;
         }
       }
       __syncthreads();
@@ -431,15 +457,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     // the bin holds.  kind(b) gives a test of scores: 1 before bin b (of what the histogram counted),
     // 2 in it, 0 neither.  With `fraction` the target is that much of what is kept so far, which the
     // first pass finds and est_total guesses.
-    auto mass_bin = [&](const Bins& g, auto kind, float fraction, float est_total, unsigned long long& target) {
+    auto mass_bin = [&](const Bins& g, auto middle, auto kind, float fraction, float est_total, unsigned long long& target) {
       int lo = 0, hi = kBins, low = -1;  // low: the last bin that was found to begin before the target
       unsigned long long low_before = 0;
       float want = fraction > 0.f ? fraction * est_total : static_cast<float>(target) * (1.f / (1ull << kMassBits));
       for (int round = 0; round < 48 && lo < hi; ++round) {
         // a guess; after a few the middle (so the bounds meet within the rounds there are)
         const int mid = lo + 1 + (hi - lo) / 2;
-        int b = round < 5 ? bin_with(g, true, 0, want, lo, hi) : -1;
-        if (b < 0) b = bin_with(g, true, 0, INFINITY, lo, min(mid, hi));
+        int b = round < 5 ? bin_with(g, middle, true, 0, want, lo, hi) : -1;
+        if (b < 0) b = bin_with(g, middle, true, 0, INFINITY, lo, min(mid, hi));
         if (b < 0) {
           lo = mid;
           continue;
@@ -481,27 +507,27 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         // the next guess: as much further as the target is from what has been summed
         want = est_before + (static_cast<float>(target) - static_cast<float>(before)) * (1.f / (1ull << kMassBits));
       }
-      (void)bin_with(g, true, 0, INFINITY, low, low + 1);  // (the last one tried may be another)
+      (void)bin_with(g, middle, true, 0, INFINITY, low, low + 1);  // (the last one tried may be another)
       target -= low_before;
       return low;
     };
-    const Bins bins = histogram([&](float x) { return bin_of(sc.z(x)); }, [](int b) { return ex2((b + 0.5f) * (-1.f / 64)); });
+    auto middle = [](int b) { return ex2((b + 0.5f) * (-1.f / 64)); };
+    const Bins bins = histogram([&](float x) { return bin_of(sc.z(x)); }, middle);
 
     // Most settings keep few tokens.  Where the bins up to the cut's hold no more than the list, one pass
-    // lists them all (and, for top-p alone, sums the row); the first CTA sorts them and does the rest.
-    // For top-p the bin is guessed from the bins' middles (2 % beyond what they say), and the listed
-    // mass shows whether it was far enough.
-    (void)bin_with(bins, true, 0, INFINITY, 0, kBins);
+    // counts them (and, for top-p alone, sums the row), another sends them to the first CTA in order of
+    // index, and that does the rest.  For top-p the bin is guessed from the bins' middles (2 % beyond
+    // what they say); the listed mass shows whether it was far enough.
+    (void)bin_with(bins, middle, true, 0, INFINITY, 0, kBins);
     float est_kept = s.est_before + s.est;
-    const int enough = by_count ? bin_with(bins, false, top_k, 0.f, 0, kBins) : bin_with(bins, true, 0, 1.02f * top_p * est_kept, 0, kBins);
-    if (s.count_before + s.count <= kList) {
-      unsigned long long* l_list = reinterpret_cast<unsigned long long*>(s_hist);
-      unsigned long long* list = reinterpret_cast<unsigned long long*>(s_all);
-      together();  // all are done with the histograms
-      if (tid == 0) s.listed = 0;
-      __syncthreads();
-      unsigned long long total = 0, in_list = 0;
+    const int enough = by_count ? bin_with(bins, middle, false, top_k, 0.f, 0, kBins) : bin_with(bins, middle, true, 0, 1.02f * top_p * est_kept, 0, kBins);
+    const uint32_t count_before = s.count_before;
+    if (count_before + s.count <= kList) {
+      unsigned long long* list = reinterpret_cast<unsigned long long*>(s_all);  // (key, ~index): larger is earlier in the order
+      unsigned long long* few = reinterpret_cast<unsigned long long*>(s_hist);
+      unsigned long long total = 0, in_list = 0, listed = 0;
       const bool alone = !by_count;
+      auto takes = [&](float x, int e) { return in_row(e) && bin_of(sc.z(x)) <= enough; };
       for (int v = v0 + lane; v < v1; v += 32) {
         float x[N];
         Vec<T>::unpack(s_x[v], x);
@@ -509,119 +535,163 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          if (alone) sum += sc.mass(x[k]);
-          if (in_row(e + k) && bin_of(sc.z(x[k])) <= enough) {
-            l_list[atomicAdd(&s.listed, 1u)] = static_cast<unsigned long long>(order_bits(x[k])) << 32 | ~static_cast<uint32_t>(e + k);
-            if (alone) in_list += whole(sc.mass(x[k]));
+          const float m = alone ? sc.mass(x[k]) : 0.f;
+          sum += m;
+          if (takes(x[k], e + k)) {
+            ++listed;
+            if (alone) in_list += whole(m);
           }
         }
         if (alone) total += whole(sum);
       }
-      unsigned long long listed = 0;
-      __syncthreads();
-      if (tid == 0) listed = s.listed;
+      const unsigned long long in_warp = warp_sum(listed);
       sum_all(total, in_list, listed);
+      // where this warp's begin: its CTA's are those of the sums before
+      unsigned long long to = 0, cta = 0;
+      __syncthreads();
+      if (lane == 0) s.warp_a[warp] = in_warp;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        to += w < warp ? s.warp_a[w] : 0;
+        cta += s.warp_a[w];
+      }
       const unsigned long long target = alone ? max(1ull, times(top_p, total, true)) : 0;
       if (in_list >= target) {
-        // its place among the first CTA's: behind those of the CTAs before
-        const Slots all = gather(s.listed, 0, 0);
-        int first = 0;
-        for (int i = 0; i < rank; ++i) first += static_cast<int>(all[0][i]);
-        const uint32_t to = cluster_map(list, 0);
-        for (uint32_t i = tid; i < s.listed; i += kThreads) remote_store(to + (first + i) * 8, l_list[i]);
+        const Slots all = gather(cta, 0, 0);  // (and all are done with the histograms)
+        for (int i = 0; i < rank; ++i) to += all[0][i];
+        if (in_warp > 0) {
+          const uint32_t first = cluster_map(list, 0);
+          for (int vv = v0; vv < v1; vv += 32) {
+            const int v = vv + lane;
+            float x[N];
+            Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
+            const int e = index_of(v);
+            uint32_t has = 0;
+#pragma unroll
+            for (int k = 0; k < N; ++k) has |= v < v1 && takes(x[k], e + k) ? 1u << k : 0;
+            if (!__any_sync(0xffffffffu, has != 0)) continue;
+            const uint32_t here = __popc(has), scan = static_cast<uint32_t>(warp_scan(here));
+            uint32_t at = static_cast<uint32_t>(to) + scan - here;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+              if (has >> k & 1)
+                remote_store(first + 8 * at++, static_cast<unsigned long long>(order_bits(x[k])) << 32 | ~static_cast<uint32_t>(e + k));
+            to += __shfl_sync(0xffffffffu, scan, 31);
+          }
+        }
         together();
         if (rank != 0) return;
+        // ------------------------------------------------------------- one CTA from here on
         const int n = static_cast<int>(listed);
-        int size = 32;
-        while (size < n) size *= 2;
-        // (sorted downwards, `skip` fills up: 0 is below every token)
-        auto sort = [&](int used) {
-          for (int i = used + tid; i < size; i += kThreads) list[i] = 0;
-          __syncthreads();
-          for (int run = 2; run <= size; run *= 2)
-            for (int gap = run / 2; gap > 0; gap /= 2) {
-              for (int i = tid; i < size / 2; i += kThreads) {
-                const int lo = 2 * i - (i & (gap - 1)), hi = lo + gap;
-                const unsigned long long x = list[lo], y = list[hi];
-                if ((x < y) == ((lo & run) == 0)) {
-                  list[lo] = y;
-                  list[hi] = x;
-                }
-              }
-              if (gap > 32 || gap == 1) __syncthreads();
-              else __syncwarp();
-            }
-        };
-        sort(n);
-        // masses and what is before: neighbours in a thread
-        unsigned long long m[kEach], before[kEach], sum;
-        const int mine0 = kEach * tid;
-        auto scan = [&](int used, auto mass_of) {
-          unsigned long long own = 0;
+        unsigned long long token[kEach], mass[kEach];  // consecutive ones of the list (0: none)
+        int bin[kEach];
 #pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            m[i] = mine0 + i < used ? whole(sc.mass(mass_of(list[mine0 + i]))) : 0;
-            own += m[i];
-          }
-          const unsigned long long inc = warp_scan(own);
-          __syncthreads();
-          if (lane == 31) s.warp_a[warp] = inc;
-          __syncthreads();
-          unsigned long long at = inc - own;
-          sum = 0;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) at += s.warp_a[w];
-            sum += s.warp_a[w];
-          }
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            before[i] = at;
-            at += m[i];
-          }
-        };
-        // how many of this thread's, over all threads: the tokens that are kept come first
-        auto count = [&](auto test) {
-          int c = 0;
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) c += test(i) ? 1 : 0;
-          c = __reduce_add_sync(0xffffffffu, c);
-          __syncthreads();
-          if (lane == 0) s.warp_a[warp] = c;
-          __syncthreads();
-          c = 0;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) c += static_cast<int>(s.warp_a[w]);
-          return c;
-        };
-        int kept = by_count ? min(n, top_k) : n;
-        scan(kept, [&](unsigned long long t) { return score_of(static_cast<uint32_t>(t >> 32)); });
-        if (by_mass) {
-          const unsigned long long below = alone ? target : max(1ull, times(top_p, sum, true));
-          kept = count([&](int i) { return mine0 + i < kept && before[i] < below; });
+        for (int i = 0; i < kEach; ++i) {
+          token[i] = kEach * tid + i < n ? list[kEach * tid + i] : 0;
+          const float x = token[i] ? score_of(static_cast<uint32_t>(token[i] >> 32)) : -INFINITY;
+          mass[i] = token[i] ? whole(sc.mass(x)) : 0;
+          bin[i] = token[i] ? bin_of(sc.z(x)) : kBins;
         }
+        auto block_sum = [&](unsigned long long v) {
+          v = warp_sum(v);
+          __syncthreads();
+          if (lane == 0) s.warp_a[warp] = v;
+          __syncthreads();
+          v = 0;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) v += s.warp_a[w];
+          return v;
+        };
+        // The last token of bin b before which, in the bin, there are fewer than `left` tokens, or less mass.
+        auto last_in = [&](int b, bool by_sum, unsigned long long left) {
+          __syncthreads();
+          if (tid == 0) s.listed = s.best = 0;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < kEach; ++i)
+            if (bin[i] == b) few[atomicAdd(&s.listed, 1u)] = token[i];
+          __syncthreads();
+          const int m = static_cast<int>(s.listed);
+          for (int i = warp; i < m; i += kWarps) {
+            const unsigned long long me = few[i];
+            uint32_t tokens = 0;
+            unsigned long long sum = 0;
+            for (int j = lane; j < m; j += 32)
+              if (few[j] > me) {
+                ++tokens;
+                if (by_sum) sum += whole(sc.mass(score_of(static_cast<uint32_t>(few[j] >> 32))));
+              }
+            tokens = __reduce_add_sync(0xffffffffu, tokens);
+            if (by_sum) sum = warp_sum(sum);
+            if (lane == 0 && (by_sum ? sum : tokens) < left) atomicMax(&s.best, tokens << 16 | (i + 1));
+          }
+          __syncthreads();
+          return m ? few[max(0, static_cast<int>(s.best & 0xFFFF) - 1)] : 0ull;
+        };
+        unsigned long long end = 0;  // the last that is kept
+        if (by_count) end = last_in(enough, false, top_k - count_before);
+        if (by_mass) {
+          unsigned long long own = 0;
+          if (by_count) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) own += token[i] >= end ? mass[i] : 0;
+            own = block_sum(own);
+          }
+          const unsigned long long below = by_count ? max(1ull, times(top_p, own, true)) : target;
+          // the last bin that begins before `below`
+          int lo = 0, hi = enough + 1;
+          unsigned long long at_lo = 0;
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            unsigned long long v = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) v += bin[i] < mid ? mass[i] : 0;
+            v = block_sum(v);
+            if (v < below) {
+              lo = mid;
+              at_lo = v;
+            } else {
+              hi = mid;
+            }
+          }
+          end = max(end, last_in(lo, true, below - at_lo));
+        }
+        uint32_t end_key = static_cast<uint32_t>(end >> 32);
+        int end_index = static_cast<int>(~static_cast<uint32_t>(end));
         if (min_p > 0.f) {
           const uint32_t least = min_p_key();
-          kept = count([&](int i) { return mine0 + i < kept && list[mine0 + i] >> 32 >= least; });
-        }
-        const unsigned long long last = list[kept - 1];
-        const uint32_t last_key = static_cast<uint32_t>(last >> 32);
-        // in order of index: (~index, key) downwards
-        __syncthreads();
-        for (int i = tid; i < kept; i += kThreads) list[i] = list[i] << 32 | list[i] >> 32;
-        size = 32;
-        while (size < kept) size *= 2;
-        __syncthreads();
-        sort(kept);
-        scan(kept, [&](unsigned long long t) { return score_of(static_cast<uint32_t>(t)); });
-        const unsigned long long want = times(u, sum, false);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-          if (want >= before[i] && want < before[i] + m[i]) {
-            const unsigned long long t = list[mine0 + i];
-            finish(static_cast<int>(~static_cast<uint32_t>(t >> 32)), score_of(static_cast<uint32_t>(t)), sum, last_key,
-                   static_cast<int>(~static_cast<uint32_t>(last)));
+          if (least > end_key) {
+            end = static_cast<unsigned long long>(least) << 32;
+            end_key = least;
+            end_index = INT32_MAX;
           }
+        }
+        // the draw, in order of index
+        unsigned long long own = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) own += token[i] >= end ? mass[i] : 0;
+        const unsigned long long inc = warp_scan(own);
+        __syncthreads();
+        if (lane == 31) s.warp_a[warp] = inc;
+        __syncthreads();
+        unsigned long long at = inc - own, sum = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          at += w < warp ? s.warp_a[w] : 0;
+          sum += s.warp_a[w];
+        }
+        const unsigned long long want = times(u, sum, false);
+        if (want < at || want >= at + own) return;
+        bool got = false;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          at += token[i] >= end ? mass[i] : 0;
+          if (!got && at > want) {
+            got = true;
+            finish(static_cast<int>(~static_cast<uint32_t>(token[i])), score_of(static_cast<uint32_t>(token[i] >> 32)), sum, end_key, end_index);
+          }
+        }
         return;
       }
     }
@@ -631,14 +701,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     auto find_cut = [&](bool mass, unsigned long long target, float fraction) {
       int bin;
       if (mass) {
-        bin = mass_bin(bins, [&](int b) {
+        bin = mass_bin(bins, middle, [&](int b) {
           return [&sc, b](float x) {
             const float z = sc.z(x) * 64.f;
             return z < b ? 1 : (z < b + 1 || b == kBins - 1 ? 2 : 0);
           };
         }, fraction, est_kept, target);
       } else {
-        bin = bin_with(bins, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
+        bin = bin_with(bins, middle, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
         target -= s.count_before;
         est_kept = s.est_before + s.est;
       }
@@ -681,11 +751,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         const int shift = max(0, 21 - __clz(khi - klo));
         const uint32_t a = klo, z = khi;
         auto first_of = [=](int b) { return z - (static_cast<uint32_t>(b) << shift); };  // a bin's highest key
-        const Bins g = histogram([&](float x) { return inside(x) ? static_cast<int>((z - order_bits(x)) >> shift) : -1; },
-                                 [&](int b) { return b <= static_cast<int>((z - a) >> shift) ? sc.mass(score_of(max(a, first_of(b)))) : 0.f; });
+        auto middle = [&](int b) { return b <= static_cast<int>((z - a) >> shift) ? sc.mass(score_of(max(a, first_of(b)))) : 0.f; };
+        const Bins g = histogram([&](float x) { return inside(x) ? static_cast<int>((z - order_bits(x)) >> shift) : -1; }, middle);
         int at;
         if (mass) {
-          at = mass_bin(g, [&](int b) {
+          at = mass_bin(g, middle, [&](int b) {
             const uint32_t h = first_of(b);
             return [=](float x) {
               const uint32_t key = order_bits(x);
@@ -693,7 +763,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             };
           }, 0.f, 0.f, target);
         } else {
-          at = bin_with(g, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
+          at = bin_with(g, middle, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
           target -= s.count_before;
         }
         count = s.count;
@@ -900,9 +970,13 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   p.pv = (vectors - 1) / C + 1;
   const size_t smem = static_cast<size_t>(p.pv) * 16 + extra;
   if (smem > kRoom) return SPECDEC_ERR_UNSUPPORTED;
-  auto kernel = sample_kernel<T>;
+  auto kernel = extra ? sample_kernel<T, true> : sample_kernel<T, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRoom));
   if (e != cudaSuccess) return map_cuda_error(e);
+  if (C > 8) {
+    const cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e2 != cudaSuccess) return map_cuda_error(e2);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -932,7 +1006,7 @@ extern "C" int specdec_sample(const specdec_sample_args* a, void* stream) {
       off(a->top_k, 4) || off(a->top_p, 4) || off(a->min_p, 4) || off(a->logprob, 4) || off(a->keep_bounds, 4))
     return SPECDEC_ERR_INVALID_ARG;
   if (a->keep_bounds && a->R > 1 && a->bounds_stride < 1) return SPECDEC_ERR_INVALID_ARG;
-  if (a->R >= (1 << 24) || a->V >= (1 << 24) || a->bounds_stride >= (1 << 30)) return SPECDEC_ERR_UNSUPPORTED;
+  if (a->R >= (1 << 24) || static_cast<long long>(a->V) * es > kMaxRow || a->bounds_stride >= (1 << 30)) return SPECDEC_ERR_UNSUPPORTED;
   SampleParams p = {};
   p.x = static_cast<const char*>(a->logits);
   p.stride = a->row_stride * es;
