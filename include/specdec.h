@@ -720,6 +720,42 @@ size_t specdec_tree_attention_workspace(int dtype, int B, int T, int heads_q, in
                                         int head_dim);
 
 /*
+ * The same over a prefix that rows share: its K/V is held once, read once for all rows that share it,
+ * and not part of their own cache rows.  [BSDDR section 2.3 batches sequences of one pool; several samples
+ * of one prompt, or requests behind one long instruction, begin with the same columns.]
+ *   out_i = the softmax-weighted sum over the prefix's columns and the row's own (those of
+ *   specdec_tree_attention, which `own` describes) together.
+ * Prefix p (of P) has prefix_len[p] >= 0 columns of row p of `prefix` from column 0 on, or from
+ * prefix_first[p] on; with prefix.rows == 1 all are in row 0 (prefix_first is then needed).  Batch rows
+ * group_start[p] <= b < group_start[p + 1] share it; rows of no group, or of one without columns, have their
+ * own columns alone.  Every node of a row sees the whole prefix; own.width, n_committed and the positions
+ * that the tree operators give count a row's own tokens alone (specdec_norm_rotary_args.start adds the
+ * prefix's).  P = 0 is specdec_tree_attention.
+ * lse is over both.  A value of V in the prefix that is not finite enters that value of the head alone.
+ * Two passes: all query rows of a group against its prefix, whose (maximum, sum, output) stay in fp32, then
+ * the rows' own columns with these merged; own.workspace has specdec_prefix_attention_workspace bytes.
+ * Device-detected errors besides those of specdec_tree_attention: bounds that are not ascending
+ * within [0, B] (SPECDEC_ERR_INPUT_RANGE, no row is written), a negative length or first column
+ * (SPECDEC_ERR_INPUT_RANGE) or columns beyond prefix.cap_cols (SPECDEC_ERR_CAPACITY): the rows of that
+ * group are not written.  Limits besides: P <= 512; prefix of the cache's dtype, heads and head_dim, with layer `own.layer`.
+ */
+typedef struct {
+  specdec_tree_attention_args own;
+  specdec_kv_view prefix;
+  int P;
+  const int32_t* prefix_len;      /* [P] */
+  const int32_t* prefix_first;    /* [P], or NULL: 0 */
+  const int32_t* group_start;     /* [P + 1] */
+} specdec_prefix_attention_args;
+
+int specdec_prefix_attention(const specdec_prefix_attention_args* args, void* stream);
+
+/* Workspace bytes specdec_prefix_attention needs for this shape on the current device, whatever the
+ * lengths and groups are (0 for an invalid shape).  It serves specdec_tree_attention too. */
+size_t specdec_prefix_attention_workspace(int dtype, int B, int T, int heads_q, int heads_kv,
+                                          int head_dim, int P);
+
+/*
  * Greedy verification of a tree.  [IE5 "Exactness Means Different Things For Greedy And Sampled
  * Output", "Draft Possible Tokens, Then Verify Them Together", along the tree's paths.]
  * Row b's walk starts at node 0.  At a node the target's choice is the maximum of its score row

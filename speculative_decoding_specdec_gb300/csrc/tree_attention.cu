@@ -71,7 +71,7 @@ struct Cursor {
 };
 
 // R: query rows of an M-tile; NB: blocks of 128 head values (1 or 2).
-template <typename T, int R, int NB>
+template <typename T, int R, int NB, bool kPrefix>
 __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnParams p) {
   extern __shared__ __align__(16) char smem[];
   __shared__ uint64_t s_full[kMaxWarps][kStages];
@@ -87,18 +87,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
   auto merge = [&](int w) {                                        // [R][hd] of warp w
     return reinterpret_cast<float*>(smem + R * hd * 4 + w * warp_bytes + kStages * 2 * kCols * pitch) + kCols * R;
   };
-  const AttnPlan plan = attn_plan_at(smem + R * hd * 4 + warps * warp_bytes, p.B);
-  if (warp == 0) attn_plan(p, tile_cols, plan);
+  const AttnPlan plan = attn_plan_at(smem + R * hd * 4 + warps * warp_bytes, kPrefix ? p.P : p.B);
+  if (warp == 0) attn_plan<kPrefix>(p, tile_cols, plan);
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
     fence_mbar_init();
   }
   __syncthreads();
-  const AttnShares sh = attn_shares(p, plan);
+  const AttnShares sh = attn_shares<kPrefix>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   if (sh.total == 0 || g >= sh.groups) return;
   const int x1 = sh.start(g + 1);
-  const int nrows = min(R, p.T * p.G - mt * R);  // query rows of this M-tile: (node, head) pairs
   // The warp's columns of the cursor's tile into stage `st`: lanes 0..15 copy K's, the others V's.
   auto fetch = [&](const Cursor& c, int st) {
     const int col = c.tile * tile_cols + warp * kCols, n = max(0, min(kCols, c.seg.cols - col));
@@ -113,12 +112,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
   };
   auto advance = [&](Cursor& c) {
     if (++c.tile >= c.seg.tile1) {
-      c.more = attn_next(p, plan, c.seg.next, x1, c.seg);
+      c.more = attn_next<kPrefix>(p, plan, c.seg.next, x1, c.seg);
       c.tile = c.seg.tile0;
     }
   };
   Cursor ahead;
-  ahead.more = attn_next(p, plan, sh.start(g), x1, ahead.seg);
+  ahead.more = attn_next<kPrefix>(p, plan, sh.start(g), x1, ahead.seg);
   ahead.tile = ahead.seg.tile0;
   int loaded = 0, used = 0, row_b = -1;  // tiles asked for, tiles done
   for (; loaded < kStages && ahead.more; ++loaded) {
@@ -127,26 +126,27 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
   }
   bool ok = true;
   AttnSegment seg;
-  for (int x = sh.start(g); attn_next(p, plan, x, x1, seg); x = seg.next) {
+  for (int x = sh.start(g); attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
     __syncthreads();  // the segment before is done with Q and the tree
-    const bool other = seg.b != row_b;
+    const int nrows = kPrefix ? seg.rows : min(R, p.T * p.G - mt * R);  // query rows of this M-tile: (node, head) pairs
+    const bool other = kPrefix ? row_b < 0 : seg.b != row_b;
     row_b = seg.b;
     if (other) {
-      if (p.parents && tid < p.T) s_par[tid] = p.parents[seg.b * p.T + tid];
+      if (!kPrefix && p.parents && tid < p.T) s_par[tid] = p.parents[seg.b * p.T + tid];
       if (tid == 0) s_bad = 0;
     }
     for (int i = tid * 4; i < R * hd; i += threads * 4) {
-      const int r = i / hd, d = i - r * hd, rr = mt * R + r;
+      const int r = i / hd, d = i - r * hd;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < nrows) {
-        const int t = rr / p.G, qh = seg.h * p.G + rr - t * p.G;
-        v = load4<T>(p.q + seg.b * p.qr + t * p.qt + (static_cast<long long>(qh) * hd + d) * es);
+        const AttnQuery at = attn_query<kPrefix>(p, seg, mt * R + r);
+        v = load4<T>(p.q + at.b * p.qr + at.t * p.qt + (static_cast<long long>(at.h) * hd + d) * es);
       }
       *reinterpret_cast<float4*>(s_q + i) = make_float4(v.x * p.scale_log2, v.y * p.scale_log2,
                                                         v.z * p.scale_log2, v.w * p.scale_log2);
     }
     __syncthreads();
-    if (other) {
+    if (!kPrefix && other) {
       for (int i = tid; i < p.T; i += threads) {
         bool bad = false;
         s_anc[i] = tree_ancestors(p.parents ? s_par : nullptr, i, bad);
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
           z[r] += __shfl_xor_sync(0xffffffffu, z[r], 16);
           if (node >= 0) {
             const int rr = mt * R + r;
-            const bool see = node < p.T && r < nrows && (s_anc[p.g_shift >= 0 ? rr >> p.g_shift : rr / p.G] >> node & 1);
+            const bool see = !kPrefix && node < p.T && r < nrows && (s_anc[p.g_shift >= 0 ? rr >> p.g_shift : rr / p.G] >> node & 1);
             if (!see) z[r] = -INFINITY;
           }
           up |= z[r] > m[r] + kGrow || (m[r] == -INFINITY && z[r] > m[r]);
@@ -308,8 +308,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
       return acc;
     };
     auto store = [&](int r, int i, float4 acc, float mm, float ll) {
-      const int rr = mt * R + r, t = rr / p.G, qh = seg.h * p.G + rr - t * p.G;
+      const AttnQuery row = attn_query<kPrefix>(p, seg, mt * R + r);
+      const int t = row.t, qh = row.h;
+      if constexpr (kPrefix) {
+        const long long at = attn_prior_at(p, row.b, t, qh);
+        if (i == 0) p.prior_ml[at] = make_float2(mm, ll);
+        *reinterpret_cast<float4*>(p.prior_o + at * hd + i * 4) = acc;
+        return;
+      }
       const bool live = s_anc[t] != 0;
+      if (p.prior) {
+        const int state = p.prior[seg.b];
+        if (state < 0) return;
+        if (state > 0) {
+          const long long at = attn_prior_at(p, seg.b, t, qh);
+          float f0, f1;
+          const float2 ml = attn_join(mm, ll, __ldcg(p.prior_ml + at), f0, f1);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.prior_o + at * hd + i * 4));
+          mm = ml.x;
+          ll = ml.y;
+          acc = make_float4(acc.x * f0 + v.x * f1, acc.y * f0 + v.y * f1, acc.z * f0 + v.z * f1, acc.w * f0 + v.w * f1);
+        }
+      }
       const float inv = 1.f / ll;
       store4<T>(p.out + seg.b * p.outr + t * p.outt + (static_cast<long long>(qh) * hd + i * 4) * es,
                 live ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
@@ -356,7 +376,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
 // shared memory (cp.async, two stages) in place of streaming their own.  A lane computes the scores
 // of one column, the softmax of a row is warp-local, and for O a lane owns 4 (or 8) of the head's
 // values.  NB: blocks of 128 head values (1 or 2).
-template <typename T, int NB>
+template <typename T, int NB, bool kPrefix>
 __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) {
   constexpr int RG = 8, kThreads = RG * 32, M = RG * 4, kTile = kRowsTile;
   extern __shared__ __align__(16) char smem[];
@@ -368,26 +388,26 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
   char* s_v = s_k + 2 * kTile * pitch;
   float* s_q = reinterpret_cast<float*>(s_v + 2 * kTile * pitch);  // [M][hd], times scale_log2
   float4* s_p = reinterpret_cast<float4*>(s_q + M * hd) + warp * kTile;  // [kTile] x 4 rows
-  const AttnPlan plan = attn_plan_at(reinterpret_cast<float4*>(s_q + M * hd) + RG * kTile, p.B);
-  if (warp == 0) attn_plan(p, kTile, plan);
+  const AttnPlan plan = attn_plan_at(reinterpret_cast<float4*>(s_q + M * hd) + RG * kTile, kPrefix ? p.P : p.B);
+  if (warp == 0) attn_plan<kPrefix>(p, kTile, plan);
   __syncthreads();
-  const AttnShares sh = attn_shares(p, plan);
+  const AttnShares sh = attn_shares<kPrefix>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   if (sh.total == 0 || g >= sh.groups) return;
   const int x1 = sh.start(g + 1);
-  const int nrows = min(M, p.T * p.G - mt * M);  // query rows of this M-tile: (node, head) pairs
   int row_b = -1;
   AttnSegment seg;
-  for (int x = sh.start(g); attn_next(p, plan, x, x1, seg); x = seg.next) {
-    if (seg.b != row_b) {  // a new batch row: its tree
+  for (int x = sh.start(g); attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
+    const int nrows = kPrefix ? seg.rows : min(M, p.T * p.G - mt * M);  // query rows of this M-tile: (node, head) pairs
+    if (kPrefix ? row_b < 0 : seg.b != row_b) {  // a new batch row: its tree
       row_b = seg.b;
       __syncthreads();
-      if (p.parents) {
+      if (!kPrefix && p.parents) {
         for (int i = tid; i < p.T; i += kThreads) s_par[i] = p.parents[seg.b * p.T + i];
         __syncthreads();
       }
       bool bad = false;
-      for (int i = tid; i < p.T; i += kThreads)
+      for (int i = tid; !kPrefix && i < p.T; i += kThreads)
         s_anc[i] = tree_ancestors(p.parents ? s_par : nullptr, i, bad);
       if (bad) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
       s_bad = 0;
@@ -400,11 +420,11 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
       continue;
     }
     for (int i = tid; i < M * hd; i += kThreads) {
-      const int r = i / hd, d = i - r * hd, rr = mt * M + r;
+      const int r = i / hd, d = i - r * hd;
       float v = 0.f;
       if (r < nrows) {
-        const int t = rr / p.G, qh = seg.h * p.G + rr % p.G;
-        v = Vec<T>::scalar(reinterpret_cast<const T*>(p.q + seg.b * p.qr + t * p.qt) + qh * hd + d);
+        const AttnQuery at = attn_query<kPrefix>(p, seg, mt * M + r);
+        v = Vec<T>::scalar(reinterpret_cast<const T*>(p.q + at.b * p.qr + at.t * p.qt) + at.h * hd + d);
       }
       s_q[i] = v * p.scale_log2;
     }
@@ -412,7 +432,7 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = warp * 4 + k;
-      anc[k] = r < nrows ? s_anc[(mt * M + r) / p.G] : 0ull;
+      anc[k] = r < nrows ? (kPrefix ? ~0ull : s_anc[(mt * M + r) / p.G]) : 0ull;
     }
     const long long crow = p.one_row ? 0 : seg.b;
     const char* kbase = p.cache.base + crow * p.cache.srow + seg.h * p.cache.shead +
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
       float* pv = reinterpret_cast<float*>(&pr);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool see = node < 0 ? anc[k] != 0 : node < p.T && (anc[k] >> node & 1);
+        const bool see = node < 0 ? anc[k] != 0 : !kPrefix && node < p.T && (anc[k] >> node & 1);
         float s = see ? z[k] : -INFINITY;
         float mx = s;
 #pragma unroll
@@ -573,9 +593,39 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int r = warp * 4 + k, rr = mt * M + r;
+      const int r = warp * 4 + k;
       if (r >= nrows) continue;
-      const int t = rr / p.G, qh = seg.h * p.G + rr % p.G;
+      const AttnQuery row = attn_query<kPrefix>(p, seg, mt * M + r);
+      const int t = row.t, qh = row.h;
+      if constexpr (kPrefix) {
+        const long long at = attn_prior_at(p, row.b, t, qh);
+        if (lane == 0) p.prior_ml[at] = make_float2(m[k], l[k]);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int d = j * 128 + lane * 4;
+          if (d < hd) *reinterpret_cast<float4*>(p.prior_o + at * hd + d) = o[k][j];
+        }
+        continue;
+      }
+      if (p.prior) {
+        const int state = p.prior[seg.b];
+        if (state < 0) continue;
+        if (state > 0) {
+          const long long at = attn_prior_at(p, seg.b, t, qh);
+          float f0, f1;
+          const float2 ml = attn_join(m[k], l[k], __ldcg(p.prior_ml + at), f0, f1);
+          m[k] = ml.x;
+          l[k] = ml.y;
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            const int d = j * 128 + lane * 4;
+            if (d < hd) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.prior_o + at * hd + d));
+              o[k][j] = make_float4(o[k][j].x * f0 + v.x * f1, o[k][j].y * f0 + v.y * f1, o[k][j].z * f0 + v.z * f1, o[k][j].w * f0 + v.w * f1);
+            }
+          }
+        }
+      }
       const float inv = 1.f / l[k];
       char* y = p.out + seg.b * p.outr + t * p.outt + static_cast<long long>(qh) * hd * sizeof(T);
 #pragma unroll
@@ -680,22 +730,79 @@ AttnWorkspace attn_workspace(const AttnShape& s, int hd) {
   return w;
 }
 
-template <typename T, typename K>
-int launch_fma(K kernel, const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
+template <typename K>
+int launch_fma(K kernel, const AttnParams& p, const AttnShape& s, bool prefix, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(s.smem) + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<s.grid, s.warps * 32, s.smem + attn_plan_bytes(p.B), stream>>>(p);
+  kernel<<<s.grid, s.warps * 32, s.smem + (prefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)), stream>>>(p);
   return map_cuda_error(cudaGetLastError());
 }
-template <typename T, int NB>
+template <typename T, int NB, bool kPrefix>
 int launch_fma_rows(const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
   switch (s.M) {
-    case 4: return launch_fma<T>(attn_fma_kernel<T, 4, NB>, p, s, stream);
-    case 8: return launch_fma<T>(attn_fma_kernel<T, 8, NB>, p, s, stream);
-    case 16: return launch_fma<T>(attn_fma_kernel<T, 16, NB>, p, s, stream);
-    default: return launch_fma<T>(attn_fma_rows_kernel<T, NB>, p, s, stream);
+    case 4: return launch_fma(attn_fma_kernel<T, 4, NB, kPrefix>, p, s, kPrefix, stream);
+    case 8: return launch_fma(attn_fma_kernel<T, 8, NB, kPrefix>, p, s, kPrefix, stream);
+    case 16: return launch_fma(attn_fma_kernel<T, 16, NB, kPrefix>, p, s, kPrefix, stream);
+    default: return launch_fma(attn_fma_rows_kernel<T, NB, kPrefix>, p, s, kPrefix, stream);
   }
+}
+// The pass that a shape is for.
+template <bool kPrefix>
+int launch_attention(const AttnParams& p, const AttnShape& s, int es, int rows, cudaStream_t stream) {
+  if (s.kind == kTc) return launch_attn_tc(p, rows, s.grid, kPrefix, stream);
+  if (s.kind == kMma) return launch_attn_mma(p, s.M, rows, s.grid, kPrefix, stream);
+  if (es == 2)
+    return p.hd <= 128 ? launch_fma_rows<uint16_t, 1, kPrefix>(p, s, stream)
+                       : launch_fma_rows<uint16_t, 2, kPrefix>(p, s, stream);
+  return p.hd <= 128 ? launch_fma_rows<float, 1, kPrefix>(p, s, stream)
+                     : launch_fma_rows<float, 2, kPrefix>(p, s, stream);
+}
+
+// The shape of a pass over prefixes for at most R query rows per K/V head, in units of up to M.
+AttnShape prefix_shape(int es, long long R, int hd, long long columns) {
+  AttnShape s = {};
+  int per_sm = 1;
+  if (es != 2 || (hd != 64 && hd != 128)) {
+    s = fma_shape(es, 1, static_cast<int>(std::min<long long>(R, 64)), hd);
+    s.groups *= s.MT;  // (units have one M-tile)
+  } else {
+    if (R <= 16 || (R <= 32 && columns <= kFewColumns)) {
+      s.kind = kMma;
+      attn_mma_shape(static_cast<int>(R), hd, &s.M, &s.MT, &s.tile, &per_sm);
+      s.open = 3;
+    } else {
+      s.kind = kTc;
+      attn_tc_shape(1, &s.M, &s.MT);
+      s.tile = 128;
+      s.open = R > 128 ? 6 : 4;
+    }
+    s.groups = std::max(1, sm_count() * per_sm);
+    s.min_tiles = 1;
+  }
+  s.MT = 1;
+  s.grid = sm_count() > 0 ? s.groups : 0;
+  return s;
+}
+
+// A workspace for prefixes too: the passes use the same room for cut units one after the other; what
+// the prefix pass leaves for the rows follows.
+struct PrefixWorkspace {
+  size_t state, ml, o, bytes;  // offsets
+};
+PrefixWorkspace prefix_workspace(int es, int B, int T, int Hq, int G, int hd) {
+  size_t most = 0;  // of the kernels that the lengths may decide for
+  for (const long long columns : {0LL, kFewColumns + 1}) {
+    most = std::max(most, attn_workspace(attn_shape(es, T, G, hd, columns), hd).bytes);
+    most = std::max(most, attn_workspace(prefix_shape(es, static_cast<long long>(B) * T * G, hd, columns), hd).bytes);
+  }
+  const size_t rows = static_cast<size_t>(B) * T * Hq;
+  PrefixWorkspace w;
+  w.state = round256(most);
+  w.ml = w.state + round256(static_cast<size_t>(B) * 4);
+  w.o = w.ml + round256(rows * 8);
+  w.bytes = w.o + round256(rows * hd * 4);
+  return w;
 }
 
 bool attn_sizes_ok(int dtype, int B, int T, int heads_q, int heads_kv, int head_dim) {
@@ -705,24 +812,8 @@ bool attn_sizes_ok(int dtype, int B, int T, int heads_q, int heads_kv, int head_
          head_dim <= 256 && head_dim * es % 16 == 0 && heads_q / heads_kv <= kMaxQueries / T;
 }
 
-}  // namespace
-}  // namespace specdec
-
-extern "C" size_t specdec_tree_attention_workspace(int dtype, int B, int T, int heads_q,
-                                                   int heads_kv, int head_dim) {
-  using namespace specdec;
-  if (!attn_sizes_ok(dtype, B, T, heads_q, heads_kv, head_dim)) return 0;
-  size_t most = 0;  // of the kernels that the lengths may decide for
-  for (const long long columns : {0LL, kFewColumns + 1}) {
-    const AttnShape s = attn_shape(elem_size(dtype), T, heads_q / heads_kv, head_dim, columns);
-    most = std::max(most, attn_workspace(s, head_dim).bytes);
-  }
-  return most;
-}
-
-extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void* stream) {
-  using namespace specdec;
-  if (!a) return SPECDEC_ERR_INVALID_ARG;
+// Host checks of a call (SPECDEC_OK with B == 0: nothing to do).
+int check_attention(const specdec_tree_attention_args* a) {
   if (a->B < 0 || a->T < 1 || a->heads_q < 1 || a->layer < 0 || !std::isfinite(a->scale))
     return SPECDEC_ERR_INVALID_ARG;
   if (a->B > kAttnMaxRows || a->T > SPECDEC_MAX_TREE) return SPECDEC_ERR_UNSUPPORTED;
@@ -748,19 +839,14 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
       (strides * es) % 16 || reinterpret_cast<uintptr_t>(a->lse) % 4)
     return SPECDEC_ERR_UNSUPPORTED;
   if (reinterpret_cast<uintptr_t>(a->workspace) % 256) return SPECDEC_ERR_INVALID_ARG;
-  if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
+  return SPECDEC_OK;
+}
+
+// What both passes take from the arguments.
+AttnParams attention_params(const specdec_tree_attention_args* a) {
+  const specdec_kv_view& c = a->cache;
+  const long long es = elem_size(c.dtype);
   const int G = a->heads_q / c.heads;
-  AttnShape s = attn_shape(static_cast<int>(es), a->T, G, c.head_dim,
-                           static_cast<long long>(a->B) * c.heads * c.cap_cols);
-  // no more groups than the longest rows could give work to
-  const long long tiles = static_cast<long long>(a->B) * c.heads * ((c.cap_cols - 1) / s.tile + 1 + s.open);
-  s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
-  s.grid = s.groups * s.MT;
-  const AttnWorkspace w = attn_workspace(s, c.head_dim);
-  if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
-  if (s.grid > static_cast<int>(kTicketBytes / 4)) return SPECDEC_ERR_UNSUPPORTED;
-  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kCols + 16) >= (1LL << 31))
-    return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   AttnParams p = {};
   p.cache = to_bytes(c);
   p.cache.base += a->layer * p.cache.sl;
@@ -777,11 +863,6 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   p.rows = a->rows;
   p.first_col = a->first_col;
   p.status = a->dev_status;
-  char* ws = static_cast<char*>(a->workspace);
-  p.ticket = reinterpret_cast<unsigned*>(ws + w.ticket);
-  p.cuts = reinterpret_cast<int4*>(ws + w.cuts);
-  p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.scale_log2 = a->scale * kLog2e;
   p.B = a->B;
   p.T = a->T;
@@ -791,17 +872,121 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   p.hd = c.head_dim;
   p.cap = c.cap_cols;
   p.one_row = c.rows == 1 ? 1 : 0;
+  p.g_shift = (G & (G - 1)) == 0 ? __builtin_ctz(G) : -1;
+  return p;
+}
+
+// How a shape's work is shared out, and where in the workspace its cut units go.
+void set_shape(AttnParams& p, const AttnShape& s, void* workspace) {
+  const AttnWorkspace w = attn_workspace(s, p.hd);
+  char* ws = static_cast<char*>(workspace);
+  p.ticket = reinterpret_cast<unsigned*>(ws + w.ticket);
+  p.cuts = reinterpret_cast<int4*>(ws + w.cuts);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.MT = s.MT;
+  p.M = s.M;
   p.groups = s.groups;
   p.min_tiles = s.min_tiles;
   p.open = s.open;
-  p.g_shift = (G & (G - 1)) == 0 ? __builtin_ctz(G) : -1;
-  cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
-  if (s.kind == kTc) return launch_attn_tc(p, c.rows, s.grid, stream_);
-  if (s.kind == kMma) return launch_attn_mma(p, s.M, c.rows, s.grid, stream_);
-  if (es == 2)
-    return c.head_dim <= 128 ? launch_fma_rows<uint16_t, 1>(p, s, stream_)
-                             : launch_fma_rows<uint16_t, 2>(p, s, stream_);
-  return c.head_dim <= 128 ? launch_fma_rows<float, 1>(p, s, stream_)
-                           : launch_fma_rows<float, 2>(p, s, stream_);
+}
+
+// The pass over the rows' own columns; p from attention_params, with what a prefix pass left if any.
+int own_pass(AttnParams p, const specdec_tree_attention_args* a, size_t room, cudaStream_t stream) {
+  if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
+  const specdec_kv_view& c = a->cache;
+  const int es = elem_size(c.dtype);
+  AttnShape s = attn_shape(es, a->T, p.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols);
+  // no more groups than the longest rows could give work to
+  const long long tiles = static_cast<long long>(a->B) * c.heads * ((c.cap_cols - 1) / s.tile + 1 + s.open);
+  s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
+  s.grid = s.groups * s.MT;
+  if (room < attn_workspace(s, c.head_dim).bytes) return SPECDEC_ERR_INVALID_ARG;
+  if (s.grid > static_cast<int>(kTicketBytes / 4)) return SPECDEC_ERR_UNSUPPORTED;
+  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kCols + 16) >= (1LL << 31))
+    return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
+  set_shape(p, s, a->workspace);
+  return launch_attention<false>(p, s, es, c.rows, stream);
+}
+
+}  // namespace
+}  // namespace specdec
+
+extern "C" size_t specdec_tree_attention_workspace(int dtype, int B, int T, int heads_q,
+                                                   int heads_kv, int head_dim) {
+  using namespace specdec;
+  if (!attn_sizes_ok(dtype, B, T, heads_q, heads_kv, head_dim)) return 0;
+  size_t most = 0;  // of the kernels that the lengths may decide for
+  for (const long long columns : {0LL, kFewColumns + 1}) {
+    const AttnShape s = attn_shape(elem_size(dtype), T, heads_q / heads_kv, head_dim, columns);
+    most = std::max(most, attn_workspace(s, head_dim).bytes);
+  }
+  return most;
+}
+
+extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void* stream) {
+  using namespace specdec;
+  if (!a) return SPECDEC_ERR_INVALID_ARG;
+  const int rc = check_attention(a);
+  if (rc || a->B == 0) return rc;
+  return own_pass(attention_params(a), a, a->workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t specdec_prefix_attention_workspace(int dtype, int B, int T, int heads_q, int heads_kv,
+                                                     int head_dim, int P) {
+  using namespace specdec;
+  if (!attn_sizes_ok(dtype, B, T, heads_q, heads_kv, head_dim) || P < 0 || P > kAttnMaxPrefixes) return 0;
+  return prefix_workspace(elem_size(dtype), B, T, heads_q, heads_q / heads_kv, head_dim).bytes;
+}
+
+extern "C" int specdec_prefix_attention(const specdec_prefix_attention_args* args, void* stream) {
+  using namespace specdec;
+  if (!args || args->P < 0) return SPECDEC_ERR_INVALID_ARG;
+  if (args->P > kAttnMaxPrefixes) return SPECDEC_ERR_UNSUPPORTED;
+  const specdec_tree_attention_args* a = &args->own;
+  const int rc = check_attention(a);
+  if (rc || a->B == 0) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AttnParams own = attention_params(a);
+  if (args->P == 0) return own_pass(own, a, a->workspace_bytes, s);
+  const specdec_kv_view &c = a->cache, &f = args->prefix;
+  const int st = check_view(f, elem_size(c.dtype));
+  if (st) return st;
+  if (f.dtype != c.dtype || f.heads != c.heads || f.head_dim != c.head_dim || a->layer >= f.layers ||
+      !(f.rows >= args->P || (f.rows == 1 && args->prefix_first)))
+    return SPECDEC_ERR_INVALID_ARG;
+  auto off = [](const void* x) { return reinterpret_cast<uintptr_t>(x) % 4 != 0; };
+  if (!args->prefix_len || !args->group_start || off(args->prefix_len) || off(args->group_start) || off(args->prefix_first))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
+  const int es = elem_size(c.dtype);
+  const PrefixWorkspace w = prefix_workspace(es, a->B, a->T, a->heads_q, own.G, c.head_dim);
+  if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(a->workspace);
+  own.prior = reinterpret_cast<int32_t*>(ws + w.state);
+  own.prior_ml = reinterpret_cast<float2*>(ws + w.ml);
+  own.prior_o = reinterpret_cast<float*>(ws + w.o);
+  AttnParams p = own;
+  p.cache = to_bytes(f);
+  p.cache.base += a->layer * p.cache.sl;
+  p.cap = f.cap_cols;
+  p.one_row = f.rows == 1 ? 1 : 0;
+  p.prefix_len = args->prefix_len;
+  p.prefix_first = args->prefix_first;
+  p.group_start = args->group_start;
+  p.P = args->P;
+  const long long R = static_cast<long long>(a->B) * a->T * own.G;
+  p.two = R > 128 ? 1 : 0;
+  AttnShape shape = prefix_shape(es, R, c.head_dim, static_cast<long long>(args->P) * c.heads * f.cap_cols);
+  // (a group's last unit may be nearly empty, so there are at most P more than full ones)
+  const long long units = ((R - 1) / shape.M + 1 + args->P) * c.heads;
+  if (units * (f.cap_cols / kCols + 16) >= (1LL << 31)) return SPECDEC_ERR_UNSUPPORTED;
+  const long long tiles = units * ((f.cap_cols - 1) / shape.tile + 1 + shape.open);
+  shape.groups = static_cast<int>(std::min<long long>(shape.groups, std::max<long long>(1, tiles / shape.min_tiles)));
+  shape.grid = shape.groups;
+  if (shape.grid > static_cast<int>(kTicketBytes / 4)) return SPECDEC_ERR_UNSUPPORTED;
+  set_shape(p, shape, a->workspace);
+  const int rp = launch_attention<true>(p, shape, es, f.rows, s);
+  if (rp) return rp;
+  return own_pass(own, a, a->workspace_bytes, s);
 }

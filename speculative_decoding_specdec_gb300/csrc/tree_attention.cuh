@@ -15,6 +15,11 @@
 // workspace and merged in share order, so that results do not depend on which CTA came last: by the
 // CTA that takes the unit's last ticket, or (tensor-core kernel, whose parts are larger) by a launch
 // of its own.  A share has at most two cut units (its first and last).
+//
+// A shared prefix.  Rows that share a prefix attend it in a pass of its own, before the pass over their
+// own columns, by the same kernels (kPrefix): a unit is then one K/V head of one prefix and up to M of
+// the query rows of all batch rows of its group, which see all its columns.  That pass leaves (m, l, o)
+// of every query row, and the pass over the rows' own columns merges them where it writes its results.
 #pragma once
 
 #include "tree.cuh"
@@ -22,6 +27,7 @@
 namespace specdec {
 
 constexpr int kAttnMaxRows = 1024;
+constexpr int kAttnMaxPrefixes = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
@@ -38,6 +44,14 @@ struct AttnParams {
   int4* cuts;        // [groups], tensor-core kernel: the units that borders cut
   float scale_log2;  // scale * log2(e)
   int B, T, Hq, H, G, hd, cap, one_row, MT, groups, min_tiles, open, g_shift;  // g_shift: log2 G, or -1
+  // A shared prefix (the prefix pass has its cache as `cache`): the rows' state (1: what the prefix pass
+  // left is to be merged; 0: there is no prefix; -1: an error), nullptr if there is none at all, and what
+  // it left, by (row, node, query head).
+  int32_t* prior;
+  float2* prior_ml;
+  float* prior_o;
+  const int32_t *prefix_len, *prefix_first, *group_start;
+  int P, M, two;  // prefixes; query rows of a unit; whether some group may have more than 128
 };
 
 // One batch row's columns.
@@ -75,21 +89,71 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b, int* err
 }
 
 // The plan in shared memory: tiles of the rows before row b, per K/V head, and the rows.
+// (a prefix pass: of the prefixes, with their first query row (b T + t) G + g and number of query rows)
 struct AttnPlan {
-  int *pre, *first, *old;  // [B + 1], [B], [B]
+  int *pre, *first, *old, *row0, *rows;  // [B + 1], [B], [B]; prefix pass: [P + 1] and [P]
 };
 __host__ __device__ constexpr int attn_plan_bytes(int B) { return (3 * B + 1) * 4; }
-__device__ __forceinline__ AttnPlan attn_plan_at(void* smem, int B) {
+__host__ __device__ constexpr int prefix_plan_bytes(int P) { return (5 * P + 1) * 4; }
+static_assert(prefix_plan_bytes(kAttnMaxPrefixes) <= attn_plan_bytes(kAttnMaxRows), "one room for either plan");
+__device__ __forceinline__ AttnPlan attn_plan_at(void* smem, int n) {
   int* p = static_cast<int*>(smem);
-  return AttnPlan{p, p + B + 1, p + 2 * B + 1};
+  return AttnPlan{p, p + n + 1, p + 2 * n + 1, p + 3 * n + 1, p + 4 * n + 1};
 }
 
 // A unit counts `p.open` tiles more than it has, for what a CTA spends on opening and closing it,
 // so that shares with many short units take no longer than others.
 // Built by warp 0 of every CTA (the caller synchronises); CTA 0 records errors.
+template <bool kPrefix = false>
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, const AttnPlan& plan) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
+  if constexpr (kPrefix) {
+    // rows of no group, or of one of a prefix without columns, are 0; where the groups' bounds are not
+    // ascending within the batch nothing is known of any row
+    bool bad = false;
+    for (int i = lane; i < p.P; i += 32) {
+      const int b0 = p.group_start[i], b1 = p.group_start[i + 1];
+      bad |= b0 < 0 || b1 < b0 || b1 > p.B;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (blockIdx.x == 0) {
+      for (int b = lane; b < p.B; b += 32) p.prior[b] = bad ? -1 : 0;
+      __syncwarp();
+      if (bad && lane == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
+    }
+    for (int i0 = 0; i0 < p.P; i0 += 32) {
+      const int i = i0 + lane;
+      int tiles = 0;
+      if (i < p.P) {
+        const int b0 = p.group_start[i], b1 = p.group_start[i + 1], len = p.prefix_len[i];
+        const int first = p.prefix_first ? p.prefix_first[i] : 0;
+        const int err = bad ? 0 : len < 0 || first < 0 ? SPECDEC_ERR_INPUT_RANGE
+                                : len > p.cap || first > p.cap - len ? SPECDEC_ERR_CAPACITY : 0;
+        const bool live = !bad && !err && len > 0 && b1 > b0;
+        const int rows = live ? (b1 - b0) * p.T * p.G : 0;
+        tiles = live ? ((rows + p.M - 1) / p.M) * ((len + tile - 1) / tile + p.open) : 0;
+        plan.first[i] = first;
+        plan.old[i] = len;
+        plan.row0[i] = live ? b0 * p.T * p.G : 0;
+        plan.rows[i] = rows;
+        if (blockIdx.x == 0 && (err || live)) {
+          if (err) set_status(p.status, err);
+          for (int b = b0; b < b1; ++b) p.prior[b] = err ? -1 : 1;
+        }
+      }
+      int inc = tiles;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, k);
+        if (lane >= k) inc += o;
+      }
+      if (i < p.P) plan.pre[i] = carry + inc - tiles;
+      carry += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) plan.pre[p.P] = carry;
+    return;
+  }
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
     int tiles = 0, first = 0, old = 0;
@@ -127,9 +191,10 @@ struct AttnShares {
     return x < more ? x / (base + 1) : rem + (x - more) / base;
   }
 };
+template <bool kPrefix = false>
 __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const AttnPlan& plan) {
   AttnShares s;
-  s.total = plan.pre[p.B] * p.H;
+  s.total = plan.pre[kPrefix ? p.P : p.B] * p.H;
   const int most = s.total / p.min_tiles;
   s.groups = most < 1 ? 1 : min(most, p.groups);
   s.base = s.total / s.groups;
@@ -140,14 +205,16 @@ __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const Att
 // A contiguous run of tiles of one unit inside a share (it may have none, if the share ends in what
 // the unit counts for being opened).
 struct AttnSegment {
-  int b, h, tile0, tile1, tiles;  // unit, its tiles [tile0, tile1) of `tiles`
+  int b, h, tile0, tile1, tiles;  // unit (its cache row), its tiles [tile0, tile1) of `tiles`
   int unit0;                      // place of the unit's first tile in the sequence
   int next;                       // place behind the segment
   int first, old, cols;           // its columns: AttnRow
+  int row0, rows;                 // prefix pass: its first query row, and how many it has
 };
+template <bool kPrefix = false>
 __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnPlan& plan,
                                                     int x, int end) {
-  int lo = 0, hi = p.B - 1;  // the last row with pre * H <= x: it has tiles
+  int lo = 0, hi = (kPrefix ? p.P : p.B) - 1;  // the last row with pre * H <= x: it has tiles
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (plan.pre[mid] * p.H <= x) lo = mid;
@@ -155,9 +222,20 @@ __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const A
   }
   AttnSegment s;
   s.b = lo;
-  const int span = plan.pre[lo + 1] - plan.pre[lo], rem = x - plan.pre[lo] * p.H;
-  s.h = rem / span;
-  const int at = rem - s.h * span;
+  int span = plan.pre[lo + 1] - plan.pre[lo];
+  const int rem = x - plan.pre[lo] * p.H;
+  if constexpr (kPrefix) {  // a head's units are neighbours: they use the same columns
+    const int units = (plan.rows[lo] + p.M - 1) / p.M;
+    span /= units;
+    const int unit = rem / span;
+    s.h = unit / units;
+    const int k = unit - s.h * units;
+    s.row0 = plan.row0[lo] + k * p.M;
+    s.rows = min(p.M, plan.rows[lo] - k * p.M);
+  } else {
+    s.h = rem / span;
+  }
+  const int at = kPrefix ? rem % span : rem - s.h * span;
   s.next = min(end, x - at + span);
   s.tiles = span - p.open;
   s.tile0 = max(0, at - p.open);
@@ -165,15 +243,16 @@ __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const A
   s.unit0 = x - at + p.open;
   s.first = plan.first[lo];
   s.old = plan.old[lo];
-  s.cols = s.old + p.T;
+  s.cols = s.old + (kPrefix ? 0 : p.T);
   return s;
 }
 
 // The next segment with tiles at or behind x; false at the share's end.
+template <bool kPrefix = false>
 __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& plan, int x, int end,
                                           AttnSegment& s) {
   while (x < end) {
-    s = attn_segment(p, plan, x, end);
+    s = attn_segment<kPrefix>(p, plan, x, end);
     if (s.tile1 > s.tile0) return true;
     x = s.next;
   }
@@ -257,12 +336,37 @@ inline __device__ __noinline__ void attn_add_not_finite(unsigned long long nodes
   }
 }
 
+// Query row r of a unit: its batch row, node and query head.  (Prefix pass: rows of a unit are counted
+// through its group's batch rows.)
+struct AttnQuery {
+  int b, t, h;
+};
+template <bool kPrefix>
+__device__ __forceinline__ AttnQuery attn_query(const AttnParams& p, const AttnSegment& s, int r) {
+  const int row = kPrefix ? s.row0 + r : r;
+  const int node = p.g_shift >= 0 ? row >> p.g_shift : row / p.G, h = s.h * p.G + row - node * p.G;
+  if constexpr (!kPrefix) return AttnQuery{s.b, node, h};
+  const int b = node / p.T;
+  return AttnQuery{b, node - b * p.T, h};
+}
+// Where the prefix pass leaves (m, l) and o / hd of a query row.
+__device__ __forceinline__ long long attn_prior_at(const AttnParams& p, int b, int t, int h) {
+  return (static_cast<long long>(b) * p.T + t) * p.Hq + h;
+}
+// Merging two parts of a row: the factors of the first's and the second's sums, and (m, l) of both.
+__device__ __forceinline__ float2 attn_join(float m0, float l0, float2 part, float& f0, float& f1) {
+  const float m = fmaxf(m0, part.x), off = m == -INFINITY ? 0.f : m;
+  f0 = exp2f(m0 - off);
+  f1 = exp2f(part.x - off);
+  return make_float2(m, l0 * f0 + part.y * f1);
+}
+
 // The tensor-core kernel (tree_attention_tc.cu): rows per M-tile and M-tiles for R query rows per
 // K/V head, and its launch (rows: of the cache).
 void attn_tc_shape(int R, int* M, int* MT);
-int launch_attn_tc(const AttnParams& p, int rows, int grid, cudaStream_t stream);
+int launch_attn_tc(const AttnParams& p, int rows, int grid, bool prefix, cudaStream_t stream);
 // The kernel for few rows (tree_attention_mma.cu).
 void attn_mma_shape(int R, int hd, int* M, int* MT, int* tile, int* per_sm);
-int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, cudaStream_t stream);
+int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, bool prefix, cudaStream_t stream);
 
 }  // namespace specdec

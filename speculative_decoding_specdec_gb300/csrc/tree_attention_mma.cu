@@ -74,8 +74,8 @@ struct Cursor {
   bool more;  // not behind the last
 };
 
-// NT: groups of 8 query rows.
-template <int HD, int NT>
+// NT: groups of 8 query rows.  kPrefix: a unit's rows are those of a group, over its prefix.
+template <int HD, int NT, bool kPrefix>
 __global__ void __launch_bounds__(kThreads)
 attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   using S = Smem<HD, NT>;
@@ -86,19 +86,18 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   __shared__ unsigned long long s_anc[kMaxTree], s_poison[kWarps];
   __shared__ float2 s_ml[kWarps][kRows];
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
-  const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, p.B);
+  const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, kPrefix ? p.P : p.B);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, qd = lane & 3;
-  if (warp == 0) attn_plan(p, kTileCols, plan);
+  if (warp == 0) attn_plan<kPrefix>(p, kTileCols, plan);
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
     fence_mbar_init();
   }
   __syncthreads();
-  const AttnShares sh = attn_shares(p, plan);
+  const AttnShares sh = attn_shares<kPrefix>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   if (sh.total == 0 || g >= sh.groups) return;
   const int x1 = sh.start(g + 1);
-  const int nrows = min(kRows, p.T * p.G - mt * kRows);
   const float scale = fmaxf(fabsf(p.scale_log2), 1.2e-38f);  // hidden scores stay -infinity
   const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
   char* mem = smem + warp * S::kWarp;
@@ -124,12 +123,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   };
   auto advance = [&](Cursor& c) {
     if (++c.tile >= c.seg.tile1) {
-      c.more = attn_next(p, plan, c.seg.next, x1, c.seg);
+      c.more = attn_next<kPrefix>(p, plan, c.seg.next, x1, c.seg);
       c.tile = c.seg.tile0;
     }
   };
   Cursor ahead;
-  ahead.more = attn_next(p, plan, sh.start(g), x1, ahead.seg);
+  ahead.more = attn_next<kPrefix>(p, plan, sh.start(g), x1, ahead.seg);
   ahead.tile = ahead.seg.tile0;
   int loaded = 0;  // tiles asked for so far
   for (; loaded < kStages && ahead.more; ++loaded) {
@@ -139,14 +138,15 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   int used = 0, row_b = -1;
   bool ok = true;
   AttnSegment seg;
-  for (int x = sh.start(g); attn_next(p, plan, x, x1, seg); x = seg.next) {
-    if (seg.b != row_b) {
+  for (int x = sh.start(g); attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
+    const int nrows = kPrefix ? seg.rows : min(kRows, p.T * p.G - mt * kRows);
+    if (kPrefix ? row_b < 0 : seg.b != row_b) {
       row_b = seg.b;
       __syncthreads();
-      if (p.parents && tid < p.T) s_par[tid] = p.parents[seg.b * p.T + tid];
+      if (!kPrefix && p.parents && tid < p.T) s_par[tid] = p.parents[seg.b * p.T + tid];
       if (tid == 0) s_bad = 0;
       __syncthreads();
-      if (tid < p.T) {
+      if (!kPrefix && tid < p.T) {
         bool bad = false;
         s_anc[tid] = tree_ancestors(p.parents ? s_par : nullptr, tid, bad);
         if (bad) {
@@ -162,9 +162,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     unsigned long long anc[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + gr, rr = mt * kRows + r;
-      const int t = r < nrows ? rr / p.G : 0, h = seg.h * p.G + (r < nrows ? rr % p.G : 0);
-      const char* src = p.q + seg.b * p.qr + t * p.qt + static_cast<long long>(h) * HD * 2 + qd * 4;
+      const int r = 8 * n + gr;
+      const AttnQuery at = attn_query<kPrefix>(p, seg, r < nrows ? mt * kRows + r : 0);
+      const char* src = p.q + at.b * p.qr + at.t * p.qt + static_cast<long long>(at.h) * HD * 2 + qd * 4;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -173,7 +173,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int ro = 8 * n + 2 * qd + i;
-        anc[n][i] = ro < nrows ? s_anc[(mt * kRows + ro) / p.G] : 0ull;
+        anc[n][i] = !kPrefix && ro < nrows ? s_anc[(mt * kRows + ro) / p.G] : 0ull;
       }
     }
     float o[NT][kSteps][4];
@@ -222,7 +222,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int node = base + gr + (k >> 1) * 8;
-              if (node >= 0 && !(node < p.T && (anc[n][k & 1] >> node & 1))) z[n][k] = -INFINITY;
+              if (node >= 0 && (kPrefix || !(node < p.T && (anc[n][k & 1] >> node & 1)))) z[n][k] = -INFINITY;
             }
           const int c = lane & 15, node = base + c;  // two lanes look after a column
           bool bad = false, drop = false;
@@ -231,7 +231,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
             return reinterpret_cast<uint4*>(vm + (ch >> 3) * kCols * 128 + c * 128 + (((ch & 7) ^ (c & 7)) << 4));
           };
           if (node >= 0) {
-            drop = node >= p.T || s_anc[node] == 0;
+            drop = kPrefix || node >= p.T || s_anc[node] == 0;
             if (!drop)
               for (int ch = ch0; ch < ch1; ++ch) bad |= inf_or_nan(*at(ch));
           }
@@ -330,10 +330,10 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     // kPer threads per row: every kPer-th group of 4 values from d0
     constexpr int kPer = kThreads / kRows, kVecs = HD / 4 / kPer;
     const int r = tid / kPer, d0 = tid % kPer * 4;
-    const int rr = mt * kRows + r;
     const bool mine = r < nrows && !s_bad;
-    const int t = mine ? rr / p.G : 0, h = seg.h * p.G + (mine ? rr % p.G : 0);
-    const bool live = mine && s_anc[t] != 0;
+    const AttnQuery row = attn_query<kPrefix>(p, seg, mine ? mt * kRows + r : 0);
+    const int t = row.t, h = row.h;
+    const bool live = mine && (kPrefix || s_anc[t] != 0);
     float mm = -INFINITY, ll = 0.f;
     float4 acc[kVecs];
 #pragma unroll
@@ -400,6 +400,24 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       }
     }
     if (!mine) continue;
+    if constexpr (kPrefix) {
+      const long long at = attn_prior_at(p, row.b, t, h);
+      if (d0 == 0) p.prior_ml[at] = make_float2(mm, ll);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+        *reinterpret_cast<float4*>(p.prior_o + at * HD + d0 + j * kPer * 4) = acc[j];
+      continue;
+    }
+    if (p.prior) {
+      const int state = p.prior[row.b];
+      if (state < 0) continue;
+      if (state > 0 && live) {
+        const long long at = attn_prior_at(p, row.b, t, h);
+        add(__ldcg(p.prior_ml + at), [&](int j) {
+          return __ldcg(reinterpret_cast<const float4*>(p.prior_o + at * HD + d0 + j * kPer * 4));
+        });
+      }
+    }
     const float inv = 1.f / ll;
     char* y = p.out + seg.b * p.outr + t * p.outt + static_cast<long long>(h) * HD * 2;
 #pragma unroll
@@ -420,14 +438,14 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   }
 }
 
-template <int HD, int NT>
+template <int HD, int NT, bool kPrefix>
 int launch_mma(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {
-  auto kernel = attn_mma_kernel<HD, NT>;
+  auto kernel = attn_mma_kernel<HD, NT, kPrefix>;
   constexpr int smem = Smem<HD, NT>::bytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              smem + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<grid, kThreads, smem + attn_plan_bytes(p.B), stream>>>(p, map);
+  kernel<<<grid, kThreads, smem + (kPrefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)), stream>>>(p, map);
   return map_cuda_error(cudaGetLastError());
 }
 
@@ -440,12 +458,17 @@ void attn_mma_shape(int R, int hd, int* M, int* MT, int* tile, int* per_sm) {
   *per_sm = hd == 64 ? 4 : 2;  // by shared memory: one CTA opens or merges while another streams
 }
 
-int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, cudaStream_t stream) {
+template <bool kPrefix>
+int launch_mma_of(const AttnParams& p, int M, const CUtensorMap& map, int grid, cudaStream_t stream) {
+  if (M == 8)
+    return p.hd == 64 ? launch_mma<64, 1, kPrefix>(p, map, grid, stream) : launch_mma<128, 1, kPrefix>(p, map, grid, stream);
+  return p.hd == 64 ? launch_mma<64, 2, kPrefix>(p, map, grid, stream) : launch_mma<128, 2, kPrefix>(p, map, grid, stream);
+}
+
+int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, bool prefix, cudaStream_t stream) {
   CUtensorMap map;
   if (!kv_tensor_map(&map, p.cache, p.hd, p.cap, p.H, rows, kCols)) return SPECDEC_ERR_UNSUPPORTED;
-  if (M == 8)
-    return p.hd == 64 ? launch_mma<64, 1>(p, map, grid, stream) : launch_mma<128, 1>(p, map, grid, stream);
-  return p.hd == 64 ? launch_mma<64, 2>(p, map, grid, stream) : launch_mma<128, 2>(p, map, grid, stream);
+  return prefix ? launch_mma_of<true>(p, M, map, grid, stream) : launch_mma_of<false>(p, M, map, grid, stream);
 }
 
 }  // namespace specdec

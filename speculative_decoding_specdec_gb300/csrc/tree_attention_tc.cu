@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t visible32(unsigned long long anc, int base) 
   return static_cast<uint32_t>(anc << -base) | ((1u << -base) - 1u);
 }
 
-template <int HD>
+template <int HD, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   using S = Smem<HD>;
@@ -108,12 +108,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   __shared__ unsigned long long s_anc[kMaxTree], s_poison;
   __shared__ float2 s_ml[kRows];
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
-  const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, p.B);
+  const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, kPrefix ? p.P : p.B);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
-  const int nrows = min(2 * kRows, p.T * p.G - mt * 2 * kRows);  // query rows of this pair
-  const bool two = nrows > kRows;  // A and B are different rows, else alternate tiles
-  if (warp == 0) attn_plan(p, kCols, plan);
+  int nrows = min(2 * kRows, p.T * p.G - mt * 2 * kRows);  // query rows of this pair (prefix pass: of the unit)
+  const bool two = kPrefix ? p.two != 0 : nrows > kRows;   // A and B are different rows, else alternate tiles
+  if (warp == 0) attn_plan<kPrefix>(p, kCols, plan);
   if (warp == 9) tmem_alloc(&s_tmem, 512);
   if (tid == 32) {
     for (int i = 0; i < kMaxKStages; ++i) {
@@ -140,7 +140,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   tmem_fence_after();
   pdl_launch_dependents();  // the merge of cut units may be set up
   const uint32_t tmem = s_tmem;
-  const AttnShares sh = attn_shares(p, plan);
+  const AttnShares sh = attn_shares<kPrefix>(p, plan);
   const bool work = sh.total > 0 && g < sh.groups;
   const int x0 = work ? sh.start(g) : 0, x1 = work ? sh.start(g + 1) : 0;
   const int nk = two ? kStages : kMaxKStages;
@@ -157,7 +157,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       uint64_t *full = is_v ? bar.v_full : bar.k_full, *empty = is_v ? bar.v_empty : bar.k_empty;
       int n = 0;  // tiles so far
       AttnSegment seg;
-      for (int x = x0; ok && attn_next(p, plan, x, x1, seg); x = seg.next) {
+      for (int x = x0; ok && attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
         const int crow = p.one_row ? 0 : seg.b;
         for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
           const int st = n % stages, col = seg.first + tile * kCols;
@@ -193,7 +193,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
                    v_desc = mma_desc(sm + S::v, kCols * 128, 1024);
     int kv = 0, seg_no = 0, done[2] = {0, 0};  // tiles, segments, jobs of A and B so far
     AttnSegment seg;
-    for (int x = x0; ok && attn_next(p, plan, x, x1, seg); x = seg.next, ++seg_no) {
+    for (int x = x0; ok && attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next, ++seg_no) {
       const int n = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0), jobs = pair ? 2 * n : n;
       const int clean = seg.old / kCols - seg.tile0;  // the first tile that needs care
       // Job i is tile i / 2 for A or B (pair), or tile i for one of them.
@@ -234,7 +234,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           char* vt = smem + S::v + st * S::kTile;
           for (int c = max(0, seg.old - col0) + lane; c < steps * 16; c += 32) {
             const int node = col0 + c - seg.old;
-            const bool drop = node >= p.T || s_anc[node] == 0;
+            const bool drop = kPrefix || node >= p.T || s_anc[node] == 0;
             auto at = [&](int k) { return reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)); };
             if (!drop) {
               bool bad = false;
@@ -284,9 +284,9 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     const int a = warp >> 2, r = tid & (kRows - 1);       // accumulator, row of it
     const int pr = two ? a * kRows + r : r;               // row of the pair
     const int rr = mt * 2 * kRows + pr;                   // query row of the unit
-    const bool mine = pr < nrows;
-    const bool idle = (two ? a * kRows : 0) + (warp & 3) * 32 >= nrows;  // a warp without rows
-    const int t_of = mine ? rr / p.G : 0;
+    bool mine = pr < nrows;
+    bool idle = (two ? a * kRows : 0) + (warp & 3) * 32 >= nrows;  // a warp without rows
+    const int t_of = !kPrefix && mine ? rr / p.G : 0;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
     const uint32_t t_s = tmem + lane_base + a * kCols, t_o = tmem + lane_base + (2 + a) * kCols;
     // a scale of zero as the smallest one: hidden scores are -infinity and have to stay so
@@ -298,21 +298,25 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     constexpr int kChunks = HD / 8, kPer = 256 / kChunks, kLoads = 2 * kRows / kPer;
     const int qc = tid % kChunks, q0 = tid / kChunks, nq = two ? kLoads : kLoads / 2;
     auto ask = [&](const AttnSegment& sg) {
-      const char* base = p.q + sg.b * p.qr + static_cast<long long>(sg.h) * p.G * HD * 2 + qc * 16;
+      const char* base = p.q + (kPrefix ? 0 : sg.b) * p.qr + static_cast<long long>(sg.h) * p.G * HD * 2 + qc * 16;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int q = q0 + k * kPer, qq = mt * 2 * kRows + q;
-        if (k < nq) {
+        if (kPrefix && k < nq) {
+          const AttnQuery at = attn_query<true>(p, sg, q < sg.rows ? q : 0);
+          cp_async16(smem + S::q + (q / kRows) * S::kQ + swizzled(q % kRows, qc, kRows),
+                     p.q + at.b * p.qr + at.t * p.qt + at.h * (HD * 2) + qc * 16, q < sg.rows);
+        } else if (k < nq) {
           const int t = p.g_shift >= 0 ? qq >> p.g_shift : qq / p.G;
           cp_async16(smem + S::q + (q / kRows) * S::kQ + swizzled(q % kRows, qc, kRows),
                      q < nrows ? base + t * p.qt + (qq - t * p.G) * (HD * 2) : p.q, q < nrows);
         }
       }
-      if (p.parents && tid < p.T) s_par[tid] = __ldg(p.parents + sg.b * p.T + tid);
+      if (!kPrefix && p.parents && tid < p.T) s_par[tid] = __ldg(p.parents + sg.b * p.T + tid);
     };
     // Q has arrived: ancestors, and the products may begin
     auto open = [&] {
-      if (tid < p.T) {
+      if (!kPrefix && tid < p.T) {
         bool bad = false;
         s_anc[tid] = tree_ancestors(p.parents ? s_par : nullptr, tid, bad);
         if (bad) {
@@ -331,7 +335,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       arrive(&bar.q_full);
     };
     AttnSegment seg;
-    bool more = attn_next(p, plan, x0, x1, seg);
+    bool more = attn_next<kPrefix>(p, plan, x0, x1, seg);
     if (more) {
       ask(seg);
       if (tid == 0) s_bad = 0;
@@ -344,13 +348,19 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     if (mt == 0 && tid == 0) {
       int4 cut = make_int4(0, 0, 0, 0);
       if (more && !s_bad && x0 > seg.unit0 && sh.owner(seg.unit0) == g - 1)
-        cut = make_int4(seg.b, seg.h, sh.start(g - 1) >= seg.unit0 ? 0 : 1,
+        cut = make_int4(kPrefix ? seg.row0 : seg.b, seg.h,
+                        (sh.start(g - 1) >= seg.unit0 ? 0 : 1) | (kPrefix ? seg.rows << 1 : 0),
                         sh.owner(seg.unit0 + seg.tiles - 1) - g + 2);
       p.cuts[g] = cut;
     }
     for (; more; ++seg_no) {
       const int n = seg.tile1 - seg.tile0;
-      const unsigned long long anc = mine ? s_anc[t_of] : 0ull;
+      if constexpr (kPrefix) {
+        nrows = seg.rows;
+        mine = pr < nrows;
+        idle = (two ? a * kRows : 0) + (warp & 3) * 32 >= nrows;
+      }
+      const unsigned long long anc = mine ? (kPrefix ? ~0ull : s_anc[t_of]) : 0ull;
       const int jobs = two ? n : (n - a + 1) >> 1;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < jobs; ++j, ++seen) {
@@ -376,7 +386,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
               tmem_wait_ld32(v);
               if (c < 3) tmem_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
               if (base + kCols > 0) {
-                const uint32_t vis = visible32(anc, base + c * 32);
+                const uint32_t vis = visible32(kPrefix ? 0ull : anc, base + c * 32);
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                   if (!(vis >> k & 1)) v[k] = __float_as_uint(-INFINITY);
@@ -437,13 +447,14 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       // opened, and its first products run, before this one is written out.
       const AttnSegment now = seg;
       if (!(ok = named_bar_all(1, 256, ok))) break;
-      more = attn_next(p, plan, seg.next, x1, seg);
+      more = attn_next<kPrefix>(p, plan, seg.next, x1, seg);
       if (more) ask(seg);
       if (jobs > 0) ok = warp_wait(&bar.o_done[a], ends++ & 1);
       ok = ok && warp_wait(&bar.v_clean, seg_no & 1);
       tmem_fence_after();
-      const unsigned long long poison = anc & s_poison;  // nodes it sees whose V is not finite somewhere
-      const bool write = mine && !s_bad;
+      const unsigned long long poison = kPrefix ? 0ull : anc & s_poison;  // nodes it sees whose V is not finite somewhere
+      const int state = !kPrefix && p.prior && mine ? p.prior[now.b] : 0;  // of a prefix pass
+      const bool write = mine && !s_bad && state >= 0;
       if (!(ok = named_bar_all(1, 256, ok))) break;  // all have read s_poison and s_bad
       if (tid == 0) s_bad = 0;
       if (tid == 0) s_poison = 0;
@@ -462,7 +473,32 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       const int slot = whole ? 0 : attn_slot(p, sh, g, mt, now.unit0);
       char* y = p.out + now.b * p.outr + t_of * p.outt +
                 static_cast<long long>(now.h * p.G + (mine ? rr % p.G : 0)) * HD * 2;
-      auto store_out = [&](int c, const float (&o)[32]) {  // (zeros for an unused node, whatever o is)
+      long long prior = 0;  // where this row's part of a prefix is or goes
+      float f_own = 1.f, f_prior = 0.f;
+      if (kPrefix && mine) {
+        const AttnQuery at = attn_query<kPrefix>(p, now, pr);
+        prior = attn_prior_at(p, at.b, at.t, at.h);
+      } else if (!kPrefix && state > 0) {
+        prior = attn_prior_at(p, now.b, t_of, now.h * p.G + rr % p.G);
+      }
+      auto store_out = [&](int c, float (&o)[32]) {  // (zeros for an unused node, whatever o is)
+        if constexpr (kPrefix) {
+          float4* to = reinterpret_cast<float4*>(p.prior_o + prior * HD + c * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          return;
+        }
+        if (state > 0) {
+          const float4* from = reinterpret_cast<const float4*>(p.prior_o + prior * HD + c * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 v = __ldcg(from + k);
+            o[4 * k] = o[4 * k] * f_own + v.x * f_prior;
+            o[4 * k + 1] = o[4 * k + 1] * f_own + v.y * f_prior;
+            o[4 * k + 2] = o[4 * k + 2] * f_own + v.z * f_prior;
+            o[4 * k + 3] = o[4 * k + 3] * f_own + v.w * f_prior;
+          }
+        }
         const float inv = 1.f / l;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -474,12 +510,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
                   : make_uint4(0, 0, 0, 0);
       };
       auto store_lse = [&](float mm, float ll) {
-        if (p.lse)
+        if (kPrefix) p.prior_ml[prior] = make_float2(mm, ll);
+        else if (p.lse)
           p.lse[(static_cast<long long>(now.b) * p.T + t_of) * p.Hq + now.h * p.G + rr % p.G] =
               anc ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
       };
       // one chunk of the row's merged sums goes to the output, or to the partial results
-      auto emit = [&](int c, const float (&o)[32]) {
+      auto emit = [&](int c, float (&o)[32]) {
         if (!write) return;
         if (whole) {
           store_out(c, o);
@@ -505,6 +542,11 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
           l = l * fa + b.y * fb;
           m = mn;
         }
+      }
+      if (!kPrefix && whole && state > 0) {
+        const float2 ml = attn_join(m, l, __ldcg(p.prior_ml + prior), f_own, f_prior);
+        m = ml.x;
+        l = ml.y;
       }
       if ((two || a == 0) && !idle)
 #pragma unroll 1
@@ -547,7 +589,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 // and needs no tickets, where the CTA that came last would add parts of 128 KB one after the other
 // behind the last share.  CTA = border and 32 rows; thread = row and 4 * kPer of its values.
 // Measured alone and cold (ncu), 75 borders of 512 rows: 14.7 us for 30 MB, the loads' latency.
-template <int HD>
+template <int HD, bool kPrefix>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   constexpr int kPer = HD / 32;  // float4 a thread holds
   constexpr int kBlock = 64;     // parts at a time
@@ -558,8 +600,8 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   pdl_wait();
   const int4 cut = __ldcg(p.cuts + g0 + 1);
   const int b = cut.x, qh = cut.y * p.G + rr - t * p.G, parts = cut.w;
-  if (parts < 2) return;
-  auto slot = [&](int i) { return 2ll * ((g0 + i) * p.MT + mt) + (i == 0 ? cut.z : 0); };
+  if (parts < 2 || (kPrefix && block * 32 >= cut.z >> 1)) return;
+  auto slot = [&](int i) { return 2ll * ((g0 + i) * p.MT + mt) + (i == 0 ? cut.z & 1 : 0); };
   // the parts in blocks: their rows' (m, l) into shared memory at once, then the sums
   const int d0 = warp * kPer;  // first float4
   bool live = true;
@@ -603,8 +645,41 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
       }
     }
   }
-  const float inv = 1.f / l;
+  if constexpr (kPrefix) {
+    if (pr >= cut.z >> 1) return;
+    AttnSegment s = {};
+    s.row0 = cut.x;
+    s.h = cut.y;
+    const AttnQuery row = attn_query<true>(p, s, pr);
+    const long long at = attn_prior_at(p, row.b, row.t, row.h);
+    if (warp == 0) p.prior_ml[at] = make_float2(m, l);
+    float4* to = reinterpret_cast<float4*>(p.prior_o + at * HD) + d0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) to[k] = o[k];
+    return;
+  }
   if (rr >= p.T * p.G) return;
+  if (p.prior) {
+    const int state = p.prior[b];
+    if (state < 0) return;
+    if (state > 0) {
+      const long long at = attn_prior_at(p, b, t, qh);
+      float f0, f1;
+      const float2 ml = attn_join(m, l, __ldcg(p.prior_ml + at), f0, f1);
+      m = ml.x;
+      l = ml.y;
+      const float4* from = reinterpret_cast<const float4*>(p.prior_o + at * HD) + d0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const float4 v = __ldcg(from + k);
+        o[k].x = o[k].x * f0 + v.x * f1;
+        o[k].y = o[k].y * f0 + v.y * f1;
+        o[k].z = o[k].z * f0 + v.z * f1;
+        o[k].w = o[k].w * f0 + v.w * f1;
+      }
+    }
+  }
+  const float inv = 1.f / l;
   char* y = p.out + b * p.outr + t * p.outt + static_cast<long long>(qh) * HD * 2 + d0 * 8;
 #pragma unroll
   for (int k = 0; k < kPer; ++k)
@@ -615,14 +690,14 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
         live ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int HD>
+template <int HD, bool kPrefix>
 int launch_tc(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {
-  auto kernel = attn_tc_kernel<HD>;
+  auto kernel = attn_tc_kernel<HD, kPrefix>;
   constexpr int smem = Smem<HD>::bytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              smem + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<grid, kThreads, smem + attn_plan_bytes(p.B), stream>>>(p, map);
+  kernel<<<grid, kThreads, smem + (kPrefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)), stream>>>(p, map);
   const cudaError_t e2 = cudaGetLastError();
   if (e2 != cudaSuccess || p.groups == 1) return map_cuda_error(e2);
   cudaLaunchConfig_t cfg = {};
@@ -634,7 +709,7 @@ int launch_tc(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return map_cuda_error(cudaLaunchKernelEx(&cfg, attn_merge_kernel<HD>, p));
+  return map_cuda_error(cudaLaunchKernelEx(&cfg, attn_merge_kernel<HD, kPrefix>, p));
 }
 
 }  // namespace
@@ -677,10 +752,12 @@ void attn_tc_shape(int R, int* M, int* MT) {
   *MT = (R + 2 * kRows - 1) / (2 * kRows);
 }
 
-int launch_attn_tc(const AttnParams& p, int rows, int grid, cudaStream_t stream) {
+int launch_attn_tc(const AttnParams& p, int rows, int grid, bool prefix, cudaStream_t stream) {
   CUtensorMap map;
   if (!kv_tensor_map(&map, p.cache, p.hd, p.cap, p.H, rows, kCols)) return SPECDEC_ERR_UNSUPPORTED;
-  return p.hd == 64 ? launch_tc<64>(p, map, grid, stream) : launch_tc<128>(p, map, grid, stream);
+  if (prefix)
+    return p.hd == 64 ? launch_tc<64, true>(p, map, grid, stream) : launch_tc<128, true>(p, map, grid, stream);
+  return p.hd == 64 ? launch_tc<64, false>(p, map, grid, stream) : launch_tc<128, false>(p, map, grid, stream);
 }
 
 }  // namespace specdec

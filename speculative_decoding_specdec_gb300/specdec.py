@@ -128,6 +128,12 @@ class TreeAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p)]
 
 
+class PrefixAttentionArgs(ctypes.Structure):
+    _fields_ = [("own", TreeAttentionArgs), ("prefix", KvView), ("P", ctypes.c_int),
+                ("prefix_len", ctypes.c_void_p), ("prefix_first", ctypes.c_void_p),
+                ("group_start", ctypes.c_void_p)]
+
+
 class TreeCommitArgs(ctypes.Structure):
     _fields_ = [("src", KvView), ("dst", KvView), ("B", ctypes.c_int), ("T", ctypes.c_int),
                 ("D", ctypes.c_int), ("width", ctypes.c_void_p), ("width_dst", ctypes.c_void_p),
@@ -189,6 +195,10 @@ lib.specdec_tree_attention.restype = _i
 lib.specdec_tree_attention.argtypes = [_vp, _vp]  # specdec_tree_attention_args
 lib.specdec_tree_attention_workspace.restype = _sz
 lib.specdec_tree_attention_workspace.argtypes = [_i, _i, _i, _i, _i, _i]
+lib.specdec_prefix_attention.restype = _i
+lib.specdec_prefix_attention.argtypes = [_vp, _vp]  # specdec_prefix_attention_args
+lib.specdec_prefix_attention_workspace.restype = _sz
+lib.specdec_prefix_attention_workspace.argtypes = [_i, _i, _i, _i, _i, _i, _i]
 lib.specdec_verify_tree_greedy.restype = _i
 lib.specdec_verify_tree_greedy.argtypes = [_vp, _i, _i, _i, _i, _ll, _vp, _vp, _i, _vp, _vp, _vp,
                                            _vp, _vp, _vp]
@@ -602,7 +612,9 @@ _KV = "Pqqqqiiiiii"
 _ROTARY = _KV + "iiiiiii" + "PPPP" + "qqqqqqqq" + "PPPPPPP"
 _PACK_ROTARY = struct.Struct("@" + _ROTARY)
 _PACK_NORM_ROTARY = struct.Struct("@" + _ROTARY + "PPiffP")
-_PACK_ATTENTION = struct.Struct("@" + _KV + "iiiif" + "PPP" + "qqqq" + "PPPPPPnP")
+_ATTENTION = _KV + "iiiif" + "PPP" + "qqqq" + "PPPPPPnP"
+_PACK_ATTENTION = struct.Struct("@" + _ATTENTION)
+_PACK_PREFIX = struct.Struct("@" + _ATTENTION + _KV + "iPPP")
 _PACK_SAMPLE = struct.Struct("@Piiiq" + "PPPPPPPP" + "qP")
 _PACK_COMMIT = struct.Struct("@" + _KV + _KV + "iii" + "PPPPPPPP")
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -747,15 +759,9 @@ def tree_attention_workspace_bytes(q, cache) -> int:
                                                     hd))
 
 
-def tree_attention(q, cache, layer, out, n_committed, width, parents, status, workspace,
-                   scale=None, lse=None, rows=None, first_col=None, stream=None):
-    """Attention of a verification pass: q [B, T, Hq, hd] (node 0 the pending token, the others the
-    drafted tree of ``parents`` [B, T], None for a chain) against every row's committed columns of
-    ``cache`` [L, 2, rows, H, cap, hd], layer ``layer``, and the nodes' own ancestors, into
-    ``out`` (and ``lse`` [B, T, Hq] float32).  ``scale`` defaults to hd ** -0.5.  ``workspace``: a
-    zero-filled uint8 CUDA tensor of tree_attention_workspace_bytes(q, cache), reused as is.
-    ``first_col`` (and ``rows``): tokens elsewhere than right-aligned at ``width``, as in a pool's
-    arena."""
+def _attention_fields(q, cache, layer, out, n_committed, width, parents, status, workspace, scale, lse,
+                      rows, first_col):
+    """The fields of specdec_tree_attention_args."""
     view = _kv(cache)
     dtype = cache.dtype
     shape = q.shape
@@ -775,16 +781,57 @@ def tree_attention(q, cache, layer, out, n_committed, width, parents, status, wo
     if (workspace.dtype is not torch.uint8 or not workspace.is_cuda
             or not workspace.is_contiguous()):
         raise ValueError("tree_attention: workspace must be a contiguous CUDA uint8 tensor")
-    args = _PACK_ATTENTION.pack(
+    return (
         *view, layer, B, T, Hq, hd ** -0.5 if scale is None else scale, qp, op, lp, qr, qt, outr,
         outt, np_, _ints_of_any(width, "width"), _ints(parents, (B, T), "parents"),
         _ints(rows, (B,), "rows"),
         _at_least(first_col, B if rows is None else n_committed.numel(), "first_col"),
         workspace.data_ptr(), workspace.numel(),
         _ints_of_any(_given(status, "status"), "status"))
-    rc = lib.specdec_tree_attention(args, _raw(stream))
+
+
+def tree_attention(q, cache, layer, out, n_committed, width, parents, status, workspace,
+                   scale=None, lse=None, rows=None, first_col=None, stream=None):
+    """Attention of a verification pass: q [B, T, Hq, hd] (node 0 the pending token, the others the
+    drafted tree of ``parents`` [B, T], None for a chain) against every row's committed columns of
+    ``cache`` [L, 2, rows, H, cap, hd], layer ``layer``, and the nodes' own ancestors, into
+    ``out`` (and ``lse`` [B, T, Hq] float32).  ``scale`` defaults to hd ** -0.5.  ``workspace``: a
+    zero-filled uint8 CUDA tensor of tree_attention_workspace_bytes(q, cache), reused as is.
+    ``first_col`` (and ``rows``): tokens elsewhere than right-aligned at ``width``, as in a pool's
+    arena."""
+    rc = lib.specdec_tree_attention(
+        _PACK_ATTENTION.pack(*_attention_fields(q, cache, layer, out, n_committed, width, parents, status,
+                                                workspace, scale, lse, rows, first_col)), _raw(stream))
     if rc:
         _check(rc, "specdec_tree_attention")
+
+
+def prefix_attention_workspace_bytes(q, cache, prefixes) -> int:
+    """Workspace bytes prefix_attention needs for this q [B, T, Hq, hd] over this cache and
+    ``prefixes`` prefixes, whatever the lengths (enough for tree_attention too)."""
+    B, T, Hq, hd = q.shape
+    return int(lib.specdec_prefix_attention_workspace(dtype_code(q.dtype), B, T, Hq, cache.shape[3],
+                                                      hd, int(prefixes)))
+
+
+def prefix_attention(q, cache, layer, out, n_committed, width, parents, status, workspace, prefix,
+                     prefix_len, group_start, prefix_first=None, scale=None, lse=None, rows=None,
+                     first_col=None, stream=None):
+    """As tree_attention, over a prefix that rows share as well: batch rows ``group_start[p]`` ..
+    ``group_start[p + 1]`` see ``prefix_len[p]`` columns of row p of ``prefix`` [L, 2, P, H, cap, hd]
+    (from ``prefix_first[p]`` on; with one row, all in it) before their own.  ``workspace``:
+    prefix_attention_workspace_bytes(q, cache, P)."""
+    fields = _attention_fields(q, cache, layer, out, n_committed, width, parents, status, workspace,
+                               scale, lse, rows, first_col)
+    P = prefix_len.shape[0]
+    one = (P,)
+    rc = lib.specdec_prefix_attention(
+        _PACK_PREFIX.pack(*fields, *_kv(prefix), P, _ints(prefix_len, one, "prefix_len"),
+                          _ints(prefix_first, one, "prefix_first"),
+                          _ints(_given(group_start, "group_start"), (P + 1,), "group_start")),
+        _raw(stream))
+    if rc:
+        _check(rc, "specdec_prefix_attention")
 
 
 def _scores(t, name):
