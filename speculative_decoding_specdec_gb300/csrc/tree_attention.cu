@@ -88,13 +88,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
     return reinterpret_cast<float*>(smem + R * hd * 4 + w * warp_bytes + kStages * 2 * kCols * pitch) + kCols * R;
   };
   const AttnPlan plan = attn_plan_at(smem + R * hd * 4 + warps * warp_bytes, kPrefix ? p.P : p.B);
-  if (warp == 0) attn_plan<kPrefix>(p, tile_cols, plan);
+  if (warp == 0) attn_plan<kPrefix ? kPrefixPass : kOwn>(p, tile_cols, plan);
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
     fence_mbar_init();
   }
   __syncthreads();
-  const AttnShares sh = attn_shares<kPrefix>(p, plan);
+  const AttnShares sh = attn_shares<kPrefix ? kPrefixPass : kOwn>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   if (sh.total == 0 || g >= sh.groups) return;
   const int x1 = sh.start(g + 1);
@@ -112,12 +112,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
   };
   auto advance = [&](Cursor& c) {
     if (++c.tile >= c.seg.tile1) {
-      c.more = attn_next<kPrefix>(p, plan, c.seg.next, x1, c.seg);
+      c.more = attn_next<kPrefix ? kPrefixPass : kOwn>(p, plan, c.seg.next, x1, c.seg);
       c.tile = c.seg.tile0;
     }
   };
   Cursor ahead;
-  ahead.more = attn_next<kPrefix>(p, plan, sh.start(g), x1, ahead.seg);
+  ahead.more = attn_next<kPrefix ? kPrefixPass : kOwn>(p, plan, sh.start(g), x1, ahead.seg);
   ahead.tile = ahead.seg.tile0;
   int loaded = 0, used = 0, row_b = -1;  // tiles asked for, tiles done
   for (; loaded < kStages && ahead.more; ++loaded) {
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
   }
   bool ok = true;
   AttnSegment seg;
-  for (int x = sh.start(g); attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
+  for (int x = sh.start(g); attn_next<kPrefix ? kPrefixPass : kOwn>(p, plan, x, x1, seg); x = seg.next) {
     __syncthreads();  // the segment before is done with Q and the tree
     const int nrows = kPrefix ? seg.rows : min(R, p.T * p.G - mt * R);  // query rows of this M-tile: (node, head) pairs
     const bool other = kPrefix ? row_b < 0 : seg.b != row_b;
@@ -389,15 +389,15 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
   float* s_q = reinterpret_cast<float*>(s_v + 2 * kTile * pitch);  // [M][hd], times scale_log2
   float4* s_p = reinterpret_cast<float4*>(s_q + M * hd) + warp * kTile;  // [kTile] x 4 rows
   const AttnPlan plan = attn_plan_at(reinterpret_cast<float4*>(s_q + M * hd) + RG * kTile, kPrefix ? p.P : p.B);
-  if (warp == 0) attn_plan<kPrefix>(p, kTile, plan);
+  if (warp == 0) attn_plan<kPrefix ? kPrefixPass : kOwn>(p, kTile, plan);
   __syncthreads();
-  const AttnShares sh = attn_shares<kPrefix>(p, plan);
+  const AttnShares sh = attn_shares<kPrefix ? kPrefixPass : kOwn>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   if (sh.total == 0 || g >= sh.groups) return;
   const int x1 = sh.start(g + 1);
   int row_b = -1;
   AttnSegment seg;
-  for (int x = sh.start(g); attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
+  for (int x = sh.start(g); attn_next<kPrefix ? kPrefixPass : kOwn>(p, plan, x, x1, seg); x = seg.next) {
     const int nrows = kPrefix ? seg.rows : min(M, p.T * p.G - mt * M);  // query rows of this M-tile: (node, head) pairs
     if (kPrefix ? row_b < 0 : seg.b != row_b) {  // a new batch row: its tree
       row_b = seg.b;
@@ -891,21 +891,38 @@ void set_shape(AttnParams& p, const AttnShape& s, void* workspace) {
   p.open = s.open;
 }
 
+// Whether a batch row's own query rows fill the tensor cores' tiles to three quarters and more, so that
+// its prefix is attended with its own columns in one pass.
+// (16384 rows in all per K/V head over 8192 columns and 512 a row over up to 1056 of its own, 32 rows
+// and 2 K/V heads: 138 us against 201 in two passes.)
+bool fills_tiles(const AttnShape& s, long long R) {
+  const long long room = R <= 128 ? 128 : (R + 255) / 256 * 256;
+  return s.kind == kTc && R * 4 >= room * 3;
+}
+
 // The pass over the rows' own columns; p from attention_params, with what a prefix pass left if any.
-int own_pass(AttnParams p, const specdec_tree_attention_args* a, size_t room, cudaStream_t stream) {
+// both: their prefixes' columns too.
+int own_pass(AttnParams p, const specdec_tree_attention_args* a, size_t room, cudaStream_t stream,
+             const specdec_kv_view* both = nullptr) {
   if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
   const specdec_kv_view& c = a->cache;
   const int es = elem_size(c.dtype);
   AttnShape s = attn_shape(es, a->T, p.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols);
   // no more groups than the longest rows could give work to
-  const long long tiles = static_cast<long long>(a->B) * c.heads * ((c.cap_cols - 1) / s.tile + 1 + s.open);
+  const long long columns = static_cast<long long>(c.cap_cols) + (both ? both->cap_cols + s.tile : 0);
+  const long long tiles = static_cast<long long>(a->B) * c.heads * ((columns - 1) / s.tile + 1 + s.open);
   s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
   s.grid = s.groups * s.MT;
   if (room < attn_workspace(s, c.head_dim).bytes) return SPECDEC_ERR_INVALID_ARG;
   if (s.grid > static_cast<int>(kTicketBytes / 4)) return SPECDEC_ERR_UNSUPPORTED;
-  if (static_cast<long long>(a->B) * c.heads * (c.cap_cols / kCols + 16) >= (1LL << 31))
+  if (static_cast<long long>(a->B) * c.heads * (columns / kCols + 16) >= (1LL << 31))
     return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   set_shape(p, s, a->workspace);
+  if (both) {
+    ByteView prefix = to_bytes(*both);
+    prefix.base += a->layer * prefix.sl;
+    return launch_attn_tc_both(p, c.rows, prefix, both->rows, s.grid, stream);
+  }
   return launch_attention<false>(p, s, es, c.rows, stream);
 }
 
@@ -962,6 +979,14 @@ extern "C" int specdec_prefix_attention(const specdec_prefix_attention_args* arg
   const int es = elem_size(c.dtype);
   const PrefixWorkspace w = prefix_workspace(es, a->B, a->T, a->heads_q, own.G, c.head_dim);
   if (a->workspace_bytes < w.bytes) return SPECDEC_ERR_INVALID_ARG;
+  own.prefix_len = args->prefix_len;
+  own.prefix_first = args->prefix_first;
+  own.group_start = args->group_start;
+  own.P = args->P;
+  own.prefix_cap = f.cap_cols;
+  own.prefix_one_row = f.rows == 1 ? 1 : 0;
+  const AttnShape alone = attn_shape(es, a->T, own.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols);
+  if (fills_tiles(alone, static_cast<long long>(a->T) * own.G)) return own_pass(own, a, a->workspace_bytes, s, &f);
   char* ws = static_cast<char*>(a->workspace);
   own.prior = reinterpret_cast<int32_t*>(ws + w.state);
   own.prior_ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -971,10 +996,6 @@ extern "C" int specdec_prefix_attention(const specdec_prefix_attention_args* arg
   p.cache.base += a->layer * p.cache.sl;
   p.cap = f.cap_cols;
   p.one_row = f.rows == 1 ? 1 : 0;
-  p.prefix_len = args->prefix_len;
-  p.prefix_first = args->prefix_first;
-  p.group_start = args->group_start;
-  p.P = args->P;
   const long long R = static_cast<long long>(a->B) * a->T * own.G;
   p.two = R > 128 ? 1 : 0;
   AttnShape shape = prefix_shape(es, R, c.head_dim, static_cast<long long>(args->P) * c.heads * f.cap_cols);

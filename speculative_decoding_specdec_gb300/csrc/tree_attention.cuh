@@ -20,6 +20,9 @@
 // own columns, by the same kernels (kPrefix): a unit is then one K/V head of one prefix and up to M of
 // the query rows of all batch rows of its group, which see all its columns.  That pass leaves (m, l, o)
 // of every query row, and the pass over the rows' own columns merges them where it writes its results.
+// Where a batch row's own query rows fill the tensor cores' tiles by themselves, nothing is gained by
+// taking several together: then (kBoth) one pass has units of one batch row whose tiles are those of its
+// prefix and then those of its own columns.
 #pragma once
 
 #include "tree.cuh"
@@ -51,7 +54,7 @@ struct AttnParams {
   float2* prior_ml;
   float* prior_o;
   const int32_t *prefix_len, *prefix_first, *group_start;
-  int P, M, two;  // prefixes; query rows of a unit; whether some group may have more than 128
+  int P, M, two, prefix_cap, prefix_one_row;  // prefixes; query rows of a unit; whether some group may have more than 128
 };
 
 // One batch row's columns.
@@ -90,25 +93,66 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b, int* err
 
 // The plan in shared memory: tiles of the rows before row b, per K/V head, and the rows.
 // (a prefix pass: of the prefixes, with their first query row (b T + t) G + g and number of query rows)
+// (kBoth: also each row's prefix: its columns, -1 for an error, first column and cache row)
 struct AttnPlan {
   int *pre, *first, *old, *row0, *rows;  // [B + 1], [B], [B]; prefix pass: [P + 1] and [P]
+  int *plen, *pfirst, *prow;             // [B]
 };
+enum AttnMode { kOwn = 0, kPrefixPass = 1, kBothParts = 2 };
 __host__ __device__ constexpr int attn_plan_bytes(int B) { return (3 * B + 1) * 4; }
 __host__ __device__ constexpr int prefix_plan_bytes(int P) { return (5 * P + 1) * 4; }
 static_assert(prefix_plan_bytes(kAttnMaxPrefixes) <= attn_plan_bytes(kAttnMaxRows), "one room for either plan");
 __device__ __forceinline__ AttnPlan attn_plan_at(void* smem, int n) {
   int* p = static_cast<int*>(smem);
-  return AttnPlan{p, p + n + 1, p + 2 * n + 1, p + 3 * n + 1, p + 4 * n + 1};
+  return AttnPlan{p, p + n + 1, p + 2 * n + 1, p + 3 * n + 1, p + 4 * n + 1, p + 3 * n + 1, p + 4 * n + 1, p + 5 * n + 1};
 }
+__host__ __device__ constexpr int both_plan_bytes(int B) { return (6 * B + 1) * 4; }
 
 // A unit counts `p.open` tiles more than it has, for what a CTA spends on opening and closing it,
 // so that shares with many short units take no longer than others.
 // Built by warp 0 of every CTA (the caller synchronises); CTA 0 records errors.
-template <bool kPrefix = false>
+template <int kMode = kOwn>
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, const AttnPlan& plan) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
-  if constexpr (kPrefix) {
+  if constexpr (kMode == kBothParts) {
+    bool bad = false;
+    for (int i = lane; i < p.P; i += 32) {
+      const int b0 = p.group_start[i], b1 = p.group_start[i + 1];
+      bad |= b0 < 0 || b1 < b0 || b1 > p.B;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && blockIdx.x == 0 && lane == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
+    for (int b = lane; b < p.B; b += 32) plan.plen[b] = bad ? -1 : 0;
+    for (int i0 = 0; i0 < p.P && !bad; i0 += 32) {
+      const int i = i0 + lane;
+      int b0 = 0, b1 = 0, len = 0, first = 0;
+      if (i < p.P) {
+        b0 = p.group_start[i];
+        b1 = p.group_start[i + 1];
+        len = p.prefix_len[i];
+        first = p.prefix_first ? p.prefix_first[i] : 0;
+        const int err = len < 0 || first < 0 ? SPECDEC_ERR_INPUT_RANGE
+                        : len > p.prefix_cap || first > p.prefix_cap - len ? SPECDEC_ERR_CAPACITY : 0;
+        if (err) {
+          len = -1;
+          if (blockIdx.x == 0) set_status(p.status, err);
+        }
+      }
+      __syncwarp();
+      for (int k = 0; k < min(32, p.P - i0); ++k) {
+        const int g0 = __shfl_sync(0xffffffffu, b0, k), g1 = __shfl_sync(0xffffffffu, b1, k);
+        const int l = __shfl_sync(0xffffffffu, len, k), f = __shfl_sync(0xffffffffu, first, k);
+        for (int b = g0 + lane; b < g1; b += 32) {
+          plan.plen[b] = l;
+          plan.pfirst[b] = f;
+          plan.prow[b] = p.prefix_one_row ? 0 : i0 + k;
+        }
+      }
+    }
+    __syncwarp();
+  }
+  if constexpr (kMode == kPrefixPass) {
     // rows of no group, or of one of a prefix without columns, are 0; where the groups' bounds are not
     // ascending within the batch nothing is known of any row
     bool bad = false;
@@ -162,6 +206,10 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int tile, const A
       const AttnRow r = attn_row(p, b, &err);
       if (err && blockIdx.x == 0) set_status(p.status, err);
       tiles = r.cols > 0 ? (r.cols + tile - 1) / tile + p.open : 0;
+      if (kMode == kBothParts && tiles > 0) {
+        const int len = plan.plen[b];
+        tiles = len < 0 ? 0 : tiles + (len + tile - 1) / tile;
+      }
       first = r.first;
       old = r.old;
     }
@@ -191,10 +239,10 @@ struct AttnShares {
     return x < more ? x / (base + 1) : rem + (x - more) / base;
   }
 };
-template <bool kPrefix = false>
+template <int kMode = kOwn>
 __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const AttnPlan& plan) {
   AttnShares s;
-  s.total = plan.pre[kPrefix ? p.P : p.B] * p.H;
+  s.total = plan.pre[kMode == kPrefixPass ? p.P : p.B] * p.H;
   const int most = s.total / p.min_tiles;
   s.groups = most < 1 ? 1 : min(most, p.groups);
   s.base = s.total / s.groups;
@@ -210,10 +258,12 @@ struct AttnSegment {
   int next;                       // place behind the segment
   int first, old, cols;           // its columns: AttnRow
   int row0, rows;                 // prefix pass: its first query row, and how many it has
+  int plen, pfirst, prow;         // kBoth: the columns of the prefix, whose tiles come first
 };
-template <bool kPrefix = false>
+template <int kMode = kOwn>
 __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnPlan& plan,
                                                     int x, int end) {
+  constexpr bool kPrefix = kMode == kPrefixPass;
   int lo = 0, hi = (kPrefix ? p.P : p.B) - 1;  // the last row with pre * H <= x: it has tiles
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -244,15 +294,20 @@ __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const A
   s.first = plan.first[lo];
   s.old = plan.old[lo];
   s.cols = s.old + (kPrefix ? 0 : p.T);
+  if constexpr (kMode == kBothParts) {
+    s.plen = plan.plen[lo];
+    s.pfirst = plan.pfirst[lo];
+    s.prow = plan.prow[lo];
+  }
   return s;
 }
 
 // The next segment with tiles at or behind x; false at the share's end.
-template <bool kPrefix = false>
+template <int kMode = kOwn>
 __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& plan, int x, int end,
                                           AttnSegment& s) {
   while (x < end) {
-    s = attn_segment<kPrefix>(p, plan, x, end);
+    s = attn_segment<kMode>(p, plan, x, end);
     if (s.tile1 > s.tile0) return true;
     x = s.next;
   }
@@ -365,6 +420,8 @@ __device__ __forceinline__ float2 attn_join(float m0, float l0, float2 part, flo
 // K/V head, and its launch (rows: of the cache).
 void attn_tc_shape(int R, int* M, int* MT);
 int launch_attn_tc(const AttnParams& p, int rows, int grid, bool prefix, cudaStream_t stream);
+// Both parts in one pass; prefix: the prefixes' cache layer and its rows.
+int launch_attn_tc_both(const AttnParams& p, int rows, const ByteView& prefix, int prefix_rows, int grid, cudaStream_t stream);
 // The kernel for few rows (tree_attention_mma.cu).
 void attn_mma_shape(int R, int hd, int* M, int* MT, int* tile, int* per_sm);
 int launch_attn_mma(const AttnParams& p, int M, int rows, int grid, bool prefix, cudaStream_t stream);

@@ -88,13 +88,13 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   char* smem = raw + (1024 - smem_addr(raw) % 1024) % 1024;
   const AttnPlan plan = attn_plan_at(smem + S::bytes - 1024, kPrefix ? p.P : p.B);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, qd = lane & 3;
-  if (warp == 0) attn_plan<kPrefix>(p, kTileCols, plan);
+  if (warp == 0) attn_plan<kPrefix ? kPrefixPass : kOwn>(p, kTileCols, plan);
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
     fence_mbar_init();
   }
   __syncthreads();
-  const AttnShares sh = attn_shares<kPrefix>(p, plan);
+  const AttnShares sh = attn_shares<kPrefix ? kPrefixPass : kOwn>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   if (sh.total == 0 || g >= sh.groups) return;
   const int x1 = sh.start(g + 1);
@@ -123,12 +123,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   };
   auto advance = [&](Cursor& c) {
     if (++c.tile >= c.seg.tile1) {
-      c.more = attn_next<kPrefix>(p, plan, c.seg.next, x1, c.seg);
+      c.more = attn_next<kPrefix ? kPrefixPass : kOwn>(p, plan, c.seg.next, x1, c.seg);
       c.tile = c.seg.tile0;
     }
   };
   Cursor ahead;
-  ahead.more = attn_next<kPrefix>(p, plan, sh.start(g), x1, ahead.seg);
+  ahead.more = attn_next<kPrefix ? kPrefixPass : kOwn>(p, plan, sh.start(g), x1, ahead.seg);
   ahead.tile = ahead.seg.tile0;
   int loaded = 0;  // tiles asked for so far
   for (; loaded < kStages && ahead.more; ++loaded) {
@@ -138,7 +138,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   int used = 0, row_b = -1;
   bool ok = true;
   AttnSegment seg;
-  for (int x = sh.start(g); attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
+  for (int x = sh.start(g); attn_next<kPrefix ? kPrefixPass : kOwn>(p, plan, x, x1, seg); x = seg.next) {
     const int nrows = kPrefix ? seg.rows : min(kRows, p.T * p.G - mt * kRows);
     if (kPrefix ? row_b < 0 : seg.b != row_b) {
       row_b = seg.b;

@@ -74,6 +74,11 @@ struct Bars {
   uint64_t q_full, v_clean, s_full[2], p_ready[2], o_done[2], drained;
 };
 
+// Tiles of a unit that are of its prefix (they come first).
+template <bool kBoth> __device__ __forceinline__ int prefix_tiles(const AttnSegment& s) {
+  return kBoth ? (s.plen + kCols - 1) / kCols : 0;
+}
+
 template <int HD> struct Smem {
   static constexpr int kQ = kRows * HD * 2, kTile = kCols * HD * 2;
   static constexpr int q = 0;                          // A's rows, then B's
@@ -96,10 +101,12 @@ __device__ __forceinline__ uint32_t visible32(unsigned long long anc, int base) 
   return static_cast<uint32_t>(anc << -base) | ((1u << -base) - 1u);
 }
 
-template <int HD, bool kPrefix>
+// kMode: over the rows' own columns, a prefix pass, or both parts in one (map2: the prefixes').
+template <int HD, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
+attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map2) {
   using S = Smem<HD>;
+  constexpr bool kPrefix = kMode == kPrefixPass, kBoth = kMode == kBothParts;
   constexpr int kSteps = HD / 16, kPanels = HD / 64;
   extern __shared__ char raw[];
   __shared__ Bars bar;
@@ -113,7 +120,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
   int nrows = min(2 * kRows, p.T * p.G - mt * 2 * kRows);  // query rows of this pair (prefix pass: of the unit)
   const bool two = kPrefix ? p.two != 0 : nrows > kRows;   // A and B are different rows, else alternate tiles
-  if (warp == 0) attn_plan<kPrefix>(p, kCols, plan);
+  if (warp == 0) attn_plan<kMode>(p, kCols, plan);
   if (warp == 9) tmem_alloc(&s_tmem, 512);
   if (tid == 32) {
     for (int i = 0; i < kMaxKStages; ++i) {
@@ -140,7 +147,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   tmem_fence_after();
   pdl_launch_dependents();  // the merge of cut units may be set up
   const uint32_t tmem = s_tmem;
-  const AttnShares sh = attn_shares<kPrefix>(p, plan);
+  const AttnShares sh = attn_shares<kMode>(p, plan);
   const bool work = sh.total > 0 && g < sh.groups;
   const int x0 = work ? sh.start(g) : 0, x1 = work ? sh.start(g + 1) : 0;
   const int nk = two ? kStages : kMaxKStages;
@@ -157,17 +164,18 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       uint64_t *full = is_v ? bar.v_full : bar.k_full, *empty = is_v ? bar.v_empty : bar.k_empty;
       int n = 0;  // tiles so far
       AttnSegment seg;
-      for (int x = x0; ok && attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next) {
-        const int crow = p.one_row ? 0 : seg.b;
+      for (int x = x0; ok && attn_next<kMode>(p, plan, x, x1, seg); x = seg.next) {
+        const int crow = p.one_row ? 0 : seg.b, pt = prefix_tiles<kBoth>(seg);
         for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
-          const int st = n % stages, col = seg.first + tile * kCols;
+          const bool of_prefix = kBoth && tile < pt;
+          const int st = n % stages, col = of_prefix ? seg.pfirst + tile * kCols : seg.first + (tile - pt) * kCols;
           // the first product needs K and Q: what comes after must not stand before Q in the queue
           if (n == (is_v ? 0 : 1) && !(ok = wait(&bar.q_full, 0))) break;
           if (!(ok = wait(&empty[st], ((n / stages) & 1) ^ 1))) break;
           mbar_arrive_expect_tx(&full[st], S::kTile);
           char* to = smem + (is_v ? S::v + st * S::kTile : S::k_stage(st));
           for (int j = 0; j < kPanels; ++j)
-            tma_load_5d(to + j * kCols * 128, &map, j * 64, col, seg.h, crow, is_v, &full[st]);
+            tma_load_5d(to + j * kCols * 128, of_prefix ? &map2 : &map, j * 64, col, seg.h, of_prefix ? seg.prow : crow, is_v, &full[st]);
         }
       }
       // no copy outlives the CTA: the last ones issued have landed (their tiles were used) unless
@@ -193,9 +201,11 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
                    v_desc = mma_desc(sm + S::v, kCols * 128, 1024);
     int kv = 0, seg_no = 0, done[2] = {0, 0};  // tiles, segments, jobs of A and B so far
     AttnSegment seg;
-    for (int x = x0; ok && attn_next<kPrefix>(p, plan, x, x1, seg); x = seg.next, ++seg_no) {
+    for (int x = x0; ok && attn_next<kMode>(p, plan, x, x1, seg); x = seg.next, ++seg_no) {
       const int n = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0), jobs = pair ? 2 * n : n;
-      const int clean = seg.old / kCols - seg.tile0;  // the first tile that needs care
+      const int pt = prefix_tiles<kBoth>(seg);
+      const int clean = pt + seg.old / kCols - seg.tile0;  // the first tile that needs care
+      const int ragged = kBoth && seg.plen % kCols ? pt - 1 - seg.tile0 : -1;  // and the prefix's last
       // Job i is tile i / 2 for A or B (pair), or tile i for one of them.
       auto tile_of = [&](int i) { return pair ? i >> 1 : i; };
       auto full = [&](uint64_t* bars, int stages, int i) {  // K or V of job i
@@ -224,17 +234,18 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       }
       for (int i = 0; i < jobs && ok; ++i) {
         const int a = i & 1, tile = tile_of(i), st = (kv + tile) % kStages;
-        const int col0 = (seg.tile0 + tile) * kCols;
-        const int steps = min(kCols / 16, (seg.cols - col0 + 15) >> 4);
-        if (tile >= clean && (!pair || a == 0)) {
+        const bool of_prefix = kBoth && seg.tile0 + tile < pt;
+        const int col0 = (seg.tile0 + tile - (of_prefix ? 0 : pt)) * kCols;
+        const int steps = min(kCols / 16, ((of_prefix ? seg.plen : seg.cols) - col0 + 15) >> 4);
+        if ((tile >= clean || (kBoth && tile == ragged)) && (!pair || a == 0)) {
           full(bar.v_full, kStages, i);
           if (!ok) break;
           // clean V where it may hold anything: a lane per column (steps of 16 columns behind the
           // last are left out of the product)
           char* vt = smem + S::v + st * S::kTile;
-          for (int c = max(0, seg.old - col0) + lane; c < steps * 16; c += 32) {
+          for (int c = max(0, (of_prefix ? seg.plen : seg.old) - col0) + lane; c < steps * 16; c += 32) {
             const int node = col0 + c - seg.old;
-            const bool drop = kPrefix || node >= p.T || s_anc[node] == 0;
+            const bool drop = kPrefix || of_prefix || node >= p.T || s_anc[node] == 0;
             auto at = [&](int k) { return reinterpret_cast<uint4*>(vt + swizzled(c, k, kCols)); };
             if (!drop) {
               bool bad = false;
@@ -335,7 +346,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       arrive(&bar.q_full);
     };
     AttnSegment seg;
-    bool more = attn_next<kPrefix>(p, plan, x0, x1, seg);
+    bool more = attn_next<kMode>(p, plan, x0, x1, seg);
     if (more) {
       ask(seg);
       if (tid == 0) s_bad = 0;
@@ -367,7 +378,9 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
         if (!(ok = warp_wait(&bar.s_full[a], seen & 1))) break;
         if (!idle) {
           tmem_fence_after();
-          const int base = (seg.tile0 + (two ? j : 2 * j + a)) * kCols - seg.old;
+          const int at = seg.tile0 + (two ? j : 2 * j + a), pt = prefix_tiles<kBoth>(seg);
+          const bool of_prefix = kBoth && at < pt;
+          const int base = of_prefix ? at * kCols - seg.plen : (at - pt) * kCols - seg.old;
           // One pass with the maximum so far: weights are taken against it while the tile's own
           // maximum is found, and only where that is too large are they taken again.
           uint32_t w[4][16];
@@ -386,7 +399,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
               tmem_wait_ld32(v);
               if (c < 3) tmem_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
               if (base + kCols > 0) {
-                const uint32_t vis = visible32(kPrefix ? 0ull : anc, base + c * 32);
+                const uint32_t vis = visible32(kPrefix || of_prefix ? 0ull : anc, base + c * 32);
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                   if (!(vis >> k & 1)) v[k] = __float_as_uint(-INFINITY);
@@ -447,7 +460,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       // opened, and its first products run, before this one is written out.
       const AttnSegment now = seg;
       if (!(ok = named_bar_all(1, 256, ok))) break;
-      more = attn_next<kPrefix>(p, plan, seg.next, x1, seg);
+      more = attn_next<kMode>(p, plan, seg.next, x1, seg);
       if (more) ask(seg);
       if (jobs > 0) ok = warp_wait(&bar.o_done[a], ends++ & 1);
       ok = ok && warp_wait(&bar.v_clean, seg_no & 1);
@@ -587,15 +600,14 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
 
 // Units that share borders cut, merged by a launch of their own: it spreads the parts over the GPU
 // and needs no tickets, where the CTA that came last would add parts of 128 KB one after the other
-// behind the last share.  CTA = border and 32 rows; thread = row and 4 * kPer of its values.
-// Measured alone and cold (ncu), 75 borders of 512 rows: 14.7 us for 30 MB, the loads' latency.
+// behind the last share.  CTA = border, 32 rows and a part of their values; thread = row and 4 of them.
 template <int HD, bool kPrefix>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
-  constexpr int kPer = HD / 32;  // float4 a thread holds
-  constexpr int kBlock = 64;     // parts at a time
+  constexpr int kSlices = HD / 32, kPer = 1;  // CTAs that share a row's values; float4 a thread holds
+  constexpr int kBlock = 64;                  // parts at a time
   __shared__ float2 s_ml[kBlock][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g0 = blockIdx.x, block = blockIdx.y & 7, mt = blockIdx.y >> 3;
+  const int slice = blockIdx.y % kSlices, block = blockIdx.y / kSlices & 7, mt = blockIdx.y / kSlices >> 3, g0 = blockIdx.x;
   const int pr = block * 32 + lane, rr = mt * 2 * kRows + pr, t = rr / p.G;
   pdl_wait();
   const int4 cut = __ldcg(p.cuts + g0 + 1);
@@ -603,7 +615,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   if (parts < 2 || (kPrefix && block * 32 >= cut.z >> 1)) return;
   auto slot = [&](int i) { return 2ll * ((g0 + i) * p.MT + mt) + (i == 0 ? cut.z & 1 : 0); };
   // the parts in blocks: their rows' (m, l) into shared memory at once, then the sums
-  const int d0 = warp * kPer;  // first float4
+  const int d0 = slice * 8 + warp;  // its float4
   bool live = true;
   float m = -INFINITY, l = 0.f;
   float4 o[kPer];
@@ -652,7 +664,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
     s.h = cut.y;
     const AttnQuery row = attn_query<true>(p, s, pr);
     const long long at = attn_prior_at(p, row.b, row.t, row.h);
-    if (warp == 0) p.prior_ml[at] = make_float2(m, l);
+    if (d0 == 0) p.prior_ml[at] = make_float2(m, l);
     float4* to = reinterpret_cast<float4*>(p.prior_o + at * HD) + d0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) to[k] = o[k];
@@ -685,31 +697,32 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
   for (int k = 0; k < kPer; ++k)
     *reinterpret_cast<uint2*>(y + k * 8) = live ? make_uint2(bf16_pack(o[k].x * inv, o[k].y * inv), bf16_pack(o[k].z * inv, o[k].w * inv))
                                                 : make_uint2(0, 0);
-  if (p.lse && warp == 0)
+  if (p.lse && d0 == 0)
     p.lse[(static_cast<long long>(b) * p.T + t) * p.Hq + qh] =
         live ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int HD, bool kPrefix>
-int launch_tc(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {
-  auto kernel = attn_tc_kernel<HD, kPrefix>;
+template <int HD, int kMode>
+int launch_tc(const AttnParams& p, const CUtensorMap& map, const CUtensorMap& map2, int grid, cudaStream_t stream) {
+  auto kernel = attn_tc_kernel<HD, kMode>;
   constexpr int smem = Smem<HD>::bytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem + attn_plan_bytes(kAttnMaxRows));
+                                             smem + (kMode == kBothParts ? both_plan_bytes(kAttnMaxRows) : attn_plan_bytes(kAttnMaxRows)));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<grid, kThreads, smem + (kPrefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)), stream>>>(p, map);
+  const int plan = kMode == kBothParts ? both_plan_bytes(p.B) : kMode == kPrefixPass ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B);
+  kernel<<<grid, kThreads, smem + plan, stream>>>(p, map, map2);
   const cudaError_t e2 = cudaGetLastError();
   if (e2 != cudaSuccess || p.groups == 1) return map_cuda_error(e2);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(p.groups - 1, p.MT * 8);
+  cfg.gridDim = dim3(p.groups - 1, p.MT * 8 * (HD / 32));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return map_cuda_error(cudaLaunchKernelEx(&cfg, attn_merge_kernel<HD, kPrefix>, p));
+  return map_cuda_error(cudaLaunchKernelEx(&cfg, attn_merge_kernel<HD, kMode == kPrefixPass>, p));
 }
 
 }  // namespace
@@ -756,8 +769,16 @@ int launch_attn_tc(const AttnParams& p, int rows, int grid, bool prefix, cudaStr
   CUtensorMap map;
   if (!kv_tensor_map(&map, p.cache, p.hd, p.cap, p.H, rows, kCols)) return SPECDEC_ERR_UNSUPPORTED;
   if (prefix)
-    return p.hd == 64 ? launch_tc<64, true>(p, map, grid, stream) : launch_tc<128, true>(p, map, grid, stream);
-  return p.hd == 64 ? launch_tc<64, false>(p, map, grid, stream) : launch_tc<128, false>(p, map, grid, stream);
+    return p.hd == 64 ? launch_tc<64, kPrefixPass>(p, map, map, grid, stream) : launch_tc<128, kPrefixPass>(p, map, map, grid, stream);
+  return p.hd == 64 ? launch_tc<64, kOwn>(p, map, map, grid, stream) : launch_tc<128, kOwn>(p, map, map, grid, stream);
+}
+
+int launch_attn_tc_both(const AttnParams& p, int rows, const ByteView& prefix, int prefix_rows, int grid, cudaStream_t stream) {
+  CUtensorMap map, map2;
+  if (!kv_tensor_map(&map, p.cache, p.hd, p.cap, p.H, rows, kCols) ||
+      !kv_tensor_map(&map2, prefix, p.hd, p.prefix_cap, p.H, prefix_rows, kCols))
+    return SPECDEC_ERR_UNSUPPORTED;
+  return p.hd == 64 ? launch_tc<64, kBothParts>(p, map, map2, grid, stream) : launch_tc<128, kBothParts>(p, map, map2, grid, stream);
 }
 
 }  // namespace specdec

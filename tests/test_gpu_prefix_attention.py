@@ -127,6 +127,8 @@ def inputs(seed, B, T, Hq, H, hd, n, dtype, P, lens, first=None, arena=None, sla
     (40, 1, 4, 2, 96, [77, 0, 31], [0, 13, 20, 40], False),   # a prefix without columns
     (7, 2, 4, 2, 128, [40, 50, 60], [0, 3, 3, 7], False),     # a group without rows
     (64, 1, 32, 8, 128, [2000], [0, 64], False),
+    (5, 32, 32, 8, 128, [700, 129], [1, 3, 4], True),         # rows whose own queries fill tiles, of no group too
+    (6, 64, 8, 2, 64, [0, 257], [0, 2, 6], True),
 ])
 def test_against_the_definition(dtype, B, T, Hq, H, hd, lens, groups, tree):
     rng = np.random.default_rng(B * T + hd)
@@ -141,7 +143,7 @@ def test_against_the_definition(dtype, B, T, Hq, H, hd, lens, groups, tree):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("B,T,G,hd", [(2, 1, 1, 64), (5, 1, 1, 128), (7, 2, 2, 64), (9, 8, 2, 128), (5, 16, 4, 64)])
+@pytest.mark.parametrize("B,T,G,hd", [(2, 1, 1, 64), (5, 1, 1, 128), (7, 2, 2, 64), (9, 8, 2, 128), (5, 16, 4, 64), (3, 32, 4, 128), (3, 25, 8, 64), (2, 64, 9, 64)])
 @pytest.mark.parametrize("cols", [1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 511])
 def test_tile_borders(dtype, B, T, G, hd, cols):
     lens, n = [cols, max(1, cols - 1)], np.arange(1, B + 1)
@@ -167,7 +169,7 @@ def test_long_prefixes_are_split(dtype, B, T, Hq, H, hd, cols):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("T,Hq,H,hd", [(1, 4, 2, 64), (6, 8, 2, 128), (20, 16, 1, 64), (3, 2, 2, 48)])
+@pytest.mark.parametrize("T,Hq,H,hd", [(1, 4, 2, 64), (6, 8, 2, 128), (20, 16, 1, 64), (16, 16, 1, 128), (3, 2, 2, 48)])
 def test_a_pool_and_prefixes_in_an_arena(dtype, T, Hq, H, hd):
     """Prefixes and rows anywhere in one cache row each."""
     rng = np.random.default_rng(T)
@@ -185,7 +187,7 @@ def test_a_pool_and_prefixes_in_an_arena(dtype, T, Hq, H, hd):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
-@pytest.mark.parametrize("B,T", [(2, 1), (6, 9), (9, 32)])
+@pytest.mark.parametrize("B,T", [(2, 1), (6, 9), (9, 32), (3, 64)])
 def test_scales(dtype, scale, B, T):
     n, lens = np.full(B, 30), [200]
     q, cache, W, prefix = inputs(7, B, T, 4, 2, 64, n, dtype, 1, lens)
@@ -197,7 +199,7 @@ def test_scales(dtype, scale, B, T):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("far", [0, 1])
-@pytest.mark.parametrize("B,T", [(2, 1), (6, 9), (9, 32)])
+@pytest.mark.parametrize("B,T", [(2, 1), (6, 9), (9, 32), (3, 64)])
 def test_one_part_far_above_the_other(dtype, far, B, T):
     """Scores of one part a hundred above the other's: the other's weights vanish, and nothing overflows."""
     n, lens = np.full(B, 20), [150]
@@ -213,7 +215,7 @@ def test_one_part_far_above_the_other(dtype, far, B, T):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("B,T,hd", [(2, 1, 64), (6, 9, 128), (9, 32, 64), (3, 4, 96)])
+@pytest.mark.parametrize("B,T,hd", [(2, 1, 64), (6, 9, 128), (9, 32, 64), (4, 64, 128), (3, 4, 96)])
 def test_values_that_are_not_finite_stay_in_their_place(dtype, B, T, hd):
     n, lens = np.full(B, 10), [70, 90]
     groups = [0, B // 2, B]
@@ -293,7 +295,7 @@ def test_without_prefixes_it_is_the_attention_of_a_tree(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("B,T,hd", [(4, 1, 64), (6, 9, 128), (9, 32, 64), (4, 3, 96)])
+@pytest.mark.parametrize("B,T,hd", [(4, 1, 64), (6, 9, 128), (9, 32, 64), (5, 50, 64), (4, 3, 96)])
 @pytest.mark.parametrize("lens,first,groups,code,written", [
     ([50, -1], None, [0, 2, 4], 5, [0, 1]),             # a negative length
     ([50, 70], [0, -3], [0, 2, 4], 5, [0, 1]),          # a negative first column
