@@ -94,9 +94,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
     fence_mbar_init();
   }
   __syncthreads();
+  if (kPrefix) pdl_launch_dependents();  // the pass over own columns may be set up
   const AttnShares sh = attn_shares<kPrefix ? kPrefixPass : kOwn>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
-  if (sh.total == 0 || g >= sh.groups) return;
+  if (sh.total == 0 || g >= sh.groups) {
+    if (!kPrefix) attn_wait_prior(p);
+    return;
+  }
   const int x1 = sh.start(g + 1);
   // The warp's columns of the cursor's tile into stage `st`: lanes 0..15 copy K's, the others V's.
   auto fetch = [&](const Cursor& c, int st) {
@@ -318,6 +322,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
       }
       const bool live = s_anc[t] != 0;
       if (p.prior) {
+        attn_wait_prior(p);
         const int state = p.prior[seg.b];
         if (state < 0) return;
         if (state > 0) {
@@ -363,6 +368,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) attn_fma_kernel(const AttnPara
       store(r, i, acc, mm, ll);
     }
   }
+  if (!kPrefix) attn_wait_prior(p);
   if (!ok) {
     set_status(p.status, SPECDEC_ERR_TIMEOUT);
     // no copy outlives the CTA: each stage's last one, which may be the one whose wait gave up, is
@@ -391,9 +397,13 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
   const AttnPlan plan = attn_plan_at(reinterpret_cast<float4*>(s_q + M * hd) + RG * kTile, kPrefix ? p.P : p.B);
   if (warp == 0) attn_plan<kPrefix ? kPrefixPass : kOwn>(p, kTile, plan);
   __syncthreads();
+  if (kPrefix) pdl_launch_dependents();  // the pass over own columns may be set up
   const AttnShares sh = attn_shares<kPrefix ? kPrefixPass : kOwn>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
-  if (sh.total == 0 || g >= sh.groups) return;
+  if (sh.total == 0 || g >= sh.groups) {
+    if (!kPrefix) attn_wait_prior(p);
+    return;
+  }
   const int x1 = sh.start(g + 1);
   int row_b = -1;
   AttnSegment seg;
@@ -608,6 +618,7 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
         continue;
       }
       if (p.prior) {
+        attn_wait_prior(p);
         const int state = p.prior[seg.b];
         if (state < 0) continue;
         if (state > 0) {
@@ -640,6 +651,7 @@ __global__ void __launch_bounds__(256) attn_fma_rows_kernel(const AttnParams p) 
             anc[k] ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
     }
   }
+  if (!kPrefix) attn_wait_prior(p);
 }
 
 // ------------------------------------------------------------------------------------- host
@@ -735,8 +747,8 @@ int launch_fma(K kernel, const AttnParams& p, const AttnShape& s, bool prefix, c
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(s.smem) + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<s.grid, s.warps * 32, s.smem + (prefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)), stream>>>(p);
-  return map_cuda_error(cudaGetLastError());
+  return map_cuda_error(attn_launch(kernel, s.grid, s.warps * 32, s.smem + (prefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)),
+                                    !prefix && p.prior, stream, p));
 }
 template <typename T, int NB, bool kPrefix>
 int launch_fma_rows(const AttnParams& p, const AttnShape& s, cudaStream_t stream) {
@@ -785,20 +797,22 @@ AttnShape prefix_shape(int es, long long R, int hd, long long columns) {
   return s;
 }
 
-// A workspace for prefixes too: the passes use the same room for cut units one after the other; what
-// the prefix pass leaves for the rows follows.
+// A workspace for prefixes too.  The passes may overlap, so each has room of its own for cut units (the
+// tickets' first half is for the own columns, its second for the prefixes); what the prefix pass leaves for
+// the rows follows.
 struct PrefixWorkspace {
-  size_t state, ml, o, bytes;  // offsets
+  size_t parts, state, ml, o, bytes;  // offsets
 };
 PrefixWorkspace prefix_workspace(int es, int B, int T, int Hq, int G, int hd) {
-  size_t most = 0;  // of the kernels that the lengths may decide for
+  size_t own = 0, prefix = 0;  // of the kernels that the lengths may decide for
   for (const long long columns : {0LL, kFewColumns + 1}) {
-    most = std::max(most, attn_workspace(attn_shape(es, T, G, hd, columns), hd).bytes);
-    most = std::max(most, attn_workspace(prefix_shape(es, static_cast<long long>(B) * T * G, hd, columns), hd).bytes);
+    own = std::max(own, attn_workspace(attn_shape(es, T, G, hd, columns), hd).bytes);
+    prefix = std::max(prefix, attn_workspace(prefix_shape(es, static_cast<long long>(B) * T * G, hd, columns), hd).bytes);
   }
   const size_t rows = static_cast<size_t>(B) * T * Hq;
   PrefixWorkspace w;
-  w.state = round256(most);
+  w.parts = round256(own);
+  w.state = w.parts + round256(prefix);
   w.ml = w.state + round256(static_cast<size_t>(B) * 4);
   w.o = w.ml + round256(rows * 8);
   w.bytes = w.o + round256(rows * hd * 4);
@@ -914,7 +928,7 @@ int own_pass(AttnParams p, const specdec_tree_attention_args* a, size_t room, cu
   s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
   s.grid = s.groups * s.MT;
   if (room < attn_workspace(s, c.head_dim).bytes) return SPECDEC_ERR_INVALID_ARG;
-  if (s.grid > static_cast<int>(kTicketBytes / 4)) return SPECDEC_ERR_UNSUPPORTED;
+  if (s.grid > static_cast<int>(kTicketBytes / (p.prior ? 8 : 4))) return SPECDEC_ERR_UNSUPPORTED;
   if (static_cast<long long>(a->B) * c.heads * (columns / kCols + 16) >= (1LL << 31))
     return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
   set_shape(p, s, a->workspace);
@@ -1005,8 +1019,9 @@ extern "C" int specdec_prefix_attention(const specdec_prefix_attention_args* arg
   const long long tiles = units * ((f.cap_cols - 1) / shape.tile + 1 + shape.open);
   shape.groups = static_cast<int>(std::min<long long>(shape.groups, std::max<long long>(1, tiles / shape.min_tiles)));
   shape.grid = shape.groups;
-  if (shape.grid > static_cast<int>(kTicketBytes / 4)) return SPECDEC_ERR_UNSUPPORTED;
-  set_shape(p, shape, a->workspace);
+  if (shape.grid > static_cast<int>(kTicketBytes / 8)) return SPECDEC_ERR_UNSUPPORTED;
+  set_shape(p, shape, ws + w.parts);
+  p.ticket = reinterpret_cast<unsigned*>(ws) + kTicketBytes / 8;
   const int rp = launch_attention<true>(p, shape, es, f.rows, s);
   if (rp) return rp;
   return own_pass(own, a, a->workspace_bytes, s);

@@ -98,7 +98,7 @@ struct AttnPlan {
   int *pre, *first, *old, *row0, *rows;  // [B + 1], [B], [B]; prefix pass: [P + 1] and [P]
   int *plen, *pfirst, *prow;             // [B]
 };
-enum AttnMode { kOwn = 0, kPrefixPass = 1, kBothParts = 2 };
+enum AttnMode { kOwn = 0, kPrefixPass = 1, kBothParts = 2, kBehind = 3 };  // kBehind: own columns behind a prefix pass
 __host__ __device__ constexpr int attn_plan_bytes(int B) { return (3 * B + 1) * 4; }
 __host__ __device__ constexpr int prefix_plan_bytes(int P) { return (5 * P + 1) * 4; }
 static_assert(prefix_plan_bytes(kAttnMaxPrefixes) <= attn_plan_bytes(kAttnMaxRows), "one room for either plan");
@@ -408,12 +408,33 @@ __device__ __forceinline__ AttnQuery attn_query(const AttnParams& p, const AttnS
 __device__ __forceinline__ long long attn_prior_at(const AttnParams& p, int b, int t, int h) {
   return (static_cast<long long>(b) * p.T + t) * p.Hq + h;
 }
+// The pass over own columns may start while the prefix pass before it still runs: what that left is read
+// behind this, and no CTA ends before (the next kernel waits for this one alone).
+__device__ __forceinline__ void attn_wait_prior(const AttnParams& p) {
+  if (p.prior) pdl_wait();
+}
 // Merging two parts of a row: the factors of the first's and the second's sums, and (m, l) of both.
 __device__ __forceinline__ float2 attn_join(float m0, float l0, float2 part, float& f0, float& f1) {
   const float m = fmaxf(m0, part.x), off = m == -INFINITY ? 0.f : m;
   f0 = exp2f(m0 - off);
   f1 = exp2f(part.x - off);
   return make_float2(m, l0 * f0 + part.y * f1);
+}
+
+// Launch of a pass, behind a prefix pass as its programmatic dependent.
+template <typename... Params, typename... Args>
+cudaError_t attn_launch(void (*kernel)(Params...), int grid, int threads, size_t smem, bool behind, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // The tensor-core kernel (tree_attention_tc.cu): rows per M-tile and M-tiles for R query rows per

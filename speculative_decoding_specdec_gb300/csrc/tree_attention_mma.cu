@@ -94,9 +94,13 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
     fence_mbar_init();
   }
   __syncthreads();
+  if (kPrefix) pdl_launch_dependents();  // the pass over own columns may be set up
   const AttnShares sh = attn_shares<kPrefix ? kPrefixPass : kOwn>(p, plan);
   const int g = blockIdx.x / p.MT, mt = blockIdx.x % p.MT;
-  if (sh.total == 0 || g >= sh.groups) return;
+  if (sh.total == 0 || g >= sh.groups) {
+    if (!kPrefix) attn_wait_prior(p);
+    return;
+  }
   const int x1 = sh.start(g + 1);
   const float scale = fmaxf(fabsf(p.scale_log2), 1.2e-38f);  // hidden scores stay -infinity
   const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -409,6 +413,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       continue;
     }
     if (p.prior) {
+      attn_wait_prior(p);
       const int state = p.prior[row.b];
       if (state < 0) continue;
       if (state > 0 && live) {
@@ -429,6 +434,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
       p.lse[(static_cast<long long>(seg.b) * p.T + t) * p.Hq + h] =
           live ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
   }
+  if (!kPrefix) attn_wait_prior(p);
   if (!ok) {
     set_status(p.status, SPECDEC_ERR_TIMEOUT);
     // no copy outlives the CTA: each stage's last one, which may be the one whose wait gave up, is
@@ -445,8 +451,8 @@ int launch_mma(const AttnParams& p, const CUtensorMap& map, int grid, cudaStream
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              smem + attn_plan_bytes(kAttnMaxRows));
   if (e != cudaSuccess) return map_cuda_error(e);
-  kernel<<<grid, kThreads, smem + (kPrefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)), stream>>>(p, map);
-  return map_cuda_error(cudaGetLastError());
+  return map_cuda_error(attn_launch(kernel, grid, kThreads, smem + (kPrefix ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B)),
+                                    !kPrefix && p.prior, stream, p, map));
 }
 
 }  // namespace

@@ -101,12 +101,13 @@ __device__ __forceinline__ uint32_t visible32(unsigned long long anc, int base) 
   return static_cast<uint32_t>(anc << -base) | ((1u << -base) - 1u);
 }
 
-// kMode: over the rows' own columns, a prefix pass, or both parts in one (map2: the prefixes').
+// kMode: over the rows' own columns, alone or behind a prefix pass, a prefix pass, or both parts in one
+// (map2: the prefixes').
 template <int HD, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map2) {
   using S = Smem<HD>;
-  constexpr bool kPrefix = kMode == kPrefixPass, kBoth = kMode == kBothParts;
+  constexpr bool kPrefix = kMode == kPrefixPass, kBoth = kMode == kBothParts, kHasPrior = kMode == kBehind;
   constexpr int kSteps = HD / 16, kPanels = HD / 64;
   extern __shared__ char raw[];
   __shared__ Bars bar;
@@ -466,7 +467,8 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, cons
       ok = ok && warp_wait(&bar.v_clean, seg_no & 1);
       tmem_fence_after();
       const unsigned long long poison = kPrefix ? 0ull : anc & s_poison;  // nodes it sees whose V is not finite somewhere
-      const int state = !kPrefix && p.prior && mine ? p.prior[now.b] : 0;  // of a prefix pass
+      if (kHasPrior) pdl_wait();
+      const int state = kHasPrior && mine ? p.prior[now.b] : 0;  // of a prefix pass
       const bool write = mine && !s_bad && state >= 0;
       if (!(ok = named_bar_all(1, 256, ok))) break;  // all have read s_poison and s_bad
       if (tid == 0) s_bad = 0;
@@ -491,7 +493,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, cons
       if (kPrefix && mine) {
         const AttnQuery at = attn_query<kPrefix>(p, now, pr);
         prior = attn_prior_at(p, at.b, at.t, at.h);
-      } else if (!kPrefix && state > 0) {
+      } else if (kHasPrior && state > 0) {
         prior = attn_prior_at(p, now.b, t_of, now.h * p.G + rr % p.G);
       }
       auto store_out = [&](int c, float (&o)[32]) {  // (zeros for an unused node, whatever o is)
@@ -501,7 +503,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, cons
           for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           return;
         }
-        if (state > 0) {
+        if (kHasPrior && state > 0) {
           const float4* from = reinterpret_cast<const float4*>(p.prior_o + prior * HD + c * 32);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -556,7 +558,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, cons
           m = mn;
         }
       }
-      if (!kPrefix && whole && state > 0) {
+      if (kHasPrior && whole && state > 0) {
         const float2 ml = attn_join(m, l, __ldcg(p.prior_ml + prior), f_own, f_prior);
         m = ml.x;
         l = ml.y;
@@ -589,6 +591,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, cons
     if (!ok) cp_async_wait_all();  // (Q of a segment that was not opened)
   }
   if (!ok) set_status(p.status, SPECDEC_ERR_TIMEOUT);
+  if (kHasPrior) pdl_wait();  // no CTA ends before the prefix pass: the next kernel waits for this one alone
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
@@ -600,22 +603,28 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map, cons
 
 // Units that share borders cut, merged by a launch of their own: it spreads the parts over the GPU
 // and needs no tickets, where the CTA that came last would add parts of 128 KB one after the other
-// behind the last share.  CTA = border, 32 rows and a part of their values; thread = row and 4 of them.
-template <int HD, bool kPrefix>
+// behind the last share.  CTA = border and 32 rows; thread = row and 4 * kPer of its values.
+// Measured alone and cold (ncu), 75 borders of 512 rows: 14.7 us for 30 MB, the loads' latency.
+// A prefix pass has few units of many parts: there kSlices CTAs share a row's values (8 units of 256 rows
+// in 19 parts: 11.3 us, 17.4 us with one).
+template <int HD, int kMode>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
-  constexpr int kSlices = HD / 32, kPer = 1;  // CTAs that share a row's values; float4 a thread holds
-  constexpr int kBlock = 64;                  // parts at a time
+  constexpr bool kPrefix = kMode == kPrefixPass;
+  constexpr int kSlices = kPrefix ? HD / 32 : 1, kPer = HD / 32 / kSlices;  // float4 a thread holds
+  constexpr int kBlock = 64;     // parts at a time
   __shared__ float2 s_ml[kBlock][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slice = blockIdx.y % kSlices, block = blockIdx.y / kSlices & 7, mt = blockIdx.y / kSlices >> 3, g0 = blockIdx.x;
+  const int slice = blockIdx.y % kSlices, by = blockIdx.y / kSlices;
+  const int g0 = blockIdx.x, block = by & 7, mt = by >> 3;
   const int pr = block * 32 + lane, rr = mt * 2 * kRows + pr, t = rr / p.G;
+  if (kPrefix) pdl_launch_dependents();  // the pass over own columns may be set up
   pdl_wait();
   const int4 cut = __ldcg(p.cuts + g0 + 1);
   const int b = cut.x, qh = cut.y * p.G + rr - t * p.G, parts = cut.w;
   if (parts < 2 || (kPrefix && block * 32 >= cut.z >> 1)) return;
   auto slot = [&](int i) { return 2ll * ((g0 + i) * p.MT + mt) + (i == 0 ? cut.z & 1 : 0); };
   // the parts in blocks: their rows' (m, l) into shared memory at once, then the sums
-  const int d0 = slice * 8 + warp;  // its float4
+  const int d0 = (slice * 8 + warp) * kPer;  // first float4
   bool live = true;
   float m = -INFINITY, l = 0.f;
   float4 o[kPer];
@@ -671,7 +680,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
     return;
   }
   if (rr >= p.T * p.G) return;
-  if (p.prior) {
+  if constexpr (kMode == kBehind) {
     const int state = p.prior[b];
     if (state < 0) return;
     if (state > 0) {
@@ -710,19 +719,18 @@ int launch_tc(const AttnParams& p, const CUtensorMap& map, const CUtensorMap& ma
                                              smem + (kMode == kBothParts ? both_plan_bytes(kAttnMaxRows) : attn_plan_bytes(kAttnMaxRows)));
   if (e != cudaSuccess) return map_cuda_error(e);
   const int plan = kMode == kBothParts ? both_plan_bytes(p.B) : kMode == kPrefixPass ? prefix_plan_bytes(p.P) : attn_plan_bytes(p.B);
-  kernel<<<grid, kThreads, smem + plan, stream>>>(p, map, map2);
-  const cudaError_t e2 = cudaGetLastError();
+  const cudaError_t e2 = attn_launch(kernel, grid, kThreads, smem + plan, kMode == kBehind, stream, p, map, map2);
   if (e2 != cudaSuccess || p.groups == 1) return map_cuda_error(e2);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(p.groups - 1, p.MT * 8 * (HD / 32));
+  cfg.gridDim = dim3(p.groups - 1, p.MT * 8 * (kMode == kPrefixPass ? HD / 32 : 1));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return map_cuda_error(cudaLaunchKernelEx(&cfg, attn_merge_kernel<HD, kMode == kPrefixPass>, p));
+  return map_cuda_error(cudaLaunchKernelEx(&cfg, attn_merge_kernel<HD, kMode>, p));
 }
 
 }  // namespace
@@ -770,6 +778,8 @@ int launch_attn_tc(const AttnParams& p, int rows, int grid, bool prefix, cudaStr
   if (!kv_tensor_map(&map, p.cache, p.hd, p.cap, p.H, rows, kCols)) return SPECDEC_ERR_UNSUPPORTED;
   if (prefix)
     return p.hd == 64 ? launch_tc<64, kPrefixPass>(p, map, map, grid, stream) : launch_tc<128, kPrefixPass>(p, map, map, grid, stream);
+  if (p.prior)
+    return p.hd == 64 ? launch_tc<64, kBehind>(p, map, map, grid, stream) : launch_tc<128, kBehind>(p, map, map, grid, stream);
   return p.hd == 64 ? launch_tc<64, kOwn>(p, map, map, grid, stream) : launch_tc<128, kOwn>(p, map, map, grid, stream);
 }
 
