@@ -662,7 +662,9 @@ struct AttnShape {
   int kind;
 };
 enum { kFma = 0, kMma = 1, kTc = 2 };
-constexpr long long kFewColumns = 128 << 10;
+// (behind a prefix pass the former up to more: 32 rows of 24 query rows, 8 K/V heads, 2400 shared columns:
+// 70 us against 91 with up to 512 columns of their own, 101 against 121 with up to 2048; 16 of 4096: 104, 115)
+constexpr long long kFewColumns = 128 << 10, kFewBehind = 1024 << 10;
 
 // Rows per M-tile, CTAs and shares of a shape; 0 CTAs if there is no device.
 AttnShape fma_shape(int es, int T, int G, int hd) {
@@ -702,11 +704,11 @@ AttnShape fma_shape(int es, int T, int G, int hd) {
 // 31.0 against 31.4 and 34.7 against 34.2; 800 thousand: 73 against 67).  So the same tokens in a
 // cache of another capacity may take the other kernel, with other roundings.
 // `columns`: an upper bound of the columns of all units.
-AttnShape attn_shape(int es, int T, int G, int hd, long long columns) {
+AttnShape attn_shape(int es, int T, int G, int hd, long long columns, bool behind = false) {
   if (es != 2 || (hd != 64 && hd != 128)) return fma_shape(es, T, G, hd);
   AttnShape s = {};
   int per_sm = 1;
-  if (T * G <= 16 || (T * G <= 32 && columns <= kFewColumns)) {
+  if (T * G <= 16 || (T * G <= 32 && columns <= (behind ? kFewBehind : kFewColumns))) {
     s.kind = kMma;
     attn_mma_shape(T * G, hd, &s.M, &s.MT, &s.tile, &per_sm);
     s.open = 3;
@@ -805,7 +807,7 @@ struct PrefixWorkspace {
 };
 PrefixWorkspace prefix_workspace(int es, int B, int T, int Hq, int G, int hd) {
   size_t own = 0, prefix = 0;  // of the kernels that the lengths may decide for
-  for (const long long columns : {0LL, kFewColumns + 1}) {
+  for (const long long columns : {0LL, kFewBehind + 1}) {
     own = std::max(own, attn_workspace(attn_shape(es, T, G, hd, columns), hd).bytes);
     prefix = std::max(prefix, attn_workspace(prefix_shape(es, static_cast<long long>(B) * T * G, hd, columns), hd).bytes);
   }
@@ -921,7 +923,7 @@ int own_pass(AttnParams p, const specdec_tree_attention_args* a, size_t room, cu
   if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
   const specdec_kv_view& c = a->cache;
   const int es = elem_size(c.dtype);
-  AttnShape s = attn_shape(es, a->T, p.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols);
+  AttnShape s = attn_shape(es, a->T, p.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols, p.prior != nullptr);
   // no more groups than the longest rows could give work to
   const long long columns = static_cast<long long>(c.cap_cols) + (both ? both->cap_cols + s.tile : 0);
   const long long tiles = static_cast<long long>(a->B) * c.heads * ((columns - 1) / s.tile + 1 + s.open);
