@@ -9,13 +9,11 @@
 //
 // A cluster holds a row in its CTAs' shared memory, read once from HBM; everything after is on chip:
 //   1. the highest score (and whether there is NaN);
-//   2. only where top-k or top-p is set: a histogram of counts over 2048 bins of z (64 an octave),
-//      each CTA's merged over the cluster by parts.  Where the tokens up to the cut are few they are listed
-//      and sorted.  Otherwise: the bin that holds a cut; its tokens, listed in every
-//      CTA and ranked by comparing all pairs.  Which bin holds top-p's cut is guessed from the counts
-//      and the bins' middles, and settled by a pass that sums what lies before and in it, which also
-//      moves the next guess: a pass or two, and no sums by atomics.  A bin of more tokens than the
-//      list has room for is split by key until it has few, or equal ones, which are counted by index;
+//   2. only where top-k or top-p is set: a histogram of the scores, each CTA's merged over the cluster by
+//      parts, and from it the bin that holds the cut.  A bf16 row has a bin for every score from 2^-8 to
+//      128 and of either sign, so that counts give the masses, and the cut is a score of which so many
+//      are kept, by index.  An fp32 row has 32 bins an octave, with the masses' sums; the cut's bin is listed
+//      in every CTA and searched there, or where it holds more than the list, split by key first;
 //   3. the kept masses' sums by warp, CTA and cluster, and in the warp that owns the draw the token.
 // Masses are fp32 exponentials, added up within a 16-byte vector and then as whole numbers of 2^-42 of
 // the highest: the sums depend on no order and no number of CTAs, so a row repeats bit for bit.
@@ -28,7 +26,8 @@ namespace specdec {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kPer = kBins / kThreads, kList = 1024, kEach = kList / kThreads;
+constexpr int kNarrow = 1024, kWide = 4096;  // bins
+constexpr int kList = 1024, kEach = kList / kThreads;
 constexpr int kMaxCluster = 16;
 constexpr int kMassBits = 42;
 constexpr long long kMaxRow = 1400 << 10;  // bytes
@@ -58,6 +57,11 @@ __device__ __forceinline__ uint32_t remote_load(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ unsigned long long remote_load64(uint32_t a) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -68,8 +72,6 @@ __device__ __forceinline__ float ex2(float x) {
 // difference of scores it is finite, or the difference is not).
 struct Scale {
   float top, sh, sl;
-  // Never falling as x falls.
-  __device__ __forceinline__ float z(float x) const { return (top - x) * sh; }
   __device__ __forceinline__ float exponent(float x) const {  // -z
     const float d = x - top;
     return fmaf(d, sh, d * sl);
@@ -77,7 +79,6 @@ struct Scale {
   // (a score of -infinity makes the exponent NaN or -infinity, either of which the maximum drops)
   __device__ __forceinline__ float mass(float x) const { return ex2(fmaxf(exponent(x), -200.f)); }
 };
-__device__ __forceinline__ int bin_of(float z) { return static_cast<int>(fminf(z * 64.f, kBins - 1.f)); }
 // A sum of masses, at most 8, as a whole number of 2^-42 (what is less is dropped).
 __device__ __forceinline__ unsigned long long whole(float v) {
   const uint32_t bits = __float_as_uint(v), e = bits >> 23;
@@ -140,19 +141,32 @@ struct Shared {
   unsigned long long slot[2][3][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
   unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kWarps];
   uint64_t bar[kWarps];
-  float warp_f[kWarps];
-  uint32_t best, listed, lo, hi;
-  uint32_t count_before, count;
-  float est_before, est;
+  unsigned long long count_before, mass_before;
+  uint32_t best, listed, count;
   int found;
 };
 
-// One thread's bins: how many tokens they hold, and of all before them how many those are and what they
-// weigh by the bins' middles.
-struct Bins {
-  uint32_t count[kPer], count_before;
-  float est_before;
-};
+// A score's place among the wide bins, which fall: scores of 128 and more; the values of bf16 (to which
+// other scores are cut off) down to 2^-8; what is nearer to zero; the values from -2^-8 to above -128; the
+// rest.  The first, the middle and the last bin hold more than one score of bf16.
+constexpr uint32_t kSmall = 119u << 7, kLarge = 134u << 7;  // upper halves of 2^-8 and 2^7
+constexpr int kValues = kLarge - kSmall, kWidePlaces = 2 * kValues + 3;
+__device__ __forceinline__ int wide_place(float x) {
+  const uint32_t bits = __float_as_uint(x), size = (bits & 0x7FFFFFFFu) >> 16;
+  const int off = static_cast<int>(min(max(size, kSmall - 1), kLarge) - kSmall);  // -1: near zero; kValues: far
+  return bits >> 31 ? kValues + 2 + off : kValues - off;
+}
+__device__ __forceinline__ int mixed(int b) { return b == 0 ? 0 : b == kValues + 1 ? 1 : b == kWidePlaces - 1 ? 2 : -1; }
+__device__ __forceinline__ float wide_score(int b) {  // of a bin of one score
+  return b <= kValues ? __uint_as_float((kSmall + kValues - b) << 16) : __uint_as_float(0x80000000u | (kSmall + b - kValues - 2) << 16);
+}
+// Keys of a bin: the highest and the lowest.
+__device__ __forceinline__ uint32_t wide_high(int b) {
+  if (b == 0) return 0xFFFFFFFFu;
+  if (b <= kValues + 1) return 0x80000000u | ((kSmall + kValues + 1 - b) << 16) - 1;
+  return ~(0x80000000u | (kSmall + b - kValues - 2) << 16);
+}
+__device__ __forceinline__ uint32_t wide_low(int b) { return b == kWidePlaces - 1 ? 0u : wide_high(b + 1) + 1; }
 
 // kCuts: whether there may be top-k or top-p.
 template <typename T, bool kCuts>
@@ -168,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
   }();
   const int r = blockIdx.x / C;
   uint4* s_x = reinterpret_cast<uint4*>(smem);
-  uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(p.pv) * 16);  // [kBins], or this CTA's list
-  uint32_t* s_all = s_hist + kBins;                                                        // merged, or the cluster's list
+  uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(p.pv) * 16);  // this CTA's counts, or lists
+  uint32_t* s_all = s_hist + kWide;                                                        // the cluster's counts
   int turn = 0;
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before the first remote store)
   auto together = [&] {
@@ -179,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
   };
   // Every CTA's values, the same in all its threads: s.slot[..][i][rank] in each.
   using Slots = const unsigned long long (*)[kMaxCluster];
-  auto gather = [&](unsigned long long a, unsigned long long b, unsigned long long c) -> Slots {
+  auto gather = [&](unsigned long long a, unsigned long long b = 0, unsigned long long c = 0) -> Slots {
     Slots got = s.slot[turn];
     if (tid < 3 * C) {
       const int i = tid / C;
@@ -275,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
   }
   if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
   {
-    const Slots all = gather(mine, gave_up, 0);
+    const Slots all = gather(mine, gave_up);
     mine = all[0][0];
     unsigned long long any = all[1][0];
     for (int i = 1; i < C; ++i) {
@@ -294,13 +308,14 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
     if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
     return;
   }
-  auto each = [&](auto f) {  // this thread's elements: f(score, index)
+  auto each = [&](auto f) {  // this thread's places: f(score, whether it is in the row)
     for (int v = v0 + lane; v < v1; v += 32) {
       float x[N];
       Vec<T>::unpack(s_x[v], x);
       const int e = index_of(v);
+      const bool full = v >= whole0 && v < whole1;
 #pragma unroll
-      for (int k = 0; k < N; ++k) f(x[k], e + k);
+      for (int k = 0; k < N; ++k) f(x[k], full || (e + k >= 0 && e + k < p.V));
     }
   };
   auto write = [&](int token, float logprob, uint32_t key, int last) {
@@ -310,16 +325,20 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
   };
   if (temperature == 0.f) {  // the first of the highest
     int at = INT32_MAX;
-    each([&](float x, int e) {
-      if (x == top) at = min(at, e);
-    });
+    for (int v = v0 + lane; v < v1; v += 32) {
+      float x[N];
+      Vec<T>::unpack(s_x[v], x);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (x[k] == top) at = min(at, index_of(v) + k);
+    }
     at = __reduce_min_sync(0xffffffffu, at);
     if (lane == 0) s.warp_b[warp] = at;
     __syncthreads();
     unsigned long long least = s.warp_b[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) least = min(least, s.warp_b[w]);
-    const Slots all = gather(least, 0, 0);
+    const Slots all = gather(least);
     for (int i = 0; i < C; ++i) least = min(least, all[0][i]);
     if (rank == 0 && tid == 0) write(static_cast<int>(least), 0.f, top_key, static_cast<int>(least));
     return;
@@ -355,521 +374,328 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
   int cut_last = INT32_MAX;
   float cut = -INFINITY;      // its score
   auto in_row = [&](int e) { return e >= 0 && e < p.V; };
-  auto is_kept = [&](float x, int e) { return x > cut || (x == cut && e <= cut_last); };
   const bool by_mass = top_p < 1.f, by_count = top_k > 0 && top_k < p.V;
   if (kCuts && (by_mass || by_count)) {
-    // Counts by place (place(x): -1 for none), merged over the cluster; middle(b): what a token of bin
-    // b weighs, roughly.
-    auto histogram = [&](auto place, auto middle) {
-      for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
+    uint32_t* all_count = s_all;                                                       // of the cluster
+    unsigned long long* all_mass = reinterpret_cast<unsigned long long*>(s_all + kNarrow);  // (not with kWide bins)
+    unsigned long long mixed_mass[3] = {0, 0, 0};  // of the wide bins that hold more than one score
+    // Counts, and with `sums` masses, of the tokens by place (-1: none), added up over the cluster.  hot: the
+    // place of the lowest scores, counted apart: masked tokens are there, perhaps nearly all.
+    auto histogram = [&](int bins, bool sums, int hot, auto place) {
+      for (int i = tid; i < bins * (sums ? 4 : 1); i += kThreads) s_hist[i] = 0;
       __syncthreads();
-      uint32_t far = 0;  // (the last place is counted apart: it may hold nearly all of a row)
-      each([&](float x, int e) {
-        const int at = in_row(e) ? place(x) : -1;
-        if (at == kBins - 1) ++far;
+      uint32_t last = 0;
+      each([&](float x, bool in) {
+        const int at = in ? place(x) : -1;
+        if (at == hot) ++last;
         else if (at >= 0) atomicAdd(&s_hist[at], 1u);
+        if (sums && at >= 0) {  // 14 bits at a time, so that 2^17 tokens' fit 32
+          const unsigned long long m = whole(sc.mass(x));
+          const uint32_t hi = static_cast<uint32_t>(m >> 28), mid = static_cast<uint32_t>(m >> 14) & 0x3FFFu, lo = static_cast<uint32_t>(m) & 0x3FFFu;
+          if (hi) atomicAdd(&s_hist[bins + at], hi);
+          if (mid) atomicAdd(&s_hist[2 * bins + at], mid);
+          if (lo) atomicAdd(&s_hist[3 * bins + at], lo);
+        }
       });
-      far = __reduce_add_sync(0xffffffffu, far);
-      if (lane == 0 && far) atomicAdd(&s_hist[kBins - 1], far);
+      last = __reduce_add_sync(0xffffffffu, last);
+      if (lane == 0 && last) atomicAdd(&s_hist[hot], last);
       together();
-      if (C > 1) {  // a CTA adds up its part of the bins over all, and tells all
-        const int part = kBins / C;
-        for (int i = tid; i < part; i += kThreads) {
-          const int b = rank * part + i;
-          uint32_t count = 0;
-          for (int c = 0; c < C; ++c) count += remote_load(cluster_map(&s_hist[b], c));
-          for (int c = 0; c < C; ++c) remote_store(cluster_map(&s_all[b], c), count);
+      // a CTA adds up its part of the bins over all, and tells all
+      const int part = bins / C;
+      for (int i = tid; i < part; i += kThreads) {
+        const int b = rank * part + i;
+        uint32_t count = 0;
+        unsigned long long mass = 0;
+        for (int c = 0; c < C; ++c) {
+          const uint32_t a = cluster_map(&s_hist[b], c);
+          count += remote_load(a);
+          if (sums)
+            mass += (static_cast<unsigned long long>(remote_load(a + 4 * bins)) << 28) +
+                    (static_cast<unsigned long long>(remote_load(a + 8 * bins)) << 14) + remote_load(a + 12 * bins);
         }
-        together();
-      }
-      Bins g;
-      uint32_t count = 0;
-      float est = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        g.count[i] = (C > 1 ? s_all : s_hist)[kPer * tid + i];
-        count += g.count[i];
-        est += static_cast<float>(g.count[i]) * middle(kPer * tid + i);
-      }
-      uint32_t ca = count;
-      float ea = est;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t oc = __shfl_up_sync(0xffffffffu, ca, d);
-        const float oe = __shfl_up_sync(0xffffffffu, ea, d);
-        if (lane >= d) {
-          ca += oc;
-          ea += oe;
+        for (int c = 0; c < C; ++c) {
+          remote_store(cluster_map(&all_count[b], c), count);
+          if (sums) remote_store(cluster_map(&all_mass[b], c), mass);
         }
       }
-      if (lane == 31) {
-        s.warp_a[warp] = ca;
-        s.warp_f[warp] = ea;
-      }
-      __syncthreads();
-      g.count_before = ca - count;
-      g.est_before = ea - est;
-      for (int w = 0; w < warp; ++w) {
-        g.count_before += static_cast<uint32_t>(s.warp_a[w]);
-        g.est_before += s.warp_f[w];
-      }
-      return g;
+      together();
     };
-    // The last bin in [lo, hi) that is not empty and begins before `tokens` tokens, or before `est`; -1
-    // if there is none.  What it holds and what comes before it are left in s.
-    auto bin_with = [&](const Bins& g, auto middle, bool mass, uint32_t tokens, float est, int lo, int hi) {
+    // The last bin that is not empty and begins before `target` tokens, or that much mass (in `wide` bins a
+    // score's mass times its count): its place; what it holds and what is before it are left in s.  With
+    // target 0 all of the mass, in s.mass_before.
+    auto bin_with = [&](int bins, bool wide, bool by_sum, unsigned long long target) {
+      const int per = bins / kThreads;
+      auto mass_in = [&](int b, uint32_t n) -> unsigned long long {
+        if (n == 0 || !by_mass) return 0;
+        if (!wide) return all_mass[b];
+        const int m = mixed(b);
+        return m < 0 ? n * whole(sc.mass(wide_score(b))) : mixed_mass[m];
+      };
+      unsigned long long count = 0, mass = 0;
+      for (int i = 0; i < per; ++i) {
+        const uint32_t n = all_count[per * tid + i];
+        count += n;
+        mass += mass_in(per * tid + i, n);
+      }
+      const unsigned long long ci = warp_scan(count), mi = warp_scan(mass);
       __syncthreads();
+      if (lane == 31) {
+        s.warp_a[warp] = ci;
+        s.warp_b[warp] = mi;
+      }
       if (tid == 0) s.best = 0;
       __syncthreads();
-      uint32_t cb = g.count_before;
-      float eb = g.est_before;
-      int at = -1;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int b = kPer * tid + i;
-        if (g.count[i] > 0 && b >= lo && b < hi && (mass ? eb < est : cb < tokens)) at = i;
-        cb += g.count[i];
-        if (mass) eb += static_cast<float>(g.count[i]) * middle(b);
+      unsigned long long cb = ci - count, mb = mi - mass;
+      for (int w = 0; w < warp; ++w) {
+        cb += s.warp_a[w];
+        mb += s.warp_b[w];
       }
-      if (at >= 0) atomicMax(&s.best, kPer * tid + at + 1);
+      if (target == 0) {
+        if (tid == kThreads - 1) s.mass_before = mb + mass;
+        __syncthreads();
+        return -1;
+      }
+      int at = -1;
+      unsigned long long c = cb, m = mb;
+      for (int i = 0; i < per; ++i) {
+        const uint32_t n = all_count[per * tid + i];
+        if (n > 0 && (by_sum ? m : c) < target) at = per * tid + i;
+        c += n;
+        m += mass_in(per * tid + i, n);
+      }
+      if (at >= 0) atomicMax(&s.best, at + 1);
       __syncthreads();
       const int best = static_cast<int>(s.best) - 1;
-      if (best >= 0 && tid == best / kPer) {
-        cb = g.count_before;
-        eb = g.est_before;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const float est_in = static_cast<float>(g.count[i]) * middle(kPer * tid + i);
-          if (kPer * tid + i == best) {
-            s.count_before = cb;
-            s.est_before = eb;
-            s.count = g.count[i];
-            s.est = est_in;
-          }
-          cb += g.count[i];
-          eb += est_in;
+      if (at == best) {
+        for (int i = per * tid; i < best; ++i) {
+          cb += all_count[i];
+          mb += mass_in(i, all_count[i]);
         }
+        s.count_before = cb;
+        s.mass_before = mb;
+        s.count = all_count[best];
       }
       __syncthreads();
       return best;
     };
-    // The bin with the cut of a target of mass, what is left of it there (in `target`), and in s what
-    // the bin holds.  kind(b) gives a test of scores: 1 before bin b (of what the histogram counted),
-    // 2 in it, 0 neither.  With `fraction` the target is that much of what is kept so far, which the
-    // first pass finds and est_total guesses.
-    auto mass_bin = [&](const Bins& g, auto middle, auto kind, float fraction, float est_total, unsigned long long& target) {
-      int lo = 0, hi = kBins, low = -1;  // low: the last bin that was found to begin before the target
-      unsigned long long low_before = 0;
-      float want = fraction > 0.f ? fraction * est_total : static_cast<float>(target) * (1.f / (1ull << kMassBits));
-      for (int round = 0; round < 48 && lo < hi; ++round) {
-        // a guess; after a few the middle (so the bounds meet within the rounds there are)
-        const int mid = lo + 1 + (hi - lo) / 2;
-        int b = round < 5 ? bin_with(g, middle, true, 0, want, lo, hi) : -1;
-        if (b < 0) b = bin_with(g, middle, true, 0, INFINITY, lo, min(mid, hi));
-        if (b < 0) {
-          lo = mid;
-          continue;
+    // The index of the want-th token of a score.
+    auto nth_equal = [&](float score, unsigned long long want) {
+      unsigned long long n = 0;
+      each([&](float x, bool in) { n += in && x == score; });
+      n = warp_sum(n);
+      __syncthreads();
+      if (lane == 0) s.warp_a[warp] = n;
+      if (tid == 0) s.found = 0;
+      __syncthreads();
+      unsigned long long before = 0, total = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? s.warp_a[w] : 0;
+        total += s.warp_a[w];
+      }
+      const Slots all = gather(total);
+      for (int i = 0; i < rank; ++i) before += all[0][i];
+      if (before < want && want <= before + n) {  // this warp has it
+        for (int vv = v0; vv < v1; vv += 32) {
+          const int v = vv + lane;
+          float x[N];
+          Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
+          const int e = index_of(v);
+          unsigned long long here = 0;
+#pragma unroll
+          for (int k = 0; k < N; ++k) here += v < v1 && in_row(e + k) && x[k] == score;
+          const unsigned long long scan = warp_scan(here);
+          unsigned long long at = before + scan - here;
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+            if (v < v1 && in_row(e + k) && x[k] == score && ++at == want) s.found = e + k + 1;
+          before += __shfl_sync(0xffffffffu, scan, 31);
         }
-        const float est_before = s.est_before;
-        const auto test = kind(b);
-        unsigned long long before = 0, in = 0, all = 0;
-        const bool first = fraction > 0.f;
+      }
+      __syncthreads();
+      const Slots who = gather(s.found);
+      unsigned long long last = 0;
+      for (int i = 0; i < C; ++i) last = max(last, who[0][i]);
+      return static_cast<int>(last) - 1;
+    };
+    auto block_sum = [&](unsigned long long v) {
+      v = warp_sum(v);
+      __syncthreads();
+      if (lane == 0) s.warp_a[warp] = v;
+      __syncthreads();
+      v = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += s.warp_a[w];
+      return v;
+    };
+
+    // The first histogram: 32 bins an octave, or for bf16 one a score.
+    constexpr bool kWideBins = sizeof(T) == 2;
+    bool first_there = false;
+    auto first = [&] {
+      if (kWideBins) {
+        unsigned long long m[4] = {0, 0, 0, 0};
+        histogram(kWide, false, kWidePlaces - 1, [&](float x) {
+          const int b = wide_place(x), k = mixed(b);
+          if (by_mass && k >= 0) {  // (few, or weighing nothing)
+            const unsigned long long w = whole(sc.mass(x));
+            m[0] += k == 0 ? w : 0;
+            m[1] += k == 1 ? w : 0;
+            m[2] += k == 2 ? w : 0;
+          }
+          return b;
+        });
+        if (by_mass) {
+          sum_all(m[0], m[1], m[2]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) mixed_mass[k] = m[k];
+        }
+      } else {
+        histogram(kNarrow, by_mass, (kWidePlaces - 1) >> 2, [&](float x) { return wide_place(x) >> 2; });
+      }
+      first_there = true;
+    };
+
+    // The cut: the last token of the order before which there are fewer than `target` tokens, or less mass.
+    // Sets cut_key, cut and cut_last; returns the mass up to and with it (where masses are counted).
+    auto find_cut = [&](bool by_sum, unsigned long long target) -> unsigned long long {
+      if (!first_there) first();
+      int b = bin_with(kWideBins ? kWide : kNarrow, kWideBins, by_sum, target);
+      uint32_t klo = kWideBins ? wide_low(b) : wide_low(min(4 * b + 3, kWidePlaces - 1)), khi = wide_high(kWideBins ? b : 4 * b);
+      bool one_score = kWideBins && mixed(b) < 0;
+      uint32_t count = s.count;
+      unsigned long long sum = s.mass_before;
+      target -= by_sum ? s.mass_before : s.count_before;
+      for (int round = 0; !one_score && klo < khi && count > kList && round < 4; ++round) {  // (each leaves a thousandth of the keys)
+        const int shift = max(0, 22 - __clz(khi - klo));
+        const uint32_t a = klo, z = khi;
+        first_there = false;
+        histogram(kNarrow, by_mass, static_cast<int>((z - a) >> shift), [&](float x) {
+          const uint32_t key = order_bits(x);
+          return key >= a && key <= z ? static_cast<int>((z - key) >> shift) : -1;
+        });
+        b = bin_with(kNarrow, false, by_sum, target);
+        khi = z - (static_cast<uint32_t>(b) << shift);
+        if (khi - a >= 1u << shift) klo = khi - ((1u << shift) - 1);
+        count = s.count;
+        sum += s.mass_before;
+        target -= by_sum ? s.mass_before : s.count_before;
+      }
+      if (one_score || klo == khi) {
+        const float score = one_score ? wide_score(b) : score_of(klo);
+        const unsigned long long one = by_mass ? whole(sc.mass(score)) : 0;
+        const unsigned long long want = !by_sum ? target : one == 0 ? count : min(static_cast<unsigned long long>(count), (target + one - 1) / one);
+        cut_key = order_bits(score);
+        cut = score;
+        cut_last = want >= count ? INT32_MAX : nth_equal(score, want);
+        return sum + want * one;
+      }
+      // this CTA's tokens in question, then everyone's in every CTA, in order of rank
+      unsigned long long *l_list = reinterpret_cast<unsigned long long*>(s_hist), *list = l_list + kList;
+      together();  // all are done with the histograms
+      if (tid == 0) s.listed = 0;
+      __syncthreads();
+      {
+        const uint32_t a = klo, z = khi;
         for (int v = v0 + lane; v < v1; v += 32) {
           float x[N];
           Vec<T>::unpack(s_x[v], x);
-          float vb = 0.f, vi = 0.f, va = 0.f;
           const int e = index_of(v);
 #pragma unroll
-          for (int k = 0; k < N; ++k) {  // (places outside the row weigh nothing)
-            const float m = sc.mass(x[k]);
-            const int c = test(x[k]);
-            vb += c == 1 ? m : 0.f;
-            vi += c == 2 ? m : 0.f;
-            if (first) va += is_kept(x[k], e + k) ? m : 0.f;
+          for (int k = 0; k < N; ++k) {
+            const uint32_t key = order_bits(x[k]);
+            if (key >= a && key <= z && in_row(e + k)) l_list[atomicAdd(&s.listed, 1u)] = static_cast<unsigned long long>(key) << 32 | static_cast<uint32_t>(e + k);
           }
-          before += whole(vb);
-          in += whole(vi);
-          all += whole(va);
         }
-        sum_all(before, in, all);
-        if (first) {
-          target = max(1ull, times(fraction, all, true));
-          fraction = 0.f;
-        }
-        if (before >= target) {
-          hi = b;
-        } else {
-          low = b;
-          low_before = before;
-          if (target <= before + in) break;
-          lo = b + 1;  // (where rounding has put the target between two bins, the earlier one is taken whole)
-        }
-        // the next guess: as much further as the target is from what has been summed
-        want = est_before + (static_cast<float>(target) - static_cast<float>(before)) * (1.f / (1ull << kMassBits));
       }
-      (void)bin_with(g, middle, true, 0, INFINITY, low, low + 1);  // (the last one tried may be another)
-      target -= low_before;
-      return low;
+      __syncthreads();
+      const Slots all = gather(s.listed);
+      int n = 0;
+      for (int c = 0; c < C; ++c) {
+        const int m = static_cast<int>(all[0][c]);
+        for (int i = tid; i < m; i += kThreads) list[n + i] = remote_load64(cluster_map(&l_list[i], c));
+        n += m;
+      }
+      __syncthreads();
+      uint32_t key[kEach];
+      int index[kEach];
+      unsigned long long weight[kEach], mass[kEach];  // what is counted, and the mass
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const bool have = kThreads * i + tid < n;
+        const unsigned long long t = have ? list[kThreads * i + tid] : 0;
+        key[i] = static_cast<uint32_t>(t >> 32);
+        index[i] = static_cast<int>(t);
+        mass[i] = have && by_mass ? whole(sc.mass(score_of(key[i]))) : 0;
+        weight[i] = by_sum ? mass[i] : have ? 1 : 0;
+      }
+      // the least key before which (among larger ones) there is less than the target, then the index
+      uint32_t k0 = klo, k1 = khi;
+      while (k0 < k1) {
+        const uint32_t mid = k0 + (k1 - k0) / 2;
+        unsigned long long v = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v += key[i] > mid ? weight[i] : 0;
+        if (block_sum(v) < target) k1 = mid;
+        else k0 = mid + 1;
+      }
+      // (that may be a key below the last kept one where nothing is between: the least that is there)
+      uint32_t least = 0xFFFFFFFFu;
+      unsigned long long larger = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (key[i] >= k1 && kThreads * i + tid < n) least = min(least, key[i]);
+        larger += key[i] > k1 ? weight[i] : 0;
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      __syncthreads();
+      if (lane == 0) s.warp_b[warp] = least;
+      larger = block_sum(larger);
+      for (int w = 0; w < kWarps; ++w) least = min(least, static_cast<uint32_t>(s.warp_b[w]));
+      unsigned long long equal = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) equal += key[i] == least && kThreads * i + tid < n ? 1 : 0;
+      equal = block_sum(equal);
+      int i0 = 0, i1 = p.V - 1;  // the last kept index: the largest before which there is less than the target
+      if (equal == 1 || least > k1) i0 = i1;
+      while (i0 < i1) {
+        const int mid = i0 + (i1 - i0 + 1) / 2;
+        unsigned long long v = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v += key[i] == least && index[i] < mid ? weight[i] : 0;
+        if (larger + block_sum(v) < target) i0 = mid;
+        else i1 = mid - 1;
+      }
+      unsigned long long in = 0;
+      int last = -1;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const bool kept = kThreads * i + tid < n && (key[i] > least || (key[i] == least && index[i] <= i0));
+        in += kept ? mass[i] : 0;
+        if (kept && key[i] == least) last = max(last, index[i]);
+      }
+      last = __reduce_max_sync(0xffffffffu, last);
+      __syncthreads();
+      if (lane == 0) s.warp_b[warp] = static_cast<unsigned long long>(last + 1);
+      in = block_sum(in);
+      for (int w = 0; w < kWarps; ++w) last = max(last, static_cast<int>(s.warp_b[w]) - 1);
+      together();  // the lists may be written again
+      cut_key = least;
+      cut = score_of(least);
+      cut_last = last;
+      return sum + in;
     };
-    auto middle = [](int b) { return ex2((b + 0.5f) * (-1.f / 64)); };
-    const Bins bins = histogram([&](float x) { return bin_of(sc.z(x)); }, middle);
-
-    // Most settings keep few tokens.  Where the bins up to the cut's hold no more than the list, one pass
-    // counts them (and, for top-p alone, sums the row), another sends them to the first CTA in order of
-    // index, and that does the rest.  For top-p the bin is guessed from the bins' middles (2 % beyond
-    // what they say); the listed mass shows whether it was far enough.
-    (void)bin_with(bins, middle, true, 0, INFINITY, 0, kBins);
-    float est_kept = s.est_before + s.est;
-    const int enough = by_count ? bin_with(bins, middle, false, top_k, 0.f, 0, kBins) : bin_with(bins, middle, true, 0, 1.02f * top_p * est_kept, 0, kBins);
-    const uint32_t count_before = s.count_before;
-    if (count_before + s.count <= kList) {
-      unsigned long long* list = reinterpret_cast<unsigned long long*>(s_all);  // (key, ~index): larger is earlier in the order
-      unsigned long long* few = reinterpret_cast<unsigned long long*>(s_hist);
-      unsigned long long total = 0, in_list = 0, listed = 0;
-      const bool alone = !by_count;
-      auto takes = [&](float x, int e) { return in_row(e) && bin_of(sc.z(x)) <= enough; };
-      for (int v = v0 + lane; v < v1; v += 32) {
-        float x[N];
-        Vec<T>::unpack(s_x[v], x);
-        const int e = index_of(v);
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const float m = alone ? sc.mass(x[k]) : 0.f;
-          sum += m;
-          if (takes(x[k], e + k)) {
-            ++listed;
-            if (alone) in_list += whole(m);
-          }
-        }
-        if (alone) total += whole(sum);
+    unsigned long long kept = 0;
+    if (by_count) kept = find_cut(false, top_k);
+    if (by_mass) {
+      if (!by_count) {
+        first();
+        (void)bin_with(kWideBins ? kWide : kNarrow, kWideBins, true, 0);
+        kept = s.mass_before;
       }
-      const unsigned long long in_warp = warp_sum(listed);
-      sum_all(total, in_list, listed);
-      // where this warp's begin: its CTA's are those of the sums before
-      unsigned long long to = 0, cta = 0;
-      __syncthreads();
-      if (lane == 0) s.warp_a[warp] = in_warp;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        to += w < warp ? s.warp_a[w] : 0;
-        cta += s.warp_a[w];
-      }
-      const unsigned long long target = alone ? max(1ull, times(top_p, total, true)) : 0;
-      if (in_list >= target) {
-        const Slots all = gather(cta, 0, 0);  // (and all are done with the histograms)
-        for (int i = 0; i < rank; ++i) to += all[0][i];
-        if (in_warp > 0) {
-          const uint32_t first = cluster_map(list, 0);
-          for (int vv = v0; vv < v1; vv += 32) {
-            const int v = vv + lane;
-            float x[N];
-            Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
-            const int e = index_of(v);
-            uint32_t has = 0;
-#pragma unroll
-            for (int k = 0; k < N; ++k) has |= v < v1 && takes(x[k], e + k) ? 1u << k : 0;
-            if (!__any_sync(0xffffffffu, has != 0)) continue;
-            const uint32_t here = __popc(has), scan = static_cast<uint32_t>(warp_scan(here));
-            uint32_t at = static_cast<uint32_t>(to) + scan - here;
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-              if (has >> k & 1)
-                remote_store(first + 8 * at++, static_cast<unsigned long long>(order_bits(x[k])) << 32 | ~static_cast<uint32_t>(e + k));
-            to += __shfl_sync(0xffffffffu, scan, 31);
-          }
-        }
-        together();
-        if (rank != 0) return;
-        // ------------------------------------------------------------- one CTA from here on
-        const int n = static_cast<int>(listed);
-        unsigned long long token[kEach], mass[kEach];  // consecutive ones of the list (0: none)
-        int bin[kEach];
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          token[i] = kEach * tid + i < n ? list[kEach * tid + i] : 0;
-          const float x = token[i] ? score_of(static_cast<uint32_t>(token[i] >> 32)) : -INFINITY;
-          mass[i] = token[i] ? whole(sc.mass(x)) : 0;
-          bin[i] = token[i] ? bin_of(sc.z(x)) : kBins;
-        }
-        auto block_sum = [&](unsigned long long v) {
-          v = warp_sum(v);
-          __syncthreads();
-          if (lane == 0) s.warp_a[warp] = v;
-          __syncthreads();
-          v = 0;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) v += s.warp_a[w];
-          return v;
-        };
-        // The last token of bin b before which, in the bin, there are fewer than `left` tokens, or less mass.
-        auto last_in = [&](int b, bool by_sum, unsigned long long left) {
-          __syncthreads();
-          if (tid == 0) s.listed = s.best = 0;
-          __syncthreads();
-#pragma unroll
-          for (int i = 0; i < kEach; ++i)
-            if (bin[i] == b) few[atomicAdd(&s.listed, 1u)] = token[i];
-          __syncthreads();
-          const int m = static_cast<int>(s.listed);
-          for (int i = warp; i < m; i += kWarps) {
-            const unsigned long long me = few[i];
-            uint32_t tokens = 0;
-            unsigned long long sum = 0;
-            for (int j = lane; j < m; j += 32)
-              if (few[j] > me) {
-                ++tokens;
-                if (by_sum) sum += whole(sc.mass(score_of(static_cast<uint32_t>(few[j] >> 32))));
-              }
-            tokens = __reduce_add_sync(0xffffffffu, tokens);
-            if (by_sum) sum = warp_sum(sum);
-            if (lane == 0 && (by_sum ? sum : tokens) < left) atomicMax(&s.best, tokens << 16 | (i + 1));
-          }
-          __syncthreads();
-          return m ? few[max(0, static_cast<int>(s.best & 0xFFFF) - 1)] : 0ull;
-        };
-        unsigned long long end = 0;  // the last that is kept
-        if (by_count) end = last_in(enough, false, top_k - count_before);
-        if (by_mass) {
-          unsigned long long own = 0;
-          if (by_count) {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) own += token[i] >= end ? mass[i] : 0;
-            own = block_sum(own);
-          }
-          const unsigned long long below = by_count ? max(1ull, times(top_p, own, true)) : target;
-          // the last bin that begins before `below`
-          int lo = 0, hi = enough + 1;
-          unsigned long long at_lo = 0;
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            unsigned long long v = 0;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) v += bin[i] < mid ? mass[i] : 0;
-            v = block_sum(v);
-            if (v < below) {
-              lo = mid;
-              at_lo = v;
-            } else {
-              hi = mid;
-            }
-          }
-          end = max(end, last_in(lo, true, below - at_lo));
-        }
-        uint32_t end_key = static_cast<uint32_t>(end >> 32);
-        int end_index = static_cast<int>(~static_cast<uint32_t>(end));
-        if (min_p > 0.f) {
-          const uint32_t least = min_p_key();
-          if (least > end_key) {
-            end = static_cast<unsigned long long>(least) << 32;
-            end_key = least;
-            end_index = INT32_MAX;
-          }
-        }
-        // the draw, in order of index
-        unsigned long long own = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) own += token[i] >= end ? mass[i] : 0;
-        const unsigned long long inc = warp_scan(own);
-        __syncthreads();
-        if (lane == 31) s.warp_a[warp] = inc;
-        __syncthreads();
-        unsigned long long at = inc - own, sum = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          at += w < warp ? s.warp_a[w] : 0;
-          sum += s.warp_a[w];
-        }
-        const unsigned long long want = times(u, sum, false);
-        if (want < at || want >= at + own) return;
-        bool got = false;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          at += token[i] >= end ? mass[i] : 0;
-          if (!got && at > want) {
-            got = true;
-            finish(static_cast<int>(~static_cast<uint32_t>(token[i])), score_of(static_cast<uint32_t>(token[i] >> 32)), sum, end_key, end_index);
-          }
-        }
-        return;
-      }
+      (void)find_cut(true, max(1ull, times(top_p, kept, true)));
     }
-
-    // The cut: the last token of the order before which there are fewer than `target` tokens, or less
-    // than `fraction` of the mass kept so far.  Sets cut_key, cut and cut_last.
-    auto find_cut = [&](bool mass, unsigned long long target, float fraction) {
-      int bin;
-      if (mass) {
-        bin = mass_bin(bins, middle, [&](int b) {
-          return [&sc, b](float x) {
-            const float z = sc.z(x) * 64.f;
-            return z < b ? 1 : (z < b + 1 || b == kBins - 1 ? 2 : 0);
-          };
-        }, fraction, est_kept, target);
-      } else {
-        bin = bin_with(bins, middle, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
-        target -= s.count_before;
-        est_kept = s.est_before + s.est;
-      }
-      uint32_t count = s.count, klo = 0, khi = 0;
-      bool by_key = false;
-      auto inside = [&](float x) {
-        const uint32_t key = order_bits(x);
-        return by_key ? key >= klo && key <= khi : bin_of(sc.z(x)) == bin;
-      };
-      for (int round = 0; count > kList && round < 8; ++round) {  // (each leaves a two-thousandth of the keys)
-        __syncthreads();
-        if (tid == 0) {
-          s.lo = 0xFFFFFFFFu;
-          s.hi = 0;
-        }
-        __syncthreads();
-        uint32_t lo = 0xFFFFFFFFu, hi = 0;
-        each([&](float x, int e) {
-          if (in_row(e) && inside(x)) {
-            lo = min(lo, order_bits(x));
-            hi = max(hi, order_bits(x));
-          }
-        });
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        if (lane == 0) {
-          atomicMin(&s.lo, lo);
-          atomicMax(&s.hi, hi);
-        }
-        __syncthreads();
-        const Slots all = gather(s.lo, s.hi, 0);
-        klo = 0xFFFFFFFFu;
-        khi = 0;
-        for (int i = 0; i < C; ++i) {
-          klo = min(klo, static_cast<uint32_t>(all[0][i]));
-          khi = max(khi, static_cast<uint32_t>(all[1][i]));
-        }
-        by_key = true;
-        if (klo == khi) break;
-        const int shift = max(0, 21 - __clz(khi - klo));
-        const uint32_t a = klo, z = khi;
-        auto first_of = [=](int b) { return z - (static_cast<uint32_t>(b) << shift); };  // a bin's highest key
-        auto middle = [&](int b) { return b <= static_cast<int>((z - a) >> shift) ? sc.mass(score_of(max(a, first_of(b)))) : 0.f; };
-        const Bins g = histogram([&](float x) { return inside(x) ? static_cast<int>((z - order_bits(x)) >> shift) : -1; }, middle);
-        int at;
-        if (mass) {
-          at = mass_bin(g, middle, [&](int b) {
-            const uint32_t h = first_of(b);
-            return [=](float x) {
-              const uint32_t key = order_bits(x);
-              return key > z || key < a ? 0 : key > h ? 1 : h - key < (1u << shift) ? 2 : 0;
-            };
-          }, 0.f, 0.f, target);
-        } else {
-          at = bin_with(g, middle, false, static_cast<uint32_t>(target), 0.f, 0, kBins);
-          target -= s.count_before;
-        }
-        count = s.count;
-        khi = first_of(at);
-        if (khi - klo >= 1u << shift) klo = khi - ((1u << shift) - 1);
-      }
-      if (count > kList) {
-        // equal scores: the last one by index
-        const uint32_t key = klo;
-        const float score = score_of(key);
-        const unsigned long long one = whole(sc.mass(score));
-        const unsigned long long want = !mass ? target : one == 0 ? count : min(static_cast<unsigned long long>(count), (target + one - 1) / one);
-        unsigned long long n = 0;
-        each([&](float x, int e) { n += in_row(e) && x == score; });
-        n = warp_sum(n);
-        __syncthreads();
-        if (lane == 0) s.warp_a[warp] = n;
-        if (tid == 0) s.found = 0;
-        __syncthreads();
-        unsigned long long before = 0, total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-          before += w < warp ? s.warp_a[w] : 0;
-          total += s.warp_a[w];
-        }
-        const Slots all = gather(total, 0, 0);
-        for (int i = 0; i < rank; ++i) before += all[0][i];
-        if (before < want && want <= before + n) {  // this warp has it
-          for (int vv = v0; vv < v1; vv += 32) {
-            const int v = vv + lane;
-            float x[N];
-            Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
-            const int e = index_of(v);
-            unsigned long long here = 0;
-#pragma unroll
-            for (int k = 0; k < N; ++k) here += v < v1 && in_row(e + k) && x[k] == score;
-            const unsigned long long scan = warp_scan(here);
-            unsigned long long at = before + scan - here;
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-              if (v < v1 && in_row(e + k) && x[k] == score && ++at == want) s.found = e + k + 1;
-            before += __shfl_sync(0xffffffffu, scan, 31);
-          }
-        }
-        __syncthreads();
-        const Slots who = gather(s.found, 0, 0);
-        unsigned long long last = 0;
-        for (int i = 0; i < C; ++i) last = max(last, who[0][i]);
-        cut_key = key;
-        cut_last = static_cast<int>(last) - 1;
-      } else {
-        // this CTA's tokens in question, then everyone's in every CTA, in order of rank
-        uint32_t *l_key = s_hist, *l_index = s_hist + kList, *a_key = s_all, *a_index = s_all + kList;
-        together();  // all are done with the histograms
-        if (tid == 0) {
-          s.listed = 0;
-          s.best = 0;
-        }
-        __syncthreads();
-        each([&](float x, int e) {
-          if (in_row(e) && inside(x)) {
-            const uint32_t i = atomicAdd(&s.listed, 1u);
-            l_key[i] = order_bits(x);
-            l_index[i] = e;
-          }
-        });
-        __syncthreads();
-        const Slots all = gather(s.listed, 0, 0);
-        int n = 0;
-        for (int c = 0; c < C; ++c) {
-          const int m = static_cast<int>(all[0][c]);
-          for (int i = tid; i < 2 * m; i += kThreads) {
-            const int f = i >= m ? 1 : 0, j = i - f * m;
-            s_all[f * kList + n + j] = remote_load(cluster_map(&s_hist[f * kList + j], c));
-          }
-          n += m;
-        }
-        __syncthreads();
-        // a warp ranks a token: what is before it, and whether it is kept
-        for (int i = rank * kWarps + warp; i < n; i += C * kWarps) {
-          const unsigned long long me = static_cast<unsigned long long>(a_key[i]) << 32 | ~a_index[i];
-          uint32_t tokens = 0;
-          unsigned long long sum = 0;
-          for (int j = lane; j < n; j += 32) {
-            const uint32_t key = a_key[j];
-            if ((static_cast<unsigned long long>(key) << 32 | ~a_index[j]) > me) {
-              ++tokens;
-              if (mass) sum += whole(sc.mass(score_of(key)));
-            }
-          }
-          tokens = __reduce_add_sync(0xffffffffu, tokens);
-          if (mass) sum = warp_sum(sum);
-          if (lane == 0 && (mass ? sum : tokens) < target) atomicMax(&s.best, tokens << 16 | (i + 1));
-        }
-        __syncthreads();
-        const Slots who = gather(s.best, 0, 0);  // (and the lists may be written again)
-        unsigned long long best = 0;
-        for (int i = 0; i < C; ++i) best = max(best, who[0][i]);
-        const int at = max(0, static_cast<int>(best & 0xFFFF) - 1);  // (the first token is always kept)
-        cut_key = a_key[at];
-        cut_last = static_cast<int>(a_index[at]);
-      }
-      cut = score_of(cut_key);
-    };
-    if (by_count) find_cut(false, top_k, 0.f);
-    if (by_mass) find_cut(true, 0, top_p);
   }
+  auto is_kept = [&](float x, int e) { return x > cut || (x == cut && e <= cut_last); };
   if (min_p > 0.f) {
     const uint32_t key = min_p_key();
     if (key > cut_key) {
@@ -896,9 +722,19 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
   unsigned long long sum = 0;
   if (cuts) {
     for (int v = v0 + lane; v < v1; v += 32) {
-      float m[N], x[N];
-      running(v, m, x);
-      sum += whole(m[N - 1]);
+      float x[N], vector = 0.f;
+      Vec<T>::unpack(s_x[v], x);
+      const int e = index_of(v);
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < N; ++k) any |= x[k] >= cut;
+      if (!any) continue;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float mass = sc.mass(x[k]);
+        vector += is_kept(x[k], e + k) ? mass : 0.f;
+      }
+      sum += whole(vector);
     }
   } else {
 #pragma unroll 4
@@ -919,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
     before += w < warp ? s.warp_a[w] : 0;
     cta += s.warp_a[w];
   }
-  const Slots all = gather(cta, 0, 0);
+  const Slots all = gather(cta);
   unsigned long long total = 0;
   for (int i = 0; i < C; ++i) {
     before += i < rank ? all[0][i] : 0;
@@ -959,12 +795,12 @@ template <typename T>
 int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
   const int vectors = (p.V + 2 * N - 2) / N;  // whatever the row's alignment
-  const size_t extra = p.top_k || p.top_p ? 2 * kBins * 4 : 0;
+  const size_t extra = p.top_k || p.top_p ? 2 * kWide * 4 : 0;
   constexpr size_t kRoom = 200 << 10;
   const int sms = std::max(1, sm_count());
   // CTAs that an SM holds at once, and of a row: what its scores need, then more while all rows' run at once
   auto bytes = [&](int c) { return static_cast<size_t>((vectors - 1) / c + 1) * 16 + extra; };
-  auto resident = [&](int c) { return std::min<long long>(4, (220 << 10) / (bytes(c) + (2 << 10))) * sms; };
+  auto resident = [&](int c) { return std::min<long long>(extra ? 3 : 4, (220 << 10) / (bytes(c) + (2 << 10))) * sms; };
   int C = 1;
   while (C < kMaxCluster && (bytes(C) > (112 << 10) || (R * 2LL * C <= resident(2 * C) && vectors > C * 256))) C *= 2;
   p.pv = (vectors - 1) / C + 1;
