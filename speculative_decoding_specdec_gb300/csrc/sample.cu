@@ -25,9 +25,9 @@
 namespace specdec {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kNarrow = 1024, kWide = 4096;  // bins
-constexpr int kList = 1024, kEach = kList / kThreads;
+constexpr int kList = 1024;
+constexpr int kMaxWarps = 16;
 constexpr int kMaxCluster = 16;
 constexpr int kMassBits = 42;
 constexpr long long kMaxRow = 1400 << 10;  // bytes
@@ -139,11 +139,11 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) { 
 
 struct Shared {
   unsigned long long slot[2][3][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
-  unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kWarps];
-  uint64_t bar[kWarps];
+  unsigned long long warp_a[kMaxWarps], warp_b[kMaxWarps], warp_c[kMaxWarps];
+  uint64_t bar[kMaxWarps];
   unsigned long long count_before, mass_before;
-  uint32_t best, listed, count;
-  int found;
+  uint32_t listed, count;
+  int bin, found;
 };
 
 // A score's place among the wide bins, which fall: scores of 128 and more; the values of bf16 (to which
@@ -169,8 +169,9 @@ __device__ __forceinline__ uint32_t wide_high(int b) {
 __device__ __forceinline__ uint32_t wide_low(int b) { return b == kWidePlaces - 1 ? 0u : wide_high(b + 1) + 1; }
 
 // kCuts: whether there may be top-k or top-p.
-template <typename T, bool kCuts>
-__global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const SampleParams p) {
+template <typename T, bool kCuts, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleParams p) {
+  constexpr int kWarps = kThreads / 32, kEach = kList / kThreads;
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) char smem[];
   __shared__ Shared s;
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
     return;
   }
   auto each = [&](auto f) {  // this thread's places: f(score, whether it is in the row)
+#pragma unroll 2
     for (int v = v0 + lane; v < v1; v += 32) {
       float x[N];
       Vec<T>::unpack(s_x[v], x);
@@ -421,62 +423,69 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
       together();
     };
     // The last bin that is not empty and begins before `target` tokens, or that much mass (in `wide` bins a
-    // score's mass times its count): its place; what it holds and what is before it are left in s.  With
-    // target 0 all of the mass, in s.mass_before.
+    // score's mass times its count): it, what it holds and what is before it are left in s.  With target 0
+    // all of the mass, in s.mass_before.
     auto bin_with = [&](int bins, bool wide, bool by_sum, unsigned long long target) {
-      const int per = bins / kThreads;
       auto mass_in = [&](int b, uint32_t n) -> unsigned long long {
         if (n == 0 || !by_mass) return 0;
         if (!wide) return all_mass[b];
         const int m = mixed(b);
-        return m < 0 ? n * whole(sc.mass(wide_score(b))) : mixed_mass[m];
+        return m < 0 ? n * whole(sc.mass(wide_score(b))) : m == 0 ? mixed_mass[0] : m == 1 ? mixed_mass[1] : mixed_mass[2];
       };
-      unsigned long long count = 0, mass = 0;
-      for (int i = 0; i < per; ++i) {
-        const uint32_t n = all_count[per * tid + i];
+      // a warp has neighbouring bins, of which a lane has every 32nd
+      const int per = bins / kWarps, b0 = warp * per + lane;
+      uint32_t count = 0;
+      unsigned long long mass = 0;
+#pragma unroll 4
+      for (int i = 0; i < per; i += 32) {
+        const uint32_t n = all_count[b0 + i];
         count += n;
-        mass += mass_in(per * tid + i, n);
+        mass += mass_in(b0 + i, n);
       }
-      const unsigned long long ci = warp_scan(count), mi = warp_scan(mass);
+      count = __reduce_add_sync(0xffffffffu, count);
+      mass = warp_sum(mass);
       __syncthreads();
-      if (lane == 31) {
-        s.warp_a[warp] = ci;
-        s.warp_b[warp] = mi;
+      if (lane == 0) {
+        s.warp_a[warp] = count;
+        s.warp_b[warp] = mass;
       }
-      if (tid == 0) s.best = 0;
       __syncthreads();
-      unsigned long long cb = ci - count, mb = mi - mass;
-      for (int w = 0; w < warp; ++w) {
-        cb += s.warp_a[w];
-        mb += s.warp_b[w];
+      unsigned long long cb = 0, mb = 0, c_at = 0, m_at = 0;
+      int owner = 0;  // the last warp with tokens that begins before the target
+      for (int w = 0; w < kWarps; ++w) {
+        const unsigned long long c = s.warp_a[w], m = s.warp_b[w];
+        if (c > 0 && (by_sum ? mb : cb) < target) {
+          owner = w;
+          c_at = cb;
+          m_at = mb;
+        }
+        cb += c;
+        mb += m;
       }
       if (target == 0) {
-        if (tid == kThreads - 1) s.mass_before = mb + mass;
+        if (tid == 0) s.mass_before = mb;
         __syncthreads();
-        return -1;
+        return;
       }
-      int at = -1;
-      unsigned long long c = cb, m = mb;
-      for (int i = 0; i < per; ++i) {
-        const uint32_t n = all_count[per * tid + i];
-        if (n > 0 && (by_sum ? m : c) < target) at = per * tid + i;
-        c += n;
-        m += mass_in(per * tid + i, n);
-      }
-      if (at >= 0) atomicMax(&s.best, at + 1);
-      __syncthreads();
-      const int best = static_cast<int>(s.best) - 1;
-      if (at == best) {
-        for (int i = per * tid; i < best; ++i) {
-          cb += all_count[i];
-          mb += mass_in(i, all_count[i]);
+      if (warp == owner) {
+        for (int i = 0; i < per; i += 32) {
+          const uint32_t n = all_count[b0 + i];
+          const unsigned long long m = mass_in(b0 + i, n), ci = warp_scan(n), mi = warp_scan(m);
+          const unsigned long long c0 = c_at + ci - n, m0 = m_at + mi - m;
+          const uint32_t could = __ballot_sync(0xffffffffu, n > 0 && (by_sum ? m0 : c0) < target);
+          if (could && lane == 31 - __clz(could)) {  // (a later one takes its place)
+            s.bin = b0 + i;
+            s.count_before = c0;
+            s.mass_before = m0;
+            s.count = n;
+          }
+          c_at += __shfl_sync(0xffffffffu, ci, 31);
+          m_at += __shfl_sync(0xffffffffu, mi, 31);
+          if ((by_sum ? m_at : c_at) >= target) break;
+          __syncwarp();
         }
-        s.count_before = cb;
-        s.mass_before = mb;
-        s.count = all_count[best];
       }
       __syncthreads();
-      return best;
     };
     // The index of the want-th token of a score.
     auto nth_equal = [&](float score, unsigned long long want) {
@@ -559,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
     // Sets cut_key, cut and cut_last; returns the mass up to and with it (where masses are counted).
     auto find_cut = [&](bool by_sum, unsigned long long target) -> unsigned long long {
       if (!first_there) first();
-      int b = bin_with(kWideBins ? kWide : kNarrow, kWideBins, by_sum, target);
+      bin_with(kWideBins ? kWide : kNarrow, kWideBins, by_sum, target);
+      int b = s.bin;
       uint32_t klo = kWideBins ? wide_low(b) : wide_low(min(4 * b + 3, kWidePlaces - 1)), khi = wide_high(kWideBins ? b : 4 * b);
       bool one_score = kWideBins && mixed(b) < 0;
       uint32_t count = s.count;
@@ -573,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
           const uint32_t key = order_bits(x);
           return key >= a && key <= z ? static_cast<int>((z - key) >> shift) : -1;
         });
-        b = bin_with(kNarrow, false, by_sum, target);
+        bin_with(kNarrow, false, by_sum, target);
+        b = s.bin;
         khi = z - (static_cast<uint32_t>(b) << shift);
         if (khi - a >= 1u << shift) klo = khi - ((1u << shift) - 1);
         count = s.count;
@@ -689,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
     if (by_mass) {
       if (!by_count) {
         first();
-        (void)bin_with(kWideBins ? kWide : kNarrow, kWideBins, true, 0);
+        bin_with(kWideBins ? kWide : kNarrow, kWideBins, true, 0);
         kept = s.mass_before;
       }
       (void)find_cut(true, max(1ull, times(top_p, kept, true)));
@@ -791,6 +802,9 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 3 : 4) sample_kernel(const S
   }
 }
 
+// Threads of a CTA: few where the draw alone is to be made, which leaves each of them little to do.
+constexpr int kCutThreads = 512, kDrawThreads = 256;
+
 template <typename T>
 int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
@@ -800,13 +814,13 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   const int sms = std::max(1, sm_count());
   // CTAs that an SM holds at once, and of a row: what its scores need, then more while all rows' run at once
   auto bytes = [&](int c) { return static_cast<size_t>((vectors - 1) / c + 1) * 16 + extra; };
-  auto resident = [&](int c) { return std::min<long long>(extra ? 3 : 4, (220 << 10) / (bytes(c) + (2 << 10))) * sms; };
+  auto resident = [&](int c) { return std::min<long long>(extra ? 2 : 4, (220 << 10) / (bytes(c) + (2 << 10))) * sms; };
   int C = 1;
   while (C < kMaxCluster && (bytes(C) > (112 << 10) || (R * 2LL * C <= resident(2 * C) && vectors > C * 256))) C *= 2;
   p.pv = (vectors - 1) / C + 1;
   const size_t smem = static_cast<size_t>(p.pv) * 16 + extra;
   if (smem > kRoom) return SPECDEC_ERR_UNSUPPORTED;
-  auto kernel = extra ? sample_kernel<T, true> : sample_kernel<T, false>;
+  auto kernel = extra ? sample_kernel<T, true, kCutThreads> : sample_kernel<T, false, kDrawThreads>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRoom));
   if (e != cudaSuccess) return map_cuda_error(e);
   if (C > 8) {
@@ -819,7 +833,7 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(R * C);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(extra ? kCutThreads : kDrawThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
