@@ -57,11 +57,6 @@ __device__ __forceinline__ uint32_t remote_load(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ unsigned long long remote_load64(uint32_t a) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -122,10 +117,12 @@ __device__ __forceinline__ unsigned long long times(float f, unsigned long long 
   return q + (up && rest ? 1 : 0);
 }
 
+// (in three parts of 26 bits, whose sums of 32 fit: three instructions in the place of ten shuffles)
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
+  const uint32_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0x3FFFFFFu),
+                 b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 26) & 0x3FFFFFFu),
+                 c = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 52));
+  return a + (static_cast<unsigned long long>(b) << 26) + (static_cast<unsigned long long>(c) << 52);
 }
 __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) {  // inclusive
   const int lane = threadIdx.x & 31;
@@ -320,10 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       for (int k = 0; k < N; ++k) f(x[k], full || (e + k >= 0 && e + k < p.V));
     }
   };
-  auto write = [&](int token, float logprob, uint32_t key, int last) {
+  auto write = [&](int token, float logprob) {
     p.token[r] = token;
     if (p.logprob) p.logprob[r] = logprob;
-    if (p.bounds) p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{key, last};
   };
   if (temperature == 0.f) {  // the first of the highest
     int at = INT32_MAX;
@@ -342,7 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     for (int w = 1; w < kWarps; ++w) least = min(least, s.warp_b[w]);
     const Slots all = gather(least);
     for (int i = 0; i < C; ++i) least = min(least, all[0][i]);
-    if (rank == 0 && tid == 0) write(static_cast<int>(least), 0.f, top_key, static_cast<int>(least));
+    if (rank == 0 && tid == 0) {
+      write(static_cast<int>(least), 0.f);
+      if (p.bounds) p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{top_key, static_cast<int>(least)};
+    }
     return;
   }
   Scale sc;
@@ -365,16 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     return min(key, top_key);
   };
   // The drawn token, of a sum of kept masses.
-  auto finish = [&](int token, float score, unsigned long long total, uint32_t key, int last) {
+  auto finish = [&](int token, float score, unsigned long long total) {
     // the highest mass is 1 and among the kept: the sum's logarithm from what it is above 1
     const float above = static_cast<float>(total - (1ull << kMassBits)) * (1.f / (1ull << kMassBits));
-    write(token, fmaf(sc.exponent(score), 0.693147181f, -log1pf(above)), key, last);
+    write(token, fmaf(sc.exponent(score), 0.693147181f, -log1pf(above)));
   };
 
   // ---------------------------------------------------------------------- the cuts
-  uint32_t cut_key = 0;       // kept: a larger key, or this one up to index cut_last
-  int cut_last = INT32_MAX;
-  float cut = -INFINITY;      // its score
+  uint32_t cut_key = 0;        // kept: a larger key, and the first `ties` tokens of this one
+  uint32_t ties = 0xFFFFFFFFu;  // (all)
+  float cut = -INFINITY;       // its score
   auto in_row = [&](int e) { return e >= 0 && e < p.V; };
   const bool by_mass = top_p < 1.f, by_count = top_k > 0 && top_k < p.V;
   if (kCuts && (by_mass || by_count)) {
@@ -408,12 +407,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         const int b = rank * part + i;
         uint32_t count = 0;
         unsigned long long mass = 0;
-        for (int c = 0; c < C; ++c) {
-          const uint32_t a = cluster_map(&s_hist[b], c);
-          count += remote_load(a);
-          if (sums)
-            mass += (static_cast<unsigned long long>(remote_load(a + 4 * bins)) << 28) +
-                    (static_cast<unsigned long long>(remote_load(a + 8 * bins)) << 14) + remote_load(a + 12 * bins);
+        for (int c0 = 0; c0 < C; c0 += 4) {  // four CTAs' at once: a remote load takes long
+          uint32_t n[4], m[4][3];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t a = cluster_map(&s_hist[b], min(c0 + c, C - 1));
+            n[c] = remote_load(a);
+            if (sums)
+#pragma unroll
+              for (int k = 0; k < 3; ++k) m[c][k] = remote_load(a + 4 * (k + 1) * bins);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c0 + c < C) {
+              count += n[c];
+              if (sums) mass += (static_cast<unsigned long long>(m[c][0]) << 28) + (static_cast<unsigned long long>(m[c][1]) << 14) + m[c][2];
+            }
         }
         for (int c = 0; c < C; ++c) {
           remote_store(cluster_map(&all_count[b], c), count);
@@ -487,45 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       }
       __syncthreads();
     };
-    // The index of the want-th token of a score.
-    auto nth_equal = [&](float score, unsigned long long want) {
-      unsigned long long n = 0;
-      each([&](float x, bool in) { n += in && x == score; });
-      n = warp_sum(n);
-      __syncthreads();
-      if (lane == 0) s.warp_a[warp] = n;
-      if (tid == 0) s.found = 0;
-      __syncthreads();
-      unsigned long long before = 0, total = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        before += w < warp ? s.warp_a[w] : 0;
-        total += s.warp_a[w];
-      }
-      const Slots all = gather(total);
-      for (int i = 0; i < rank; ++i) before += all[0][i];
-      if (before < want && want <= before + n) {  // this warp has it
-        for (int vv = v0; vv < v1; vv += 32) {
-          const int v = vv + lane;
-          float x[N];
-          Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
-          const int e = index_of(v);
-          unsigned long long here = 0;
-#pragma unroll
-          for (int k = 0; k < N; ++k) here += v < v1 && in_row(e + k) && x[k] == score;
-          const unsigned long long scan = warp_scan(here);
-          unsigned long long at = before + scan - here;
-#pragma unroll
-          for (int k = 0; k < N; ++k)
-            if (v < v1 && in_row(e + k) && x[k] == score && ++at == want) s.found = e + k + 1;
-          before += __shfl_sync(0xffffffffu, scan, 31);
-        }
-      }
-      __syncthreads();
-      const Slots who = gather(s.found);
-      unsigned long long last = 0;
-      for (int i = 0; i < C; ++i) last = max(last, who[0][i]);
-      return static_cast<int>(last) - 1;
-    };
     auto block_sum = [&](unsigned long long v) {
       v = warp_sum(v);
       __syncthreads();
@@ -565,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     };
 
     // The cut: the last token of the order before which there are fewer than `target` tokens, or less mass.
-    // Sets cut_key, cut and cut_last; returns the mass up to and with it (where masses are counted).
+    // Sets cut_key, cut and ties; returns the mass up to and with it (where masses are counted).
     auto find_cut = [&](bool by_sum, unsigned long long target) -> unsigned long long {
       if (!first_there) first();
       bin_with(kWideBins ? kWide : kNarrow, kWideBins, by_sum, target);
@@ -597,11 +567,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         const unsigned long long want = !by_sum ? target : one == 0 ? count : min(static_cast<unsigned long long>(count), (target + one - 1) / one);
         cut_key = order_bits(score);
         cut = score;
-        cut_last = want >= count ? INT32_MAX : nth_equal(score, want);
+        ties = want >= count ? 0xFFFFFFFFu : static_cast<uint32_t>(want);
         return sum + want * one;
       }
       // this CTA's tokens in question, then everyone's in every CTA, in order of rank
-      unsigned long long *l_list = reinterpret_cast<unsigned long long*>(s_hist), *list = l_list + kList;
+      uint32_t *l_list = s_hist, *list = l_list + kList;  // keys
       together();  // all are done with the histograms
       if (tid == 0) s.listed = 0;
       __syncthreads();
@@ -614,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
 #pragma unroll
           for (int k = 0; k < N; ++k) {
             const uint32_t key = order_bits(x[k]);
-            if (key >= a && key <= z && in_row(e + k)) l_list[atomicAdd(&s.listed, 1u)] = static_cast<unsigned long long>(key) << 32 | static_cast<uint32_t>(e + k);
+            if (key >= a && key <= z && in_row(e + k)) l_list[atomicAdd(&s.listed, 1u)] = key;
           }
         }
       }
@@ -623,23 +593,20 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       int n = 0;
       for (int c = 0; c < C; ++c) {
         const int m = static_cast<int>(all[0][c]);
-        for (int i = tid; i < m; i += kThreads) list[n + i] = remote_load64(cluster_map(&l_list[i], c));
+        for (int i = tid; i < m; i += kThreads) list[n + i] = remote_load(cluster_map(&l_list[i], c));
         n += m;
       }
       __syncthreads();
       uint32_t key[kEach];
-      int index[kEach];
       unsigned long long weight[kEach], mass[kEach];  // what is counted, and the mass
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const bool have = kThreads * i + tid < n;
-        const unsigned long long t = have ? list[kThreads * i + tid] : 0;
-        key[i] = static_cast<uint32_t>(t >> 32);
-        index[i] = static_cast<int>(t);
+        key[i] = have ? list[kThreads * i + tid] : 0;
         mass[i] = have && by_mass ? whole(sc.mass(score_of(key[i]))) : 0;
         weight[i] = by_sum ? mass[i] : have ? 1 : 0;
       }
-      // the least key before which (among larger ones) there is less than the target, then the index
+      // the least key before which (among larger ones) there is less than the target
       uint32_t k0 = klo, k1 = khi;
       while (k0 < k1) {
         const uint32_t mid = k0 + (k1 - k0) / 2;
@@ -662,38 +629,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       if (lane == 0) s.warp_b[warp] = least;
       larger = block_sum(larger);
       for (int w = 0; w < kWarps; ++w) least = min(least, static_cast<uint32_t>(s.warp_b[w]));
-      unsigned long long equal = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) equal += key[i] == least && kThreads * i + tid < n ? 1 : 0;
-      equal = block_sum(equal);
-      int i0 = 0, i1 = p.V - 1;  // the last kept index: the largest before which there is less than the target
-      if (equal == 1 || least > k1) i0 = i1;
-      while (i0 < i1) {
-        const int mid = i0 + (i1 - i0 + 1) / 2;
-        unsigned long long v = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) v += key[i] == least && index[i] < mid ? weight[i] : 0;
-        if (larger + block_sum(v) < target) i0 = mid;
-        else i1 = mid - 1;
-      }
-      unsigned long long in = 0;
-      int last = -1;
+      unsigned long long equal = 0, above = 0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const bool kept = kThreads * i + tid < n && (key[i] > least || (key[i] == least && index[i] <= i0));
-        in += kept ? mass[i] : 0;
-        if (kept && key[i] == least) last = max(last, index[i]);
+        const bool have = kThreads * i + tid < n;
+        equal += have && key[i] == least ? 1 : 0;
+        above += have && key[i] > least ? mass[i] : 0;
       }
-      last = __reduce_max_sync(0xffffffffu, last);
-      __syncthreads();
-      if (lane == 0) s.warp_b[warp] = static_cast<unsigned long long>(last + 1);
-      in = block_sum(in);
-      for (int w = 0; w < kWarps; ++w) last = max(last, static_cast<int>(s.warp_b[w]) - 1);
+      equal = block_sum(equal);
+      if (by_mass) above = block_sum(above);
       together();  // the lists may be written again
       cut_key = least;
       cut = score_of(least);
-      cut_last = last;
-      return sum + in;
+      const unsigned long long one = by_mass ? whole(sc.mass(cut)) : 0;
+      unsigned long long want = equal;
+      if (least == k1) want = min(equal, !by_sum ? target - larger : one == 0 ? equal : (target - larger + one - 1) / one);
+      ties = want == equal ? 0xFFFFFFFFu : static_cast<uint32_t>(want);
+      return sum + above + want * one;
     };
     unsigned long long kept = 0;
     if (by_count) kept = find_cut(false, top_k);
@@ -706,36 +658,27 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       (void)find_cut(true, max(1ull, times(top_p, kept, true)));
     }
   }
-  auto is_kept = [&](float x, int e) { return x > cut || (x == cut && e <= cut_last); };
   if (min_p > 0.f) {
     const uint32_t key = min_p_key();
     if (key > cut_key) {
       cut_key = key;
-      cut_last = INT32_MAX;
+      ties = 0xFFFFFFFFu;
       cut = score_of(key);
     }
   }
 
   // ---------------------------------------------------------------------- the draw
-  const bool cuts = cut_key != 0;
-  // the running masses of a vector's tokens, as sums of floats: the last is what the vector adds
-  auto running = [&](int v, float (&m)[N], float (&x)[N]) {
-    Vec<T>::unpack(s_x[v], x);
-    const int e = index_of(v);
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const float mass = sc.mass(x[k]);
-      sum += !cuts || is_kept(x[k], e + k) ? mass : 0.f;
-      m[k] = sum;
-    }
-  };
+  // Of a vector: the running masses of what is kept above the cut (as sums of floats: the last is what the
+  // vector adds; with all ties kept, them too) and how many tokens are at it.
+  const bool cuts = cut_key != 0, some = ties != 0xFFFFFFFFu;
+  const unsigned long long one = some ? whole(sc.mass(cut)) : 0;
+  const bool lowest = cut == -INFINITY;  // (places outside the row hold that)
   unsigned long long sum = 0;
+  uint32_t equal = 0;
   if (cuts) {
     for (int v = v0 + lane; v < v1; v += 32) {
       float x[N], vector = 0.f;
       Vec<T>::unpack(s_x[v], x);
-      const int e = index_of(v);
       bool any = false;
 #pragma unroll
       for (int k = 0; k < N; ++k) any |= x[k] >= cut;
@@ -743,7 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const float mass = sc.mass(x[k]);
-        vector += is_kept(x[k], e + k) ? mass : 0.f;
+        vector += x[k] > cut || (!some && x[k] == cut) ? mass : 0.f;
+        equal += x[k] == cut && (!lowest || in_row(index_of(v) + k));
       }
       sum += whole(vector);
     }
@@ -758,47 +702,71 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
   }
   sum = warp_sum(sum);
+  if (some) equal = __reduce_add_sync(0xffffffffu, equal);
   __syncthreads();
-  if (lane == 0) s.warp_a[warp] = sum;
+  if (lane == 0) {
+    s.warp_a[warp] = sum;
+    s.warp_b[warp] = equal;
+  }
   __syncthreads();
-  unsigned long long before = 0, cta = 0;
+  unsigned long long before = 0, cta = 0, ties_before = 0, ties_cta = 0;
   for (int w = 0; w < kWarps; ++w) {
     before += w < warp ? s.warp_a[w] : 0;
     cta += s.warp_a[w];
+    if (some) {
+      ties_before += w < warp ? s.warp_b[w] : 0;
+      ties_cta += s.warp_b[w];
+    }
   }
-  const Slots all = gather(cta);
+  const Slots all = gather(cta, ties_cta);
   unsigned long long total = 0;
   for (int i = 0; i < C; ++i) {
     before += i < rank ? all[0][i] : 0;
     total += all[0][i];
+    if (some) ties_before += i < rank ? all[1][i] : 0;
   }
+  // (of the ties the first `ties` in the row)
+  auto of_ties = [&](unsigned long long n) { return some ? min(n, static_cast<unsigned long long>(ties)) * one : 0; };
+  if (some) total += ties * one;
   const unsigned long long want = times(u, total, false);  // the first whose running mass is above it
-  if (want < before || want >= before + sum) return;
-  for (int vv = v0; vv < v1; vv += 32) {
+  const unsigned long long begin = before + of_ties(ties_before), end = before + sum + of_ties(ties_before + equal);
+  // the warp of the last kept tie tells its index, where a bound is wanted
+  const bool tells = some && p.bounds && ties_before < ties && ties <= ties_before + equal, draws = want >= begin && want < end;
+  if (p.bounds && !some && rank == 0 && tid == 0)
+    p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{cut_key, INT32_MAX};
+  if (!tells && !draws) return;
+  bool drawn = !draws, told = !tells;
+  for (int vv = v0; vv < v1 && !(drawn && told); vv += 32) {
     const int v = vv + lane;
     float m[N], x[N];
-    unsigned long long here = 0;
-    if (v < v1) {
-      running(v, m, x);
-      here = whole(m[N - 1]);
-    }
-    const unsigned long long scan = warp_scan(here), at = before + scan - here;
-    if (want >= at && want < at + here) {
-      int token = 0;
-      float score = 0.f;
-      bool got = false;
+    Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
+    float vector = 0.f;
+    uint32_t t = 0;
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (!got && at + whole(m[k]) > want) {
-          got = true;
-          token = index_of(v) + k;
-          score = x[k];
-        }
-      finish(token, score, total, cut_key, cut_last);
+    for (int k = 0; k < N; ++k) {
+      const float mass = sc.mass(x[k]);
+      vector += !cuts || x[k] > cut || (!some && x[k] == cut) ? mass : 0.f;
+      m[k] = vector;
+      t += some && x[k] == cut && (!lowest || in_row(index_of(v) + k));
     }
-    const unsigned long long step = __shfl_sync(0xffffffffu, scan, 31);
-    if (want < before + step) return;
-    before += step;
+    const unsigned long long here = whole(vector), scan = warp_scan(here), at = before + scan - here;
+    const unsigned long long t_scan = some ? warp_scan(t) : 0, t_at = ties_before + t_scan - t;
+    const bool mine = !drawn && want >= at + of_ties(t_at) && want < at + here + of_ties(t_at + t);
+    unsigned long long n = t_at;
+    bool got = false;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (some && x[k] == cut && (!lowest || in_row(index_of(v) + k)) && ++n == ties && !told)
+        p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{cut_key, index_of(v) + k};
+      if (mine && !got && at + whole(m[k]) + of_ties(n) > want) {
+        got = true;
+        finish(index_of(v) + k, x[k], total);
+      }
+    }
+    drawn |= __any_sync(0xffffffffu, got);
+    told |= __any_sync(0xffffffffu, n >= ties);
+    before += __shfl_sync(0xffffffffu, scan, 31);
+    ties_before += __shfl_sync(0xffffffffu, t_scan, 31);
   }
 }
 

@@ -183,9 +183,24 @@ def test_masked_tokens(dtype, hidden):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("lead", [0, 1, 5])
+def test_a_cut_among_hidden_tokens(dtype, lead):
+    """More tokens are to be kept than have a score: the cut lies among those of -infinity, by index."""
+    for V in (40, 5003, 30007):
+        x = torch.full((3, V), float("-inf"))
+        x[:, 3::V // 7] = torch.randn(3, len(range(3, V, V // 7)))
+        run(x.to(dtype), [0.0, 0.5, 1 - 2.0 ** -24], top_k=[20, V - 1, V // 2], lead=lead, exact_set=True)
+
+
+@pytest.mark.gpu
 def test_large_scores_and_the_largest_rows():
     x = scores(2, 4000, 4) * 1e37
     run(x, [0.3, 0.9], top_k=10)
+    run(scores(3, 9000, 4) * 60, [0.3, 0.9, 0.5], top_k=[10, 4000, 0], top_p=[1.0, 0.9, 0.99])
+    run((scores(3, 9000, 4) * 60).bfloat16(), [0.3, 0.9, 0.5], temperature=40.0, top_k=[10, 4000, 0], top_p=[1.0, 0.9, 0.99])
+    run((scores(3, 9000, 4) - 500).bfloat16(), [0.3, 0.9, 0.5], top_k=[10, 4000, 0], top_p=[1.0, 0.9, 0.99])
+    run((scores(3, 9000, 4) * 1e-4).bfloat16(), [0.3, 0.9, 0.5], top_k=[10, 4000, 0], top_p=[1.0, 0.9, 0.99])
     run(scores(1, 350000, 5), [0.7], top_p=0.9)
     run(scores(1, 700000, 6, dtype=torch.bfloat16), [0.7], top_k=50, min_p=0.01)
 
