@@ -51,6 +51,14 @@ __device__ __forceinline__ void remote_store(uint32_t a, uint32_t v) {
 __device__ __forceinline__ void remote_store(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
+__device__ __forceinline__ void remote_store4(uint32_t a, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 remote_load4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t remote_load(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -228,7 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // ---------------------------------------------------------------------- the row, once
   const char* row = p.x + static_cast<long long>(r) * p.stride;
   const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));  // elements before it in its first vector
-  const int pw = (p.pv + kWarps - 1) / kWarps, v0 = warp * pw, v1 = min(p.pv, v0 + pw);  // a warp's vectors are consecutive
+  // a warp's vectors are consecutive, and of them a lane's in the draw (an odd number, so that the lanes'
+  // reads fall into different banks)
+  const int run = ((p.pv - 1) / (32 * kWarps) + 1) | 1, v0 = min(p.pv, warp * 32 * run), v1 = min(p.pv, v0 + 32 * run);
+  const int run0 = min(v1, v0 + lane * run), run1 = min(v1, run0 + run);
   const int base = rank * p.pv;
   const float temperature = p.temperature ? p.temperature[r] : 1.f, u = p.uniforms[r];
   const int top_k = p.top_k ? p.top_k[r] : 0;
@@ -401,32 +412,55 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       last = __reduce_add_sync(0xffffffffu, last);
       if (lane == 0 && last) atomicAdd(&s_hist[hot], last);
       together();
-      // a CTA adds up its part of the bins over all, and tells all
-      const int part = bins / C;
+      // a CTA adds up its part of the bins over all (four lanes to four bins, a quarter of the CTAs each), and
+      // tells all
+      const int part = bins / C, b0 = rank * part;
       for (int i = tid; i < part; i += kThreads) {
-        const int b = rank * part + i;
-        uint32_t count = 0;
-        unsigned long long mass = 0;
-        for (int c0 = 0; c0 < C; c0 += 4) {  // four CTAs' at once: a remote load takes long
-          uint32_t n[4], m[4][3];
+        const int b = b0 + (i & ~3);
+        uint4 n = make_uint4(0, 0, 0, 0);
+        unsigned long long m[4] = {0, 0, 0, 0};
+        auto add = [](uint4& a, uint4 v) {
+          a.x += v.x;
+          a.y += v.y;
+          a.z += v.z;
+          a.w += v.w;
+        };
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t a = cluster_map(&s_hist[b], min(c0 + c, C - 1));
-            n[c] = remote_load(a);
-            if (sums)
+        for (int k = 0; k < kMaxCluster / 4; ++k) {
+          const int c = 4 * k + (i & 3);
+          if (c >= C) break;
+          const uint32_t a = cluster_map(&s_hist[b], c);
+          add(n, remote_load4(a));
+          if (sums)
 #pragma unroll
-              for (int k = 0; k < 3; ++k) m[c][k] = remote_load(a + 4 * (k + 1) * bins);
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c0 + c < C) {
-              count += n[c];
-              if (sums) mass += (static_cast<unsigned long long>(m[c][0]) << 28) + (static_cast<unsigned long long>(m[c][1]) << 14) + m[c][2];
+            for (int h = 0; h < 3; ++h) {
+              const uint4 v = remote_load4(a + 4 * (h + 1) * bins);
+              m[0] += static_cast<unsigned long long>(v.x) << (28 - 14 * h);
+              m[1] += static_cast<unsigned long long>(v.y) << (28 - 14 * h);
+              m[2] += static_cast<unsigned long long>(v.z) << (28 - 14 * h);
+              m[3] += static_cast<unsigned long long>(v.w) << (28 - 14 * h);
             }
         }
-        for (int c = 0; c < C; ++c) {
-          remote_store(cluster_map(&all_count[b], c), count);
-          if (sums) remote_store(cluster_map(&all_mass[b], c), mass);
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2) {
+          add(n, make_uint4(__shfl_xor_sync(0xffffffffu, n.x, d), __shfl_xor_sync(0xffffffffu, n.y, d),
+                            __shfl_xor_sync(0xffffffffu, n.z, d), __shfl_xor_sync(0xffffffffu, n.w, d)));
+          if (sums)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k], d);
+        }
+        const int k = i & 3;  // (each lane has all four)
+        all_count[b + k] = k == 0 ? n.x : k == 1 ? n.y : k == 2 ? n.z : n.w;
+        if (sums) all_mass[b + k] = k == 0 ? m[0] : k == 1 ? m[1] : k == 2 ? m[2] : m[3];
+      }
+      __syncthreads();
+      for (int i = tid; i < part / 4 * C; i += kThreads) {
+        const int c = i / (part / 4), b = b0 + 4 * (i - c * (part / 4));
+        if (c == rank) continue;
+        remote_store4(cluster_map(&all_count[b], c), *reinterpret_cast<const uint4*>(&all_count[b]));
+        if (sums) {
+          remote_store4(cluster_map(&all_mass[b], c), *reinterpret_cast<const uint4*>(&all_mass[b]));
+          remote_store4(cluster_map(&all_mass[b + 2], c), *reinterpret_cast<const uint4*>(&all_mass[b + 2]));
         }
       }
       together();
@@ -676,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   unsigned long long sum = 0;
   uint32_t equal = 0;
   if (cuts) {
-    for (int v = v0 + lane; v < v1; v += 32) {
+    for (int v = run0; v < run1; ++v) {
       float x[N], vector = 0.f;
       Vec<T>::unpack(s_x[v], x);
       bool any = false;
@@ -693,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
   } else {
 #pragma unroll 4
-    for (int v = v0 + lane; v < v1; v += 32) {
+    for (int v = run0; v < run1; ++v) {
       float x[N], vector = 0.f;
       Vec<T>::unpack(s_x[v], x);
 #pragma unroll
@@ -701,6 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       sum += whole(vector);
     }
   }
+  const unsigned long long of_lane = sum;
+  const uint32_t equal_of_lane = equal;
   sum = warp_sum(sum);
   if (some) equal = __reduce_add_sync(0xffffffffu, equal);
   __syncthreads();
@@ -735,38 +771,46 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   if (p.bounds && !some && rank == 0 && tid == 0)
     p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{cut_key, INT32_MAX};
   if (!tells && !draws) return;
-  bool drawn = !draws, told = !tells;
-  for (int vv = v0; vv < v1 && !(drawn && told); vv += 32) {
-    const int v = vv + lane;
-    float m[N], x[N];
-    Vec<T>::unpack(v < v1 ? s_x[v] : none, x);
-    float vector = 0.f;
-    uint32_t t = 0;
+  // the run that has the token, or the tie, then the place in it: a vector a lane
+  const unsigned long long lane_before = before + warp_scan(of_lane) - of_lane;
+  const unsigned long long lane_ties = some ? ties_before + warp_scan(equal_of_lane) - equal_of_lane : 0;
+  for (const bool tie : {false, true}) {
+    if (tie ? !tells : !draws) continue;
+    const bool here = tie ? lane_ties < ties && ties <= lane_ties + equal_of_lane
+                          : want >= lane_before + of_ties(lane_ties) && want < lane_before + of_lane + of_ties(lane_ties + equal_of_lane);
+    const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    if (owner < 0) continue;
+    unsigned long long at = __shfl_sync(0xffffffffu, lane_before, owner), t_at = __shfl_sync(0xffffffffu, lane_ties, owner);
+    const int first = __shfl_sync(0xffffffffu, run0, owner), last = __shfl_sync(0xffffffffu, run1, owner);
+    for (int vv = first; vv < last; vv += 32) {
+      const int v = vv + lane;
+      float m[N], x[N], vector = 0.f;
+      Vec<T>::unpack(v < last ? s_x[v] : none, x);
+      uint32_t t = 0;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const float mass = sc.mass(x[k]);
-      vector += !cuts || x[k] > cut || (!some && x[k] == cut) ? mass : 0.f;
-      m[k] = vector;
-      t += some && x[k] == cut && (!lowest || in_row(index_of(v) + k));
-    }
-    const unsigned long long here = whole(vector), scan = warp_scan(here), at = before + scan - here;
-    const unsigned long long t_scan = some ? warp_scan(t) : 0, t_at = ties_before + t_scan - t;
-    const bool mine = !drawn && want >= at + of_ties(t_at) && want < at + here + of_ties(t_at + t);
-    unsigned long long n = t_at;
-    bool got = false;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if (some && x[k] == cut && (!lowest || in_row(index_of(v) + k)) && ++n == ties && !told)
-        p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{cut_key, index_of(v) + k};
-      if (mine && !got && at + whole(m[k]) + of_ties(n) > want) {
-        got = true;
-        finish(index_of(v) + k, x[k], total);
+      for (int k = 0; k < N; ++k) {
+        const float mass = sc.mass(x[k]);
+        vector += !cuts || x[k] > cut || (!some && x[k] == cut) ? mass : 0.f;
+        m[k] = vector;
+        t += some && v < last && x[k] == cut && (!lowest || in_row(index_of(v) + k));
       }
+      const unsigned long long add = whole(vector), scan = warp_scan(add), mine = at + scan - add;
+      const unsigned long long t_scan = some ? warp_scan(t) : 0;
+      unsigned long long n = t_at + t_scan - t;
+      const bool has = want >= mine + of_ties(n) && want < mine + add + of_ties(n + t);
+      bool got = false;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (some && v < last && x[k] == cut && (!lowest || in_row(index_of(v) + k)) && ++n == ties && tie)
+          p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{cut_key, index_of(v) + k};
+        if (!tie && has && !got && mine + whole(m[k]) + of_ties(n) > want) {
+          got = true;
+          finish(index_of(v) + k, x[k], total);
+        }
+      }
+      at += __shfl_sync(0xffffffffu, scan, 31);
+      t_at += __shfl_sync(0xffffffffu, t_scan, 31);
     }
-    drawn |= __any_sync(0xffffffffu, got);
-    told |= __any_sync(0xffffffffu, n >= ties);
-    before += __shfl_sync(0xffffffffu, scan, 31);
-    ties_before += __shfl_sync(0xffffffffu, t_scan, 31);
   }
 }
 
