@@ -45,9 +45,6 @@ struct SampleParams {
   int32_t* status;
 };
 
-__device__ __forceinline__ void remote_store(uint32_t a, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
 __device__ __forceinline__ void remote_store(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
@@ -317,15 +314,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     if (rank == 0 && tid == 0) set_status(p.status, SPECDEC_ERR_INPUT_RANGE);
     return;
   }
-  auto each = [&](auto f) {  // this thread's places: f(score, whether it is in the row)
-#pragma unroll 2
+  auto each = [&](auto f) {  // this thread's scores of the row
     for (int v = v0 + lane; v < v1; v += 32) {
       float x[N];
       Vec<T>::unpack(s_x[v], x);
-      const int e = index_of(v);
-      const bool full = v >= whole0 && v < whole1;
+      if (v >= whole0 && v < whole1) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) f(x[k], full || (e + k >= 0 && e + k < p.V));
+        for (int k = 0; k < N; ++k) f(x[k]);
+      } else {
+        const int e = index_of(v);
+        for (int k = 0; k < N; ++k)
+          if (e + k >= 0 && e + k < p.V) f(x[k]);
+      }
     }
   };
   auto write = [&](int token, float logprob) {
@@ -391,23 +391,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     uint32_t* all_count = s_all;                                                       // of the cluster
     unsigned long long* all_mass = reinterpret_cast<unsigned long long*>(s_all + kNarrow);  // (not with kWide bins)
     unsigned long long mixed_mass[3] = {0, 0, 0};  // of the wide bins that hold more than one score
-    // Counts, and with `sums` masses, of the tokens by place (-1: none), added up over the cluster.  hot: the
-    // place of the lowest scores, counted apart: masked tokens are there, perhaps nearly all.
-    auto histogram = [&](int bins, bool sums, int hot, auto place) {
+    // Counts, and with `sums` masses, of tokens by place, added up over the cluster: pass(add) calls
+    // add(place) for each.  hot: the place of the lowest scores, counted apart: masked tokens are there,
+    // perhaps nearly all.
+    auto histogram = [&](int bins, bool sums, int hot, auto pass) {
       for (int i = tid; i < bins * (sums ? 4 : 1); i += kThreads) s_hist[i] = 0;
       __syncthreads();
       uint32_t last = 0;
-      each([&](float x, bool in) {
-        const int at = in ? place(x) : -1;
+      pass([&](int at) {
         if (at == hot) ++last;
-        else if (at >= 0) atomicAdd(&s_hist[at], 1u);
-        if (sums && at >= 0) {  // 14 bits at a time, so that 2^17 tokens' fit 32
-          const unsigned long long m = whole(sc.mass(x));
-          const uint32_t hi = static_cast<uint32_t>(m >> 28), mid = static_cast<uint32_t>(m >> 14) & 0x3FFFu, lo = static_cast<uint32_t>(m) & 0x3FFFu;
-          if (hi) atomicAdd(&s_hist[bins + at], hi);
-          if (mid) atomicAdd(&s_hist[2 * bins + at], mid);
-          if (lo) atomicAdd(&s_hist[3 * bins + at], lo);
-        }
+        else atomicAdd(&s_hist[at], 1u);
       });
       last = __reduce_add_sync(0xffffffffu, last);
       if (lane == 0 && last) atomicAdd(&s_hist[hot], last);
@@ -464,6 +457,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         }
       }
       together();
+    };
+    // A pass for fp32 and for what one bin holds: place(x) < 0 is none.
+    auto by_place = [&](int bins, auto place) {
+      return [&, bins, place](auto add) {
+        each([&](float x) {
+          const int at = place(x);
+          if (at < 0) return;
+          add(at);
+          if (by_mass) {  // 14 bits at a time, so that 2^17 tokens' fit 32
+            const unsigned long long m = whole(sc.mass(x));
+            const uint32_t hi = static_cast<uint32_t>(m >> 28), mid = static_cast<uint32_t>(m >> 14) & 0x3FFFu, lo = static_cast<uint32_t>(m) & 0x3FFFu;
+            if (hi) atomicAdd(&s_hist[bins + at], hi);
+            if (mid) atomicAdd(&s_hist[2 * bins + at], mid);
+            if (lo) atomicAdd(&s_hist[3 * bins + at], lo);
+          }
+        });
+      };
     };
     // The last bin that is not empty and begins before `target` tokens, or that much mass (in `wide` bins a
     // score's mass times its count): it, what it holds and what is before it are left in s.  With target 0
@@ -546,16 +556,33 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     bool first_there = false;
     auto first = [&] {
       if (kWideBins) {
-        unsigned long long m[4] = {0, 0, 0, 0};
-        histogram(kWide, false, kWidePlaces - 1, [&](float x) {
-          const int b = wide_place(x), k = mixed(b);
-          if (by_mass && k >= 0) {  // (few, or weighing nothing)
-            const unsigned long long w = whole(sc.mass(x));
-            m[0] += k == 0 ? w : 0;
-            m[1] += k == 1 ? w : 0;
-            m[2] += k == 2 ? w : 0;
+        unsigned long long m[3] = {0, 0, 0};
+        histogram(kWide, false, kWidePlaces - 1, [&](auto add) {
+          auto one_of = [&](uint32_t b, uint32_t bits) {
+            add(static_cast<int>(b));
+            const int k = mixed(static_cast<int>(b));
+            if (by_mass && k >= 0) {  // (few, or weighing nothing)
+              const unsigned long long w = whole(sc.mass(__uint_as_float(bits)));
+              m[0] += k == 0 ? w : 0;
+              m[1] += k == 1 ? w : 0;
+              m[2] += k == 2 ? w : 0;
+            }
+          };
+          for (int v = v0 + lane; v < v1; v += 32) {
+            const uint4 q = s_x[v];
+            const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+            const int e = index_of(v);
+            const bool full = v >= whole0 && v < whole1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // wide_place of two scores at once
+              const uint32_t w = word[k];
+              const uint32_t size = __vminu2(__vmaxu2(w & 0x7FFF7FFFu, (kSmall - 1) * 0x10001u), kLarge * 0x10001u) - (kSmall - 1) * 0x10001u;
+              const uint32_t minus = (w >> 15 & 0x10001u) * 0xFFFFu, middle = (kValues + 1) * 0x10001u;
+              const uint32_t b = ((middle + size) & minus) | ((middle - size) & ~minus);
+              if (full || in_row(e + 2 * k)) one_of(b & 0xFFFFu, w << 16);
+              if (full || in_row(e + 2 * k + 1)) one_of(b >> 16, w & 0xFFFF0000u);
+            }
           }
-          return b;
         });
         if (by_mass) {
           sum_all(m[0], m[1], m[2]);
@@ -563,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
           for (int k = 0; k < 3; ++k) mixed_mass[k] = m[k];
         }
       } else {
-        histogram(kNarrow, by_mass, (kWidePlaces - 1) >> 2, [&](float x) { return wide_place(x) >> 2; });
+        histogram(kNarrow, by_mass, (kWidePlaces - 1) >> 2, by_place(kNarrow, [](float x) { return wide_place(x) >> 2; }));
       }
       first_there = true;
     };
@@ -583,10 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         const int shift = max(0, 22 - __clz(khi - klo));
         const uint32_t a = klo, z = khi;
         first_there = false;
-        histogram(kNarrow, by_mass, static_cast<int>((z - a) >> shift), [&](float x) {
+        histogram(kNarrow, by_mass, static_cast<int>((z - a) >> shift), by_place(kNarrow, [=](float x) {
           const uint32_t key = order_bits(x);
           return key >= a && key <= z ? static_cast<int>((z - key) >> shift) : -1;
-        });
+        }));
         bin_with(kNarrow, false, by_sum, target);
         b = s.bin;
         khi = z - (static_cast<uint32_t>(b) << shift);
