@@ -26,8 +26,8 @@ namespace specdec {
 namespace {
 
 constexpr int kNarrow = 1024, kWide = 4096;  // bins
-constexpr int kList = 1024;
-constexpr int kMaxWarps = 16;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kList = 1024, kEach = kList / kThreads;
 constexpr int kMaxCluster = 16;
 constexpr int kMassBits = 42;
 constexpr long long kMaxRow = 1400 << 10;  // bytes
@@ -76,7 +76,7 @@ struct Scale {
     const float d = x - top;
     return fmaf(d, sh, d * sl);
   }
-  // (a score of -infinity makes the exponent NaN or -infinity, either of which the maximum drops)
+  // (a score of -infinity or NaN makes the exponent NaN or -infinity, either of which the maximum drops)
   __device__ __forceinline__ float mass(float x) const { return ex2(fmaxf(exponent(x), -200.f)); }
 };
 // A sum of masses, at most 8, as a whole number of 2^-42 (what is less is dropped).
@@ -141,8 +141,8 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) { 
 
 struct Shared {
   unsigned long long slot[2][3][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
-  unsigned long long warp_a[kMaxWarps], warp_b[kMaxWarps], warp_c[kMaxWarps];
-  uint64_t bar[kMaxWarps];
+  unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kWarps];
+  uint64_t bar[kWarps];
   unsigned long long count_before, mass_before;
   uint32_t listed, count;
   int bin, found;
@@ -152,7 +152,9 @@ struct Shared {
 // other scores are cut off) down to 2^-8; what is nearer to zero; the values from -2^-8 to above -128; the
 // rest.  The first, the middle and the last bin hold more than one score of bf16.
 constexpr uint32_t kSmall = 119u << 7, kLarge = 134u << 7;  // upper halves of 2^-8 and 2^7
-constexpr int kValues = kLarge - kSmall, kWidePlaces = 2 * kValues + 3;
+constexpr uint32_t kValues = kLarge - kSmall;
+constexpr int kWidePlaces = 2 * kValues + 3;
+static_assert(kWidePlaces <= kWide - 32 && (kWidePlaces - 1) / 4 < kNarrow - 32, "room for the masked tokens' counts");
 __device__ __forceinline__ int wide_place(float x) {
   const uint32_t bits = __float_as_uint(x), size = (bits & 0x7FFFFFFFu) >> 16;
   const int off = static_cast<int>(min(max(size, kSmall - 1), kLarge) - kSmall);  // -1: near zero; kValues: far
@@ -171,9 +173,8 @@ __device__ __forceinline__ uint32_t wide_high(int b) {
 __device__ __forceinline__ uint32_t wide_low(int b) { return b == kWidePlaces - 1 ? 0u : wide_high(b + 1) + 1; }
 
 // kCuts: whether there may be top-k or top-p.
-template <typename T, bool kCuts, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleParams p) {
-  constexpr int kWarps = kThreads / 32, kEach = kList / kThreads;
+template <typename T, bool kCuts>
+__global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const SampleParams p) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) char smem[];
   __shared__ Shared s;
@@ -244,8 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   auto index_of = [&](int v) { return (base + v) * N - skew; };  // of a vector's first element
   float top = -INFINITY;
   bool odd = false;  // NaN or +infinity
-  const uint4 none = sizeof(T) == 2 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
-                                    : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  // (places outside the row are NaN, which no comparison below takes and which weighs nothing)
+  const uint32_t nan = sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+  const uint4 none = make_uint4(nan, nan, nan, nan);
   // A warp fetches its own vectors: those that lie in the row whole by one bulk copy, all of a CTA's in
   // flight together; the others by element.
   const int whole0 = max(v0, min(v1, (skew > 0 ? 1 : 0) - base)), whole1 = max(whole0, min(v1, (p.V + skew) / N - base));
@@ -273,11 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   for (int v = v0 + lane; v < v1; v += 32) {
     float f[N];
     Vec<T>::unpack(s_x[v], f);
+    const bool full = v >= whole0 && v < whole1;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       top = fmaxf(top, f[k]);
-      odd |= !(f[k] < INFINITY);
+      odd |= full && !(f[k] < INFINITY);
     }
+    if (!full)
+      for (int k = 0; k < N; ++k)
+        odd |= index_of(v) + k >= 0 && index_of(v) + k < p.V && !(f[k] < INFINITY);
   }
   if (late) (void)mbar_wait_sleep(&s.bar[warp], 0, kTries, kNs);  // (no copy outlives the CTA)
   const bool bad_setting = !(temperature >= 0.f && temperature < INFINITY) || top_k < 0 || !(top_p > 0.f && top_p <= 1.f) ||
@@ -392,18 +398,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     unsigned long long* all_mass = reinterpret_cast<unsigned long long*>(s_all + kNarrow);  // (not with kWide bins)
     unsigned long long mixed_mass[3] = {0, 0, 0};  // of the wide bins that hold more than one score
     // Counts, and with `sums` masses, of tokens by place, added up over the cluster: pass(add) calls
-    // add(place) for each.  hot: the place of the lowest scores, counted apart: masked tokens are there,
-    // perhaps nearly all.
+    // add(place) for each.  hot: the place of the lowest scores, where masked tokens are, perhaps nearly all:
+    // they are counted in the last 32 bins, by lane (negative: it is a place like the others).  Nothing here
+    // branches for a token: branches were most of what a token cost.
     auto histogram = [&](int bins, bool sums, int hot, auto pass) {
       for (int i = tid; i < bins * (sums ? 4 : 1); i += kThreads) s_hist[i] = 0;
       __syncthreads();
-      uint32_t last = 0;
-      pass([&](int at) {
-        if (at == hot) ++last;
-        else atomicAdd(&s_hist[at], 1u);
-      });
-      last = __reduce_add_sync(0xffffffffu, last);
-      if (lane == 0 && last) atomicAdd(&s_hist[hot], last);
+      pass([&](int at) { atomicAdd(&s_hist[at == hot ? bins - 32 + lane : at], 1u); });
+      if (hot >= 0) {
+        __syncthreads();
+        if (warp == 0) {
+          const uint32_t n = __reduce_add_sync(0xffffffffu, s_hist[bins - 32 + lane]);
+          s_hist[bins - 32 + lane] = 0;
+          if (lane == 0) s_hist[hot] += n;
+        }
+      }
       together();
       // a CTA adds up its part of the bins over all (four lanes to four bins, a quarter of the CTAs each), and
       // tells all
@@ -467,10 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
           add(at);
           if (by_mass) {  // 14 bits at a time, so that 2^17 tokens' fit 32
             const unsigned long long m = whole(sc.mass(x));
-            const uint32_t hi = static_cast<uint32_t>(m >> 28), mid = static_cast<uint32_t>(m >> 14) & 0x3FFFu, lo = static_cast<uint32_t>(m) & 0x3FFFu;
-            if (hi) atomicAdd(&s_hist[bins + at], hi);
-            if (mid) atomicAdd(&s_hist[2 * bins + at], mid);
-            if (lo) atomicAdd(&s_hist[3 * bins + at], lo);
+            const uint32_t hi = static_cast<uint32_t>(m >> 28);
+            if (hi) atomicAdd(&s_hist[bins + at], hi);  // (few)
+            atomicAdd(&s_hist[2 * bins + at], static_cast<uint32_t>(m >> 14) & 0x3FFFu);
+            atomicAdd(&s_hist[3 * bins + at], static_cast<uint32_t>(m) & 0x3FFFu);
           }
         });
       };
@@ -558,29 +567,38 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       if (kWideBins) {
         unsigned long long m[3] = {0, 0, 0};
         histogram(kWide, false, kWidePlaces - 1, [&](auto add) {
-          auto one_of = [&](uint32_t b, uint32_t bits) {
-            add(static_cast<int>(b));
-            const int k = mixed(static_cast<int>(b));
-            if (by_mass && k >= 0) {  // (few, or weighing nothing)
-              const unsigned long long w = whole(sc.mass(__uint_as_float(bits)));
-              m[0] += k == 0 ? w : 0;
-              m[1] += k == 1 ? w : 0;
-              m[2] += k == 2 ? w : 0;
-            }
-          };
           for (int v = v0 + lane; v < v1; v += 32) {
             const uint4 q = s_x[v];
             const uint32_t word[4] = {q.x, q.y, q.z, q.w};
-            const int e = index_of(v);
             const bool full = v >= whole0 && v < whole1;
+            uint32_t apart = full ? 0u : 0xFFu;  // bits of those to be seen one by one (few, or weighing nothing)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // wide_place of two scores at once
               const uint32_t w = word[k];
               const uint32_t size = __vminu2(__vmaxu2(w & 0x7FFF7FFFu, (kSmall - 1) * 0x10001u), kLarge * 0x10001u) - (kSmall - 1) * 0x10001u;
               const uint32_t minus = (w >> 15 & 0x10001u) * 0xFFFFu, middle = (kValues + 1) * 0x10001u;
               const uint32_t b = ((middle + size) & minus) | ((middle - size) & ~minus);
-              if (full || in_row(e + 2 * k)) one_of(b & 0xFFFFu, w << 16);
-              if (full || in_row(e + 2 * k + 1)) one_of(b >> 16, w & 0xFFFF0000u);
+              if (full) {
+                add(static_cast<int>(b & 0xFFFFu));
+                add(static_cast<int>(b >> 16));
+              }
+              if (by_mass) {  // in bins of several scores
+                if ((size & 0xFFFFu) - 1 >= kValues) apart |= 1u << (2 * k);
+                if ((size >> 16) - 1 >= kValues) apart |= 2u << (2 * k);
+              }
+            }
+            for (; apart; apart &= apart - 1) {
+              const int k = __ffs(apart) - 1;
+              const uint32_t w = k < 4 ? (k < 2 ? q.x : q.y) : (k < 6 ? q.z : q.w);
+              if (!full && !in_row(index_of(v) + k)) continue;
+              const float x = __uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16);
+              const int b = wide_place(x), of = mixed(b);
+              if (!full) add(b);
+              if (!by_mass || of < 0) continue;
+              const unsigned long long weight = whole(sc.mass(x));
+              m[0] += of == 0 ? weight : 0;
+              m[1] += of == 1 ? weight : 0;
+              m[2] += of == 2 ? weight : 0;
             }
           }
         });
@@ -610,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         const int shift = max(0, 22 - __clz(khi - klo));
         const uint32_t a = klo, z = khi;
         first_there = false;
-        histogram(kNarrow, by_mass, static_cast<int>((z - a) >> shift), by_place(kNarrow, [=](float x) {
+        histogram(kNarrow, by_mass, -1, by_place(kNarrow, [=](float x) {
           const uint32_t key = order_bits(x);
           return key >= a && key <= z ? static_cast<int>((z - key) >> shift) : -1;
         }));
@@ -733,7 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // vector adds; with all ties kept, them too) and how many tokens are at it.
   const bool cuts = cut_key != 0, some = ties != 0xFFFFFFFFu;
   const unsigned long long one = some ? whole(sc.mass(cut)) : 0;
-  const bool lowest = cut == -INFINITY;  // (places outside the row hold that)
   unsigned long long sum = 0;
   uint32_t equal = 0;
   if (cuts) {
@@ -748,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       for (int k = 0; k < N; ++k) {
         const float mass = sc.mass(x[k]);
         vector += x[k] > cut || (!some && x[k] == cut) ? mass : 0.f;
-        equal += x[k] == cut && (!lowest || in_row(index_of(v) + k));
+        equal += x[k] == cut;
       }
       sum += whole(vector);
     }
@@ -819,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         const float mass = sc.mass(x[k]);
         vector += !cuts || x[k] > cut || (!some && x[k] == cut) ? mass : 0.f;
         m[k] = vector;
-        t += some && v < last && x[k] == cut && (!lowest || in_row(index_of(v) + k));
+        t += some && x[k] == cut;
       }
       const unsigned long long add = whole(vector), scan = warp_scan(add), mine = at + scan - add;
       const unsigned long long t_scan = some ? warp_scan(t) : 0;
@@ -828,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       bool got = false;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        if (some && v < last && x[k] == cut && (!lowest || in_row(index_of(v) + k)) && ++n == ties && tie)
+        if (some && x[k] == cut && ++n == ties && tie)
           p.bounds[static_cast<long long>(r) * p.bounds_stride] = specdec_keep_bound{cut_key, index_of(v) + k};
         if (!tie && has && !got && mine + whole(m[k]) + of_ties(n) > want) {
           got = true;
@@ -840,9 +857,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
   }
 }
-
-// Threads of a CTA: few where the draw alone is to be made, which leaves each of them little to do.
-constexpr int kCutThreads = 512, kDrawThreads = 256;
 
 template <typename T>
 int launch_sample(SampleParams p, int R, cudaStream_t stream) {
@@ -859,7 +873,7 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   p.pv = (vectors - 1) / C + 1;
   const size_t smem = static_cast<size_t>(p.pv) * 16 + extra;
   if (smem > kRoom) return SPECDEC_ERR_UNSUPPORTED;
-  auto kernel = extra ? sample_kernel<T, true, kCutThreads> : sample_kernel<T, false, kDrawThreads>;
+  auto kernel = extra ? sample_kernel<T, true> : sample_kernel<T, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRoom));
   if (e != cudaSuccess) return map_cuda_error(e);
   if (C > 8) {
@@ -872,7 +886,7 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(R * C);
-  cfg.blockDim = dim3(extra ? kCutThreads : kDrawThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
