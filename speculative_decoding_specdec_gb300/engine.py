@@ -174,6 +174,17 @@ class EqspecBatch:
                               self.accept_len, self.out_token, self.status, residual, stream,
                               keep_bounds=bounds)
 
+    def sample(self, logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
+               logprob=None, keep_bounds=None, stream=None):
+        """This round's tokens drawn from ``logits`` [B, V] (one a row, nothing drafted), with each
+        row's settings (see specdec.sample); a realignment commits them."""
+        self._results_row()
+        with torch.cuda.stream(stream):      # (None: the current one)
+            self.accept_len.zero_()
+        specdec.sample(logits, uniforms, self.out_token, self.status, temperature=temperature,
+                       top_k=top_k, top_p=top_p, min_p=min_p, logprob=logprob,
+                       keep_bounds=keep_bounds, stream=stream)
+
     def realign(self, draft, copy_engine=0, stream=None):
         """Realign after this round's verification; with ``pdl`` (constructor) the realignment
         is launched as a programmatic dependent of the verification kernel ahead of it."""
@@ -285,6 +296,89 @@ class TreeBatch(EqspecBatch):
             self.realign(self.drafts, stream=stream)
             specdec.tree_commit(src, self.cache, width, self.accept_len, self.path, self.status,
                                 width_dst=self.w_hist[r + 1], nodes=self.nodes, stream=stream)
+
+
+class SharedPromptBatch(TreeBatch):
+    """A TreeBatch of several rows per prompt: ``samples[p]`` rows go on from prompt ``prompts[p]``.
+
+    The K/V of a prompt (all its tokens but the last, which is every row's pending one) is held once,
+    in ``prefix`` [L, 2, P, H, columns, hd]; the batch's cache holds what the rows have of their own,
+    and ``n_committed``, ``width`` and the ids count that alone.  ``prefill`` gives the passes that fill
+    ``prefix``; a round is then as of a TreeBatch (or, without drafts, ``sample`` and ``realign``), with
+    heads normed where weights are given and every row's prompt in its attention."""
+
+    CHUNK = specdec.MAX_TREE    # prompt tokens of a prefill pass
+
+    def __init__(self, layers, heads_q, heads, head_dim, kv_dtype, prompts, samples, nodes, D, cap,
+                 max_rounds, device="cuda", pad_id=0, in_place=False, scheduled=True):
+        if len(prompts) != len(samples) or min(samples, default=0) < 1 or not all(prompts):
+            raise ValueError("need a non-empty prompt and a number of rows for each")
+        super().__init__(layers, heads_q, heads, head_dim, kv_dtype, sum(samples), nodes, D, cap,
+                         max_rounds, device=device, pad_id=pad_id, in_place=in_place,
+                         scheduled=scheduled)
+        dev = self.status.device
+        self.prompts = [list(p) for p in prompts]
+        held = [len(p) - 1 for p in prompts]
+        group = [0]
+        for k in samples:
+            group.append(group[-1] + k)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.prefix = torch.empty((layers, 2, len(prompts), heads, max(held) + self.CHUNK, head_dim),
+                                  dtype=kv_dtype, device=dev)
+        self.prefix_len = torch.tensor(held, **i32)
+        self.group_start = torch.tensor(group, **i32)
+        self.prompt_of = [p for p, k in enumerate(samples) for _ in range(k)]
+        self.prefix_of_row = torch.tensor([held[p] for p in self.prompt_of], **i32)
+        self.start([[self.prompts[p][-1]] for p in self.prompt_of])
+
+    def prefill(self):
+        """The passes that fill ``prefix``, CHUNK tokens of every prompt each: yields tokens [P, T],
+        ``append(layer, q, k, v, table, q_out, ...)`` and ``attend(layer, q, out, scale)``, to be
+        called for every layer in order before the next."""
+        dev, P = self.status.device, len(self.prompts)
+        held = torch.tensor([len(p) - 1 for p in self.prompts])
+        for t0 in range(0, int(held.max()), self.CHUNK):
+            T = min(self.CHUNK, int(held.max()) - t0)
+            at = t0 + torch.arange(T)[None].expand(P, T)
+            live = at < held[:, None]
+            tokens = torch.tensor([(p[t0:min(t0 + T, len(p) - 1)] + [0] * T)[:T] for p in self.prompts])
+            chain = torch.arange(-1, T - 1)[None].expand(P, T)
+            on = lambda t: t.to(dtype=torch.int32, device=dev).contiguous()
+            where = dict(positions=on(torch.where(live, at, 0)), columns=on(torch.where(live, at, -1)))
+            parents = on(torch.where(live, chain, -2))
+            any_live = live.any(1)               # (a prompt that is through has no nodes)
+            done, first = on(torch.where(any_live, t0 + 1, 1)), on(torch.zeros(P))
+
+            def append(layer, q, k, v, table, q_out, q_weight=None, k_weight=None, eps=1e-6,
+                       weight_offset=0.0, interleaved=False, stream=None):
+                specdec.norm_rotary_append(q, k, v, self.prefix, layer, table, q_out, self.status,
+                                           q_weight, k_weight, eps=eps, weight_offset=weight_offset,
+                                           interleaved=interleaved, stream=stream, **where)
+
+            def attend(layer, q, out, scale=None, stream=None):
+                ws = self.workspaces.get("prefill", specdec.tree_attention_workspace_bytes(q, self.prefix), stream)
+                specdec.tree_attention(q, self.prefix, layer, out, done, None, parents, self.status,
+                                       ws, scale=scale, first_col=first, stream=stream)
+
+            yield on(tokens), append, attend
+
+    def rotary_append(self, layer, q, k, v, table, q_out, parents, interleaved=False, stream=None,
+                      q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0):
+        """Positions of the nodes' queries and keys, behind their prompts, with norms of the heads where
+        weights are given, and their K/V into the cache's columns."""
+        specdec.norm_rotary_append(q, k, v, self.cache, layer, table, q_out, self.status, q_weight,
+                                   k_weight, eps=eps, weight_offset=weight_offset,
+                                   start=self.prefix_of_row, n_committed=self.n_committed,
+                                   width=self.width, parents=parents, interleaved=interleaved,
+                                   stream=stream)
+
+    def attention(self, layer, q, out, parents, scale=None, lse=None, stream=None):
+        """Attention of the nodes over their prompt, the committed columns and their ancestors."""
+        P = len(self.prompts)
+        ws = self.workspaces.get("prefix", specdec.prefix_attention_workspace_bytes(q, self.cache, P), stream)
+        specdec.prefix_attention(q, self.cache, layer, out, self.n_committed, self.width, parents,
+                                 self.status, ws, self.prefix, self.prefix_len, self.group_start,
+                                 scale=scale, lse=lse, stream=stream)
 
 
 class HostRounds:
