@@ -139,9 +139,12 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) { 
   return v;
 }
 
-struct Shared {
-  unsigned long long slot[2][3][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
-  unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kWarps];
+// (without cuts as small as can be: a few hundred bytes decide whether an SM holds a third CTA of a row of
+// 151552 fp32 scores in eight parts, 53 us for 256 rows against 63)
+template <bool kCuts> struct Shared {
+  static constexpr int kTold = kCuts ? 3 : 2;
+  unsigned long long slot[2][kTold][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
+  unsigned long long warp_a[kWarps], warp_b[kWarps], warp_c[kCuts ? kWarps : 1];
   uint64_t bar[kWarps];
   unsigned long long count_before, mass_before;
   uint32_t listed, count;
@@ -177,7 +180,8 @@ template <typename T, bool kCuts>
 __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const SampleParams p) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) char smem[];
-  __shared__ Shared s;
+  using Sh = Shared<kCuts>;
+  __shared__ Sh s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cluster_rank(), C = [] {
     uint32_t n;
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
   using Slots = const unsigned long long (*)[kMaxCluster];
   auto gather = [&](unsigned long long a, unsigned long long b = 0, unsigned long long c = 0) -> Slots {
     Slots got = s.slot[turn];
-    if (tid < 3 * C) {
+    if (tid < Sh::kTold * C) {
       const int i = tid / C;
       remote_store(cluster_map(&s.slot[turn][i][rank], tid - i * C), i == 0 ? a : i == 1 ? b : c);
     }
