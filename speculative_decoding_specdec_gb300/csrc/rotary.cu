@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams 
 // A warp takes an item, a token's heads or a part of them, by itself.  What a token costs besides its
 // values (its place, addresses, cosines) is spent once per warp: with a CTA per token eight warps
 // spent it, and instructions bounded it (47 us for the prompts below at 2.3 instructions a cycle and
-// SM, 4600 of them a token).  A thread keeps its place in the head and with it its weights (kSame: of q's
+// SM, 3600 of them a token).  A thread keeps its place in the head and with it its weights (kSame: of q's
 // type, N values in a vector), asks for the next item's place before this one's values, and has three
 // heads in flight: two CTAs per SM with room for that in registers (32 us; three CTAs, spilling: 56).
 // Bulk copies into a ring of shared memory, with a CTA's barrier per token, were slower (50 us).

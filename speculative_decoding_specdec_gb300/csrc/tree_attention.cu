@@ -11,6 +11,20 @@
 // (302 MB, 3.8 TB/s); one row of 65536 columns and 8 query rows: 193 us (2.8 TB/s).
 // bf16 heads of other sizes than 64 and 128 come here too: chains of 6, 32 heads of 96, 8 rows of up
 // to 1024 columns: 55 us.
+//
+// Columns that batch rows share (specdec_prefix_attention).  A softmax over two sets of columns is that of
+// their (m, l, o): m the larger of the maxima, l and o the sums of 2^(m_i - m) (l_i, o_i).  So all query
+// rows of a group, which may fill a matrix tile where a row's own do not, attend its prefix in one pass that
+// reads the prefix once and leaves (m, l, o) in fp32, and the pass over the rows' own columns takes these
+// in where it writes its output.  The second is launched as the first's programmatic dependent: it
+// starts where SMs are free, and waits before it reads what the first wrote.  Measured, heads of 128:
+//   64 rows of one token, 32 query and 8 K/V heads, one prompt of 65537 columns: 108 us (the shared pass
+//     78, 269 MB in 3.4 TB/s; its cut units' merge 12, the own columns 26, partly at once);
+//   32 chains of 6 of the same heads, 4 prompts of 6000: 70 us (38, 10, 27);
+//   8 rows of one token of 32 K/V heads, one prompt of 2048: 22 us.
+// Rows that fill the tiles by themselves gain nothing from a pass of their group and would pay for (m, l,
+// o): they take both parts in one pass, from two tensor maps, the prefix's tiles first (fills_tiles):
+//   32 trees of 32 nodes, 32 query and 2 K/V heads, one prompt of 8192 columns: 132 us, 0.97 PFLOP/s.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -910,7 +924,7 @@ void set_shape(AttnParams& p, const AttnShape& s, void* workspace) {
 // Whether a batch row's own query rows fill the tensor cores' tiles to three quarters and more, so that
 // its prefix is attended with its own columns in one pass.
 // (16384 rows in all per K/V head over 8192 columns and 512 a row over up to 1056 of its own, 32 rows
-// and 2 K/V heads: 138 us against 201 in two passes.)
+// and 2 K/V heads: 132 us against 201 in two passes.)
 bool fills_tiles(const AttnShape& s, long long R) {
   const long long room = R <= 128 ? 128 : (R + 255) / 256 * 256;
   return s.kind == kTc && R * 4 >= room * 3;
