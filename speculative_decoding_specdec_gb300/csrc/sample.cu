@@ -882,12 +882,13 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   // CTAs that an SM holds at once, and of a row: what its scores need, then more while all rows' run at once.
   // (A CTA's part is as large as lets two be on an SM: of 60 KB at most, with more CTAs to a row, 256 bf16 rows
   // of 151936 with top-k took 299 us against 93, 256 fp32 rows without cuts 78 against 53.  More while all
-  // run at once: one bf16 row of 151936 with top-p 20 us against 29, 8 of 32000 20 against 26; up to 8 CTAs
-  // in place of 16, 24 and 18.)
+  // run at once, of 8 KB of scores each and from 8 CTAs to 16 of 16 KB: bf16 with top-p, one row of 151936
+  // 20 us against 29 with what it needs, or 24 with 8; of 4 KB, or of 16: 8 rows of 32000 18.3, 21.0, 19.1; of
+  // 16000 20.3, 19.8, 21.3; 16 CTAs of 8 KB in place of 8: 8 rows of 64000 22.0 against 19.7.)
   auto bytes = [&](int c) { return static_cast<size_t>((vectors - 1) / c + 1) * 16 + extra; };
   auto resident = [&](int c) { return std::min<long long>(extra ? 2 : 4, (220 << 10) / (bytes(c) + (2 << 10))) * sms; };
   int C = 1;
-  while (C < kMaxCluster && (bytes(C) > (112 << 10) || (R * 2LL * C <= resident(2 * C) && vectors > C * 256))) C *= 2;
+  while (C < kMaxCluster && (bytes(C) > (112 << 10) || (R * 2LL * C <= resident(2 * C) && vectors > C * (C < 8 ? 512 : 1024)))) C *= 2;
   p.pv = (vectors - 1) / C + 1;
   const size_t smem = static_cast<size_t>(p.pv) * 16 + extra;
   if (smem > kRoom) return SPECDEC_ERR_UNSUPPORTED;
