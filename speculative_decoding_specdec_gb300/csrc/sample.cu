@@ -87,7 +87,26 @@ struct Scale {
   }
   // (a score of -infinity or NaN makes the exponent NaN or -infinity, either of which the maximum drops)
   __device__ __forceinline__ float mass(float x) const { return ex2(fmaxf(exponent(x), -200.f)); }
+  // Of N scores, two at a time: the same roundings.
+  template <int N> __device__ __forceinline__ void masses(const float* x, float* m) const {
+    const uint64_t t2 = pack2(-top, -top), h2 = pack2(sh, sh), l2 = pack2(sl, sl);
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const uint64_t d = add2(pack2(x[k], x[k + 1]), t2);
+      const float2 e = unpack2(fma2(d, h2, mul2(d, l2)));
+      m[k] = ex2(fmaxf(e.x, -200.f));
+      m[k + 1] = ex2(fmaxf(e.y, -200.f));
+    }
+  }
 };
+
+// The larger of two words' scores, NaN where either is (of bf16 in both halves).
+template <typename T> __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if constexpr (sizeof(T) == 2) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  else asm("max.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
 // A sum of masses, at most 8, as a whole number of 2^-42 (what is less is dropped).
 __device__ __forceinline__ unsigned long long whole(float v) {
   const uint32_t bits = __float_as_uint(v), e = bits >> 23;
@@ -285,19 +304,32 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
   }
   __syncwarp();
   const bool late = whole1 > whole0 && !mbar_wait_sleep(&s.bar[warp], 0, kTries, kNs);
-#pragma unroll 4
-  for (int v = v0 + lane; v < v1; v += 32) {
-    float f[N];
-    Vec<T>::unpack(s_x[v], f);
-    const bool full = v >= whole0 && v < whole1;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      top = fmaxf(top, f[k]);
-      odd |= full && !(f[k] < INFINITY);
-    }
-    if (!full)
-      for (int k = 0; k < N; ++k)
+  {
+    // (-infinity is a word of its own for each type; NaN stays, and so does +infinity)
+    const uint32_t least = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    uint32_t most[4] = {least, least, least, least};
+    auto edge = [&](int v) {  // a vector that lies in the row in part
+      float f[N];
+      Vec<T>::unpack(s_x[v], f);
+      for (int k = 0; k < N; ++k) {
+        top = fmaxf(top, f[k]);
         odd |= index_of(v) + k >= 0 && index_of(v) + k < p.V && !(f[k] < INFINITY);
+      }
+    };
+#pragma unroll 4
+    for (int v = whole0 + lane; v < whole1; v += 32) {
+      const uint4 w = s_x[v];
+      most[0] = max_nan<T>(most[0], w.x);
+      most[1] = max_nan<T>(most[1], w.y);
+      most[2] = max_nan<T>(most[2], w.z);
+      most[3] = max_nan<T>(most[3], w.w);
+    }
+    for (int v = v0 + lane; v < whole0; v += 32) edge(v);
+    for (int v = whole1 + lane; v < v1; v += 32) edge(v);
+    const uint32_t word = max_nan<T>(max_nan<T>(most[0], most[1]), max_nan<T>(most[2], most[3]));
+    const float a = __uint_as_float(sizeof(T) == 2 ? word << 16 : word), b = __uint_as_float(word & 0xFFFF0000u);
+    top = fmaxf(top, sizeof(T) == 2 ? fmaxf(a, b) : a);
+    odd |= !(a < INFINITY) || (sizeof(T) == 2 && !(b < INFINITY));
   }
   if (late) (void)mbar_wait_sleep(&s.bar[warp], 0, kTries, kNs);  // (no copy outlives the CTA)
   const bool bad_setting = !(temperature >= 0.f && temperature < INFINITY) || top_k < 0 || !(top_p > 0.f && top_p <= 1.f) ||
@@ -775,10 +807,11 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
 #pragma unroll
       for (int k = 0; k < N; ++k) any |= x[k] >= cut;
       if (!any) continue;
+      float mass[N];
+      sc.masses<N>(x, mass);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const float mass = sc.mass(x[k]);
-        vector += x[k] > cut || (!some && x[k] == cut) ? mass : 0.f;
+        vector += x[k] > cut || (!some && x[k] == cut) ? mass[k] : 0.f;
         equal += x[k] == cut;
       }
       sum += whole(vector);
@@ -786,10 +819,11 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
   } else {
 #pragma unroll 4
     for (int v = run0; v < run1; ++v) {
-      float x[N], vector = 0.f;
+      float x[N], mass[N], vector = 0.f;
       Vec<T>::unpack(s_x[v], x);
+      sc.masses<N>(x, mass);
 #pragma unroll
-      for (int k = 0; k < N; ++k) vector += sc.mass(x[k]);
+      for (int k = 0; k < N; ++k) vector += mass[k];
       sum += whole(vector);
     }
   }
