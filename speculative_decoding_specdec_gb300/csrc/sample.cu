@@ -18,14 +18,15 @@
 // Masses are fp32 exponentials, added up within a 16-byte vector and then as whole numbers of 2^-42 of
 // the highest: the sums depend on no order and no number of CTAs, so a row repeats bit for bit.
 //
-// Measured (rows whose scores fit L2 come from there).  No cuts: 256 rows of 151552, fp32 53 us (2.9
-// TB/s), bf16 32 us; one bf16 row of 151936 6 us.  There instructions issue in 54 % of the cycles and
-// DRAM is at 36 %: a row's steps follow each other, with three CTAs on an SM to fill the gaps.  With cuts,
-// bf16 rows of 151936, 64: top-k 26 us, top-p 36; 256: top-k 93; one with top-p 20.  Shared-memory atomics
+// Measured (rows whose scores fit L2 come from there).  No cuts: 256 rows of 151552, fp32 49 us (3.2
+// TB/s), bf16 27 us; one bf16 row of 151936 5.8 us.  There instructions issue in 49 % of the cycles and
+// DRAM is at 40 %: a row's steps follow each other, with three CTAs on an SM to fill the gaps (of 192 or
+// 384 threads 47 and 53 us, bf16 27 and 28).  With cuts,
+// bf16 rows of 151936, 64: top-k 24 us, top-p 34; 256: top-k 88; one with top-p 20.  Shared-memory atomics
 // and exchanges over the cluster, one after the other, are what is left.  fp32, 64 rows of 151936: top-k
-// 54, top-p 80 us (three more atomics a token, and the list).  2 rows of 1000: 14 us, all latency.
-// One bin a score for bf16 against 32 an octave and the list: 64 rows with top-k 26 us against 37, with
-// top-p 36 against 60; one with top-p 20 against 28.
+// 53, top-p 78 us (three more atomics a token, and the list).  2 rows of 1000: 14 us, all latency.
+// One bin a score for bf16 against 32 an octave and the list: 64 rows with top-k 24 us against 36, with
+// top-p 34 against 58; one with top-p 20 against 28.
 #include <algorithm>
 #include <cmath>
 
@@ -168,7 +169,7 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) { 
 }
 
 // (without cuts as small as can be: a few hundred bytes decide whether an SM holds a third CTA of a row of
-// 151552 fp32 scores in eight parts, 53 us for 256 rows against 63)
+// 151552 fp32 scores in eight parts, 54 us for 256 rows against 63)
 template <bool kCuts> struct Shared {
   static constexpr int kTold = kCuts ? 3 : 2;
   unsigned long long slot[2][kTold][kMaxCluster];  // what the cluster's CTAs tell each other, in turn
@@ -203,8 +204,8 @@ __device__ __forceinline__ uint32_t wide_high(int b) {
 }
 __device__ __forceinline__ uint32_t wide_low(int b) { return b == kWidePlaces - 1 ? 0u : wide_high(b + 1) + 1; }
 
-// kCuts: whether there may be top-k or top-p.  (Without, in the same kernel: 256 rows of 151552 fp32 67 us
-// against 53, bf16 41 against 32: the histograms' room and registers.)
+// kCuts: whether there may be top-k or top-p.  (Without, in the same kernel: 256 rows of 151552 fp32 62 us
+// against 49, bf16 34 against 27: the histograms' room and registers.)
 template <typename T, bool kCuts>
 __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const SampleParams p) {
   constexpr int N = Vec<T>::N;
@@ -915,9 +916,9 @@ int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   const int sms = std::max(1, sm_count());
   // CTAs that an SM holds at once, and of a row: what its scores need, then more while all rows' run at once.
   // (A CTA's part is as large as lets two be on an SM: of 60 KB at most, with more CTAs to a row, 256 bf16 rows
-  // of 151936 with top-k took 299 us against 93, 256 fp32 rows without cuts 78 against 53.  More while all
+  // of 151936 with top-k took 292 us against 88, 256 fp32 rows without cuts 72 against 49.  More while all
   // run at once, of 8 KB of scores each and from 8 CTAs to 16 of 16 KB: bf16 with top-p, one row of 151936
-  // 20 us against 29 with what it needs, or 24 with 8; of 4 KB, or of 16: 8 rows of 32000 18.3, 21.0, 19.1; of
+  // 20 us against 27 with what it needs, or 23 with 8; of 4 KB, or of 16: 8 rows of 32000 18.3, 21.0, 19.1; of
   // 16000 20.3, 19.8, 21.3; 16 CTAs of 8 KB in place of 8: 8 rows of 64000 22.0 against 19.7.)
   auto bytes = [&](int c) { return static_cast<size_t>((vectors - 1) / c + 1) * 16 + extra; };
   auto resident = [&](int c) { return std::min<long long>(extra ? 2 : 4, (220 << 10) / (bytes(c) + (2 << 10))) * sms; };
