@@ -18,15 +18,15 @@
 // Masses are fp32 exponentials, added up within a 16-byte vector and then as whole numbers of 2^-42 of
 // the highest: the sums depend on no order and no number of CTAs, so a row repeats bit for bit.
 //
-// Measured (rows whose scores fit L2 come from there).  No cuts: 256 rows of 151552, fp32 49 us (3.2
-// TB/s), bf16 27 us; one bf16 row of 151936 5.8 us.  There instructions issue in 49 % of the cycles and
-// DRAM is at 40 %: a row's steps follow each other, with three CTAs on an SM to fill the gaps (of 192 or
-// 384 threads 47 and 53 us, bf16 27 and 28).  With cuts,
-// bf16 rows of 151936, 64: top-k 24 us, top-p 34; 256: top-k 88; one with top-p 20.  Shared-memory atomics
+// Measured (rows whose scores fit L2 come from there).  No cuts: 256 rows of 151552, fp32 46 us (3.4
+// TB/s), bf16 25 us; one bf16 row of 151936 5.7 us.  There instructions issue in 48 % of the cycles and
+// DRAM is at 42 %: a row's steps follow each other, with three CTAs on an SM to fill the gaps (of 192 or
+// 384 threads 47 and 53 us against 49 before the last step, bf16 27 and 28 against 26).  With cuts,
+// bf16 rows of 151936, 64: top-k 24 us, top-p 33; 256: top-k 86; one with top-p 20.  Shared-memory atomics
 // and exchanges over the cluster, one after the other, are what is left.  fp32, 64 rows of 151936: top-k
-// 53, top-p 78 us (three more atomics a token, and the list).  2 rows of 1000: 14 us, all latency.
+// 52, top-p 77 us (three more atomics a token, and the list).  2 rows of 1000: 14 us, all latency.
 // One bin a score for bf16 against 32 an octave and the list: 64 rows with top-k 24 us against 36, with
-// top-p 34 against 58; one with top-p 20 against 28.
+// top-p 33 against 58; one with top-p 20 against 28.
 #include <algorithm>
 #include <cmath>
 
@@ -114,6 +114,21 @@ __device__ __forceinline__ unsigned long long whole(float v) {
   const unsigned long long m = static_cast<unsigned long long>((bits & 0x7FFFFFu) | 0x800000u) << 22;
   return e < 70 ? 0 : m >> (130 - e);  // v = m 2^(e - 172)
 }
+
+// The sum of whole(v) over up to 2^8 such v, in half the instructions (256 rows without cuts: fp32 46 us
+// against 49, bf16 25 against 27; by conversions of floats to 64 bits 51, 27): v rounded to 2^-19 is the last bits of
+// v + 24, and what that left (exact, at most 2^-20 of either sign) in 2^-42, rounded down, those of its sum with
+// 1.5 * 2^23.
+struct WholeSum {
+  uint32_t high = 0;
+  int low = 0;
+  __device__ __forceinline__ void add(float v) {
+    const float h = v + 24.f, l = __fmaf_rd(v - (h - 24.f), 1ll << kMassBits, 12582912.f);
+    high += __float_as_uint(h) - __float_as_uint(24.f);
+    low += __float_as_int(l) - __float_as_int(12582912.f);
+  }
+  __device__ __forceinline__ unsigned long long value() const { return (static_cast<unsigned long long>(high) << (kMassBits - 19)) + low; }
+};
 
 // The natural logarithm of 0 < f <= 1 in two floats, to about 2^-40: f = 2^k m, ln m = 2 artanh(r) with
 // r = (m - 1) / (m + 1), |r| <= 0.2, whose first term alone needs both.
@@ -204,8 +219,8 @@ __device__ __forceinline__ uint32_t wide_high(int b) {
 }
 __device__ __forceinline__ uint32_t wide_low(int b) { return b == kWidePlaces - 1 ? 0u : wide_high(b + 1) + 1; }
 
-// kCuts: whether there may be top-k or top-p.  (Without, in the same kernel: 256 rows of 151552 fp32 62 us
-// against 49, bf16 34 against 27: the histograms' room and registers.)
+// kCuts: whether there may be top-k or top-p.  (Without, in the same kernel: 256 rows of 151552 fp32 58 us
+// against 46, bf16 33 against 25: the histograms' room and registers.)
 template <typename T, bool kCuts>
 __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const SampleParams p) {
   constexpr int N = Vec<T>::N;
@@ -798,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
   // vector adds; with all ties kept, them too) and how many tokens are at it.
   const bool cuts = cut_key != 0, some = ties != 0xFFFFFFFFu;
   const unsigned long long one = some ? whole(sc.mass(cut)) : 0;
-  unsigned long long sum = 0;
+  WholeSum masses;
   uint32_t equal = 0;
   if (cuts) {
     for (int v = run0; v < run1; ++v) {
@@ -815,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
         vector += x[k] > cut || (!some && x[k] == cut) ? mass[k] : 0.f;
         equal += x[k] == cut;
       }
-      sum += whole(vector);
+      masses.add(vector);
     }
   } else {
 #pragma unroll 4
@@ -825,9 +840,10 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
       sc.masses<N>(x, mass);
 #pragma unroll
       for (int k = 0; k < N; ++k) vector += mass[k];
-      sum += whole(vector);
+      masses.add(vector);
     }
   }
+  unsigned long long sum = masses.value();
   const unsigned long long of_lane = sum;
   const uint32_t equal_of_lane = equal;
   sum = warp_sum(sum);
