@@ -8,6 +8,7 @@ examined afterwards.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -329,38 +330,51 @@ class SharedPromptBatch(TreeBatch):
         self.group_start = torch.tensor(group, **i32)
         self.prompt_of = [p for p, k in enumerate(samples) for _ in range(k)]
         self.prefix_of_row = torch.tensor([held[p] for p in self.prompt_of], **i32)
+        self._passes = None                      # of prefill
+        self._prefill_first = torch.tensor([0] * len(prompts), **i32)
         self.start([[self.prompts[p][-1]] for p in self.prompt_of])
 
     def prefill(self):
         """The passes that fill ``prefix``, CHUNK tokens of every prompt each: yields tokens [P, T],
         ``append(layer, q, k, v, table, q_out, ...)`` and ``attend(layer, q, out, scale)``, to be
-        called for every layer in order before the next."""
-        dev, P = self.status.device, len(self.prompts)
+        called for every layer in order before the next.  What a pass passes on is made before the
+        first one and kept with the batch: calls on other streams, and graphs, may use it later."""
+        if self._passes is None:
+            self._passes = self._prefill_passes()
+        for tokens, positions, columns, parents, done in self._passes:
+            yield (tokens, functools.partial(self._prefill_append, positions, columns),
+                   functools.partial(self._prefill_attend, parents, done))
+
+    def _prefill_passes(self):
+        """Per pass tokens, positions, columns and parents [P, T] and lengths [P]: views of one copy."""
+        P = len(self.prompts)
         held = torch.tensor([len(p) - 1 for p in self.prompts])
+        passes = []
         for t0 in range(0, int(held.max()), self.CHUNK):
             T = min(self.CHUNK, int(held.max()) - t0)
             at = t0 + torch.arange(T)[None].expand(P, T)
             live = at < held[:, None]
             tokens = torch.tensor([(p[t0:min(t0 + T, len(p) - 1)] + [0] * T)[:T] for p in self.prompts])
             chain = torch.arange(-1, T - 1)[None].expand(P, T)
-            on = lambda t: t.to(dtype=torch.int32, device=dev).contiguous()
-            where = dict(positions=on(torch.where(live, at, 0)), columns=on(torch.where(live, at, -1)))
-            parents = on(torch.where(live, chain, -2))
             any_live = live.any(1)               # (a prompt that is through has no nodes)
-            done, first = on(torch.where(any_live, t0 + 1, 1)), on(torch.zeros(P))
+            passes.append((tokens, torch.where(live, at, 0), torch.where(live, at, -1),
+                           torch.where(live, chain, -2), torch.where(any_live, t0 + 1, 1)))
+        if not passes:
+            return []
+        flat = torch.cat([t.to(torch.int32).reshape(-1) for one in passes for t in one])
+        parts = iter(flat.to(self.status.device).split([t.numel() for one in passes for t in one]))
+        return [tuple(next(parts).view(t.shape) for t in one) for one in passes]
 
-            def append(layer, q, k, v, table, q_out, q_weight=None, k_weight=None, eps=1e-6,
-                       weight_offset=0.0, interleaved=False, stream=None):
-                specdec.norm_rotary_append(q, k, v, self.prefix, layer, table, q_out, self.status,
-                                           q_weight, k_weight, eps=eps, weight_offset=weight_offset,
-                                           interleaved=interleaved, stream=stream, **where)
+    def _prefill_append(self, positions, columns, layer, q, k, v, table, q_out, q_weight=None, k_weight=None,
+                        eps=1e-6, weight_offset=0.0, interleaved=False, stream=None):
+        specdec.norm_rotary_append(q, k, v, self.prefix, layer, table, q_out, self.status, q_weight, k_weight,
+                                   eps=eps, weight_offset=weight_offset, positions=positions, columns=columns,
+                                   interleaved=interleaved, stream=stream)
 
-            def attend(layer, q, out, scale=None, stream=None):
-                ws = self.workspaces.get("prefill", specdec.tree_attention_workspace_bytes(q, self.prefix), stream)
-                specdec.tree_attention(q, self.prefix, layer, out, done, None, parents, self.status,
-                                       ws, scale=scale, first_col=first, stream=stream)
-
-            yield on(tokens), append, attend
+    def _prefill_attend(self, parents, done, layer, q, out, scale=None, stream=None):
+        ws = self.workspaces.get("prefill", specdec.tree_attention_workspace_bytes(q, self.prefix), stream)
+        specdec.tree_attention(q, self.prefix, layer, out, done, None, parents, self.status, ws, scale=scale,
+                               first_col=self._prefill_first, stream=stream)
 
     def rotary_append(self, layer, q, k, v, table, q_out, parents, interleaved=False, stream=None,
                       q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0):
