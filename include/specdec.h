@@ -270,11 +270,12 @@ int specdec_sampling_filter(const void* target_logits, const void* draft_logits,
  *                temperature 0).
  *   keep_bounds  NULL, or specdec_keep_bound out of row r at keep_bounds[r * bounds_stride]: the row's
  *                kept set, as specdec_verify_sample takes it (key 0 and index INT32_MAX: all).
- * One read of the scores.  Masses are fp32 exponentials (off by some 2^-21), added up as whole numbers
- * of 2^-42 of the highest, so that a row repeats bit for bit whatever is beside it: a draw can differ from
- * an exact one only where u lies within about 1e-6 of a border between two tokens, top-p's cut where
- * top_p lies that near a cumulative mass; top-k and min-p are exact.  Tokens below 2^-42 of the highest
- * are not drawn.
+ * One read of the scores.  A mass 2^-z is an fp32 exponential, off by at most 2^-22 + 3 ln 2 z 2^-24 of
+ * itself.  Masses are added up in fp32 within 16 bytes of scores, counted from the row's first one, and
+ * these sums as whole numbers of 2^-42 of the highest mass, so that a row repeats bit for bit wherever it
+ * lies and whatever is beside it.  A draw can differ from an exact one only where u lies within about 1e-6
+ * of a border between two tokens, top-p's cut where top_p lies that near a cumulative mass; top-k and min-p
+ * are exact.  Sixteen bytes of scores that weigh less than 2^-42 of the highest in all are not drawn from.
  * Device-detected errors (SPECDEC_ERR_INPUT_RANGE; the row's outputs are not written): a setting or
  * uniform out of its range (NaN included), a row with NaN, +infinity or nothing above -infinity.
  * Limits: R >= 0, V >= 1, row_stride >= V, bounds_stride >= 1 for several rows; a row of at most 1.4 MB

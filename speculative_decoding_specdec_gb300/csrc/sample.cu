@@ -15,8 +15,9 @@
 //      are kept, by index.  An fp32 row has 32 bins an octave, with the masses' sums; the cut's bin is listed
 //      in every CTA and searched there, or where it holds more than the list, split by key first;
 //   3. the kept masses' sums by warp, CTA and cluster, and in the warp that owns the draw the token.
-// Masses are fp32 exponentials, added up within a 16-byte vector and then as whole numbers of 2^-42 of
-// the highest: the sums depend on no order and no number of CTAs, so a row repeats bit for bit.
+// Masses are fp32 exponentials, added up within a 16-byte vector, counted from the row's first score, and
+// then as whole numbers of 2^-42 of the highest: the sums depend on no order, no number of CTAs and no
+// address, so a row repeats bit for bit.
 //
 // Measured (rows whose scores fit L2 come from there).  No cuts: 256 rows of 151552, fp32 46 us (3.4
 // TB/s), bf16 25 us; one bf16 row of 151936 5.7 us.  There instructions issue in 48 % of the cycles and
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
 
   // ---------------------------------------------------------------------- the row, once
   const char* row = p.x + static_cast<long long>(r) * p.stride;
-  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));  // elements before it in its first vector
+  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));  // elements before it in memory's 16 bytes
   // a warp's vectors are consecutive, and of them a lane's in the draw (an odd number, so that the lanes'
   // reads fall into different banks)
   const int run = ((p.pv - 1) / (32 * kWarps) + 1) | 1, v0 = min(p.pv, warp * 32 * run), v1 = min(p.pv, v0 + 32 * run);
@@ -291,35 +292,61 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
   const float temperature = p.temperature ? p.temperature[r] : 1.f, u = p.uniforms[r];
   const int top_k = p.top_k ? p.top_k[r] : 0;
   const float top_p = p.top_p ? p.top_p[r] : 1.f, min_p = p.min_p ? p.min_p[r] : 0.f;
-  auto index_of = [&](int v) { return (base + v) * N - skew; };  // of a vector's first element
+  auto index_of = [&](int v) { return (base + v) * N; };  // of a vector's first element
   float top = -INFINITY;
   bool odd = false;  // NaN or +infinity
   // (places outside the row are NaN, which no comparison below takes and which weighs nothing)
   const uint32_t nan = sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
   const uint4 none = make_uint4(nan, nan, nan, nan);
-  // A warp fetches its own vectors: those that lie in the row whole by one bulk copy, all of a CTA's in
-  // flight together; the others by element.
-  const int whole0 = max(v0, min(v1, (skew > 0 ? 1 : 0) - base)), whole1 = max(whole0, min(v1, (p.V + skew) / N - base));
+  // A warp fetches its own vectors by one bulk copy, all of a CTA's in flight together, and what lies in the row in
+  // part by element.  Vectors are counted from the row's first element, so that what is added up in one
+  // does not follow from where the row lies: where it begins inside memory's 16 bytes, the copy brings
+  // those that lie in it whole, `skew` elements too far on, and the warp moves them to their places (128 rows
+  // of 50257 without cuts, most of them so: fp32 11.1 us, bf16 10.4; left where memory puts them 8.9, 8.8).
+  const int copy0 = max(v0, min(v1, (skew > 0 ? 1 : 0) - base)), copy1 = max(copy0, min(v1, (p.V + skew) / N - base));
+  const int whole1 = max(v0, min(v1, p.V / N - base));  // vectors from v0 on that lie in the row whole
   if (lane == 0) {
     mbar_init(&s.bar[warp], 1);
     fence_mbar_init();
-    if (whole1 > whole0) {
-      mbar_arrive_expect_tx(&s.bar[warp], (whole1 - whole0) * 16);
-      bulk_g2s(s_x + whole0, row + static_cast<long long>(index_of(whole0)) * static_cast<int>(sizeof(T)), (whole1 - whole0) * 16, &s.bar[warp]);
+    if (copy1 > copy0) {
+      mbar_arrive_expect_tx(&s.bar[warp], (copy1 - copy0) * 16);
+      bulk_g2s(s_x + copy0, row + static_cast<long long>(index_of(copy0) - skew) * static_cast<int>(sizeof(T)), (copy1 - copy0) * 16, &s.bar[warp]);
     }
   }
-  for (int v = v0 + lane; v < v1; v += 32) {
-    if (v >= whole0 && v < whole1) continue;
+  auto by_element = [&](int v) {
     uint4 w = none;
     T* q = reinterpret_cast<T*>(&w);
     const int e = index_of(v);
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      if (e + k >= 0 && e + k < p.V) q[k] = reinterpret_cast<const T*>(row)[e + k];
-    s_x[v] = w;
-  }
+      if (e + k < p.V) q[k] = reinterpret_cast<const T*>(row)[e + k];
+    return w;
+  };
+  for (int v = v0 + lane; v < v1; v += 32)
+    if (v < copy0 || v >= copy1) s_x[v] = by_element(v);
+  // (moved: the last copied vector's second part lies in one that was not copied, or for another warp)
+  const bool moves = skew > 0 && copy1 > copy0;
+  const uint4 last = moves && lane == 0 ? by_element(copy1 - 1) : none;
   __syncwarp();
-  const bool late = whole1 > whole0 && !mbar_wait_sleep(&s.bar[warp], 0, kTries, kNs);
+  const bool late = copy1 > copy0 && !mbar_wait_sleep(&s.bar[warp], 0, kTries, kNs);
+  if (moves) {
+    const int words = skew * static_cast<int>(sizeof(T)) / 4, bits = skew * static_cast<int>(sizeof(T)) % 4 * 8;
+    for (int vv = copy0; vv < copy1 - 1; vv += 32) {
+      const int v = vv + lane;
+      const uint4 a = v < copy1 - 1 ? s_x[v] : none, b = v < copy1 - 1 ? s_x[v + 1] : none;
+      uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      __syncwarp();  // all have read
+#pragma unroll
+      for (int k = 0; k < 6; ++k) w[k] = words & 2 ? w[k + 2] : w[k];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) w[k] = words & 1 ? w[k + 1] : w[k];
+      if (v < copy1 - 1)
+        s_x[v] = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                            __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+    }
+    if (lane == 0) s_x[copy1 - 1] = last;
+    __syncwarp();
+  }
   {
     // (-infinity is a word of its own for each type; NaN stays, and so does +infinity)
     const uint32_t least = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
@@ -329,18 +356,17 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
       Vec<T>::unpack(s_x[v], f);
       for (int k = 0; k < N; ++k) {
         top = fmaxf(top, f[k]);
-        odd |= index_of(v) + k >= 0 && index_of(v) + k < p.V && !(f[k] < INFINITY);
+        odd |= index_of(v) + k < p.V && !(f[k] < INFINITY);
       }
     };
 #pragma unroll 4
-    for (int v = whole0 + lane; v < whole1; v += 32) {
+    for (int v = v0 + lane; v < whole1; v += 32) {
       const uint4 w = s_x[v];
       most[0] = max_nan<T>(most[0], w.x);
       most[1] = max_nan<T>(most[1], w.y);
       most[2] = max_nan<T>(most[2], w.z);
       most[3] = max_nan<T>(most[3], w.w);
     }
-    for (int v = v0 + lane; v < whole0; v += 32) edge(v);
     for (int v = whole1 + lane; v < v1; v += 32) edge(v);
     const uint32_t word = max_nan<T>(max_nan<T>(most[0], most[1]), max_nan<T>(most[2], most[3]));
     const float a = __uint_as_float(sizeof(T) == 2 ? word << 16 : word), b = __uint_as_float(word & 0xFFFF0000u);
@@ -386,13 +412,13 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
     for (int v = v0 + lane; v < v1; v += 32) {
       float x[N];
       Vec<T>::unpack(s_x[v], x);
-      if (v >= whole0 && v < whole1) {
+      if (v < whole1) {
 #pragma unroll
         for (int k = 0; k < N; ++k) f(x[k]);
       } else {
         const int e = index_of(v);
         for (int k = 0; k < N; ++k)
-          if (e + k >= 0 && e + k < p.V) f(x[k]);
+          if (e + k < p.V) f(x[k]);
       }
     }
   };
@@ -453,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
   uint32_t cut_key = 0;        // kept: a larger key, and the first `ties` tokens of this one
   uint32_t ties = 0xFFFFFFFFu;  // (all)
   float cut = -INFINITY;       // its score
-  auto in_row = [&](int e) { return e >= 0 && e < p.V; };
+  auto in_row = [&](int e) { return e < p.V; };
   const bool by_mass = top_p < 1.f, by_count = top_k > 0 && top_k < p.V;
   if (kCuts && (by_mass || by_count)) {
     uint32_t* all_count = s_all;                                                       // of the cluster
@@ -632,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
           for (int v = v0 + lane; v < v1; v += 32) {
             const uint4 q = s_x[v];
             const uint32_t word[4] = {q.x, q.y, q.z, q.w};
-            const bool full = v >= whole0 && v < whole1;
+            const bool full = v < whole1;
             uint32_t apart = full ? 0u : 0xFFu;  // bits of those to be seen one by one (few, or weighing nothing)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // wide_place of two scores at once
@@ -926,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, kCuts ? 2 : 4) sample_kernel(const S
 template <typename T>
 int launch_sample(SampleParams p, int R, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
-  const int vectors = (p.V + 2 * N - 2) / N;  // whatever the row's alignment
+  const int vectors = (p.V + N - 1) / N;
   const size_t extra = p.top_k || p.top_p ? 2 * kWide * 4 : 0;
   constexpr size_t kRoom = 200 << 10;
   const int sms = std::max(1, sm_count());
