@@ -930,30 +930,39 @@ bool fills_tiles(const AttnShape& s, long long R) {
   return s.kind == kTc && R * 4 >= room * 3;
 }
 
-// The pass over the rows' own columns; p from attention_params, with what a prefix pass left if any.
-// both: their prefixes' columns too.
-int own_pass(AttnParams p, const specdec_tree_attention_args* a, size_t room, cudaStream_t stream,
-             const specdec_kv_view* both = nullptr) {
+// The shape of the pass over the rows' own columns, and whether it can run; p from attention_params, behind
+// a prefix pass with where that leaves its parts.  both: over their prefixes' columns too.
+int own_shape(const AttnParams& p, const specdec_tree_attention_args* a, const specdec_kv_view* both, AttnShape& s) {
   if (sm_count() <= 0) return SPECDEC_ERR_CUDA;
   const specdec_kv_view& c = a->cache;
-  const int es = elem_size(c.dtype);
-  AttnShape s = attn_shape(es, a->T, p.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols, p.prior != nullptr);
+  s = attn_shape(elem_size(c.dtype), a->T, p.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols, p.prior != nullptr);
   // no more groups than the longest rows could give work to
   const long long columns = static_cast<long long>(c.cap_cols) + (both ? both->cap_cols + s.tile : 0);
   const long long tiles = static_cast<long long>(a->B) * c.heads * ((columns - 1) / s.tile + 1 + s.open);
   s.groups = static_cast<int>(std::min<long long>(s.groups, std::max<long long>(1, tiles / s.min_tiles)));
   s.grid = s.groups * s.MT;
-  if (room < attn_workspace(s, c.head_dim).bytes) return SPECDEC_ERR_INVALID_ARG;
+  if (a->workspace_bytes < attn_workspace(s, c.head_dim).bytes) return SPECDEC_ERR_INVALID_ARG;
   if (s.grid > static_cast<int>(kTicketBytes / (p.prior ? 8 : 4))) return SPECDEC_ERR_UNSUPPORTED;
   if (static_cast<long long>(a->B) * c.heads * (columns / kCols + 16) >= (1LL << 31))
     return SPECDEC_ERR_UNSUPPORTED;  // the sequence of tiles is numbered in 32 bits
+  return SPECDEC_OK;
+}
+
+int launch_own(AttnParams p, const specdec_tree_attention_args* a, const specdec_kv_view* both, const AttnShape& s, cudaStream_t stream) {
+  const specdec_kv_view& c = a->cache;
   set_shape(p, s, a->workspace);
   if (both) {
     ByteView prefix = to_bytes(*both);
     prefix.base += a->layer * prefix.sl;
     return launch_attn_tc_both(p, c.rows, prefix, both->rows, s.grid, stream);
   }
-  return launch_attention<false>(p, s, es, c.rows, stream);
+  return launch_attention<false>(p, s, elem_size(c.dtype), c.rows, stream);
+}
+
+int own_pass(const AttnParams& p, const specdec_tree_attention_args* a, cudaStream_t stream, const specdec_kv_view* both = nullptr) {
+  AttnShape s;
+  const int rc = own_shape(p, a, both, s);
+  return rc ? rc : launch_own(p, a, both, s, stream);
 }
 
 }  // namespace
@@ -976,7 +985,7 @@ extern "C" int specdec_tree_attention(const specdec_tree_attention_args* a, void
   if (!a) return SPECDEC_ERR_INVALID_ARG;
   const int rc = check_attention(a);
   if (rc || a->B == 0) return rc;
-  return own_pass(attention_params(a), a, a->workspace_bytes, static_cast<cudaStream_t>(stream));
+  return own_pass(attention_params(a), a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t specdec_prefix_attention_workspace(int dtype, int B, int T, int heads_q, int heads_kv,
@@ -995,7 +1004,7 @@ extern "C" int specdec_prefix_attention(const specdec_prefix_attention_args* arg
   if (rc || a->B == 0) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AttnParams own = attention_params(a);
-  if (args->P == 0) return own_pass(own, a, a->workspace_bytes, s);
+  if (args->P == 0) return own_pass(own, a, s);
   const specdec_kv_view &c = a->cache, &f = args->prefix;
   const int st = check_view(f, elem_size(c.dtype));
   if (st) return st;
@@ -1016,11 +1025,14 @@ extern "C" int specdec_prefix_attention(const specdec_prefix_attention_args* arg
   own.prefix_cap = f.cap_cols;
   own.prefix_one_row = f.rows == 1 ? 1 : 0;
   const AttnShape alone = attn_shape(es, a->T, own.G, c.head_dim, static_cast<long long>(a->B) * c.heads * c.cap_cols);
-  if (fills_tiles(alone, static_cast<long long>(a->T) * own.G)) return own_pass(own, a, a->workspace_bytes, s, &f);
+  if (fills_tiles(alone, static_cast<long long>(a->T) * own.G)) return own_pass(own, a, s, &f);
   char* ws = static_cast<char*>(a->workspace);
   own.prior = reinterpret_cast<int32_t*>(ws + w.state);
   own.prior_ml = reinterpret_cast<float2*>(ws + w.ml);
   own.prior_o = reinterpret_cast<float*>(ws + w.o);
+  AttnShape behind;  // (refused before anything is launched)
+  const int rc_own = own_shape(own, a, nullptr, behind);
+  if (rc_own) return rc_own;
   AttnParams p = own;
   p.cache = to_bytes(f);
   p.cache.base += a->layer * p.cache.sl;
@@ -1040,5 +1052,5 @@ extern "C" int specdec_prefix_attention(const specdec_prefix_attention_args* arg
   p.ticket = reinterpret_cast<unsigned*>(ws) + kTicketBytes / 8;
   const int rp = launch_attention<true>(p, shape, es, f.rows, s);
   if (rp) return rp;
-  return own_pass(own, a, a->workspace_bytes, s);
+  return launch_own(own, a, nullptr, behind, s);
 }
