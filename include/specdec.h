@@ -269,7 +269,8 @@ int specdec_sampling_filter(const void* target_logits, const void* draft_logits,
  *   logprob      [R] float32 out, or NULL: the natural logarithm of its probability among the kept (0 at
  *                temperature 0).
  *   keep_bounds  NULL, or specdec_keep_bound out of row r at keep_bounds[r * bounds_stride]: the row's
- *                kept set, as specdec_verify_sample takes it (key 0 and index INT32_MAX: all).
+ *                kept set, as specdec_verify_sample takes it (key 0 and index INT32_MAX: all).  That has
+ *                one temperature for all rows; verification of trees takes no bounds.
  * One read of the scores.  A mass 2^-z is an fp32 exponential, off by at most 2^-22 + 3 ln 2 z 2^-24 of
  * itself.  Masses are added up in fp32 within 16 bytes of scores, counted from the row's first one, and
  * these sums as whole numbers of 2^-42 of the highest mass, so that a row repeats bit for bit wherever it
@@ -723,7 +724,8 @@ size_t specdec_tree_attention_workspace(int dtype, int B, int T, int heads_q, in
 /*
  * The same over a prefix that rows share: its K/V is held once, read once for all rows that share it,
  * and not part of their own cache rows.  [BSDDR section 2.3 batches sequences of one pool; several samples
- * of one prompt, or requests behind one long instruction, begin with the same columns.]
+ * of one prompt, or requests behind one long instruction, begin with the same columns.]  A request's own
+ * text behind the prefix is a row's own columns, appended by passes of up to SPECDEC_MAX_TREE tokens.
  *   out_i = the softmax-weighted sum over the prefix's columns and the row's own (those of
  *   specdec_tree_attention, which `own` describes) together.
  * Prefix p (of P) has prefix_len[p] >= 0 columns of row p of `prefix` from column 0 on, or from

@@ -19,15 +19,16 @@
 // then as whole numbers of 2^-42 of the highest: the sums depend on no order, no number of CTAs and no
 // address, so a row repeats bit for bit.
 //
-// Measured (rows whose scores fit L2 come from there).  No cuts: 256 rows of 151552, fp32 46 us (3.4
-// TB/s), bf16 25 us; one bf16 row of 151936 5.7 us.  There instructions issue in 48 % of the cycles and
+// Measured (rows whose scores fit L2 come from there).  No cuts: 256 rows of 151552, fp32 47 us (3.3
+// TB/s), bf16 25 us; one bf16 row of 151936 5.8 us.  There instructions issue in 49 % of the cycles and
 // DRAM is at 42 %: a row's steps follow each other, with three CTAs on an SM to fill the gaps (of 192 or
-// 384 threads 47 and 53 us against 49 before the last step, bf16 27 and 28 against 26).  With cuts,
-// bf16 rows of 151936, 64: top-k 24 us, top-p 33; 256: top-k 86; one with top-p 20.  Shared-memory atomics
-// and exchanges over the cluster, one after the other, are what is left.  fp32, 64 rows of 151936: top-k
-// 52, top-p 77 us (three more atomics a token, and the list).  2 rows of 1000: 14 us, all latency.
-// One bin a score for bf16 against 32 an octave and the list: 64 rows with top-k 24 us against 36, with
-// top-p 33 against 58; one with top-p 20 against 28.
+// 384 threads 47 and 53 us against 49 before sums in two parts, bf16 27 and 28 against 26).  With cuts,
+// bf16 rows of 151936 with eight likely tokens over a long tail, 64: top-k 24 us, top-p 36; 256: top-k 81; one
+// with top-p 21.  Shared-memory atomics and exchanges over the cluster, one after the other, are what is left.
+// fp32, 64 rows of 151936: top-k 51, top-p 71 us (three more atomics a token, and the list).  2 rows of 1000:
+// 14 us, all latency.
+// One bin a score for bf16 against 32 an octave and the list, on other rows: 64 with top-k 24 us against 36,
+// with top-p 33 against 58; one with top-p 20 against 28.
 #include <algorithm>
 #include <cmath>
 
@@ -146,7 +147,8 @@ __device__ __forceinline__ Two log_two(float f) {
   const float n = m - 1.f, d = m + 1.f, d_lo = m - (d - 1.f);  // m - 1 is exact
   const float r = __fdiv_rn(n, d), r_lo = __fdiv_rn(fmaf(-r, d, n) - r * d_lo, d);
   const float q = r * r, series = r * q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 13, 1.f / 11), 1.f / 9), 1.f / 7), 1.f / 5), 1.f / 3);
-  // k ln 2: the first float has few enough bits for an exact product
+  // k ln 2, ln 2 in two parts as Cody and Waite split it ("Software Manual for the Elementary Functions"):
+  // the first has few enough bits for an exact product
   const float kf = static_cast<float>(k), base = kf * 0.693359375f;
   const float hi = base + 2.f * r, back = hi - base;
   const float lo = ((base - (hi - back)) + (2.f * r - back)) + fmaf(kf, -2.12194440e-4f, 2.f * (series + r_lo));

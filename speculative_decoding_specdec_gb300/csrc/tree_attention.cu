@@ -20,7 +20,7 @@
 // starts where SMs are free, and waits before it reads what the first wrote.  Measured, heads of 128:
 //   64 rows of one token, 32 query and 8 K/V heads, one prompt of 65537 columns: 108 us (the shared pass
 //     78, 269 MB in 3.4 TB/s; its cut units' merge 12, the own columns 26, partly at once);
-//   32 chains of 6 of the same heads, 4 prompts of 6000: 70 us (38, 10, 27);
+//   32 chains of 6 of the same heads, 4 prompts of 6000 to 2400 (264 to 120 query rows): 70 us (38, 10, 27);
 //   8 rows of one token of 32 K/V heads, one prompt of 2048: 22 us.
 // Rows that fill the tiles by themselves gain nothing from a pass of their group and would pay for (m, l,
 // o): they take both parts in one pass, from two tensor maps, the prefix's tiles first (fills_tiles):
@@ -924,7 +924,10 @@ void set_shape(AttnParams& p, const AttnShape& s, void* workspace) {
 // Whether a batch row's own query rows fill the tensor cores' tiles to three quarters and more, so that
 // its prefix is attended with its own columns in one pass.
 // (16384 rows in all per K/V head over 8192 columns and 512 a row over up to 1056 of its own, 32 rows
-// and 2 K/V heads: 132 us against 201 in two passes.)
+// and 2 K/V heads: 132 us against 201 in two passes.  32 rows of up to 512 columns, 8 K/V heads, behind one
+// prefix of 8192 and of 1024, one pass and two: 96 query rows a row 134, 170 and 51, 103 us; 128: 137, 203 and
+// 54, 116; 192: 237, 278 and 77, 150; 256: 243, 335 and 81, 172.  Below the border one pass is ahead too,
+// 64 rows 133, 137 and 50, 88, 160 rows 220, 243 and 70, 138, down to 32 rows: 117, 82 and 46, 53.)
 bool fills_tiles(const AttnShape& s, long long R) {
   const long long room = R <= 128 ? 128 : (R + 255) / 256 * 256;
   return s.kind == kTc && R * 4 >= room * 3;

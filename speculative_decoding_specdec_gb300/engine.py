@@ -306,7 +306,8 @@ class SharedPromptBatch(TreeBatch):
     in ``prefix`` [L, 2, P, H, columns, hd]; the batch's cache holds what the rows have of their own,
     and ``n_committed``, ``width`` and the ids count that alone.  ``prefill`` gives the passes that fill
     ``prefix``; a round is then as of a TreeBatch (or, without drafts, ``sample`` and ``realign``), with
-    heads normed where weights are given and every row's prompt in its attention."""
+    heads normed where weights are given and every row's prompt in its attention.  Every row starts at its
+    prompt's last token: there is none of its own before the first round."""
 
     CHUNK = specdec.MAX_TREE    # prompt tokens of a prefill pass
 
