@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.tree_oracle as TO
 import test_gpu_prefix_attention as PA
 from tree_testlib import DEV, i32, random_parents, status
 
@@ -119,3 +120,29 @@ def test_groups_of_very_unlike_sizes(dtype, T, Hq, H, hd):
     PA.check(out, lse, q, cache, 1, n, W, None, prefix, lens, groups)
     again = PA.run(q, cache, 1, n, W, None, prefix, lens, groups)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("B,T,Hq,H,hd", SHAPES)
+@pytest.mark.parametrize("shared", [40, 2500])
+def test_own_values_that_are_not_finite_stay_in_their_place(dtype, B, T, Hq, H, hd, shared):
+    """Of a committed column: that value of all the row's nodes; of a node's: of those below it alone."""
+    rng = np.random.default_rng(T)
+    n, lens, groups = np.array([40, 9, 30, 12]), [shared, 33], [0, 3, 4]
+    par = random_parents(rng, B, T)
+    q, cache, W, prefix = PA.inputs(2, B, T, Hq, H, hd, n, dtype, 2, lens)
+    clean = PA.run(q, cache, 1, n, W, par, prefix, lens, groups)
+    node, G = T // 2, Hq // H
+    cache[1, 1, 0, 0, W - 3, 5] = float("inf")               # committed, row 0
+    cache[1, 1, 2, H - 1, W - 1 + node, hd - 1] = float("nan")    # a node's, row 2
+    cache[1, 1, 3, 0, W - 1, 0] = float("-inf")              # the pending token's, row 3
+    out, lse, st = PA.run(q, cache, 1, n, W, par, prefix, lens, groups)
+    assert st == 0 and torch.equal(lse, clean[1])
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, :, :G, 5] = True
+    for t in range(T):
+        if node in TO.line_of(par[2], t):
+            hit[2, t, -G:, hd - 1] = True
+    hit[3, :, :G, 0] = True
+    assert not torch.isfinite(out[hit]).any() and torch.equal(out[~hit], clean[0][~hit])

@@ -103,3 +103,13 @@ def test_top_p_cuts_beside_min_p(dtype, V):
             assert e[:n].sum() / e.sum() >= top_p[r] - d
             tighter += 1
     assert tighter >= 6
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 358399), (torch.bfloat16, 716799)])
+def test_the_longest_rows_at_any_address(dtype, V):
+    """Sixteen CTAs to a row, whose parts end anywhere in memory's 16 bytes."""
+    x = SA.scores(2, V, 1, dtype=dtype)
+    for lead in (0, 1, 3):
+        for kw in (dict(), dict(top_p=0.9), dict(top_k=[50, V - 1], min_p=0.01)):
+            SA.run(x, [0.3, 0.999], lead=lead, **kw)
